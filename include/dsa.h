@@ -231,6 +231,120 @@ dsa_status dsa_indexer_prolog(const dsa_dims* dims, const void* k_I_new, const v
                               dsa_stream_t stream);
 
 /*
+ * Rotary positions: the rotated columns of every head turn by position * frequency. With
+ * angle_i = pos * freq[i], i < rot / 2, and (a, b) the columns of pair i,
+ *   y_a = scale * (x_a cos angle_i - x_b sin angle_i),  y_b = scale * (x_a sin angle_i + x_b cos angle_i)
+ *   DSA_ROPE_INTERLEAVED: (a, b) = (2i, 2i + 1);  DSA_ROPE_HALF: (a, b) = (i, i + rot / 2).
+ * The arithmetic is fp32 (the angle fp64), rounded once to the tensor's type.
+ *
+ * dsa_rope_frequencies: freq[rot / 2] on the HOST, in radians per position, for base^(-2i / rot)
+ *   stretched to contexts `factor` times the trained length (factor 1: no scaling):
+ *   DSA_ROPE_LINEAR  every frequency / factor (positions interpolated)
+ *   DSA_ROPE_BASE    base * factor^(rot / (rot - 2)) (slow pairs stretched by factor, the fastest kept)
+ *   DSA_ROPE_YARN    pairs with fewer than beta_slow turns over original_length positions / factor,
+ *                    those with more than beta_fast turns kept, a linear ramp over the pairs between
+ *   rot even, 2..DSA_ROPE_MAX_WIDTH; base > 0, factor >= 1; YaRN: base > 1, original_length > 0,
+ *   beta_fast >= beta_slow > 0.
+ *
+ * dsa_rope: n <= DSA_ROPE_MAX_TENSORS tensors of the same T tokens in one launch (a query and an indexer
+ *   query). Each is [T][heads][rot] fp32 (type DSA_F32) or bf16 (DSA_BF16) through its strides, counted in
+ *   elements: x points at the first rotated column of token 0's head 0, so part of a wider head is its
+ *   address. out may be x itself (in place: same address and strides); any other overlap is undefined.
+ *   freq       DEVICE fp64 [rot / 2], 8-byte aligned
+ *   seq_lens, q_pos   as in dsa_indexer_topk: row t has position q_pos[t], or seq_lens[t] - 1 with q_pos
+ *              NULL (decode). A row with a negative position (an empty sequence) is copied unchanged.
+ *   transpose  nonzero: the transposed rotation, the backward pass (gradients of y in, of x out)
+ */
+#define DSA_ROPE_MAX_TENSORS 4
+#define DSA_ROPE_MAX_WIDTH 512
+typedef enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 } dsa_rope_layout;
+typedef enum { DSA_ROPE_LINEAR = 0, DSA_ROPE_BASE = 1, DSA_ROPE_YARN = 2 } dsa_rope_scaling;
+typedef struct {
+    const void* x;
+    void* out;
+    int32_t heads;
+    int32_t layout; /* dsa_rope_layout */
+    int64_t x_stride_t, x_stride_h, out_stride_t, out_stride_h;
+} dsa_rope_tensor;
+
+dsa_status dsa_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_length,
+                                double beta_fast, double beta_slow, double* freq_host);
+dsa_status dsa_rope(int32_t type, const dsa_rope_tensor* x, int32_t n, int32_t rot, const double* freq,
+                    const int32_t* seq_lens, const int32_t* q_pos, int32_t T, float scale, int32_t transpose,
+                    dsa_stream_t stream);
+
+/*
+ * dsa_cache_append of rows whose rotary columns are not turned yet: columns kv_offset .. kv_offset + rot
+ * of every latent row and k_offset .. k_offset + rot of every indexer key turn by the row's position
+ * (as in dsa_rope), then the rows are written and quantised as in dsa_cache_append, in one launch. The
+ * rotated values stay in fp32 until that one rounding, so quantised caches can differ in the last bit from
+ * a rotation stored as bf16 first. An offset of -1 leaves that row's columns as they are.
+ * Arguments, requirements and faults otherwise as in dsa_cache_append; rot even, 2..256.
+ */
+typedef struct {
+    int32_t rot;
+    int32_t k_offset, k_layout;   /* indexer key: first rotated column (-1: none), dsa_rope_layout */
+    int32_t kv_offset, kv_layout; /* latent row */
+    float scale;
+} dsa_rope_append;
+
+dsa_status dsa_cache_append_rope(const dsa_dims* dims, const dsa_rope_append* rope, const double* freq,
+                                 const void* k_I_new, const void* kv_new, const int32_t* block_table,
+                                 const int32_t* seq_lens, const int32_t* q_seq, const int32_t* q_pos, int32_t T,
+                                 void* k_I_cache, void* k_I_scale, void* kv_cache, void* ws, size_t ws_bytes,
+                                 dsa_stream_t stream);
+
+/*
+ * Cache read-back: ranges of the paged caches as dense rows, dequantised (a chunked prompt reads its
+ * cached prefix back to project it up for dsa_prompt_attn).
+ *   cu_rows  [B + 1]   sequence b fills rows cu_rows[b] .. cu_rows[b + 1] - 1 of the outputs with its
+ *                      positions start[b], start[b] + 1, ...
+ *   start    [B]       first position read of each sequence; NULL: 0
+ *   R                  rows of the outputs; rows outside cu_rows[0] .. cu_rows[B] - 1 are left as they were
+ *   k_out    [R][d_I]  indexer keys: fp32 (DSA_F32) or bf16; NULL: not read
+ *   kv_out   [R][d]    latent rows: fp32 (DSA_F32) or bf16; NULL: not read
+ * Quantised values (code * scale, code * 2^X) are formed in fp32 and rounded once to bf16. A position
+ * outside [0, seq_lens[b]) (DSA_FAULT_INDEX) or in an invalid block (DSA_FAULT_BLOCK_TABLE) reads as a row
+ * of zeros. Requires (d * elem) and (d_I * elem) to be multiples of 16 bytes; FP8 / MXFP8 keys: d_I
+ * a multiple of 16 / 32. ws as for dsa_cache_append (only its error word is used).
+ */
+dsa_status dsa_cache_read(const dsa_dims* dims, const void* k_I_cache, const void* k_I_scale, const void* kv_cache,
+                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* start,
+                          const int32_t* cu_rows, int32_t R, void* k_out, void* kv_out, void* ws, size_t ws_bytes,
+                          dsa_stream_t stream);
+
+/*
+ * Prompt attention: dense attention over packed sequences, for prompts that the selection keeps whole
+ * (no longer than K), dense layers and chunks behind a read-back prefix. Sequence b has the queries
+ * cu_q[b] .. cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1; its queries are the last of its
+ * positions, so with lq queries and lk keys query i sees the keys j <= i + lk - lq (causal) or all of them.
+ *   q    [Tq][H][d_qk], k [Tk][H_kv][d_qk], v [Tk][H_kv][d_v]   fp32 (DSA_F32) or bf16 (DSA_BF16), with
+ *        the strides of dsa_prompt_dims (elements; a head's columns are dense). Query heads
+ *        h * H / H_kv .. share key head h.
+ *   cu_q, cu_k  [B + 1]  ascending from 0 or more; rows at and past cu_q[B] / cu_k[B] are not read as
+ *        values and not written. A sequence whose entries descend or leave [0, Tq] / [0, Tk] is skipped and
+ *        reported (DSA_FAULT_INDEX).
+ *   out  [Tq][H][d_v] in q's type, lse [Tq][H] fp32 (natural log; may be NULL), dense. A query that sees no
+ *        key gives out = 0, lse = -inf.
+ *   sm_scale > 0. Inputs of a sequence are finite.
+ * Widths: d_qk, d_v <= 256; H a multiple of H_kv; addresses, strides and row widths multiples of 16 bytes.
+ * ws: at least dsa_prompt_workspace_size bytes, 256-byte aligned, initialised with dsa_workspace_init.
+ */
+typedef struct {
+    int32_t type;    /* DSA_F32 or DSA_BF16 */
+    int32_t B;       /* packed sequences */
+    int32_t H, H_kv; /* query heads, key / value heads */
+    int32_t d_qk, d_v;
+    int32_t causal;
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+} dsa_prompt_dims;
+
+size_t dsa_prompt_workspace_size(const dsa_prompt_dims* dims, int32_t Tq);
+dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const void* k, const void* v,
+                           const int32_t* cu_q, const int32_t* cu_k, int32_t Tq, int32_t Tk, float sm_scale, void* out,
+                           float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/*
  * Hierarchical (coarse -> fine) index selection ("Engineering Path for Day-0 Adaptation ..." §3.1:
  * coarse filtering at block granularity followed by refinement; "How the Ascend Computing
  * Platform Achieves Same-Day Inference Adaptation ..." §3.1: the coarse filter reuses summary

@@ -13,13 +13,18 @@ Entry points (same names as the C ABI):
 * :func:`cache_append` -- new tokens' indexer keys and latent rows into the paged caches (FP8 keys:
   block requantisation; FP8 latent rows: per-tile quantisation).
 * :func:`indexer_prolog` -- the cache append and the MXFP8 query quantisation in one launch.
+* :func:`rope`, :func:`rope_frequencies` -- rotary positions of queries, in place or into another tensor, and
+  the frequencies of long contexts.
+* :func:`cache_append_rope` -- the cache append of rows whose rotary columns are not turned yet.
+* :func:`cache_read` -- ranges of the paged caches read back as dense, dequantised rows.
+* :func:`prompt_attn` -- dense causal attention over packed prompts (grouped heads, prefixes).
 * :func:`block_summaries`, :func:`indexer_topk_hier` -- hierarchical (coarse -> fine) selection over
   per-block summary keys.
 * :func:`indexer_topk_noalloc` -- :func:`indexer_topk` with the library's static scratch instead of
   a workspace, for callers that cannot allocate device memory.
 
-Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives; the
-calls are enqueued on the current stream (or ``stream=``). A decode step over a batch of B
+Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`
+and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or ``stream=``). A decode step over a batch of B
 sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
 
     dims = make_dims("bf16", B, max_blocks, num_blocks, H_I=64, d_I=128, H=128, d=576, d_v=512, K=2048)
@@ -47,6 +52,21 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace", 4: "
 class Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("mode", "B", "max_blocks", "num_blocks", "block_size", "H_I", "d_I", "H", "d", "d_v", "K")]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32), ("layout", ctypes.c_int32)] + \
+        [(n, ctypes.c_int64) for n in ("x_stride_t", "x_stride_h", "out_stride_t", "out_stride_h")]
+
+
+class RopeAppend(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot", "k_offset", "k_layout", "kv_offset", "kv_layout")] + \
+        [("scale", ctypes.c_float)]
+
+
+class PromptDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("type", "B", "H", "H_kv", "d_qk", "d_v", "causal")] + \
+        [(n, ctypes.c_int64) for n in ("q_stride_t", "q_stride_h", "k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h")]
 
 
 class DsaError(RuntimeError):
@@ -86,6 +106,20 @@ def lib():
         L.dsa_cache_append.argtypes = [D, P, P, P, P, P, P, I32, P, P, P, P, SZ, P]
         L.dsa_indexer_prolog.restype = ctypes.c_int
         L.dsa_indexer_prolog.argtypes = [D, P, P, P, P, P, P, I32, P, P, P, P, I32, P, P, SZ, P]
+        F32, F64 = ctypes.c_float, ctypes.c_double
+        L.dsa_rope_frequencies.restype = ctypes.c_int
+        L.dsa_rope_frequencies.argtypes = [I32, F64, I32, F64, F64, F64, F64, ctypes.POINTER(F64)]
+        L.dsa_rope.restype = ctypes.c_int
+        L.dsa_rope.argtypes = [I32, ctypes.POINTER(RopeTensor), I32, I32, P, P, P, I32, F32, I32, P]
+        L.dsa_cache_append_rope.restype = ctypes.c_int
+        L.dsa_cache_append_rope.argtypes = [D, ctypes.POINTER(RopeAppend), P, P, P, P, P, P, P, I32, P, P, P, P, SZ, P]
+        L.dsa_cache_read.restype = ctypes.c_int
+        L.dsa_cache_read.argtypes = [D, P, P, P, P, P, P, P, I32, P, P, P, SZ, P]
+        PD = ctypes.POINTER(PromptDims)
+        L.dsa_prompt_workspace_size.restype = SZ
+        L.dsa_prompt_workspace_size.argtypes = [PD, I32]
+        L.dsa_prompt_attn.restype = ctypes.c_int
+        L.dsa_prompt_attn.argtypes = [PD, P, P, P, P, P, I32, I32, F32, P, P, P, SZ, P]
         L.dsa_indexer_topk_noalloc.restype = ctypes.c_int
         L.dsa_indexer_topk_noalloc.argtypes = [D, P, P, P, P, P, P, P, P, I32, P, P, P]
         L.dsa_read_error.restype = ctypes.c_int
@@ -272,6 +306,180 @@ def indexer_prolog(dims: Dims, k_I_new, kv_new, block_table, seq_lens, k_I_cache
                                   _p(q_out), _p(ws), ws.numel(), _stream(stream))
     _check("dsa_indexer_prolog", st)
     return q_out
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"linear": 0, "base": 1, "yarn": 2}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(*tensors):
+    """Every tensor on the current CUDA device (the library launches there)."""
+    for t in tensors:
+        if t is not None:
+            _need(t.is_cuda, "tensor arguments must be CUDA tensors (the library takes device pointers)")
+            _need(t.device.index == torch.cuda.current_device(), "tensor arguments must be on the current CUDA device")
+
+
+def _int32(t, n: int, name: str):
+    _need(t is None or (t.dtype == torch.int32 and t.numel() >= n), f"{name} must be an int32 tensor of {n} elements")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new output that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _layout(name) -> int:
+    _need(name in ROPE_LAYOUTS, f"unknown rotary layout {name!r}")
+    return ROPE_LAYOUTS[name]
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str = "linear", factor: float = 1.0,
+                     original_length: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda") -> torch.Tensor:
+    """The rot / 2 angular frequencies (radians per position, float64) :func:`rope` takes, for contexts
+    ``factor`` times the trained length: "linear", "base" or "yarn" (factor 1: unscaled)."""
+    _need(scaling in ROPE_SCALINGS, f"unknown rotary scaling {scaling!r}")
+    f = (ctypes.c_double * max(1, rot // 2))()
+    _check("dsa_rope_frequencies", lib().dsa_rope_frequencies(rot, base, ROPE_SCALINGS[scaling], factor, original_length,
+                                                              beta_fast, beta_slow, f))
+    return torch.tensor(list(f), dtype=torch.float64, device=device)
+
+
+def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, scale: float = 1.0,
+         transpose: bool = False, stream=None):
+    """Turns the columns of ``x`` ([T][heads][rot], fp32 or bf16; rot = 2 freq.numel()) by the rows'
+    positions ``q_pos`` (or seq_lens - 1), in place or into ``out``, and returns the result.
+
+    ``x`` may be a view of part of wider heads (``q[..., 512:]``), or a list of up to four tensors of the
+    same tokens, with ``out`` and ``layout`` lists as well. ``transpose=True`` is the backward pass."""
+    many = isinstance(x, (list, tuple))
+    xs = list(x) if many else [x]
+    outs = xs if out is None else list(out) if many else [out]
+    layouts = list(layout) if isinstance(layout, (list, tuple)) else [layout] * len(xs)
+    _need(0 < len(xs) == len(outs) == len(layouts), "x, out and layout must have the same number of tensors")
+    _on_device(freq, seq_lens, q_pos, *xs, *outs)
+    _need(freq.dtype == torch.float64 and freq.dim() == 1, "freq must be a float64 tensor of rot / 2 elements")
+    T, rot = xs[0].shape[0], 2 * freq.numel()
+    _need(q_pos is not None or seq_lens is not None, "rope needs q_pos or seq_lens")
+    _int32(q_pos, T, "q_pos")
+    if q_pos is None:
+        _int32(seq_lens, T, "seq_lens")
+    _need(xs[0].dtype in _TYPES, "x must be float32 or bfloat16")
+    arr = (RopeTensor * len(xs))()
+    for r, s, d, lay in zip(arr, xs, outs, layouts):
+        for t in (s, d):
+            _need(t.dim() == 3 and t.shape == xs[0].shape[:1] + s.shape[1:2] + (rot,) and t.dtype == xs[0].dtype,
+                  "rope tensors must be [T][heads][rot] of one type and one T")
+            _need(t.stride(2) == 1 or t.numel() == 0, "a head's rotated columns must be dense")
+        _need(d.numel() == 0 or (0 not in (d.stride(0) if d.shape[0] > 1 else 1, d.stride(1) if d.shape[1] > 1 else 1)),
+              "out must not repeat rows (expanded views)")
+        r.x, r.out, r.heads, r.layout = s.data_ptr(), d.data_ptr(), s.shape[1], _layout(lay)
+        r.x_stride_t, r.x_stride_h, r.out_stride_t, r.out_stride_h = s.stride(0), s.stride(1), d.stride(0), d.stride(1)
+    _check("dsa_rope", lib().dsa_rope(_TYPES[xs[0].dtype], arr, len(xs), rot, _p(freq), _p(seq_lens), _p(q_pos), T,
+                                      float(scale), int(transpose), _stream(stream)))
+    return outs if many else outs[0]
+
+
+def cache_append_rope(dims: Dims, freq, k_I_new, kv_new, block_table, seq_lens, k_I_cache, k_I_scale, kv_cache,
+                      q_seq=None, q_pos=None, *, k_offset=0, k_layout="half", kv_offset=None, kv_layout="interleaved",
+                      scale: float = 1.0, ws, stream=None) -> None:
+    """:func:`cache_append` of rows whose rotary columns are not turned yet: ``rot`` = 2 freq.numel()
+    columns from ``k_offset`` of the indexer keys and from ``kv_offset`` of the latent rows (default: their
+    last columns; -1: none) turn by the rows' positions in the same launch."""
+    T, rot = kv_new.shape[0], 2 * freq.numel()
+    _on_device(freq, k_I_new, kv_new, block_table, seq_lens, k_I_cache, k_I_scale, kv_cache, q_seq, q_pos, ws)
+    _need(freq.dtype == torch.float64, "freq must be a float64 tensor of rot / 2 elements")
+    act = torch.float32 if dims.mode == MODES["f32"] else torch.bfloat16
+    _need(k_I_new.dtype == act and k_I_new.numel() == T * dims.d_I, f"k_I_new must be a {act} tensor of T x d_I elements")
+    _need(kv_new.dtype == act and kv_new.numel() == T * dims.d, f"kv_new must be a {act} tensor of T x d elements")
+    _int32(block_table, dims.B * dims.max_blocks, "block_table")
+    _int32(seq_lens, dims.B, "seq_lens")
+    _int32(q_seq, T, "q_seq")
+    _int32(q_pos, T, "q_pos")
+    r = RopeAppend(rot, k_offset, _layout(k_layout), dims.d - rot if kv_offset is None else kv_offset, _layout(kv_layout),
+                   float(scale))
+    st = lib().dsa_cache_append_rope(ctypes.byref(dims), ctypes.byref(r), _p(freq), _p(k_I_new), _p(kv_new),
+                                     _p(block_table), _p(seq_lens), _p(q_seq), _p(q_pos), T, _p(k_I_cache), _p(k_I_scale),
+                                     _p(kv_cache), _p(ws), ws.numel(), _stream(stream))
+    _check("dsa_cache_append_rope", st)
+
+
+def cache_read(dims: Dims, k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, cu_rows, R: int, start=None, *,
+               k_out=None, kv_out=None, want_k: bool = True, want_kv: bool = True, ws, stream=None):
+    """(k[R][d_I], kv[R][d]) of the positions start[b], start[b] + 1, ... of every sequence b, dequantised,
+    in rows cu_rows[b] .. cu_rows[b + 1] - 1 (fp32 or bf16). An output not wanted is None."""
+    _on_device(k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, cu_rows, start, k_out, kv_out, ws)
+    act = torch.float32 if dims.mode == MODES["f32"] else torch.bfloat16
+    if k_out is None and want_k:
+        k_out = _empty((R, dims.d_I), act, ws.device, stream)
+    if kv_out is None and want_kv:
+        kv_out = _empty((R, dims.d), act, ws.device, stream)
+    for t, d, name in ((k_out, dims.d_I, "k_out"), (kv_out, dims.d, "kv_out")):
+        _need(t is None or (t.dtype == act and t.numel() >= R * d), f"{name} must be a {act} tensor of R x {d} elements")
+    _int32(block_table, dims.B * dims.max_blocks, "block_table")
+    _int32(seq_lens, dims.B, "seq_lens")
+    _int32(cu_rows, dims.B + 1, "cu_rows")
+    _int32(start, dims.B, "start")
+    st = lib().dsa_cache_read(ctypes.byref(dims), _p(k_I_cache), _p(k_I_scale), _p(kv_cache), _p(block_table),
+                              _p(seq_lens), _p(start), _p(cu_rows), R, _p(k_out), _p(kv_out), _p(ws), ws.numel(),
+                              _stream(stream))
+    _check("dsa_cache_read", st)
+    return k_out, kv_out
+
+
+def prompt_dims(q, k, v, B: int, causal: bool = True) -> PromptDims:
+    """The dims of :func:`prompt_attn` for B sequences packed in q [Tq][H][d_qk], k [Tk][H_kv][d_qk] and
+    v [Tk][H_kv][d_v] (strided views allowed; a head's columns are dense)."""
+    for t in (q, k, v):
+        _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), "q, k and v must be [tokens][heads][width] with dense columns")
+    _need(q.dtype in _TYPES and k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must be all float32 or all bfloat16")
+    _need(k.shape[:2] == v.shape[:2] and q.shape[2] == k.shape[2], "k and v must have the same tokens and heads, q and k the same width")
+    return PromptDims(_TYPES[q.dtype], B, q.shape[1], k.shape[1], q.shape[2], v.shape[2], int(causal), q.stride(0),
+                      q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+
+
+def prompt_workspace(dims: PromptDims, Tq: int, device="cuda", stream=None) -> torch.Tensor:
+    """Allocates and initialises a workspace for :func:`prompt_attn` calls of up to Tq query tokens."""
+    n = int(lib().dsa_prompt_workspace_size(ctypes.byref(dims), Tq))
+    if n == 0:
+        raise ValueError("invalid dims")
+    ws = _empty(n + 256, torch.uint8, device, stream)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off: off + n]
+    _check("dsa_workspace_init", lib().dsa_workspace_init(_p(ws), n, _stream(stream)))
+    return ws
+
+
+def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, out=None, lse=None, stream=None):
+    """(out[Tq][H][d_v], lse[Tq][H]) of dense attention over packed sequences: sequence b has the queries
+    cu_q[b] .. cu_q[b + 1] - 1, the last of its positions, and the keys cu_k[b] .. cu_k[b + 1] - 1."""
+    now = prompt_dims(q, k, v, dims.B, dims.causal)
+    _need(bytes(now) == bytes(dims), "q, k and v differ from the tensors dims was made for")
+    _on_device(q, k, v, cu_q, cu_k, out, lse, ws)
+    _int32(cu_q, dims.B + 1, "cu_q")
+    _int32(cu_k, dims.B + 1, "cu_k")
+    Tq, H = q.shape[:2]
+    if out is None:
+        out = _empty((Tq, H, dims.d_v), q.dtype, q.device, stream)
+    if lse is None:
+        lse = _empty((Tq, H), torch.float32, q.device, stream)
+    _need(out.dtype == q.dtype and out.numel() >= Tq * H * dims.d_v, "out must be a tensor of Tq x H x d_v elements in q's type")
+    _need(lse.dtype == torch.float32 and lse.numel() >= Tq * H, "lse must be a float32 tensor of Tq x H elements")
+    st = lib().dsa_prompt_attn(ctypes.byref(dims), ctypes.c_void_p(q.data_ptr()), ctypes.c_void_p(k.data_ptr()),
+                               ctypes.c_void_p(v.data_ptr()), _p(cu_q), _p(cu_k), Tq, k.shape[0], float(sm_scale), _p(out),
+                               _p(lse), _p(ws), ws.numel(), _stream(stream))
+    _check("dsa_prompt_attn", st)
+    return out, lse
 
 
 def summaries_buffer(dims: Dims, device="cuda") -> torch.Tensor:

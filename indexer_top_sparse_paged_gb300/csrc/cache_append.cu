@@ -208,6 +208,231 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (g < q_groups) mx_quantize_group32(q + g * 32, q_out + g * 32);
 }
 
+// ------------------------------------------------------------------------------------------------
+// the rotated append: the same caches, the new rows' rotary columns turned on the way in
+// ------------------------------------------------------------------------------------------------
+
+struct RopeAppendArgs {
+    AppendArgs a;
+    dsa_rope_append r;
+    const double* freq;
+    int token_ctas;  // CTAs of warps that each write one row; the rest requantise FP8-key blocks
+    int jobs_per_cta;
+};
+
+__device__ __forceinline__ float row_value(const void* x, bool f32, int e) {
+    return f32 ? static_cast<const float*>(x)[e]
+               : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(x)[e]) << 16);
+}
+
+// The pairs first, first + step, ... of one row's rotated columns, turned in fp32 into buf[0 .. rot).
+__device__ __forceinline__ void rotate_row(const RopeAppendArgs& p, const void* x, int offset, int layout, int pos,
+                                           float* buf, int first, int step) {
+    const int half = p.r.rot / 2;
+    for (int i = first; i < half; i += step) {
+        const int e0 = layout == DSA_ROPE_INTERLEAVED ? 2 * i : i;
+        const int e1 = layout == DSA_ROPE_INTERLEAVED ? 2 * i + 1 : i + half;
+        const bool f32 = p.a.mode == DSA_F32;
+        const float u = row_value(x, f32, offset + e0), v = row_value(x, f32, offset + e1);
+        const float2 cs = rope_cos_sin(pos, p.freq[i], p.r.scale, false);
+        const float2 y = rope_turn(u, v, cs);
+        buf[e0] = y.x;
+        buf[e1] = y.y;
+    }
+}
+
+// Elements e .. e + 3 of a row whose columns offset .. offset + rot come from buf (offset < 0: none).
+__device__ __forceinline__ float4 row_load4(const void* x, bool f32, int e, const float* buf, int offset, int rot) {
+    float v[4];
+    if (f32) {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + e);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + e);
+        v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    }
+    if (offset >= 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (static_cast<unsigned>(e + k - offset) < static_cast<unsigned>(rot)) v[k] = buf[e + k - offset];
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ float amax4(const float4& v) {
+    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(const float4& v) {
+    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(v.x, __NV_SATFINITE, __NV_E4M3)) |
+           static_cast<uint32_t>(__nv_cvt_float_to_fp8(v.y, __NV_SATFINITE, __NV_E4M3)) << 8 |
+           static_cast<uint32_t>(__nv_cvt_float_to_fp8(v.z, __NV_SATFINITE, __NV_E4M3)) << 16 |
+           static_cast<uint32_t>(__nv_cvt_float_to_fp8(v.w, __NV_SATFINITE, __NV_E4M3)) << 24;
+}
+
+// One row of n elements (fp32 or bf16) into dst in the same type.
+__device__ __forceinline__ void store_plain_row(const void* x, bool f32, int n, void* dst, const float* buf, int offset,
+                                                int rot, int lane) {
+    for (int e = 4 * lane; e < n; e += 128) {
+        const float4 v = row_load4(x, f32, e, buf, offset, rot);
+        if (f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(dst) + e) = v;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst) + e) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+    }
+}
+
+// FP8 keys: the block of new token t, requantised as a whole if t is its first new token (the CTA).
+__device__ void requantise_block_rope(const RopeAppendArgs& p, int t, float* buf) {
+    const AppendArgs& a = p.a;
+    __shared__ float red[kAppendThreads / 32];
+    __shared__ int run_end;
+    int b, pos;
+    const int blk = append_block(a, t, b, pos);
+    if (blk < 0) return;  // reported by the token's own warps
+    const int lb = pos / kBlock;
+    if (t > 0) {
+        int b0, p0;
+        if (append_block(a, t - 1, b0, p0) >= 0 && b0 == b && p0 / kBlock == lb) return;
+    }
+    if (threadIdx.x == 0) run_end = min(a.T, t + kBlock);
+    __syncthreads();
+    if (threadIdx.x < kBlock && threadIdx.x > 0) {
+        const int u = t + static_cast<int>(threadIdx.x);
+        int b2, p2;
+        const bool same = u < a.T && append_block(a, u, b2, p2) >= 0 && b2 == b && p2 / kBlock == lb;
+        if (!same) atomicMin(&run_end, u);
+    }
+    __syncthreads();
+    const int m = run_end - t, n_old = pos - lb * kBlock, d_I = a.d_I;
+    const uint16_t* knew = static_cast<const uint16_t*>(a.k_new) + static_cast<int64_t>(t) * d_I;
+    const bool turned = p.r.k_offset >= 0;
+    if (turned) {
+        for (int u = threadIdx.x >> 5; u < m; u += kAppendThreads / 32)
+            rotate_row(p, knew + u * d_I, p.r.k_offset, p.r.k_layout, a.q_pos ? a.q_pos[t + u] : pos, buf + u * p.r.rot,
+                       threadIdx.x & 31, 32);
+        __syncthreads();
+    }
+    auto fresh = [&](int i) {  // element i of the run's new keys
+        const int u = i / d_I, e = i - u * d_I - p.r.k_offset;
+        return turned && static_cast<unsigned>(e) < static_cast<unsigned>(p.r.rot) ? buf[u * p.r.rot + e]
+                                                                                    : row_value(knew, false, i);
+    };
+    const float old_scale = static_cast<const float*>(a.k_scale)[blk];
+    uint8_t* codes = static_cast<uint8_t*>(a.k_cache) + static_cast<int64_t>(blk) * kBlock * d_I;
+    float amax = 0.0f;
+    for (int i = threadIdx.x; i < n_old * d_I; i += kAppendThreads) amax = fmaxf(amax, fabsf(e4m3_value(codes[i]) * old_scale));
+    for (int i = threadIdx.x; i < m * d_I; i += kAppendThreads) amax = fmaxf(amax, fabsf(fresh(i)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = red[0];
+#pragma unroll
+    for (int w = 1; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+    const float scale = amax > 0.0f ? amax / 448.0f : 1.0f;
+    for (int i = threadIdx.x; i < n_old * d_I; i += kAppendThreads)
+        codes[i] = static_cast<uint8_t>(
+            __nv_cvt_float_to_fp8(e4m3_value(codes[i]) * old_scale / scale, __NV_SATFINITE, __NV_E4M3));
+    for (int i = threadIdx.x; i < m * d_I; i += kAppendThreads) {
+        const int u = t + i / d_I;
+        const int pu = a.q_pos ? a.q_pos[u] : pos;
+        codes[(pu % kBlock) * d_I + i % d_I] =
+            static_cast<uint8_t>(__nv_cvt_float_to_fp8(fresh(i) / scale, __NV_SATFINITE, __NV_E4M3));
+    }
+    if (threadIdx.x == 0) static_cast<float*>(a.k_scale)[blk] = scale;
+}
+
+// Warp jobs 2t and 2t + 1 write token t's latent row and its key: the rotated columns go through a
+// per-warp buffer in shared memory in fp32 and are rounded once, into the cache's type.
+__global__ void __launch_bounds__(kAppendThreads) cache_append_rope_kernel(RopeAppendArgs p) {
+    extern __shared__ float rope_buf[];
+    const AppendArgs& a = p.a;
+    if (static_cast<int>(blockIdx.x) >= p.token_ctas) {
+        requantise_block_rope(p, blockIdx.x - p.token_ctas, rope_buf);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * p.jobs_per_cta + warp;
+    if (warp >= p.jobs_per_cta || job >= 2ll * a.T) return;
+    const int t = static_cast<int>(job >> 1);
+    const bool key = job & 1;
+    int b, pos;
+    const int blk = append_block(a, t, b, pos);
+    if (blk < 0) {
+        if (lane == 0) atomicOr(a.err, (b < 0 || b >= a.B) ? DSA_FAULT_INDEX : DSA_FAULT_BLOCK_TABLE);
+        return;
+    }
+    if (key && a.mode == DSA_BF16_KFP8) return;
+    const int64_t row = static_cast<int64_t>(blk) * kBlock + pos % kBlock;
+    const bool f32 = a.mode == DSA_F32;
+    const int act = f32 ? 4 : 2, n = key ? a.d_I : a.d, rot = p.r.rot;
+    const int offset = key ? p.r.k_offset : p.r.kv_offset;
+    const void* x = static_cast<const uint8_t*>(key ? a.k_new : a.kv_new) + static_cast<int64_t>(t) * n * act;
+    float* buf = rope_buf + warp * rot;
+    if (offset >= 0) {
+        rotate_row(p, x, offset, key ? p.r.k_layout : p.r.kv_layout, pos, buf, lane, 32);
+        __syncwarp();
+    }
+    if (!key && a.kv_fp8) {
+        uint8_t* rec = static_cast<uint8_t*>(a.kv_cache) + row * DSA_KV_FP8_RECORD_BYTES(n);
+        const int ntiles = (n + 127) / 128;
+        for (int j = 0; j < ntiles; ++j) {
+            const int e = 128 * j + 4 * lane;
+            const float4 v = e < n ? row_load4(x, f32, e, buf, offset, rot) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float amax = amax4(v);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            const float scale = amax > 0.0f ? amax / 448.0f : 1.0f;
+            if (e < n) *reinterpret_cast<uint32_t*>(rec + e) = e4m3x4(make_float4(v.x / scale, v.y / scale, v.z / scale, v.w / scale));
+            if (lane == 0) *reinterpret_cast<float*>(rec + n + 4 * j) = scale;
+        }
+        for (int i = n + 4 * ntiles + lane; i < DSA_KV_FP8_RECORD_BYTES(n); i += 32) rec[i] = 0;
+    } else if (key && a.mode == DSA_MXFP8) {
+        for (int e0 = 0; e0 < n; e0 += 128) {  // eight lanes hold one group of 32
+            const int e = e0 + 4 * lane;
+            const float4 v = e < n ? row_load4(x, f32, e, buf, offset, rot) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float amax = amax4(v);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            if (e >= n) continue;
+            const int X = mx_exponent(amax);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.k_cache) + row * n + e) =
+                e4m3x4(make_float4(v.x * down, v.y * down, v.z * down, v.w * down));
+            if ((lane & 7) == 0) static_cast<uint8_t*>(a.k_scale)[row * (n / 32) + e / 32] = static_cast<uint8_t>(X + 127);
+        }
+    } else {
+        store_plain_row(x, f32, n, static_cast<uint8_t*>(key ? a.k_cache : a.kv_cache) + row * n * act, buf, offset, rot, lane);
+    }
+}
+
+bool launch_cache_append_rope(const dsa_dims& d, bool kv_fp8, const dsa_rope_append& r, const double* freq,
+                              const void* k_new, const void* kv_new, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* q_seq, const int32_t* q_pos, int T, void* k_cache,
+                              void* k_scale, void* kv_cache, int* err, cudaStream_t s, int* launches) {
+    if (T == 0) return true;
+    RopeAppendArgs p{};
+    p.a = AppendArgs{d.mode, kv_fp8 ? 1 : 0, d.B, d.max_blocks, d.num_blocks, d.d_I, d.d, T, k_new, kv_new, block_table,
+                     seq_lens, q_seq, q_pos, k_cache, k_scale, kv_cache, err};
+    p.r = r;
+    p.freq = freq;
+    p.jobs_per_cta = kAppendThreads / 32;
+    p.token_ctas = static_cast<int>((2ll * T + p.jobs_per_cta - 1) / p.jobs_per_cta);
+    const bool blocks = d.mode == DSA_BF16_KFP8;
+    const size_t smem = sizeof(float) * r.rot * (blocks ? kBlock : kAppendThreads / 32);
+    if (!set_max_dynamic_smem(reinterpret_cast<const void*>(cache_append_rope_kernel), smem)) return false;
+    if (!launch_kernel(false, cache_append_rope_kernel, dim3(p.token_ctas + (blocks ? T : 0)), dim3(kAppendThreads), smem,
+                       s, p))
+        return false;
+    ++*launches;
+    return true;
+}
+
 bool launch_cache_append(const dsa_dims& d, bool kv_fp8, const void* k_new, const void* kv_new,
                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_seq,
                          const int32_t* q_pos, int T, void* k_cache, void* k_scale, void* kv_cache, int* err,

@@ -443,6 +443,22 @@ __device__ __forceinline__ int mx_exponent(float amax) {
     return max(E - 135, -127);
 }
 
+// (scale cos, scale sin) of position pos at angular frequency freq (radians per position). The angle
+// is formed in fp64 as turns and its whole part dropped there, so that far positions keep their
+// fraction (4e-11 turns at a million positions); the transpose turns the other way.
+__device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale, bool transpose) {
+    const double turns = static_cast<double>(pos) * (freq * 0.15915494309189535);  // 1 / (2 pi)
+    const float f = static_cast<float>(turns - rint(turns));
+    float s, c;
+    sincospif(2.0f * f, &s, &c);
+    return make_float2(scale * c, transpose ? -scale * s : scale * s);
+}
+
+// One pair turned, with the roundings written out (the same bits in every kernel).
+__device__ __forceinline__ float2 rope_turn(float u, float v, float2 cs) {
+    return make_float2(fmaf(u, cs.x, -__fmul_rn(v, cs.y)), fmaf(u, cs.y, __fmul_rn(v, cs.x)));
+}
+
 // OCP MX quantisation of 32 bf16 values (16 words of two, the lower element in the low half):
 // returns the shared exponent X and writes the codes RNE_e4m3(x * 2^-X), saturating at +-448,
 // four per word (element 4i + k in byte k of word i). x * 2^-X is exact in fp32 whenever the

@@ -10,6 +10,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -382,6 +383,50 @@ static HierLayout hier_layout(const dsa_dims& d, int T, int n_sel) {
     return h;
 }
 
+// ------------------------------------------------------------------------------------------------
+// prompt attention: checks and workspace
+// ------------------------------------------------------------------------------------------------
+
+struct PromptLayout {
+    size_t n_units;  // int32
+    size_t units;    // PromptUnit [max_units]
+    size_t total;
+    int tile_rows;
+    int max_units;
+};
+
+static dsa_status check_prompt_dims(const dsa_prompt_dims* p, int32_t Tq) {
+    if (!p) return DSA_ERR_INVALID_ARG;
+    if (p->type != DSA_F32 && p->type != DSA_BF16) return DSA_ERR_UNSUPPORTED;
+    if (p->B <= 0 || p->H <= 0 || p->H_kv <= 0 || p->d_qk <= 0 || p->d_v <= 0 || Tq < 0) return DSA_ERR_INVALID_ARG;
+    if (p->H % p->H_kv) return DSA_ERR_INVALID_ARG;
+    if (p->d_qk > 256 || p->d_v > 256 || p->H_kv > 65535) return DSA_ERR_UNSUPPORTED;
+    const int unit = p->type == DSA_F32 ? 4 : 8;  // elements per 16 bytes
+    if (p->d_qk % unit || p->d_v % unit) return DSA_ERR_UNSUPPORTED;
+    const int64_t strides[6] = {p->q_stride_t, p->q_stride_h, p->k_stride_t, p->k_stride_h, p->v_stride_t, p->v_stride_h};
+    for (int64_t s : strides)
+        if (s < 0 || s % unit || s > (1ll << 36)) return DSA_ERR_INVALID_ARG;
+    // rows (token, head of the group) and tiles are counted in 32 bits
+    if (static_cast<int64_t>(Tq) * (p->H / p->H_kv) + p->B >= (1ll << 31) - (1 << 16)) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
+    PromptLayout w{};
+    w.tile_rows = kPromptSimtRows;
+    // every sequence fills whole tiles but its last
+    w.max_units = static_cast<int>(static_cast<int64_t>(Tq) * (p.H / p.H_kv) / w.tile_rows) + p.B;
+    size_t off = 256;  // the error word
+    w.n_units = off;
+    off += 256;
+    w.units = off;
+    off = align256(off + sizeof(PromptUnit) * static_cast<size_t>(w.max_units));
+    w.total = off;
+    return w;
+}
+
+static bool rope_layout_ok(int layout) { return layout == DSA_ROPE_INTERLEAVED || layout == DSA_ROPE_HALF; }
+
 }  // namespace dsa
 
 using namespace dsa;
@@ -603,6 +648,186 @@ dsa_status dsa_indexer_prolog(const dsa_dims* dims_in, const void* k_I_new, cons
                                k_I_scale, kv_cache, q_I, q_I_mx, q_elements, static_cast<int*>(ws),
                                reinterpret_cast<cudaStream_t>(stream), &launches))
         st = DSA_ERR_LAUNCH;
+    g_last_launches = launches;
+    return st;
+}
+
+dsa_status dsa_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original_length,
+                                double beta_fast, double beta_slow, double* freq_host) {
+    if (!freq_host || rot < 2 || rot % 2) return DSA_ERR_INVALID_ARG;
+    if (rot > DSA_ROPE_MAX_WIDTH || scaling < DSA_ROPE_LINEAR || scaling > DSA_ROPE_YARN) return DSA_ERR_UNSUPPORTED;
+    if (!(base > 0.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor)) return DSA_ERR_INVALID_ARG;
+    const int half = rot / 2;
+    double low = 0.0, high = 0.0;
+    if (scaling == DSA_ROPE_YARN) {
+        if (!(base > 1.0) || !(original_length > 0.0) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+            !std::isfinite(original_length) || !std::isfinite(beta_fast))
+            return DSA_ERR_INVALID_ARG;
+        // the pair that makes `turns` turns over the trained length: original_length f = 2 pi turns
+        auto pair_of = [&](double turns) {
+            return rot * std::log(original_length / (turns * 2.0 * M_PI)) / (2.0 * std::log(base));
+        };
+        low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.0);
+        if (high - low < 0.001) high = low + 0.001;
+    }
+    if (scaling == DSA_ROPE_BASE && factor > 1.0 && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    for (int i = 0; i < half; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == DSA_ROPE_LINEAR) f /= factor;
+        if (scaling == DSA_ROPE_YARN) {
+            const double ramp = std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        freq_host[i] = f;
+    }
+    return DSA_OK;
+}
+
+dsa_status dsa_rope(int32_t type, const dsa_rope_tensor* x, int32_t n, int32_t rot, const double* freq,
+                    const int32_t* seq_lens, const int32_t* q_pos, int32_t T, float scale, int32_t transpose,
+                    dsa_stream_t stream) {
+    if (type != DSA_F32 && type != DSA_BF16) return DSA_ERR_UNSUPPORTED;
+    if (!x || n <= 0 || rot < 2 || rot % 2 || T < 0 || !std::isfinite(scale)) return DSA_ERR_INVALID_ARG;
+    if (n > DSA_ROPE_MAX_TENSORS || rot > DSA_ROPE_MAX_WIDTH) return DSA_ERR_UNSUPPORTED;
+    const uintptr_t elem = type == DSA_F32 ? 4 : 2;
+    for (int i = 0; i < n; ++i) {
+        if (x[i].heads < 0 || !rope_layout_ok(x[i].layout)) return DSA_ERR_INVALID_ARG;
+        if (static_cast<int64_t>(x[i].heads) * rot >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+        if (T > 0 && x[i].heads > 0) {
+            const uintptr_t src = reinterpret_cast<uintptr_t>(x[i].x), dst = reinterpret_cast<uintptr_t>(x[i].out);
+            if (!src || !dst || src % elem || dst % elem) return DSA_ERR_INVALID_ARG;
+            if (src == dst && (x[i].x_stride_t != x[i].out_stride_t || x[i].x_stride_h != x[i].out_stride_h))
+                return DSA_ERR_INVALID_ARG;
+        }
+    }
+    if (T > 0 && (!freq || (reinterpret_cast<uintptr_t>(freq) & 7u) || (!q_pos && !seq_lens))) return DSA_ERR_INVALID_ARG;
+    int launches = 0;
+    const bool ok = launch_rope(type, x, n, rot, freq, seq_lens, q_pos, T, scale, transpose != 0,
+                                reinterpret_cast<cudaStream_t>(stream), &launches);
+    g_last_launches = launches;
+    return ok ? DSA_OK : DSA_ERR_LAUNCH;
+}
+
+dsa_status dsa_cache_append_rope(const dsa_dims* dims_in, const dsa_rope_append* rope, const double* freq,
+                                 const void* k_I_new, const void* kv_new, const int32_t* block_table,
+                                 const int32_t* seq_lens, const int32_t* q_seq, const int32_t* q_pos, int32_t T,
+                                 void* k_I_cache, void* k_I_scale, void* kv_cache, void* ws, size_t ws_bytes,
+                                 dsa_stream_t stream) {
+    dsa_dims D;
+    bool kv8;
+    {
+        const dsa_status split = split_mode(dims_in, &D, &kv8);
+        if (split != DSA_OK) return split;
+    }
+    const dsa_dims* dims = &D;
+    dsa_status st = check_common(dims);
+    if (st != DSA_OK) return st;
+    if (T < 0 || dims->d_I <= 0 || dims->d <= 0) return DSA_ERR_INVALID_ARG;
+    if (!rope || rope->rot < 2 || rope->rot % 2 || !std::isfinite(rope->scale)) return DSA_ERR_INVALID_ARG;
+    if (rope->rot > 256) return DSA_ERR_UNSUPPORTED;
+    if (!rope_layout_ok(rope->k_layout) || !rope_layout_ok(rope->kv_layout)) return DSA_ERR_INVALID_ARG;
+    if (rope->k_offset < -1 || (rope->k_offset >= 0 && rope->k_offset > dims->d_I - rope->rot)) return DSA_ERR_INVALID_ARG;
+    if (rope->kv_offset < -1 || (rope->kv_offset >= 0 && rope->kv_offset > dims->d - rope->rot)) return DSA_ERR_INVALID_ARG;
+    if (!q_seq && T != dims->B) return DSA_ERR_INVALID_ARG;
+    if (T > 0 && (!freq || (reinterpret_cast<uintptr_t>(freq) & 7u))) return DSA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_I_new || !kv_new || !block_table || !seq_lens || !k_I_cache || !kv_cache)) return DSA_ERR_INVALID_ARG;
+    if (!scale_ok(dims, k_I_scale)) return DSA_ERR_INVALID_ARG;
+    const int act = dims->mode == DSA_F32 ? 4 : 2;
+    if ((dims->d * act) % 16 || (dims->d_I * act) % 16) return DSA_ERR_UNSUPPORTED;
+    if (dims->mode == DSA_MXFP8 && dims->d_I % 32) return DSA_ERR_UNSUPPORTED;
+    if (!aligned16(k_I_new) || !aligned16(kv_new) || !aligned16(k_I_cache) || !aligned16(kv_cache))
+        return DSA_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    if (!launch_cache_append_rope(*dims, kv8, *rope, freq, k_I_new, kv_new, block_table, seq_lens, q_seq, q_pos, T,
+                                  k_I_cache, k_I_scale, kv_cache, static_cast<int*>(ws),
+                                  reinterpret_cast<cudaStream_t>(stream), &launches))
+        st = DSA_ERR_LAUNCH;
+    g_last_launches = launches;
+    return st;
+}
+
+dsa_status dsa_cache_read(const dsa_dims* dims_in, const void* k_I_cache, const void* k_I_scale, const void* kv_cache,
+                          const int32_t* block_table, const int32_t* seq_lens, const int32_t* start,
+                          const int32_t* cu_rows, int32_t R, void* k_out, void* kv_out, void* ws, size_t ws_bytes,
+                          dsa_stream_t stream) {
+    dsa_dims D;
+    bool kv8;
+    {
+        const dsa_status split = split_mode(dims_in, &D, &kv8);
+        if (split != DSA_OK) return split;
+    }
+    const dsa_dims* dims = &D;
+    dsa_status st = check_common(dims);
+    if (st != DSA_OK) return st;
+    if (R < 0 || dims->d_I <= 0 || dims->d <= 0) return DSA_ERR_INVALID_ARG;
+    const int act = dims->mode == DSA_F32 ? 4 : 2;
+    if ((dims->d * act) % 16 || (dims->d_I * act) % 16) return DSA_ERR_UNSUPPORTED;
+    if (dims->mode == DSA_MXFP8 && dims->d_I % 32) return DSA_ERR_UNSUPPORTED;
+    if (dims->mode == DSA_BF16_KFP8 && dims->d_I % 16) return DSA_ERR_UNSUPPORTED;
+    if (R > 0 && (!block_table || !seq_lens || !cu_rows || (!k_out && !kv_out))) return DSA_ERR_INVALID_ARG;
+    if (k_out && (!k_I_cache || !scale_ok(dims, k_I_scale) || !aligned16(k_I_cache) || !aligned16(k_out)))
+        return DSA_ERR_INVALID_ARG;
+    if (kv_out && (!kv_cache || !aligned16(kv_cache) || !aligned16(kv_out))) return DSA_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    if (!launch_cache_read(*dims, kv8, k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, start, cu_rows, R, k_out,
+                           kv_out, static_cast<int*>(ws), reinterpret_cast<cudaStream_t>(stream), &launches))
+        st = DSA_ERR_LAUNCH;
+    g_last_launches = launches;
+    return st;
+}
+
+size_t dsa_prompt_workspace_size(const dsa_prompt_dims* dims, int32_t Tq) {
+    return check_prompt_dims(dims, Tq) == DSA_OK ? prompt_layout(*dims, Tq).total : 0;
+}
+
+dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const void* k, const void* v,
+                           const int32_t* cu_q, const int32_t* cu_k, int32_t Tq, int32_t Tk, float sm_scale, void* out,
+                           float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    dsa_status st = check_prompt_dims(dims, Tq);
+    if (st != DSA_OK) return st;
+    if (Tk < 0 || !(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (Tq > 0 && (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v)))) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+    const PromptLayout L = prompt_layout(*dims, Tq);
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    if (Tq > 0) {
+        uint8_t* base = static_cast<uint8_t*>(ws);
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        PromptArgs a{};
+        a.type = dims->type;
+        a.B = dims->B;
+        a.H = dims->H;
+        a.H_kv = dims->H_kv;
+        a.d_qk = dims->d_qk;
+        a.d_v = dims->d_v;
+        a.causal = dims->causal ? 1 : 0;
+        a.Tq = Tq;
+        a.Tk = Tk;
+        a.sm_scale = sm_scale;
+        a.q = q;
+        a.k = k;
+        a.v = v;
+        a.q_stride_t = dims->q_stride_t;
+        a.q_stride_h = dims->q_stride_h;
+        a.k_stride_t = dims->k_stride_t;
+        a.k_stride_h = dims->k_stride_h;
+        a.v_stride_t = dims->v_stride_t;
+        a.v_stride_h = dims->v_stride_h;
+        a.cu_q = cu_q;
+        a.cu_k = cu_k;
+        a.out = out;
+        a.lse = lse;
+        a.err = reinterpret_cast<int*>(base);
+        a.tile_rows = L.tile_rows;
+        a.max_units = L.max_units;
+        a.n_units = reinterpret_cast<int32_t*>(base + L.n_units);
+        a.units = reinterpret_cast<PromptUnit*>(base + L.units);
+        if (!launch_prompt_plan(a, s, &launches) || !launch_prompt_simt(a, s, &launches)) st = DSA_ERR_LAUNCH;
+    }
     g_last_launches = launches;
     return st;
 }

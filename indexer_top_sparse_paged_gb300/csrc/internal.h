@@ -139,6 +139,48 @@ bool launch_indexer_prolog(const dsa_dims& d, bool kv_fp8, const void* k_new, co
                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_seq,
                            const int32_t* q_pos, int T, void* k_cache, void* k_scale, void* kv_cache, const void* q_I,
                            void* q_out, int64_t q_elements, int* err, cudaStream_t s, int* launches);
+bool launch_rope(int type, const dsa_rope_tensor* x, int n, int rot, const double* freq, const int32_t* seq_lens,
+                 const int32_t* q_pos, int T, float scale, bool transpose, cudaStream_t s, int* launches);
+bool launch_cache_append_rope(const dsa_dims& d, bool kv_fp8, const dsa_rope_append& r, const double* freq,
+                              const void* k_new, const void* kv_new, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* q_seq, const int32_t* q_pos, int T, void* k_cache,
+                              void* k_scale, void* kv_cache, int* err, cudaStream_t s, int* launches);
+bool launch_cache_read(const dsa_dims& d, bool kv_fp8, const void* k_cache, const void* k_scale, const void* kv_cache,
+                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* start, const int32_t* cu_rows,
+                       int R, void* k_out, void* kv_out, int* err, cudaStream_t s, int* launches);
+
+// ---- prompt attention ----------------------------------------------------------------------------
+
+constexpr int kPromptSimtRows = 64;  // rows (token, head of the group) per tile
+
+struct PromptUnit {
+    int seq;   // packed sequence
+    int tile;  // tile of the sequence's rows
+};
+
+struct PromptArgs {
+    int type;
+    int B, H, H_kv, d_qk, d_v, causal;
+    int Tq, Tk;
+    float sm_scale;
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;  // elements
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    void* out;
+    float* lse;
+    int* err;
+    int tile_rows;      // rows per tile
+    int max_units;      // bound on the work list's length
+    int32_t* n_units;
+    PromptUnit* units;
+};
+
+bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches);
+bool launch_prompt_simt(const PromptArgs& a, cudaStream_t s, int* launches);
+
 bool launch_attn_tc(const AttnArgs& a, cudaStream_t s, int* launches);
 bool launch_wait_timeout(int* err, cudaStream_t s, int* launches);
 
