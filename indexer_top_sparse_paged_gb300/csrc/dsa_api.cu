@@ -60,6 +60,12 @@ bool attn_uses_tc(const dsa_dims& d) {
            d.d_v == 512;
 }
 
+// Widths that two query tiles and their accumulators leave room for in shared and tensor memory; the
+// keys' and values' rows are found through tensor maps, whose outer strides are not 0.
+bool prompt_uses_tc(const dsa_prompt_dims& p) {
+    return p.type == DSA_BF16 && p.d_qk <= 192 && p.d_v <= 128 && p.k_stride_t > 0 && p.v_stride_t > 0;
+}
+
 int indexer_ctas(const dsa_dims& d) {
     const int sms = device_sm_count();
     const int G = indexer_uses_tc(d) ? sms : 2 * sms;
@@ -144,6 +150,19 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                  const uint32_t (&box)[3]) {
+    EncodeTiled fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+    const cuuint64_t s[2] = {strides[0], strides[1]};
+    const cuuint32_t b[3] = {box[0], box[1], box[2]};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, s, b, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -388,11 +407,13 @@ static HierLayout hier_layout(const dsa_dims& d, int T, int n_sel) {
 // ------------------------------------------------------------------------------------------------
 
 struct PromptLayout {
-    size_t n_units;  // int32
-    size_t units;    // PromptUnit [max_units]
+    size_t head;      // PromptHead
+    size_t units;     // PromptUnit [max_units]
+    size_t counters;  // int32 [max_slots * H_kv][2]
+    size_t part_ml;   // float2 [max_slots * H_kv][slot_rows]
+    size_t part_o;    // fp32 [max_slots * H_kv][slot_rows][d_v]
     size_t total;
-    int tile_rows;
-    int max_units;
+    int tile_rows, max_units, ctas, max_slots, slot_rows;
 };
 
 static dsa_status check_prompt_dims(const dsa_prompt_dims* p, int32_t Tq) {
@@ -407,20 +428,34 @@ static dsa_status check_prompt_dims(const dsa_prompt_dims* p, int32_t Tq) {
     for (int64_t s : strides)
         if (s < 0 || s % unit || s > (1ll << 36)) return DSA_ERR_INVALID_ARG;
     // rows (token, head of the group) and tiles are counted in 32 bits
-    if (static_cast<int64_t>(Tq) * (p->H / p->H_kv) + p->B >= (1ll << 31) - (1 << 16)) return DSA_ERR_UNSUPPORTED;
+    const int64_t rows = static_cast<int64_t>(Tq) * (p->H / p->H_kv), limit = (1ll << 31) - (1 << 16);
+    if (rows + p->B >= limit || (rows / kPromptSimtRows + p->B) * p->H_kv >= limit) return DSA_ERR_UNSUPPORTED;
     return DSA_OK;
 }
 
 static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     PromptLayout w{};
-    w.tile_rows = kPromptSimtRows;
+    const int64_t rows = static_cast<int64_t>(Tq) * (p.H / p.H_kv);
+    w.tile_rows = prompt_uses_tc(p) ? kPromptTcRows : kPromptSimtRows;
+    w.ctas = device_sm_count();
+    // The plan splits no more than 2 x ctas partials out of all key heads (see there), so at most
+    // 2 x ctas / H_kv of one head.
+    w.max_slots = 2 * w.ctas / p.H_kv;
+    w.slot_rows = static_cast<int>(rows < w.tile_rows ? rows : w.tile_rows);
     // every sequence fills whole tiles but its last
-    w.max_units = static_cast<int>(static_cast<int64_t>(Tq) * (p.H / p.H_kv) / w.tile_rows) + p.B;
+    w.max_units = static_cast<int>(rows / w.tile_rows) + p.B + w.max_slots;
+    const size_t slots = static_cast<size_t>(w.max_slots) * p.H_kv;
     size_t off = 256;  // the error word
-    w.n_units = off;
+    w.head = off;
     off += 256;
     w.units = off;
     off = align256(off + sizeof(PromptUnit) * static_cast<size_t>(w.max_units));
+    w.counters = off;
+    off = align256(off + sizeof(int32_t) * 2 * slots);
+    w.part_ml = off;
+    off = align256(off + sizeof(float2) * slots * w.slot_rows);
+    w.part_o = off;
+    off = align256(off + sizeof(float) * slots * w.slot_rows * p.d_v);
     w.total = off;
     return w;
 }
@@ -824,9 +859,18 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
         a.err = reinterpret_cast<int*>(base);
         a.tile_rows = L.tile_rows;
         a.max_units = L.max_units;
-        a.n_units = reinterpret_cast<int32_t*>(base + L.n_units);
+        a.ctas = L.ctas;
+        a.max_slots = L.max_slots;
+        a.slot_rows = L.slot_rows;
+        a.head = reinterpret_cast<PromptHead*>(base + L.head);
         a.units = reinterpret_cast<PromptUnit*>(base + L.units);
-        if (!launch_prompt_plan(a, s, &launches) || !launch_prompt_simt(a, s, &launches)) st = DSA_ERR_LAUNCH;
+        a.counters = reinterpret_cast<int32_t*>(base + L.counters);
+        a.part_o = reinterpret_cast<float*>(base + L.part_o);
+        a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+        const bool tc = prompt_uses_tc(*dims);
+        if (!launch_prompt_plan(a, s, &launches) ||
+            !(tc ? launch_prompt_tc(a, s, &launches) : launch_prompt_simt(a, s, &launches)))
+            st = DSA_ERR_LAUNCH;
     }
     g_last_launches = launches;
     return st;

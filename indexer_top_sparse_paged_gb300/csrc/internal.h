@@ -60,6 +60,10 @@ bool attn_uses_tc(const dsa_dims& d);
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t cols, uint64_t rows,
                   uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows);
 
+// The same for a 3-D bf16 tensor (columns dense, the two outer extents at byte strides).
+bool make_tmap_3d(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                  const uint32_t (&box)[3]);
+
 // Raises a kernel's dynamic shared memory limit once per device (cached).
 bool set_max_dynamic_smem(const void* func, size_t bytes);
 
@@ -151,11 +155,23 @@ bool launch_cache_read(const dsa_dims& d, bool kv_fp8, const void* k_cache, cons
 
 // ---- prompt attention ----------------------------------------------------------------------------
 
-constexpr int kPromptSimtRows = 64;  // rows (token, head of the group) per tile
+constexpr int kPromptSimtRows = 64;  // rows (token, head of the group) per unit of the CUDA-core kernel
+constexpr int kPromptTcRows = 256;   // ... of the tensor-core kernel: two tiles of 128
+constexpr int kPromptKeys = 128;     // keys per tile of the work list's key ranges
 
-struct PromptUnit {
-    int seq;   // packed sequence
-    int tile;  // tile of the sequence's rows
+// One unit of work per key head: up to tile_rows rows of a sequence against a range of its key tiles.
+struct alignas(16) PromptUnit {
+    int q0, lq, k0, lk;  // the sequence's first query and key, and their numbers
+    int row0;            // first row (token, head of the group) of the unit within the sequence
+    int kt0, kt1;        // key tiles [kt0, kt1)
+    int slot;            // first partial of the rows' parts (parts > 1)
+    int part, parts;     // this unit's place among the units that share its rows
+    int pad[2];
+};
+
+struct PromptHead {  // written by the plan
+    int n_units;
+    int head_group;  // key heads whose units run next to each other
 };
 
 struct PromptArgs {
@@ -172,14 +188,22 @@ struct PromptArgs {
     void* out;
     float* lse;
     int* err;
-    int tile_rows;      // rows per tile
+    int tile_rows;      // rows per unit
     int max_units;      // bound on the work list's length
-    int32_t* n_units;
+    int ctas;           // CTAs the keys may be split over
+    int max_slots;      // partials the workspace holds, per key head
+    int slot_rows;      // rows of one partial
+    PromptHead* head;
     PromptUnit* units;
+    int32_t* counters;  // [max_slots * H_kv][2] parts that have arrived
+    float* part_o;      // [max_slots * H_kv][slot_rows][d_v] unnormalised outputs
+    float2* part_ml;    // [max_slots * H_kv][slot_rows] (running maximum in powers of two, sum)
 };
 
+bool prompt_uses_tc(const dsa_prompt_dims& p);
 bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches);
 bool launch_prompt_simt(const PromptArgs& a, cudaStream_t s, int* launches);
+bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches);
 
 bool launch_attn_tc(const AttnArgs& a, cudaStream_t s, int* launches);
 bool launch_wait_timeout(int* err, cudaStream_t s, int* launches);

@@ -1,64 +1,153 @@
-// Work list of the prompt attention: the packed sequences' query tiles, found on the device (the host
-// never reads the lengths).
+// Work list of the prompt attention, made on the device (the host never reads the lengths).
 //
 // The G = H / H_kv query heads of a key head share its keys, so a sequence of lq tokens gives each key
-// head one column of lq * G rows, row r = token r / G, head r % G of the group; a tile is kRows of them.
+// head one column of lq * G rows, row r = token r / G, head r % G of the group. A unit is tile_rows of
+// them against a range of the key tiles they see; every unit runs once for each key head.
+//
+// Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads
+// and C CTAs, no unit gets more than max(W / C, kMinTiles) tiles. An item of n tiles over that bound s
+// becomes ceil(n / s) < 2 n / s parts, so all heads together get fewer than 2 W / s <= 2 C partials.
+// Units are listed by falling number of tiles: the last ones to run are the short ones.
 #include "internal.h"
 
 namespace dsa {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kMinTiles = 4;     // a part of fewer tiles costs more to join than it saves
+constexpr int kBuckets = 1024;
+
+struct PlanItem {
+    int q0, lq, k0, lk, row0, tiles;
+};
+
+// Key tiles that rows row0 .. row0 + tile_rows - 1 of a sequence see.
+__device__ __forceinline__ int item_tiles(const PromptArgs& a, int G, int lq, int lk, int row0) {
+    const int last = min(lq * G, row0 + a.tile_rows) - 1;
+    const int seen = a.causal ? min(lk, max(0, last / G + 1 + lk - lq)) : lk;
+    return (seen + kPromptKeys - 1) / kPromptKeys;
+}
+
+__device__ __forceinline__ int block_scan(int x, int* warp_sum) {  // inclusive, over the CTA
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += y;
+        }
+        warp_sum[lane] = w;
+    }
+    __syncthreads();
+    return x + (warp ? warp_sum[warp - 1] : 0);
+}
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a) {
     __shared__ int prefix[kPlanThreads + 1];
+    __shared__ int4 seqs[kPlanThreads];
     __shared__ int warp_sum[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.H / a.H_kv;
-    int done = 0;  // units written for earlier sequences
-    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int n = 0;
-        if (b < a.B) {
-            const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-            if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) atomicOr(a.err, DSA_FAULT_INDEX);
-            else n = static_cast<int>((static_cast<int64_t>(q1 - q0) * G + a.tile_rows - 1) / a.tile_rows);
-        }
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sum[warp] = x;
-        __syncthreads();
-        if (warp == 0) {
-            int w = warp_sum[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
-                if (lane >= o) w += y;
-            }
-            warp_sum[lane] = w;
-        }
-        __syncthreads();
-        prefix[tid + 1] = x + (warp ? warp_sum[warp - 1] : 0);
-        if (tid == 0) prefix[0] = 0;
-        __syncthreads();
-        const int total = prefix[kPlanThreads];
-        for (int i = tid; i < total && done + i < a.max_units; i += kPlanThreads) {
-            int lo = 0, hi = kPlanThreads - 1;  // the last sequence whose first tile is at or before i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (prefix[mid] <= i) lo = mid;
-                else hi = mid - 1;
-            }
-            a.units[done + i] = PromptUnit{b0 + lo, i - prefix[lo]};
-        }
-        done += total;
-        __syncthreads();
+    __shared__ int bucket[kBuckets];
+    __shared__ unsigned long long total_tiles;
+    __shared__ int most_tiles, most_keys, slots;
+    const int tid = threadIdx.x, G = a.H / a.H_kv;
+    griddep_launch_dependents();  // the attention's prologue may start (it waits for this grid)
+    if (tid == 0) {
+        total_tiles = 0;
+        most_tiles = most_keys = slots = 0;
     }
-    if (tid == 0) *a.n_units = min(done, a.max_units);
+    for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
+    for (int i = tid; i < 2 * a.max_slots * a.H_kv; i += kPlanThreads) a.counters[i] = 0;
+    __syncthreads();
+    bool loaded = false;  // up to 1024 sequences stay in shared memory
+    // every item of sequences b0 .. b0 + 1023 in turn, shared out over the threads
+    auto for_items = [&](auto&& f) {
+        for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+            const int b = b0 + tid;
+            if (a.B > kPlanThreads || !loaded) {
+                loaded = true;
+                int n = 0;
+                int4 s = make_int4(0, 0, 0, 0);
+                if (b < a.B) {
+                    const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+                    if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
+                        atomicOr(a.err, DSA_FAULT_INDEX);
+                    } else {
+                        s = make_int4(q0, q1 - q0, k0, k1 - k0);
+                        n = (s.y * G + a.tile_rows - 1) / a.tile_rows;
+                    }
+                }
+                seqs[tid] = s;
+                const int x = block_scan(n, warp_sum);
+                prefix[tid + 1] = x;
+                if (tid == 0) prefix[0] = 0;
+                __syncthreads();
+            }
+            const int total = prefix[kPlanThreads];
+            for (int i = tid; i < total; i += kPlanThreads) {
+                int lo = 0, hi = kPlanThreads - 1;  // the last sequence whose first item is at or before i
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (prefix[mid] <= i) lo = mid;
+                    else hi = mid - 1;
+                }
+                const int4 s = seqs[lo];
+                const int row0 = (i - prefix[lo]) * a.tile_rows;
+                f(PlanItem{s.x, s.y, s.z, s.w, row0, item_tiles(a, G, s.y, s.w, row0)});
+            }
+            __syncthreads();
+        }
+    };
+    for_items([&](const PlanItem& it) {
+        atomicAdd(&total_tiles, static_cast<unsigned long long>(it.tiles));
+        atomicMax(&most_tiles, it.tiles);
+        atomicMax(&most_keys, it.lk);
+    });
+    const long long work = static_cast<long long>(total_tiles) * a.H_kv;
+    const int bound = a.max_slots > 1 ? static_cast<int>(max(static_cast<long long>(kMinTiles), (work + a.ctas - 1) / a.ctas))
+                                      : 1 << 30;
+    const int longest = max(1, min(most_tiles, bound));
+    auto bucket_of = [&](int tiles) {  // falling number of tiles
+        return kBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kBuckets - 1) / longest);
+    };
+    auto parts_of = [&](int tiles) { return max(1, (tiles + bound - 1) / bound); };
+    for_items([&](const PlanItem& it) {
+        const int parts = parts_of(it.tiles);
+        for (int p = 0; p < parts; ++p) {
+            const int t0 = static_cast<int>(static_cast<long long>(it.tiles) * p / parts);
+            const int t1 = static_cast<int>(static_cast<long long>(it.tiles) * (p + 1) / parts);
+            atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
+        }
+    });
+    const int x = block_scan(bucket[tid], warp_sum);
+    if (tid == kPlanThreads - 1) {
+        a.head->n_units = min(x, a.max_units);
+        // heads whose keys and values (read again by every row tile) fit a part of L2 run side by side
+        const long long head_bytes = 2ll * (a.d_qk + a.d_v) * max(1, most_keys);
+        a.head->head_group = static_cast<int>(max(1ll, min(static_cast<long long>(a.H_kv), (48ll << 20) / head_bytes)));
+    }
+    bucket[tid] = x - bucket[tid];
+    __syncthreads();
+    for_items([&](const PlanItem& it) {
+        const int parts = parts_of(it.tiles);
+        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0;
+        for (int p = 0; p < parts; ++p) {
+            const int t0 = static_cast<int>(static_cast<long long>(it.tiles) * p / parts);
+            const int t1 = static_cast<int>(static_cast<long long>(it.tiles) * (p + 1) / parts);
+            const int at = atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
+            if (at < a.max_units && slot + parts <= max(a.max_slots, 1))
+                a.units[at] = PromptUnit{it.q0, it.lq, it.k0, it.lk, it.row0, t0, t1, slot, p, parts, {0, 0}};
+        }
+    });
 }
+static_assert(kBuckets == kPlanThreads, "the bucket scan takes one bucket per thread");
 
 bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
     if (!launch_kernel(false, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a)) return false;

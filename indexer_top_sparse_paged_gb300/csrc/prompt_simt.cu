@@ -7,7 +7,7 @@
 // One CTA per tile of 64 rows (token, head of the group) and key head, one pass over the keys in tiles
 // of 32 with the running maximum and sum of each row in fp32. A thread holds 4 rows x 2 keys of the
 // logits and 4 rows x d_v / 16 columns of the output in registers.
-#include "internal.h"
+#include "prompt.cuh"
 
 namespace dsa {
 namespace psimt {
@@ -46,19 +46,19 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     float* sk = sq + kRows * pq;
     float* sv = sk + kKeys * pq;
     float* sp = sv + kKeys * pv;
+    __shared__ int last_part;
     griddep_wait();
-    if (static_cast<int>(blockIdx.x) >= *a.n_units) return;
+    if (static_cast<int>(blockIdx.x) >= a.head->n_units) return;
     const PromptUnit u = a.units[blockIdx.x];
     const int hk = blockIdx.y, G = a.H / a.H_kv;
-    const int q0 = a.cu_q[u.seq], lq = a.cu_q[u.seq + 1] - q0, k0 = a.cu_k[u.seq], lk = a.cu_k[u.seq + 1] - k0;
-    const int64_t nrows = static_cast<int64_t>(lq) * G, row0 = static_cast<int64_t>(u.tile) * kRows;
+    const int q0 = u.q0, lq = u.lq, k0 = u.k0, lk = u.lk, nrows = lq * G, row0 = u.row0;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     // queries, and for each of the thread's rows the number of keys it sees
     for (int i = tid; i < kRows * (a.d_qk / 4); i += kThreads) {
         const int r = i / (a.d_qk / 4), e = 4 * (i - r * (a.d_qk / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row0 + r < nrows) {
-            const int t = static_cast<int>((row0 + r) / G), g = static_cast<int>((row0 + r) % G);
+            const int t = (row0 + r) / G, g = (row0 + r) % G;
             v = load4(static_cast<const T*>(a.q) + (q0 + t) * a.q_stride_t + (hk * G + g) * a.q_stride_h + e);
         }
         store4(sq + r * pq + e, v);
@@ -66,11 +66,11 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     int seen[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = row0 + 4 * ty + i;
-        seen[i] = r < nrows ? (a.causal ? min(lk, max(0, static_cast<int>(r / G) + 1 + lk - lq)) : lk) : 0;
+        const int r = row0 + 4 * ty + i;
+        seen[i] = r < nrows ? prompt_keys_seen(a, r / G, lq, lk) : 0;
     }
-    const int64_t last = min(nrows, row0 + kRows) - 1;
-    const int n_keys = a.causal ? min(lk, max(0, static_cast<int>(last / G) + 1 + lk - lq)) : lk;
+    // this part's keys, up to the last that the tile's last row sees
+    const int n_keys = min(prompt_keys_seen(a, (min(nrows, row0 + kRows) - 1) / G, lq, lk), u.kt1 * kPromptKeys);
     const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
     float m[4], l[4];
     float4 o[4][kCols];
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int s0 = 0; s0 < n_keys; s0 += kKeys) {
+    for (int s0 = u.kt0 * kPromptKeys; s0 < n_keys; s0 += kKeys) {
         __syncthreads();
         for (int i = tid; i < kKeys * (a.d_qk / 4); i += kThreads) {
             const int r = i / (a.d_qk / 4), e = 4 * (i - r * (a.d_qk / 4));
@@ -156,13 +156,22 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
             }
         }
     }
+    const int64_t slot0 = (static_cast<int64_t>(u.slot) * a.H_kv + static_cast<int64_t>(hk) * u.parts);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], w);
-        const int64_t r = row0 + 4 * ty + i;
-        if (r >= nrows) continue;
-        const int64_t at = (static_cast<int64_t>(q0) + r / G) * a.H + hk * G + r % G;  // (token, head)
+        const int r = 4 * ty + i;
+        if (row0 + r >= nrows) continue;
+        if (u.parts > 1) {
+            const int64_t at = (slot0 + u.part) * a.slot_rows + r;
+            if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                if (4 * tx + 64 * j < a.d_v) *reinterpret_cast<float4*>(a.part_o + at * a.d_v + 4 * tx + 64 * j) = o[i][j];
+            continue;
+        }
+        const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;  // (token, head)
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : 0.0f;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
@@ -172,6 +181,23 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
                        make_float4(o[i][j].x * inv, o[i][j].y * inv, o[i][j].z * inv, o[i][j].w * inv));
         }
         if (tx == 0 && a.lse) a.lse[at] = l[i] > 0.0f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+    }
+    if (u.parts == 1) return;
+    // the last part of these rows to arrive joins them all
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last_part = atomicAdd(&a.counters[2 * slot0], 1) == u.parts - 1;
+    __syncthreads();
+    if (!last_part) return;
+    __threadfence();
+    const int cols = a.d_v / 4;
+    for (int i = tid; i < min(kRows, nrows - row0) * cols; i += kThreads) {
+        const int r = i / cols, e = 4 * (i - r * cols);
+        const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;
+        float lse;
+        const float4 v = prompt_join4(a, slot0, u.parts, r, e, &lse);
+        store4(static_cast<T*>(a.out) + at * a.d_v + e, v);
+        if (e == 0 && a.lse) a.lse[at] = lse;
     }
 }
 

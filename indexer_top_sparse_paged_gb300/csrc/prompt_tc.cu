@@ -1,0 +1,604 @@
+// Dense attention over packed prompts on tcgen05 tensor cores (bf16, d_qk <= 192, d_v <= 128).
+//
+//   z = sm_scale q k^T over the keys j <= i + lk - lq (causal) or all of them, out = softmax(z) v,
+//   lse = log sum exp z; a row without keys gives 0 and -inf.
+//
+// A CTA takes 256 rows (token, head of the group) of one key head as two query tiles A and B of 128 and
+// passes over their keys once, 128 at a time. Tensor memory holds both tiles' logits S (fp32, their bf16
+// weights P written over them) and outputs O (fp32). While the softmax of one tile runs on the CUDA
+// cores, the tensor pipe works for the other: P_A V, Q_A K, P_B V, Q_B K, ... in that order, where Q_X K
+// of the next keys may follow P_X V of the last at once, since the pipe runs in order.
+//
+// Softmax: one thread per row, the running maximum m and sum l in fp32; O is rescaled only when a row's
+// maximum has grown by more than 2^8 since the last time (weights then stay below 2^8, and O and l hold
+// the same factor). Weights are rounded to bf16 for the product (half a step, 2^-8 of a weight, as the
+// values' own); l sums them unrounded, so that lse keeps fp32.
+//
+// Keys and values arrive by TMA as chunks of 128 rows x 64 columns (16 KB, 128-byte swizzle) in a ring
+// shared by both; columns past the width and rows past the tensor read as zeros. Value rows that the
+// sequence does not own are zeroed before the product: a weight of 0 would not silence a NaN there.
+//
+// Roles (384 threads): warps 0-3 softmax and epilogue of tile A, 4-7 of tile B, warp 8 MMA issuer, warp 9
+// TMA, warps 10 and 11 copy the queries of tile A and B (any strides) into the swizzled layout. CTAs are
+// persistent over the plan's work list; the next unit's queries and keys arrive, and its first products
+// run, while the last one's outputs are written.
+#include "prompt.cuh"
+
+namespace dsa {
+namespace ptc {
+
+constexpr int kThreads = 384;
+constexpr int kSoftRegs = 208, kOtherRegs = 80;  // 256 x 208 + 128 x 80 registers of the launch's 384 x 168
+static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * 168, "register shares");
+constexpr int kRows = 128;                     // rows of a query tile
+constexpr int kKeys = kPromptKeys;             // keys of a key tile
+constexpr int kChunk = 128 * 128;              // 128 rows x 64 bf16
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;     // S/P of tile A, B at 0, 128; O at 256, 384
+constexpr uint32_t kIdescQK = idesc_f16(128, kKeys, 1u, 0u, 0u);
+constexpr uint32_t kIdescPV = idesc_f16(128, 64, 1u, 0u, 1u);
+constexpr uint32_t kIdescPV2 = idesc_f16(128, 128, 1u, 0u, 1u);
+constexpr int kMaxStages = 12;                 // chunks in the ring, and groups (key or value tiles) in flight
+constexpr int kSmemMax = 232448;
+
+struct Ctl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: per half of the keys
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+    int last_part[2];
+};
+
+// A turn around the kMaxStages group barriers, with the parity of its phase.
+struct Turn {
+    int i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == kMaxStages) i = 0, phase ^= 1;
+    }
+    __device__ __forceinline__ void back() {
+        if (i-- == 0) i = kMaxStages - 1, phase ^= 1;
+    }
+};
+
+template <int kQC>
+struct Layout {
+    static constexpr size_t kOffRing = 2 * static_cast<size_t>(kQC) * kChunk;
+    static constexpr int kFit = static_cast<int>((kSmemMax - 1024 - sizeof(Ctl) - kOffRing) / kChunk);
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr size_t kOffCtl = kOffRing + static_cast<size_t>(kStages) * kChunk;
+    static constexpr size_t kBytes = 1024 + kOffCtl + sizeof(Ctl);
+};
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// Pairs of fp32 in one 64-bit register: two products or sums an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(v));
+    return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
+// One unit of the work list for one key head.
+struct Work {
+    PromptUnit u;
+    int hk;
+    int nrows;   // rows of the sequence for this head
+    int n0, n1;  // key tiles [kt0, n0) of tile A, [kt0, n1) of tile B
+};
+
+// Units are run head group by head group, the heads of a group side by side.
+__device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int group, int w) {
+    Work x;
+    const int per = n_units * group;  // n_units * H_kv is below 2^31
+    const int g = group == a.H_kv ? 0 : w / per;
+    const int heads = min(group, a.H_kv - g * group);
+    const int rem = w - g * per;
+    const int unit = rem / heads;
+    x.hk = g * group + rem - unit * heads;
+    x.u = a.units[unit];
+    const int G = a.H / a.H_kv;
+    x.nrows = x.u.lq * G;
+    auto tiles = [&](int r0) {
+        int n = 0;
+        if (r0 < x.nrows)
+            n = (prompt_keys_seen(a, (min(x.nrows, r0 + kRows) - 1) / G, x.u.lq, x.u.lk) + kKeys - 1) / kKeys;
+        return max(x.u.kt0, min(x.u.kt1, n));
+    };
+    x.n0 = tiles(x.u.row0);
+    x.n1 = tiles(x.u.row0 + kRows);
+    return x;
+}
+
+template <int kQC, int kVC>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     int k_swap, int v_swap) {
+    using Lay = Layout<kQC>;
+    constexpr int kStages = Lay::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sQ = smem_u32(smem), sRing = smem_u32(smem + Lay::kOffRing);
+    Ctl& S = *reinterpret_cast<Ctl*>(smem + Lay::kOffCtl);
+    volatile int* abort_flag = &S.abort_flag;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(smem_u32(&S.full[i]), 1);
+            mbar_init(smem_u32(&S.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&S.q_full[i]), 32);  // every lane of the copying warp
+            mbar_init(smem_u32(&S.q_free[i]), 1);
+            mbar_init(smem_u32(&S.s_full[i]), 1);
+            mbar_init(smem_u32(&S.p_full[i][0]), 4);
+            mbar_init(smem_u32(&S.p_full[i][1]), 4);
+            mbar_init(smem_u32(&S.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&S.mma_done), 1);
+        S.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&S.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    block_sync();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    griddep_wait();  // the work list
+    const int n_units = a.head->n_units, group = a.head->head_group;
+    const int n_work = n_units * a.H_kv, stride = gridDim.x;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= 10) {
+        // ----------------------------------------------------------------------------- queries
+        // 16-byte pieces of tile x's 128 rows, kPieces to a row; rows and columns past the end are zeros
+        constexpr int kPieces = kQC * 8, kStep = 32 / kPieces > 0 ? 32 / kPieces : 1, kTurns = kPieces > 32 ? kPieces / 32 : 1;
+        static_assert(kPieces == 8 || kPieces == 16 || kPieces == 24, "pieces of a row");
+        const int x = warp - 10, G = a.H / a.H_kv;
+        const int piece = kPieces == 24 ? lane : lane % kPieces;
+        int phase = 1;
+        (void)kTurns;
+        for (int w = blockIdx.x; w < n_work; w += stride) {
+            const Work k = get_work(a, n_units, group, w);
+            if ((x ? k.n1 : k.n0) == k.u.kt0) continue;
+            const int row0 = k.u.row0 + x * kRows;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), phase, abort_flag, a.err))) break;
+            phase ^= 1;
+            if (piece < kPieces) {
+                int r = lane / kPieces;
+                int t = (row0 + r) / G, g = row0 + r - t * G;
+                const uint32_t bytes = piece * 8 < a.d_qk ? 16 : 0;
+                const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(k.u.q0) * a.q_stride_t +
+                                       static_cast<int64_t>(k.hk) * G * a.q_stride_h + (bytes ? piece * 8 : 0);
+                const uint32_t dst = sQ + (x * kQC + piece / 8) * kChunk;
+#pragma unroll 4
+                for (; r < kRows; r += kStep) {
+                    const bool in = row0 + r < k.nrows;
+                    cp_async16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                               in ? base + t * a.q_stride_t + g * a.q_stride_h : static_cast<const uint16_t*>(a.q), in ? bytes : 0);
+                    g += kStep;
+                    while (g >= G) {
+                        g -= G;
+                        ++t;
+                    }
+                }
+            }
+            cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
+        }
+        cp_async_wait<0>();
+    } else if (warp == 9) {
+        // --------------------------------------------------------------------------------- TMA
+        if (lane == 0) {
+            // a group (a key tile of kQC chunks, then its value tile of kVC) fills the ring's next chunks
+            // once the groups that held them are released, in order
+            int slot = 0, in_use = 0;
+            Turn put, freed;
+            bool freed_v = false, ok = true;
+            int groups = 0;
+            auto load = [&](const CUtensorMap* map, int n, int head, int row, int swap) {
+                while (ok && in_use + n > kStages) {
+                    ok = mbar_wait(smem_u32(&S.empty[freed.i]), freed.phase, abort_flag, a.err);
+                    in_use -= freed_v ? kVC : kQC;
+                    freed_v = !freed_v;
+                    freed.next();
+                }
+                if (!ok) return;
+                const uint32_t bar = smem_u32(&S.full[put.i]);
+                mbar_arrive_expect_tx(bar, n * kChunk);
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    if (c == n) break;
+                    if (swap) tma_load_3d(sRing + slot * kChunk, map, c * 64, row, head, bar);
+                    else tma_load_3d(sRing + slot * kChunk, map, c * 64, head, row, bar);
+                    if (++slot == kStages) slot = 0;
+                }
+                in_use += n;
+                put.next();
+                ++groups;
+            };
+            for (int w = blockIdx.x; ok && w < n_work; w += stride) {
+                const Work x = get_work(a, n_units, group, w);
+                const int kh = a.k_stride_h ? x.hk : 0, vh = a.v_stride_h ? x.hk : 0;  // a shared head is stored once
+                const int end = max(x.n0, x.n1);
+                for (int j = x.u.kt0; ok && j < end; ++j) {
+                    const int row = x.u.k0 + j * kKeys;
+                    load(&map_k, kQC, kh, row, k_swap);
+                    load(&map_v, kVC, vh, row, v_swap);
+                }
+            }
+            // nothing may still be landing when the CTA exits
+            for (int i = groups < kMaxStages ? groups : kMaxStages; i > 0; --i) {
+                put.back();
+                mbar_wait_drain(smem_u32(&S.full[put.i]), put.phase, a.err);
+            }
+        }
+    } else {
+        // --------------------------------------------------------------------------------- MMA
+        // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4).
+        int slot = 0;         // the ring's next chunk
+        Turn got, released;   // its group, the next group to give back
+        int qphase0 = 0, qphase1 = 0, pphase0 = 0, pphase1 = 0;
+        bool ok = true;
+        auto next = [&](int s, int n) { return s + n < kStages ? s + n : s + n - kStages; };
+        auto wait = [&](const uint64_t* bar, int phase) {
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), phase, abort_flag, a.err));
+            tc_fence_after();
+        };
+        auto wait_group = [&] {
+            wait(&S.full[got.i], got.phase);
+            got.next();
+        };
+        auto release = [&] {  // once every MMA issued so far is done
+            warp_tc_commit(smem_u32(&S.empty[released.i]));
+            released.next();
+        };
+        const uint64_t dq = sw128_desc(sQ, 16, 1024), dr = sw128_desc(sRing, 16, 1024);
+        const uint64_t dv = sw128_desc(sRing, kChunk, 1024);
+        // S_x = Q_x K^T with the key chunks from ring slot s on
+        auto qk = [&](int x, int s) {
+#pragma unroll
+            for (int c = 0; c < kQC; ++c)
+                warp_mma_ss_x4(tmem + kColS + x * 128, dq + static_cast<uint64_t>(((x * kQC + c) * kChunk) >> 4),
+                               dr + static_cast<uint64_t>((next(s, c) * kChunk) >> 4), kIdescQK, c != 0 ? 1u : 0u);
+            warp_tc_commit(smem_u32(&S.s_full[x]));
+        };
+        // O_x += P_x V with the value chunks from slot s on; `steps` groups of 16 keys
+        auto pv = [&](int x, int s, int steps, bool first, int& phase) {
+            const uint32_t o = tmem + kColO + x * 128, p = tmem + kColS + x * 128;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                wait(&S.p_full[x][hf], phase);
+                if (!ok) return;
+                const int from = hf * (kKeys / 32), n = min(steps - from, kKeys / 32);
+                const uint32_t acc = first && hf == 0 ? 0u : 1u;
+                const uint64_t vd = dv + static_cast<uint64_t>((s * kChunk + from * 2048) >> 4);
+                if (kVC == 2 && s + 1 < kStages) {  // side by side in the ring: all columns in one product
+                    if (n == kKeys / 32) {
+                        warp_mma_ts_x4(o, p + from * 8, vd, kIdescPV2, acc);
+                    } else {
+                        for (int kk = 0; kk < n; ++kk) warp_mma_ts(o, p + (from + kk) * 8, vd + kk * 128, kIdescPV2, kk ? 1u : acc);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kVC; ++c) {
+                        const uint64_t vc = dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
+                        if (n == kKeys / 32) {
+                            warp_mma_ts_x4(o + c * 64, p + from * 8, vc, kIdescPV, acc);
+                        } else {
+                            for (int kk = 0; kk < n; ++kk) warp_mma_ts(o + c * 64, p + (from + kk) * 8, vc + kk * 128, kIdescPV, kk ? 1u : acc);
+                        }
+                    }
+                }
+            }
+            phase ^= 1;
+        };
+        for (int w = blockIdx.x; ok && w < n_work; w += stride) {
+            const Work x = get_work(a, n_units, group, w);
+            const int k_begin = x.u.kt0, lk = x.u.lk, n0 = x.n0, n1 = x.n1, end = max(n0, n1);
+            if (k_begin >= end) continue;
+            if (n0 > k_begin) {  // a tile without keys takes part in nothing
+                wait(&S.q_full[0], qphase0);
+                qphase0 ^= 1;
+            }
+            if (n1 > k_begin) {
+                wait(&S.q_full[1], qphase1);
+                qphase1 ^= 1;
+            }
+            fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
+            wait_group();
+            if (!ok) break;
+            // a tile's last product with its queries frees them
+            if (n0 > k_begin) qk(0, slot);
+            if (n0 == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[0]));
+            if (n1 > k_begin) qk(1, slot);
+            if (n1 == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[1]));
+            slot = next(slot, kQC);
+            release();
+            for (int j = k_begin; j < end; ++j) {
+                const int vs = slot, ks = next(slot, kVC);
+                const bool more = j + 1 < end;
+                wait_group();
+                if (more) wait_group();
+                if (!ok) break;
+                const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
+                const int steps = (valid + 15) / 16;
+                if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
+                    for (int c = 0; c < kVC; ++c) {
+                        uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
+                        for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (j < n0) {
+                    pv(0, vs, steps, j == k_begin, pphase0);
+                    if (j + 1 < n0) qk(0, ks);
+                    if (j + 1 == n0) warp_tc_commit(smem_u32(&S.o_full[0]));
+                    if (j + 2 == n0) warp_tc_commit(smem_u32(&S.q_free[0]));
+                }
+                if (j < n1) {
+                    pv(1, vs, steps, j == k_begin, pphase1);
+                    release();
+                    if (j + 1 < n1) qk(1, ks);
+                    if (j + 1 == n1) warp_tc_commit(smem_u32(&S.o_full[1]));
+                    if (j + 2 == n1) warp_tc_commit(smem_u32(&S.q_free[1]));
+                } else {
+                    release();
+                }
+                if (!ok) break;
+                slot = ks;
+                if (more) {
+                    slot = next(slot, kQC);
+                    release();
+                }
+            }
+        }
+        warp_tc_commit(smem_u32(&S.mma_done));
+        mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // --------------------------------------------------------------------- softmax + epilogue
+        const int x = warp >> 2, r = threadIdx.x & 127;  // tile, row = TMEM lane
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + kColS + x * 128, tO = tmem + lane_base + kColO + x * 128;
+        const int G = a.H / a.H_kv;
+        const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
+        int sphase = 0, ophase = 0;
+        bool dead = false;
+        for (int w = blockIdx.x; w < n_work; w += stride) {
+            const Work k = get_work(a, n_units, group, w);
+            const int row0 = k.u.row0 + x * kRows, row = row0 + r;
+            const int t = row < k.nrows ? row / G : 0, head = k.hk * G + (row < k.nrows ? row - t * G : 0);
+            const int end = x ? k.n1 : k.n0;
+            const bool any = end > k.u.kt0;
+            const int seen = row < k.nrows ? prompt_keys_seen(a, t, k.u.lq, k.u.lk) : 0;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = k.u.kt0; j < end; ++j) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.s_full[x]), sphase, abort_flag, a.err))) {
+                    dead = true;
+                    break;
+                }
+                sphase ^= 1;
+                tc_fence_after();
+                const int vis = seen - j * kKeys;  // keys of the tile this row sees
+                const bool cut = !__all_sync(0xFFFFFFFFu, vis >= kKeys);
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, s[i]);
+                tmem_ld_wait();
+                if (cut) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[i][e] = i * 32 + e < vis ? s[i][e] : 0xFF800000u;
+                }
+                float mx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(__uint_as_float(s[i / 2][16 * (i & 1)]), __uint_as_float(s[i / 2][16 * (i & 1) + 1]));
+#pragma unroll
+                for (int e = 2; e < 16; e += 2)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], __uint_as_float(s[i / 2][16 * (i & 1) + e]), __uint_as_float(s[i / 2][16 * (i & 1) + e + 1]));
+                const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c2;
+                const bool need = mt > m + 8.0f;
+                if (__any_sync(0xFFFFFFFFu, need)) {
+                    const float m_new = need ? mt : m;
+                    if (j > k.u.kt0) {  // P V of the last tile is done: its commit came before S's
+                        const float alpha = m_new == m ? 1.0f : exp2f(m - m_new);
+#pragma unroll 1
+                        for (int c = 0; c < 2 * kVC; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + c * 32, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                            tmem_st32(tO + c * 32, v);
+                        }
+                        l *= alpha;
+                    }
+                    m = m_new;
+                }
+                const float neg = m == -INFINITY ? 0.0f : -m;  // no key yet: every weight is 2^-inf = 0
+                const uint64_t c2c2 = pack2(c2, c2), nn = pack2(neg, neg);
+                uint64_t ls[4] = {0, 0, 0, 0};  // pairs of sums
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 z = unpack2(fma2(pack2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2c2, nn));
+                        const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+                        pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    tmem_st16(tS + i * 16, pk);  // over columns that have been read
+                    if (i & 1) {  // half of the keys: the product may begin
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][i >> 1]));
+                    }
+                }
+                const float2 lp = unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])));
+                l += lp.x + lp.y;
+            }
+            if (any && !dead) {
+                dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.o_full[x]), ophase, abort_flag, a.err));
+                ophase ^= 1;
+            }
+            if (named_bar_or(1 + x, 128, dead)) break;  // every warp of the tile leaves together
+            tc_fence_after();
+            const bool live = row < k.nrows;
+            const int64_t at = (static_cast<int64_t>(k.u.q0) + t) * a.H + head;  // (token, head)
+            if (k.u.parts == 1) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint16_t* out = static_cast<uint16_t*>(a.out) + at * a.d_v;
+#pragma unroll
+                for (int c = 0; c < 2 * kVC; ++c) {
+                    uint32_t v[32];
+                    if (any) {
+                        tmem_ld32(tO + c * 32, v);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y0 = l > 0.0f ? __uint_as_float(v[8 * e + 2 * i]) * inv : 0.0f;
+                            const float y1 = l > 0.0f ? __uint_as_float(v[8 * e + 2 * i + 1]) * inv : 0.0f;
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                            o[i] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                        if (live && c * 32 + e * 8 < a.d_v)
+                            *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (live && a.lse) a.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                const int64_t slot0 = static_cast<int64_t>(k.u.slot) * a.H_kv + static_cast<int64_t>(k.hk) * k.u.parts;
+                const int rr = x * kRows + r;  // row of the partial
+                const int64_t prow = (slot0 + k.u.part) * a.slot_rows + rr;
+                if (live) a.part_ml[prow] = make_float2(l > 0.0f ? m : -INFINITY, l);
+#pragma unroll 1
+                for (int c = 0; c < 2 * kVC && any; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(tO + c * 32, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (live && c * 32 + e * 4 < a.d_v)
+                            *reinterpret_cast<uint4*>(a.part_o + prow * a.d_v + c * 32 + e * 4) =
+                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+                // the last part of this tile's rows to arrive joins them all
+                __threadfence();
+                named_bar_sync(1 + x, 128);
+                if (r == 0) S.last_part[x] = atomicAdd(&a.counters[2 * slot0 + x], 1) == k.u.parts - 1;
+                named_bar_sync(1 + x, 128);
+                if (S.last_part[x]) {
+                    __threadfence();
+                    const int cols = a.d_v / 4, rows = min(kRows, k.nrows - row0);
+                    for (int i = r; i < rows * cols; i += 128) {
+                        const int jr = i / cols, e = 4 * (i - jr * cols);
+                        const int jt = (row0 + jr) / G;
+                        const int64_t jat = (static_cast<int64_t>(k.u.q0) + jt) * a.H + k.hk * G + (row0 + jr - jt * G);
+                        float lse;
+                        const float4 o = prompt_join4(a, slot0, k.u.parts, x * kRows + jr, e, &lse);
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + jat * a.d_v + e) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        if (e == 0 && a.lse) a.lse[jat] = lse;
+                    }
+                }
+            }
+            tc_fence_before();  // O has been read before the next unit's first product may overwrite it
+        }
+    }
+    tc_fence_before();
+    block_sync();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// A map of [tokens][heads][cols] with boxes of 128 tokens x 64 columns; the outer extent is the one of
+// the larger stride (*swap: heads). A stride of 0 between the heads: they share one.
+static bool make_map(CUtensorMap* map, const void* base, int cols, int heads, int tokens, int64_t stride_t, int64_t stride_h,
+                     int* swap) {
+    if (stride_h == 0) heads = 1;
+    if (heads == 1) stride_h = stride_t;
+    if (tokens == 1) stride_t = stride_h;
+    *swap = stride_h > stride_t ? 1 : 0;
+    const uint64_t n[2] = {static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
+    const uint64_t st[2] = {static_cast<uint64_t>(stride_h) * 2, static_cast<uint64_t>(stride_t) * 2};
+    const uint32_t bx[2] = {1, 128};
+    const int i = *swap, j = 1 - i;
+    return make_tmap_3d(map, base, {static_cast<uint64_t>(cols), n[i], n[j]}, {st[i], st[j]}, {64, bx[i], bx[j]});
+}
+
+template <int kQC, int kVC>
+static bool launch_typed(const PromptArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int ks, int vs, cudaStream_t s) {
+    constexpr size_t smem = Layout<kQC>::kBytes;
+    static_assert(smem <= kSmemMax && Layout<kQC>::kStages >= 2 * kQC + kVC, "two key tiles and a value tile in flight");
+    if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_tc_kernel<kQC, kVC>), smem)) return false;
+    const int64_t most = static_cast<int64_t>(a.max_units) * a.H_kv;  // below 2^31 (checked by the caller)
+    const int grid = static_cast<int>(most < a.ctas ? most : a.ctas);
+    return launch_kernel(true, prompt_tc_kernel<kQC, kVC>, dim3(grid), dim3(kThreads), smem, s, a, mk, mv, ks, vs);
+}
+
+}  // namespace ptc
+
+bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches) {
+    CUtensorMap mk{}, mv{};
+    int ks = 0, vs = 0;
+    // without keys no tile is loaded and no map read
+    if (a.Tk > 0 && (!ptc::make_map(&mk, a.k, a.d_qk, a.H_kv, a.Tk, a.k_stride_t, a.k_stride_h, &ks) ||
+                     !ptc::make_map(&mv, a.v, a.d_v, a.H_kv, a.Tk, a.v_stride_t, a.v_stride_h, &vs)))
+        return false;
+    const int qc = (a.d_qk + 63) / 64;
+    bool ok;
+    if (a.d_v <= 64)
+        ok = qc == 1 ? ptc::launch_typed<1, 1>(a, mk, mv, ks, vs, s)
+                     : qc == 2 ? ptc::launch_typed<2, 1>(a, mk, mv, ks, vs, s) : ptc::launch_typed<3, 1>(a, mk, mv, ks, vs, s);
+    else
+        ok = qc == 1 ? ptc::launch_typed<1, 2>(a, mk, mv, ks, vs, s)
+                     : qc == 2 ? ptc::launch_typed<2, 2>(a, mk, mv, ks, vs, s) : ptc::launch_typed<3, 2>(a, mk, mv, ks, vs, s);
+    if (ok) ++*launches;
+    return ok;
+}
+
+}  // namespace dsa

@@ -114,6 +114,18 @@ def test_longer_prompts(dtype):
         check(attend(q, k, v, nq, nk, d_qk ** -0.5), q, k, v, nq, nk, d_qk ** -0.5)
 
 
+def test_many_short_sequences():
+    """Several units a CTA, most of them with one short query tile, some with no keys: every one in turn."""
+    nq = [100, 1, 128, 129, 3, 0, 256, 257, 40] * 9
+    nk = [max(0, n - 7) if i % 4 == 0 else n + 5 * (i % 3) for i, n in enumerate(nq)]
+    q, k, v = make(torch.bfloat16, nq, nk, 16, 16, 192, 128, seed=11, pad=3)
+    check(attend(q, k, v, nq, nk, 192 ** -0.5), q, k, v, nq, nk, 192 ** -0.5)
+    nq = [1] * 1500  # more sequences than the plan looks at in one go
+    nk = [i % 5 for i in range(1500)]
+    q, k, v = make(torch.bfloat16, nq, nk, 4, 2, 64, 64, seed=12)
+    check(attend(q, k, v, nq, nk, 0.125), q, k, v, nq, nk, 0.125)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_large_and_growing_logits(dtype):
     """Scores that grow along the keys move every row's running maximum in every tile; then a few huge ones."""
