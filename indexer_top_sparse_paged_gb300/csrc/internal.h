@@ -172,6 +172,7 @@ struct alignas(16) PromptUnit {
 struct PromptHead {  // written by the plan
     int n_units;
     int head_group;  // key heads whose units run next to each other
+    int next;        // units drawn, beyond every CTA's first
 };
 
 struct PromptArgs {

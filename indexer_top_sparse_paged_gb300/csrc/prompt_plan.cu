@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     const int x = block_scan(bucket[tid], warp_sum);
     if (tid == kPlanThreads - 1) {
         a.head->n_units = min(x, a.max_units);
+        a.head->next = 0;
         // heads whose keys and values (read again by every row tile) fit a part of L2 run side by side
         const long long head_bytes = 2ll * (a.d_qk + a.d_v) * max(1, most_keys);
         a.head->head_group = static_cast<int>(max(1ll, min(static_cast<long long>(a.H_kv), (48ll << 20) / head_bytes)));

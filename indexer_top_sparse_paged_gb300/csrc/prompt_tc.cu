@@ -18,10 +18,11 @@
 // shared by both; columns past the width and rows past the tensor read as zeros. Value rows that the
 // sequence does not own are zeroed before the product: a weight of 0 would not silence a NaN there.
 //
-// Roles (384 threads): warps 0-3 softmax and epilogue of tile A, 4-7 of tile B, warp 8 MMA issuer, warp 9
-// TMA, warps 10 and 11 copy the queries of tile A and B (any strides) into the swizzled layout. CTAs are
-// persistent over the plan's work list; the next unit's queries and keys arrive, and its first products
-// run, while the last one's outputs are written.
+// Roles (384 threads): warps 0-3 softmax and epilogue of tile A, 4-7 of tile B, warps 8 and 9 issue the
+// MMAs of tile A and B (two issuers: the tensor pipe takes little work ahead, and one's waits and commits
+// would leave it idle), warp 10 loads keys and values, warp 11 hands out the units and loads queries. CTAs are
+// persistent and draw units from the plan's list by a counter; the next unit's queries and keys arrive,
+// and its first products run, while the last one's outputs are written.
 #include "prompt.cuh"
 
 namespace dsa {
@@ -41,9 +42,25 @@ constexpr uint32_t kIdescPV2 = idesc_f16(128, 128, 1u, 0u, 1u);
 constexpr int kMaxStages = 12;                 // chunks in the ring, and groups (key or value tiles) in flight
 constexpr int kSmemMax = 232448;
 
+// One unit of the work list for one key head.
+struct Work {
+    int q0, lq, k0, lk, row0, kt0;
+    int slot, part, parts;
+    int hk;      // key head; -1: no more work
+    int nrows;   // rows of the sequence for this head
+    int n0, n1;  // key tiles [kt0, n0) of tile A, [kt0, n1) of tile B
+    int pad[3];
+};
+
+constexpr int kQueue = 2;            // units handed out and not yet taken up by every role
+constexpr int kTakers = 11;          // 8 softmax warps, 2 MMA warps, the key loader
+
 struct Ctl {
+    Work work[kQueue];
+    uint64_t work_full[kQueue], work_free[kQueue];
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: per half of the keys
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: the first 96 keys' weights, the rest
+    uint64_t turn[2];  // the tensor pipe's next turn belongs to tile A, B
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
@@ -103,13 +120,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return y;
 }
 
-// One unit of the work list for one key head.
-struct Work {
-    PromptUnit u;
-    int hk;
-    int nrows;   // rows of the sequence for this head
-    int n0, n1;  // key tiles [kt0, n0) of tile A, [kt0, n1) of tile B
-};
+// Eight words to a 32-byte aligned address.
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 
 // Units are run head group by head group, the heads of a group side by side.
 __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int group, int w) {
@@ -120,24 +136,26 @@ __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int g
     const int rem = w - g * per;
     const int unit = rem / heads;
     x.hk = g * group + rem - unit * heads;
-    x.u = a.units[unit];
+    const PromptUnit u = a.units[unit];
     const int G = a.H / a.H_kv;
-    x.nrows = x.u.lq * G;
+    x.nrows = u.lq * G;
     auto tiles = [&](int r0) {
         int n = 0;
         if (r0 < x.nrows)
-            n = (prompt_keys_seen(a, (min(x.nrows, r0 + kRows) - 1) / G, x.u.lq, x.u.lk) + kKeys - 1) / kKeys;
-        return max(x.u.kt0, min(x.u.kt1, n));
+            n = (prompt_keys_seen(a, (min(x.nrows, r0 + kRows) - 1) / G, u.lq, u.lk) + kKeys - 1) / kKeys;
+        return max(u.kt0, min(u.kt1, n));
     };
-    x.n0 = tiles(x.u.row0);
-    x.n1 = tiles(x.u.row0 + kRows);
+    x.n0 = tiles(u.row0);
+    x.n1 = tiles(u.row0 + kRows);
+    x.q0 = u.q0, x.lq = u.lq, x.k0 = u.k0, x.lk = u.lk, x.row0 = u.row0, x.kt0 = u.kt0;
+    x.slot = u.slot, x.part = u.part, x.parts = u.parts;
     return x;
 }
 
 template <int kQC, int kVC>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     int k_swap, int v_swap) {
+    prompt_tc_kernel(PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, int q_map, int k_swap, int v_swap) {
     using Lay = Layout<kQC>;
     constexpr int kStages = Lay::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -150,17 +168,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_u32(&S.full[i]), 1);
-            mbar_init(smem_u32(&S.empty[i]), 1);
+            mbar_init(smem_u32(&S.empty[i]), 2);  // both tiles are done with the group
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&S.q_full[i]), 32);  // every lane of the copying warp
+            mbar_init(smem_u32(&S.q_full[i]), q_map ? 1 : 32);  // TMA, or every lane of the copying warp
             mbar_init(smem_u32(&S.q_free[i]), 1);
             mbar_init(smem_u32(&S.s_full[i]), 1);
+            mbar_init(smem_u32(&S.turn[i]), 1);
             mbar_init(smem_u32(&S.p_full[i][0]), 4);
             mbar_init(smem_u32(&S.p_full[i][1]), 4);
             mbar_init(smem_u32(&S.o_full[i]), 1);
         }
-        mbar_init(smem_u32(&S.mma_done), 1);
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(smem_u32(&S.work_full[i]), 1);
+            mbar_init(smem_u32(&S.work_free[i]), kTakers);
+        }
+        mbar_init(smem_u32(&S.mma_done), 2);
         S.abort_flag = 0;
         fence_mbar_init();
     }
@@ -174,50 +197,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = S.tmem_base;
     griddep_wait();  // the work list
     const int n_units = a.head->n_units, group = a.head->head_group;
-    const int n_work = n_units * a.H_kv, stride = gridDim.x;
+    const int n_work = n_units * a.H_kv;
+    // The next unit, for every role but the one that hands them out; false: no more, or a wait gave up.
+    int turn = 0, turn_phase = 0;
+    auto take = [&](Work& k) {
+        const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.work_full[turn]), turn_phase, abort_flag, a.err));
+        if (!got) return false;
+        k = S.work[turn];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&S.work_free[turn]));
+        if (++turn == kQueue) turn = 0, turn_phase ^= 1;
+        return k.hk >= 0;
+    };
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp >= 10) {
-        // ----------------------------------------------------------------------------- queries
-        // 16-byte pieces of tile x's 128 rows, kPieces to a row; rows and columns past the end are zeros
-        constexpr int kPieces = kQC * 8, kStep = 32 / kPieces > 0 ? 32 / kPieces : 1, kTurns = kPieces > 32 ? kPieces / 32 : 1;
-        static_assert(kPieces == 8 || kPieces == 16 || kPieces == 24, "pieces of a row");
-        const int x = warp - 10, G = a.H / a.H_kv;
-        const int piece = kPieces == 24 ? lane : lane % kPieces;
-        int phase = 1;
-        (void)kTurns;
-        for (int w = blockIdx.x; w < n_work; w += stride) {
-            const Work k = get_work(a, n_units, group, w);
-            if ((x ? k.n1 : k.n0) == k.u.kt0) continue;
-            const int row0 = k.u.row0 + x * kRows;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), phase, abort_flag, a.err))) break;
-            phase ^= 1;
-            if (piece < kPieces) {
-                int r = lane / kPieces;
-                int t = (row0 + r) / G, g = row0 + r - t * G;
-                const uint32_t bytes = piece * 8 < a.d_qk ? 16 : 0;
-                const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(k.u.q0) * a.q_stride_t +
-                                       static_cast<int64_t>(k.hk) * G * a.q_stride_h + (bytes ? piece * 8 : 0);
-                const uint32_t dst = sQ + (x * kQC + piece / 8) * kChunk;
+    if (warp == 11) {
+        // ------------------------------------------------------------------ units and their queries
+        const int G = a.H / a.H_kv;
+        int qphase0 = 1, qphase1 = 1, fphase = 1, slot = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; ok;) {
+            Work k;
+            k.hk = -1;
+            if (w < n_work) k = get_work(a, n_units, group, w);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.work_free[slot]), fphase, abort_flag, a.err));
+            if (!ok) break;
+            if (lane == 0) {
+                S.work[slot] = k;
+                mbar_arrive(smem_u32(&S.work_full[slot]));
+                if (k.hk >= 0) w = gridDim.x + atomicAdd(&a.head->next, 1);
+            }
+            if (++slot == kQueue) slot = 0, fphase ^= 1;
+            w = __shfl_sync(0xFFFFFFFFu, w, 0);
+            if (k.hk < 0) break;
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+                if ((x ? k.n1 : k.n0) == k.kt0) continue;  // no keys: the tile's queries are not used
+                const int row0 = k.row0 + x * kRows;
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), x ? qphase1 : qphase0, abort_flag, a.err));
+                if (!ok) break;
+                if (x) qphase1 ^= 1;
+                else qphase0 ^= 1;
+                const uint32_t dst = sQ + x * kQC * kChunk;
+                if (q_map) {  // 128 / G tokens of G heads; what lies behind the sequence is never used
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(smem_u32(&S.q_full[x]), kQC * kChunk);
+#pragma unroll
+                        for (int c = 0; c < kQC; ++c)
+                            tma_load_3d(dst + c * kChunk, &map_q, c * 64, k.hk * G, k.q0 + row0 / G, smem_u32(&S.q_full[x]));
+                    }
+                    continue;
+                }
+                // 16-byte pieces of 128 rows, kPieces to a row; rows and columns past the end are zeros
+                constexpr int kPieces = kQC * 8, kStep = 32 / kPieces;
+                const int piece = lane % kPieces;
+                if (lane < kStep * kPieces) {
+                    int r = lane / kPieces;
+                    int t = (row0 + r) / G, g = row0 + r - t * G;
+                    const uint32_t bytes = piece * 8 < a.d_qk ? 16 : 0;
+                    const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(k.q0) * a.q_stride_t +
+                                           static_cast<int64_t>(k.hk) * G * a.q_stride_h + (bytes ? piece * 8 : 0);
 #pragma unroll 4
-                for (; r < kRows; r += kStep) {
-                    const bool in = row0 + r < k.nrows;
-                    cp_async16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
-                               in ? base + t * a.q_stride_t + g * a.q_stride_h : static_cast<const uint16_t*>(a.q), in ? bytes : 0);
-                    g += kStep;
-                    while (g >= G) {
-                        g -= G;
-                        ++t;
+                    for (; r < kRows; r += kStep) {
+                        const bool in = row0 + r < k.nrows;
+                        cp_async16(dst + (piece / 8) * kChunk + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                                   in ? base + t * a.q_stride_t + g * a.q_stride_h : static_cast<const uint16_t*>(a.q), in ? bytes : 0);
+                        g += kStep;
+                        while (g >= G) {
+                            g -= G;
+                            ++t;
+                        }
                     }
                 }
+                cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
             }
-            cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
         }
+        // nothing may still be landing when the CTA exits
         cp_async_wait<0>();
-    } else if (warp == 9) {
+        if (q_map && lane == 0) {  // each tile's last load has this phase
+            mbar_wait_drain(smem_u32(&S.q_full[0]), qphase0, a.err);
+            mbar_wait_drain(smem_u32(&S.q_full[1]), qphase1, a.err);
+        }
+    } else if (warp == 10) {
         // --------------------------------------------------------------------------------- TMA
-        if (lane == 0) {
             // a group (a key tile of kQC chunks, then its value tile of kVC) fills the ring's next chunks
             // once the groups that held them are released, in order
             int slot = 0, in_use = 0;
@@ -245,28 +308,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put.next();
                 ++groups;
             };
-            for (int w = blockIdx.x; ok && w < n_work; w += stride) {
-                const Work x = get_work(a, n_units, group, w);
-                const int kh = a.k_stride_h ? x.hk : 0, vh = a.v_stride_h ? x.hk : 0;  // a shared head is stored once
-                const int end = max(x.n0, x.n1);
-                for (int j = x.u.kt0; ok && j < end; ++j) {
-                    const int row = x.u.k0 + j * kKeys;
-                    load(&map_k, kQC, kh, row, k_swap);
-                    load(&map_v, kVC, vh, row, v_swap);
+            for (Work k; ok && take(k);) {
+                if (lane == 0) {
+                    const int kh = a.k_stride_h ? k.hk : 0, vh = a.v_stride_h ? k.hk : 0;  // a shared head is stored once
+                    const int end = max(k.n0, k.n1);
+                    for (int j = k.kt0; ok && j < end; ++j) {
+                        const int row = k.k0 + j * kKeys;
+                        load(&map_k, kQC, kh, row, k_swap);
+                        load(&map_v, kVC, vh, row, v_swap);
+                    }
                 }
+                ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
             }
             // nothing may still be landing when the CTA exits
             for (int i = groups < kMaxStages ? groups : kMaxStages; i > 0; --i) {
                 put.back();
                 mbar_wait_drain(smem_u32(&S.full[put.i]), put.phase, a.err);
             }
-        }
     } else {
         // --------------------------------------------------------------------------------- MMA
         // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4).
-        int slot = 0;         // the ring's next chunk
-        Turn got, released;   // its group, the next group to give back
-        int qphase0 = 0, qphase1 = 0, pphase0 = 0, pphase1 = 0;
+        const int x = warp - 8;  // tile
+        int slot = 0;            // the ring's next chunk
+        Turn got, released;      // its group, the next group to give back
+        int qphase = 0, pphase = 0, tphase = 1 - x;  // the first turn is tile A's
         bool ok = true;
         auto next = [&](int s, int n) { return s + n < kStages ? s + n : s + n - kStages; };
         auto wait = [&](const uint64_t* bar, int phase) {
@@ -277,106 +342,104 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&S.full[got.i], got.phase);
             got.next();
         };
-        auto release = [&] {  // once every MMA issued so far is done
+        auto release = [&] {  // once every MMA that this warp has issued is done
             warp_tc_commit(smem_u32(&S.empty[released.i]));
             released.next();
         };
-        const uint64_t dq = sw128_desc(sQ, 16, 1024), dr = sw128_desc(sRing, 16, 1024);
+        const uint32_t tS = tmem + kColS + x * 128, tO = tmem + kColO + x * 128;
+        const uint64_t dq = sw128_desc(sQ + x * kQC * kChunk, 16, 1024), dk = sw128_desc(sRing, 16, 1024);
         const uint64_t dv = sw128_desc(sRing, kChunk, 1024);
-        // S_x = Q_x K^T with the key chunks from ring slot s on
-        auto qk = [&](int x, int s) {
+        // While both tiles have work they take turns, so that each tile's product with its weights and the
+        // next one with its keys run back to back: interleaved, both tiles' logits would be ready at the
+        // same time, and the pipe idle while both softmaxes work.
+        auto take_turn = [&](bool both) {
+            if (!both) return;
+            wait(&S.turn[x], tphase);
+            tphase ^= 1;
+        };
+        auto pass_turn = [&](bool both) {
+            if (both && lane == 0) mbar_arrive(smem_u32(&S.turn[x ^ 1]));
+            __syncwarp();
+        };
+        // S = Q K^T with the key chunks from ring slot s on; the turn goes over before the last of them
+        auto qk = [&](int s, bool both) {
 #pragma unroll
-            for (int c = 0; c < kQC; ++c)
-                warp_mma_ss_x4(tmem + kColS + x * 128, dq + static_cast<uint64_t>(((x * kQC + c) * kChunk) >> 4),
-                               dr + static_cast<uint64_t>((next(s, c) * kChunk) >> 4), kIdescQK, c != 0 ? 1u : 0u);
+            for (int c = 0; c < kQC; ++c) {
+                if (c == kQC - 1) pass_turn(both);
+                warp_mma_ss_x4(tS, dq + static_cast<uint64_t>((c * kChunk) >> 4),
+                               dk + static_cast<uint64_t>((next(s, c) * kChunk) >> 4), kIdescQK, c != 0 ? 1u : 0u);
+            }
             warp_tc_commit(smem_u32(&S.s_full[x]));
         };
-        // O_x += P_x V with the value chunks from slot s on; `steps` groups of 16 keys
-        auto pv = [&](int x, int s, int steps, bool first, int& phase) {
-            const uint32_t o = tmem + kColO + x * 128, p = tmem + kColS + x * 128;
+        // O += P V with the value chunks from slot s on, steps [from, from + most) of the `steps` groups of
+        // 16 keys that the sequence has there
+        auto pv = [&](int from, int most, int s, int steps, bool first) {
+            const int n = min(steps - from, most);
+            const uint32_t acc = first && from == 0 ? 0u : 1u;
+            const uint64_t vd = dv + static_cast<uint64_t>((s * kChunk + from * 2048) >> 4);
+            const bool wide = kVC == 2 && s + 1 < kStages;  // side by side in the ring: all columns in one product
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                wait(&S.p_full[x][hf], phase);
-                if (!ok) return;
-                const int from = hf * (kKeys / 32), n = min(steps - from, kKeys / 32);
-                const uint32_t acc = first && hf == 0 ? 0u : 1u;
-                const uint64_t vd = dv + static_cast<uint64_t>((s * kChunk + from * 2048) >> 4);
-                if (kVC == 2 && s + 1 < kStages) {  // side by side in the ring: all columns in one product
-                    if (n == kKeys / 32) {
-                        warp_mma_ts_x4(o, p + from * 8, vd, kIdescPV2, acc);
-                    } else {
-                        for (int kk = 0; kk < n; ++kk) warp_mma_ts(o, p + (from + kk) * 8, vd + kk * 128, kIdescPV2, kk ? 1u : acc);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kVC; ++c) {
-                        const uint64_t vc = dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
-                        if (n == kKeys / 32) {
-                            warp_mma_ts_x4(o + c * 64, p + from * 8, vc, kIdescPV, acc);
-                        } else {
-                            for (int kk = 0; kk < n; ++kk) warp_mma_ts(o + c * 64, p + (from + kk) * 8, vc + kk * 128, kIdescPV, kk ? 1u : acc);
-                        }
-                    }
+            for (int c = 0; c < kVC; ++c) {
+                if (c > 0 && wide) break;
+                const uint64_t vc = wide ? vd : dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
+                const uint32_t o = tO + c * 64, idesc = wide ? kIdescPV2 : kIdescPV;
+                int kk = 0;
+                if (n >= 4) {
+                    warp_mma_ts_x4(o, tS + from * 8, vc, idesc, acc);
+                    kk = 4;
                 }
+                for (; kk < n; ++kk) warp_mma_ts(o, tS + (from + kk) * 8, vc + kk * 128, idesc, kk ? 1u : acc);
             }
-            phase ^= 1;
         };
-        for (int w = blockIdx.x; ok && w < n_work; w += stride) {
-            const Work x = get_work(a, n_units, group, w);
-            const int k_begin = x.u.kt0, lk = x.u.lk, n0 = x.n0, n1 = x.n1, end = max(n0, n1);
+        for (Work k; ok && take(k);) {
+            const int k_begin = k.kt0, lk = k.lk, n = x ? k.n1 : k.n0, end = max(k.n0, k.n1);
             if (k_begin >= end) continue;
-            if (n0 > k_begin) {  // a tile without keys takes part in nothing
-                wait(&S.q_full[0], qphase0);
-                qphase0 ^= 1;
+            if (n > k_begin) {  // a tile without keys only walks the groups
+                wait(&S.q_full[x], qphase);
+                qphase ^= 1;
+                fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
             }
-            if (n1 > k_begin) {
-                wait(&S.q_full[1], qphase1);
-                qphase1 ^= 1;
-            }
-            fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
             wait_group();
+            const int both_end = min(k.n0, k.n1);  // key tiles [k_begin, both_end): both tiles work
+            take_turn(k_begin < both_end);
             if (!ok) break;
-            // a tile's last product with its queries frees them
-            if (n0 > k_begin) qk(0, slot);
-            if (n0 == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[0]));
-            if (n1 > k_begin) qk(1, slot);
-            if (n1 == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[1]));
+            if (n > k_begin) qk(slot, k_begin < both_end);
+            if (n == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[x]));  // the last product with these queries
             slot = next(slot, kQC);
             release();
             for (int j = k_begin; j < end; ++j) {
                 const int vs = slot, ks = next(slot, kVC);
-                const bool more = j + 1 < end;
+                const bool more = j + 1 < end, both = j < both_end, qk_next = j + 1 < n;
                 wait_group();
                 if (more) wait_group();
                 if (!ok) break;
-                const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
-                const int steps = (valid + 15) / 16;
-                if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
-                    for (int c = 0; c < kVC; ++c) {
-                        uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
-                        for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+                if (j < n) {
+                    const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
+                    const int steps = (valid + 15) / 16;
+                    if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
+                        for (int c = 0; c < kVC; ++c) {  // (both tiles' warps write the same zeros)
+                            uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
+                            for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    wait(&S.p_full[x][0], pphase);
+                    take_turn(both);
+                    if (!ok) break;
+                    pv(0, 6, vs, steps, j == k_begin);
+                    wait(&S.p_full[x][1], pphase);
+                    pphase ^= 1;
+                    if (!ok) break;
+                    if (!qk_next) pass_turn(both);
+                    pv(6, 2, vs, steps, j == k_begin);
+                    if (j + 1 == n) warp_tc_commit(smem_u32(&S.o_full[x]));
                 }
-                if (j < n0) {
-                    pv(0, vs, steps, j == k_begin, pphase0);
-                    if (j + 1 < n0) qk(0, ks);
-                    if (j + 1 == n0) warp_tc_commit(smem_u32(&S.o_full[0]));
-                    if (j + 2 == n0) warp_tc_commit(smem_u32(&S.q_free[0]));
-                }
-                if (j < n1) {
-                    pv(1, vs, steps, j == k_begin, pphase1);
-                    release();
-                    if (j + 1 < n1) qk(1, ks);
-                    if (j + 1 == n1) warp_tc_commit(smem_u32(&S.o_full[1]));
-                    if (j + 2 == n1) warp_tc_commit(smem_u32(&S.q_free[1]));
-                } else {
-                    release();
-                }
-                if (!ok) break;
+                release();
                 slot = ks;
                 if (more) {
+                    if (qk_next) qk(ks, both);
+                    if (j + 2 == n) warp_tc_commit(smem_u32(&S.q_free[x]));
                     slot = next(slot, kQC);
                     release();
                 }
@@ -395,15 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
         int sphase = 0, ophase = 0;
         bool dead = false;
-        for (int w = blockIdx.x; w < n_work; w += stride) {
-            const Work k = get_work(a, n_units, group, w);
-            const int row0 = k.u.row0 + x * kRows, row = row0 + r;
+        for (;;) {
+            // every warp of the tile leaves at the same barrier, so that none waits there for one that left
+            Work k;
+            const bool got = take(k);
+            if (named_bar_or(1 + x, 128, !got)) break;
+            const int row0 = k.row0 + x * kRows, row = row0 + r;
             const int t = row < k.nrows ? row / G : 0, head = k.hk * G + (row < k.nrows ? row - t * G : 0);
             const int end = x ? k.n1 : k.n0;
-            const bool any = end > k.u.kt0;
-            const int seen = row < k.nrows ? prompt_keys_seen(a, t, k.u.lq, k.u.lk) : 0;
+            const bool any = end > k.kt0;
+            const int seen = row < k.nrows ? prompt_keys_seen(a, t, k.lq, k.lk) : 0;
             float m = -INFINITY, l = 0.0f;
-            for (int j = k.u.kt0; j < end; ++j) {
+            for (int j = k.kt0; j < end; ++j) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.s_full[x]), sphase, abort_flag, a.err))) {
                     dead = true;
                     break;
@@ -433,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need = mt > m + 8.0f;
                 if (__any_sync(0xFFFFFFFFu, need)) {
                     const float m_new = need ? mt : m;
-                    if (j > k.u.kt0) {  // P V of the last tile is done: its commit came before S's
+                    if (j > k.kt0) {  // P V of the last tile is done: its commit came before S's
                         const float alpha = m_new == m ? 1.0f : exp2f(m - m_new);
 #pragma unroll 1
                         for (int c = 0; c < 2 * kVC; ++c) {
@@ -463,11 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[e] = *reinterpret_cast<const uint32_t*>(&b);
                     }
                     tmem_st16(tS + i * 16, pk);  // over columns that have been read
-                    if (i & 1) {  // half of the keys: the product may begin
+                    if (i >= 2) {  // the product may begin while the last quarter is made
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][i >> 1]));
+                        if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][i - 2]));
                     }
                 }
                 const float2 lp = unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])));
@@ -480,10 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (named_bar_or(1 + x, 128, dead)) break;  // every warp of the tile leaves together
             tc_fence_after();
             const bool live = row < k.nrows;
-            const int64_t at = (static_cast<int64_t>(k.u.q0) + t) * a.H + head;  // (token, head)
-            if (k.u.parts == 1) {
+            const int64_t at = (static_cast<int64_t>(k.q0) + t) * a.H + head;  // (token, head)
+            if (k.parts == 1) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 uint16_t* out = static_cast<uint16_t*>(a.out) + at * a.d_v;
+                const bool sectors = a.d_v % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
                 for (int c = 0; c < 2 * kVC; ++c) {
                     uint32_t v[32];
@@ -492,24 +559,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t o[4];
+                    for (int e = 0; e < 32; e += 16) {  // a whole 32-byte sector a store, where rows allow it
+                        uint32_t o[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float y0 = l > 0.0f ? __uint_as_float(v[8 * e + 2 * i]) * inv : 0.0f;
-                            const float y1 = l > 0.0f ? __uint_as_float(v[8 * e + 2 * i + 1]) * inv : 0.0f;
+                        for (int i = 0; i < 8; ++i) {
+                            const float y0 = l > 0.0f ? __uint_as_float(v[e + 2 * i]) * inv : 0.0f;
+                            const float y1 = l > 0.0f ? __uint_as_float(v[e + 2 * i + 1]) * inv : 0.0f;
                             const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
                             o[i] = *reinterpret_cast<const uint32_t*>(&b);
                         }
-                        if (live && c * 32 + e * 8 < a.d_v)
-                            *reinterpret_cast<uint4*>(out + c * 32 + e * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (live && c * 32 + e + 16 <= a.d_v && sectors) {
+                            store_32b(out + c * 32 + e, o);
+                        } else {
+                            if (live && c * 32 + e < a.d_v) *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (live && c * 32 + e + 8 < a.d_v) *reinterpret_cast<uint4*>(out + c * 32 + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
                 if (live && a.lse) a.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             } else {
-                const int64_t slot0 = static_cast<int64_t>(k.u.slot) * a.H_kv + static_cast<int64_t>(k.hk) * k.u.parts;
+                const int64_t slot0 = static_cast<int64_t>(k.slot) * a.H_kv + static_cast<int64_t>(k.hk) * k.parts;
                 const int rr = x * kRows + r;  // row of the partial
-                const int64_t prow = (slot0 + k.u.part) * a.slot_rows + rr;
+                const int64_t prow = (slot0 + k.part) * a.slot_rows + rr;
                 if (live) a.part_ml[prow] = make_float2(l > 0.0f ? m : -INFINITY, l);
 #pragma unroll 1
                 for (int c = 0; c < 2 * kVC && any; ++c) {
@@ -525,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the last part of this tile's rows to arrive joins them all
                 __threadfence();
                 named_bar_sync(1 + x, 128);
-                if (r == 0) S.last_part[x] = atomicAdd(&a.counters[2 * slot0 + x], 1) == k.u.parts - 1;
+                if (r == 0) S.last_part[x] = atomicAdd(&a.counters[2 * slot0 + x], 1) == k.parts - 1;
                 named_bar_sync(1 + x, 128);
                 if (S.last_part[x]) {
                     __threadfence();
@@ -533,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = r; i < rows * cols; i += 128) {
                         const int jr = i / cols, e = 4 * (i - jr * cols);
                         const int jt = (row0 + jr) / G;
-                        const int64_t jat = (static_cast<int64_t>(k.u.q0) + jt) * a.H + k.hk * G + (row0 + jr - jt * G);
+                        const int64_t jat = (static_cast<int64_t>(k.q0) + jt) * a.H + k.hk * G + (row0 + jr - jt * G);
                         float lse;
-                        const float4 o = prompt_join4(a, slot0, k.u.parts, x * kRows + jr, e, &lse);
+                        const float4 o = prompt_join4(a, slot0, k.parts, x * kRows + jr, e, &lse);
                         const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
                         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + jat * a.d_v + e) =
                             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -555,48 +626,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// A map of [tokens][heads][cols] with boxes of 128 tokens x 64 columns; the outer extent is the one of
-// the larger stride (*swap: heads). A stride of 0 between the heads: they share one.
+// A map of [tokens][heads][cols] with boxes of `box_tokens` tokens x `box_heads` heads x 64 columns; the
+// outer extent is the one of the larger stride (*swap: heads). A stride of 0 between the heads: they share one.
 static bool make_map(CUtensorMap* map, const void* base, int cols, int heads, int tokens, int64_t stride_t, int64_t stride_h,
-                     int* swap) {
+                     int box_heads, int box_tokens, int* swap) {
     if (stride_h == 0) heads = 1;
     if (heads == 1) stride_h = stride_t;
     if (tokens == 1) stride_t = stride_h;
     *swap = stride_h > stride_t ? 1 : 0;
     const uint64_t n[2] = {static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
     const uint64_t st[2] = {static_cast<uint64_t>(stride_h) * 2, static_cast<uint64_t>(stride_t) * 2};
-    const uint32_t bx[2] = {1, 128};
+    const uint32_t bx[2] = {static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_tokens)};
     const int i = *swap, j = 1 - i;
     return make_tmap_3d(map, base, {static_cast<uint64_t>(cols), n[i], n[j]}, {st[i], st[j]}, {64, bx[i], bx[j]});
 }
 
+struct Maps {
+    CUtensorMap q{}, k{}, v{};
+    int q_map = 0, k_swap = 0, v_swap = 0;
+};
+
 template <int kQC, int kVC>
-static bool launch_typed(const PromptArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int ks, int vs, cudaStream_t s) {
+static bool launch_typed(const PromptArgs& a, const Maps& m, cudaStream_t s) {
     constexpr size_t smem = Layout<kQC>::kBytes;
     static_assert(smem <= kSmemMax && Layout<kQC>::kStages >= 2 * kQC + kVC, "two key tiles and a value tile in flight");
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_tc_kernel<kQC, kVC>), smem)) return false;
     const int64_t most = static_cast<int64_t>(a.max_units) * a.H_kv;  // below 2^31 (checked by the caller)
     const int grid = static_cast<int>(most < a.ctas ? most : a.ctas);
-    return launch_kernel(true, prompt_tc_kernel<kQC, kVC>, dim3(grid), dim3(kThreads), smem, s, a, mk, mv, ks, vs);
+    return launch_kernel(true, prompt_tc_kernel<kQC, kVC>, dim3(grid), dim3(kThreads), smem, s, a, m.q, m.k, m.v, m.q_map,
+                         m.k_swap, m.v_swap);
 }
 
 }  // namespace ptc
 
 bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches) {
-    CUtensorMap mk{}, mv{};
-    int ks = 0, vs = 0;
+    ptc::Maps m;
     // without keys no tile is loaded and no map read
-    if (a.Tk > 0 && (!ptc::make_map(&mk, a.k, a.d_qk, a.H_kv, a.Tk, a.k_stride_t, a.k_stride_h, &ks) ||
-                     !ptc::make_map(&mv, a.v, a.d_v, a.H_kv, a.Tk, a.v_stride_t, a.v_stride_h, &vs)))
-        return false;
+    if (a.Tk > 0) {
+        if (!ptc::make_map(&m.k, a.k, a.d_qk, a.H_kv, a.Tk, a.k_stride_t, a.k_stride_h, 1, 128, &m.k_swap) ||
+            !ptc::make_map(&m.v, a.v, a.d_v, a.H_kv, a.Tk, a.v_stride_t, a.v_stride_h, 1, 128, &m.v_swap))
+            return false;
+        // A box of 128 / G tokens x G heads is a query tile where G divides 128 and the heads are the inner
+        // extent; other groups and orders are copied 16 bytes at a time (4K cycles a tile).
+        const int G = a.H / a.H_kv;
+        int swap = 0;
+        m.q_map = 128 % G == 0 && a.q_stride_t > 0 && a.q_stride_h > 0 &&
+                  ptc::make_map(&m.q, a.q, a.d_qk, a.H, a.Tq, a.q_stride_t, a.q_stride_h, G, 128 / G, &swap) && !swap;
+    }
     const int qc = (a.d_qk + 63) / 64;
     bool ok;
     if (a.d_v <= 64)
-        ok = qc == 1 ? ptc::launch_typed<1, 1>(a, mk, mv, ks, vs, s)
-                     : qc == 2 ? ptc::launch_typed<2, 1>(a, mk, mv, ks, vs, s) : ptc::launch_typed<3, 1>(a, mk, mv, ks, vs, s);
+        ok = qc == 1 ? ptc::launch_typed<1, 1>(a, m, s) : qc == 2 ? ptc::launch_typed<2, 1>(a, m, s) : ptc::launch_typed<3, 1>(a, m, s);
     else
-        ok = qc == 1 ? ptc::launch_typed<1, 2>(a, mk, mv, ks, vs, s)
-                     : qc == 2 ? ptc::launch_typed<2, 2>(a, mk, mv, ks, vs, s) : ptc::launch_typed<3, 2>(a, mk, mv, ks, vs, s);
+        ok = qc == 1 ? ptc::launch_typed<1, 2>(a, m, s) : qc == 2 ? ptc::launch_typed<2, 2>(a, m, s) : ptc::launch_typed<3, 2>(a, m, s);
     if (ok) ++*launches;
     return ok;
 }
