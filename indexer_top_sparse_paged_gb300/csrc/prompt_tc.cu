@@ -120,6 +120,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return y;
 }
 
+// A value that is the same in every lane, as the compiler can tell (it may live in a uniform register).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Eight words to a 32-byte aligned address.
 __device__ __forceinline__ void store_32b(void* p, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sQ = smem_u32(smem), sRing = smem_u32(smem + Lay::kOffRing);
     Ctl& S = *reinterpret_cast<Ctl*>(smem + Lay::kOffCtl);
     volatile int* abort_flag = &S.abort_flag;
-    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     block_sync();
     tc_fence_after();
-    const uint32_t tmem = S.tmem_base;
+    const uint32_t tmem = uniform(S.tmem_base);
     griddep_wait();  // the work list
     const int n_units = a.head->n_units, group = a.head->head_group;
     const int n_work = n_units * a.H_kv;
@@ -327,7 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
     } else {
         // --------------------------------------------------------------------------------- MMA
-        // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4).
+        constexpr bool kEarlyV = kQC == 3;
+        // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4); what the descriptors and
+        // the branches depend on is made uniform by hand where it comes from memory.
         const int x = warp - 8;  // tile
         int slot = 0;            // the ring's next chunk
         Turn got, released;      // its group, the next group to give back
@@ -383,16 +388,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c > 0 && wide) break;
                 const uint64_t vc = wide ? vd : dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
                 const uint32_t o = tO + c * 64, idesc = wide ? kIdescPV2 : kIdescPV;
-                int kk = 0;
-                if (n >= 4) {
-                    warp_mma_ts_x4(o, tS + from * 8, vc, idesc, acc);
-                    kk = 4;
+                if (n == most) {  // (known where it is called: 8, 6 or 2)
+                    if (most > 2) warp_mma_ts_x4(o, tS + from * 8, vc, idesc, acc);
+                    if (most == 8) warp_mma_ts_x4(o, tS + 32, vc + 512, idesc, 1u);
+                    else warp_mma_ts_x2(o, tS + (from + most - 2) * 8, vc + (most - 2) * 128, idesc, most == 6 ? 1u : acc);
+                    continue;
                 }
+                int kk = 0;
                 for (; kk < n; ++kk) warp_mma_ts(o, tS + (from + kk) * 8, vc + kk * 128, idesc, kk ? 1u : acc);
             }
         };
         for (Work k; ok && take(k);) {
-            const int k_begin = k.kt0, lk = k.lk, n = x ? k.n1 : k.n0, end = max(k.n0, k.n1);
+            const int k_begin = uniform(k.kt0), lk = uniform(k.lk), n0 = uniform(k.n0), n1 = uniform(k.n1);
+            const int n = x ? n1 : n0, end = max(n0, n1);
             if (k_begin >= end) continue;
             if (n > k_begin) {  // a tile without keys only walks the groups
                 wait(&S.q_full[x], qphase);
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
             }
             wait_group();
-            const int both_end = min(k.n0, k.n1);  // key tiles [k_begin, both_end): both tiles work
+            const int both_end = min(n0, n1);  // key tiles [k_begin, both_end): both tiles work
             take_turn(k_begin < both_end);
             if (!ok) break;
             if (n > k_begin) qk(slot, k_begin < both_end);
@@ -427,20 +435,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(&S.p_full[x][0], pphase);
                     take_turn(both);
                     if (!ok) break;
-                    pv(0, 6, vs, steps, j == k_begin);
-                    wait(&S.p_full[x][1], pphase);
+                    // the last quarter's weights are mostly there by now; if not, the first three go ahead
+                    const bool whole = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[x][1]), pphase));
+                    if (whole) {
+                        tc_fence_after();
+                        pv(0, 8, vs, steps, j == k_begin);
+                    } else {
+                        pv(0, 6, vs, steps, j == k_begin);
+                        wait(&S.p_full[x][1], pphase);
+                        if (!ok) break;
+                        pv(6, 2, vs, steps, j == k_begin);
+                    }
                     pphase ^= 1;
-                    if (!ok) break;
-                    if (!qk_next) pass_turn(both);
-                    pv(6, 2, vs, steps, j == k_begin);
-                    if (j + 1 == n) warp_tc_commit(smem_u32(&S.o_full[x]));
+                    if (j + 1 == n) {
+                        pass_turn(both);
+                        warp_tc_commit(smem_u32(&S.o_full[x]));
+                    }
                 }
-                release();
+                if (kEarlyV) release();
                 slot = ks;
                 if (more) {
                     if (qk_next) qk(ks, both);
                     if (j + 2 == n) warp_tc_commit(smem_u32(&S.q_free[x]));
                     slot = next(slot, kQC);
+                    if (!kEarlyV) release();
+                    release();
+                } else if (!kEarlyV) {
                     release();
                 }
             }
