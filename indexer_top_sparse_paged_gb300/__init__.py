@@ -318,16 +318,36 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_device(*tensors):
-    """Every tensor on the current CUDA device (the library launches there)."""
+def _device(*tensors) -> int:
+    """The current CUDA device's index, on which the library launches; every tensor must be there."""
+    dev = None
     for t in tensors:
         if t is not None:
-            _need(t.is_cuda, "tensor arguments must be CUDA tensors (the library takes device pointers)")
-            _need(t.device.index == torch.cuda.current_device(), "tensor arguments must be on the current CUDA device")
+            d = t.get_device()
+            if d != dev:
+                _need(d >= 0, "tensor arguments must be CUDA tensors (the library takes device pointers)")
+                _need(dev is None, "tensor arguments must be on one CUDA device")
+                dev = d
+    _need(dev == torch.cuda.current_device(), "tensor arguments must be on the current CUDA device")
+    return dev
+
+
+def _at(t):
+    """The address of a contiguous tensor whose device has been checked (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous (the library reads densely packed rows)")
+    return t.data_ptr()
+
+
+def _raw_stream(dev: int, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _int32(t, n: int, name: str):
-    _need(t is None or (t.dtype == torch.int32 and t.numel() >= n), f"{name} must be an int32 tensor of {n} elements")
+    if t is not None and (t.dtype is not torch.int32 or t.numel() < n):
+        raise ValueError(f"{name} must be an int32 tensor of {n} elements")
 
 
 def _empty(shape, dtype, device, stream):
@@ -363,30 +383,46 @@ def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, 
     ``x`` may be a view of part of wider heads (``q[..., 512:]``), or a list of up to four tensors of the
     same tokens, with ``out`` and ``layout`` lists as well. ``transpose=True`` is the backward pass."""
     many = isinstance(x, (list, tuple))
-    xs = list(x) if many else [x]
-    outs = xs if out is None else list(out) if many else [out]
-    layouts = list(layout) if isinstance(layout, (list, tuple)) else [layout] * len(xs)
-    _need(0 < len(xs) == len(outs) == len(layouts), "x, out and layout must have the same number of tensors")
-    _on_device(freq, seq_lens, q_pos, *xs, *outs)
-    _need(freq.dtype == torch.float64 and freq.dim() == 1, "freq must be a float64 tensor of rot / 2 elements")
-    T, rot = xs[0].shape[0], 2 * freq.numel()
-    _need(q_pos is not None or seq_lens is not None, "rope needs q_pos or seq_lens")
-    _int32(q_pos, T, "q_pos")
+    xs = x if many else (x,)
+    outs = xs if out is None else out if many else (out,)
+    n = len(xs)
+    layouts = layout if isinstance(layout, (list, tuple)) else (layout,) * n
+    if not 0 < n == len(outs) == len(layouts):
+        raise ValueError("x, out and layout must have the same number of tensors")
+    dev = _device(freq, seq_lens, q_pos, *xs) if out is None else _device(freq, seq_lens, q_pos, *xs, *outs)
+    if freq.dtype is not torch.float64 or freq.dim() != 1:
+        raise ValueError("freq must be a float64 tensor of rot / 2 elements")
+    dt, T, rot = xs[0].dtype, xs[0].shape[0], 2 * freq.shape[0]
+    if dt not in _TYPES:
+        raise ValueError("x must be float32 or bfloat16")
     if q_pos is None:
+        _need(seq_lens is not None, "rope needs q_pos or seq_lens")
         _int32(seq_lens, T, "seq_lens")
-    _need(xs[0].dtype in _TYPES, "x must be float32 or bfloat16")
-    arr = (RopeTensor * len(xs))()
-    for r, s, d, lay in zip(arr, xs, outs, layouts):
-        for t in (s, d):
-            _need(t.dim() == 3 and t.shape == xs[0].shape[:1] + s.shape[1:2] + (rot,) and t.dtype == xs[0].dtype,
-                  "rope tensors must be [T][heads][rot] of one type and one T")
-            _need(t.stride(2) == 1 or t.numel() == 0, "a head's rotated columns must be dense")
-        _need(d.numel() == 0 or (0 not in (d.stride(0) if d.shape[0] > 1 else 1, d.stride(1) if d.shape[1] > 1 else 1)),
-              "out must not repeat rows (expanded views)")
-        r.x, r.out, r.heads, r.layout = s.data_ptr(), d.data_ptr(), s.shape[1], _layout(lay)
-        r.x_stride_t, r.x_stride_h, r.out_stride_t, r.out_stride_h = s.stride(0), s.stride(1), d.stride(0), d.stride(1)
-    _check("dsa_rope", lib().dsa_rope(_TYPES[xs[0].dtype], arr, len(xs), rot, _p(freq), _p(seq_lens), _p(q_pos), T,
-                                      float(scale), int(transpose), _stream(stream)))
+    else:
+        _int32(q_pos, T, "q_pos")
+    arr = (RopeTensor * n)()
+    for i in range(n):
+        s, d = xs[i], outs[i]
+        shape, st = s.shape, s.stride()
+        if len(shape) != 3 or shape[0] != T or shape[2] != rot or s.dtype is not dt:
+            raise ValueError("rope tensors must be [T][heads][rot] of one type and one T")
+        if d is s:
+            so = st
+        else:
+            so = d.stride()
+            if d.shape != shape or d.dtype is not dt:
+                raise ValueError("out must have x's shape and type")
+        H = shape[1]
+        if T and H:
+            if st[2] != 1 or so[2] != 1:
+                raise ValueError("a head's rotated columns must be dense")
+            if (T > 1 and so[0] == 0) or (H > 1 and so[1] == 0):
+                raise ValueError("out must not repeat rows (expanded views)")
+        arr[i] = (s.data_ptr(), d.data_ptr(), H, _layout(layouts[i]), st[0], st[1], so[0], so[1])
+    st = lib().dsa_rope(_TYPES[dt], arr, n, rot, _at(freq), _at(seq_lens), _at(q_pos), T, scale, transpose,
+                        _raw_stream(dev, stream))
+    if st:
+        _check("dsa_rope", st)
     return outs if many else outs[0]
 
 
@@ -397,55 +433,67 @@ def cache_append_rope(dims: Dims, freq, k_I_new, kv_new, block_table, seq_lens, 
     columns from ``k_offset`` of the indexer keys and from ``kv_offset`` of the latent rows (default: their
     last columns; -1: none) turn by the rows' positions in the same launch."""
     T, rot = kv_new.shape[0], 2 * freq.numel()
-    _on_device(freq, k_I_new, kv_new, block_table, seq_lens, k_I_cache, k_I_scale, kv_cache, q_seq, q_pos, ws)
-    _need(freq.dtype == torch.float64, "freq must be a float64 tensor of rot / 2 elements")
-    act = torch.float32 if dims.mode == MODES["f32"] else torch.bfloat16
-    _need(k_I_new.dtype == act and k_I_new.numel() == T * dims.d_I, f"k_I_new must be a {act} tensor of T x d_I elements")
-    _need(kv_new.dtype == act and kv_new.numel() == T * dims.d, f"kv_new must be a {act} tensor of T x d elements")
+    dev = _device(freq, k_I_new, kv_new, block_table, seq_lens, k_I_cache, k_I_scale, kv_cache, q_seq, q_pos, ws)
+    if freq.dtype is not torch.float64:
+        raise ValueError("freq must be a float64 tensor of rot / 2 elements")
+    act = torch.float32 if dims.mode == 0 else torch.bfloat16
+    if k_I_new.dtype is not act or k_I_new.numel() != T * dims.d_I:
+        raise ValueError(f"k_I_new must be a {act} tensor of T x d_I elements")
+    if kv_new.dtype is not act or kv_new.numel() != T * dims.d:
+        raise ValueError(f"kv_new must be a {act} tensor of T x d elements")
     _int32(block_table, dims.B * dims.max_blocks, "block_table")
     _int32(seq_lens, dims.B, "seq_lens")
     _int32(q_seq, T, "q_seq")
     _int32(q_pos, T, "q_pos")
     r = RopeAppend(rot, k_offset, _layout(k_layout), dims.d - rot if kv_offset is None else kv_offset, _layout(kv_layout),
                    float(scale))
-    st = lib().dsa_cache_append_rope(ctypes.byref(dims), ctypes.byref(r), _p(freq), _p(k_I_new), _p(kv_new),
-                                     _p(block_table), _p(seq_lens), _p(q_seq), _p(q_pos), T, _p(k_I_cache), _p(k_I_scale),
-                                     _p(kv_cache), _p(ws), ws.numel(), _stream(stream))
-    _check("dsa_cache_append_rope", st)
+    st = lib().dsa_cache_append_rope(ctypes.byref(dims), ctypes.byref(r), _at(freq), _at(k_I_new), _at(kv_new),
+                                     _at(block_table), _at(seq_lens), _at(q_seq), _at(q_pos), T, _at(k_I_cache),
+                                     _at(k_I_scale), _at(kv_cache), _at(ws), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _check("dsa_cache_append_rope", st)
 
 
 def cache_read(dims: Dims, k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, cu_rows, R: int, start=None, *,
                k_out=None, kv_out=None, want_k: bool = True, want_kv: bool = True, ws, stream=None):
     """(k[R][d_I], kv[R][d]) of the positions start[b], start[b] + 1, ... of every sequence b, dequantised,
     in rows cu_rows[b] .. cu_rows[b + 1] - 1 (fp32 or bf16). An output not wanted is None."""
-    _on_device(k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, cu_rows, start, k_out, kv_out, ws)
-    act = torch.float32 if dims.mode == MODES["f32"] else torch.bfloat16
+    dev = _device(k_I_cache, k_I_scale, kv_cache, block_table, seq_lens, cu_rows, start, k_out, kv_out, ws)
+    act = torch.float32 if dims.mode == 0 else torch.bfloat16
     if k_out is None and want_k:
         k_out = _empty((R, dims.d_I), act, ws.device, stream)
     if kv_out is None and want_kv:
         kv_out = _empty((R, dims.d), act, ws.device, stream)
     for t, d, name in ((k_out, dims.d_I, "k_out"), (kv_out, dims.d, "kv_out")):
-        _need(t is None or (t.dtype == act and t.numel() >= R * d), f"{name} must be a {act} tensor of R x {d} elements")
+        if t is not None and (t.dtype is not act or t.numel() < R * d):
+            raise ValueError(f"{name} must be a {act} tensor of R x {d} elements")
     _int32(block_table, dims.B * dims.max_blocks, "block_table")
     _int32(seq_lens, dims.B, "seq_lens")
     _int32(cu_rows, dims.B + 1, "cu_rows")
     _int32(start, dims.B, "start")
-    st = lib().dsa_cache_read(ctypes.byref(dims), _p(k_I_cache), _p(k_I_scale), _p(kv_cache), _p(block_table),
-                              _p(seq_lens), _p(start), _p(cu_rows), R, _p(k_out), _p(kv_out), _p(ws), ws.numel(),
-                              _stream(stream))
-    _check("dsa_cache_read", st)
+    st = lib().dsa_cache_read(ctypes.byref(dims), _at(k_I_cache), _at(k_I_scale), _at(kv_cache), _at(block_table),
+                              _at(seq_lens), _at(start), _at(cu_rows), R, _at(k_out), _at(kv_out), _at(ws), ws.numel(),
+                              _raw_stream(dev, stream))
+    if st:
+        _check("dsa_cache_read", st)
     return k_out, kv_out
 
 
 def prompt_dims(q, k, v, B: int, causal: bool = True) -> PromptDims:
     """The dims of :func:`prompt_attn` for B sequences packed in q [Tq][H][d_qk], k [Tk][H_kv][d_qk] and
     v [Tk][H_kv][d_v] (strided views allowed; a head's columns are dense)."""
-    for t in (q, k, v):
-        _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), "q, k and v must be [tokens][heads][width] with dense columns")
-    _need(q.dtype in _TYPES and k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must be all float32 or all bfloat16")
-    _need(k.shape[:2] == v.shape[:2] and q.shape[2] == k.shape[2], "k and v must have the same tokens and heads, q and k the same width")
-    return PromptDims(_TYPES[q.dtype], B, q.shape[1], k.shape[1], q.shape[2], v.shape[2], int(causal), q.stride(0),
-                      q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    return PromptDims(*_prompt_fields(q, k, v, B, causal))
+
+
+def _prompt_fields(q, k, v, B, causal):
+    qn, kn, vn, qs, ks, vs, dt = q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), q.dtype
+    if not len(qn) == len(kn) == len(vn) == 3 or (qs[2] != 1 and q.numel()) or (ks[2] != 1 and k.numel()) or (vs[2] != 1 and v.numel()):
+        raise ValueError("q, k and v must be [tokens][heads][width] with dense columns")
+    if dt not in _TYPES or k.dtype is not dt or v.dtype is not dt:
+        raise ValueError("q, k and v must be all float32 or all bfloat16")
+    if kn[:2] != vn[:2] or qn[2] != kn[2]:
+        raise ValueError("k and v must have the same tokens and heads, q and k the same width")
+    return (_TYPES[dt], B, qn[1], kn[1], qn[2], vn[2], int(causal), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
 
 
 def prompt_workspace(dims: PromptDims, Tq: int, device="cuda", stream=None) -> torch.Tensor:
@@ -463,22 +511,24 @@ def prompt_workspace(dims: PromptDims, Tq: int, device="cuda", stream=None) -> t
 def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, out=None, lse=None, stream=None):
     """(out[Tq][H][d_v], lse[Tq][H]) of dense attention over packed sequences: sequence b has the queries
     cu_q[b] .. cu_q[b + 1] - 1, the last of its positions, and the keys cu_k[b] .. cu_k[b + 1] - 1."""
-    now = prompt_dims(q, k, v, dims.B, dims.causal)
-    _need(bytes(now) == bytes(dims), "q, k and v differ from the tensors dims was made for")
-    _on_device(q, k, v, cu_q, cu_k, out, lse, ws)
+    if bytes(PromptDims(*_prompt_fields(q, k, v, dims.B, dims.causal))) != bytes(dims):
+        raise ValueError("q, k and v differ from the tensors dims was made for")
+    dev = _device(q, k, v, cu_q, cu_k, out, lse, ws)
     _int32(cu_q, dims.B + 1, "cu_q")
     _int32(cu_k, dims.B + 1, "cu_k")
     Tq, H = q.shape[:2]
     if out is None:
         out = _empty((Tq, H, dims.d_v), q.dtype, q.device, stream)
+    elif out.dtype is not q.dtype or out.numel() < Tq * H * dims.d_v:
+        raise ValueError("out must be a tensor of Tq x H x d_v elements in q's type")
     if lse is None:
         lse = _empty((Tq, H), torch.float32, q.device, stream)
-    _need(out.dtype == q.dtype and out.numel() >= Tq * H * dims.d_v, "out must be a tensor of Tq x H x d_v elements in q's type")
-    _need(lse.dtype == torch.float32 and lse.numel() >= Tq * H, "lse must be a float32 tensor of Tq x H elements")
-    st = lib().dsa_prompt_attn(ctypes.byref(dims), ctypes.c_void_p(q.data_ptr()), ctypes.c_void_p(k.data_ptr()),
-                               ctypes.c_void_p(v.data_ptr()), _p(cu_q), _p(cu_k), Tq, k.shape[0], float(sm_scale), _p(out),
-                               _p(lse), _p(ws), ws.numel(), _stream(stream))
-    _check("dsa_prompt_attn", st)
+    elif lse.dtype is not torch.float32 or lse.numel() < Tq * H:
+        raise ValueError("lse must be a float32 tensor of Tq x H elements")
+    st = lib().dsa_prompt_attn(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(cu_q), _at(cu_k), Tq,
+                               k.shape[0], sm_scale, _at(out), _at(lse), _at(ws), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _check("dsa_prompt_attn", st)
     return out, lse
 
 
