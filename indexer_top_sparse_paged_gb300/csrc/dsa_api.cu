@@ -438,10 +438,10 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     const int64_t rows = static_cast<int64_t>(Tq) * (p.H / p.H_kv);
     w.tile_rows = prompt_uses_tc(p) ? kPromptTcRows : kPromptSimtRows;
     w.ctas = device_sm_count();
-    // The plan splits no more than 2 x ctas partials out of all key heads (see there), so at most
-    // 2 x ctas / H_kv of one head.
-    w.max_slots = 2 * w.ctas / p.H_kv;
-    w.slot_rows = static_cast<int>(rows < w.tile_rows ? rows : w.tile_rows);
+    // The plan makes fewer than 4 x ctas partials over all key heads (see there), so at most
+    // 4 x ctas / H_kv of one head.
+    w.max_slots = 4 * w.ctas / p.H_kv;
+    w.slot_rows = static_cast<int>(rows < w.tile_rows ? (rows + 31) / 32 * 32 : w.tile_rows);
     // every sequence fills whole tiles but its last
     w.max_units = static_cast<int>(rows / w.tile_rows) + p.B + w.max_slots;
     const size_t slots = static_cast<size_t>(w.max_slots) * p.H_kv;

@@ -197,7 +197,7 @@ struct PromptArgs {
     PromptHead* head;
     PromptUnit* units;
     int32_t* counters;  // [max_slots * H_kv][2] parts that have arrived
-    float* part_o;      // [max_slots * H_kv][slot_rows][d_v] unnormalised outputs
+    float* part_o;      // [max_slots * H_kv][d_v][slot_rows] unnormalised outputs
     float2* part_ml;    // [max_slots * H_kv][slot_rows] (running maximum in powers of two, sum)
 };
 

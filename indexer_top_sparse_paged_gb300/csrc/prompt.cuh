@@ -10,32 +10,76 @@ __device__ __forceinline__ int prompt_keys_seen(const PromptArgs& a, int t, int 
     return a.causal ? min(lk, max(0, t + 1 + lk - lq)) : lk;
 }
 
-// Columns e .. e + 3 of row r of the partials slot0 .. slot0 + parts - 1, joined in that order:
-// sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, and the row's lse.
-__device__ __forceinline__ float4 prompt_join4(const PromptArgs& a, int64_t slot0, int parts, int r, int e, float* lse) {
-    float M = -INFINITY;
-    for (int p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(&a.part_ml[(slot0 + p) * a.slot_rows + r]).x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M == -INFINITY) {  // no part saw a key
-        *lse = -INFINITY;
-        return o;
+// Column c of row r of partial `slot`: the rows of a column lie side by side, so that a warp whose lanes hold
+// rows writes and reads whole lines.
+__device__ __forceinline__ int64_t part_at(const PromptArgs& a, int64_t slot, int c, int r) {
+    return (slot * a.d_v + c) * a.slot_rows + r;
+}
+
+__device__ __forceinline__ void store_cols(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    float l = 0.0f;
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Joins `rows` rows of the partials slot0 .. slot0 + parts - 1 (rows rr0 .. of each, the rows row0 .. of the
+// sequence) in that order and writes them out: sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p. n threads
+// (a power of two, at least the rows) share the work; a thread keeps one row and a run of columns, 8 at a
+// time, with the loads of two parts in flight.
+template <typename T>
+__device__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int rr0, int rows, int q0, int row0, int hk, int tid,
+                            int n) {
+    int width = 1;  // threads side by side on the rows
+    while (width < rows) width *= 2;
+    const int groups = n / width, r = tid % width, G = a.H / a.H_kv;
+    if (r >= rows) return;
+    const int per = ((a.d_v + groups - 1) / groups + 7) / 8 * 8, c0 = tid / width * per, c1 = min(a.d_v, c0 + per);
+    const int t = (row0 + r) / G;
+    const int64_t at = (static_cast<int64_t>(q0) + t) * a.H + hk * G + (row0 + r - t * G);  // (token, head)
+    const float2* ml = a.part_ml + slot0 * a.slot_rows + rr0 + r;
+    float M = -INFINITY, l = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(ml + static_cast<int64_t>(p) * a.slot_rows).x);
+    const float ref = M == -INFINITY ? 0.0f : M;  // no part saw a key: every factor is 0
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
-        const int64_t at = (slot0 + p) * a.slot_rows + r;
-        const float2 ml = __ldcg(&a.part_ml[at]);
-        if (ml.x == -INFINITY) continue;
-        const float f = exp2f(ml.x - M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * a.d_v + e));
-        l += f * ml.y;
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z);
-        o.w = fmaf(f, v.w, o.w);
+        const float2 v = __ldcg(ml + static_cast<int64_t>(p) * a.slot_rows);
+        l += exp2f(v.x - ref) * v.y;
     }
-    const float inv = 1.0f / l;
-    *lse = (M + log2f(l)) * 0.6931471805599453f;
-    return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (c0 == 0 && a.lse) a.lse[at] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    T* out = static_cast<T*>(a.out) + at * a.d_v;
+    for (int c = c0; c < c1; c += 8) {
+        const int m = min(8, c1 - c);  // 8, or 4 (fp32 rows of an odd number of pieces)
+        float o[8] = {};
+#pragma unroll 2
+        for (int p = 0; p < parts; ++p) {
+            const float x = __ldcg(ml + static_cast<int64_t>(p) * a.slot_rows).x;
+            if (x == -INFINITY) continue;  // nothing was written
+            const float f = exp2f(x - ref);
+            const float* po = a.part_o + part_at(a, slot0 + p, c, rr0 + r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < m) o[i] = fmaf(f, __ldcg(po + static_cast<int64_t>(i) * a.slot_rows), o[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
+        if (m == 8) {
+            store_cols(out + c, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < m) out[c + i] = static_cast<T>(o[i]);
+        }
+    }
 }
 
 }  // namespace dsa

@@ -4,9 +4,12 @@
 // head one column of lq * G rows, row r = token r / G, head r % G of the group. A unit is tile_rows of
 // them against a range of the key tiles they see; every unit runs once for each key head.
 //
-// Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads
-// and C CTAs, no unit gets more than max(W / C, kMinTiles) tiles. An item of n tiles over that bound s
-// becomes ceil(n / s) < 2 n / s parts, so all heads together get fewer than 2 W / s <= 2 C partials.
+// Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
+// CTAs, if the longest item has more than 1.5 W / C tiles. Every item is then cut at the multiples of
+// s = max(W / 2C, a 32nd of the longest, kMinTiles); a last part shorter than kMinTiles stays with the one
+// before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
+// same keys (cuts at even shares of all tiles instead: a chunk of 2048 on 32K keys 1.1 ms against 0.7).
+// An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.
 #include "internal.h"
 
@@ -14,6 +17,7 @@ namespace dsa {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kMinTiles = 4;     // a part of fewer tiles costs more to join than it saves
+constexpr int kMaxParts = 32;    // of one item, about: one CTA joins them
 constexpr int kBuckets = 1024;
 
 struct PlanItem {
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     for (int i = tid; i < 2 * a.max_slots * a.H_kv; i += kPlanThreads) a.counters[i] = 0;
     __syncthreads();
     bool loaded = false;  // up to 1024 sequences stay in shared memory
-    // every item of sequences b0 .. b0 + 1023 in turn, shared out over the threads
+    // f(valid, item) for every item in turn, 1024 at a time by the whole CTA
     auto for_items = [&](auto&& f) {
         for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
             const int b = b0 + tid;
@@ -90,42 +94,54 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
                 if (tid == 0) prefix[0] = 0;
                 __syncthreads();
             }
-            const int total = prefix[kPlanThreads];
-            for (int i = tid; i < total; i += kPlanThreads) {
-                int lo = 0, hi = kPlanThreads - 1;  // the last sequence whose first item is at or before i
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (prefix[mid] <= i) lo = mid;
-                    else hi = mid - 1;
+            const int total = prefix[kPlanThreads], seqs_here = min(kPlanThreads, a.B - b0);
+            for (int i0 = 0; i0 < total; i0 += kPlanThreads) {
+                const int i = i0 + tid;
+                PlanItem it{};
+                if (i < total) {
+                    int lo = 0, hi = seqs_here - 1;  // the last sequence whose first item is at or before i
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (prefix[mid] <= i) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    const int4 s = seqs[lo];
+                    const int row0 = (i - prefix[lo]) * a.tile_rows;
+                    it = PlanItem{s.x, s.y, s.z, s.w, row0, item_tiles(a, G, s.y, s.w, row0)};
                 }
-                const int4 s = seqs[lo];
-                const int row0 = (i - prefix[lo]) * a.tile_rows;
-                f(PlanItem{s.x, s.y, s.z, s.w, row0, item_tiles(a, G, s.y, s.w, row0)});
+                f(i < total, it);
             }
-            __syncthreads();
+            if (a.B > kPlanThreads) __syncthreads();  // the next sequences take their place
         }
     };
-    for_items([&](const PlanItem& it) {
-        atomicAdd(&total_tiles, static_cast<unsigned long long>(it.tiles));
-        atomicMax(&most_tiles, it.tiles);
-        atomicMax(&most_keys, it.lk);
+    for_items([&](bool valid, const PlanItem& it) {
+        const unsigned tiles = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(it.tiles));
+        const int longest = __reduce_max_sync(0xFFFFFFFFu, it.tiles), keys = __reduce_max_sync(0xFFFFFFFFu, it.lk);
+        if ((tid & 31) == 0) {
+            atomicAdd(&total_tiles, static_cast<unsigned long long>(tiles));
+            atomicMax(&most_tiles, longest);
+            atomicMax(&most_keys, keys);
+        }
+        (void)valid;
     });
+    __syncthreads();
     const long long work = static_cast<long long>(total_tiles) * a.H_kv;
-    const int bound = a.max_slots > 1 ? static_cast<int>(max(static_cast<long long>(kMinTiles), (work + a.ctas - 1) / a.ctas))
-                                      : 1 << 30;
-    const int longest = max(1, min(most_tiles, bound));
+    const bool cut = a.max_slots > 1 && 2ll * a.ctas * most_tiles > 3 * work;
+    const int s = static_cast<int>(max(max(static_cast<long long>(kMinTiles), (work + 2 * a.ctas - 1) / (2 * a.ctas)),
+                                       static_cast<long long>((most_tiles + kMaxParts - 1) / kMaxParts)));
+    const int longest = max(1, cut ? min(most_tiles, s + kMinTiles) : most_tiles);
     auto bucket_of = [&](int tiles) {  // falling number of tiles
-        return kBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kBuckets - 1) / longest);
+        return kBuckets - 1 - static_cast<int>(static_cast<long long>(min(tiles, longest)) * (kBuckets - 1) / longest);
     };
-    auto parts_of = [&](int tiles) { return max(1, (tiles + bound - 1) / bound); };
-    for_items([&](const PlanItem& it) {
-        const int parts = parts_of(it.tiles);
-        for (int p = 0; p < parts; ++p) {
-            const int t0 = static_cast<int>(static_cast<long long>(it.tiles) * p / parts);
-            const int t1 = static_cast<int>(static_cast<long long>(it.tiles) * (p + 1) / parts);
-            atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
-        }
+    // f(part, parts, its first tile, its last + 1) for every unit of an item
+    auto units_of = [&](int tiles, auto&& f) {
+        const int parts = cut ? max(1, (tiles + s - kMinTiles) / s) : 1;
+        for (int p = 0; p < parts; ++p) f(p, parts, p * s, p == parts - 1 ? tiles : (p + 1) * s);
+    };
+    for_items([&](bool valid, const PlanItem& it) {
+        if (valid) units_of(it.tiles, [&](int, int, int t0, int t1) { atomicAdd(&bucket[bucket_of(t1 - t0)], 1); });
     });
+    __syncthreads();
     const int x = block_scan(bucket[tid], warp_sum);
     if (tid == kPlanThreads - 1) {
         a.head->n_units = min(x, a.max_units);
@@ -136,16 +152,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     }
     bucket[tid] = x - bucket[tid];
     __syncthreads();
-    for_items([&](const PlanItem& it) {
-        const int parts = parts_of(it.tiles);
-        const int slot = parts > 1 ? atomicAdd(&slots, parts) : 0;
-        for (int p = 0; p < parts; ++p) {
-            const int t0 = static_cast<int>(static_cast<long long>(it.tiles) * p / parts);
-            const int t1 = static_cast<int>(static_cast<long long>(it.tiles) * (p + 1) / parts);
+    for_items([&](bool valid, const PlanItem& it) {
+        int slot = 0;
+        if (!valid) return;
+        units_of(it.tiles, [&](int p, int parts, int t0, int t1) {
+            if (p == 0 && parts > 1) slot = atomicAdd(&slots, parts);
             const int at = atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
-            if (at < a.max_units && slot + parts <= max(a.max_slots, 1))
+            if (at < a.max_units && slot + (parts > 1 ? parts : 0) <= a.max_slots)
                 a.units[at] = PromptUnit{it.q0, it.lq, it.k0, it.lk, it.row0, t0, t1, slot, p, parts, {0, 0}};
-        }
+        });
     });
 }
 static_assert(kBuckets == kPlanThreads, "the bucket scan takes one bucket per thread");

@@ -164,11 +164,16 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
         const int r = 4 * ty + i;
         if (row0 + r >= nrows) continue;
         if (u.parts > 1) {
-            const int64_t at = (slot0 + u.part) * a.slot_rows + r;
-            if (tx == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+            if (tx == 0) a.part_ml[(slot0 + u.part) * a.slot_rows + r] = make_float2(m[i], l[i]);
 #pragma unroll
-            for (int j = 0; j < kCols; ++j)
-                if (4 * tx + 64 * j < a.d_v) *reinterpret_cast<float4*>(a.part_o + at * a.d_v + 4 * tx + 64 * j) = o[i][j];
+            for (int j = 0; j < kCols; ++j) {
+                const int e = 4 * tx + 64 * j;
+                if (e >= a.d_v) continue;
+                a.part_o[part_at(a, slot0 + u.part, e, r)] = o[i][j].x;
+                a.part_o[part_at(a, slot0 + u.part, e + 1, r)] = o[i][j].y;
+                a.part_o[part_at(a, slot0 + u.part, e + 2, r)] = o[i][j].z;
+                a.part_o[part_at(a, slot0 + u.part, e + 3, r)] = o[i][j].w;
+            }
             continue;
         }
         const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;  // (token, head)
@@ -190,15 +195,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     __syncthreads();
     if (!last_part) return;
     __threadfence();
-    const int cols = a.d_v / 4;
-    for (int i = tid; i < min(kRows, nrows - row0) * cols; i += kThreads) {
-        const int r = i / cols, e = 4 * (i - r * cols);
-        const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;
-        float lse;
-        const float4 v = prompt_join4(a, slot0, u.parts, r, e, &lse);
-        store4(static_cast<T*>(a.out) + at * a.d_v + e, v);
-        if (e == 0 && a.lse) a.lse[at] = lse;
-    }
+    prompt_join<T>(a, slot0, u.parts, 0, min(kRows, nrows - row0), q0, row0, hk, tid, kThreads);
 }
 
 template <typename T, int kCols>

@@ -9,6 +9,9 @@
 // cores, the tensor pipe works for the other: P_A V, Q_A K, P_B V, Q_B K, ... in that order, where Q_X K
 // of the next keys may follow P_X V of the last at once, since the pipe runs in order.
 //
+// Units of at most 32 rows (single tokens) would leave tile B without work and every step waiting for the
+// last: there both tiles hold the same rows and take every other key tile, and one warp joins the two.
+//
 // Softmax: one thread per row, the running maximum m and sum l in fp32; O is rescaled only when a row's
 // maximum has grown by more than 2^8 since the last time (weights then stay below 2^8, and O and l hold
 // the same factor). Weights are rounded to bf16 for the product (half a step, 2^-8 of a weight, as the
@@ -49,8 +52,11 @@ struct Work {
     int hk;      // key head; -1: no more work
     int nrows;   // rows of the sequence for this head
     int n0, n1;  // key tiles [kt0, n0) of tile A, [kt0, n1) of tile B
-    int pad[3];
+    int apart;   // few rows: both tiles hold the same ones, A takes the key tiles kt0, kt0 + 2, ..., B the others
+    int pad[2];
 };
+
+constexpr int kApartRows = 32;       // one warp's rows, so that it can join both tiles' outputs from tensor memory
 
 constexpr int kQueue = 2;            // units handed out and not yet taken up by every role
 constexpr int kTakers = 11;          // 8 softmax warps, 2 MMA warps, the key loader
@@ -61,6 +67,9 @@ struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: the first 96 keys' weights, the rest
     uint64_t turn[2];  // the tensor pipe's next turn belongs to tile A, B
+    uint64_t rows_sync[2];          // the four warps of a tile, around the join of a row's parts
+    uint64_t join_full, join_free;  // tile B's part of a unit apart: ready, read
+    float2 join_ml[kApartRows];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
@@ -150,6 +159,8 @@ __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int g
     };
     x.n0 = tiles(u.row0);
     x.n1 = tiles(u.row0 + kRows);
+    x.apart = x.nrows - u.row0 <= kApartRows && x.n0 - u.kt0 >= 2;
+    if (x.apart) x.n1 = x.n0;
     x.q0 = u.q0, x.lq = u.lq, x.k0 = u.k0, x.lk = u.lk, x.row0 = u.row0, x.kt0 = u.kt0;
     x.slot = u.slot, x.part = u.part, x.parts = u.parts;
     return x;
@@ -178,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.q_free[i]), 1);
             mbar_init(smem_u32(&S.s_full[i]), 1);
             mbar_init(smem_u32(&S.turn[i]), 1);
+            mbar_init(smem_u32(&S.rows_sync[i]), 4);
             mbar_init(smem_u32(&S.p_full[i][0]), 4);
             mbar_init(smem_u32(&S.p_full[i][1]), 4);
             mbar_init(smem_u32(&S.o_full[i]), 1);
@@ -186,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.work_full[i]), 1);
             mbar_init(smem_u32(&S.work_free[i]), kTakers);
         }
+        mbar_init(smem_u32(&S.join_full), 32);
+        mbar_init(smem_u32(&S.join_free), 32);
         mbar_init(smem_u32(&S.mma_done), 2);
         S.abort_flag = 0;
         fence_mbar_init();
@@ -237,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if ((x ? k.n1 : k.n0) == k.kt0) continue;  // no keys: the tile's queries are not used
-                const int row0 = k.row0 + x * kRows;
+                const int row0 = k.row0 + (k.apart ? 0 : x * kRows);
                 ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), x ? qphase1 : qphase0, abort_flag, a.err));
                 if (!ok) break;
                 if (x) qphase1 ^= 1;
@@ -284,21 +298,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 10) {
         // --------------------------------------------------------------------------------- TMA
-            // a group (a key tile of kQC chunks, then its value tile of kVC) fills the ring's next chunks
+            // a group (a key tile of kQC chunks or a value tile of kVC) fills the ring's next chunks
             // once the groups that held them are released, in order
             int slot = 0, in_use = 0;
             Turn put, freed;
-            bool freed_v = false, ok = true;
+            uint32_t values = 0;  // bit i: the group of barrier i holds values
+            bool ok = true;
             int groups = 0;
-            auto load = [&](const CUtensorMap* map, int n, int head, int row, int swap) {
+            auto load = [&](bool value, int head, int row) {
+                const int n = value ? kVC : kQC, swap = value ? v_swap : k_swap;
+                const CUtensorMap* map = value ? &map_v : &map_k;
                 while (ok && in_use + n > kStages) {
                     ok = mbar_wait(smem_u32(&S.empty[freed.i]), freed.phase, abort_flag, a.err);
-                    in_use -= freed_v ? kVC : kQC;
-                    freed_v = !freed_v;
+                    in_use -= (values >> freed.i) & 1 ? kVC : kQC;
                     freed.next();
                 }
                 if (!ok) return;
                 const uint32_t bar = smem_u32(&S.full[put.i]);
+                values = (values & ~(1u << put.i)) | (value ? 1u << put.i : 0u);
                 mbar_arrive_expect_tx(bar, n * kChunk);
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
@@ -315,10 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     const int kh = a.k_stride_h ? k.hk : 0, vh = a.v_stride_h ? k.hk : 0;  // a shared head is stored once
                     const int end = max(k.n0, k.n1);
+                    // keys run one tile ahead of the values, two where the tiles go apart (see the MMA warps)
+                    const int lead = k.apart ? 2 : 1;
+                    for (int j = k.kt0; ok && j < min(end, k.kt0 + lead); ++j) load(false, kh, k.k0 + j * kKeys);
                     for (int j = k.kt0; ok && j < end; ++j) {
-                        const int row = k.k0 + j * kKeys;
-                        load(&map_k, kQC, kh, row, k_swap);
-                        load(&map_v, kVC, vh, row, v_swap);
+                        load(true, vh, k.k0 + j * kKeys);
+                        if (j + lead < end) load(false, kh, k.k0 + (j + lead) * kKeys);
                     }
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
@@ -400,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (Work k; ok && take(k);) {
             const int k_begin = uniform(k.kt0), lk = uniform(k.lk), n0 = uniform(k.n0), n1 = uniform(k.n1);
+            const bool apart = uniform(k.apart) != 0;
             const int n = x ? n1 : n0, end = max(n0, n1);
             if (k_begin >= end) continue;
             if (n > k_begin) {  // a tile without keys only walks the groups
@@ -407,25 +427,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 qphase ^= 1;
                 fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
             }
-            wait_group();
-            const int both_end = min(n0, n1);  // key tiles [k_begin, both_end): both tiles work
-            take_turn(k_begin < both_end);
-            if (!ok) break;
-            if (n > k_begin) qk(slot, k_begin < both_end);
-            if (n == k_begin + 1) warp_tc_commit(smem_u32(&S.q_free[x]));  // the last product with these queries
-            slot = next(slot, kQC);
-            release();
-            for (int j = k_begin; j < end; ++j) {
+            // Key tile j is this warp's below n, or every other one where the tiles go apart; the groups of
+            // the others are walked past. Products with keys run `lead` tiles ahead of those with values.
+            const int lead = apart ? 2 : 1, first = k_begin + (apart ? x : 0);
+            const int both_end = apart ? k_begin : min(n0, n1);  // [k_begin, both_end): the tiles take turns
+            auto mine = [&](int j) { return j < n && (!apart || ((j - first) & 1) == 0); };
+            for (int j = k_begin; j < min(end, k_begin + lead); ++j) {
+                wait_group();
+                take_turn(j < both_end);
+                if (!ok) break;
+                if (mine(j)) {
+                    qk(slot, j < both_end);
+                    if (j + lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));  // the last product with these queries
+                }
+                slot = next(slot, kQC);
+                release();
+            }
+            for (int j = k_begin; ok && j < end; ++j) {
                 const int vs = slot, ks = next(slot, kVC);
-                const bool more = j + 1 < end, both = j < both_end, qk_next = j + 1 < n;
+                const bool more = j + lead < end, both = j < both_end, own = mine(j), own_next = own && j + lead < n;
                 wait_group();
                 if (more) wait_group();
                 if (!ok) break;
-                if (j < n) {
+                if (own) {
                     const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
                     const int steps = (valid + 15) / 16;
                     if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
-                        for (int c = 0; c < kVC; ++c) {  // (both tiles' warps write the same zeros)
+                        for (int c = 0; c < kVC; ++c) {  // (both tiles' warps may write the same zeros)
                             uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
                             for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
                         }
@@ -439,15 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool whole = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[x][1]), pphase));
                     if (whole) {
                         tc_fence_after();
-                        pv(0, 8, vs, steps, j == k_begin);
+                        pv(0, 8, vs, steps, j == first);
                     } else {
-                        pv(0, 6, vs, steps, j == k_begin);
+                        pv(0, 6, vs, steps, j == first);
                         wait(&S.p_full[x][1], pphase);
                         if (!ok) break;
-                        pv(6, 2, vs, steps, j == k_begin);
+                        pv(6, 2, vs, steps, j == first);
                     }
                     pphase ^= 1;
-                    if (j + 1 == n) {
+                    if (!own_next) {
                         pass_turn(both);
                         warp_tc_commit(smem_u32(&S.o_full[x]));
                     }
@@ -455,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kEarlyV) release();
                 slot = ks;
                 if (more) {
-                    if (qk_next) qk(ks, both);
-                    if (j + 2 == n) warp_tc_commit(smem_u32(&S.q_free[x]));
+                    if (own_next) {
+                        qk(ks, both);
+                        if (j + 2 * lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));
+                    }
                     slot = next(slot, kQC);
                     if (!kEarlyV) release();
                     release();
@@ -476,26 +506,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base + kColS + x * 128, tO = tmem + lane_base + kColO + x * 128;
         const int G = a.H / a.H_kv;
         const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
-        int sphase = 0, ophase = 0;
+        int sphase = 0, ophase = 0, jphase = 0, yphase = 0;
         bool dead = false;
         for (;;) {
-            // every warp of the tile leaves at the same barrier, so that none waits there for one that left
             Work k;
-            const bool got = take(k);
-            if (named_bar_or(1 + x, 128, !got)) break;
-            const int row0 = k.row0 + x * kRows, row = row0 + r;
+            if (!take(k)) break;
+            const int row0 = k.row0 + (k.apart ? 0 : x * kRows), row = row0 + r;
             const int t = row < k.nrows ? row / G : 0, head = k.hk * G + (row < k.nrows ? row - t * G : 0);
             const int end = x ? k.n1 : k.n0;
             const bool any = end > k.kt0;
             const int seen = row < k.nrows ? prompt_keys_seen(a, t, k.lq, k.lk) : 0;
             float m = -INFINITY, l = 0.0f;
-            for (int j = k.kt0; j < end; ++j) {
+            const int first = k.kt0 + (k.apart ? x : 0), step = k.apart ? 2 : 1;
+            const bool idle = row0 + (warp & 3) * 32 >= k.nrows;  // none of the warp's rows exist
+            for (int j = first; j < end; j += step) {
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.s_full[x]), sphase, abort_flag, a.err))) {
                     dead = true;
                     break;
                 }
                 sphase ^= 1;
                 tc_fence_after();
+                if (idle) {  // whatever the product makes of these rows is not used
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(smem_u32(&S.p_full[x][lane]));
+                    continue;
+                }
                 const int vis = seen - j * kKeys;  // keys of the tile this row sees
                 const bool cut = !__all_sync(0xFFFFFFFFu, vis >= kKeys);
                 uint32_t s[4][32];
@@ -519,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need = mt > m + 8.0f;
                 if (__any_sync(0xFFFFFFFFu, need)) {
                     const float m_new = need ? mt : m;
-                    if (j > k.kt0) {  // P V of the last tile is done: its commit came before S's
+                    if (j > first) {  // P V of the last tile is done: its commit came before S's
                         const float alpha = m_new == m ? 1.0f : exp2f(m - m_new);
 #pragma unroll 1
                         for (int c = 0; c < 2 * kVC; ++c) {
@@ -563,8 +598,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.o_full[x]), ophase, abort_flag, a.err));
                 ophase ^= 1;
             }
-            if (named_bar_or(1 + x, 128, dead)) break;  // every warp of the tile leaves together
+            if (dead) break;
             tc_fence_after();
+            if (k.apart) {
+                if (idle) continue;  // all rows belong to the first warp of each tile
+                if (x == 1) {  // tile B's maximum and sum to A's warp, which finds O in tensor memory
+                    S.join_ml[lane] = make_float2(m, l);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&S.join_full));
+                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_free), jphase, abort_flag, a.err));
+                    jphase ^= 1;
+                    if (dead) break;
+                    continue;
+                }
+                dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_full), jphase, abort_flag, a.err));
+                jphase ^= 1;
+                if (dead) break;
+                tc_fence_after();
+            }
+            float fa = 1.0f, fb = 0.0f;  // out = fa O_A + fb O_B
+            if (k.apart) {
+                const float2 o = S.join_ml[lane];
+                const float top = fmaxf(m, o.x);
+                fa = m == -INFINITY ? 0.0f : exp2f(m - top);
+                fb = o.x == -INFINITY ? 0.0f : exp2f(o.x - top);
+                l = l * fa + o.y * fb;
+                m = top;
+            }
+            auto load_o = [&](int c, uint32_t (&v)[32]) {  // columns 32c .. of the row's unnormalised output
+                tmem_ld32(tO + c * 32, v);
+                tmem_ld_wait();
+                tmem_ld_use32(v);
+                if (k.apart) {
+                    uint32_t u[32];
+                    tmem_ld32(tO + 128 + c * 32, u);
+                    tmem_ld_wait();
+                    tmem_ld_use32(u);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = __float_as_uint(__uint_as_float(v[e]) * fa + __uint_as_float(u[e]) * fb);
+                }
+            };
             const bool live = row < k.nrows;
             const int64_t at = (static_cast<int64_t>(k.q0) + t) * a.H + head;  // (token, head)
             if (k.parts == 1) {
@@ -573,19 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool sectors = a.d_v % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
                 for (int c = 0; c < 2 * kVC; ++c) {
-                    uint32_t v[32];
-                    if (any) {
-                        tmem_ld32(tO + c * 32, v);
-                        tmem_ld_wait();
-                    }
+                    uint32_t v[32] = {};
+                    if (any) load_o(c, v);
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {  // a whole 32-byte sector a store, where rows allow it
                         uint32_t o[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float y0 = l > 0.0f ? __uint_as_float(v[e + 2 * i]) * inv : 0.0f;
-                            const float y1 = l > 0.0f ? __uint_as_float(v[e + 2 * i + 1]) * inv : 0.0f;
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[e + 2 * i]) * inv,
+                                                                           __uint_as_float(v[e + 2 * i + 1]) * inv);
                             o[i] = *reinterpret_cast<const uint32_t*>(&b);
                         }
                         if (live && c * 32 + e + 16 <= a.d_v && sectors) {
@@ -605,36 +675,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < 2 * kVC && any; ++c) {
                     uint32_t v[32];
-                    tmem_ld32(tO + c * 32, v);
-                    tmem_ld_wait();
+                    load_o(c, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (live && c * 32 + e * 4 < a.d_v)
-                            *reinterpret_cast<uint4*>(a.part_o + prow * a.d_v + c * 32 + e * 4) =
-                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    for (int e = 0; e < 32; ++e)
+                        if (live && c * 32 + e < a.d_v)
+                            a.part_o[part_at(a, slot0 + k.part, c * 32 + e, rr)] = __uint_as_float(v[e]);
                 }
                 // the last part of this tile's rows to arrive joins them all
+                auto sync_rows = [&] {  // the warps that hold the tile's rows (each wait ends, whoever has left)
+                    __syncwarp();
+                    if (k.apart) return;
+                    if (lane == 0) mbar_arrive(smem_u32(&S.rows_sync[x]));
+                    dead |= !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.rows_sync[x]), yphase, abort_flag, a.err));
+                    yphase ^= 1;
+                };
                 __threadfence();
-                named_bar_sync(1 + x, 128);
+                sync_rows();
                 if (r == 0) S.last_part[x] = atomicAdd(&a.counters[2 * slot0 + x], 1) == k.parts - 1;
-                named_bar_sync(1 + x, 128);
+                sync_rows();
+                if (dead) break;
                 if (S.last_part[x]) {
                     __threadfence();
-                    const int cols = a.d_v / 4, rows = min(kRows, k.nrows - row0);
-                    for (int i = r; i < rows * cols; i += 128) {
-                        const int jr = i / cols, e = 4 * (i - jr * cols);
-                        const int jt = (row0 + jr) / G;
-                        const int64_t jat = (static_cast<int64_t>(k.q0) + jt) * a.H + k.hk * G + (row0 + jr - jt * G);
-                        float lse;
-                        const float4 o = prompt_join4(a, slot0, k.parts, x * kRows + jr, e, &lse);
-                        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + jat * a.d_v + e) =
-                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                        if (e == 0 && a.lse) a.lse[jat] = lse;
-                    }
+                    const int rows = min(k.apart ? kApartRows : kRows, k.nrows - row0);
+                    if (rows > 0)
+                        prompt_join<__nv_bfloat16>(a, slot0, k.parts, x * kRows, rows, k.q0, row0, k.hk, r, k.apart ? 32 : 128);
                 }
             }
             tc_fence_before();  // O has been read before the next unit's first product may overwrite it
+            if (k.apart) mbar_arrive(smem_u32(&S.join_free));
         }
     }
     tc_fence_before();
