@@ -409,11 +409,11 @@ static HierLayout hier_layout(const dsa_dims& d, int T, int n_sel) {
 struct PromptLayout {
     size_t head;      // PromptHead
     size_t units;     // PromptUnit [max_units]
-    size_t counters;  // int32 [max_slots * H_kv][2]
+    size_t joins;     // PromptJoin [max_slots / 2]
     size_t part_ml;   // float2 [max_slots * H_kv][slot_rows]
     size_t part_o;    // fp32 [max_slots * H_kv][slot_rows][d_v]
     size_t total;
-    int tile_rows, max_units, ctas, max_slots, slot_rows;
+    int tile_rows, max_units, ctas, shares, max_slots, slot_rows;
 };
 
 static dsa_status check_prompt_dims(const dsa_prompt_dims* p, int32_t Tq) {
@@ -438,10 +438,11 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     const int64_t rows = static_cast<int64_t>(Tq) * (p.H / p.H_kv);
     w.tile_rows = prompt_uses_tc(p) ? kPromptTcRows : kPromptSimtRows;
     w.ctas = device_sm_count();
-    // The plan makes fewer than 4 x ctas partials over all key heads (see there), so at most
-    // 4 x ctas / H_kv of one head.
-    w.max_slots = 4 * w.ctas / p.H_kv;
     w.slot_rows = static_cast<int>(rows < w.tile_rows ? (rows + 31) / 32 * 32 : w.tile_rows);
+    // Few query rows (single tokens): the batch's longest sequences are cut finer. The plan makes fewer than
+    // 2 x shares partials over all key heads (see there), so at most 2 x shares / H_kv of one head.
+    w.shares = (static_cast<int64_t>(Tq) <= 4ll * p.B ? 4 : 2) * w.ctas;
+    w.max_slots = 2 * w.shares / p.H_kv;
     // every sequence fills whole tiles but its last
     w.max_units = static_cast<int>(rows / w.tile_rows) + p.B + w.max_slots;
     const size_t slots = static_cast<size_t>(w.max_slots) * p.H_kv;
@@ -450,8 +451,8 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     off += 256;
     w.units = off;
     off = align256(off + sizeof(PromptUnit) * static_cast<size_t>(w.max_units));
-    w.counters = off;
-    off = align256(off + sizeof(int32_t) * 2 * slots);
+    w.joins = off;
+    off = align256(off + sizeof(PromptJoin) * static_cast<size_t>(w.max_slots / 2));
     w.part_ml = off;
     off = align256(off + sizeof(float2) * slots * w.slot_rows);
     w.part_o = off;
@@ -860,16 +861,18 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
         a.tile_rows = L.tile_rows;
         a.max_units = L.max_units;
         a.ctas = L.ctas;
+        a.shares = L.shares;
         a.max_slots = L.max_slots;
         a.slot_rows = L.slot_rows;
         a.head = reinterpret_cast<PromptHead*>(base + L.head);
         a.units = reinterpret_cast<PromptUnit*>(base + L.units);
-        a.counters = reinterpret_cast<int32_t*>(base + L.counters);
+        a.joins = reinterpret_cast<PromptJoin*>(base + L.joins);
         a.part_o = reinterpret_cast<float*>(base + L.part_o);
         a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
         const bool tc = prompt_uses_tc(*dims);
         if (!launch_prompt_plan(a, s, &launches) ||
-            !(tc ? launch_prompt_tc(a, s, &launches) : launch_prompt_simt(a, s, &launches)))
+            !(tc ? launch_prompt_tc(a, s, &launches) : launch_prompt_simt(a, s, &launches)) ||
+            !launch_prompt_join(a, s, &launches))
             st = DSA_ERR_LAUNCH;
     }
     g_last_launches = launches;

@@ -169,8 +169,16 @@ struct alignas(16) PromptUnit {
     int pad[2];
 };
 
+// Rows whose keys were split: their partials slot, slot + 1, ... (times the key heads) are joined at the end.
+struct alignas(16) PromptJoin {
+    int q0, row0, rows;
+    int slot, parts;
+    int pad[3];
+};
+
 struct PromptHead {  // written by the plan
     int n_units;
+    int n_joins;
     int head_group;  // key heads whose units run next to each other
     int next;        // units drawn, beyond every CTA's first
 };
@@ -191,12 +199,13 @@ struct PromptArgs {
     int* err;
     int tile_rows;      // rows per unit
     int max_units;      // bound on the work list's length
-    int ctas;           // CTAs the keys may be split over
+    int ctas;           // CTAs
+    int shares;         // parts that all key tiles are cut into, about
     int max_slots;      // partials the workspace holds, per key head
     int slot_rows;      // rows of one partial
     PromptHead* head;
     PromptUnit* units;
-    int32_t* counters;  // [max_slots * H_kv][2] parts that have arrived
+    PromptJoin* joins;  // [max_slots / 2]
     float* part_o;      // [max_slots * H_kv][d_v][slot_rows] unnormalised outputs
     float2* part_ml;    // [max_slots * H_kv][slot_rows] (running maximum in powers of two, sum)
 };
@@ -204,6 +213,7 @@ struct PromptArgs {
 bool prompt_uses_tc(const dsa_prompt_dims& p);
 bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches);
 bool launch_prompt_simt(const PromptArgs& a, cudaStream_t s, int* launches);
+bool launch_prompt_join(const PromptArgs& a, cudaStream_t s, int* launches);
 bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches);
 
 bool launch_attn_tc(const AttnArgs& a, cudaStream_t s, int* launches);

@@ -6,19 +6,19 @@
 //
 // Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
 // CTAs, if the longest item has more than 1.5 W / C tiles. Every item is then cut at the multiples of
-// s = max(W / 2C, a 32nd of the longest, kMinTiles); a last part shorter than kMinTiles stays with the one
-// before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
+// s = max(W / 2C, a 32nd of the longest, kMinTiles) (W / 4C where a partial has few rows and costs little to
+// join); a last part shorter than kMinTiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
 // same keys (cuts at even shares of all tiles instead: a chunk of 2048 on 32K keys 1.1 ms against 0.7).
-// An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C partials.
+// An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C (8 C) partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.
-#include "internal.h"
+#include "prompt.cuh"
 
 namespace dsa {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 constexpr int kMinTiles = 4;     // a part of fewer tiles costs more to join than it saves
 constexpr int kMaxParts = 32;    // of one item, about: one CTA joins them
-constexpr int kBuckets = 1024;
+constexpr int kBuckets = kPlanThreads;
 
 struct PlanItem {
     int q0, lq, k0, lk, row0, tiles;
@@ -42,13 +42,13 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum) {  // inclusive,
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int w = warp_sum[lane];
+        int w = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
             if (lane >= o) w += y;
         }
-        warp_sum[lane] = w;
+        if (lane < kPlanThreads / 32) warp_sum[lane] = w;
     }
     __syncthreads();
     return x + (warp ? warp_sum[warp - 1] : 0);
@@ -57,21 +57,20 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum) {  // inclusive,
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a) {
     __shared__ int prefix[kPlanThreads + 1];
     __shared__ int4 seqs[kPlanThreads];
-    __shared__ int warp_sum[32];
+    __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int bucket[kBuckets];
     __shared__ unsigned long long total_tiles;
-    __shared__ int most_tiles, most_keys, slots;
+    __shared__ int most_tiles, most_keys, slots, joins;
     const int tid = threadIdx.x, G = a.H / a.H_kv;
     griddep_launch_dependents();  // the attention's prologue may start (it waits for this grid)
     if (tid == 0) {
         total_tiles = 0;
-        most_tiles = most_keys = slots = 0;
+        most_tiles = most_keys = slots = joins = 0;
     }
     for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
-    for (int i = tid; i < 2 * a.max_slots * a.H_kv; i += kPlanThreads) a.counters[i] = 0;
     __syncthreads();
-    bool loaded = false;  // up to 1024 sequences stay in shared memory
-    // f(valid, item) for every item in turn, 1024 at a time by the whole CTA
+    bool loaded = false;  // up to 256 sequences stay in shared memory
+    // f(valid, item) for every item in turn, 256 at a time by the whole CTA
     auto for_items = [&](auto&& f) {
         for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
             const int b = b0 + tid;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     __syncthreads();
     const long long work = static_cast<long long>(total_tiles) * a.H_kv;
     const bool cut = a.max_slots > 1 && 2ll * a.ctas * most_tiles > 3 * work;
-    const int s = static_cast<int>(max(max(static_cast<long long>(kMinTiles), (work + 2 * a.ctas - 1) / (2 * a.ctas)),
+    const int s = static_cast<int>(max(max(static_cast<long long>(kMinTiles), (work + a.shares - 1) / a.shares),
                                        static_cast<long long>((most_tiles + kMaxParts - 1) / kMaxParts)));
     const int longest = max(1, cut ? min(most_tiles, s + kMinTiles) : most_tiles);
     auto bucket_of = [&](int tiles) {  // falling number of tiles
@@ -156,12 +155,19 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
         int slot = 0;
         if (!valid) return;
         units_of(it.tiles, [&](int p, int parts, int t0, int t1) {
-            if (p == 0 && parts > 1) slot = atomicAdd(&slots, parts);
+            if (p == 0 && parts > 1) {
+                slot = atomicAdd(&slots, parts);
+                const int j = atomicAdd(&joins, 1);
+                if (slot + parts <= a.max_slots && j < a.max_slots / 2)
+                    a.joins[j] = PromptJoin{it.q0, it.row0, min(a.tile_rows, it.lq * G - it.row0), slot, parts, {0, 0, 0}};
+            }
             const int at = atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
             if (at < a.max_units && slot + (parts > 1 ? parts : 0) <= a.max_slots)
                 a.units[at] = PromptUnit{it.q0, it.lq, it.k0, it.lk, it.row0, t0, t1, slot, p, parts, {0, 0}};
         });
     });
+    __syncthreads();
+    if (tid == 0) a.head->n_joins = min(joins, a.max_slots / 2);
 }
 static_assert(kBuckets == kPlanThreads, "the bucket scan takes one bucket per thread");
 
@@ -169,6 +175,29 @@ bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
     if (!launch_kernel(false, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a)) return false;
     ++*launches;
     return true;
+}
+
+// Joins the rows whose keys were split, one CTA per item and key head. In the attention kernel itself, by the
+// last part to arrive, it held up the units behind it (16 single tokens over up to 16K keys: 195 us there).
+constexpr int kJoinThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
+    griddep_wait();
+    if (static_cast<int>(blockIdx.x) >= a.head->n_joins) return;
+    const PromptJoin j = a.joins[blockIdx.x];
+    const int64_t slot0 = static_cast<int64_t>(j.slot) * a.H_kv + static_cast<int64_t>(blockIdx.y) * j.parts;
+    prompt_join<T>(a, slot0, j.parts, j.rows, j.q0, j.row0, blockIdx.y, threadIdx.x, kJoinThreads);
+}
+
+bool launch_prompt_join(const PromptArgs& a, cudaStream_t s, int* launches) {
+    if (a.max_slots < 2) return true;  // no room to split: the plan does not
+    const dim3 grid(a.max_slots / 2, a.H_kv);
+    const bool ok = a.type == DSA_F32
+                        ? launch_kernel(true, prompt_join_kernel<float>, grid, dim3(kJoinThreads), 0, s, a)
+                        : launch_kernel(true, prompt_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a);
+    if (ok) ++*launches;
+    return ok;
 }
 
 }  // namespace dsa

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     float* sk = sq + kRows * pq;
     float* sv = sk + kKeys * pq;
     float* sp = sv + kKeys * pv;
-    __shared__ int last_part;
+    griddep_launch_dependents();
     griddep_wait();
     if (static_cast<int>(blockIdx.x) >= a.head->n_units) return;
     const PromptUnit u = a.units[blockIdx.x];
@@ -187,15 +187,6 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
         }
         if (tx == 0 && a.lse) a.lse[at] = l[i] > 0.0f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
     }
-    if (u.parts == 1) return;
-    // the last part of these rows to arrive joins them all
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last_part = atomicAdd(&a.counters[2 * slot0], 1) == u.parts - 1;
-    __syncthreads();
-    if (!last_part) return;
-    __threadfence();
-    prompt_join<T>(a, slot0, u.parts, 0, min(kRows, nrows - row0), q0, row0, hk, tid, kThreads);
 }
 
 template <typename T, int kCols>

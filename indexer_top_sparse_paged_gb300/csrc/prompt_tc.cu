@@ -67,13 +67,11 @@ struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: the first 96 keys' weights, the rest
     uint64_t turn[2];  // the tensor pipe's next turn belongs to tile A, B
-    uint64_t rows_sync[2];          // the four warps of a tile, around the join of a row's parts
     uint64_t join_full, join_free;  // tile B's part of a unit apart: ready, read
     float2 join_ml[kApartRows];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
-    int last_part[2];
 };
 
 // A turn around the kMaxStages group barriers, with the parity of its phase.
@@ -189,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.q_free[i]), 1);
             mbar_init(smem_u32(&S.s_full[i]), 1);
             mbar_init(smem_u32(&S.turn[i]), 1);
-            mbar_init(smem_u32(&S.rows_sync[i]), 4);
             mbar_init(smem_u32(&S.p_full[i][0]), 4);
             mbar_init(smem_u32(&S.p_full[i][1]), 4);
             mbar_init(smem_u32(&S.o_full[i]), 1);
@@ -212,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     block_sync();
     tc_fence_after();
     const uint32_t tmem = uniform(S.tmem_base);
+    griddep_launch_dependents();
     griddep_wait();  // the work list
     const int n_units = a.head->n_units, group = a.head->head_group;
     const int n_work = n_units * a.H_kv;
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base + kColS + x * 128, tO = tmem + lane_base + kColO + x * 128;
         const int G = a.H / a.H_kv;
         const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
-        int sphase = 0, ophase = 0, jphase = 0, yphase = 0;
+        int sphase = 0, ophase = 0, jphase = 0;
         bool dead = false;
         for (;;) {
             Work k;
@@ -672,33 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rr = x * kRows + r;  // row of the partial
                 const int64_t prow = (slot0 + k.part) * a.slot_rows + rr;
                 if (live) a.part_ml[prow] = make_float2(l > 0.0f ? m : -INFINITY, l);
+                float* po = a.part_o + part_at(a, slot0 + k.part, 0, rr);
+                const int64_t pitch = a.slot_rows;
 #pragma unroll 1
                 for (int c = 0; c < 2 * kVC && any; ++c) {
                     uint32_t v[32];
                     load_o(c, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (live && c * 32 + e < a.d_v)
-                            a.part_o[part_at(a, slot0 + k.part, c * 32 + e, rr)] = __uint_as_float(v[e]);
-                }
-                // the last part of this tile's rows to arrive joins them all
-                auto sync_rows = [&] {  // the warps that hold the tile's rows (each wait ends, whoever has left)
-                    __syncwarp();
-                    if (k.apart) return;
-                    if (lane == 0) mbar_arrive(smem_u32(&S.rows_sync[x]));
-                    dead |= !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.rows_sync[x]), yphase, abort_flag, a.err));
-                    yphase ^= 1;
-                };
-                __threadfence();
-                sync_rows();
-                if (r == 0) S.last_part[x] = atomicAdd(&a.counters[2 * slot0 + x], 1) == k.parts - 1;
-                sync_rows();
-                if (dead) break;
-                if (S.last_part[x]) {
-                    __threadfence();
-                    const int rows = min(k.apart ? kApartRows : kRows, k.nrows - row0);
-                    if (rows > 0)
-                        prompt_join<__nv_bfloat16>(a, slot0, k.parts, x * kRows, rows, k.q0, row0, k.hk, r, k.apart ? 32 : 128);
+                    for (int e = 0; e < 32; e += 8) {
+                        if (!live || c * 32 + e >= a.d_v) break;  // d_v is a multiple of 8
+#pragma unroll
+                        for (int i = 0; i < 8; ++i, po += pitch) *po = __uint_as_float(v[e + i]);
+                    }
                 }
             }
             tc_fence_before();  // O has been read before the next unit's first product may overwrite it
