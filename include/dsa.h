@@ -306,7 +306,7 @@ dsa_status dsa_cache_append_rope(const dsa_dims* dims, const dsa_rope_append* ro
  * Quantised values (code * scale, code * 2^X) are formed in fp32 and rounded once to bf16. A position
  * outside [0, seq_lens[b]) (DSA_FAULT_INDEX) or in an invalid block (DSA_FAULT_BLOCK_TABLE) reads as a row
  * of zeros. Requires (d * elem) and (d_I * elem) to be multiples of 16 bytes; FP8 / MXFP8 keys: d_I
- * a multiple of 16 / 32. ws as for dsa_cache_append (only its error word is used).
+ * a multiple of 16 / 32; d, d_I <= 65536. ws as for dsa_cache_append (only its error word is used).
  */
 dsa_status dsa_cache_read(const dsa_dims* dims, const void* k_I_cache, const void* k_I_scale, const void* kv_cache,
                           const int32_t* block_table, const int32_t* seq_lens, const int32_t* start,

@@ -802,6 +802,7 @@ dsa_status dsa_cache_read(const dsa_dims* dims_in, const void* k_I_cache, const 
     if ((dims->d * act) % 16 || (dims->d_I * act) % 16) return DSA_ERR_UNSUPPORTED;
     if (dims->mode == DSA_MXFP8 && dims->d_I % 32) return DSA_ERR_UNSUPPORTED;
     if (dims->mode == DSA_BF16_KFP8 && dims->d_I % 16) return DSA_ERR_UNSUPPORTED;
+    if (dims->d > 65536 || dims->d_I > 65536) return DSA_ERR_UNSUPPORTED;  // pieces of a row are counted in 16 bits
     if (R > 0 && (!block_table || !seq_lens || !cu_rows || (!k_out && !kv_out))) return DSA_ERR_INVALID_ARG;
     if (k_out && (!k_I_cache || !scale_ok(dims, k_I_scale) || !aligned16(k_I_cache) || !aligned16(k_out)))
         return DSA_ERR_INVALID_ARG;

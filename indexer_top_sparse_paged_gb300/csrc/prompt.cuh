@@ -5,6 +5,28 @@
 
 namespace dsa {
 
+// Pairs of fp32 in one 64-bit register: two products or sums an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(v));
+    return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
 // Keys that the sequence's query token t sees: its first ones, up to its own position when causal.
 __device__ __forceinline__ int prompt_keys_seen(const PromptArgs& a, int t, int lq, int lk) {
     return a.causal ? min(lk, max(0, t + 1 + lk - lq)) : lk;
@@ -30,11 +52,11 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[8]
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kJoinAhead = 4;
+constexpr int kJoinAhead = 8;
 
 // Joins the `rows` rows of the partials slot0 .. slot0 + parts - 1 (rows row0 .. of the sequence) in that order and writes them out: sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p. n threads
 // (a power of two, at least the rows) share the work; a thread keeps one row and a run of columns, 8 at a
-// time, with the loads of four parts in flight.
+// time, with the loads of eight parts in flight.
 template <typename T>
 __device__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int rows, int q0, int row0, int hk, int tid, int n) {
     int width = 1;  // threads side by side on the rows

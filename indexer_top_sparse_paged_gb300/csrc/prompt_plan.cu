@@ -70,8 +70,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
     __syncthreads();
     bool loaded = false;  // up to 256 sequences stay in shared memory
+    bool kept = false;
+    PlanItem mine{};  // the thread's item, if there are no more than threads
     // f(valid, item) for every item in turn, 256 at a time by the whole CTA
     auto for_items = [&](auto&& f) {
+        if (kept) {
+            f(tid < prefix[kPlanThreads], mine);
+            return;
+        }
         for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
             const int b = b0 + tid;
             if (a.B > kPlanThreads || !loaded) {
@@ -109,6 +115,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
                     it = PlanItem{s.x, s.y, s.z, s.w, row0, item_tiles(a, G, s.y, s.w, row0)};
                 }
                 f(i < total, it);
+                if (a.B <= kPlanThreads && total <= kPlanThreads) {
+                    kept = true;
+                    mine = it;
+                }
             }
             if (a.B > kPlanThreads) __syncthreads();  // the next sequences take their place
         }
@@ -184,8 +194,9 @@ constexpr int kJoinThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
     griddep_wait();
-    if (static_cast<int>(blockIdx.x) >= a.head->n_joins) return;
-    const PromptJoin j = a.joins[blockIdx.x];
+    const int n = __ldcg(&a.head->n_joins);
+    const PromptJoin j = a.joins[blockIdx.x];  // (within the list's room, whatever it holds)
+    if (static_cast<int>(blockIdx.x) >= n) return;
     const int64_t slot0 = static_cast<int64_t>(j.slot) * a.H_kv + static_cast<int64_t>(blockIdx.y) * j.parts;
     prompt_join<T>(a, slot0, j.parts, j.rows, j.q0, j.row0, blockIdx.y, threadIdx.x, kJoinThreads);
 }

@@ -105,37 +105,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-// Pairs of fp32 in one 64-bit register: two products or sums an instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t y;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
-    return y;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(v));
-    return y;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
-    return y;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t y;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
-
 // A value that is the same in every lane, as the compiler can tell (it may live in a uniform register).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-
-// Eight words to a 32-byte aligned address.
-__device__ __forceinline__ void store_32b(void* p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 
 // Units are run head group by head group, the heads of a group side by side.
 __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int group, int w) {

@@ -46,6 +46,13 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
     return r != 0;
 }
 
+// Eight words to a 32-byte aligned address.
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Programmatic dependent launch: allow the next kernel of the stream to start launching (its blocks
 // run their prologue while this grid finishes) / wait until the previous kernel of the stream has
 // completed and its memory writes are visible. Both are no-ops for kernels launched without it.
