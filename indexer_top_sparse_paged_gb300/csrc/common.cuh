@@ -445,13 +445,17 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 
 // (scale cos, scale sin) of position pos at angular frequency freq (radians per position). The angle
 // is formed in fp64 as turns and its whole part dropped there, so that far positions keep their
-// fraction (4e-11 turns at a million positions); the transpose turns the other way.
+// fraction (4e-11 turns at a million positions); what fp32 leaves of the fraction (up to 2^-26 turns, one
+// and a half steps of a cosine near 1) comes back to first order. The transpose turns the other way.
 __device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale, bool transpose) {
-    const double turns = static_cast<double>(pos) * (freq * 0.15915494309189535);  // 1 / (2 pi)
-    const float f = static_cast<float>(turns - rint(turns));
+    double turns = static_cast<double>(pos) * (freq * 0.15915494309189535);  // 1 / (2 pi)
+    turns -= rint(turns);
+    const float f = static_cast<float>(turns);
+    const float rest = 6.2831853f * static_cast<float>(turns - static_cast<double>(f));
     float s, c;
     sincospif(2.0f * f, &s, &c);
-    return make_float2(scale * c, transpose ? -scale * s : scale * s);
+    const float cc = fmaf(-s, rest, c), ss = fmaf(c, rest, s);
+    return make_float2(scale * cc, transpose ? -scale * ss : scale * ss);
 }
 
 // One pair turned, with the roundings written out (the same bits in every kernel).
