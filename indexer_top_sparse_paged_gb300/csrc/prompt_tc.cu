@@ -318,7 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
     } else {
         // --------------------------------------------------------------------------------- MMA
-        constexpr bool kEarlyV = kQC == 3;
+        // With three key chunks the ring holds little more than what is in use: values go back before the product
+        // with the next keys, not after it, and those keys are waited for as late as that, inside the turn
+        // (8192 tokens, 192 / 128 columns: 478 us against 589 and 504; with 128 columns the same costs 440 against 410).
+        constexpr bool kTight = kQC == 3;
         // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4); what the descriptors and
         // the branches depend on is made uniform by hand where it comes from memory.
         const int x = warp - 8;  // tile
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int vs = slot, ks = next(slot, kVC);
                 const bool more = j + lead < end, both = j < both_end, own = mine(j), own_next = own && j + lead < n;
                 wait_group();
-                if (more) wait_group();
+                if (more && !kTight) wait_group();
                 if (!ok) break;
                 if (own) {
                     const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
@@ -449,17 +452,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         warp_tc_commit(smem_u32(&S.o_full[x]));
                     }
                 }
-                if (kEarlyV) release();
+                if (kTight) release();
                 slot = ks;
                 if (more) {
+                    if (kTight) wait_group();
+                    if (!ok) break;
                     if (own_next) {
                         qk(ks, both);
                         if (j + 2 * lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));
                     }
                     slot = next(slot, kQC);
-                    if (!kEarlyV) release();
+                    if (!kTight) release();
                     release();
-                } else if (!kEarlyV) {
+                } else if (!kTight) {
                     release();
                 }
             }
@@ -512,14 +517,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[i][e] = i * 32 + e < vis ? s[i][e] : 0xFF800000u;
                 }
-                float mx[8];
+                const uint64_t c2c2 = pack2(c2, c2);
+                uint64_t ls[4] = {0, 0, 0, 0};  // pairs of sums
+                auto weights = [&](int i, uint64_t nn) {  // over columns that have been read
+                    uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = fmaxf(__uint_as_float(s[i / 2][16 * (i & 1)]), __uint_as_float(s[i / 2][16 * (i & 1) + 1]));
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 z = unpack2(fma2(pack2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2c2, nn));
+                        const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+                        pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    tmem_st16(tS + i * 16, pk);
+                };
+                auto send = [&](int part) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][part]));
+                };
+                // Once every row of the warp has a reference, the weights are made with it at once and the tile's
+                // own maximum is found beside them; a row that outgrew its reference by 2^8 sends the warp back.
+                constexpr bool early = false;
+                float mx[4];
+                uint64_t nn = pack2(-m, -m);
 #pragma unroll
-                for (int e = 2; e < 16; e += 2)
+                for (int i = 0; i < 4; ++i) {
+                    float y0 = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1])), y1 = fmaxf(__uint_as_float(s[i][2]), __uint_as_float(s[i][3]));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mx[i] = max3(mx[i], __uint_as_float(s[i / 2][16 * (i & 1) + e]), __uint_as_float(s[i / 2][16 * (i & 1) + e + 1]));
-                const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c2;
+                    for (int e = 4; e < 32; e += 4) {
+                        y0 = max3(y0, __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+                        y1 = max3(y1, __uint_as_float(s[i][e + 2]), __uint_as_float(s[i][e + 3]));
+                    }
+                    mx[i] = fmaxf(y0, y1);
+                    if (early && i < 3) weights(i, nn);
+                }
+                const float mt = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c2;
                 const bool need = mt > m + 8.0f;
                 if (__any_sync(0xFFFFFFFFu, need)) {
                     const float m_new = need ? mt : m;
@@ -530,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t v[32];
                             tmem_ld32(tO + c * 32, v);
                             tmem_ld_wait();
+                            tmem_ld_use32(v);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
                             tmem_st32(tO + c * 32, v);
@@ -539,27 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = m_new;
                 }
                 const float neg = m == -INFINITY ? 0.0f : -m;  // no key yet: every weight is 2^-inf = 0
-                const uint64_t c2c2 = pack2(c2, c2), nn = pack2(neg, neg);
-                uint64_t ls[4] = {0, 0, 0, 0};  // pairs of sums
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 z = unpack2(fma2(pack2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2c2, nn));
-                        const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-                        pk[e] = *reinterpret_cast<const uint32_t*>(&b);
-                    }
-                    tmem_st16(tS + i * 16, pk);  // over columns that have been read
-                    if (i >= 2) {  // the product may begin while the last quarter is made
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][i - 2]));
-                    }
-                }
+                nn = pack2(neg, neg);
+                weights(0, nn);
+                weights(1, nn);
+                weights(2, nn);
+                send(0);  // the product may begin while the last quarter is made
+                weights(3, nn);
+                send(1);
                 const float2 lp = unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])));
                 l += lp.x + lp.y;
             }
