@@ -92,7 +92,7 @@ __device__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int r
                 M = top;
             }
         }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= inv;
         if (m == 8) {
@@ -102,7 +102,7 @@ __device__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int r
             for (int e = 0; e < 8; ++e)
                 if (e < m) out[c + e] = static_cast<T>(o[e]);
         }
-        if (c == 0 && a.lse) a.lse[at] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (c == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     }
 }
 

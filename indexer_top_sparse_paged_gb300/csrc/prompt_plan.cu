@@ -6,8 +6,8 @@
 //
 // Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
 // CTAs, if the longest item has more than 1.5 W / C tiles. Every item is then cut at the multiples of
-// s = max(W / 2C, a 32nd of the longest, kMinTiles) (W / 4C where a partial has few rows and costs little to
-// join); a last part shorter than kMinTiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
+// s = max(W / 2C, a 32nd of the longest, kMinTiles) (W / 4C where a partial has few rows); a last part shorter
+// than kMinTiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
 // same keys (cuts at even shares of all tiles instead: a chunk of 2048 on 32K keys 1.1 ms against 0.7).
 // An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C (8 C) partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.

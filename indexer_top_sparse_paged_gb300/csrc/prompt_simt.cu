@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
             continue;
         }
         const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;  // (token, head)
-        const float inv = l[i] > 0.0f ? 1.0f / l[i] : 0.0f;
+        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
             const int e = 4 * tx + 64 * j;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
             if (e < a.d_v)
                 store4(static_cast<T*>(a.out) + at * a.d_v + e, make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv));
         }
-        if (tx == 0 && a.lse) a.lse[at] = l[i] > 0.0f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+        if (tx == 0 && a.lse) a.lse[at] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
 }
 

@@ -590,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (dead) break;
             tc_fence_after();
+            if (idle) continue;  // (a unit apart: all rows belong to the first warp of each tile)
             if (k.apart) {
-                if (idle) continue;  // all rows belong to the first warp of each tile
                 if (x == 1) {  // tile B's maximum and sum to A's warp, which finds O in tensor memory
                     S.join_ml[lane] = make_float2(m, l);
                     tc_fence_before();
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = row < k.nrows;
             const int64_t at = (static_cast<int64_t>(k.q0) + t) * a.H + head;  // (token, head)
             if (k.parts == 1) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint16_t* out = static_cast<uint16_t*>(a.out) + at * a.d_v;
                 const bool sectors = a.d_v % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
@@ -656,12 +656,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (live && a.lse) a.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                if (live && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
                 const int64_t slot0 = static_cast<int64_t>(k.slot) * a.H_kv + static_cast<int64_t>(k.hk) * k.parts;
                 const int rr = x * kRows + r;  // row of the partial
                 const int64_t prow = (slot0 + k.part) * a.slot_rows + rr;
-                if (live) a.part_ml[prow] = make_float2(l > 0.0f ? m : -INFINITY, l);
+                if (live) a.part_ml[prow] = make_float2(l == 0.0f ? -INFINITY : m, l);
                 float* po = a.part_o + part_at(a, slot0 + k.part, 0, rr);
                 const int64_t pitch = a.slot_rows;
 #pragma unroll 1

@@ -156,6 +156,39 @@ def test_strided_views_and_rows_left_alone(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_key_head_expanded_over_all(dtype):
+    """Key heads that are one stored head (stride 0), alone and together with one value row for all keys."""
+    nq, nk = [130, 7], [130, 300]
+    q, k, v = make(dtype, nq, nk, 6, 1, 128, 64, seed=21)
+    k, v = k.expand(-1, 3, -1), v.expand(-1, 3, -1)
+    check(attend(q, k, v, nq, nk, 0.1), q, k, v, nq, nk, 0.1)
+    v = v[:1].expand(len(v), -1, -1)
+    check(attend(q, k, v, nq, nk, 0.1), q, k, v, nq, nk, 0.1)
+    q = q[:, :1].expand(-1, 6, -1)
+    check(attend(q, k, v, nq, nk, 0.1), q, k, v, nq, nk, 0.1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_workspace_serves_smaller_calls_and_the_least_size_does(dtype):
+    """The size grows with the query tokens, and a call with just that many bytes is not refused and writes no
+    byte behind them: long single tokens split their keys over every partial there is room for."""
+    for B, H, H_kv, L in ((1, 8, 1, 9000), (3, 64, 8, 5000), (40, 8, 2, 700), (5, 130, 130, 600)):
+        nq, nk = [1] * B, [L - 13 * i for i in range(B)]
+        q, k, v = make(dtype, nq, nk, H, H_kv, 64, 64, seed=B)
+        dims = dsa.prompt_dims(q, k, v, B)
+        sizes = [dsa.prompt_workspace(dims, n).numel() for n in (0, 1, B, 4 * B, 4 * B + 1, 300, 5000)]
+        assert sizes == sorted(sizes)
+        n = sizes[2]
+        room = torch.full((n + 4096 + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+        off = -room.data_ptr() % 256
+        ws = room[off:off + n]
+        ws[:256] = 0
+        got = dsa.prompt_attn(dims, q, k, v, starts(nq), starts(nk), 0.125, ws=ws)
+        check(got, q, k, v, nq, nk, 0.125)
+        assert dsa.read_error(ws) == 0 and bool((room[off + n:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_bad_offsets_are_skipped_and_reported(dtype):
     q, k, v = make(dtype, [100], [100], 4, 2, 64, 64)
     dims = dsa.prompt_dims(q, k, v, 3)
