@@ -485,6 +485,9 @@ def prompt_dims(q, k, v, B: int, causal: bool = True) -> PromptDims:
     return PromptDims(*_prompt_fields(q, k, v, B, causal))
 
 
+_PROMPT_FIELDS = tuple(f for f, _ in PromptDims._fields_)
+
+
 def _prompt_fields(q, k, v, B, causal):
     qn, kn, vn, qs, ks, vs, dt = q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), q.dtype
     if not len(qn) == len(kn) == len(vn) == 3 or (qs[2] != 1 and q.numel()) or (ks[2] != 1 and k.numel()) or (vs[2] != 1 and v.numel()):
@@ -511,7 +514,7 @@ def prompt_workspace(dims: PromptDims, Tq: int, device="cuda", stream=None) -> t
 def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, out=None, lse=None, stream=None):
     """(out[Tq][H][d_v], lse[Tq][H]) of dense attention over packed sequences: sequence b has the queries
     cu_q[b] .. cu_q[b + 1] - 1, the last of its positions, and the keys cu_k[b] .. cu_k[b + 1] - 1."""
-    if bytes(PromptDims(*_prompt_fields(q, k, v, dims.B, dims.causal))) != bytes(dims):
+    if tuple(getattr(dims, f) for f in _PROMPT_FIELDS) != _prompt_fields(q, k, v, dims.B, dims.causal):
         raise ValueError("q, k and v differ from the tensors dims was made for")
     dev = _device(q, k, v, cu_q, cu_k, out, lse, ws)
     _int32(cu_q, dims.B + 1, "cu_q")

@@ -875,9 +875,17 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
         a.part_o = reinterpret_cast<float*>(base + L.part_o);
         a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
         const bool tc = prompt_uses_tc(*dims);
-        if (!launch_prompt_plan(a, s, &launches) ||
+        // Keys are split into parts of at least min_tiles tiles; where that cannot be and there are CTAs for
+        // all units at once, their order does not matter either, and one launch does (a prompt of 100 tokens:
+        // 17 us a call against 28).
+        const int64_t items = static_cast<int64_t>(Tq) * (dims->H / dims->H_kv) / L.tile_rows + dims->B;
+        a.min_tiles = tc ? kPromptTcMinTiles : kPromptSimtMinTiles;
+        const bool whole = Tk <= (2 * a.min_tiles - 1) * kPromptKeys;
+        a.self_plan = whole && dims->B <= 32 && items * dims->H_kv <= (tc ? L.ctas : 2 * L.ctas) ? 1 : 0;
+        if (a.self_plan) a.max_units = static_cast<int>(items);
+        if ((!a.self_plan && !launch_prompt_plan(a, s, &launches)) ||
             !(tc ? launch_prompt_tc(a, s, &launches) : launch_prompt_simt(a, s, &launches)) ||
-            !launch_prompt_join(a, s, &launches))
+            (!whole && !launch_prompt_join(a, s, &launches)))
             st = DSA_ERR_LAUNCH;
     }
     g_last_launches = launches;

@@ -158,6 +158,8 @@ bool launch_cache_read(const dsa_dims& d, bool kv_fp8, const void* k_cache, cons
 constexpr int kPromptSimtRows = 64;  // rows (token, head of the group) per unit of the CUDA-core kernel
 constexpr int kPromptTcRows = 256;   // ... of the tensor-core kernel: two tiles of 128
 constexpr int kPromptKeys = 128;     // keys per tile of the work list's key ranges
+// A part of fewer key tiles costs more to join than it saves (tensor cores, CUDA cores).
+constexpr int kPromptTcMinTiles = 4, kPromptSimtMinTiles = 2;
 
 // One unit of work per key head: up to tile_rows rows of a sequence against a range of its key tiles.
 struct alignas(16) PromptUnit {
@@ -201,6 +203,8 @@ struct PromptArgs {
     int max_units;      // bound on the work list's length
     int ctas;           // CTAs
     int shares;         // parts that all key tiles are cut into, about
+    int min_tiles;      // key tiles of a part at least
+    int self_plan;      // small calls: no work list, every CTA finds its unit in the lengths itself
     int max_slots;      // partials the workspace holds, per key head
     int slot_rows;      // rows of one partial
     PromptHead* head;

@@ -32,6 +32,46 @@ __device__ __forceinline__ int prompt_keys_seen(const PromptArgs& a, int t, int 
     return a.causal ? min(lk, max(0, t + 1 + lk - lq)) : lk;
 }
 
+// Small calls (at most 32 sequences and 7 key tiles, so that nothing is split) have no work list: a warp reads
+// every sequence's bounds, and all its lanes return unit `index`; false past the last one. The sequences
+// whose bounds are no ranges have no units (reported by the first).
+__device__ __forceinline__ bool prompt_self_unit(const PromptArgs& a, int index, PromptUnit& u) {
+    const int lane = threadIdx.x & 31, G = a.H / a.H_kv;
+    int q0 = 0, lq = 0, k0 = 0, lk = 0, n = 0;
+    if (lane < a.B) {
+        const int q1 = a.cu_q[lane + 1], k1 = a.cu_k[lane + 1];
+        q0 = a.cu_q[lane];
+        k0 = a.cu_k[lane];
+        if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
+            if (index == 0) atomicOr(a.err, DSA_FAULT_INDEX);
+        } else {
+            lq = q1 - q0;
+            lk = k1 - k0;
+            n = (lq * G + a.tile_rows - 1) / a.tile_rows;
+        }
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    const unsigned owner = __ballot_sync(0xFFFFFFFFu, index >= upto - n && index < upto);
+    if (!owner) return false;
+    const int src = __ffs(owner) - 1;
+    u.q0 = __shfl_sync(0xFFFFFFFFu, q0, src);
+    u.lq = __shfl_sync(0xFFFFFFFFu, lq, src);
+    u.k0 = __shfl_sync(0xFFFFFFFFu, k0, src);
+    u.lk = __shfl_sync(0xFFFFFFFFu, lk, src);
+    u.row0 = (index - __shfl_sync(0xFFFFFFFFu, upto - n, src)) * a.tile_rows;
+    u.kt0 = 0;
+    u.kt1 = (u.lk + kPromptKeys - 1) / kPromptKeys;
+    u.slot = 0;
+    u.part = 0;
+    u.parts = 1;
+    return true;
+}
+
 // Column c of row r of partial `slot`: the rows of a column lie side by side, so that a warp whose lanes hold
 // rows writes and reads whole lines.
 __device__ __forceinline__ int64_t part_at(const PromptArgs& a, int64_t slot, int c, int r) {

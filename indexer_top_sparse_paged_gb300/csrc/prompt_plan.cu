@@ -5,9 +5,9 @@
 // them against a range of the key tiles they see; every unit runs once for each key head.
 //
 // Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
-// CTAs, if the longest item has more than 1.5 W / C tiles. Every item is then cut at the multiples of
-// s = max(W / 2C, a 32nd of the longest, kMinTiles) (W / 4C where a partial has few rows); a last part shorter
-// than kMinTiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
+// CTAs, if the longest item has more than 1.25 W / C tiles. Every item is then cut at the multiples of
+// s = max(W / 2C, a 32nd of the longest, min_tiles) (W / 4C where a partial has few rows); a last part shorter
+// than min_tiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
 // same keys (cuts at even shares of all tiles instead: a chunk of 2048 on 32K keys 1.1 ms against 0.7).
 // An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C (8 C) partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.
@@ -16,7 +16,6 @@
 namespace dsa {
 
 constexpr int kPlanThreads = 256;
-constexpr int kMinTiles = 4;     // a part of fewer tiles costs more to join than it saves
 constexpr int kMaxParts = 32;    // of one item, about: one CTA joins them
 constexpr int kBuckets = kPlanThreads;
 
@@ -135,16 +134,16 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     });
     __syncthreads();
     const long long work = static_cast<long long>(total_tiles) * a.H_kv;
-    const bool cut = a.max_slots > 1 && 2ll * a.ctas * most_tiles > 3 * work;
-    const int s = static_cast<int>(max(max(static_cast<long long>(kMinTiles), (work + a.shares - 1) / a.shares),
+    const bool cut = a.max_slots > 1 && 4ll * a.ctas * most_tiles > 5 * work;
+    const int s = static_cast<int>(max(max(static_cast<long long>(a.min_tiles), (work + a.shares - 1) / a.shares),
                                        static_cast<long long>((most_tiles + kMaxParts - 1) / kMaxParts)));
-    const int longest = max(1, cut ? min(most_tiles, s + kMinTiles) : most_tiles);
+    const int longest = max(1, cut ? min(most_tiles, s + a.min_tiles) : most_tiles);
     auto bucket_of = [&](int tiles) {  // falling number of tiles
         return kBuckets - 1 - static_cast<int>(static_cast<long long>(min(tiles, longest)) * (kBuckets - 1) / longest);
     };
     // f(part, parts, its first tile, its last + 1) for every unit of an item
     auto units_of = [&](int tiles, auto&& f) {
-        const int parts = cut ? max(1, (tiles + s - kMinTiles) / s) : 1;
+        const int parts = cut ? max(1, (tiles + s - a.min_tiles) / s) : 1;
         for (int p = 0; p < parts; ++p) f(p, parts, p * s, p == parts - 1 ? tiles : (p + 1) * s);
     };
     for_items([&](bool valid, const PlanItem& it) {

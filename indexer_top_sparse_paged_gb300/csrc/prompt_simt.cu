@@ -62,7 +62,7 @@ __device__ __forceinline__ void load_rows(float* dst, int pitch, const T* src, i
 }
 
 template <typename T, int kCols>  // kCols: float4 columns of the output per thread, ceil(d_v / 64)
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(PromptArgs a) {
     extern __shared__ float smem[];
     const int pq = pitch(a.d_qk), pv = pitch(a.d_v);
     float* sq = smem;
@@ -71,8 +71,13 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(PromptArgs a) {
     float* sv = sk + max(kKeys * pq, kRows * kPitchP);
     griddep_launch_dependents();
     griddep_wait();
-    if (static_cast<int>(blockIdx.x) >= a.head->n_units) return;
-    const PromptUnit u = a.units[blockIdx.x];
+    PromptUnit u;
+    if (a.self_plan) {
+        if (!prompt_self_unit(a, blockIdx.x, u)) return;  // (every warp for itself)
+    } else {
+        if (static_cast<int>(blockIdx.x) >= a.head->n_units) return;
+        u = a.units[blockIdx.x];
+    }
     const int hk = blockIdx.y, G = a.H / a.H_kv;
     const int q0 = u.q0, lq = u.lq, k0 = u.k0, lk = u.lk, nrows = lq * G, row0 = u.row0;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;  // the thread's rows: kR * ty ..
@@ -224,7 +229,7 @@ template <typename T, int kCols>
 static bool launch_typed(const PromptArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d_qk, a.d_v);
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_simt_kernel<T, kCols>), smem)) return false;
-    return launch_kernel(true, prompt_simt_kernel<T, kCols>, dim3(a.max_units, a.H_kv), dim3(kThreads), smem, s, a);
+    return launch_kernel(!a.self_plan, prompt_simt_kernel<T, kCols>, dim3(a.max_units, a.H_kv), dim3(kThreads), smem, s, a);
 }
 
 template <typename T>

@@ -109,15 +109,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Units are run head group by head group, the heads of a group side by side.
+// A whole warp calls (every lane gets the same); hk is -1 past the last unit.
 __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int group, int w) {
     Work x;
-    const int per = n_units * group;  // n_units * H_kv is below 2^31
-    const int g = group == a.H_kv ? 0 : w / per;
-    const int heads = min(group, a.H_kv - g * group);
-    const int rem = w - g * per;
-    const int unit = rem / heads;
-    x.hk = g * group + rem - unit * heads;
-    const PromptUnit u = a.units[unit];
+    PromptUnit u;
+    x.hk = -1;
+    if (a.self_plan) {
+        if (!prompt_self_unit(a, w / a.H_kv, u)) return x;
+        x.hk = w % a.H_kv;
+    } else {
+        if (w >= n_units * a.H_kv) return x;  // n_units * H_kv is below 2^31
+        const int per = n_units * group;
+        const int g = group == a.H_kv ? 0 : w / per;
+        const int heads = min(group, a.H_kv - g * group);
+        const int rem = w - g * per;
+        const int unit = rem / heads;
+        x.hk = g * group + rem - unit * heads;
+        u = a.units[unit];
+    }
     const int G = a.H / a.H_kv;
     x.nrows = u.lq * G;
     auto tiles = [&](int r0) {
@@ -182,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = uniform(S.tmem_base);
     griddep_launch_dependents();
     griddep_wait();  // the work list
-    const int n_units = a.head->n_units, group = a.head->head_group;
-    const int n_work = n_units * a.H_kv;
+    const int n_units = a.self_plan ? 0 : a.head->n_units, group = a.self_plan ? 0 : a.head->head_group;
     // The next unit, for every role but the one that hands them out; false: no more, or a wait gave up.
     int turn = 0, turn_phase = 0;
     auto take = [&](Work& k) {
@@ -204,15 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int qphase0 = 1, qphase1 = 1, fphase = 1, slot = 0;
         bool ok = true;
         for (int w = blockIdx.x; ok;) {
-            Work k;
-            k.hk = -1;
-            if (w < n_work) k = get_work(a, n_units, group, w);
+            const Work k = get_work(a, n_units, group, w);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.work_free[slot]), fphase, abort_flag, a.err));
             if (!ok) break;
             if (lane == 0) {
                 S.work[slot] = k;
                 mbar_arrive(smem_u32(&S.work_full[slot]));
-                if (k.hk >= 0) w = gridDim.x + atomicAdd(&a.head->next, 1);
+                // (without a list there is a CTA for every unit)
+                if (k.hk >= 0) w = a.self_plan ? 0x7FFFFFFF : gridDim.x + atomicAdd(&a.head->next, 1);
             }
             if (++slot == kQueue) slot = 0, fphase ^= 1;
             w = __shfl_sync(0xFFFFFFFFu, w, 0);
@@ -715,8 +722,8 @@ static bool launch_typed(const PromptArgs& a, const Maps& m, cudaStream_t s) {
     static_assert(smem <= kSmemMax && Layout<kQC>::kStages >= 2 * kQC + kVC, "two key tiles and a value tile in flight");
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_tc_kernel<kQC, kVC>), smem)) return false;
     const int64_t most = static_cast<int64_t>(a.max_units) * a.H_kv;  // below 2^31 (checked by the caller)
-    const int grid = static_cast<int>(most < a.ctas ? most : a.ctas);
-    return launch_kernel(true, prompt_tc_kernel<kQC, kVC>, dim3(grid), dim3(kThreads), smem, s, a, m.q, m.k, m.v, m.q_map,
+    const int grid = static_cast<int>(a.self_plan || most < a.ctas ? most : a.ctas);
+    return launch_kernel(!a.self_plan, prompt_tc_kernel<kQC, kVC>, dim3(grid), dim3(kThreads), smem, s, a, m.q, m.k, m.v, m.q_map,
                          m.k_swap, m.v_swap);
 }
 

@@ -189,6 +189,17 @@ def test_a_workspace_serves_smaller_calls_and_the_least_size_does(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_calls_around_the_one_launch_form(dtype):
+    """32 and 33 sequences, 896 and 897 keys in all, as many units as CTAs and more: the same answers with and
+    without a work list."""
+    for nq, nk, H, H_kv in (([3] * 32, [28] * 32, 4, 2), ([3] * 33, [27] * 33, 4, 2), ([100], [896], 2, 2), ([100], [897], 2, 2),
+                            ([1], [896], 130, 130), ([5], [300], 152, 152), ([5], [300], 153, 153), ([1] * 8, [112] * 8, 19, 19),
+                            ([0, 0, 4], [0, 9, 4], 3, 1), ([896], [896], 19, 19)):
+        q, k, v = make(dtype, nq, nk, H, H_kv, 64, 64, seed=H)
+        check(attend(q, k, v, nq, nk, 0.125), q, k, v, nq, nk, 0.125)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_bad_offsets_are_skipped_and_reported(dtype):
     q, k, v = make(dtype, [100], [100], 4, 2, 64, 64)
     dims = dsa.prompt_dims(q, k, v, 3)
