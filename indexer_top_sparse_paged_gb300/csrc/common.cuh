@@ -443,18 +443,25 @@ __device__ __forceinline__ int mx_exponent(float amax) {
     return max(E - 135, -127);
 }
 
-// (scale cos, scale sin) of position pos at angular frequency freq (radians per position). The angle
-// is formed in fp64 as turns and its whole part dropped there, so that far positions keep their
-// fraction (4e-11 turns at a million positions); what fp32 leaves of the fraction (up to 2^-26 turns, one
-// and a half steps of a cosine near 1) comes back to first order. The transpose turns the other way.
+// (scale cos, scale sin) of position pos at angular frequency freq (radians per position, finite). The
+// turns per position are held as a 64-bit binary fraction (freq / 2 pi in fp64, cut at 2^-64), so that their
+// product with the position drops its whole part by itself and far positions keep their fraction (to
+// 2^-33 turns from the cut, 2^-53 of the angle from fp64); one fp64 product, where the fp64 pipe takes 16 cycles
+// a warp. What fp32 leaves of the fraction (up to 2^-26 turns, one and a half steps of a cosine near 1)
+// comes back to first order. The transpose turns the other way.
 __device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale, bool transpose) {
-    double turns = static_cast<double>(pos) * (freq * 0.15915494309189535);  // 1 / (2 pi)
-    turns -= rint(turns);
-    const float f = static_cast<float>(turns);
-    const float rest = 6.2831853f * static_cast<float>(turns - static_cast<double>(f));
+    const long long bits = __double_as_longlong(freq * 0.15915494309189535);  // 1 / (2 pi)
+    const int shift = static_cast<int>((bits >> 52) & 0x7FF) - 1011;          // mantissa * 2^(exponent - 1075 + 64)
+    const unsigned long long m = (bits & 0xFFFFFFFFFFFFFll) | 0x10000000000000ll;
+    unsigned long long unit = shift >= 64 || shift <= -64 ? 0ull : shift >= 0 ? m << shift : m >> -shift;
+    if (bits < 0) unit = 0ull - unit;
+    const long long turns = static_cast<long long>(unit * static_cast<unsigned long long>(static_cast<long long>(pos)));
+    const float f = static_cast<float>(static_cast<int>(turns >> 32));  // in 2^-32 turns, rounded to 24 bits
+    const long long rest = turns - (static_cast<long long>(f) << 32);
     float s, c;
-    sincospif(2.0f * f, &s, &c);
-    const float cc = fmaf(-s, rest, c), ss = fmaf(c, rest, s);
+    sincospif(f * 0x1p-31f, &s, &c);
+    const float r = 6.2831853f * 0x1p-64f * static_cast<float>(rest);
+    const float cc = fmaf(-s, r, c), ss = fmaf(c, r, s);
     return make_float2(scale * cc, transpose ? -scale * ss : scale * ss);
 }
 
