@@ -235,7 +235,7 @@ dsa_status dsa_indexer_prolog(const dsa_dims* dims, const void* k_I_new, const v
  * angle_i = pos * freq[i], i < rot / 2, and (a, b) the columns of pair i,
  *   y_a = scale * (x_a cos angle_i - x_b sin angle_i),  y_b = scale * (x_a sin angle_i + x_b cos angle_i)
  *   DSA_ROPE_INTERLEAVED: (a, b) = (2i, 2i + 1);  DSA_ROPE_HALF: (a, b) = (i, i + rot / 2).
- * The arithmetic is fp32 (the angle fp64), rounded once to the tensor's type.
+ * The arithmetic is fp32 (the angle in 64 bits), rounded once to the tensor's type.
  *
  * dsa_rope_frequencies: freq[rot / 2] on the HOST, in radians per position, for base^(-2i / rot)
  *   stretched to contexts `factor` times the trained length (factor 1: no scaling):
@@ -325,7 +325,7 @@ dsa_status dsa_cache_read(const dsa_dims* dims, const void* k_I_cache, const voi
  *        values and not written. A sequence whose entries descend or leave [0, Tq] / [0, Tk] is skipped and
  *        reported (DSA_FAULT_INDEX).
  *   out  [Tq][H][d_v] in q's type, lse [Tq][H] fp32 (natural log; may be NULL), dense. A query that sees no
- *        key gives out = 0, lse = -inf.
+ *        key gives out = 0, lse = -inf. Neither may overlap an input.
  *   sm_scale > 0. Inputs of a sequence are finite.
  * Widths: d_qk, d_v <= 256; H a multiple of H_kv; addresses, strides and row widths multiples of 16 bytes.
  * ws: at least dsa_prompt_workspace_size bytes, 256-byte aligned, initialised with dsa_workspace_init.

@@ -60,7 +60,7 @@ __device__ __forceinline__ void write_piece(const ReadPiece& p, bool codes) {
 }
 
 // First the rows' places (the sequences' first rows in shared memory, so that the search waits for memory
-// once, then each row's block), then every thread's pieces of latent rows and keys, four loads at a time.
+// once, then each row's block), then every thread's pieces of latent rows and keys, kReadBatch at a time.
 template <bool kKvCodes, int kKeyMode>  // latent rows as FP8 records; keys: DSA_BF16 (copied), DSA_BF16_KFP8, DSA_MXFP8
 __global__ void __launch_bounds__(kReadThreads, kReadCtas) cache_read_kernel(ReadArgs a) {
     __shared__ int64_t phys[kReadRows];  // physical cache row, -1: zeros, -2: not written

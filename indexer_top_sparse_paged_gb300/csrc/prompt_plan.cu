@@ -7,8 +7,9 @@
 // Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
 // CTAs, if the longest item has more than 1.25 W / C tiles. Every item is then cut at the multiples of
 // s = max(W / 2C, a 32nd of the longest, min_tiles) (W / 4C where a partial has few rows); a last part shorter
-// than min_tiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the
-// same keys (cuts at even shares of all tiles instead: a chunk of 2048 on 32K keys 1.1 ms against 0.7).
+// than min_tiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that
+// run side by side read the same keys (a chunk of 2048 on 32K keys: 0.7 ms where cuts at even shares of all
+// tiles took 1.1).
 // An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C (8 C) partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.
 #include "prompt.cuh"
@@ -30,27 +31,31 @@ __device__ __forceinline__ int item_tiles(const PromptArgs& a, int G, int lq, in
     return (seen + kPromptKeys - 1) / kPromptKeys;
 }
 
-__device__ __forceinline__ int block_scan(int x, int* warp_sum) {  // inclusive, over the CTA
+// Inclusive sums over the CTA of values of 0 or more, none above `most` (below 2^31): sequences that overlap,
+// which some descending entry has let happen, may have more items than the lists were made for.
+__device__ __forceinline__ int block_scan(int value, int most, int* warp_sum) {
+    unsigned x = min(value, most);
+    const unsigned top = most;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
+        const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x = min(x + y, top);
     }
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = x;
+    if (lane == 31) warp_sum[warp] = static_cast<int>(x);
     __syncthreads();
     if (warp == 0) {
-        int w = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
+        unsigned w = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
-            if (lane >= o) w += y;
+            const unsigned y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w = min(w + y, top);
         }
-        if (lane < kPlanThreads / 32) warp_sum[lane] = w;
+        if (lane < kPlanThreads / 32) warp_sum[lane] = static_cast<int>(w);
     }
     __syncthreads();
-    return x + (warp ? warp_sum[warp - 1] : 0);
+    return static_cast<int>(min(x + (warp ? warp_sum[warp - 1] : 0), top));
 }
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a) {
@@ -77,6 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
             f(tid < prefix[kPlanThreads], mine);
             return;
         }
+        int left = a.max_units;  // items
         for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
             const int b = b0 + tid;
             if (a.B > kPlanThreads || !loaded) {
@@ -93,11 +99,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
                     }
                 }
                 seqs[tid] = s;
-                const int x = block_scan(n, warp_sum);
+                const int x = block_scan(n, left, warp_sum);
                 prefix[tid + 1] = x;
                 if (tid == 0) prefix[0] = 0;
                 __syncthreads();
             }
+            left -= prefix[kPlanThreads];
             const int total = prefix[kPlanThreads], seqs_here = min(kPlanThreads, a.B - b0);
             for (int i0 = 0; i0 < total; i0 += kPlanThreads) {
                 const int i = i0 + tid;
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
         if (valid) units_of(it.tiles, [&](int, int, int t0, int t1) { atomicAdd(&bucket[bucket_of(t1 - t0)], 1); });
     });
     __syncthreads();
-    const int x = block_scan(bucket[tid], warp_sum);
+    const int x = block_scan(bucket[tid], 0x7FFFFFFF, warp_sum);
     if (tid == kPlanThreads - 1) {
         a.head->n_units = min(x, a.max_units);
         a.head->next = 0;

@@ -544,11 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.p_full[x][part]));
                 };
-                // Once every row of the warp has a reference, the weights are made with it at once and the tile's
-                // own maximum is found beside them; a row that outgrew its reference by 2^8 sends the warp back.
-                constexpr bool early = false;
                 float mx[4];
-                uint64_t nn = pack2(-m, -m);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float y0 = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1])), y1 = fmaxf(__uint_as_float(s[i][2]), __uint_as_float(s[i][3]));
@@ -558,7 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         y1 = max3(y1, __uint_as_float(s[i][e + 2]), __uint_as_float(s[i][e + 3]));
                     }
                     mx[i] = fmaxf(y0, y1);
-                    if (early && i < 3) weights(i, nn);
                 }
                 const float mt = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c2;
                 const bool need = mt > m + 8.0f;
@@ -581,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = m_new;
                 }
                 const float neg = m == -INFINITY ? 0.0f : -m;  // no key yet: every weight is 2^-inf = 0
-                nn = pack2(neg, neg);
+                const uint64_t nn = pack2(neg, neg);
                 weights(0, nn);
                 weights(1, nn);
                 weights(2, nn);

@@ -3,15 +3,15 @@
 //   angle_i = p f_i,   y_a = s (x_a cos - x_b sin),   y_b = s (x_a sin + x_b cos)
 //
 // with (a, b) = (2i, 2i + 1) (interleaved) or (i, i + rot / 2) (half). The transpose turns the other
-// way: it is the backward pass (the Jacobian s R is linear in x). The angle is formed in fp64 as turns,
-// p * (f / 2 pi), whose fraction is exact to 4e-11 at a million positions; fp32 would keep no more
-// than two digits of it there. Sine and cosine are taken of the fraction in fp32.
+// way: it is the backward pass (the Jacobian s R is linear in x). The angle is formed as turns, p * (f / 2 pi),
+// in 64-bit fixed point, whose fraction is exact to 2^-33 turns at any position; fp32 would keep no more than
+// two digits of it at a million positions. Sine and cosine are taken of the fraction in fp32.
 //
 // Bound by memory: the rotated columns are read and written once. One CTA per token, so that its table of
 // rot / 2 cosines and sines is formed once for all heads of up to four tensors (one fp64 product and one
 // sincospi each); every thread asks for up to four pieces of 16 bytes (half layout: pairs of pieces)
-// before it waits for the table. 8192 tokens of 128 + 64 heads with 64 bf16 columns: 75 us, 79% of the measured copy bandwidth.
-// Views that are not aligned to 16 bytes go pair by pair.
+// before it waits for the table. 8192 tokens of 128 + 64 heads with 64 bf16 columns: 74 us, 80% of the measured
+// copy bandwidth. Views that are not aligned to 16 bytes go pair by pair.
 #include "internal.h"
 
 namespace dsa {

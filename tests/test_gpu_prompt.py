@@ -291,3 +291,26 @@ def test_a_prompt_step_around_the_decode_step():
     # two orders of the same fp32 products, of order 1, through at most d + r + dv roundings each
     assert float((o - out).abs().max()) <= 2 * (d + r + dv) * 2.0 ** -24 * 32
     assert float((e - lse).abs().max()) <= 2 * (d + r + dv) * 2.0 ** -24 * 32
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_overlapping_sequences_fit_the_lists(dtype):
+    """Entries that descend every other time leave 300 sequences over the same rows, with far more row tiles
+    than the lists were made for: reported, the rows either right or left as they were, and the workspace
+    good for the next call."""
+    n, m, B = 3000, 70, 600
+    q, k, v = make(dtype, [n], [m], 4, 1, 64, 64)
+    dims = dsa.prompt_dims(q, k, v, B, False)
+    ws = dsa.prompt_workspace(dims, n)
+    cu_q = torch.tensor([0, n], dtype=torch.int32, device="cuda").repeat(B // 2 + 1)[: B + 1].contiguous()
+    cu_k = torch.tensor([0, m], dtype=torch.int32, device="cuda").repeat(B // 2 + 1)[: B + 1].contiguous()
+    out = torch.full((n, 4, 64), 9.0, dtype=dtype, device="cuda")
+    got, _ = dsa.prompt_attn(dims, q, k, v, cu_q, cu_k, 0.125, ws=ws, out=out)
+    assert dsa.read_error(ws) == 2
+    want, _ = attend(q, k, v, [n], [m], 0.125, causal=False)
+    left = (got == 9.0).all(-1)
+    assert torch.equal(got[~left], want[~left]) and not left.all()
+    nq, nk = [n] + [0] * (B - 1), [m] + [0] * (B - 1)
+    got = dsa.prompt_attn(dims, q, k, v, starts(nq), starts(nk), 0.125, ws=ws)
+    assert dsa.read_error(ws) == 0
+    check(got, q, k, v, nq, nk, 0.125, causal=False)
