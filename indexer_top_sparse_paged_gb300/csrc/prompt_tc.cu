@@ -9,8 +9,9 @@
 // cores, the tensor pipe works for the other: P_A V, Q_A K, P_B V, Q_B K, ... in that order, where Q_X K
 // of the next keys may follow P_X V of the last at once, since the pipe runs in order.
 //
-// Units of at most 32 rows (single tokens) would leave tile B without work and every step waiting for the
-// last: there both tiles hold the same rows and take every other key tile, and one warp joins the two.
+// Units of at most 128 rows (single tokens, the end of a prompt) would leave tile B without work and every step
+// waiting for the last: there both tiles hold the same rows and take every other key tile, and tile A's warps
+// join the two.
 //
 // Softmax: one thread per row, the running maximum m and sum l in fp32; O is rescaled only when a row's
 // maximum has grown by more than 2^8 since the last time (weights then stay below 2^8, and O and l hold
@@ -56,8 +57,6 @@ struct Work {
     int pad[2];
 };
 
-constexpr int kApartRows = 32;       // one warp's rows, so that it can join both tiles' outputs from tensor memory
-
 constexpr int kQueue = 2;            // units handed out and not yet taken up by every role
 constexpr int kTakers = 11;          // 8 softmax warps, 2 MMA warps, the key loader
 
@@ -67,8 +66,8 @@ struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: the first 96 keys' weights, the rest
     uint64_t turn[2];  // the tensor pipe's next turn belongs to tile A, B
-    uint64_t join_full, join_free;  // tile B's part of a unit apart: ready, read
-    float2 join_ml[kApartRows];
+    uint64_t join_full[4], join_free[4];  // tile B's part of a unit apart, by warp: ready, read
+    float2 join_ml[kRows];
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
@@ -137,7 +136,7 @@ __device__ __forceinline__ Work get_work(const PromptArgs& a, int n_units, int g
     };
     x.n0 = tiles(u.row0);
     x.n1 = tiles(u.row0 + kRows);
-    x.apart = x.nrows - u.row0 <= kApartRows && x.n0 - u.kt0 >= 2;
+    x.apart = x.nrows - u.row0 <= kRows && x.n0 - u.kt0 >= 2;
     if (x.apart) x.n1 = x.n0;
     x.q0 = u.q0, x.lq = u.lq, x.k0 = u.k0, x.lk = u.lk, x.row0 = u.row0, x.kt0 = u.kt0;
     x.slot = u.slot, x.part = u.part, x.parts = u.parts;
@@ -175,8 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.work_full[i]), 1);
             mbar_init(smem_u32(&S.work_free[i]), kTakers);
         }
-        mbar_init(smem_u32(&S.join_full), 32);
-        mbar_init(smem_u32(&S.join_free), 32);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&S.join_full[i]), 32);
+            mbar_init(smem_u32(&S.join_free[i]), 32);
+        }
         mbar_init(smem_u32(&S.mma_done), 2);
         S.abort_flag = 0;
         fence_mbar_init();
@@ -592,25 +593,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (dead) break;
             tc_fence_after();
-            if (idle) continue;  // (a unit apart: all rows belong to the first warp of each tile)
+            if (idle) continue;  // (of a unit apart: in both tiles)
             if (k.apart) {
                 if (x == 1) {  // tile B's maximum and sum to A's warp, which finds O in tensor memory
-                    S.join_ml[lane] = make_float2(m, l);
+                    S.join_ml[r] = make_float2(m, l);
                     tc_fence_before();
-                    mbar_arrive(smem_u32(&S.join_full));
-                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_free), jphase, abort_flag, a.err));
+                    mbar_arrive(smem_u32(&S.join_full[warp & 3]));
+                    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_free[warp & 3]), jphase, abort_flag, a.err));
                     jphase ^= 1;
                     if (dead) break;
                     continue;
                 }
-                dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_full), jphase, abort_flag, a.err));
+                dead = !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.join_full[warp & 3]), jphase, abort_flag, a.err));
                 jphase ^= 1;
                 if (dead) break;
                 tc_fence_after();
             }
             float fa = 1.0f, fb = 0.0f;  // out = fa O_A + fb O_B
             if (k.apart) {
-                const float2 o = S.join_ml[lane];
+                const float2 o = S.join_ml[r];
                 const float top = fmaxf(m, o.x);
                 fa = m == -INFINITY ? 0.0f : exp2f(m - top);
                 fb = o.x == -INFINITY ? 0.0f : exp2f(o.x - top);
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();  // O has been read before the next unit's first product may overwrite it
-            if (k.apart) mbar_arrive(smem_u32(&S.join_free));
+            if (k.apart) mbar_arrive(smem_u32(&S.join_free[warp & 3]));
         }
     }
     tc_fence_before();
