@@ -181,6 +181,7 @@ struct alignas(16) PromptJoin {
 struct PromptHead {  // written by the plan
     int n_units;
     int n_joins;
+    int join_rows;  // most rows of a join
     int head_group;  // key heads whose units run next to each other
     int next;        // units drawn, beyond every CTA's first
 };

@@ -92,58 +92,49 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[8]
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kJoinAhead = 8;
-
-// Joins the `rows` rows of the partials slot0 .. slot0 + parts - 1 (rows row0 .. of the sequence) in that order and writes them out: sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p. n threads
-// (a power of two, at least the rows) share the work; a thread keeps one row and a run of columns, 8 at a
-// time, with the loads of eight parts in flight.
-template <typename T>
-__device__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int rows, int q0, int row0, int hk, int tid, int n) {
-    int width = 1;  // threads side by side on the rows
-    while (width < rows) width *= 2;
-    const int groups = n / width, r = tid % width, G = a.H / a.H_kv;
-    if (r >= rows) return;
-    const int per = ((a.d_v + groups - 1) / groups + 7) / 8 * 8, c0 = tid / width * per, c1 = min(a.d_v, c0 + per);
-    const int t = (row0 + r) / G;
+// Joins row r (row0 + r of the sequence) of the partials slot0 .. slot0 + parts - 1 in that order and writes its
+// columns c .. c + 7 out: sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, the loads of kAhead parts in flight (past the last
+// it is loaded again: without a branch between them the loads go out together).
+template <int kAhead, typename T>
+__device__ __forceinline__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int q0, int row0, int hk, int r, int c) {
+    const int G = a.H / a.H_kv, t = (row0 + r) / G;
     const int64_t at = (static_cast<int64_t>(q0) + t) * a.H + hk * G + (row0 + r - t * G);  // (token, head)
     const float2* ml = a.part_ml + slot0 * a.slot_rows + r;
     T* out = static_cast<T*>(a.out) + at * a.d_v;
-    for (int c = c0; c < c1; c += 8) {
-        const int m = min(8, c1 - c);  // 8, or 4 (fp32 rows of an odd number of pieces)
-        float M = -INFINITY, l = 0.0f, o[8] = {};
-        for (int p0 = 0; p0 < parts; p0 += kJoinAhead) {
-            float2 v[kJoinAhead];
-            float y[kJoinAhead][8];
+    const int m = min(8, a.d_v - c);  // 8, or 4 (fp32 rows of an odd number of pieces)
+    float M = -INFINITY, l = 0.0f, o[8] = {};
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+        float2 v[kAhead];
+        float y[kAhead][8];
 #pragma unroll
-            for (int i = 0; i < kJoinAhead; ++i) {  // every load of these parts before the first is used
-                const int p = min(p0 + i, parts - 1);
-                v[i] = __ldcg(ml + static_cast<int64_t>(p) * a.slot_rows);
-                const float* po = a.part_o + part_at(a, slot0 + p, c, r);
+        for (int i = 0; i < kAhead; ++i) {  // every load of these parts before the first is used
+            const int p = min(p0 + i, parts - 1);
+            v[i] = __ldcg(ml + static_cast<int64_t>(p) * a.slot_rows);
+            const float* po = a.part_o + part_at(a, slot0 + p, c, r);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[i][e] = e < m ? __ldcg(po + static_cast<int64_t>(e) * a.slot_rows) : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < kJoinAhead; ++i) {
-                if (p0 + i >= parts || v[i].x == -INFINITY) continue;  // a part without keys wrote no columns
-                const float top = fmaxf(M, v[i].x), f = exp2f(v[i].x - top), keep = exp2f(M - top);
-                l = l * keep + f * v[i].y;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = o[e] * keep + f * y[i][e];
-                M = top;
-            }
+            for (int e = 0; e < 8; ++e) y[i][e] = e < m ? __ldcg(po + static_cast<int64_t>(e) * a.slot_rows) : 0.0f;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= inv;
-        if (m == 8) {
-            store_cols(out + c, o);
-        } else {
+        for (int i = 0; i < kAhead; ++i) {
+            if (p0 + i >= parts || v[i].x == -INFINITY) continue;  // a part without keys wrote no columns
+            const float top = fmaxf(M, v[i].x), f = exp2f(v[i].x - top), keep = exp2f(M - top);
+            l = l * keep + f * v[i].y;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < m) out[c + e] = static_cast<T>(o[e]);
+            for (int e = 0; e < 8; ++e) o[e] = o[e] * keep + f * y[i][e];
+            M = top;
         }
-        if (c == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    if (m == 8) {
+        store_cols(out + c, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < m) out[c + e] = static_cast<T>(o[e]);
+    }
+    if (c == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace dsa

@@ -64,12 +64,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int bucket[kBuckets];
     __shared__ unsigned long long total_tiles;
-    __shared__ int most_tiles, most_keys, slots, joins;
+    __shared__ int most_tiles, most_keys, slots, joins, join_rows;
     const int tid = threadIdx.x, G = a.H / a.H_kv;
     griddep_launch_dependents();  // the attention's prologue may start (it waits for this grid)
     if (tid == 0) {
         total_tiles = 0;
-        most_tiles = most_keys = slots = joins = 0;
+        most_tiles = most_keys = slots = joins = join_rows = 0;
     }
     for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
     __syncthreads();
@@ -174,8 +174,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
             if (p == 0 && parts > 1) {
                 slot = atomicAdd(&slots, parts);
                 const int j = atomicAdd(&joins, 1);
+                const int rows = min(a.tile_rows, it.lq * G - it.row0);
+                atomicMax(&join_rows, rows);
                 if (slot + parts <= a.max_slots && j < a.max_slots / 2)
-                    a.joins[j] = PromptJoin{it.q0, it.row0, min(a.tile_rows, it.lq * G - it.row0), slot, parts, {0, 0, 0}};
+                    a.joins[j] = PromptJoin{it.q0, it.row0, rows, slot, parts, {0, 0, 0}};
             }
             const int at = atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
             if (at < a.max_units && slot + (parts > 1 ? parts : 0) <= a.max_slots)
@@ -183,7 +185,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
         });
     });
     __syncthreads();
-    if (tid == 0) a.head->n_joins = min(joins, a.max_slots / 2);
+    if (tid == 0) {
+        a.head->n_joins = min(joins, a.max_slots / 2);
+        a.head->join_rows = join_rows;
+    }
 }
 static_assert(kBuckets == kPlanThreads, "the bucket scan takes one bucket per thread");
 
@@ -193,23 +198,34 @@ bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
     return true;
 }
 
-// Joins the rows whose keys were split, one CTA per item and key head. In the attention kernel itself, by the
-// last part to arrive, it held up the units behind it (16 single tokens over up to 16K keys: 195 us there).
+// Joins the rows whose keys were split: a run of CTAs shares the columns of an item and key head, 8 to a thread
+// (a prompt of 1024 tokens, 32 / 8 heads: with one CTA for all columns the call took 60 us, with this 31). In the
+// attention kernel itself, by the last part to arrive, it held up the units behind it (16 single tokens over up
+// to 16K keys: 195 us, 126 so).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 2;  // per SM
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
     griddep_wait();
-    const int n = __ldcg(&a.head->n_joins);
-    const PromptJoin j = a.joins[blockIdx.x];  // (within the list's room, whatever it holds)
-    if (static_cast<int>(blockIdx.x) >= n) return;
-    const int64_t slot0 = static_cast<int64_t>(j.slot) * a.H_kv + static_cast<int64_t>(blockIdx.y) * j.parts;
-    prompt_join<T>(a, slot0, j.parts, j.rows, j.q0, j.row0, blockIdx.y, threadIdx.x, kJoinThreads);
+    const int n = __ldcg(&a.head->n_joins), most = __ldcg(&a.head->join_rows);
+    int width = 1;  // threads side by side on the rows
+    while (width < most) width *= 2;
+    const int per = kJoinThreads / width, runs = ((a.d_v + 7) / 8 + per - 1) / per;  // columns of a CTA / 8, CTAs
+    for (int w = blockIdx.x; w < n * a.H_kv * runs; w += gridDim.x) {  // the runs of an item and head side by side
+        const int i = w / runs, hk = i % a.H_kv;
+        const PromptJoin j = a.joins[i / a.H_kv];
+        const int64_t slot0 = static_cast<int64_t>(j.slot) * a.H_kv + static_cast<int64_t>(hk) * j.parts;
+        const int c = ((w - i * runs) * per + threadIdx.x / width) * 8, r = threadIdx.x % width;
+        if (r >= j.rows || c >= a.d_v) continue;
+        if (j.parts <= 4) prompt_join<4, T>(a, slot0, j.parts, j.q0, j.row0, hk, r, c);  // (8: 34 us, not 31, there)
+        else prompt_join<8, T>(a, slot0, j.parts, j.q0, j.row0, hk, r, c);  // (4: 129 us, not 126, for the single tokens)
+    }
 }
 
 bool launch_prompt_join(const PromptArgs& a, cudaStream_t s, int* launches) {
     if (a.max_slots < 2) return true;  // no room to split: the plan does not
-    const dim3 grid(a.max_slots / 2, a.H_kv);
+    const dim3 grid(kJoinCtas * a.ctas);
     const bool ok = a.type == DSA_F32
                         ? launch_kernel(true, prompt_join_kernel<float>, grid, dim3(kJoinThreads), 0, s, a)
                         : launch_kernel(true, prompt_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a);
