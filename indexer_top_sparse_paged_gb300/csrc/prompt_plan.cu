@@ -203,7 +203,6 @@ bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
 // attention kernel itself, by the last part to arrive, it held up the units behind it (16 single tokens over up
 // to 16K keys: 195 us, 126 so).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCtas = 2;  // per SM
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
 
 bool launch_prompt_join(const PromptArgs& a, cudaStream_t s, int* launches) {
     if (a.max_slots < 2) return true;  // no room to split: the plan does not
-    const dim3 grid(kJoinCtas * a.ctas);
+    const dim3 grid(a.ctas);  // (twice as many cost calls that split nothing 1 us)
     const bool ok = a.type == DSA_F32
                         ? launch_kernel(true, prompt_join_kernel<float>, grid, dim3(kJoinThreads), 0, s, a)
                         : launch_kernel(true, prompt_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a);

@@ -9,7 +9,7 @@
 // logits and 4 rows x d_v / 16 columns of the output; multiply-adds are issued in pairs (fma.rn.f32x2). Bound by
 // what shared memory returns to the registers (16 bytes a lane take four cycles, however many lanes share
 // them): 8 (12) loads feed 64 (128) multiply-adds. 21 TFLOP/s at 4096 tokens, 8 heads of 128 (1.6 ms). Tiles of
-// 4 x 8 a thread, with half the warps, were slower (213 us against 130 for five prompts of up to 600 tokens).
+// 4 x 8 a thread, with half the warps, were slower (213 us, then 130, for five prompts of up to 600 tokens).
 #include "prompt.cuh"
 
 namespace dsa {
@@ -71,157 +71,159 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(PromptArgs a) 
     float* sv = sk + max(kKeys * pq, kRows * kPitchP);
     griddep_launch_dependents();
     griddep_wait();
-    PromptUnit u;
-    if (a.self_plan) {
-        if (!prompt_self_unit(a, blockIdx.x, u)) return;  // (every warp for itself)
-    } else {
-        if (static_cast<int>(blockIdx.x) >= a.head->n_units) return;
-        u = a.units[blockIdx.x];
-    }
-    const int hk = blockIdx.y, G = a.H / a.H_kv;
-    const int q0 = u.q0, lq = u.lq, k0 = u.k0, lk = u.lk, nrows = lq * G, row0 = u.row0;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;  // the thread's rows: kR * ty ..
-    // queries, and for each of the thread's rows the number of keys it sees
-    {
-        const int lane = tid & 31;
-        for (int r = tid >> 5; r < kRows; r += kThreads / 32) {
-            const bool in = row0 + r < nrows;
-            const int t = in ? (row0 + r) / G : 0, g = in ? row0 + r - t * G : 0;
-            const T* src = static_cast<const T*>(a.q) + (q0 + t) * a.q_stride_t + (hk * G + g) * a.q_stride_h;
-            for (int e = 4 * lane; e < a.d_qk; e += 128)
-                store4(sq + r * pq + e, in ? load4(src + e) : make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int index = blockIdx.x;; index += gridDim.x) {
+        PromptUnit u;
+        if (a.self_plan) {
+            if (!prompt_self_unit(a, index, u)) return;  // (every warp for itself)
+        } else {
+            if (index >= a.head->n_units) return;
+            u = a.units[index];
         }
-    }
-    int seen[kR];
-#pragma unroll
-    for (int i = 0; i < kR; ++i) {
-        const int r = row0 + kR * ty + i;
-        seen[i] = r < nrows ? prompt_keys_seen(a, r / G, lq, lk) : 0;
-    }
-    // this part's keys, up to the last that the tile's last row sees
-    const int n_keys = min(prompt_keys_seen(a, (min(nrows, row0 + kRows) - 1) / G, lq, lk), u.kt1 * kPromptKeys);
-    const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
-    float m[kR], l[kR];
-    uint64_t o[kR][kCols][2];  // pairs of columns
-#pragma unroll
-    for (int i = 0; i < kR; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) o[i][j][0] = o[i][j][1] = 0;
-    }
-    for (int s0 = u.kt0 * kPromptKeys; s0 < n_keys; s0 += kKeys) {
-        const int64_t at = static_cast<int64_t>(k0) + s0;
-        load_rows(sk, pq, static_cast<const T*>(a.k) + at * a.k_stride_t + hk * a.k_stride_h, a.k_stride_t, a.d_qk, lk - s0);
-        load_rows(sv, pv, static_cast<const T*>(a.v) + at * a.v_stride_t + hk * a.v_stride_h, a.v_stride_t, a.d_v, lk - s0);
-        cp_async_commit();
-        cp_async_wait<0>();
-        __syncthreads();
-        uint64_t zz[kR][kJ];  // sums over the even and the odd columns
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) zz[i][j] = 0;
-#pragma unroll 2
-        for (int e = 0; e < a.d_qk; e += 4) {
-            ulonglong2 kv[kJ];
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * pq + e);
-#pragma unroll
-            for (int i = 0; i < kR; ++i) {
-                const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(sq + (kR * ty + i) * pq + e);
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) zz[i][j] = fma2(qv.y, kv[j].y, fma2(qv.x, kv[j].x, zz[i][j]));
+        const int hk = blockIdx.y, G = a.H / a.H_kv;
+        const int q0 = u.q0, lq = u.lq, k0 = u.k0, lk = u.lk, nrows = lq * G, row0 = u.row0;
+        const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;  // the thread's rows: kR * ty ..
+        // queries, and for each of the thread's rows the number of keys it sees
+        {
+            const int lane = tid & 31;
+            for (int r = tid >> 5; r < kRows; r += kThreads / 32) {
+                const bool in = row0 + r < nrows;
+                const int t = in ? (row0 + r) / G : 0, g = in ? row0 + r - t * G : 0;
+                const T* src = static_cast<const T*>(a.q) + (q0 + t) * a.q_stride_t + (hk * G + g) * a.q_stride_h;
+                for (int e = 4 * lane; e < a.d_qk; e += 128)
+                    store4(sq + r * pq + e, in ? load4(src + e) : make_float4(0.f, 0.f, 0.f, 0.f));
             }
         }
-        __syncthreads();  // every warp has read the keys
+        int seen[kR];
 #pragma unroll
         for (int i = 0; i < kR; ++i) {
-            float z[kJ], mt = -INFINITY;
+            const int r = row0 + kR * ty + i;
+            seen[i] = r < nrows ? prompt_keys_seen(a, r / G, lq, lk) : 0;
+        }
+        // this part's keys, up to the last that the tile's last row sees
+        const int n_keys = min(prompt_keys_seen(a, (min(nrows, row0 + kRows) - 1) / G, lq, lk), u.kt1 * kPromptKeys);
+        const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
+        float m[kR], l[kR];
+        uint64_t o[kR][kCols][2];  // pairs of columns
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                const float2 h = unpack2(zz[i][j]);
-                z[j] = s0 + tx + 16 * j < seen[i] ? (h.x + h.y) * c2 : -INFINITY;
-                mt = fmaxf(mt, z[j]);
-            }
+        for (int i = 0; i < kR; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
 #pragma unroll
-            for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, w));
-            const float m_new = fmaxf(m[i], mt);
-            const float ref = m_new == -INFINITY ? 0.0f : m_new;  // no key yet: every weight is 0
-            const float alpha = exp2f(m[i] - ref);
-            float sum = 0.0f;
+            for (int j = 0; j < kCols; ++j) o[i][j][0] = o[i][j][1] = 0;
+        }
+        for (int s0 = u.kt0 * kPromptKeys; s0 < n_keys; s0 += kKeys) {
+            const int64_t at = static_cast<int64_t>(k0) + s0;
+            load_rows(sk, pq, static_cast<const T*>(a.k) + at * a.k_stride_t + hk * a.k_stride_h, a.k_stride_t, a.d_qk, lk - s0);
+            load_rows(sv, pv, static_cast<const T*>(a.v) + at * a.v_stride_t + hk * a.v_stride_h, a.v_stride_t, a.d_v, lk - s0);
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+            uint64_t zz[kR][kJ];  // sums over the even and the odd columns
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                const float w = exp2f(z[j] - ref);
-                sum += w;
-                sp[(kR * ty + i) * kPitchP + tx + 16 * j] = w;
-            }
-            l[i] = l[i] * alpha + sum;  // this thread's keys; joined at the end
-            m[i] = m_new;
-            if (alpha != 1.0f) {
-                const uint64_t aa = pack2(alpha, alpha);
+            for (int i = 0; i < kR; ++i)
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    o[i][j][0] = fma2(o[i][j][0], aa, 0);
-                    o[i][j][1] = fma2(o[i][j][1], aa, 0);
+                for (int j = 0; j < kJ; ++j) zz[i][j] = 0;
+#pragma unroll 2
+            for (int e = 0; e < a.d_qk; e += 4) {
+                ulonglong2 kv[kJ];
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * pq + e);
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(sq + (kR * ty + i) * pq + e);
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) zz[i][j] = fma2(qv.y, kv[j].y, fma2(qv.x, kv[j].x, zz[i][j]));
                 }
             }
+            __syncthreads();  // every warp has read the keys
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                float z[kJ], mt = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const float2 h = unpack2(zz[i][j]);
+                    z[j] = s0 + tx + 16 * j < seen[i] ? (h.x + h.y) * c2 : -INFINITY;
+                    mt = fmaxf(mt, z[j]);
+                }
+#pragma unroll
+                for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, w));
+                const float m_new = fmaxf(m[i], mt);
+                const float ref = m_new == -INFINITY ? 0.0f : m_new;  // no key yet: every weight is 0
+                const float alpha = exp2f(m[i] - ref);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const float w = exp2f(z[j] - ref);
+                    sum += w;
+                    sp[(kR * ty + i) * kPitchP + tx + 16 * j] = w;
+                }
+                l[i] = l[i] * alpha + sum;  // this thread's keys; joined at the end
+                m[i] = m_new;
+                if (alpha != 1.0f) {
+                    const uint64_t aa = pack2(alpha, alpha);
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        o[i][j][0] = fma2(o[i][j][0], aa, 0);
+                        o[i][j][1] = fma2(o[i][j][1], aa, 0);
+                    }
+                }
+            }
+            __syncwarp();  // a row's 16 threads are in one warp
+            for (int r = 0; r < kKeys; r += 4) {
+                float4 p[kR];
+#pragma unroll
+                for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (kR * ty + i) * kPitchP + r);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        const int e = 4 * tx + 64 * j;
+                        if (e >= a.d_v) continue;
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sv + (r + q) * pv + e);
+#pragma unroll
+                        for (int i = 0; i < kR; ++i) {
+                            const float w = q == 0 ? p[i].x : q == 1 ? p[i].y : q == 2 ? p[i].z : p[i].w;
+                            const uint64_t ww = pack2(w, w);
+                            o[i][j][0] = fma2(ww, v.x, o[i][j][0]);
+                            o[i][j][1] = fma2(ww, v.y, o[i][j][1]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();  // the tiles may be filled again
         }
-        __syncwarp();  // a row's 16 threads are in one warp
-        for (int r = 0; r < kKeys; r += 4) {
-            float4 p[kR];
+        const int64_t slot0 = (static_cast<int64_t>(u.slot) * a.H_kv + static_cast<int64_t>(hk) * u.parts);
 #pragma unroll
-            for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (kR * ty + i) * kPitchP + r);
+        for (int i = 0; i < kR; ++i) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], w);
+            const int r = kR * ty + i;
+            if (row0 + r >= nrows) continue;
+            if (u.parts > 1) {
+                if (tx == 0) a.part_ml[(slot0 + u.part) * a.slot_rows + r] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
                     const int e = 4 * tx + 64 * j;
                     if (e >= a.d_v) continue;
-                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sv + (r + q) * pv + e);
-#pragma unroll
-                    for (int i = 0; i < kR; ++i) {
-                        const float w = q == 0 ? p[i].x : q == 1 ? p[i].y : q == 2 ? p[i].z : p[i].w;
-                        const uint64_t ww = pack2(w, w);
-                        o[i][j][0] = fma2(ww, v.x, o[i][j][0]);
-                        o[i][j][1] = fma2(ww, v.y, o[i][j][1]);
-                    }
+                    const float2 lo = unpack2(o[i][j][0]), hi = unpack2(o[i][j][1]);
+                    a.part_o[part_at(a, slot0 + u.part, e, r)] = lo.x;
+                    a.part_o[part_at(a, slot0 + u.part, e + 1, r)] = lo.y;
+                    a.part_o[part_at(a, slot0 + u.part, e + 2, r)] = hi.x;
+                    a.part_o[part_at(a, slot0 + u.part, e + 3, r)] = hi.y;
                 }
+                continue;
             }
-        }
-        __syncthreads();  // the tiles may be filled again
-    }
-    const int64_t slot0 = (static_cast<int64_t>(u.slot) * a.H_kv + static_cast<int64_t>(hk) * u.parts);
-#pragma unroll
-    for (int i = 0; i < kR; ++i) {
-#pragma unroll
-        for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], w);
-        const int r = kR * ty + i;
-        if (row0 + r >= nrows) continue;
-        if (u.parts > 1) {
-            if (tx == 0) a.part_ml[(slot0 + u.part) * a.slot_rows + r] = make_float2(m[i], l[i]);
+            const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;  // (token, head)
+            const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) {
                 const int e = 4 * tx + 64 * j;
-                if (e >= a.d_v) continue;
                 const float2 lo = unpack2(o[i][j][0]), hi = unpack2(o[i][j][1]);
-                a.part_o[part_at(a, slot0 + u.part, e, r)] = lo.x;
-                a.part_o[part_at(a, slot0 + u.part, e + 1, r)] = lo.y;
-                a.part_o[part_at(a, slot0 + u.part, e + 2, r)] = hi.x;
-                a.part_o[part_at(a, slot0 + u.part, e + 3, r)] = hi.y;
+                if (e < a.d_v)
+                    store4(static_cast<T*>(a.out) + at * a.d_v + e, make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv));
             }
-            continue;
+            if (tx == 0 && a.lse) a.lse[at] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
         }
-        const int64_t at = (static_cast<int64_t>(q0) + (row0 + r) / G) * a.H + hk * G + (row0 + r) % G;  // (token, head)
-        const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-            const int e = 4 * tx + 64 * j;
-            const float2 lo = unpack2(o[i][j][0]), hi = unpack2(o[i][j][1]);
-            if (e < a.d_v)
-                store4(static_cast<T*>(a.out) + at * a.d_v + e, make_float4(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv));
-        }
-        if (tx == 0 && a.lse) a.lse[at] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
 }
 
@@ -229,7 +231,13 @@ template <typename T, int kCols>
 static bool launch_typed(const PromptArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d_qk, a.d_v);
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_simt_kernel<T, kCols>), smem)) return false;
-    return launch_kernel(!a.self_plan, prompt_simt_kernel<T, kCols>, dim3(a.max_units, a.H_kv), dim3(kThreads), smem, s, a);
+    // A CTA for every whole item, and for as many parts as the plan aims at; should there be more, a CTA takes
+    // several. (One for every part that there could be, most of them empty: 5 prompts of up to 600 tokens 119 us
+    // against 117.)
+    const int items = static_cast<int>(static_cast<int64_t>(a.Tq) * (a.H / a.H_kv) / a.tile_rows) + a.B;
+    const int parts = 2 * a.shares / a.H_kv, most = items > parts ? items : parts;
+    const int grid = most < a.max_units ? most : a.max_units;
+    return launch_kernel(!a.self_plan, prompt_simt_kernel<T, kCols>, dim3(grid, a.H_kv), dim3(kThreads), smem, s, a);
 }
 
 template <typename T>

@@ -26,7 +26,13 @@
 // MMAs of tile A and B (two issuers: the tensor pipe takes little work ahead, and one's waits and commits
 // would leave it idle), warp 10 loads keys and values, warp 11 hands out the units and loads queries. CTAs are
 // persistent and draw units from the plan's list by a counter; the next unit's queries and keys arrive,
-// and its first products run, while the last one's outputs are written.
+// and its first products run, while the last one's outputs are written. (Four more warps for the outputs leave
+// the softmax 192 registers instead of 208: 304 us, not 297, for 9 prompts with 128 heads.)
+//
+// 8192 tokens, 32 / 8 heads of 128 columns: 407 us, 1350 TFLOP/s of the causal products, 71% of the measured bf16
+// rate. Bound by the chain of each tile, logits -> weights -> product, two of which take turns: a pair of
+// tiles takes about 2900 cycles and its products 2048 of them. Short prompts pay the filling and draining of that
+// chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 296 us where the bytes take 119).
 #include "prompt.cuh"
 
 namespace dsa {
@@ -206,75 +212,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 11) {
-        // ------------------------------------------------------------------ units and their queries
-        const int G = a.H / a.H_kv;
-        int qphase0 = 1, qphase1 = 1, fphase = 1, slot = 0;
-        bool ok = true;
-        for (int w = blockIdx.x; ok;) {
-            const Work k = get_work(a, n_units, group, w);
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.work_free[slot]), fphase, abort_flag, a.err));
-            if (!ok) break;
-            if (lane == 0) {
-                S.work[slot] = k;
-                mbar_arrive(smem_u32(&S.work_full[slot]));
-                // (without a list there is a CTA for every unit)
-                if (k.hk >= 0) w = a.self_plan ? 0x7FFFFFFF : gridDim.x + atomicAdd(&a.head->next, 1);
-            }
-            if (++slot == kQueue) slot = 0, fphase ^= 1;
-            w = __shfl_sync(0xFFFFFFFFu, w, 0);
-            if (k.hk < 0) break;
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-                if ((x ? k.n1 : k.n0) == k.kt0) continue;  // no keys: the tile's queries are not used
-                const int row0 = k.row0 + (k.apart ? 0 : x * kRows);
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), x ? qphase1 : qphase0, abort_flag, a.err));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 11) {
+            // ------------------------------------------------------------------ units and their queries
+            const int G = a.H / a.H_kv;
+            int qphase0 = 1, qphase1 = 1, fphase = 1, slot = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; ok;) {
+                const Work k = get_work(a, n_units, group, w);
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.work_free[slot]), fphase, abort_flag, a.err));
                 if (!ok) break;
-                if (x) qphase1 ^= 1;
-                else qphase0 ^= 1;
-                const uint32_t dst = sQ + x * kQC * kChunk;
-                if (q_map) {  // 128 / G tokens of G heads; what lies behind the sequence is never used
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(smem_u32(&S.q_full[x]), kQC * kChunk);
-#pragma unroll
-                        for (int c = 0; c < kQC; ++c)
-                            tma_load_3d(dst + c * kChunk, &map_q, c * 64, k.hk * G, k.q0 + row0 / G, smem_u32(&S.q_full[x]));
-                    }
-                    continue;
+                if (lane == 0) {
+                    S.work[slot] = k;
+                    mbar_arrive(smem_u32(&S.work_full[slot]));
+                    // (without a list there is a CTA for every unit)
+                    if (k.hk >= 0) w = a.self_plan ? 0x7FFFFFFF : gridDim.x + atomicAdd(&a.head->next, 1);
                 }
-                // 16-byte pieces of 128 rows, kPieces to a row; rows and columns past the end are zeros
-                constexpr int kPieces = kQC * 8, kStep = 32 / kPieces;
-                const int piece = lane % kPieces;
-                if (lane < kStep * kPieces) {
-                    int r = lane / kPieces;
-                    int t = (row0 + r) / G, g = row0 + r - t * G;
-                    const uint32_t bytes = piece * 8 < a.d_qk ? 16 : 0;
-                    const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(k.q0) * a.q_stride_t +
-                                           static_cast<int64_t>(k.hk) * G * a.q_stride_h + (bytes ? piece * 8 : 0);
-#pragma unroll 4
-                    for (; r < kRows; r += kStep) {
-                        const bool in = row0 + r < k.nrows;
-                        cp_async16(dst + (piece / 8) * kChunk + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
-                                   in ? base + t * a.q_stride_t + g * a.q_stride_h : static_cast<const uint16_t*>(a.q), in ? bytes : 0);
-                        g += kStep;
-                        while (g >= G) {
-                            g -= G;
-                            ++t;
+                if (++slot == kQueue) slot = 0, fphase ^= 1;
+                w = __shfl_sync(0xFFFFFFFFu, w, 0);
+                if (k.hk < 0) break;
+    #pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    if ((x ? k.n1 : k.n0) == k.kt0) continue;  // no keys: the tile's queries are not used
+                    const int row0 = k.row0 + (k.apart ? 0 : x * kRows);
+                    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_free[x]), x ? qphase1 : qphase0, abort_flag, a.err));
+                    if (!ok) break;
+                    if (x) qphase1 ^= 1;
+                    else qphase0 ^= 1;
+                    const uint32_t dst = sQ + x * kQC * kChunk;
+                    if (q_map) {  // 128 / G tokens of G heads; what lies behind the sequence is never used
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(smem_u32(&S.q_full[x]), kQC * kChunk);
+    #pragma unroll
+                            for (int c = 0; c < kQC; ++c)
+                                tma_load_3d(dst + c * kChunk, &map_q, c * 64, k.hk * G, k.q0 + row0 / G,
+                                            smem_u32(&S.q_full[x]));
+                        }
+                        continue;
+                    }
+                    // 16-byte pieces of 128 rows, kPieces to a row; rows and columns past the end are zeros
+                    constexpr int kPieces = kQC * 8, kStep = 32 / kPieces;
+                    const int piece = lane % kPieces;
+                    if (lane < kStep * kPieces) {
+                        int r = lane / kPieces;
+                        int t = (row0 + r) / G, g = row0 + r - t * G;
+                        const uint32_t bytes = piece * 8 < a.d_qk ? 16 : 0;
+                        const uint16_t* base = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(k.q0) * a.q_stride_t +
+                                               static_cast<int64_t>(k.hk) * G * a.q_stride_h + (bytes ? piece * 8 : 0);
+    #pragma unroll 4
+                        for (; r < kRows; r += kStep) {
+                            const bool in = row0 + r < k.nrows;
+                            cp_async16(dst + (piece / 8) * kChunk + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                                       in ? base + t * a.q_stride_t + g * a.q_stride_h : static_cast<const uint16_t*>(a.q),
+                                       in ? bytes : 0);
+                            g += kStep;
+                            while (g >= G) {
+                                g -= G;
+                                ++t;
+                            }
                         }
                     }
+                    cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
                 }
-                cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
             }
-        }
-        // nothing may still be landing when the CTA exits
-        cp_async_wait<0>();
-        if (q_map && lane == 0) {  // each tile's last load has this phase
-            mbar_wait_drain(smem_u32(&S.q_full[0]), qphase0, a.err);
-            mbar_wait_drain(smem_u32(&S.q_full[1]), qphase1, a.err);
-        }
-    } else if (warp == 10) {
-        // --------------------------------------------------------------------------------- TMA
+            // nothing may still be landing when the CTA exits
+            cp_async_wait<0>();
+            if (q_map && lane == 0) {  // each tile's last load has this phase
+                mbar_wait_drain(smem_u32(&S.q_full[0]), qphase0, a.err);
+                mbar_wait_drain(smem_u32(&S.q_full[1]), qphase1, a.err);
+            }
+        } else if (warp == 10) {
+            // --------------------------------------------------------------------------------- TMA
             // a group (a key tile of kQC chunks or a value tile of kVC) fills the ring's next chunks
             // once the groups that held them are released, in order
             int slot = 0, in_use = 0;
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bar = smem_u32(&S.full[put.i]);
                 values = (values & ~(1u << put.i)) | (value ? 1u << put.i : 0u);
                 mbar_arrive_expect_tx(bar, n * kChunk);
-#pragma unroll
+    #pragma unroll
                 for (int c = 0; c < 3; ++c) {
                     if (c == n) break;
                     if (swap) tma_load_3d(sRing + slot * kChunk, map, c * 64, row, head, bar);
@@ -324,162 +332,162 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put.back();
                 mbar_wait_drain(smem_u32(&S.full[put.i]), put.phase, a.err);
             }
-    } else {
-        // --------------------------------------------------------------------------------- MMA
-        // With three key chunks the ring holds little more than what is in use: values go back before the product
-        // with the next keys, not after it, and those keys are waited for as late as that, inside the turn
-        // (8192 tokens, 192 / 128 columns: 478 us against 589 and 504; with 128 columns the same costs 440 against 410).
-        constexpr bool kTight = kQC == 3;
-        // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4); what the descriptors and
-        // the branches depend on is made uniform by hand where it comes from memory.
-        const int x = warp - 8;  // tile
-        int slot = 0;            // the ring's next chunk
-        Turn got, released;      // its group, the next group to give back
-        int qphase = 0, pphase = 0, tphase = 1 - x;  // the first turn is tile A's
-        bool ok = true;
-        auto next = [&](int s, int n) { return s + n < kStages ? s + n : s + n - kStages; };
-        auto wait = [&](const uint64_t* bar, int phase) {
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), phase, abort_flag, a.err));
-            tc_fence_after();
-        };
-        auto wait_group = [&] {
-            wait(&S.full[got.i], got.phase);
-            got.next();
-        };
-        auto release = [&] {  // once every MMA that this warp has issued is done
-            warp_tc_commit(smem_u32(&S.empty[released.i]));
-            released.next();
-        };
-        const uint32_t tS = tmem + kColS + x * 128, tO = tmem + kColO + x * 128;
-        const uint64_t dq = sw128_desc(sQ + x * kQC * kChunk, 16, 1024), dk = sw128_desc(sRing, 16, 1024);
-        const uint64_t dv = sw128_desc(sRing, kChunk, 1024);
-        // While both tiles have work they take turns, so that each tile's product with its weights and the
-        // next one with its keys run back to back: interleaved, both tiles' logits would be ready at the
-        // same time, and the pipe idle while both softmaxes work.
-        auto take_turn = [&](bool both) {
-            if (!both) return;
-            wait(&S.turn[x], tphase);
-            tphase ^= 1;
-        };
-        auto pass_turn = [&](bool both) {
-            if (both && lane == 0) mbar_arrive(smem_u32(&S.turn[x ^ 1]));
-            __syncwarp();
-        };
-        // S = Q K^T with the key chunks from ring slot s on; the turn goes over before the last of them
-        auto qk = [&](int s, bool both) {
-#pragma unroll
-            for (int c = 0; c < kQC; ++c) {
-                if (c == kQC - 1) pass_turn(both);
-                warp_mma_ss_x4(tS, dq + static_cast<uint64_t>((c * kChunk) >> 4),
-                               dk + static_cast<uint64_t>((next(s, c) * kChunk) >> 4), kIdescQK, c != 0 ? 1u : 0u);
-            }
-            warp_tc_commit(smem_u32(&S.s_full[x]));
-        };
-        // O += P V with the value chunks from slot s on, steps [from, from + most) of the `steps` groups of
-        // 16 keys that the sequence has there
-        auto pv = [&](int from, int most, int s, int steps, bool first) {
-            const int n = min(steps - from, most);
-            const uint32_t acc = first && from == 0 ? 0u : 1u;
-            const uint64_t vd = dv + static_cast<uint64_t>((s * kChunk + from * 2048) >> 4);
-            const bool wide = kVC == 2 && s + 1 < kStages;  // side by side in the ring: all columns in one product
-#pragma unroll
-            for (int c = 0; c < kVC; ++c) {
-                if (c > 0 && wide) break;
-                const uint64_t vc = wide ? vd : dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
-                const uint32_t o = tO + c * 64, idesc = wide ? kIdescPV2 : kIdescPV;
-                if (n == most) {  // (known where it is called: 8, 6 or 2)
-                    if (most > 2) warp_mma_ts_x4(o, tS + from * 8, vc, idesc, acc);
-                    if (most == 8) warp_mma_ts_x4(o, tS + 32, vc + 512, idesc, 1u);
-                    else warp_mma_ts_x2(o, tS + (from + most - 2) * 8, vc + (most - 2) * 128, idesc, most == 6 ? 1u : acc);
-                    continue;
+        } else {
+            // --------------------------------------------------------------------------------- MMA
+            // With three key chunks the ring holds little more than what is in use: values go back before the product
+            // with the next keys, not after it, and those keys are waited for as late as that, inside the turn
+            // (8192 tokens, 192 / 128 columns: 478 us against 589 and 504; with 128 columns the same costs 440 against 410).
+            constexpr bool kTight = kQC == 3;
+            // The whole warp runs along, one elected lane issues (see warp_mma_ss_x4); what the descriptors and
+            // the branches depend on is made uniform by hand where it comes from memory.
+            const int x = warp - 8;  // tile
+            int slot = 0;            // the ring's next chunk
+            Turn got, released;      // its group, the next group to give back
+            int qphase = 0, pphase = 0, tphase = 1 - x;  // the first turn is tile A's
+            bool ok = true;
+            auto next = [&](int s, int n) { return s + n < kStages ? s + n : s + n - kStages; };
+            auto wait = [&](const uint64_t* bar, int phase) {
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), phase, abort_flag, a.err));
+                tc_fence_after();
+            };
+            auto wait_group = [&] {
+                wait(&S.full[got.i], got.phase);
+                got.next();
+            };
+            auto release = [&] {  // once every MMA that this warp has issued is done
+                warp_tc_commit(smem_u32(&S.empty[released.i]));
+                released.next();
+            };
+            const uint32_t tS = tmem + kColS + x * 128, tO = tmem + kColO + x * 128;
+            const uint64_t dq = sw128_desc(sQ + x * kQC * kChunk, 16, 1024), dk = sw128_desc(sRing, 16, 1024);
+            const uint64_t dv = sw128_desc(sRing, kChunk, 1024);
+            // While both tiles have work they take turns, so that each tile's product with its weights and the
+            // next one with its keys run back to back: interleaved, both tiles' logits would be ready at the
+            // same time, and the pipe idle while both softmaxes work.
+            auto take_turn = [&](bool both) {
+                if (!both) return;
+                wait(&S.turn[x], tphase);
+                tphase ^= 1;
+            };
+            auto pass_turn = [&](bool both) {
+                if (both && lane == 0) mbar_arrive(smem_u32(&S.turn[x ^ 1]));
+                __syncwarp();
+            };
+            // S = Q K^T with the key chunks from ring slot s on; the turn goes over before the last of them
+            auto qk = [&](int s, bool both) {
+    #pragma unroll
+                for (int c = 0; c < kQC; ++c) {
+                    if (c == kQC - 1) pass_turn(both);
+                    warp_mma_ss_x4(tS, dq + static_cast<uint64_t>((c * kChunk) >> 4),
+                                   dk + static_cast<uint64_t>((next(s, c) * kChunk) >> 4), kIdescQK, c != 0 ? 1u : 0u);
                 }
-                int kk = 0;
-                for (; kk < n; ++kk) warp_mma_ts(o, tS + (from + kk) * 8, vc + kk * 128, idesc, kk ? 1u : acc);
-            }
-        };
-        for (Work k; ok && take(k);) {
-            const int k_begin = uniform(k.kt0), lk = uniform(k.lk), n0 = uniform(k.n0), n1 = uniform(k.n1);
-            const bool apart = uniform(k.apart) != 0;
-            const int n = x ? n1 : n0, end = max(n0, n1);
-            if (k_begin >= end) continue;
-            if (n > k_begin) {  // a tile without keys only walks the groups
-                wait(&S.q_full[x], qphase);
-                qphase ^= 1;
-                fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
-            }
-            // Key tile j is this warp's below n, or every other one where the tiles go apart; the groups of
-            // the others are walked past. Products with keys run `lead` tiles ahead of those with values.
-            const int lead = apart ? 2 : 1, first = k_begin + (apart ? x : 0);
-            const int both_end = apart ? k_begin : min(n0, n1);  // [k_begin, both_end): the tiles take turns
-            auto mine = [&](int j) { return j < n && (!apart || ((j - first) & 1) == 0); };
-            for (int j = k_begin; j < min(end, k_begin + lead); ++j) {
-                wait_group();
-                take_turn(j < both_end);
-                if (!ok) break;
-                if (mine(j)) {
-                    qk(slot, j < both_end);
-                    if (j + lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));  // the last product with these queries
-                }
-                slot = next(slot, kQC);
-                release();
-            }
-            for (int j = k_begin; ok && j < end; ++j) {
-                const int vs = slot, ks = next(slot, kVC);
-                const bool more = j + lead < end, both = j < both_end, own = mine(j), own_next = own && j + lead < n;
-                wait_group();
-                if (more && !kTight) wait_group();
-                if (!ok) break;
-                if (own) {
-                    const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
-                    const int steps = (valid + 15) / 16;
-                    if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
-                        for (int c = 0; c < kVC; ++c) {  // (both tiles' warps may write the same zeros)
-                            uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
-                            for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                warp_tc_commit(smem_u32(&S.s_full[x]));
+            };
+            // O += P V with the value chunks from slot s on, steps [from, from + most) of the `steps` groups of
+            // 16 keys that the sequence has there
+            auto pv = [&](int from, int most, int s, int steps, bool first) {
+                const int n = min(steps - from, most);
+                const uint32_t acc = first && from == 0 ? 0u : 1u;
+                const uint64_t vd = dv + static_cast<uint64_t>((s * kChunk + from * 2048) >> 4);
+                const bool wide = kVC == 2 && s + 1 < kStages;  // side by side in the ring: all columns in one product
+    #pragma unroll
+                for (int c = 0; c < kVC; ++c) {
+                    if (c > 0 && wide) break;
+                    const uint64_t vc = wide ? vd : dv + static_cast<uint64_t>((next(s, c) * kChunk + from * 2048) >> 4);
+                    const uint32_t o = tO + c * 64, idesc = wide ? kIdescPV2 : kIdescPV;
+                    if (n == most) {  // (known where it is called: 8, 6 or 2)
+                        if (most > 2) warp_mma_ts_x4(o, tS + from * 8, vc, idesc, acc);
+                        if (most == 8) warp_mma_ts_x4(o, tS + 32, vc + 512, idesc, 1u);
+                        else warp_mma_ts_x2(o, tS + (from + most - 2) * 8, vc + (most - 2) * 128, idesc, most == 6 ? 1u : acc);
+                        continue;
                     }
-                    wait(&S.p_full[x][0], pphase);
-                    take_turn(both);
+                    int kk = 0;
+                    for (; kk < n; ++kk) warp_mma_ts(o, tS + (from + kk) * 8, vc + kk * 128, idesc, kk ? 1u : acc);
+                }
+            };
+            for (Work k; ok && take(k);) {
+                const int k_begin = uniform(k.kt0), lk = uniform(k.lk), n0 = uniform(k.n0), n1 = uniform(k.n1);
+                const bool apart = uniform(k.apart) != 0;
+                const int n = x ? n1 : n0, end = max(n0, n1);
+                if (k_begin >= end) continue;
+                if (n > k_begin) {  // a tile without keys only walks the groups
+                    wait(&S.q_full[x], qphase);
+                    qphase ^= 1;
+                    fence_proxy_async_smem();  // queries written by cp.async -> visible to the tensor core
+                }
+                // Key tile j is this warp's below n, or every other one where the tiles go apart; the groups of
+                // the others are walked past. Products with keys run `lead` tiles ahead of those with values.
+                const int lead = apart ? 2 : 1, first = k_begin + (apart ? x : 0);
+                const int both_end = apart ? k_begin : min(n0, n1);  // [k_begin, both_end): the tiles take turns
+                auto mine = [&](int j) { return j < n && (!apart || ((j - first) & 1) == 0); };
+                for (int j = k_begin; j < min(end, k_begin + lead); ++j) {
+                    wait_group();
+                    take_turn(j < both_end);
                     if (!ok) break;
-                    // the last quarter's weights are mostly there by now; if not, the first three go ahead
-                    const bool whole = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[x][1]), pphase));
-                    if (whole) {
-                        tc_fence_after();
-                        pv(0, 8, vs, steps, j == first);
-                    } else {
-                        pv(0, 6, vs, steps, j == first);
-                        wait(&S.p_full[x][1], pphase);
-                        if (!ok) break;
-                        pv(6, 2, vs, steps, j == first);
-                    }
-                    pphase ^= 1;
-                    if (!own_next) {
-                        pass_turn(both);
-                        warp_tc_commit(smem_u32(&S.o_full[x]));
-                    }
-                }
-                if (kTight) release();
-                slot = ks;
-                if (more) {
-                    if (kTight) wait_group();
-                    if (!ok) break;
-                    if (own_next) {
-                        qk(ks, both);
-                        if (j + 2 * lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));
+                    if (mine(j)) {
+                        qk(slot, j < both_end);
+                        if (j + lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));  // the last product with these queries
                     }
                     slot = next(slot, kQC);
-                    if (!kTight) release();
-                    release();
-                } else if (!kTight) {
                     release();
                 }
+                for (int j = k_begin; ok && j < end; ++j) {
+                    const int vs = slot, ks = next(slot, kVC);
+                    const bool more = j + lead < end, both = j < both_end, own = mine(j), own_next = own && j + lead < n;
+                    wait_group();
+                    if (more && !kTight) wait_group();
+                    if (!ok) break;
+                    if (own) {
+                        const int valid = min(kKeys, lk - j * kKeys);  // value rows of this sequence
+                        const int steps = (valid + 15) / 16;
+                        if (valid & 15) {  // the rest of the last step belongs to another sequence, or to nobody
+                            for (int c = 0; c < kVC; ++c) {  // (both tiles' warps may write the same zeros)
+                                uint4* row = reinterpret_cast<uint4*>(smem + Lay::kOffRing + next(vs, c) * kChunk + valid * 128);
+                                for (int i = lane; i < (steps * 16 - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        wait(&S.p_full[x][0], pphase);
+                        take_turn(both);
+                        if (!ok) break;
+                        // the last quarter's weights are mostly there by now; if not, the first three go ahead
+                        const bool whole = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[x][1]), pphase));
+                        if (whole) {
+                            tc_fence_after();
+                            pv(0, 8, vs, steps, j == first);
+                        } else {
+                            pv(0, 6, vs, steps, j == first);
+                            wait(&S.p_full[x][1], pphase);
+                            if (!ok) break;
+                            pv(6, 2, vs, steps, j == first);
+                        }
+                        pphase ^= 1;
+                        if (!own_next) {
+                            pass_turn(both);
+                            warp_tc_commit(smem_u32(&S.o_full[x]));
+                        }
+                    }
+                    if (kTight) release();
+                    slot = ks;
+                    if (more) {
+                        if (kTight) wait_group();
+                        if (!ok) break;
+                        if (own_next) {
+                            qk(ks, both);
+                            if (j + 2 * lead >= n) warp_tc_commit(smem_u32(&S.q_free[x]));
+                        }
+                        slot = next(slot, kQC);
+                        if (!kTight) release();
+                        release();
+                    } else if (!kTight) {
+                        release();
+                    }
+                }
             }
+            warp_tc_commit(smem_u32(&S.mma_done));
+            mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
         }
-        warp_tc_commit(smem_u32(&S.mma_done));
-        mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // --------------------------------------------------------------------- softmax + epilogue
@@ -548,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float mx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float y0 = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1])), y1 = fmaxf(__uint_as_float(s[i][2]), __uint_as_float(s[i][3]));
+                    float y0 = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+                    float y1 = fmaxf(__uint_as_float(s[i][2]), __uint_as_float(s[i][3]));
 #pragma unroll
                     for (int e = 4; e < 32; e += 4) {
                         y0 = max3(y0, __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
@@ -654,8 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (live && c * 32 + e + 16 <= a.d_v && sectors) {
                             store_32b(out + c * 32 + e, o);
                         } else {
-                            if (live && c * 32 + e < a.d_v) *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(o[0], o[1], o[2], o[3]);
-                            if (live && c * 32 + e + 8 < a.d_v) *reinterpret_cast<uint4*>(out + c * 32 + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                            uint4* to = reinterpret_cast<uint4*>(out + c * 32 + e);
+                            if (live && c * 32 + e < a.d_v) to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (live && c * 32 + e + 8 < a.d_v) to[1] = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                 }
