@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -57,6 +58,9 @@ class Dims(ctypes.Structure):
 class RopeTensor(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32), ("layout", ctypes.c_int32)] + \
         [(n, ctypes.c_int64) for n in ("x_stride_t", "x_stride_h", "out_stride_t", "out_stride_h")]
+
+
+_ROPE_TENSOR = struct.Struct("@PPiiqqqq")  # the same bytes, made faster
 
 
 class RopeAppend(ctypes.Structure):
@@ -110,7 +114,7 @@ def lib():
         L.dsa_rope_frequencies.restype = ctypes.c_int
         L.dsa_rope_frequencies.argtypes = [I32, F64, I32, F64, F64, F64, F64, ctypes.POINTER(F64)]
         L.dsa_rope.restype = ctypes.c_int
-        L.dsa_rope.argtypes = [I32, ctypes.POINTER(RopeTensor), I32, I32, P, P, P, I32, F32, I32, P]
+        L.dsa_rope.argtypes = [I32, P, I32, I32, P, P, P, I32, F32, I32, P]
         L.dsa_cache_append_rope.restype = ctypes.c_int
         L.dsa_cache_append_rope.argtypes = [D, ctypes.POINTER(RopeAppend), P, P, P, P, P, P, P, I32, P, P, P, P, SZ, P]
         L.dsa_cache_read.restype = ctypes.c_int
@@ -400,7 +404,7 @@ def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, 
         _int32(seq_lens, T, "seq_lens")
     else:
         _int32(q_pos, T, "q_pos")
-    arr = (RopeTensor * n)()
+    arr = b""  # dsa_rope_tensor [n]
     for i in range(n):
         s, d = xs[i], outs[i]
         shape, st = s.shape, s.stride()
@@ -418,7 +422,7 @@ def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, 
                 raise ValueError("a head's rotated columns must be dense")
             if (T > 1 and so[0] == 0) or (H > 1 and so[1] == 0):
                 raise ValueError("out must not repeat rows (expanded views)")
-        arr[i] = (s.data_ptr(), d.data_ptr(), H, _layout(layouts[i]), st[0], st[1], so[0], so[1])
+        arr += _ROPE_TENSOR.pack(s.data_ptr(), d.data_ptr(), H, _layout(layouts[i]), st[0], st[1], so[0], so[1])
     st = lib().dsa_rope(_TYPES[dt], arr, n, rot, _at(freq), _at(seq_lens), _at(q_pos), T, scale, transpose,
                         _raw_stream(dev, stream))
     if st:
@@ -485,7 +489,7 @@ def prompt_dims(q, k, v, B: int, causal: bool = True) -> PromptDims:
     return PromptDims(*_prompt_fields(q, k, v, B, causal))
 
 
-_PROMPT_FIELDS = tuple(f for f, _ in PromptDims._fields_)
+_PROMPT_DIMS = struct.Struct("@7i4x6q")  # dsa_prompt_dims
 
 
 def _prompt_fields(q, k, v, B, causal):
@@ -514,7 +518,7 @@ def prompt_workspace(dims: PromptDims, Tq: int, device="cuda", stream=None) -> t
 def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, out=None, lse=None, stream=None):
     """(out[Tq][H][d_v], lse[Tq][H]) of dense attention over packed sequences: sequence b has the queries
     cu_q[b] .. cu_q[b + 1] - 1, the last of its positions, and the keys cu_k[b] .. cu_k[b + 1] - 1."""
-    if tuple(getattr(dims, f) for f in _PROMPT_FIELDS) != _prompt_fields(q, k, v, dims.B, dims.causal):
+    if bytes(dims) != _PROMPT_DIMS.pack(*_prompt_fields(q, k, v, dims.B, dims.causal)):
         raise ValueError("q, k and v differ from the tensors dims was made for")
     dev = _device(q, k, v, cu_q, cu_k, out, lse, ws)
     _int32(cu_q, dims.B + 1, "cu_q")
