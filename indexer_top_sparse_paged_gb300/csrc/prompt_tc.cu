@@ -25,14 +25,14 @@
 // Roles (384 threads): warps 0-3 softmax and epilogue of tile A, 4-7 of tile B, warps 8 and 9 issue the
 // MMAs of tile A and B (two issuers: the tensor pipe takes little work ahead, and one's waits and commits
 // would leave it idle), warp 10 loads keys and values, warp 11 hands out the units and loads queries. CTAs are
-// persistent and draw units from the plan's list by a counter; the next unit's queries and keys arrive,
+// persistent and draw units from the plan's list by a counter, late; the next unit's queries and keys arrive,
 // and its first products run, while the last one's outputs are written. (Four more warps for the outputs leave
 // the softmax 192 registers instead of 208: 304 us, not 297, for 9 prompts with 128 heads.)
 //
-// 8192 tokens, 32 / 8 heads of 128 columns: 407 us, 1350 TFLOP/s of the causal products, 71% of the measured bf16
+// 8192 tokens, 32 / 8 heads of 128 columns: 398 us, 1380 TFLOP/s of the causal products, 73% of the measured bf16
 // rate. Bound by the chain of each tile, logits -> weights -> product, two of which take turns: a pair of
 // tiles takes about 2900 cycles and its products 2048 of them. Short prompts pay the filling and draining of that
-// chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 296 us where the bytes take 119).
+// chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 294 us where the bytes take 119).
 #include "prompt.cuh"
 
 namespace dsa {
@@ -64,11 +64,13 @@ struct Work {
 };
 
 constexpr int kQueue = 2;            // units handed out and not yet taken up by every role
+constexpr int kDrawAhead = 6;        // key tiles of a unit still to come when the next one is drawn
 constexpr int kTakers = 11;          // 8 softmax warps, 2 MMA warps, the key loader
 
 struct Ctl {
     Work work[kQueue];
     uint64_t work_full[kQueue], work_free[kQueue];
+    uint64_t draw;  // the unit's last tiles are at work: the next unit is drawn
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2];  // p_full: the first 96 keys' weights, the rest
     uint64_t turn[2];  // the tensor pipe's next turn belongs to tile A, B
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&S.join_free[i]), 32);
         }
         mbar_init(smem_u32(&S.mma_done), 2);
+        mbar_init(smem_u32(&S.draw), 1);
         S.abort_flag = 0;
         fence_mbar_init();
     }
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 11) {
             // ------------------------------------------------------------------ units and their queries
             const int G = a.H / a.H_kv;
-            int qphase0 = 1, qphase1 = 1, fphase = 1, slot = 0;
+            int qphase0 = 1, qphase1 = 1, fphase = 1, dphase = 0, slot = 0;
             bool ok = true;
             for (int w = blockIdx.x; ok;) {
                 const Work k = get_work(a, n_units, group, w);
@@ -225,11 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     S.work[slot] = k;
                     mbar_arrive(smem_u32(&S.work_full[slot]));
-                    // (without a list there is a CTA for every unit)
-                    if (k.hk >= 0) w = a.self_plan ? 0x7FFFFFFF : gridDim.x + atomicAdd(&a.head->next, 1);
                 }
                 if (++slot == kQueue) slot = 0, fphase ^= 1;
-                w = __shfl_sync(0xFFFFFFFFu, w, 0);
                 if (k.hk < 0) break;
     #pragma unroll 1
                 for (int x = 0; x < 2; ++x) {
@@ -274,6 +274,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     cp_async_arrive_noinc(smem_u32(&S.q_full[x]));
                 }
+                if (a.self_plan) {
+                    w = 0x7FFFFFFF;  // there is a CTA for every unit
+                    continue;
+                }
+                // The next unit is drawn late, so that CTAs with longer ones draw fewer, yet ahead of this one's end
+                // (2048 tokens, 32 / 8 heads: 55 us with two units drawn ahead, 44 so).
+                // (This wait lasts as long as the unit, 2^24 tiles at most; what stalls in it gives up by itself.)
+                const long long t0 = clock64();
+                while (ok && !mbar_try_wait(smem_u32(&S.draw), dphase)) {
+                    if (clock64() - t0 > 64 * kWaitCycles) {
+                        *abort_flag = 1;
+                        atomicOr(a.err, DSA_FAULT_TIMEOUT);
+                    }
+                    ok = !*abort_flag;
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                dphase ^= 1;
+                if (lane == 0) w = gridDim.x + atomicAdd(&a.head->next, 1);
+                w = __shfl_sync(0xFFFFFFFFu, w, 0);
             }
             // nothing may still be landing when the CTA exits
             cp_async_wait<0>();
@@ -509,7 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;
             const int first = k.kt0 + (k.apart ? x : 0), step = k.apart ? 2 : 1;
             const bool idle = row0 + (warp & 3) * 32 >= k.nrows;  // none of the warp's rows exist
+            // One warp says when the next unit is to be drawn: of the tile that has the last keys.
+            const bool last = warp == (k.n1 >= k.n0 ? 4 : 0) && !a.self_plan;
+            int late = last ? max(first, end - kDrawAhead) : end;
+            if (last && !any && lane == 0) mbar_arrive(smem_u32(&S.draw));
             for (int j = first; j < end; j += step) {
+                if (j >= late) {
+                    late = end;
+                    if (lane == 0) mbar_arrive(smem_u32(&S.draw));
+                }
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.s_full[x]), sphase, abort_flag, a.err))) {
                     dead = true;
                     break;
