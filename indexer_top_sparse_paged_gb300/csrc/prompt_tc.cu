@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         atomicOr(a.err, DSA_FAULT_TIMEOUT);
                     }
                     ok = !*abort_flag;
+                    __nanosleep(64);
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 dphase ^= 1;
