@@ -24,8 +24,8 @@ Entry points (same names as the C ABI):
   a workspace, for callers that cannot allocate device memory.
 
 Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`
-and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or ``stream=``). A decode step over a batch of B
-sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
+and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or
+``stream=``). A decode step over a batch of B sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
 
     dims = make_dims("bf16", B, max_blocks, num_blocks, H_I=64, d_I=128, H=128, d=576, d_v=512, K=2048)
     ws = workspace(dims, B)                      # sized for calls of B rows (the library checks it)

@@ -438,7 +438,7 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     const int64_t rows = static_cast<int64_t>(Tq) * (p.H / p.H_kv);
     w.tile_rows = prompt_uses_tc(p) ? kPromptTcRows : kPromptSimtRows;
     w.ctas = device_sm_count();
-    // Few query rows have small partials: keys are cut finer there (16 single tokens: 127 us against 140). The
+    // Few query rows have small partials: keys are cut finer there (16 single tokens: 140 us, then 127). The
     // plan makes fewer than 2 x shares partials over all key heads (see there), so at most 2 x shares / H_kv
     // of one head. Every size here grows with Tq (partials of twice the rows where they are half as many,
     // lists for either number), so that a workspace serves smaller calls.

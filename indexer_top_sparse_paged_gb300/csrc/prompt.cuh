@@ -96,7 +96,8 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[8]
 // columns c .. c + 7 out: sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p, the loads of kAhead parts in flight (past the last
 // it is loaded again: without a branch between them the loads go out together).
 template <int kAhead, typename T>
-__device__ __forceinline__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int q0, int row0, int hk, int r, int c) {
+__device__ __forceinline__ void prompt_join(const PromptArgs& a, int64_t slot0, int parts, int q0, int row0, int hk, int r,
+                                            int c) {
     const int G = a.H / a.H_kv, t = (row0 + r) / G;
     const int64_t at = (static_cast<int64_t>(q0) + t) * a.H + hk * G + (row0 + r - t * G);  // (token, head)
     const float2* ml = a.part_ml + slot0 * a.slot_rows + r;

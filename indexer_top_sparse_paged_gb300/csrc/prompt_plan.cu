@@ -201,7 +201,7 @@ bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
 // Joins the rows whose keys were split: a run of CTAs shares the columns of an item and key head, 8 to a thread
 // (a prompt of 1024 tokens, 32 / 8 heads: with one CTA for all columns the call took 60 us, with this 31). In the
 // attention kernel itself, by the last part to arrive, it held up the units behind it (16 single tokens over up
-// to 16K keys: 195 us, 126 so).
+// to 16K keys: 195 us, then 127).
 constexpr int kJoinThreads = 256;
 
 template <typename T>

@@ -314,3 +314,20 @@ def test_overlapping_sequences_fit_the_lists(dtype):
     got = dsa.prompt_attn(dims, q, k, v, starts(nq), starts(nk), 0.125, ws=ws)
     assert dsa.read_error(ws) == 0
     check(got, q, k, v, nq, nk, 0.125, causal=False)
+
+
+@pytest.mark.parametrize("dtype,d_qk,d_v", [(torch.float32, 20, 12), (torch.float32, 64, 68), (torch.bfloat16, 72, 88),
+                                            (torch.bfloat16, 200, 24)])
+@pytest.mark.parametrize("nq,nk", [([1, 1, 1], [5000, 1, 2100]), ([96], [6000]), ([300], [4000])])
+def test_split_keys_of_odd_widths(dtype, d_qk, d_v, nq, nk):
+    """Rows whose keys are split and joined where the last columns fill no run of eight or sixteen."""
+    q, k, v = make(dtype, nq, nk, 6, 2, d_qk, d_v, seed=d_v, pad=3)
+    check(attend(q, k, v, nq, nk, d_qk ** -0.5), q, k, v, nq, nk, d_qk ** -0.5)
+
+
+def test_many_units_of_mixed_lengths():
+    """Far more units than CTAs, long ones, short ones and ones without keys in turn."""
+    nq = [700, 1, 130, 0, 129, 300, 40] * 6
+    nk = [900, 3000, 130, 64, 0, 300, 20] * 6
+    q, k, v = make(torch.bfloat16, nq, nk, 32, 8, 64, 64, seed=3, pad=5)
+    check(attend(q, k, v, nq, nk, 0.125), q, k, v, nq, nk, 0.125)
