@@ -438,17 +438,13 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     const int64_t rows = static_cast<int64_t>(Tq) * (p.H / p.H_kv);
     w.tile_rows = prompt_uses_tc(p) ? kPromptTcRows : kPromptSimtRows;
     w.ctas = device_sm_count();
-    // Few query rows have small partials: keys are cut finer there (16 single tokens: 140 us, then 127). The
-    // plan makes fewer than 2 x shares partials over all key heads (see there), so at most 2 x shares / H_kv
-    // of one head. Every size here grows with Tq (partials of twice the rows where they are half as many,
-    // lists for either number), so that a workspace serves smaller calls.
-    const int most_slots = 8 * w.ctas / p.H_kv;
-    const bool fine = prompt_uses_tc(p) && rows <= kPromptTcRows / 2;
-    w.shares = (fine ? 4 : 2) * w.ctas;
-    w.max_slots = fine ? most_slots : (most_slots + 1) / 2;
-    w.slot_rows = fine || rows < w.tile_rows / 2 ? static_cast<int>((rows + 31) / 32 * 32) : w.tile_rows;
+    // The plan makes fewer than 2 x shares partials over all key heads (see there), so at most 2 x shares / H_kv
+    // of one head. Every size here grows with Tq, so that a workspace serves smaller calls.
+    w.shares = 2 * w.ctas;
+    w.max_slots = 2 * w.shares / p.H_kv;
+    w.slot_rows = rows <= w.tile_rows / 2 ? static_cast<int>((rows + 31) / 32 * 32) : w.tile_rows;
     // every sequence fills whole tiles but its last
-    w.max_units = static_cast<int>(rows / w.tile_rows) + p.B + most_slots;
+    w.max_units = static_cast<int>(rows / w.tile_rows) + p.B + w.max_slots;
     const size_t slots = static_cast<size_t>(w.max_slots) * p.H_kv;
     size_t off = 256;  // the error word
     w.head = off;
@@ -456,7 +452,7 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
     w.units = off;
     off = align256(off + sizeof(PromptUnit) * static_cast<size_t>(w.max_units));
     w.joins = off;
-    off = align256(off + sizeof(PromptJoin) * static_cast<size_t>(most_slots / 2));
+    off = align256(off + sizeof(PromptJoin) * static_cast<size_t>(w.max_slots / 2));
     w.part_ml = off;
     off = align256(off + sizeof(float2) * slots * w.slot_rows);
     w.part_o = off;

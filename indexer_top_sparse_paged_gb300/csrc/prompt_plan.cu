@@ -6,12 +6,18 @@
 //
 // Keys are split when the rows are too few to fill the SMs: with W key tiles over all rows and heads and C
 // CTAs, if the longest item has more than 1.25 W / C tiles. Every item is then cut at the multiples of
-// s = max(W / 2C, a 32nd of the longest, min_tiles) (W / 4C where a partial has few rows); a last part shorter
-// than min_tiles stays with the one before. The cuts are the same for all rows of a sequence, so that CTAs that
-// run side by side read the same keys (a chunk of 2048 on 32K keys: 0.7 ms where cuts at even shares of all
-// tiles took 1.1).
-// An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C (8 C) partials.
+// s = max(W / f C, a 32nd of the longest, min_tiles); a last part shorter than min_tiles stays with the one
+// before. The cuts are the same for all rows of a sequence, so that CTAs that run side by side read the same
+// keys (a chunk of 2048 on 32K keys: 0.7 ms where cuts at even shares of all tiles took 1.1). f is 2, so that
+// CTAs that are done early find more; on the tensor cores 1 where the items are few, and so cut into parts of one
+// length that fill one turn of CTAs (a single token, 64 / 8 heads, on 70K keys: 58 us against 73), or where a
+// CTA's share is short beside the cost of a unit (16 tokens on up to 2000 keys: 29 us against 35; on up to 16K keys
+// f = 2: 118 us against 125).
+// An item of n > s tiles becomes at most ceil(n / s) < 2 n / s parts: fewer than 2 W / s <= 4 C partials.
 // Units are listed by falling number of tiles: the last ones to run are the short ones.
+//
+// One CTA, bound by its latency, much of it instructions that are fetched for the first time: the three passes over
+// the items (tiles in all, units of each length, the list) are one loop.
 #include "prompt.cuh"
 
 namespace dsa {
@@ -64,133 +70,124 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptArgs a)
     __shared__ int warp_sum[kPlanThreads / 32];
     __shared__ int bucket[kBuckets];
     __shared__ unsigned long long total_tiles;
-    __shared__ int most_tiles, most_keys, slots, joins, join_rows;
-    const int tid = threadIdx.x, G = a.H / a.H_kv;
+    __shared__ int most_tiles, most_keys, items, slots, joins, join_rows;
+    const int tid = threadIdx.x, G = a.H / a.H_kv, shift = 31 - __clz(a.tile_rows);
     griddep_launch_dependents();  // the attention's prologue may start (it waits for this grid)
     if (tid == 0) {
         total_tiles = 0;
-        most_tiles = most_keys = slots = joins = join_rows = 0;
+        most_tiles = most_keys = items = slots = joins = join_rows = 0;
     }
-    for (int i = tid; i < kBuckets; i += kPlanThreads) bucket[i] = 0;
+    bucket[tid] = 0;
     __syncthreads();
-    bool loaded = false;  // up to 256 sequences stay in shared memory
-    bool kept = false;
-    PlanItem mine{};  // the thread's item, if there are no more than threads
-    // f(valid, item) for every item in turn, 256 at a time by the whole CTA
-    auto for_items = [&](auto&& f) {
-        if (kept) {
-            f(tid < prefix[kPlanThreads], mine);
-            return;
+    bool kept = false;  // the thread's item stays in registers, if there are no more than threads
+    PlanItem it{};
+    bool cut = false;
+    int s = 1, longest = 1;
+    float per_tile = 0.0f;  // buckets
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        if (pass == 1) {
+            const long long work = static_cast<long long>(total_tiles) * a.H_kv;
+            cut = a.max_slots > 1 && 4ll * a.ctas * most_tiles > 5 * work;
+            const bool once = a.tile_rows == kPromptTcRows && (2ll * items * a.H_kv <= a.ctas || work < 16ll * a.ctas);
+            // (rounded up: s >= W / f C bounds the number of partials)
+            const float share = static_cast<float>(work) / static_cast<float>(once ? a.ctas : a.shares) * 1.000001f;
+            s = max(max(a.min_tiles, static_cast<int>(fminf(share, 1e9f)) + 1), (most_tiles + kMaxParts - 1) / kMaxParts);
+            longest = max(1, cut ? min(most_tiles, s + a.min_tiles) : most_tiles);
+            per_tile = static_cast<float>(kBuckets - 1) / static_cast<float>(longest);
+        } else if (pass == 2) {
+            const int x = block_scan(bucket[tid], 0x7FFFFFFF, warp_sum);
+            if (tid == kPlanThreads - 1) {
+                a.head->n_units = min(x, a.max_units);
+                a.head->next = 0;
+                // heads whose keys and values (read again by every row tile) fit a part of L2 run side by side
+                const float head_bytes = 2.0f * (a.d_qk + a.d_v) * max(1, most_keys);
+                a.head->head_group = static_cast<int>(fmaxf(1.0f, fminf(static_cast<float>(a.H_kv), 48.0f * 1048576.0f / head_bytes)));
+            }
+            bucket[tid] = x - bucket[tid];
+            __syncthreads();
         }
         int left = a.max_units;  // items
         for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-            const int b = b0 + tid;
-            if (a.B > kPlanThreads || !loaded) {
-                loaded = true;
+            if (a.B > kPlanThreads || pass == 0) {  // up to 256 sequences stay in shared memory
+                const int b = b0 + tid;
                 int n = 0;
-                int4 s = make_int4(0, 0, 0, 0);
+                int4 q = make_int4(0, 0, 0, 0);
                 if (b < a.B) {
                     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
                     if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) {
                         atomicOr(a.err, DSA_FAULT_INDEX);
                     } else {
-                        s = make_int4(q0, q1 - q0, k0, k1 - k0);
-                        n = (s.y * G + a.tile_rows - 1) / a.tile_rows;
+                        q = make_int4(q0, q1 - q0, k0, k1 - k0);
+                        n = (q.y * G + a.tile_rows - 1) >> shift;
                     }
                 }
-                seqs[tid] = s;
+                seqs[tid] = q;
                 const int x = block_scan(n, left, warp_sum);
                 prefix[tid + 1] = x;
                 if (tid == 0) prefix[0] = 0;
                 __syncthreads();
             }
-            left -= prefix[kPlanThreads];
             const int total = prefix[kPlanThreads], seqs_here = min(kPlanThreads, a.B - b0);
+            left -= total;
             for (int i0 = 0; i0 < total; i0 += kPlanThreads) {
                 const int i = i0 + tid;
-                PlanItem it{};
-                if (i < total) {
-                    int lo = 0, hi = seqs_here - 1;  // the last sequence whose first item is at or before i
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (prefix[mid] <= i) lo = mid;
-                        else hi = mid - 1;
+                const bool valid = i < total;
+                if (!kept) {
+                    it = PlanItem{};
+                    if (valid) {
+                        int lo = 0, hi = seqs_here - 1;  // the last sequence whose first item is at or before i
+                        while (lo < hi) {
+                            const int mid = (lo + hi + 1) >> 1;
+                            if (prefix[mid] <= i) lo = mid;
+                            else hi = mid - 1;
+                        }
+                        const int4 q = seqs[lo];
+                        const int row0 = (i - prefix[lo]) << shift;
+                        it = PlanItem{q.x, q.y, q.z, q.w, row0, item_tiles(a, G, q.y, q.w, row0)};
                     }
-                    const int4 s = seqs[lo];
-                    const int row0 = (i - prefix[lo]) * a.tile_rows;
-                    it = PlanItem{s.x, s.y, s.z, s.w, row0, item_tiles(a, G, s.y, s.w, row0)};
+                    kept = a.B <= kPlanThreads && total <= kPlanThreads;
                 }
-                f(i < total, it);
-                if (a.B <= kPlanThreads && total <= kPlanThreads) {
-                    kept = true;
-                    mine = it;
+                if (pass == 0) {
+                    const unsigned tiles = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(it.tiles));
+                    const int most = __reduce_max_sync(0xFFFFFFFFu, it.tiles), keys = __reduce_max_sync(0xFFFFFFFFu, it.lk);
+                    if ((tid & 31) == 0) {
+                        atomicAdd(&total_tiles, static_cast<unsigned long long>(tiles));
+                        atomicMax(&most_tiles, most);
+                        atomicMax(&most_keys, keys);
+                    }
+                } else if (valid) {
+                    const int parts = cut ? max(1, (it.tiles + s - a.min_tiles) / s) : 1;
+                    int slot = 0;
+                    if (pass == 2 && parts > 1) {
+                        slot = atomicAdd(&slots, parts);
+                        const int j = atomicAdd(&joins, 1);
+                        const int rows = min(a.tile_rows, it.lq * G - it.row0);
+                        atomicMax(&join_rows, rows);
+                        if (slot + parts <= a.max_slots && j < a.max_slots / 2)
+                            a.joins[j] = PromptJoin{it.q0, it.row0, rows, slot, parts, {0, 0, 0}};
+                    }
+                    for (int p = 0; p < parts; ++p) {
+                        const int t0 = p * s, t1 = p == parts - 1 ? it.tiles : t0 + s;
+                        const int to = max(0, kBuckets - 1 - static_cast<int>(static_cast<float>(min(t1 - t0, longest)) * per_tile));
+                        const int at = atomicAdd(&bucket[to], 1);  // falling number of tiles
+                        if (pass == 2 && at < a.max_units && slot + (parts > 1 ? parts : 0) <= a.max_slots)
+                            a.units[at] = PromptUnit{it.q0, it.lq, it.k0, it.lk, it.row0, t0, t1, slot, p, parts, {0, 0}};
+                    }
                 }
             }
+            if (tid == 0 && pass == 0) items += total;
             if (a.B > kPlanThreads) __syncthreads();  // the next sequences take their place
         }
-    };
-    for_items([&](bool valid, const PlanItem& it) {
-        const unsigned tiles = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(it.tiles));
-        const int longest = __reduce_max_sync(0xFFFFFFFFu, it.tiles), keys = __reduce_max_sync(0xFFFFFFFFu, it.lk);
-        if ((tid & 31) == 0) {
-            atomicAdd(&total_tiles, static_cast<unsigned long long>(tiles));
-            atomicMax(&most_tiles, longest);
-            atomicMax(&most_keys, keys);
-        }
-        (void)valid;
-    });
-    __syncthreads();
-    const long long work = static_cast<long long>(total_tiles) * a.H_kv;
-    const bool cut = a.max_slots > 1 && 4ll * a.ctas * most_tiles > 5 * work;
-    const int s = static_cast<int>(max(max(static_cast<long long>(a.min_tiles), (work + a.shares - 1) / a.shares),
-                                       static_cast<long long>((most_tiles + kMaxParts - 1) / kMaxParts)));
-    const int longest = max(1, cut ? min(most_tiles, s + a.min_tiles) : most_tiles);
-    auto bucket_of = [&](int tiles) {  // falling number of tiles
-        return kBuckets - 1 - static_cast<int>(static_cast<long long>(min(tiles, longest)) * (kBuckets - 1) / longest);
-    };
-    // f(part, parts, its first tile, its last + 1) for every unit of an item
-    auto units_of = [&](int tiles, auto&& f) {
-        const int parts = cut ? max(1, (tiles + s - a.min_tiles) / s) : 1;
-        for (int p = 0; p < parts; ++p) f(p, parts, p * s, p == parts - 1 ? tiles : (p + 1) * s);
-    };
-    for_items([&](bool valid, const PlanItem& it) {
-        if (valid) units_of(it.tiles, [&](int, int, int t0, int t1) { atomicAdd(&bucket[bucket_of(t1 - t0)], 1); });
-    });
-    __syncthreads();
-    const int x = block_scan(bucket[tid], 0x7FFFFFFF, warp_sum);
-    if (tid == kPlanThreads - 1) {
-        a.head->n_units = min(x, a.max_units);
-        a.head->next = 0;
-        // heads whose keys and values (read again by every row tile) fit a part of L2 run side by side
-        const long long head_bytes = 2ll * (a.d_qk + a.d_v) * max(1, most_keys);
-        a.head->head_group = static_cast<int>(max(1ll, min(static_cast<long long>(a.H_kv), (48ll << 20) / head_bytes)));
+        __syncthreads();
     }
-    bucket[tid] = x - bucket[tid];
-    __syncthreads();
-    for_items([&](bool valid, const PlanItem& it) {
-        int slot = 0;
-        if (!valid) return;
-        units_of(it.tiles, [&](int p, int parts, int t0, int t1) {
-            if (p == 0 && parts > 1) {
-                slot = atomicAdd(&slots, parts);
-                const int j = atomicAdd(&joins, 1);
-                const int rows = min(a.tile_rows, it.lq * G - it.row0);
-                atomicMax(&join_rows, rows);
-                if (slot + parts <= a.max_slots && j < a.max_slots / 2)
-                    a.joins[j] = PromptJoin{it.q0, it.row0, rows, slot, parts, {0, 0, 0}};
-            }
-            const int at = atomicAdd(&bucket[bucket_of(t1 - t0)], 1);
-            if (at < a.max_units && slot + (parts > 1 ? parts : 0) <= a.max_slots)
-                a.units[at] = PromptUnit{it.q0, it.lq, it.k0, it.lk, it.row0, t0, t1, slot, p, parts, {0, 0}};
-        });
-    });
-    __syncthreads();
     if (tid == 0) {
         a.head->n_joins = min(joins, a.max_slots / 2);
         a.head->join_rows = join_rows;
     }
 }
 static_assert(kBuckets == kPlanThreads, "the bucket scan takes one bucket per thread");
+static_assert((kPromptTcRows & (kPromptTcRows - 1)) == 0 && (kPromptSimtRows & (kPromptSimtRows - 1)) == 0, "rows are shifted");
 
 bool launch_prompt_plan(const PromptArgs& a, cudaStream_t s, int* launches) {
     if (!launch_kernel(false, prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a)) return false;
