@@ -32,7 +32,7 @@
 // 8192 tokens, 32 / 8 heads of 128 columns: 398 us, 1380 TFLOP/s of the causal products, 73% of the measured bf16
 // rate. Bound by the chain of each tile, logits -> weights -> product, two of which take turns: a pair of
 // tiles takes about 2900 cycles and its products 2048 of them. Short prompts pay the filling and draining of that
-// chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 294 us where the bytes take 119).
+// chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 289 us where the bytes take 119).
 #include "prompt.cuh"
 
 namespace dsa {
