@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(PromptArgs a) 
             const int r = row0 + kR * ty + i;
             seen[i] = r < nrows ? prompt_keys_seen(a, r / G, lq, lk) : 0;
         }
+        const bool idle = row0 + tid / 32 * 2 * kR >= nrows;  // none of the warp's rows exist: it only loads (16 tokens on 1000 keys: 201 us, then 170)
         // this part's keys, up to the last that the tile's last row sees
         const int n_keys = min(prompt_keys_seen(a, (min(nrows, row0 + kRows) - 1) / G, lq, lk), u.kt1 * kPromptKeys);
         const float c2 = a.sm_scale * 1.4426950408889634f;  // logits in powers of two
@@ -123,69 +124,73 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_simt_kernel(PromptArgs a) 
             for (int i = 0; i < kR; ++i)
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) zz[i][j] = 0;
+            if (!idle) {
 #pragma unroll 2
-            for (int e = 0; e < a.d_qk; e += 4) {
-                ulonglong2 kv[kJ];
+                for (int e = 0; e < a.d_qk; e += 4) {
+                    ulonglong2 kv[kJ];
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * pq + e);
+                    for (int j = 0; j < kJ; ++j) kv[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * pq + e);
 #pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(sq + (kR * ty + i) * pq + e);
+                    for (int i = 0; i < kR; ++i) {
+                        const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(sq + (kR * ty + i) * pq + e);
 #pragma unroll
-                    for (int j = 0; j < kJ; ++j) zz[i][j] = fma2(qv.y, kv[j].y, fma2(qv.x, kv[j].x, zz[i][j]));
-                }
-            }
-            __syncthreads();  // every warp has read the keys
-#pragma unroll
-            for (int i = 0; i < kR; ++i) {
-                float z[kJ], mt = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const float2 h = unpack2(zz[i][j]);
-                    z[j] = s0 + tx + 16 * j < seen[i] ? (h.x + h.y) * c2 : -INFINITY;
-                    mt = fmaxf(mt, z[j]);
-                }
-#pragma unroll
-                for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, w));
-                const float m_new = fmaxf(m[i], mt);
-                const float ref = m_new == -INFINITY ? 0.0f : m_new;  // no key yet: every weight is 0
-                const float alpha = exp2f(m[i] - ref);
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const float w = exp2f(z[j] - ref);
-                    sum += w;
-                    sp[(kR * ty + i) * kPitchP + tx + 16 * j] = w;
-                }
-                l[i] = l[i] * alpha + sum;  // this thread's keys; joined at the end
-                m[i] = m_new;
-                if (alpha != 1.0f) {
-                    const uint64_t aa = pack2(alpha, alpha);
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) {
-                        o[i][j][0] = fma2(o[i][j][0], aa, 0);
-                        o[i][j][1] = fma2(o[i][j][1], aa, 0);
+                        for (int j = 0; j < kJ; ++j) zz[i][j] = fma2(qv.y, kv[j].y, fma2(qv.x, kv[j].x, zz[i][j]));
                     }
                 }
             }
-            __syncwarp();  // a row's 16 threads are in one warp
-            for (int r = 0; r < kKeys; r += 4) {
-                float4 p[kR];
+            __syncthreads();  // every warp has read the keys
+            if (!idle) {
 #pragma unroll
-                for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (kR * ty + i) * kPitchP + r);
+                for (int i = 0; i < kR; ++i) {
+                    float z[kJ], mt = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                    for (int j = 0; j < kJ; ++j) {
+                        const float2 h = unpack2(zz[i][j]);
+                        z[j] = s0 + tx + 16 * j < seen[i] ? (h.x + h.y) * c2 : -INFINITY;
+                        mt = fmaxf(mt, z[j]);
+                    }
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j) {
-                        const int e = 4 * tx + 64 * j;
-                        if (e >= a.d_v) continue;
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sv + (r + q) * pv + e);
+                    for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, w));
+                    const float m_new = fmaxf(m[i], mt);
+                    const float ref = m_new == -INFINITY ? 0.0f : m_new;  // no key yet: every weight is 0
+                    const float alpha = exp2f(m[i] - ref);
+                    float sum = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < kR; ++i) {
-                            const float w = q == 0 ? p[i].x : q == 1 ? p[i].y : q == 2 ? p[i].z : p[i].w;
-                            const uint64_t ww = pack2(w, w);
-                            o[i][j][0] = fma2(ww, v.x, o[i][j][0]);
-                            o[i][j][1] = fma2(ww, v.y, o[i][j][1]);
+                    for (int j = 0; j < kJ; ++j) {
+                        const float w = exp2f(z[j] - ref);
+                        sum += w;
+                        sp[(kR * ty + i) * kPitchP + tx + 16 * j] = w;
+                    }
+                    l[i] = l[i] * alpha + sum;  // this thread's keys; joined at the end
+                    m[i] = m_new;
+                    if (alpha != 1.0f) {
+                        const uint64_t aa = pack2(alpha, alpha);
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) {
+                            o[i][j][0] = fma2(o[i][j][0], aa, 0);
+                            o[i][j][1] = fma2(o[i][j][1], aa, 0);
+                        }
+                    }
+                }
+                __syncwarp();  // a row's 16 threads are in one warp
+                for (int r = 0; r < kKeys; r += 4) {
+                    float4 p[kR];
+#pragma unroll
+                    for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (kR * ty + i) * kPitchP + r);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) {
+                            const int e = 4 * tx + 64 * j;
+                            if (e >= a.d_v) continue;
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sv + (r + q) * pv + e);
+#pragma unroll
+                            for (int i = 0; i < kR; ++i) {
+                                const float w = q == 0 ? p[i].x : q == 1 ? p[i].y : q == 2 ? p[i].z : p[i].w;
+                                const uint64_t ww = pack2(w, w);
+                                o[i][j][0] = fma2(ww, v.x, o[i][j][0]);
+                                o[i][j][1] = fma2(ww, v.y, o[i][j][1]);
+                            }
                         }
                     }
                 }
@@ -232,8 +237,8 @@ static bool launch_typed(const PromptArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d_qk, a.d_v);
     if (!set_max_dynamic_smem(reinterpret_cast<const void*>(prompt_simt_kernel<T, kCols>), smem)) return false;
     // A CTA for every whole item, and for as many parts as the plan aims at; should there be more, a CTA takes
-    // several. (One for every part that there could be, most of them empty: 5 prompts of up to 600 tokens 119 us
-    // against 117.)
+    // several. (One for every part that there could be, most of them empty, took 2 us longer for 5 prompts of up to
+    // 600 tokens, 120 us.)
     const int items = static_cast<int>(static_cast<int64_t>(a.Tq) * (a.H / a.H_kv) / a.tile_rows) + a.B;
     const int parts = 2 * a.shares / a.H_kv, most = items > parts ? items : parts;
     const int grid = most < a.max_units ? most : a.max_units;
