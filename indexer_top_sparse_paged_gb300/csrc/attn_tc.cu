@@ -298,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             uint32_t v0[32], v1[32];
             tmem_ld32(tmem + lane_base + kColS + sb * kRows, v0);
             tmem_ld32(tmem + lane_base + kColS + sb * kRows + 32, v1);
-            tmem_ld_wait();
+            tmem_ld_wait(v0, v1);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.s_sent[sb]));  // the softmax may overwrite S(j) with P
@@ -587,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
                 // both in units of 2^8 (the scale is folded into scale2)
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_base + kColS + sb * kRows + grp * 32, v);
-                tmem_ld_wait();
+                tmem_ld_wait(v);
                 const uint8_t* theirs = smem + kOffX + sb * kXBytes;
                 const uint32_t vm = valid_bits[2 * i + grp];  // rows without a position take no weight
 #pragma unroll
@@ -630,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
                             const uint32_t col = kColO + grp * (kDVH / 2) + cc * 32;
                             uint32_t v[32];
                             tmem_ld32(tmem + lane_base + col, v);
-                            tmem_ld_wait();
+                            tmem_ld_wait(v);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
                             tmem_st32(tmem + lane_base + col, v);
@@ -693,7 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             uint32_t v[32];
             if (have_o) {
                 tmem_ld32(tmem + lane_base + kColO + grp * (kDVH / 2) + cc * 32, v);
-                tmem_ld_wait();
+                tmem_ld_wait(v);
             }
             __syncwarp();
 #pragma unroll

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
                     uint32_t v0[32], v1[32];
                     tmem_ld32(taddr + q * kHeads, v0);
                     tmem_ld32(taddr + q * kHeads + 32, v1);
-                    tmem_ld_wait();
+                    tmem_ld_wait(v0, v1);
                     if (q == q0 + 1) {  // this warp has read all of its columns of the accumulator
                         tc_fence_before();
                         __syncwarp();

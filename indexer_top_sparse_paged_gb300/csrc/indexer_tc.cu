@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
                 const uint32_t taddr = tmem + acc * kHeads + ((quarter * 32) << 16);
                 tmem_ld32(taddr, v0);
                 tmem_ld32(taddr + 32, v1);
-                tmem_ld_wait();
+                tmem_ld_wait(v0, v1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.tempty[acc]));
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
                 const uint32_t taddr = tmem + acc * kHeads + ((quarter * 32) << 16);
                 tmem_ld32(taddr, v0);
                 tmem_ld32(taddr + 32, v1);
-                tmem_ld_wait();
+                tmem_ld_wait(v0, v1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.tempty[acc]));

@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t s[4][32];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, s[i]);
-                tmem_ld_wait();
+                tmem_ld_wait(s[0], s[1], s[2], s[3]);
                 if (cut) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -603,8 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 2 * kVC; ++c) {
                             uint32_t v[32];
                             tmem_ld32(tO + c * 32, v);
-                            tmem_ld_wait();
-                            tmem_ld_use32(v);
+                            tmem_ld_wait(v);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
                             tmem_st32(tO + c * 32, v);
@@ -657,13 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             auto load_o = [&](int c, uint32_t (&v)[32]) {  // columns 32c .. of the row's unnormalised output
                 tmem_ld32(tO + c * 32, v);
-                tmem_ld_wait();
-                tmem_ld_use32(v);
+                tmem_ld_wait(v);
                 if (k.apart) {
                     uint32_t u[32];
                     tmem_ld32(tO + 128 + c * 32, u);
-                    tmem_ld_wait();
-                    tmem_ld_use32(u);
+                    tmem_ld_wait(u);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         v[e] = __float_as_uint(__uint_as_float(v[e]) * fa + __uint_as_float(u[e]) * fb);

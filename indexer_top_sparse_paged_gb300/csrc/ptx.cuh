@@ -461,7 +461,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, uint32_t ab_type,
 
 // ---- TMEM loads / stores (32 lanes x 32 bits; each thread owns one lane = one row) -------------
 
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -483,13 +482,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
-// The values of a load are there after tmem_ld_wait; this keeps the compiler from using them earlier.
-__device__ __forceinline__ void tmem_ld_use32(uint32_t (&r)[32]) {
+// A register that the compiler takes for written here (no instruction).
+__device__ __forceinline__ void tmem_ld_use(uint32_t (&r)[32]) {
     asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
                    "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                    "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Waits for this thread's loads. To the compiler a load's registers are there as soon as it is issued, and a
+// "memory" clobber does not hold back arithmetic on registers: so the wait takes the arrays that were loaded
+// and every use of theirs stays behind it.
+template <typename... Arrays>
+__device__ __forceinline__ void tmem_ld_wait(Arrays&... loaded) {
+    static_assert(sizeof...(loaded) > 0, "name the registers that were loaded");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    (tmem_ld_use(loaded), ...);
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
