@@ -117,7 +117,8 @@ __device__ __forceinline__ void prompt_join(const PromptArgs& a, int64_t slot0, 
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (p0 + i >= parts || v[i].x == -INFINITY) continue;  // a part without keys wrote no columns
+            // a part without keys has no sum and wrote no columns (a NaN sum beside a maximum of -inf is joined)
+            if (p0 + i >= parts || v[i].y == 0.0f) continue;
             const float top = fmaxf(M, v[i].x), f = exp2f(v[i].x - top), keep = exp2f(M - top);
             l = l * keep + f * v[i].y;
 #pragma unroll

@@ -331,3 +331,20 @@ def test_many_units_of_mixed_lengths():
     nk = [900, 3000, 130, 64, 0, 300, 20] * 6
     q, k, v = make(torch.bfloat16, nq, nk, 32, 8, 64, 64, seed=3, pad=5)
     check(attend(q, k, v, nq, nk, 0.125), q, k, v, nq, nk, 0.125)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 200])
+def test_a_row_of_nan_stays_nan_whether_its_keys_are_split_or_not(dtype, d):
+    """A query that is NaN has no logit that compares, in no part of its keys: its row is NaN all the same, in
+    one pass over the keys and joined from many, and the other rows are what they are without it."""
+    for nq, nk in (([3, 2], [40, 300]), ([1, 2, 1], [9000, 6000, 700])):
+        q, k, v = make(dtype, nq, nk, 8, 2, d, d, seed=31)
+        clean = attend(q, k, v, nq, nk, d ** -0.5)
+        row, head = nq[0], 5  # the second sequence's first query
+        q[row, head] = float("nan")
+        out, lse = attend(q, k, v, nq, nk, d ** -0.5)
+        assert out[row, head].isnan().all() and lse[row, head].isnan()
+        rest = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+        rest[row, head] = False
+        assert torch.equal(out[rest], clean[0][rest]) and torch.equal(lse[rest], clean[1][rest])
