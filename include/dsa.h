@@ -250,7 +250,7 @@ dsa_status dsa_indexer_prolog(const dsa_dims* dims, const void* k_I_new, const v
  *   query). Each is [T][heads][rot] fp32 (type DSA_F32) or bf16 (DSA_BF16) through its strides, counted in
  *   elements: x points at the first rotated column of token 0's head 0, so part of a wider head is its
  *   address. out may be x itself (in place: same address and strides); any other overlap is undefined.
- *   freq       DEVICE fp64 [rot / 2], 8-byte aligned
+ *   freq       DEVICE fp64 [rot / 2], 8-byte aligned; one that is infinite or NaN turns its pair into NaN
  *   seq_lens, q_pos   as in dsa_indexer_topk: row t has position q_pos[t], or seq_lens[t] - 1 with q_pos
  *              NULL (decode). A row with a negative position (an empty sequence) is copied unchanged.
  *   transpose  nonzero: the transposed rotation, the backward pass (gradients of y in, of x out)

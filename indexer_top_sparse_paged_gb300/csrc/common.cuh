@@ -443,12 +443,13 @@ __device__ __forceinline__ int mx_exponent(float amax) {
     return max(E - 135, -127);
 }
 
-// (scale cos, scale sin) of position pos at angular frequency freq (radians per position, finite). The
+// (scale cos, scale sin) of position pos at angular frequency freq (radians per position). The
 // turns per position are held as a 64-bit binary fraction (freq / 2 pi in fp64, cut at 2^-64), so that their
 // product with the position drops its whole part by itself and far positions keep their fraction (to
 // 2^-33 turns from the cut, 2^-53 of the angle from fp64); one fp64 product, where the fp64 pipe takes 16 cycles
 // a warp. What fp32 leaves of the fraction (up to 2^-26 turns, one and a half steps of a cosine near 1)
-// comes back to first order. The transpose turns the other way.
+// comes back to first order. A frequency that is infinite or NaN has no angle, at position 0 either: NaN.
+// The transpose turns the other way.
 __device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale, bool transpose) {
     const long long bits = __double_as_longlong(freq * 0.15915494309189535);  // 1 / (2 pi)
     const int shift = static_cast<int>((bits >> 52) & 0x7FF) - 1011;          // mantissa * 2^(exponent - 1075 + 64)
@@ -460,7 +461,8 @@ __device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale
     const long long rest = turns - (static_cast<long long>(f) << 32);
     float s, c;
     sincospif(f * 0x1p-31f, &s, &c);
-    const float r = 6.2831853f * 0x1p-64f * static_cast<float>(rest);
+    float r = 6.2831853f * 0x1p-64f * static_cast<float>(rest);
+    if ((bits & 0x7FF0000000000000ll) == 0x7FF0000000000000ll) r = __int_as_float(0x7FFFFFFF);
     const float cc = fmaf(-s, r, c), ss = fmaf(c, r, s);
     return make_float2(scale * cc, transpose ? -scale * ss : scale * ss);
 }

@@ -304,3 +304,41 @@ def test_append_rope_bad_rows_are_skipped_and_reported():
         x, y = x.view(torch.uint8).view(-1, w), y.view(torch.uint8).view(-1, w)
         diff = (x != y).any(1).nonzero().flatten().tolist()
         assert set(diff) <= {int(at[i]) for i in (1, 2, 4)} and len(diff) == 3
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_frequency_that_is_no_number_gives_nan(dtype, bad):
+    """pos * f is no angle then, at position 0 either: its pair is NaN, the other pairs and the rows with a
+    negative position are what they are without it."""
+    T, H, rot = 5, 3, 64
+    freq = dsa.rope_frequencies(rot)
+    x = torch.randn((T, H, rot), device="cuda").to(dtype)
+    pos = torch.tensor([0, 7, -1, 100000, 3], dtype=torch.int32, device="cuda")
+    for layout, cols in (("interleaved", [10, 11]), ("half", [5, 37])):
+        want = dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(x))
+        f = freq.clone()
+        f[5] = bad
+        got = dsa.rope(x, f, q_pos=pos, layout=layout, out=torch.empty_like(x))
+        turned = pos >= 0
+        assert got[turned][..., cols].isnan().all() and torch.equal(got[~turned], x[~turned])
+        rest = [c for c in range(rot) if c not in cols]
+        assert torch.equal(got[..., rest], want[..., rest])
+
+
+def test_append_with_a_frequency_that_is_no_number_writes_nan():
+    p = Append("bf16", "act", [100, 200], [3, 2], 440)
+    s, rot = p.case.spec, 16
+    a, b = p.caches(), p.caches()
+    freq = dsa.rope_frequencies(rot)
+    f = freq.clone()
+    f[2] = math.inf
+    for c, g in ((a, freq), (b, f)):
+        dsa.cache_append_rope(p.dims, g, p.k_new, p.kv_new, p.table, p.lens, *c, p.q_seq, p.q_pos, ws=p.ws)
+    assert dsa.read_error(p.ws) == 0
+    at = p.rows()
+    for x, y, w, cols in ((a[0], b[0], s.d_I, [2, 2 + rot // 2]), (a[2], b[2], s.d, [s.d - rot + 4, s.d - rot + 5])):
+        x, y = x.view(-1, w)[at], y.view(-1, w)[at]
+        assert y[:, cols].isnan().all()
+        rest = [c for c in range(w) if c not in cols]
+        assert torch.equal(x[:, rest], y[:, rest])
