@@ -25,7 +25,9 @@ Entry points (same names as the C ABI):
 
 Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`
 and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or
-``stream=``). A decode step over a batch of B sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
+``stream=``). Nothing is recorded for autograd: :func:`rope`, :func:`cache_append_rope`, :func:`cache_read` and
+:func:`prompt_attn` refuse tensors that require gradients outside ``torch.no_grad()``. A decode step over a batch of B
+sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
 
     dims = make_dims("bf16", B, max_blocks, num_blocks, H_I=64, d_I=128, H=128, d=576, d_v=512, K=2048)
     ws = workspace(dims, B)                      # sized for calls of B rows (the library checks it)
@@ -323,7 +325,13 @@ def _need(ok: bool, what: str):
 
 
 def _device(*tensors) -> int:
-    """The current CUDA device's index, on which the library launches; every tensor must be there."""
+    """The current CUDA device's index, on which the library launches; every tensor must be there. Nothing is
+    recorded for autograd, so a tensor whose gradient would get lost is refused."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("tensor arguments must not record gradients (none would arrive: call under torch.no_grad(), "
+                                 "or from an autograd.Function)")
     dev = None
     for t in tensors:
         if t is not None:
@@ -385,7 +393,8 @@ def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, 
     positions ``q_pos`` (or seq_lens - 1), in place or into ``out``, and returns the result.
 
     ``x`` may be a view of part of wider heads (``q[..., 512:]``), or a list of up to four tensors of the
-    same tokens, with ``out`` and ``layout`` lists as well. ``transpose=True`` is the backward pass."""
+    same tokens, with ``out`` and ``layout`` lists as well. ``transpose=True`` is the backward pass, for an
+    autograd.Function of the caller's: nothing is recorded here, and tensors that record gradients are refused."""
     many = isinstance(x, (list, tuple))
     xs = x if many else (x,)
     outs = xs if out is None else out if many else (out,)

@@ -342,3 +342,30 @@ def test_append_with_a_frequency_that_is_no_number_writes_nan():
         assert y[:, cols].isnan().all()
         rest = [c for c in range(w) if c not in cols]
         assert torch.equal(x[:, rest], y[:, rest])
+
+
+class Turn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, freq, pos, layout):
+        ctx.save_for_backward(freq, pos)
+        ctx.layout = layout
+        return dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(x), scale=0.7)
+
+    @staticmethod
+    def backward(ctx, dy):
+        freq, pos = ctx.saved_tensors
+        return dsa.rope(dy, freq, q_pos=pos, layout=ctx.layout, out=torch.empty_like(dy), scale=0.7, transpose=True), None, None, None
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_gradients_come_from_a_function_of_the_callers_and_are_not_lost(layout):
+    T, H, rot = 9, 4, 32
+    freq = dsa.rope_frequencies(rot)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 771
+    x, dy = torch.randn((T, H, rot), device="cuda", requires_grad=True), torch.randn((T, H, rot), device="cuda")
+    Turn.apply(x, freq, pos, layout).backward(dy)
+    check(x.grad, dy, pos, freq, layout, 0.7, True)
+    with pytest.raises(ValueError, match="gradient"):
+        dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(dy))
+    with torch.no_grad():
+        check(dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(dy)), x.detach(), pos, freq, layout)

@@ -132,3 +132,25 @@ def test_binding_refusals(L):
     with pytest.raises(ValueError, match="CUDA"):
         dsa.prompt_attn(d, q, k, k, pos, pos, 0.1, ws=x)
     assert L.dsa_last_launch_count() == 0
+
+
+def test_tensors_that_record_gradients_are_refused(L):
+    """None of these calls records anything for autograd; a gradient that would get lost is an error, and under
+    no_grad the same tensors go on to the next check."""
+    x, freq, i32 = torch.zeros((4, 2, 64), requires_grad=True), torch.ones(32, dtype=torch.float64), torch.zeros(8, dtype=torch.int32)
+    q, k = torch.zeros((4, 8, 64)), torch.zeros((4, 2, 64))
+    ws, row = torch.zeros(1024, dtype=torch.uint8), torch.zeros((1, 576), dtype=torch.bfloat16)
+    dims = _dims(B=1)
+    new = torch.zeros((1, 128), dtype=torch.bfloat16, requires_grad=True)
+    calls = [lambda: dsa.rope(x, freq, q_pos=i32[:4]), lambda: dsa.rope([q, x * 1], freq, q_pos=i32[:4]),
+             lambda: dsa.rope(x.detach(), freq, q_pos=i32[:4], out=x),
+             lambda: dsa.cache_append_rope(dims, freq, new, row, i32, i32, ws, ws, ws, ws=ws),
+             lambda: dsa.cache_read(dims, ws, ws, new, i32, i32, i32, 1, ws=ws)]
+    for a, b, c in ((q.clone().requires_grad_(), k, k), (q, k.clone().requires_grad_(), k), (q, k, k.clone().requires_grad_())):
+        calls.append(lambda a=a, b=b, c=c: dsa.prompt_attn(dsa.prompt_dims(a, b, c, 1), a, b, c, i32, i32, 0.1, ws=ws))
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert L.dsa_last_launch_count() == 0
