@@ -26,8 +26,10 @@ Entry points (same names as the C ABI):
 Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`
 and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or
 ``stream=``). Nothing is recorded for autograd: :func:`rope`, :func:`cache_append_rope`, :func:`cache_read` and
-:func:`prompt_attn` refuse tensors that require gradients outside ``torch.no_grad()``. A decode step over a batch of B
-sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent rows::
+:func:`prompt_attn` refuse tensors that require gradients outside ``torch.no_grad()``, and the caller's outputs of the
+first and the last two count as changed in place (the paged caches, which belong to the library's calls, do not).
+A decode step over a batch of B sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent
+rows::
 
     dims = make_dims("bf16", B, max_blocks, num_blocks, H_I=64, d_I=128, H=128, d=576, d_v=512, K=2048)
     ws = workspace(dims, B)                      # sized for calls of B rows (the library checks it)
@@ -42,6 +44,7 @@ import os
 import struct
 
 import torch
+from torch.autograd.graph import increment_version
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
@@ -436,6 +439,7 @@ def rope(x, freq, seq_lens=None, q_pos=None, *, layout="interleaved", out=None, 
                         _raw_stream(dev, stream))
     if st:
         _check("dsa_rope", st)
+    increment_version(outs)  # a backward pass that kept what was here fails, and does not go on with the new values
     return outs if many else outs[0]
 
 
@@ -489,6 +493,7 @@ def cache_read(dims: Dims, k_I_cache, k_I_scale, kv_cache, block_table, seq_lens
                               _raw_stream(dev, stream))
     if st:
         _check("dsa_cache_read", st)
+    increment_version([t for t in (k_out, kv_out) if t is not None])
     return k_out, kv_out
 
 
@@ -545,6 +550,7 @@ def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, o
                                k.shape[0], sm_scale, _at(out), _at(lse), _at(ws), ws.numel(), _raw_stream(dev, stream))
     if st:
         _check("dsa_prompt_attn", st)
+    increment_version((out, lse))
     return out, lse
 
 

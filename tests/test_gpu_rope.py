@@ -369,3 +369,38 @@ def test_gradients_come_from_a_function_of_the_callers_and_are_not_lost(layout):
         dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(dy))
     with torch.no_grad():
         check(dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(dy)), x.detach(), pos, freq, layout)
+
+
+def test_what_is_written_in_place_counts_as_changed():
+    """A tensor that autograd keeps for a backward pass and that one of these calls then overwrites is an error in
+    that pass, as with any operation in place: its gradient would be formed from the new values."""
+    def changed(t, call):
+        w = torch.ones((), device="cuda", requires_grad=True)
+        y = (w * t).sum()
+        call()
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.backward()
+
+    freq, pos = dsa.rope_frequencies(16), torch.arange(6, dtype=torch.int32, device="cuda")
+    x, a, b = (torch.randn((6, 2, 48), device="cuda") for _ in range(3))
+    changed(x, lambda: dsa.rope(x[..., :16], freq, q_pos=pos))
+    changed(b, lambda: dsa.rope([x[..., :16], a[..., :16]], freq, q_pos=pos, out=[a[..., 16:32], b[..., 32:]]))
+    p = Append("bf16", "act", [100, 200], [3, 2], 450)
+    k, _, kv = p.caches()
+    s = p.case.spec
+    k_out, kv_out = torch.empty((300, s.d_I), device="cuda").bfloat16(), torch.empty((300, s.d), device="cuda").bfloat16()
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    read = lambda: dsa.cache_read(p.dims, k, None, kv, p.table, p.lens, cu, 300, k_out=k_out, kv_out=kv_out, ws=p.ws)  # noqa: E731
+    changed(k_out, read)
+    changed(kv_out, read)
+    q = torch.randn((6, 2, 16), device="cuda")
+    dims = dsa.prompt_dims(q, q, q, 1)
+    ws, out, lse = dsa.prompt_workspace(dims, 6), torch.empty_like(q), torch.empty((6, 2), device="cuda")
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    attend = lambda: dsa.prompt_attn(dims, q, q, q, cu, cu, 0.25, ws=ws, out=out, lse=lse)  # noqa: E731
+    changed(out, attend)
+    changed(lse, attend)
+    with torch.inference_mode():  # tensors without a count of changes
+        y = torch.randn((6, 2, 16), device="cuda")
+        assert dsa.rope(y, freq, q_pos=pos) is y
+    assert dsa.read_error(p.ws) == 0 and dsa.read_error(ws) == 0
