@@ -329,6 +329,7 @@ dsa_status dsa_cache_read(const dsa_dims* dims, const void* k_I_cache, const voi
  *   sm_scale > 0. Inputs of a sequence are finite; a query of NaN gives a row of NaN and leaves the others as they
  *   are, a key or value of NaN reaches any row of its sequence.
  * Widths: d_qk, d_v <= 256; H a multiple of H_kv; addresses, strides and row widths multiples of 16 bytes.
+ * Tq * H / H_kv + B and Tk stay below 2^31 - 2^16.
  * ws: at least dsa_prompt_workspace_size bytes, 256-byte aligned, initialised with dsa_workspace_init.
  */
 typedef struct {

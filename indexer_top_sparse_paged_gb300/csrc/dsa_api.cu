@@ -406,6 +406,9 @@ static HierLayout hier_layout(const dsa_dims& d, int T, int n_sel) {
 // prompt attention: checks and workspace
 // ------------------------------------------------------------------------------------------------
 
+// Rows (token, head of the group), keys and tiles are counted in 32 bits, with room to round up to tiles.
+constexpr int64_t kPromptCount = (1ll << 31) - (1 << 16);
+
 struct PromptLayout {
     size_t head;      // PromptHead
     size_t units;     // PromptUnit [max_units]
@@ -427,8 +430,7 @@ static dsa_status check_prompt_dims(const dsa_prompt_dims* p, int32_t Tq) {
     const int64_t strides[6] = {p->q_stride_t, p->q_stride_h, p->k_stride_t, p->k_stride_h, p->v_stride_t, p->v_stride_h};
     for (int64_t s : strides)
         if (s < 0 || s % unit || s > (1ll << 36)) return DSA_ERR_INVALID_ARG;
-    // rows (token, head of the group) and tiles are counted in 32 bits
-    const int64_t rows = static_cast<int64_t>(Tq) * (p->H / p->H_kv), limit = (1ll << 31) - (1 << 16);
+    const int64_t rows = static_cast<int64_t>(Tq) * (p->H / p->H_kv), limit = kPromptCount;
     if (rows + p->B >= limit || (rows / kPromptSimtRows + p->B) * p->H_kv >= limit) return DSA_ERR_UNSUPPORTED;
     return DSA_OK;
 }
@@ -826,6 +828,7 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
     dsa_status st = check_prompt_dims(dims, Tq);
     if (st != DSA_OK) return st;
     if (Tk < 0 || !(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (Tk >= kPromptCount) return DSA_ERR_UNSUPPORTED;
     if (Tq > 0 && (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v)))) return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     const PromptLayout L = prompt_layout(*dims, Tq);

@@ -29,7 +29,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // Keys that the sequence's query token t sees: its first ones, up to its own position when causal.
 __device__ __forceinline__ int prompt_keys_seen(const PromptArgs& a, int t, int lq, int lk) {
-    return a.causal ? min(lk, max(0, t + 1 + lk - lq)) : lk;
+    return a.causal ? min(lk, max(0, lk - lq + t + 1)) : lk;
 }
 
 // Small calls (at most 32 sequences and 7 key tiles, so that nothing is split) have no work list: a warp reads

@@ -33,7 +33,7 @@ struct PlanItem {
 // Key tiles that rows row0 .. row0 + tile_rows - 1 of a sequence see.
 __device__ __forceinline__ int item_tiles(const PromptArgs& a, int G, int lq, int lk, int row0) {
     const int last = min(lq * G, row0 + a.tile_rows) - 1;
-    const int seen = a.causal ? min(lk, max(0, last / G + 1 + lk - lq)) : lk;
+    const int seen = a.causal ? min(lk, max(0, lk - lq + last / G + 1)) : lk;
     return (seen + kPromptKeys - 1) / kPromptKeys;
 }
 

@@ -154,3 +154,16 @@ def test_tensors_that_record_gradients_are_refused(L):
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             call()
     assert L.dsa_last_launch_count() == 0
+
+
+def test_prompts_longer_than_32_bits_count_are_refused(L):
+    """The keys of a call are counted in 32 bits and rounded up to tiles: a count that leaves no room for that is
+    refused (it gave rows without keys), whatever the strides that make so many keys cheap."""
+    for type_, strides in ((0, (0, 8, 0, 8)), (1, (0, 8, 0, 8)), (1, (8, 8, 8, 8))):
+        dims = _prompt(type=type_, B=1, H=1, H_kv=1, d_qk=8, d_v=8, q_stride_t=8, q_stride_h=8, k_stride_t=strides[0], k_stride_h=strides[1],
+                       v_stride_t=strides[2], v_stride_h=strides[3])
+        for Tk in ((1 << 31) - 1, (1 << 31) - (1 << 16)):
+            assert L.dsa_prompt_attn(ctypes.byref(dims), FAKE, FAKE, FAKE, FAKE, FAKE, 1, Tk, 0.1, FAKE, None, None, BIG, None) == 2
+        # the largest count goes on to the next check
+        assert L.dsa_prompt_attn(ctypes.byref(dims), FAKE, FAKE, FAKE, FAKE, FAKE, 1, (1 << 31) - (1 << 16) - 1, 0.1, FAKE, None, None, BIG,
+                                 None) == 3
