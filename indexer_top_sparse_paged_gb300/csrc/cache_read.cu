@@ -152,7 +152,8 @@ bool launch_cache_read(const dsa_dims& d, bool kv_fp8, const void* k_cache, cons
                              : key == DSA_MXFP8 ? cache_read_kernel<true, DSA_MXFP8> : cache_read_kernel<true, DSA_BF16_KFP8>)
                           : (key == DSA_BF16 ? cache_read_kernel<false, DSA_BF16>
                              : key == DSA_MXFP8 ? cache_read_kernel<false, DSA_MXFP8> : cache_read_kernel<false, DSA_BF16_KFP8>);
-    if (!launch_kernel(false, kernel, dim3((R + rows - 1) / rows), dim3(kReadThreads), 0, s, a)) return false;
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(R) + rows - 1) / rows);
+    if (!launch_kernel(false, kernel, dim3(grid), dim3(kReadThreads), 0, s, a)) return false;
     ++*launches;
     return true;
 }

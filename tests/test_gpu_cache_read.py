@@ -132,3 +132,18 @@ def test_append_then_read_is_the_identity_of_stored_values():
         if group == 32:
             bound = torch.maximum(bound, torch.where(want.abs() >= top * 0.875, want.abs() * 0.125 * 1.05, bound))
         assert bool(((got.float() - want).abs() <= bound).all())
+
+
+def test_rows_up_to_what_32_bits_count():
+    """The last rows of an output of 2^31 - 1 rows (32 GB of them, three of which are written)."""
+    c = Cache("bf16", "act", [100], d=8, d_v=8, d_I=8, H=2, H_I=2)
+    R = (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("32 GB of outputs do not fit")
+    k_out = torch.empty((R, 8), dtype=torch.bfloat16, device="cuda")
+    k_out[-4:] = 7
+    k, _ = c.read([R - 3, R], R, [50], k_out=k_out, want_kv=False)
+    assert dsa.read_error(c.ws) == 0
+    assert bool((k_out[-4] == 7).all()) and torch.equal(k_out[-3:], c.want(0, 50, 3)[0])
+    del k, k_out
+    torch.cuda.empty_cache()
