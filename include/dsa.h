@@ -243,8 +243,8 @@ dsa_status dsa_indexer_prolog(const dsa_dims* dims, const void* k_I_new, const v
  *   DSA_ROPE_BASE    base * factor^(rot / (rot - 2)) (slow pairs stretched by factor, the fastest kept)
  *   DSA_ROPE_YARN    pairs with fewer than beta_slow turns over original_length positions / factor,
  *                    those with more than beta_fast turns kept, a linear ramp over the pairs between
- *   rot even, 2..DSA_ROPE_MAX_WIDTH; base > 0, factor >= 1; YaRN: base > 1, original_length > 0,
- *   beta_fast >= beta_slow > 0.
+ *   rot even, 2..DSA_ROPE_MAX_WIDTH; base > 0, factor >= 1 (frequencies within fp64's range); YaRN: base > 1,
+ *   original_length > 0, beta_fast >= beta_slow > 0.
  *
  * dsa_rope: n <= DSA_ROPE_MAX_TENSORS tensors of the same T tokens in one launch (a query and an indexer
  *   query). Each is [T][heads][rot] fp32 (type DSA_F32) or bf16 (DSA_BF16) through its strides, counted in

@@ -710,6 +710,7 @@ dsa_status dsa_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
         if (high - low < 0.001) high = low + 0.001;
     }
     if (scaling == DSA_ROPE_BASE && factor > 1.0 && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    if (!std::isfinite(base) || !std::isfinite(std::pow(base, -2.0 * (half - 1) / rot))) return DSA_ERR_INVALID_ARG;
     for (int i = 0; i < half; ++i) {
         double f = std::pow(base, -2.0 * i / rot);
         if (scaling == DSA_ROPE_LINEAR) f /= factor;

@@ -167,3 +167,16 @@ def test_prompts_longer_than_32_bits_count_are_refused(L):
         # the largest count goes on to the next check
         assert L.dsa_prompt_attn(ctypes.byref(dims), FAKE, FAKE, FAKE, FAKE, FAKE, 1, (1 << 31) - (1 << 16) - 1, 0.1, FAKE, None, None, BIG,
                                  None) == 3
+
+
+def test_frequencies_outside_of_64_bits_are_refused(L):
+    """A stretched base or a frequency that overflows is no set of frequencies (all but the first came out as 0, or
+    the last ones as infinite); the outermost bases that do not overflow give what the definition gives."""
+    f = (ctypes.c_double * 32)()
+    for base, scaling, factor in ((1e300, 1, 1e10), (1e-300, 1, 1.7e308), (5e-324, 0, 1.0), (1e-310, 0, 1.0)):
+        assert L.dsa_rope_frequencies(64, base, scaling, factor, 4096.0, 32.0, 1.0, f) == 1 or all(math.isfinite(x) and x > 0 for x in f), base
+    assert L.dsa_rope_frequencies(64, 1e300, 1, 1e10, 4096.0, 32.0, 1.0, f) == 1
+    assert L.dsa_rope_frequencies(64, 5e-324, 0, 1.0, 4096.0, 32.0, 1.0, f) == 1
+    for base in (1e300, 1e-300):
+        assert L.dsa_rope_frequencies(64, base, 0, 1.0, 4096.0, 32.0, 1.0, f) == 0
+        assert all(abs(f[i] / base ** (-2.0 * i / 64) - 1) < 1e-12 for i in range(32))
