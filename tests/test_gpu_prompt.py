@@ -348,3 +348,64 @@ def test_a_row_of_nan_stays_nan_whether_its_keys_are_split_or_not(dtype, d):
         rest = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
         rest[row, head] = False
         assert torch.equal(out[rest], clean[0][rest]) and torch.equal(lse[rest], clean[1][rest])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("nq,nk", [([40, 50, 30], [40, 50, 30]), ([40, 50, 30], [500, 300, 2000]), ([2] * 40, [30] * 40)])
+def test_bad_sequences_between_good_ones(dtype, nq, nk):
+    """A sequence whose bounds descend or leave the tensors, in calls with and without a work list (more than 896
+    keys, more than 32 sequences): reported; the good sequences around it are right, and the rows of the bad one
+    and those behind the last one stay as they were."""
+    B, spare = len(nq), 20
+    q, k, v = (t.nan_to_num() for t in make(dtype, nq, nk, 8, 2, 64, 64, seed=B, pad=spare))
+    dims = dsa.prompt_dims(q, k, v, B)
+    ws = dsa.prompt_workspace(dims, len(q))
+    for which in ("queries descend", "keys descend", "queries leave", "keys leave"):
+        cu_q, cu_k = starts(nq).tolist(), starts(nk).tolist()
+        cu, n = (cu_q, len(q)) if which.startswith("queries") else (cu_k, len(k))
+        if which.endswith("descend"):  # sequence 1 ends before it starts; sequence 2 begins there
+            cu[2] = cu[1] - 1
+        else:
+            cu[-1] = n + 1
+        bad = 1 if which.endswith("descend") else B - 1
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        out, lse = torch.full((len(q), 8, 64), 3.0, dtype=dtype, device="cuda"), torch.full((len(q), 8), 3.0, device="cuda")
+        dsa.prompt_attn(dims, q, k, v, i32(cu_q), i32(cu_k), 0.125, ws=ws, out=out, lse=lse)
+        assert dsa.read_error(ws) == 2
+        untouched = torch.ones(len(q), dtype=torch.bool, device="cuda")
+        for b in range(B):
+            if b == bad:
+                continue
+            a, e = cu_q[b], cu_q[b + 1]
+            untouched[a:e] = False
+            # a row that two sequences claim has the answer of either: leave it out (the rest are the last positions still)
+            a, e = a + (which == "queries descend" and b == 2), e - (which == "queries descend" and b == 0)
+            ka, ke = cu_k[b], cu_k[b + 1] - (which == "queries descend" and b == 0)
+            check((out[a:e], lse[a:e]), q[a:e], k[ka:ke], v[ka:ke], [e - a], [ke - ka], 0.125)
+        assert bool((out[untouched] == 3).all()) and bool((lse[untouched] == 3).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,H_kv", [(8, 2), (6, 2), (4, 4)])
+def test_orders_of_heads_and_tokens(dtype, H, H_kv):
+    """Queries stored head by head, keys and values token by token and the other way round; token strides that are
+    no multiple of the head's; keys whose rows overlap in memory."""
+    nq, nk, d = [130, 1, 64], [130, 900, 300], 64
+    q, k, v = make(dtype, nq, nk, H, H_kv, d, d, seed=H)
+    want = attend(q, k, v, nq, nk, 0.125)
+    check(want, q, k, v, nq, nk, 0.125)
+    by_head = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+
+    def padded(t, extra):
+        room = torch.full((t.shape[0], t.shape[1] * t.shape[2] + extra), float("nan"), device="cuda").to(dtype)
+        view = room[:, :t.shape[1] * t.shape[2]].unflatten(1, t.shape[1:])
+        view.copy_(t)
+        return view
+
+    for a, b, c in ((by_head(q), k, v), (by_head(q), by_head(k), v), (q, k, by_head(v)), (padded(q, 8), padded(k, 24), padded(v, 40)),
+                    (by_head(q), padded(k, 8), by_head(v)), (padded(q, 72), by_head(k), padded(v, 8))):
+        got = attend(a, b, c, nq, nk, 0.125)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    line = torch.randn((sum(nk) * 8 + 64 * H_kv,), device="cuda").to(dtype)
+    k = line.as_strided((sum(nk), H_kv, d), (8, d, 1))  # each key starts 8 elements after the one before
+    check(attend(q, k, v, nq, nk, 0.125), q, k, v, nq, nk, 0.125)
