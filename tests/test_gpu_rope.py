@@ -404,3 +404,38 @@ def test_what_is_written_in_place_counts_as_changed():
         y = torch.randn((6, 2, 16), device="cuda")
         assert dsa.rope(y, freq, q_pos=pos) is y
     assert dsa.read_error(p.ws) == 0 and dsa.read_error(ws) == 0
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("lo,hi", [(0, 1 << 12), (1 << 12, 1 << 20), ((1 << 31) - 5000, 1 << 31)])
+def test_rope_error_of_near_and_far_positions(layout, lo, hi):
+    """fp32: cos and sin within two steps (2^-23; one is what the function promises), their correction rounds by
+    2^-25, the products with the scale and with an element by 2^-24 each, the sum by half a step of the result.
+    The angle is off by the cut of the frequency's turns, 2 pi 2^-33, and by fp64's roundings of the frequency in
+    turns (two, 2^-52 of the angle) and, in the definition, of the product (2^-53)."""
+    T, H, rot = 300, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(lo % 1000 + 7)
+    x = torch.randn((T, H, rot), generator=g, device="cuda")
+    pos = torch.randint(lo, hi, (T,), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    freq = dsa.rope_frequencies(rot)
+    y = dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(x), scale=1.25)
+    want, mag = rotated64(x, pos, freq, layout, 1.25)
+    angle = pos.double()[:, None] * freq
+    angle = torch.cat((angle, angle), -1) if layout == "half" else angle.repeat_interleave(2, -1)
+    arith = 4.5 * 2.0 ** -24 + 2 * math.pi * 2.0 ** -33 + 1.5 * 2.0 ** -52 * angle[:, None]
+    tol = want.abs() * 2.0 ** -24 + 1.25 * arith * mag * (1 + 2.0 ** -24)
+    assert bool(((y.double() - want).abs() <= tol * (1 + 2.0 ** -7)).all()), float(((y.double() - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("dtype,rot,layout", [(torch.bfloat16, 16, "half"), (torch.bfloat16, 8, "interleaved"), (torch.float32, 8, "half"),
+                                              (torch.float32, 4, "interleaved")])
+def test_rope_of_heads_of_one_piece(dtype, rot, layout):
+    """Aligned heads whose columns, or halves of them, fill just 16 bytes; alone and as part of wider heads."""
+    T, H = 50, 5
+    freq = dsa.rope_frequencies(rot)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 313
+    wide = torch.randn((T, H, 3 * rot), device="cuda").to(dtype)
+    for x in (wide[..., :rot].contiguous(), wide[..., rot:2 * rot]):
+        keep = x.clone()
+        check(dsa.rope(x, freq, q_pos=pos, layout=layout, out=torch.empty_like(keep)), keep, pos, freq, layout)
+        check(dsa.rope(x, freq, q_pos=pos, layout=layout), keep, pos, freq, layout)
