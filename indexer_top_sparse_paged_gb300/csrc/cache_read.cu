@@ -20,7 +20,7 @@ constexpr int kReadBatch = 2;    // pieces a thread has in flight
 constexpr int kReadSeqs = 1024;  // sequences whose first rows fit shared memory
 
 struct ReadArgs {
-    int mode, kv_fp8;
+    int mode;
     int B, max_blocks, num_blocks;
     int d_I, d;
     int R;
@@ -146,7 +146,7 @@ bool launch_cache_read(const dsa_dims& d, bool kv_fp8, const void* k_cache, cons
     const int64_t most = ((1ll << 32) - 1) / (units * units);
     if (rows > most) rows = static_cast<int>(most);
     const uint32_t magic = units > 1 ? static_cast<uint32_t>(((1ll << 32) + units - 1) / units) : 0;
-    ReadArgs a{d.mode, kv_fp8 ? 1 : 0, d.B, d.max_blocks, d.num_blocks, d.d_I, d.d, R, k_cache, k_scale, kv_cache,
+    ReadArgs a{d.mode, d.B, d.max_blocks, d.num_blocks, d.d_I, d.d, R, k_cache, k_scale, kv_cache,
                block_table, seq_lens, start, cu_rows, k_out, kv_out, err, rows, magic};
     auto* kernel = kv_fp8 ? (key == DSA_BF16 ? cache_read_kernel<true, DSA_BF16>
                              : key == DSA_MXFP8 ? cache_read_kernel<true, DSA_MXFP8> : cache_read_kernel<true, DSA_BF16_KFP8>)
