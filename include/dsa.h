@@ -326,6 +326,9 @@ dsa_status dsa_cache_read(const dsa_dims* dims, const void* k_I_cache, const voi
  *        reported (DSA_FAULT_INDEX).
  *   out  [Tq][H][d_v] in q's type, lse [Tq][H] fp32 (natural log; may be NULL), dense. A query that sees no
  *        key gives out = 0, lse = -inf. Neither may overlap an input.
+ *   DSA_BF16: with d_qk <= 192 and d_v <= 128 (and key and value rows of a positive stride) the softmax weights are
+ *   rounded to bf16 for their product with the values, half a step (2^-8) of each; sums and lse keep fp32. DSA_F32 and
+ *   wider heads keep fp32 weights.
  *   sm_scale > 0. Inputs of a sequence are finite; a query of NaN gives a row of NaN and leaves the others as they
  *   are, a key or value of NaN reaches any row of its sequence.
  * Widths: d_qk, d_v <= 256; H a multiple of H_kv; addresses, strides and row widths multiples of 16 bytes.

@@ -349,9 +349,10 @@ __device__ void requantise_block_rope(const RopeAppendArgs& p, int t, float* buf
 
 // Warp jobs 2t and 2t + 1 write token t's latent row and its key: the rotated columns go through a
 // per-warp buffer in shared memory in fp32 and are rounded once, into the cache's type. Bound by the chain
-// of loads that leads to a token's place and by the divisions by its scales. (One warp for both rows of a
-// token, its tiles in registers, took 30 us for 8192 fp8 tokens of 512 + 128 from a cold L2, two warps without
-// the prefetch and one tile at a time 24, this form 20.)
+// of loads that leads to a token's place and by the arithmetic of its rows (a token's two warps execute 1458
+// instructions for an FP8 record and an MXFP8 key, the divisions by its scales among them; the schedulers issue in 53%
+// of the cycles). (One warp for both rows of a token, its tiles in registers, took 30 us for 8192 fp8 tokens of
+// 512 + 128 from a cold L2, two warps without the prefetch and one tile at a time 24, this form 20.)
 __global__ void __launch_bounds__(kAppendThreads) cache_append_rope_kernel(RopeAppendArgs p) {
     extern __shared__ float rope_buf[];
     const AppendArgs& a = p.a;

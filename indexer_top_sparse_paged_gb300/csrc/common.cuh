@@ -446,8 +446,8 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 // (scale cos, scale sin) of position pos at angular frequency freq (radians per position). The
 // turns per position are held as a 64-bit binary fraction (freq / 2 pi in fp64, cut at 2^-64), so that their
 // product with the position drops its whole part by itself and far positions keep their fraction (to
-// 2^-33 turns from the cut, 2^-53 of the angle from fp64); one fp64 product, where the fp64 pipe takes 16 cycles
-// a warp. What fp32 leaves of the fraction (up to 2^-26 turns, one and a half steps of a cosine near 1)
+// 2^-33 turns from the cut, 2^-52 of the angle from fp64's two roundings); one fp64 product, where the fp64
+// pipe takes 16 cycles a warp. What fp32 leaves of the fraction (up to 2^-26 turns, one and a half steps of a cosine near 1)
 // comes back to first order. A frequency that is infinite or NaN has no angle, at position 0 either: NaN.
 // The transpose turns the other way.
 __device__ __forceinline__ float2 rope_cos_sin(int pos, double freq, float scale, bool transpose) {
@@ -529,9 +529,10 @@ __device__ __forceinline__ void mx_quantize_group32(const uint16_t* src, uint16_
     for (int i = 0; i < 4; ++i) d4[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
-// 16 e4m3 codes times the power of two f -> 16 bf16. The fp32 products are exact (at most 4
-// significant bits, magnitudes >= 2^-136); so is their bf16 rounding unless a value lies below
-// bf16's normal range (an MX exponent under -117).
+// 16 e4m3 codes times f -> 16 bf16. With a power of two f (an MX scale) the fp32 products are exact (at
+// most 4 significant bits, magnitudes >= 2^-136), and so is their bf16 rounding unless a value lies below
+// bf16's normal range (an MX exponent under -117). With any other f (a tile's or a block's scale) the product
+// is rounded to fp32 and then to bf16.
 __device__ __forceinline__ void e4m3x16_to_bf16_scaled(const uint4& in, float f, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     uint32_t o[8];

@@ -414,7 +414,7 @@ struct PromptLayout {
     size_t units;     // PromptUnit [max_units]
     size_t joins;     // PromptJoin [max_slots / 2]
     size_t part_ml;   // float2 [max_slots * H_kv][slot_rows]
-    size_t part_o;    // fp32 [max_slots * H_kv][slot_rows][d_v]
+    size_t part_o;    // fp32 [max_slots * H_kv][d_v][slot_rows]
     size_t total;
     int tile_rows, max_units, ctas, shares, max_slots, slot_rows;
 };

@@ -6,10 +6,13 @@
 //
 // One CTA per tile of 64 rows (token, head of the group), key head and range of keys; one pass over the keys
 // in tiles of 64 with the running maximum and sum of each row in fp32. A thread holds 4 rows x 4 keys of the
-// logits and 4 rows x d_v / 16 columns of the output; multiply-adds are issued in pairs (fma.rn.f32x2). Bound by
-// what shared memory returns to the registers (16 bytes a lane take four cycles, however many lanes share
-// them): 8 (12) loads feed 64 (128) multiply-adds. 21 TFLOP/s at 4096 tokens, 8 heads of 128 (1.6 ms). Tiles of
-// 4 x 8 a thread, with half the warps, were slower (213 us, then 130, for five prompts of up to 600 tokens).
+// logits and 4 rows x d_v / 16 columns of the output; multiply-adds are issued in pairs (fma.rn.f32x2): 8 (12)
+// loads of 16 bytes a lane feed 64 (128) of them. 20 TFLOP/s at 4096 tokens, 8 heads of 128 (1.7 ms); five prompts of
+// up to 600 tokens, 8 / 2 heads, 121 us. Bound by latency: 206 registers a thread leave one CTA of 8 warps to an SM,
+// which issue in 37% (33%) of its cycles, waiting for shared memory (its pipe half used) and for their own last
+// instruction; keys and values are waited for before every tile, with nothing under way during the arithmetic; and
+// SMs that are done early stand idle, 23% (18%) of the time. Tiles of 4 x 8 a thread, with half the warps, were
+// slower (213 us, then 130, for the five prompts).
 #include "prompt.cuh"
 
 namespace dsa {

@@ -29,8 +29,11 @@
 // and its first products run, while the last one's outputs are written. (Four more warps for the outputs leave
 // the softmax 192 registers instead of 208: 304 us, not 297, for 9 prompts with 128 heads.)
 //
-// 8192 tokens, 32 / 8 heads of 128 columns: 398 us, 1380 TFLOP/s of the causal products, 73% of the measured bf16
-// rate. Bound by the chain of each tile, logits -> weights -> product, two of which take turns: a pair of
+// The two tiles in turn, the late rescaling and weights that are sent before the last of them is made are ideas
+// known from published attention kernels for this kind of GPU; roles, turns, work list and units apart are this file's own.
+//
+// 8192 tokens, 32 / 8 heads of 128 columns: 398 us back to back (407-414 among other calls), 1380 (1330) TFLOP/s of
+// the causal products, 73% (70%) of the measured bf16 rate. Bound by the chain of each tile, logits -> weights -> product, two of which take turns: a pair of
 // tiles takes about 2900 cycles and its products 2048 of them. Short prompts pay the filling and draining of that
 // chain for every unit (9 prompts of up to 1100 tokens, 128 heads of 192 / 128: 289 us where the bytes take 119).
 #include "prompt.cuh"

@@ -4,14 +4,17 @@
 //
 // with (a, b) = (2i, 2i + 1) (interleaved) or (i, i + rot / 2) (half). The transpose turns the other
 // way: it is the backward pass (the Jacobian s R is linear in x). The angle is formed as turns, p * (f / 2 pi),
-// in 64-bit fixed point, whose fraction is exact to 2^-33 turns at any position; fp32 would keep no more than
-// two digits of it at a million positions. Sine and cosine are taken of the fraction in fp32.
+// in 64-bit fixed point: off by at most 2^-33 turns, from the cut of the frequency's turns, and 2^-52 of the whole
+// angle, from their two roundings in fp64 (2^-21 radians at position 2^31 of the fastest pair; the fp64 product of
+// the definition itself rounds by half that). fp32 would keep no more than two digits of the fraction at a million
+// positions. Sine and cosine are taken of the fraction in fp32.
 //
 // Bound by memory: the rotated columns are read and written once. One CTA per token, so that its table of
 // rot / 2 cosines and sines is formed once for all heads of up to four tensors (one fp64 product and one
 // sincospi each); every thread asks for up to four pieces of 16 bytes (half layout: pairs of pieces)
 // before it waits for the table. 8192 tokens of 128 + 64 heads with 64 bf16 columns: 74 us, 80% of the measured
-// copy bandwidth. Views that are not aligned to 16 bytes go pair by pair.
+// copy bandwidth. Views that are not aligned to 16 bytes go pair by pair, and so do heads whose columns (half
+// layout: halves) are one piece or no whole number of them.
 #include "internal.h"
 
 namespace dsa {
