@@ -350,6 +350,86 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
                            float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream);
 
 /*
+ * Grouped-head cache: dense attention layers (grouped key / value heads, as in dsa_prompt_attn) in decode. Keys and
+ * values are cached in 8 bits, paged by the same block tables as the latent cache:
+ *   k_cache [num_blocks][H_kv][64][d_qk]  e4m3 codes     k_scale [num_blocks][H_kv]  fp32
+ *   v_cache [num_blocks][H_kv][64][d_v]   e4m3 codes     v_scale [num_blocks][H_kv]  fp32
+ * and a cached value is code * scale of its block and head, the scales positive and finite.
+ *   dims->type   DSA_F32 or DSA_BF16: type of q, out and of the new keys and values
+ *   widths       d_qk, d_v: multiples of 16, <= 256; H a multiple of H_kv; block_size 64
+ *   cu           [B + 1] ascending: the T rows of a call (queries or new tokens) cu[b] .. cu[b + 1] - 1 are the last
+ *                positions of sequence b, whose seq_lens[b] counts them; NULL: one row for each sequence (T == B).
+ *                Rows at and past cu[B] are not read as values and not written.
+ *   strides      of q, k_new and v_new in elements (token, head): multiples of 16 bytes, 0 or more; columns dense
+ * A sequence whose cu entries descend or leave [0, T], or whose seq_lens entry leaves [0, max_blocks * 64], is
+ * skipped by the append, has no positions in the attention and counts as empty in the eviction (DSA_FAULT_INDEX).
+ */
+typedef struct {
+    int32_t type;
+    int32_t B, max_blocks, num_blocks, block_size;
+    int32_t H, H_kv; /* query heads, key / value heads; query heads h * H / H_kv .. share key head h */
+    int32_t d_qk, d_v;
+} dsa_grouped_dims;
+
+/*
+ * Append of the sequences' new tokens (k_new [T][H_kv][d_qk], v_new [T][H_kv][d_v]), in fp32. With a the largest
+ * magnitude among the new rows that a block receives for a head, its scale becomes
+ *   a / 448 (1 when a is 0)       if the block held no earlier token of the sequence
+ *   max(old scale, a / 448)       if it did; when that is larger, the earlier codes become
+ *                                 RNE_e4m3(code * old scale / scale)
+ * and each new code RNE_e4m3(x / scale), saturating at +-448. Slots behind the new tokens stay as they were. A token
+ * whose position is negative or whose block is invalid is skipped and reported. New values are finite.
+ * ws as for dsa_cache_append (only its error word is used).
+ */
+dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, int64_t k_stride_t, int64_t k_stride_h,
+                              const void* v_new, int64_t v_stride_t, int64_t v_stride_h, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu, int32_t T, void* k_cache, float* k_scale,
+                              void* v_cache, float* v_scale, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Attention over the cache: query i of a sequence's n sees its positions s <= seq_lens[b] - n + i,
+ *   z = sm_scale * q . k_s,  out = sum softmax(z)_s v_s,  lse = ln sum exp(z_s).
+ *   q    [T][H][d_qk]; out [T][H][d_v] in q's type and lse [T][H] fp32 (may be NULL), dense. A query that sees no
+ *        position gives out = 0, lse = -inf.
+ *   weights, weights_out  [B][H_kv][max_blocks * 64] fp32, both NULL or weights_out given: the attention weight of every
+ *        position, summed over the sequence's queries and the query heads of its key head, is added to weights
+ *        (NULL: to 0; it may be weights_out itself) and written to weights_out for the positions below seq_lens[b];
+ *        the others stay as they were.
+ * Positions in invalid blocks are left out and reported. What unused slots of a block hold does not matter, NaN codes
+ * included. A query of NaN or infinities gives a row of NaN (and NaN weights); other inputs are finite. sm_scale > 0.
+ * ws: at least dsa_grouped_workspace_size(dims, T, weights wanted) bytes, 256-byte aligned, initialised with
+ * dsa_workspace_init.
+ */
+size_t dsa_grouped_workspace_size(const dsa_grouped_dims* dims, int32_t T, int32_t weights);
+dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                            const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int32_t T,
+                            float sm_scale, void* out, float* lse, const float* weights, float* weights_out, void* ws,
+                            size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Eviction by accumulated weight: every sequence of more than `keep` positions is cut to `keep` for each key head:
+ * the first `sink`, the last `recent`, and of the rest those of the largest weights (ties: the lower position; NaN counts as
+ * the lowest). The kept rows are copied, in order, into the blocks that new_table [B][new_max_blocks] names, each block
+ * and head requantised: x = code * scale, scale = max |x| / 448 (1 when that is 0), code = RNE_e4m3(x / scale), in fp32.
+ * A sequence of up to `keep` positions is copied as it is.
+ *   weights [B][H_kv][max_blocks * 64] fp32, only read
+ *   kept [B][H_kv][keep]  int32 out: the kept positions, ascending, then -1
+ *   new_lens [B]          int32 out: min(seq_len, keep); neither seq_lens nor anything else read here
+ *   weights_out [B][H_kv][new_max_blocks * 64]  fp32 out: the kept weights, then zeros; not weights itself
+ * New blocks are distinct from every block that the call reads, but that a sequence which is not cut may keep its own
+ * blocks (an entry equal to the old one is left alone). keep <= new_max_blocks * 64; sink, recent >= 0, together at
+ * most keep. Keys carry the rotation of the positions they were appended at; later tokens go on from new_lens.
+ * Rows from or into invalid blocks are skipped (their codes stay as they were) and reported. ws as for
+ * dsa_cache_append (only its error word is used).
+ */
+dsa_status dsa_grouped_evict(const dsa_grouped_dims* dims, const float* weights, int32_t keep, int32_t sink, int32_t recent,
+                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_table,
+                             int32_t new_max_blocks, void* k_cache, float* k_scale, void* v_cache, float* v_scale,
+                             int32_t* kept, int32_t* new_lens, float* weights_out, void* ws, size_t ws_bytes,
+                             dsa_stream_t stream);
+
+/*
  * Hierarchical (coarse -> fine) index selection ("Engineering Path for Day-0 Adaptation ..." §3.1:
  * coarse filtering at block granularity followed by refinement; "How the Ascend Computing
  * Platform Achieves Same-Day Inference Adaptation ..." §3.1: the coarse filter reuses summary

@@ -18,16 +18,19 @@ Entry points (same names as the C ABI):
 * :func:`cache_append_rope` -- the cache append of rows whose rotary columns are not turned yet.
 * :func:`cache_read` -- ranges of the paged caches read back as dense, dequantised rows.
 * :func:`prompt_attn` -- dense causal attention over packed prompts (grouped heads, prefixes).
+* :func:`grouped_append`, :func:`grouped_attn`, :func:`grouped_evict` -- a paged cache of grouped heads in 8 bits:
+  its append, decode attention over it (with the weight each position receives, if wanted), and eviction by it.
 * :func:`block_summaries`, :func:`indexer_topk_hier` -- hierarchical (coarse -> fine) selection over
   per-block summary keys.
 * :func:`indexer_topk_noalloc` -- :func:`indexer_topk` with the library's static scratch instead of
   a workspace, for callers that cannot allocate device memory.
 
-Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`
-and :func:`prompt_attn` take strided views as well); the calls are enqueued on the current stream (or
-``stream=``). Nothing is recorded for autograd: :func:`rope`, :func:`cache_append_rope`, :func:`cache_read` and
-:func:`prompt_attn` refuse tensors that require gradients outside ``torch.no_grad()``, and the caller's outputs of the
-first and the last two count as changed in place (the paged caches, which belong to the library's calls, do not).
+Every tensor argument is a contiguous CUDA tensor in the layout ``include/dsa.h`` gives (:func:`rope`,
+:func:`prompt_attn` and the new rows and queries of the grouped-head calls may be strided views); the calls are enqueued on the current stream (or
+``stream=``). Nothing is recorded for autograd: :func:`rope`, :func:`cache_append_rope`, :func:`cache_read`,
+:func:`prompt_attn` and the grouped-head calls refuse tensors that require gradients outside ``torch.no_grad()``, and
+the caller's outputs of all but the appends count as changed in place (the paged caches, which belong to the library's
+calls, do not).
 A decode step over a batch of B sequences, bf16 everywhere, 64 indexer heads of 128, 128 heads over 576-wide latent
 rows::
 
@@ -76,6 +79,11 @@ class RopeAppend(ctypes.Structure):
 class PromptDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("type", "B", "H", "H_kv", "d_qk", "d_v", "causal")] + \
         [(n, ctypes.c_int64) for n in ("q_stride_t", "q_stride_h", "k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h")]
+
+
+class GroupedDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("type", "B", "max_blocks", "num_blocks", "block_size", "H", "H_kv", "d_qk", "d_v")]
 
 
 class DsaError(RuntimeError):
@@ -129,6 +137,15 @@ def lib():
         L.dsa_prompt_workspace_size.argtypes = [PD, I32]
         L.dsa_prompt_attn.restype = ctypes.c_int
         L.dsa_prompt_attn.argtypes = [PD, P, P, P, P, P, I32, I32, F32, P, P, P, SZ, P]
+        GD, I64 = ctypes.POINTER(GroupedDims), ctypes.c_int64
+        L.dsa_grouped_append.restype = ctypes.c_int
+        L.dsa_grouped_append.argtypes = [GD, P, I64, I64, P, I64, I64, P, P, P, I32, P, P, P, P, P, SZ, P]
+        L.dsa_grouped_workspace_size.restype = SZ
+        L.dsa_grouped_workspace_size.argtypes = [GD, I32, I32]
+        L.dsa_grouped_attn.restype = ctypes.c_int
+        L.dsa_grouped_attn.argtypes = [GD, P, I64, I64, P, P, P, P, P, P, P, I32, F32, P, P, P, P, P, SZ, P]
+        L.dsa_grouped_evict.restype = ctypes.c_int
+        L.dsa_grouped_evict.argtypes = [GD, P, I32, I32, I32, P, P, P, I32, P, P, P, P, P, P, P, P, SZ, P]
         L.dsa_indexer_topk_noalloc.restype = ctypes.c_int
         L.dsa_indexer_topk_noalloc.argtypes = [D, P, P, P, P, P, P, P, P, I32, P, P, P]
         L.dsa_read_error.restype = ctypes.c_int
@@ -552,6 +569,133 @@ def prompt_attn(dims: PromptDims, q, k, v, cu_q, cu_k, sm_scale: float, *, ws, o
         _check("dsa_prompt_attn", st)
     increment_version((out, lse))
     return out, lse
+
+
+def grouped_dims(type: str, B: int, max_blocks: int, num_blocks: int, H: int, H_kv: int, d_qk: int, d_v: int,
+                 block_size: int = 64) -> GroupedDims:
+    """The dims of the grouped-head calls: ``type`` ("f32" or "bf16") is that of q, out and the new keys and values."""
+    _need(type in ("f32", "bf16"), f"unknown type {type!r}")
+    return GroupedDims(MODES[type], B, max_blocks, num_blocks, block_size, H, H_kv, d_qk, d_v)
+
+
+def grouped_workspace(dims: GroupedDims, T: int, weights: bool = False, device="cuda", stream=None) -> torch.Tensor:
+    """Allocates and initialises a workspace for the grouped-head calls of up to T query tokens (``weights``:
+    :func:`grouped_attn` with weights_out as well)."""
+    n = int(lib().dsa_grouped_workspace_size(ctypes.byref(dims), T, weights))
+    if n == 0:
+        raise ValueError("invalid dims")
+    ws = _empty(n + 256, torch.uint8, device, stream)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off: off + n]
+    _check("dsa_workspace_init", lib().dsa_workspace_init(_p(ws), n, _stream(stream)))
+    return ws
+
+
+def _grouped_rows(x, T: int, heads: int, width: int, dims: GroupedDims, name: str):
+    """Address and strides of [T][heads][width] rows, which may be a strided view."""
+    t, shape, st = torch.bfloat16 if dims.type else torch.float32, x.shape, x.stride()
+    if x.dtype is not t or len(shape) != 3 or shape[0] != T or shape[1] != heads or shape[2] != width:
+        raise ValueError(f"{name} must be a {t} tensor of [{T}][{heads}][{width}]")
+    if st[2] != 1 and T:
+        raise ValueError(f"a head's columns of {name} must be dense")
+    return x.data_ptr(), st[0], st[1]
+
+
+def _grouped_caches(dims: GroupedDims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T: int):
+    rows = dims.num_blocks * dims.H_kv
+    for t, n, name in ((k_cache, rows * 64 * dims.d_qk, "k_cache"), (v_cache, rows * 64 * dims.d_v, "v_cache")):
+        if t.element_size() != 1 or t.numel() < n:
+            raise ValueError(f"{name} must be a tensor of {n} bytes")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype is not torch.float32 or t.numel() < rows:
+            raise ValueError(f"{name} must be a float32 tensor of num_blocks x H_kv elements")
+    _int32(block_table, dims.B * dims.max_blocks, "block_table")
+    _int32(seq_lens, dims.B, "seq_lens")
+    _int32(cu, dims.B + 1, "cu")
+    if cu is None and T >= 0:
+        _need(T == dims.B, "without cu there is one row for each sequence")
+
+
+def _fp32(t, n: int, name: str):
+    if t.dtype is not torch.float32 or t.numel() < n:
+        raise ValueError(f"{name} must be a float32 tensor of {n} elements")
+
+
+def grouped_append(dims: GroupedDims, k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu=None, *,
+                   ws, stream=None) -> None:
+    """Writes new tokens (k_new[T][H_kv][d_qk], v_new[T][H_kv][d_v], strided views allowed) into the caches as e4m3 codes
+    with one scale per block and head: rows cu[b] .. cu[b + 1] - 1 are the last of sequence b's seq_lens[b] positions."""
+    T = k_new.shape[0]
+    dev = _device(k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu, ws)
+    k = _grouped_rows(k_new, T, dims.H_kv, dims.d_qk, dims, "k_new")
+    v = _grouped_rows(v_new, T, dims.H_kv, dims.d_v, dims, "v_new")
+    _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
+    st = lib().dsa_grouped_append(dims, *k, *v, _at(block_table), _at(seq_lens), _at(cu), T, _at(k_cache), _at(k_scale),
+                                  _at(v_cache), _at(v_scale), _at(ws), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _check("dsa_grouped_append", st)
+
+
+def grouped_attn(dims: GroupedDims, q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, sm_scale: float, cu=None,
+                 *, weights=None, weights_out=None, ws, out=None, lse=None, stream=None):
+    """(out[T][H][d_v], lse[T][H]) of attention over the cached positions: queries cu[b] .. cu[b + 1] - 1 (default: one for
+    each sequence) are the last of sequence b's positions, and each sees those up to its own.
+
+    ``weights_out`` ([B][H_kv][max_blocks * 64] fp32; default: ``weights`` itself, in place) receives ``weights`` plus the
+    attention weight of every position, summed over the sequence's queries and the heads of its group."""
+    T = q.shape[0]
+    if weights_out is None:
+        weights_out = weights
+    dev = _device(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, weights, weights_out, out, lse, ws)
+    rows = _grouped_rows(q, T, dims.H, dims.d_qk, dims, "q")
+    _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
+    for t, name in ((weights, "weights"), (weights_out, "weights_out")):
+        if t is not None:
+            _fp32(t, dims.B * dims.H_kv * dims.max_blocks * 64, name)
+    if out is None:
+        out = _empty((T, dims.H, dims.d_v), q.dtype, q.device, stream)
+    elif out.dtype is not q.dtype or out.numel() < T * dims.H * dims.d_v:
+        raise ValueError("out must be a tensor of T x H x d_v elements in q's type")
+    if lse is None:
+        lse = _empty((T, dims.H), torch.float32, q.device, stream)
+    else:
+        _fp32(lse, T * dims.H, "lse")
+    st = lib().dsa_grouped_attn(dims, *rows, _at(k_cache), _at(k_scale), _at(v_cache), _at(v_scale), _at(block_table),
+                                _at(seq_lens), _at(cu), T, sm_scale, _at(out), _at(lse), _at(weights), _at(weights_out),
+                                _at(ws), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _check("dsa_grouped_attn", st)
+    increment_version((out, lse) if weights_out is None else (out, lse, weights_out))
+    return out, lse
+
+
+def grouped_evict(dims: GroupedDims, weights, keep: int, block_table, seq_lens, new_table, k_cache, k_scale, v_cache, v_scale,
+                  *, sink: int = 0, recent: int = 0, ws, kept=None, new_lens=None, weights_out=None, stream=None):
+    """(kept[B][H_kv][keep], new_lens[B], weights_out[B][H_kv][blocks * 64]): every sequence cut to ``keep`` positions for each
+    key head -- the first ``sink``, the last ``recent`` and the heaviest of the rest by ``weights`` -- and the kept rows
+    copied into the blocks of ``new_table`` ([B][blocks]), requantised. Go on with new_table, new_lens and weights_out."""
+    _need(new_table.dim() == 2 and new_table.shape[0] == dims.B, "new_table must be [B][blocks]")
+    dev = _device(weights, block_table, seq_lens, new_table, k_cache, k_scale, v_cache, v_scale, ws, kept, new_lens, weights_out)
+    _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, None, -1)
+    _int32(new_table, 0, "new_table")
+    _fp32(weights, dims.B * dims.H_kv * dims.max_blocks * 64, "weights")
+    blocks = new_table.shape[1]
+    if kept is None:
+        kept = _empty((dims.B, dims.H_kv, max(0, keep)), torch.int32, ws.device, stream)
+    _int32(kept, dims.B * dims.H_kv * keep, "kept")
+    if new_lens is None:
+        new_lens = _empty((dims.B,), torch.int32, ws.device, stream)
+    _int32(new_lens, dims.B, "new_lens")
+    if weights_out is None:
+        weights_out = _empty((dims.B, dims.H_kv, blocks * 64), torch.float32, ws.device, stream)
+    _fp32(weights_out, dims.B * dims.H_kv * blocks * 64, "weights_out")
+    st = lib().dsa_grouped_evict(dims, _at(weights), keep, sink, recent, _at(block_table), _at(seq_lens), _at(new_table), blocks,
+                                 _at(k_cache), _at(k_scale), _at(v_cache), _at(v_scale), _at(kept), _at(new_lens),
+                                 _at(weights_out), _at(ws), ws.numel(), _raw_stream(dev, stream))
+    if st:
+        _check("dsa_grouped_evict", st)
+    increment_version((kept, new_lens, weights_out))
+    return kept, new_lens, weights_out
 
 
 def summaries_buffer(dims: Dims, device="cuda") -> torch.Tensor:

@@ -14,6 +14,7 @@
 #include <mutex>
 #include <vector>
 
+#include "grouped.cuh"
 #include "internal.h"
 
 namespace dsa {
@@ -465,6 +466,61 @@ static PromptLayout prompt_layout(const dsa_prompt_dims& p, int Tq) {
 
 static bool rope_layout_ok(int layout) { return layout == DSA_ROPE_INTERLEAVED || layout == DSA_ROPE_HALF; }
 
+// ------------------------------------------------------------------------------------------------
+// grouped-head cache: checks and workspace
+// ------------------------------------------------------------------------------------------------
+
+static dsa_status check_grouped_dims(const dsa_grouped_dims* d) {
+    if (!d) return DSA_ERR_INVALID_ARG;
+    if ((d->type != DSA_F32 && d->type != DSA_BF16) || d->block_size != kBlock) return DSA_ERR_UNSUPPORTED;
+    if (d->B <= 0 || d->max_blocks <= 0 || d->num_blocks <= 0 || d->H <= 0 || d->H_kv <= 0 || d->d_qk <= 0 || d->d_v <= 0)
+        return DSA_ERR_INVALID_ARG;
+    if (d->H % d->H_kv) return DSA_ERR_INVALID_ARG;
+    if (d->d_qk > 256 || d->d_v > 256 || d->d_qk % 16 || d->d_v % 16) return DSA_ERR_UNSUPPORTED;
+    // rows of the caches (the tensor maps count them in 32 bits), positions, and the grids
+    if (static_cast<int64_t>(d->num_blocks) * d->H_kv * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d->max_blocks) * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (d->H_kv > 32767 || static_cast<int64_t>(d->B) * d->H_kv >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+static bool grouped_strides_ok(const dsa_grouped_dims* d, int64_t st, int64_t sh) {
+    const int64_t unit = d->type == DSA_F32 ? 4 : 8;  // elements per 16 bytes
+    return st >= 0 && sh >= 0 && st % unit == 0 && sh % unit == 0 && st <= (1ll << 36) && sh <= (1ll << 36);
+}
+
+static bool ws_ok(const void* ws, size_t ws_bytes, size_t need) {
+    return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && ws_bytes >= need;
+}
+
+struct GroupedLayout {
+    size_t part_ml, part_o, row_lse, z, total;
+    int row_tile, ctas;
+    int64_t max_tiles;
+};
+
+// Rows of an item: as many as the average sequence of the call has for a key head, in powers of two.
+static GroupedLayout grouped_layout(const dsa_grouped_dims& d, int T, bool weights) {
+    GroupedLayout w{};
+    const int64_t G = d.H / d.H_kv;
+    w.row_tile = grouped_row_tile(d, T);
+    w.ctas = grouped_ctas(d);
+    // every sequence fills whole items but its last
+    w.max_tiles = (T * G / w.row_tile + d.B) * d.H_kv * ((d.max_blocks + 1) / 2);
+    size_t off = 256;  // the error word
+    const size_t slot_rows = static_cast<size_t>(2) * w.ctas * w.row_tile;
+    w.part_ml = off;
+    off = align256(off + sizeof(float2) * slot_rows);
+    w.part_o = off;
+    off = align256(off + sizeof(float) * slot_rows * d.d_v);
+    w.row_lse = off;
+    if (weights) off = align256(off + sizeof(float) * static_cast<size_t>(T) * d.H);
+    w.z = off;
+    if (weights) off = align256(off + sizeof(float) * static_cast<size_t>(w.max_tiles) * kGroupedTile * w.row_tile);
+    w.total = off;
+    return w;
+}
+
 }  // namespace dsa
 
 using namespace dsa;
@@ -888,6 +944,122 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
             (!whole && !launch_prompt_join(a, s, &launches)))
             st = DSA_ERR_LAUNCH;
     }
+    g_last_launches = launches;
+    return st;
+}
+
+dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, int64_t k_stride_t, int64_t k_stride_h,
+                              const void* v_new, int64_t v_stride_t, int64_t v_stride_h, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu, int32_t T, void* k_cache, float* k_scale,
+                              void* v_cache, float* v_scale, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+    dsa_status st = check_grouped_dims(dims);
+    if (st != DSA_OK) return st;
+    if (T < 0 || (!cu && T != dims->B)) return DSA_ERR_INVALID_ARG;
+    if (!grouped_strides_ok(dims, k_stride_t, k_stride_h) || !grouped_strides_ok(dims, v_stride_t, v_stride_h))
+        return DSA_ERR_INVALID_ARG;
+    if (T > 0 && (!k_new || !v_new || !block_table || !seq_lens || !k_cache || !k_scale || !v_cache || !v_scale))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache)) return DSA_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, 256)) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    const GroupedAppendArgs a{dims->type, dims->B, dims->max_blocks, dims->num_blocks, dims->H_kv, dims->d_qk, dims->d_v, T,
+                              k_new, v_new, k_stride_t, k_stride_h, v_stride_t, v_stride_h, block_table, seq_lens, cu,
+                              static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale,
+                              static_cast<int*>(ws)};
+    if (!launch_grouped_append(a, reinterpret_cast<cudaStream_t>(stream), &launches)) st = DSA_ERR_LAUNCH;
+    g_last_launches = launches;
+    return st;
+}
+
+size_t dsa_grouped_workspace_size(const dsa_grouped_dims* dims, int32_t T, int32_t weights) {
+    if (check_grouped_dims(dims) != DSA_OK || T < 0 || static_cast<int64_t>(T) * dims->H >= (1ll << 31)) return 0;
+    return grouped_layout(*dims, T, weights != 0).total;
+}
+
+dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                            const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int32_t T,
+                            float sm_scale, void* out, float* lse, const float* weights, float* weights_out, void* ws,
+                            size_t ws_bytes, dsa_stream_t stream) {
+    dsa_status st = check_grouped_dims(dims);
+    if (st != DSA_OK) return st;
+    if (T < 0 || (!cu && T != dims->B) || !(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(T) * dims->H >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
+    if (!grouped_strides_ok(dims, q_stride_t, q_stride_h)) return DSA_ERR_INVALID_ARG;
+    if (!block_table || !seq_lens || !k_cache || !k_scale || !v_cache || !v_scale || (T > 0 && (!q || !out)))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+    if (weights && !weights_out) return DSA_ERR_INVALID_ARG;
+    const GroupedLayout L = grouped_layout(*dims, T, weights_out != nullptr);
+    if (!ws_ok(ws, ws_bytes, L.total)) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    if (T > 0 || weights_out) {
+        uint8_t* base = static_cast<uint8_t*>(ws);
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        GroupedArgs a{};
+        a.type = dims->type;
+        a.B = dims->B;
+        a.max_blocks = dims->max_blocks;
+        a.num_blocks = dims->num_blocks;
+        a.H = dims->H;
+        a.H_kv = dims->H_kv;
+        a.G = dims->H / dims->H_kv;
+        a.d_qk = dims->d_qk;
+        a.d_v = dims->d_v;
+        a.T = T;
+        a.q = q;
+        a.q_stride_t = q_stride_t;
+        a.q_stride_h = q_stride_h;
+        a.k = static_cast<const uint8_t*>(k_cache);
+        a.v = static_cast<const uint8_t*>(v_cache);
+        a.k_scale = k_scale;
+        a.v_scale = v_scale;
+        a.block_table = block_table;
+        a.seq_lens = seq_lens;
+        a.cu = cu;
+        a.sm_scale = sm_scale;
+        a.out = out;
+        a.lse = lse;
+        a.weights = weights;
+        a.weights_out = weights_out;
+        a.err = reinterpret_cast<int*>(base);
+        a.row_tile = L.row_tile;
+        a.ctas = L.ctas;
+        a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+        a.part_o = reinterpret_cast<float*>(base + L.part_o);
+        a.row_lse = reinterpret_cast<float*>(base + L.row_lse);
+        a.z = reinterpret_cast<float*>(base + L.z);
+        a.max_tiles = L.max_tiles;
+        if (!launch_grouped_attn(a, s, &launches) || !launch_grouped_join(a, s, &launches)) st = DSA_ERR_LAUNCH;
+    }
+    g_last_launches = launches;
+    return st;
+}
+
+dsa_status dsa_grouped_evict(const dsa_grouped_dims* dims, const float* weights, int32_t keep, int32_t sink, int32_t recent,
+                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_table,
+                             int32_t new_max_blocks, void* k_cache, float* k_scale, void* v_cache, float* v_scale,
+                             int32_t* kept, int32_t* new_lens, float* weights_out, void* ws, size_t ws_bytes,
+                             dsa_stream_t stream) {
+    dsa_status st = check_grouped_dims(dims);
+    if (st != DSA_OK) return st;
+    if (keep <= 0 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > keep || new_max_blocks <= 0)
+        return DSA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(new_max_blocks) * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (keep > new_max_blocks * kBlock) return DSA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(dims->B) * dims->H_kv * ((keep + kBlock - 1) / kBlock) >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (!weights || !block_table || !seq_lens || !new_table || !k_cache || !k_scale || !v_cache || !v_scale || !kept ||
+        !new_lens || !weights_out)
+        return DSA_ERR_INVALID_ARG;
+    if (weights == weights_out || seq_lens == new_lens) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return DSA_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, 256)) return DSA_ERR_WORKSPACE;
+    int launches = 0;
+    const GroupedEvictArgs a{dims->B, dims->max_blocks, dims->num_blocks, dims->H_kv, dims->d_qk, dims->d_v, keep, sink, recent,
+                             new_max_blocks, weights, block_table, seq_lens, new_table, static_cast<uint8_t*>(k_cache),
+                             static_cast<uint8_t*>(v_cache), k_scale, v_scale, kept, new_lens, weights_out,
+                             static_cast<int*>(ws)};
+    if (!launch_grouped_evict(a, reinterpret_cast<cudaStream_t>(stream), &launches)) st = DSA_ERR_LAUNCH;
     g_last_launches = launches;
     return st;
 }

@@ -1,0 +1,138 @@
+// Shared by the kernels of the grouped-head cache: the arguments, the sequences' places and the work of the
+// attention, which every CTA finds in the lengths itself.
+//
+// The G = H / H_kv query heads of a key head share its keys, so a sequence's n queries give each key head one column of
+// n * G rows, row r = token r / G, head r % G of the group. An item is (sequence, key head, row_tile of those rows); its
+// positions are cut into tiles of 128. All tiles of all items, in this order, are one line, and CTA c of C takes the
+// tiles [c * per, (c + 1) * per), per = ceil(total / C): an even share of the cached bytes whatever the lengths. An item
+// cut by that leaves a partial (maximum, sum, unnormalised output) in its CTA's slot, and the join puts them together in
+// order of positions, so that results do not depend on timing.
+#pragma once
+
+#include "internal.h"
+
+namespace dsa {
+
+constexpr int kGroupedTile = 128;  // positions per tile: two cache blocks
+
+struct GroupedSeq {
+    int q0, n;       // first row of q, number of them
+    int len;         // cached positions
+    int items;       // row tiles
+    int tiles;       // position tiles
+};
+
+// Sequence b's place. What the host cannot see is checked here: a bad entry is reported (`report`), and the sequence is
+// left with no rows (cu) or no positions (seq_lens).
+__device__ __forceinline__ GroupedSeq grouped_seq(const GroupedArgs& a, int b, bool report) {
+    GroupedSeq s;
+    s.q0 = b;
+    s.n = 1;
+    if (a.cu) {
+        s.q0 = a.cu[b];
+        s.n = a.cu[b + 1] - s.q0;
+        if (s.q0 < 0 || s.q0 > a.T || s.n < 0 || s.n > a.T - s.q0) {
+            if (report) atomicOr(a.err, DSA_FAULT_INDEX);
+            s.q0 = s.n = 0;
+        }
+    }
+    s.len = a.seq_lens[b];
+    if (s.len < 0 || s.len > a.max_blocks * kBlock) {
+        if (report) atomicOr(a.err, DSA_FAULT_INDEX);
+        s.len = 0;
+    }
+    s.items = static_cast<int>((static_cast<int64_t>(s.n) * a.G + a.row_tile - 1) / a.row_tile);
+    s.tiles = (s.len + kGroupedTile - 1) / kGroupedTile;
+    return s;
+}
+
+__device__ __forceinline__ int64_t grouped_seq_tiles(const GroupedArgs& a, const GroupedSeq& s) {
+    return static_cast<int64_t>(s.items) * s.tiles * a.H_kv;
+}
+
+// Sum over the block's threads, and the sum of the threads before this one.
+template <int kThreads>
+__device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* total, int64_t* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) y += t;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = y;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sums[w];
+        all += warp_sums[w];
+    }
+    *total = all;
+    return before + y - x;
+}
+
+struct GroupedShare {
+    int64_t total;  // tiles of the call
+    int64_t per;    // tiles of a CTA
+    int b;          // the sequence that holds the share's first tile
+    int64_t base;   // the first tile of that sequence
+};
+
+// The sequence that holds unit `at` of the line that count(b) units of every sequence b make, and the first unit of that
+// sequence; at < 0 or past the end: only the total. All threads of the block call it, with the same `at`.
+template <int kThreads, typename Count>
+__device__ __forceinline__ void find_sequence(int B, int64_t at, Count count, int64_t* total, int* b_out, int64_t* base_out,
+                                              int64_t* warp_sums, int64_t* found) {
+    int64_t sum = 0;
+    if (threadIdx.x == 0) found[0] = -1;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        const int64_t n = b < B ? count(b) : 0;
+        int64_t all;
+        const int64_t before = sum + block_prefix<kThreads>(n, &all, warp_sums);
+        if (at >= before && at < before + n) {
+            found[0] = b;
+            found[1] = before;
+        }
+        sum += all;
+    }
+    __syncthreads();
+    *total = sum;
+    *b_out = static_cast<int>(found[0]);
+    *base_out = found[1];
+    __syncthreads();
+}
+
+// Slot of the partial that CTA c leaves of an item: its share's first item, if that is cut, uses slot 2c, and the last
+// one 2c + 1 (an item that fills the whole share is its first).
+__device__ __forceinline__ int grouped_slot(int64_t share_begin, int64_t piece_begin, int c) {
+    return 2 * c + (piece_begin > share_begin ? 1 : 0);
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint32_t code) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);  // exact
+    return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// 16 codes as fp32 values (exact).
+__device__ __forceinline__ void e4m3x16_values(const uint4& in, float (&x)[16]) {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+        const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3x4_codes(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+}  // namespace dsa

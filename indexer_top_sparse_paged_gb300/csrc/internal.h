@@ -222,6 +222,78 @@ bool launch_prompt_simt(const PromptArgs& a, cudaStream_t s, int* launches);
 bool launch_prompt_join(const PromptArgs& a, cudaStream_t s, int* launches);
 bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches);
 
+// ---- grouped-head cache -------------------------------------------------------------------------
+
+struct GroupedArgs {
+    int type;
+    int B, max_blocks, num_blocks;
+    int H, H_kv, G, d_qk, d_v;
+    int T;
+    const void* q;
+    int64_t q_stride_t, q_stride_h;  // elements
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu;
+    float sm_scale;
+    void* out;
+    float* lse;
+    const float* weights;
+    float* weights_out;
+    int* err;
+    int row_tile;       // rows of an item
+    int ctas;           // CTAs of the attention
+    float* part_o;      // [2 * ctas][row_tile][d_v] unnormalised outputs of cut items
+    float2* part_ml;    // [2 * ctas][row_tile] (running maximum in powers of two, sum)
+    float* row_lse;     // [T][H] log2 of the sums of 2^z (weights only)
+    float* z;           // [max_tiles][128][row_tile] logits in powers of two (weights only)
+    int64_t max_tiles;
+};
+
+struct GroupedAppendArgs {
+    int type;
+    int B, max_blocks, num_blocks, H_kv, d_qk, d_v;
+    int T;
+    const void* k_new;
+    const void* v_new;
+    int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu;
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int* err;
+};
+
+struct GroupedEvictArgs {
+    int B, max_blocks, num_blocks, H_kv, d_qk, d_v;
+    int keep, sink, recent, new_max_blocks;
+    const float* weights;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* new_table;
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t* kept;
+    int32_t* new_lens;
+    float* weights_out;
+    int* err;
+};
+
+int grouped_row_tile(const dsa_grouped_dims& d, int T);
+int grouped_ctas(const dsa_grouped_dims& d);
+bool launch_grouped_append(const GroupedAppendArgs& a, cudaStream_t s, int* launches);
+bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches);
+bool launch_grouped_join(const GroupedArgs& a, cudaStream_t s, int* launches);
+bool launch_grouped_evict(const GroupedEvictArgs& a, cudaStream_t s, int* launches);
+
 bool launch_attn_tc(const AttnArgs& a, cudaStream_t s, int* launches);
 bool launch_wait_timeout(int* err, cudaStream_t s, int* launches);
 

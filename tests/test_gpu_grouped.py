@@ -1,0 +1,615 @@
+"""The grouped-head cache in 8 bits (dsa_grouped_append, dsa_grouped_attn, dsa_grouped_evict) against the definitions in
+64 bits: lengths from none to many tiles, drafts, grouped heads, widths, strided views, queries without positions, codes
+of NaN in unused slots, invalid blocks and sequences, weights, ties, graphs and streams."""
+import math
+
+import pytest
+import torch
+
+import indexer_top_sparse_paged_gb300 as dsa
+
+pytestmark = pytest.mark.gpu
+ACT = {"f32": torch.float32, "bf16": torch.bfloat16}
+NAN_CODE = 0x7F
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def starts(n):
+    return ints([0] + torch.tensor(n, dtype=torch.int64).cumsum(0).tolist())
+
+
+def value(codes):
+    return codes.view(torch.float8_e4m3fn).double()
+
+
+class Cache:
+    """Caches of sequences of `lens` positions (room for `room`) in shuffled blocks; unused slots and blocks hold NaN codes."""
+
+    def __init__(self, lens, H, H_kv, d_qk, d_v, type="bf16", seed=0, room=None, spread=1.0):
+        self.g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens, self.H, self.H_kv, self.d_qk, self.d_v, self.type = list(lens), H, H_kv, d_qk, d_v, type
+        room = room or [max(1, n) for n in lens]
+        need = [(max(n, r) + 63) // 64 for n, r in zip(lens, room)]
+        self.blocks, self.width = sum(need) + 3, max(need) + 1
+        perm = torch.randperm(self.blocks, generator=self.g, device="cuda").to(torch.int32)
+        self.table = torch.full((len(lens), self.width), -1, dtype=torch.int32, device="cuda")
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = perm[at:at + n]
+            at += n
+        self.free = perm[at:]
+        make = lambda d: torch.full((self.blocks, H_kv, 64, d), NAN_CODE, dtype=torch.uint8, device="cuda")  # noqa: E731
+        self.k, self.v = make(d_qk), make(d_v)
+        self.ks, self.vs = (torch.full((self.blocks, H_kv), float("nan"), device="cuda") for _ in range(2))
+        for cache, scale, d in ((self.k, self.ks, d_qk), (self.v, self.vs, d_v)):
+            for b, n in enumerate(self.lens):
+                for j in range((n + 63) // 64):
+                    m, blk = min(64, n - 64 * j), int(self.table[b, j])
+                    x = torch.randn((H_kv, m, d), generator=self.g, device="cuda")
+                    scale[blk] = x.abs().amax(dim=(1, 2)) / 448 * spread ** (j % 5 - 2)
+                    cache[blk, :, :m] = (x * 448 / x.abs().amax(dim=(1, 2), keepdim=True)).to(torch.float8_e4m3fn).view(torch.uint8)
+        self.seq_lens = ints(self.lens)
+
+    def dims(self):
+        return dsa.grouped_dims(self.type, len(self.lens), self.width, self.blocks, self.H, self.H_kv, self.d_qk, self.d_v)
+
+    def args(self):
+        return self.k, self.ks, self.v, self.vs, self.table, self.seq_lens
+
+    def rows(self, b, h):
+        """(k, v) of sequence b and key head h in fp64, and which positions are in valid blocks."""
+        n = self.lens[b]
+        at = self.table[b, :(n + 63) // 64].long()
+        ok = (at >= 0) & (at < self.blocks)
+        at = at.clamp(0, self.blocks - 1)
+        k = (value(self.k[at, h]) * self.ks[at, h].double()[:, None, None]).flatten(0, 1)[:n]
+        v = (value(self.v[at, h]) * self.vs[at, h].double()[:, None, None]).flatten(0, 1)[:n]
+        ok = ok.repeat_interleave(64)[:n]
+        return torch.where(ok[:, None], k, 0.0), torch.where(ok[:, None], v, 0.0), ok
+
+    def queries(self, T, sharp=1.0):
+        return (sharp * torch.randn((T, self.H, self.d_qk), generator=self.g, device="cuda")).to(ACT[self.type])
+
+
+def check(c, q, new, got, scale, weights=None, weights_out=None):
+    """(out, lse) and the weights of the queries q against softmax attention in 64 bits."""
+    out, lse = got
+    bf16 = c.type == "bf16"
+    G, t0 = c.H // c.H_kv, 0
+    u = 2.0 ** -24
+    for b, (n, m) in enumerate(zip(c.lens, new)):
+        for h in range(c.H_kv):
+            k, v, ok = c.rows(b, h)
+            w = torch.zeros(n, dtype=torch.float64, device="cuda")
+            w_tol = torch.zeros_like(w)
+            for i in range(m):
+                Q = q[t0 + i, h * G:h * G + G].double()
+                seen = (torch.arange(n, device="cuda") <= n - m + i) & ok
+                z = (Q @ k.T * scale).masked_fill(~seen, -math.inf)
+                e = torch.logsumexp(z, -1)
+                o_got, e_got = out[t0 + i, h * G:h * G + G].double(), lse[t0 + i, h * G:h * G + G].double()
+                if not seen.any():
+                    assert not o_got.any() and bool((e_got == -math.inf).all())
+                    continue
+                p = torch.exp(z - e[:, None])
+                # A logit: the products and their fp32 sum round d + 2 times, the query's small elements keep an absolute
+                # error of 2^-22 of its largest (bf16 queries are split into two 4-bit significands, fp32 ones into six:
+                # both below that), and the factor to powers of two and the subtraction round twice more.
+                ka = k.abs()
+                z_tol = ((c.d_qk + 4) * u * (Q.abs() @ ka.T) + 2.0 ** -22 * Q.abs().amax(-1, keepdim=True) * ka.sum(-1)) * scale
+                z_tol = torch.where(seen, z_tol, 0.0).amax(-1) + 2.0 ** -22 * (1 + z[:, seen].abs().amax(-1))
+                # A weight: twice that, 2^-22 of the exponential, in bf16 2^-10 for its fp16 value and the parts of 4 bits it is
+                # split into (2^-11 each), and 2^-26 of the largest weight absolutely; sums add one rounding a position.
+                p_rel = 2 * z_tol + 2.0 ** -21 + (2.0 ** -10 if bf16 else 0.0) + (n + 8) * u
+                mag = p @ v.abs() + 2.0 ** -26 * p.amax(-1, keepdim=True) * v[ok].abs().sum(0) * (1.0 if bf16 else 2.0 ** -10)
+                o = p @ v
+                tol = p_rel[:, None] * mag * 1.01 + (2.0 ** -8 if bf16 else 2.0 ** -22) * o.abs() * 1.01 + 1e-30
+                tol = tol + 2.0 ** -26 * p.amax(-1, keepdim=True) * v[ok].abs().sum(0) * (1.01 if bf16 else 2.0 ** -10)
+                err = (o_got - o).abs()
+                assert bool((err <= tol).all()), (b, h, i, float((err - tol).max()), float(err.max()))
+                e_tol = z_tol + (n + 8) * u + 2.0 ** -22 * (1 + e.abs())
+                assert bool(((e_got - e).abs() <= e_tol).all()), (b, h, i, float(((e_got - e).abs() - e_tol).max()))
+                w += p.sum(0)
+                w_tol += ((2 * z_tol + e_tol + 2.0 ** -20)[:, None] * p).sum(0)
+            if weights_out is not None:
+                old = torch.zeros_like(w) if weights is None else weights[b, h, :n].double()
+                err = (weights_out[b, h, :n].double() - old - w).abs()
+                w_tol = w_tol + (m * G + 2) * u * (w + old.abs()) + 1e-30
+                assert bool((err <= w_tol).all()), (b, h, float((err - w_tol).max()))
+        t0 += m
+
+
+def attend(c, q, new, scale, faults=0, **kw):
+    ws = dsa.grouped_workspace(c.dims(), q.shape[0], weights=kw.get("weights_out") is not None or kw.get("weights") is not None)
+    cu = None if new == [1] * len(c.lens) and q.shape[0] == len(c.lens) else starts(new)
+    got = dsa.grouped_attn(c.dims(), q, *c.args(), scale, cu, ws=ws, **kw)
+    assert dsa.read_error(ws) == faults
+    return got
+
+
+LENS = [([1], [1]), ([64], [1]), ([128, 129, 127], [1, 1, 1]), ([0, 5, 0, 700], [1, 1, 1, 1]), ([65, 1, 2048, 63], [3, 1, 2, 5]),
+        ([300, 7, 40], [0, 4, 1]), ([3, 0, 1], [5, 2, 1]), ([5000], [1]), ([130, 2000], [16, 9])]
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,new", LENS)
+def test_lengths_and_drafts(type, lens, new):
+    c = Cache(lens, 8, 2, 128, 128, type, seed=len(lens))
+    q = c.queries(sum(new))
+    check(c, q, new, attend(c, q, new, 128 ** -0.5), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (7, 1), (12, 4), (6, 6), (64, 8), (130, 1), (48, 2), (10, 2), (33, 1)])
+def test_grouped_heads(type, H, H_kv):
+    lens, new = [300, 70, 1], [1, 3, 1]
+    c = Cache(lens, H, H_kv, 64, 64, type, seed=H)
+    q = c.queries(sum(new))
+    check(c, q, new, attend(c, q, new, 0.125), 0.125)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("d_qk,d_v", [(192, 128), (16, 16), (80, 48), (96, 96), (64, 128), (128, 64), (256, 256), (208, 144), (16, 256), (240, 16)])
+def test_widths(type, d_qk, d_v):
+    lens, new = [150, 900], [2, 1]
+    c = Cache(lens, 8, 2, d_qk, d_v, type, seed=d_qk + d_v)
+    q = c.queries(sum(new))
+    check(c, q, new, attend(c, q, new, d_qk ** -0.5), d_qk ** -0.5)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_many_sequences_and_long_ones(type):
+    """More sequences than a CTA has threads, most of them short or empty; then few long ones whose positions are split."""
+    lens = [(i * 37) % 200 if i % 3 else 0 for i in range(700)]
+    c = Cache(lens, 4, 2, 32, 32, type, seed=1)
+    q = c.queries(700)
+    check(c, q, [1] * 700, attend(c, q, [1] * 700, 0.2), 0.2)
+    c = Cache([40000, 129, 7000], 16, 2, 64, 64, type, seed=2)
+    q = c.queries(4)
+    check(c, q, [1, 2, 1], attend(c, q, [1, 2, 1], 0.125), 0.125)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_large_and_growing_logits(type):
+    """Logits that grow along the positions move every row's maximum in every tile; huge ones; equal ones; scales of the
+    blocks that lie far apart."""
+    c = Cache([1500], 4, 1, 64, 64, type, seed=3)
+    for j in range(24):
+        c.ks[int(c.table[0, j])] *= 0.2 + j
+    for sharp in (1.0, 64.0, 0.0):
+        q = c.queries(1, sharp)
+        check(c, q, [1], attend(c, q, [1], 0.5), 0.5)
+    for spread in (1e3, 1e-4):
+        c = Cache([1500, 40], 4, 1, 64, 64, type, seed=4, spread=spread)
+        c.ks.fill_(0.01)
+        q = c.queries(2)
+        check(c, q, [1, 1], attend(c, q, [1, 1], 0.125), 0.125)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_one_heavy_position_among_many_light_ones(type):
+    """Half of the weight on one position, the other half evenly on 30,000: light weights are not lost."""
+    n = 30001
+    c = Cache([n], 2, 1, 16, 16, type, seed=5)
+    c.k[c.table[0, :469].long()] = 0
+    c.k[int(c.table[0, 0]), 0, 3, 0] = 0x38  # 1.0
+    c.ks.fill_(1.0)
+    c.vs.fill_(1.0)
+    c.v[c.table[0, :469].long()] = 0x38
+    c.v[int(c.table[0, 0]), 0, 3] = 0
+    q = torch.zeros((1, 2, 16), dtype=ACT[type], device="cuda")
+    q[..., 0] = math.log(n - 1)
+    out, lse = attend(c, q, [1], 1.0)
+    check(c, q, [1], (out, lse), 1.0)
+    assert abs(float(out.float().mean()) - 0.5) < 0.01
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_strided_queries_and_rows_left_alone(type):
+    c = Cache([300, 64, 5], 8, 2, 64, 32, type, seed=6)
+    new = [2, 0, 1]
+    wide = torch.full((9, 8, 192), float("nan"), dtype=ACT[type], device="cuda")
+    q = wide[..., 64:128]
+    q[:3] = c.queries(3)
+    out = torch.full((9, 8, 32), 3.0, dtype=ACT[type], device="cuda")
+    lse = torch.full((9, 8), 4.0, device="cuda")
+    ws = dsa.grouped_workspace(c.dims(), 9)
+    dsa.grouped_attn(c.dims(), q, *c.args(), 0.125, starts(new), ws=ws, out=out, lse=lse)
+    assert dsa.read_error(ws) == 0
+    check(c, q, new, (out, lse), 0.125)
+    assert bool((out[3:] == 3.0).all()) and bool((lse[3:] == 4.0).all())
+    q = c.queries(3).transpose(0, 1).contiguous().transpose(0, 1)  # heads outermost
+    got = attend(c, q, new, 0.125)
+    check(c, q, new, got, 0.125)
+    q = c.queries(1)[:, :1].expand(3, 8, 64)  # one row for all
+    check(c, q, new, attend(c, q, new, 0.125), 0.125)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_queries_of_nan_and_infinity(type):
+    c = Cache([200, 300, 0], 8, 2, 64, 64, type, seed=7)
+    new = [2, 1, 1]
+    q = c.queries(4)
+    ref, ref_lse = attend(c, q, new, 0.125)
+    q[0, 1, 3], q[2, 5, 0], q[3, 0, 0] = float("nan"), math.inf, float("nan")
+    w = torch.zeros((3, 2, c.width * 64), device="cuda")
+    out, lse = attend(c, q, new, 0.125, weights_out=w)
+    bad = torch.zeros((4, 8), dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[2, 5] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], ref_lse[~bad])
+    assert w[0, 0, :199].isnan().all() and w[1, 1, :300].isnan().all()
+    assert not w[0, 0, 199:].isnan().any() and not w[0, 1].isnan().any() and not w[1, 0].isnan().any() and not w[2].any()
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_invalid_blocks_and_sequences(type):
+    c = Cache([700, 300, 130], 8, 2, 64, 64, type, seed=8)
+    q = c.queries(3)
+    c.table[0, 3], c.table[0, 10], c.table[1, 0] = -1, c.blocks, 1 << 30
+    w = torch.rand((3, 2, c.width * 64), device="cuda")
+    w0 = w.clone()
+    got = attend(c, q, [1, 1, 1], 0.125, faults=1, weights=w)
+    check(c, q, [1, 1, 1], got, 0.125, w0, w)
+    c.table[2] = -1  # no valid block: no positions
+    out, lse = attend(c, q, [1, 1, 1], 0.125, faults=1)
+    assert not out[2].any() and bool((lse[2] == -math.inf).all())
+    # sequences whose cu entries descend or leave the rows are skipped; lengths that leave the table have no positions
+    c = Cache([200, 100, 64], 4, 1, 32, 32, type, seed=9)
+    q = c.queries(4)
+    ws = dsa.grouped_workspace(c.dims(), 4)
+    for cu, live in (([0, 2, 1, 4], {0: (0, 2), 2: (1, 3)}), ([0, 1, 9, 4], {0: (0, 1)}), ([-1, 1, 2, 4], {1: (1, 1), 2: (2, 2)})):
+        out, lse = torch.full((4, 4, 32), 7.0, dtype=ACT[type], device="cuda"), torch.full((4, 4), 7.0, device="cuda")
+        dsa.grouped_attn(c.dims(), q, *c.args(), 0.2, ints(cu), ws=ws, out=out, lse=lse)
+        assert dsa.read_error(ws) == 2, cu
+        touched = torch.zeros(4, dtype=torch.bool)
+        for b, (t0, m) in live.items():
+            touched[t0:t0 + m] = True
+        assert bool((lse[~touched] == 7.0).all()) and not (lse[touched] == 7.0).any()
+    lens = c.seq_lens.clone()
+    for bad in (-1, c.width * 64 + 1, (1 << 31) - 1):
+        c.seq_lens = lens.clone()
+        c.seq_lens[1] = bad
+        out, lse = dsa.grouped_attn(c.dims(), q[:3], *c.args(), 0.2, ws=ws)
+        assert dsa.read_error(ws) == 2 and not out[1].any() and bool((lse[1] == -math.inf).all())
+        c.lens[1] = 0
+        check(c, q, [1, 1, 1], (out, lse), 0.2)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("H,H_kv,new", [(8, 2, [1, 1, 1, 1]), (64, 2, [3, 0, 2, 1]), (130, 1, [2, 1, 5, 1]), (4, 4, [9, 1, 1, 0])])
+def test_weights(type, H, H_kv, new):
+    """Added in place, into another tensor, and to nothing; positions behind a sequence's end stay as they were."""
+    lens = [700, 300, 3, 0]
+    c = Cache(lens, H, H_kv, 32, 48, type, seed=H)
+    q = c.queries(sum(new), 2.0)
+    base = torch.rand((4, H_kv, c.width * 64), device="cuda")
+    w = base.clone()
+    got = attend(c, q, new, 0.2, weights=w)
+    check(c, q, new, got, 0.2, base, w)
+    other = torch.full_like(base, 5.0)
+    got2 = attend(c, q, new, 0.2, weights=base, weights_out=other)
+    assert torch.equal(got[0], got2[0]) and torch.equal(got[1], got2[1])
+    plain = attend(c, q, new, 0.2)
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+    fresh = torch.full_like(base, 5.0)
+    attend(c, q, new, 0.2, weights_out=fresh)
+    check(c, q, new, got, 0.2, None, fresh)
+    for b, n in enumerate(lens):
+        assert torch.equal(other[b, :, :n], w[b, :, :n])
+        assert bool((other[b, :, n:] == 5.0).all()) and torch.equal(w[b, :, n:], base[b, :, n:]) and bool((fresh[b, :, n:] == 5.0).all())
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_repeats_graphs_and_streams(type):
+    """The same bits call after call, from a captured graph with new inputs, from another stream, and from two streams at once."""
+    c = Cache([9000, 64, 700, 0], 16, 2, 128, 128, type, seed=11)
+    q = c.queries(4)
+    w = torch.zeros((4, 2, c.width * 64), device="cuda")
+    ws = dsa.grouped_workspace(c.dims(), 4, weights=True)
+    run = lambda ws=ws, q=q, **kw: dsa.grouped_attn(c.dims(), q, *c.args(), 0.1, weights_out=w if ws is not None else None, ws=ws, **kw)  # noqa: E731
+    ref = run()
+    ref_w = w.clone()
+    for _ in range(3):
+        again = run()
+        assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1]) and torch.equal(w, ref_w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = run(stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], ref[0]) and torch.equal(w, ref_w)
+    out, lse = torch.zeros_like(ref[0]), torch.zeros_like(ref[1])
+    with torch.cuda.stream(side):
+        run(out=out, lse=lse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run(out=out, lse=lse)
+    torch.cuda.synchronize()
+    q.copy_(c.queries(4))
+    c.seq_lens.copy_(ints([8999, 1, 650, 0]))
+    c.lens = [8999, 1, 650, 0]
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, q, [1] * 4, (out, lse), 0.1, None, w)
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [dsa.grouped_workspace(c.dims(), 4) for _ in range(2)]
+    torch.cuda.synchronize()
+    both = [dsa.grouped_attn(c.dims(), q, *c.args(), 0.1, ws=s, stream=st) for _ in range(4) for s, st in zip(spaces, streams)]
+    torch.cuda.synchronize()
+    for o, e in both:
+        assert torch.equal(o, out) and torch.equal(e, lse)
+
+
+def test_a_larger_workspace_serves_smaller_calls():
+    big = Cache([500] * 20, 16, 2, 64, 64, seed=12)
+    ws = dsa.grouped_workspace(big.dims(), 60, weights=True)
+    for B in (20, 3, 1):
+        for m in (1, 3):
+            c = Cache([500] * B, 16, 2, 64, 64, seed=B)
+            q = c.queries(B * m)
+            w = torch.zeros((B, 2, c.width * 64), device="cuda")
+            got = dsa.grouped_attn(c.dims(), q, *c.args(), 0.1, starts([m] * B), weights=w, ws=ws)
+            assert dsa.read_error(ws) == 0
+            check(c, q, [m] * B, got, 0.1, None, w)
+
+
+# ------------------------------------------------------------------------------------------------ append
+
+def expected_append(codes, scale, table, x, first):
+    """The definition, block by block in fp32 on the CPU: rows x [n][H_kv][d] at positions first, first + 1, ... of the sequence
+    whose blocks `table` names."""
+    n, p = x.shape[0], first
+    while p < first + n:
+        blk, lo = int(table[p // 64]), p % 64
+        m = min(64 - lo, first + n - p)
+        rows = x[p - first:p - first + m].float().transpose(0, 1)
+        top = rows.abs().amax(dim=(1, 2)) / 448.0
+        if lo:
+            old = scale[blk]
+            new = torch.maximum(old, top)
+            again = (codes[blk, :, :lo].view(torch.float8_e4m3fn).float() * old[:, None, None] / new[:, None, None])
+            again = again.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            codes[blk, :, :lo] = torch.where((new > old)[:, None, None], again, codes[blk, :, :lo])
+        else:
+            new = torch.where(top > 0, top, 1.0)
+        codes[blk, :, lo:lo + m] = (rows / new[:, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        scale[blk] = new
+        p += m
+
+
+def same(a, b):
+    return torch.equal(a.cpu().nan_to_num(nan=-7.0), b.cpu().nan_to_num(nan=-7.0)) if a.is_floating_point() else torch.equal(a.cpu(), b.cpu())
+
+
+def append_and_check(c, new, spread=1.0, faults=0, strided=False):
+    """Appends new[b] tokens to every sequence and compares all caches with the definition's, and new values with their codes."""
+    T = sum(new)
+    make = lambda d: (spread * torch.randn((T, c.H_kv, d + (32 if strided else 0)), generator=c.g, device="cuda")).to(ACT[c.type])[..., :d]  # noqa: E731
+    k, v = make(c.d_qk), make(c.d_v)
+    want = [t.cpu().clone() for t in (c.k, c.ks, c.v, c.vs)]
+    t0, table = 0, c.table.cpu()
+    for b, m in enumerate(new):
+        expected_append(want[0], want[1], table[b], k[t0:t0 + m].cpu(), c.lens[b])
+        expected_append(want[2], want[3], table[b], v[t0:t0 + m].cpu(), c.lens[b])
+        c.lens[b] += m
+        t0 += m
+    c.seq_lens.copy_(ints(c.lens))
+    ws = dsa.grouped_workspace(c.dims(), T)
+    cu = None if new == [1] * len(c.lens) else starts(new)
+    dsa.grouped_append(c.dims(), k, v, c.table, c.seq_lens, c.k, c.ks, c.v, c.vs, cu, ws=ws)
+    assert dsa.read_error(ws) == faults
+    for got, ref in zip((c.k, c.ks, c.v, c.vs), want):
+        assert same(got, ref)
+    t0 = 0
+    for b, m in enumerate(new):  # half a step of a code's 3 bits, or of its smallest one, and the quotient's and scale's roundings
+        pos = torch.arange(c.lens[b] - m, c.lens[b], device="cuda")
+        blk = c.table[b].long()[pos // 64]
+        for x, codes, scale in ((k, c.k, c.ks), (v, c.v, c.vs)):
+            s = scale[blk].double()[..., None]
+            y, x = value(codes[blk, :, pos % 64]) * s, x[t0:t0 + m].double()
+            assert bool(((y - x).abs() <= torch.maximum(x.abs() * 2.0 ** -4, s * 2.0 ** -10) * (1 + 2.0 ** -20)).all())
+        t0 += m
+    return k, v
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,new", [([0], [1]), ([0, 63, 64, 130], [1, 1, 1, 1]), ([0, 10, 64, 0], [64, 200, 65, 0]), ([5], [1000]),
+                                      ([1, 0, 100], [63, 0, 28])])
+def test_append(type, lens, new):
+    room = [n + m + 1 for n, m in zip(lens, new)]
+    for H_kv, d_qk, d_v in ((2, 128, 128), (3, 16, 80), (1, 256, 192)):
+        c = Cache(lens, 6, H_kv, d_qk, d_v, type, seed=len(new) + d_qk, room=room)
+        append_and_check(c, new, strided=d_qk == 128)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_append_step_by_step(type):
+    """130 decode steps of rising, falling and zero values: scales grow within a block, never shrink, and start anew."""
+    c = Cache([0, 60, 7], 4, 2, 32, 48, type, seed=21, room=[140, 200, 140])
+    for i in range(130):
+        append_and_check(c, [1, 1, 1], spread=[1.0, 0.1, 3.0, 0.0, 0.5, 8.0, 1e-3][i % 7] * 1.01 ** i)
+    append_and_check(c, [0, 2, 0], spread=0.0)
+
+
+def test_append_of_zeros_extremes_and_a_batch_of_many():
+    c = Cache([0, 0], 2, 1, 16, 16, "f32", seed=22, room=[70, 70])
+    append_and_check(c, [65, 3], spread=0.0)
+    assert bool((c.ks[c.table[0, 0].long()] == 1.0).all())
+    c = Cache([0, 40], 2, 1, 16, 16, "f32", seed=23, room=[70, 70])
+    append_and_check(c, [65, 3], spread=1e30)
+    c = Cache([i % 130 for i in range(600)], 2, 2, 16, 16, "bf16", seed=24, room=[140] * 600)
+    append_and_check(c, [1] * 600)
+    append_and_check(c, [i % 3 for i in range(600)])
+
+
+def test_append_faults():
+    c = Cache([10, 20, 30], 4, 2, 32, 32, "bf16", seed=25, room=[80, 80, 80])
+    k, v = (torch.randn((3, 2, 32), device="cuda").bfloat16() for _ in range(2))
+    ws = dsa.grouped_workspace(c.dims(), 8)
+    call = lambda lens, cu=None, table=c.table, k=k, v=v: dsa.grouped_append(c.dims(), k, v, table, ints(lens), c.k, c.ks, c.v, c.vs,  # noqa: E731
+                                                                             None if cu is None else ints(cu), ws=ws)
+    before = [t.clone() for t in (c.k, c.ks, c.v, c.vs)]
+    untouched = lambda: all(same(a, b) for a, b in zip((c.k, c.ks, c.v, c.vs), before))  # noqa: E731
+    call([0, 0, 0], [0, 0, 0, 0], k=k[:0], v=v[:0])
+    assert dsa.read_error(ws) == 0 and untouched()
+    call([11, 21, 31], [0, 0, 4, 3])
+    assert dsa.read_error(ws) == 2 and untouched()
+    call([-1, c.width * 64 + 1, 1 << 30])
+    assert dsa.read_error(ws) == 2 and untouched()
+    bad = c.table.clone()
+    bad[0, 0], bad[1, 0], bad[2, 0] = -1, c.blocks, -(1 << 31)
+    call([11, 21, 31], table=bad)
+    assert dsa.read_error(ws) == 1 and untouched()
+    # more new tokens than positions: the first are skipped
+    call([11, 21, 2], [0, 0, 0, 3])
+    assert dsa.read_error(ws) == 2
+    blk = int(c.table[2, 0])
+    for got, x, scale in ((c.k, k, c.ks), (c.v, v, c.vs)):
+        y = value(got[blk, :, :2]) * scale[blk].double()[:, None, None]
+        assert bool(((y - x[1:].double().transpose(0, 1)).abs() <= 0.07 * x.double().abs().amax()).all())
+    keep = torch.ones(c.blocks, dtype=torch.bool, device="cuda")
+    keep[blk] = False
+    assert all(same(a[keep], b[keep]) for a, b in zip((c.k, c.ks, c.v, c.vs), before))
+
+
+# ------------------------------------------------------------------------------------------------ eviction
+
+def expected_kept(w, n, keep, sink, recent):
+    """Ascending positions of one sequence and head (a list)."""
+    if n <= keep:
+        return list(range(n))
+    w = [(-math.inf if x != x else x) for x in w[:n].tolist()]
+    rest = sorted(range(sink, n - recent), key=lambda i: (-w[i], i))[:keep - sink - recent]
+    return sorted(list(range(sink)) + list(range(n - recent, n)) + rest)
+
+
+def evict_and_check(c, w, keep, sink, recent, faults=0, new_table=None, extra=0):
+    B, blocks = len(c.lens), (keep + 63) // 64 + extra
+    if new_table is None:  # new blocks behind the old ones
+        more = B * blocks
+        new_table = (c.blocks + torch.randperm(more, generator=c.g, device="cuda")).to(torch.int32).view(B, blocks)
+        for name, fill in (("k", NAN_CODE), ("v", NAN_CODE), ("ks", float("nan")), ("vs", float("nan"))):
+            t = getattr(c, name)
+            setattr(c, name, torch.cat([t, torch.full((more,) + t.shape[1:], fill, dtype=t.dtype, device="cuda")]))
+        c.blocks += more
+    want = [t.cpu().clone() for t in (c.k, c.ks, c.v, c.vs)]
+    table, to, w_cpu = c.table.cpu(), new_table.cpu(), w.cpu()
+    ws = dsa.grouped_workspace(c.dims(), B)
+    kept, lens, w_out = dsa.grouped_evict(c.dims(), w, keep, c.table, c.seq_lens, new_table, c.k, c.ks, c.v, c.vs, sink=sink, recent=recent, ws=ws)
+    assert dsa.read_error(ws) == faults
+    assert lens.tolist() == [min(n, keep) for n in c.lens]
+    kept, w_out = kept.cpu(), w_out.cpu()
+    for b, n in enumerate(c.lens):
+        m = min(n, keep)
+        for h in range(c.H_kv):
+            at = expected_kept(w_cpu[b, h], n, keep, sink, recent)
+            assert kept[b, h].tolist() == at + [-1] * (keep - m)
+            assert same(w_out[b, h, :m], w_cpu[b, h, at]) and not w_out[b, h, m:].any()
+            for codes, scale in ((want[0], want[1]), (want[2], want[3])):
+                for j in range(0, m, 64):
+                    i = torch.tensor(at[j:j + 64])
+                    old, dst = table[b].long()[i // 64], int(to[b, j // 64])
+                    ok = (old >= 0) & (old < c.blocks)
+                    if not 0 <= dst < c.blocks:
+                        continue
+                    src = codes[old.clamp(0, c.blocks - 1), h, i % 64]
+                    s = scale[old.clamp(0, c.blocks - 1), h]
+                    if n > keep:
+                        x = src.view(torch.float8_e4m3fn).float() * s[:, None]
+                        top = x[ok].abs().max() / 448.0 if ok.any() else torch.tensor(0.0)
+                        new = top if top > 0 else torch.tensor(1.0)
+                        src = (x / new).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                        scale[dst, h] = new
+                    elif ok[0]:
+                        scale[dst, h] = s[0]
+                    codes[dst, h, :len(i)][ok] = src[ok]
+    for got, ref in zip((c.k, c.ks, c.v, c.vs), want):
+        assert same(got, ref)
+    c.table, c.width, c.lens, c.seq_lens = new_table, new_table.shape[1], lens.tolist(), lens
+    return kept, w_out.cuda()
+
+
+@pytest.mark.parametrize("keep,sink,recent", [(1, 0, 0), (64, 4, 10), (100, 0, 100), (129, 129, 0), (300, 1, 37), (300, 150, 150), (700, 3, 0)])
+def test_evict(keep, sink, recent):
+    for H_kv, d_qk, d_v in ((2, 128, 128), (3, 16, 80), (1, 256, 192)):
+        c = Cache([700, 1, 0, 300, 301, 64, 1500], 6, H_kv, d_qk, d_v, seed=keep + d_qk)
+        w = torch.randn((7, H_kv, c.width * 64), generator=c.g, device="cuda").mul_(2).exp_()
+        evict_and_check(c, w, keep, sink, recent, extra=keep % 2)
+
+
+def test_evict_ties_and_special_weights():
+    c = Cache([500] * 6, 2, 1, 16, 16, seed=31)
+    w = torch.zeros((6, 1, c.width * 64), device="cuda")
+    w[1] = torch.arange(w.shape[2], device="cuda") % 3
+    w[2] = -1.0
+    w[2, 0, ::5] = -0.0
+    w[2, 0, 1::5] = 0.0
+    w[3] = float("nan")
+    w[3, 0, ::7] = -math.inf
+    w[3, 0, 3::50] = math.inf
+    w[4] = torch.rand_like(w[4]) * 1e-42  # subnormal
+    w[5] = 1.0 + torch.randint(0, 4, w[5].shape, device="cuda") * 2.0 ** -23
+    for keep in (100, 250, 499):
+        evict_and_check(Cache([500] * 6, 2, 1, 16, 16, seed=31), w, keep, 5, 20)
+
+
+def test_evict_long_sequences():
+    c = Cache([70000, 20000], 2, 1, 16, 16, seed=32)
+    w = torch.randn((2, 1, c.width * 64), generator=c.g, device="cuda").exp_()
+    evict_and_check(c, w, 33000, 16, 500)
+
+
+def test_evict_in_place_and_faults():
+    """A sequence that is not cut may keep its blocks; rows from and into invalid blocks are skipped."""
+    c = Cache([100, 400, 64], 4, 2, 32, 32, seed=33, room=[100, 900, 64])
+    w = torch.rand((3, 2, c.width * 64), generator=c.g, device="cuda")
+    to = c.table[:, :4].clone()
+    to[1] = c.table[1, 7:11]
+    evict_and_check(c, w, 200, 2, 8, new_table=to)
+    c = Cache([100, 400, 300], 4, 2, 32, 32, seed=34, room=[100, 900, 900])
+    w = torch.rand((3, 2, c.width * 64), generator=c.g, device="cuda")
+    c.table[1, 2], c.table[0, 1] = -1, c.blocks
+    to = c.table[:, 7:11].clone()
+    to[0], to[2, 1] = c.free[:1].expand(4), 1 << 20
+    to[0, 0] = c.free[1]
+    evict_and_check(c, w, 200, 2, 8, new_table=to, faults=1)
+    c = Cache([100, 400, 64], 4, 2, 32, 32, seed=35, room=[100, 900, 64])
+    c.seq_lens = ints([100, -5, c.width * 64 + 1])
+    c.lens = [100, 0, 0]
+    evict_and_check(c, torch.rand((3, 2, c.width * 64), device="cuda"), 200, 2, 8, faults=2)
+
+
+# ------------------------------------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_decode_loop_with_eviction(type):
+    """A prompt appended, decode steps that append, attend and count weights, an eviction, and further steps on what is left,
+    with drafts that are dropped again by a shorter length."""
+    H, H_kv, d = 8, 2, 64
+    lens = [150, 70, 0]
+    c = Cache([0, 0, 0], H, H_kv, d, d, type, seed=41, room=[400, 400, 400])
+    append_and_check(c, lens)
+    w = torch.zeros((3, H_kv, c.width * 64), device="cuda")
+
+    def step(new):
+        nonlocal w
+        append_and_check(c, new)
+        q = c.queries(sum(new), 2.0)
+        before = w.clone()
+        check(c, q, new, attend(c, q, new, d ** -0.5, weights=w), d ** -0.5, before, w)
+
+    for i in range(5):
+        step([1, 1, 1])
+    step([4, 2, 3])
+    c.lens = [n - m for n, m in zip(c.lens, [2, 0, 3])]  # rejected drafts
+    c.seq_lens = ints(c.lens)
+    step([1, 1, 1])
+    blocks = 3
+    new_table = c.table[:, -1 - blocks:-1].clone()
+    _, w = evict_and_check(c, w, 80, 4, 16, new_table=new_table)
+    assert max(c.lens) == 80
+    for i in range(3):
+        step([1, 1, 1])
+    step([5, 1, 2])

@@ -1,0 +1,152 @@
+"""Refusals of the grouped-head calls, before anything is launched (no GPU needed)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import indexer_top_sparse_paged_gb300 as dsa
+from indexer_top_sparse_paged_gb300.build import build_library
+
+FAKE = ctypes.c_void_p(1 << 20)  # never dereferenced: every call below fails its checks first
+FAKE2 = ctypes.c_void_p(1 << 21)
+ODD = ctypes.c_void_p((1 << 20) + 4)
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_library()
+    return dsa.lib()
+
+
+def _dims(**kw):
+    d = dict(type="bf16", B=2, max_blocks=4, num_blocks=8, H=8, H_kv=2, d_qk=128, d_v=128, block_size=64)
+    d.update(kw)
+    return dsa.grouped_dims(**d)
+
+
+def _raw(**kw):
+    d = _dims()
+    for n, v in kw.items():
+        setattr(d, n, v)
+    return d
+
+
+BAD_DIMS = [(dict(type=2), 2), (dict(type=-1), 2), (dict(block_size=32), 2), (dict(B=0), 1), (dict(max_blocks=0), 1), (dict(num_blocks=0), 1),
+            (dict(H=0), 1), (dict(H_kv=0), 1), (dict(H=7), 1), (dict(d_qk=0), 1), (dict(d_v=-16), 1), (dict(d_qk=272), 2), (dict(d_v=264), 2),
+            (dict(d_qk=72), 2), (dict(d_v=8), 2), (dict(num_blocks=1 << 25), 2), (dict(max_blocks=1 << 25), 2),
+            (dict(H=40000, H_kv=40000, num_blocks=1), 2)]
+
+
+def test_dims(L):
+    size = lambda d, T=2, w=0: L.dsa_grouped_workspace_size(ctypes.byref(d), T, w)  # noqa: E731
+    assert L.dsa_grouped_workspace_size(None, 2, 0) == 0 and size(_dims(), -1) == 0 and size(_dims(), 1 << 29) == 0
+    assert 0 < size(_dims()) < size(_dims(), 2, 1)
+    assert size(_dims(), 4) >= size(_dims(), 2) and size(_dims(), 4, 1) >= size(_dims(), 2, 1)
+    for kw, st in BAD_DIMS:
+        d = _raw(**kw)
+        assert size(d) == 0, kw
+        assert _append(L, d) == st and _attn(L, d) == st and _evict(L, d) == st, kw
+    with pytest.raises(ValueError, match="type"):
+        _dims(type="fp16")
+
+
+def _append(L, dims=None, k=FAKE, ks=(256, 128), v=FAKE, vs=(256, 128), table=FAKE, lens=FAKE, cu=None, T=2, kc=FAKE, sc=FAKE, vc=FAKE,
+            vsc=FAKE, ws=FAKE, nbytes=BIG):
+    return L.dsa_grouped_append(dims or _dims(), k, *ks, v, *vs, table, lens, cu, T, kc, sc, vc, vsc, ws, nbytes, None)
+
+
+def test_append_refusals(L):
+    assert _append(L, cu=FAKE, T=0) == 0 and L.dsa_last_launch_count() == 0
+    for name in ("k", "v", "table", "lens", "kc", "sc", "vc", "vsc"):
+        assert _append(L, **{name: None}) == 1, name
+    for name in ("k", "v", "kc", "vc"):
+        assert _append(L, **{name: ODD}) == 1, name
+    for bad in ((-256, 128), (256, -128), (257, 128), (256, 4), (1 << 40, 128)):
+        assert _append(L, ks=bad) == 1 and _append(L, vs=bad) == 1, bad
+    assert _append(L, T=3) == 1 and _append(L, T=-1, cu=FAKE) == 1
+    assert _append(L, ws=None) == 3 and _append(L, ws=ODD) == 3 and _append(L, nbytes=255) == 3
+    assert L.dsa_grouped_append(None, FAKE, 256, 128, FAKE, 256, 128, FAKE, FAKE, None, 2, FAKE, FAKE, FAKE, FAKE, FAKE, BIG, None) == 1
+
+
+def _attn(L, dims=None, q=FAKE, qs=(1024, 128), kc=FAKE, sc=FAKE, vc=FAKE, vsc=FAKE, table=FAKE, lens=FAKE, cu=None, T=2, scale=0.1, out=FAKE,
+          lse=None, w=None, wo=None, ws=FAKE, nbytes=BIG):
+    return L.dsa_grouped_attn(dims or _dims(), q, *qs, kc, sc, vc, vsc, table, lens, cu, T, scale, out, lse, w, wo, ws, nbytes, None)
+
+
+def test_attn_refusals(L):
+    assert _attn(L, cu=FAKE, T=0) == 0 and L.dsa_last_launch_count() == 0
+    for name in ("q", "kc", "sc", "vc", "vsc", "table", "lens", "out"):
+        assert _attn(L, **{name: None}) == 1, name
+    for name in ("q", "kc", "vc", "out"):
+        assert _attn(L, **{name: ODD}) == 1, name
+    for bad in ((-1024, 128), (1024, -128), (1025, 128), (1024, 4), (1 << 40, 128)):
+        assert _attn(L, qs=bad) == 1, bad
+    for s in (0.0, -1.0, math.nan, math.inf):
+        assert _attn(L, scale=s) == 1
+    assert _attn(L, T=3) == 1 and _attn(L, T=-1, cu=FAKE) == 1 and _attn(L, T=1 << 29, cu=FAKE) == 2
+    assert _attn(L, w=FAKE) == 1  # weights to add to, and nowhere to write them
+    d = _dims()
+    for w in (None, FAKE2):
+        need = L.dsa_grouped_workspace_size(d, 2, w is not None)
+        assert _attn(L, ws=None, wo=w) == 3 and _attn(L, ws=ODD, wo=w) == 3 and _attn(L, nbytes=need - 1, wo=w) == 3
+
+
+def _evict(L, dims=None, w=FAKE, keep=100, sink=4, recent=10, table=FAKE, lens=FAKE, new=FAKE, blocks=2, kc=FAKE, sc=FAKE, vc=FAKE, vsc=FAKE,
+           kept=FAKE, new_lens=FAKE2, wo=FAKE2, ws=FAKE, nbytes=BIG):
+    return L.dsa_grouped_evict(dims or _dims(), w, keep, sink, recent, table, lens, new, blocks, kc, sc, vc, vsc, kept, new_lens, wo, ws, nbytes,
+                               None)
+
+
+def test_evict_refusals(L):
+    for name in ("w", "table", "lens", "new", "kc", "sc", "vc", "vsc", "kept", "new_lens", "wo"):
+        assert _evict(L, **{name: None}) == 1, name
+    assert _evict(L, kc=ODD) == 1 and _evict(L, vc=ODD) == 1
+    assert _evict(L, keep=0) == 1 and _evict(L, keep=129) == 1 and _evict(L, sink=-1) == 1 and _evict(L, recent=-1) == 1
+    assert _evict(L, sink=50, recent=51) == 1 and _evict(L, sink=(1 << 31) - 1, recent=(1 << 31) - 1) == 1
+    assert _evict(L, blocks=0) == 1 and _evict(L, blocks=1 << 25) == 2
+    assert _evict(L, wo=FAKE) == 1 and _evict(L, new_lens=FAKE) == 1  # in place
+    assert _evict(L, ws=None) == 3 and _evict(L, ws=ODD) == 3 and _evict(L, nbytes=0) == 3
+    assert _evict(L, _dims(B=1 << 20, H=1 << 10, H_kv=1 << 10, num_blocks=1), keep=128) == 2
+    assert L.dsa_last_launch_count() == 0
+
+
+def test_binding_refusals(L):
+    """Host tensors, wrong types, shapes and sizes, and tensors that record gradients are refused in Python."""
+    d = _dims()
+    q, kv = torch.zeros((2, 8, 128), dtype=torch.bfloat16), torch.zeros((2, 2, 128), dtype=torch.bfloat16)
+    cache, sc = torch.zeros((8, 2, 64, 128), dtype=torch.uint8), torch.zeros((8, 2))
+    table, lens, ws = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1024, dtype=torch.uint8)
+    w = torch.zeros((2, 2, 256))
+    calls = [lambda q=q, kv=kv, w=w, c=cache: dsa.grouped_attn(d, q, c, sc, c, sc, table, lens, 0.1, weights=w, ws=ws),
+             lambda q=q, kv=kv, w=w, c=cache: dsa.grouped_append(d, kv, kv, table, lens, c, sc, c, sc, ws=ws),
+             lambda q=q, kv=kv, w=w, c=cache: dsa.grouped_evict(d, w, 64, table, lens, table, c, sc, c, sc, ws=ws)]
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    grad = dict(q=q.clone().requires_grad_(), kv=kv.clone().requires_grad_(), w=w.clone().requires_grad_())
+    for call, name in zip(calls, ("q", "kv", "w")):
+        with pytest.raises(ValueError, match="gradient"):
+            call(**{name: grad[name]})
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call(**{name: grad[name]})
+    rows = lambda x, T=2, h=8, n=128, dims=d: dsa._grouped_rows(x, T, h, n, dims, "q")  # noqa: E731
+    assert rows(q) == (q.data_ptr(), 1024, 128)
+    for bad in (q.float(), q[:1], q[:, :4], q[..., :64], q[0]):
+        with pytest.raises(ValueError, match="q must"):
+            rows(bad)
+    with pytest.raises(ValueError, match="dense"):
+        rows(torch.zeros((2, 8, 256), dtype=torch.bfloat16)[..., ::2])
+    check = lambda **kw: dsa._grouped_caches(d, **{**dict(k_cache=cache, k_scale=sc, v_cache=cache, v_scale=sc, block_table=table,  # noqa: E731
+                                                          seq_lens=lens, cu=None, T=2), **kw})
+    check()
+    for kw, what in ((dict(k_cache=cache[:7]), "k_cache"), (dict(v_cache=cache.int()), "v_cache"), (dict(k_scale=sc[:7]), "k_scale"),
+                     (dict(v_scale=sc.double()), "v_scale"), (dict(block_table=table[:1]), "block_table"), (dict(seq_lens=lens.long()), "seq_lens"),
+                     (dict(cu=lens), "cu"), (dict(T=3), "one row")):
+        with pytest.raises(ValueError, match=what):
+            check(**kw)
+    with pytest.raises(ValueError, match="new_table"):
+        dsa.grouped_evict(d, w, 64, table, lens, table[:1], cache, sc, cache, sc, ws=ws)
+    with pytest.raises(ValueError, match="dims"):
+        dsa.grouped_workspace(_raw(H=7), 2)
