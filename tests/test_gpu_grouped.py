@@ -95,11 +95,12 @@ def check(c, q, new, got, scale, weights=None, weights_out=None):
                     assert not o_got.any() and bool((e_got == -math.inf).all())
                     continue
                 p = torch.exp(z - e[:, None])
-                # A logit: the products and their fp32 sum round d + 2 times, the query's small elements keep an absolute
-                # error of 2^-22 of its largest (bf16 queries are split into two 4-bit significands, fp32 ones into six:
-                # both below that), and the factor to powers of two and the subtraction round twice more.
+                # A logit: the products and their fp32 sum round d + 2 times, and the factor to powers of two and the
+                # subtraction twice more. A bf16 query is split into two e4m3 parts, the second in units of 1/16: elements that
+                # are normal in the first part are exact (8 bits), smaller ones are off by half a step of the second, 2^-10 / 16,
+                # where the largest element stands above 224: 2^-14 / 224 < 2^-21 of it. fp32 ones, in six parts: less.
                 ka = k.abs()
-                z_tol = ((c.d_qk + 4) * u * (Q.abs() @ ka.T) + 2.0 ** -22 * Q.abs().amax(-1, keepdim=True) * ka.sum(-1)) * scale
+                z_tol = ((c.d_qk + 4) * u * (Q.abs() @ ka.T) + 2.0 ** -21 * Q.abs().amax(-1, keepdim=True) * ka.sum(-1)) * scale
                 z_tol = torch.where(seen, z_tol, 0.0).amax(-1) + 2.0 ** -22 * (1 + z[:, seen].abs().amax(-1))
                 # A weight: twice that, 2^-22 of the exponential, in bf16 2^-10 for its fp16 value and the parts of 4 bits it is
                 # split into (2^-11 each), and 2^-26 of the largest weight absolutely; sums add one rounding a position.
