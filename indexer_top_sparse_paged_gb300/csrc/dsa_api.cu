@@ -470,6 +470,9 @@ static bool rope_layout_ok(int layout) { return layout == DSA_ROPE_INTERLEAVED |
 // grouped-head cache: checks and workspace
 // ------------------------------------------------------------------------------------------------
 
+// Positions are counted in 32 bits, with room to round up to tiles.
+constexpr int64_t kGroupedPositions = (1ll << 31) - (1 << 16);
+
 static dsa_status check_grouped_dims(const dsa_grouped_dims* d) {
     if (!d) return DSA_ERR_INVALID_ARG;
     if ((d->type != DSA_F32 && d->type != DSA_BF16) || d->block_size != kBlock) return DSA_ERR_UNSUPPORTED;
@@ -479,7 +482,7 @@ static dsa_status check_grouped_dims(const dsa_grouped_dims* d) {
     if (d->d_qk > 256 || d->d_v > 256 || d->d_qk % 16 || d->d_v % 16) return DSA_ERR_UNSUPPORTED;
     // rows of the caches (the tensor maps count them in 32 bits), positions, and the grids
     if (static_cast<int64_t>(d->num_blocks) * d->H_kv * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(d->max_blocks) * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(d->max_blocks) * kBlock > kGroupedPositions) return DSA_ERR_UNSUPPORTED;
     if (d->H_kv > 32767 || static_cast<int64_t>(d->B) * d->H_kv >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
     return DSA_OK;
 }
@@ -494,7 +497,7 @@ static bool ws_ok(const void* ws, size_t ws_bytes, size_t need) {
 }
 
 struct GroupedLayout {
-    size_t part_ml, part_o, row_lse, z, total;
+    size_t cuts, part_ml, part_o, row_lse, z, total;
     int row_tile, ctas;
     int64_t max_tiles;
 };
@@ -509,6 +512,8 @@ static GroupedLayout grouped_layout(const dsa_grouped_dims& d, int T, bool weigh
     w.max_tiles = (T * G / w.row_tile + d.B) * d.H_kv * ((d.max_blocks + 1) / 2);
     size_t off = 256;  // the error word
     const size_t slot_rows = static_cast<size_t>(2) * w.ctas * w.row_tile;
+    w.cuts = off;
+    off = align256(off + sizeof(GroupedCut) * w.ctas);
     w.part_ml = off;
     off = align256(off + sizeof(float2) * slot_rows);
     w.part_o = off;
@@ -1025,6 +1030,7 @@ dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t
         a.err = reinterpret_cast<int*>(base);
         a.row_tile = L.row_tile;
         a.ctas = L.ctas;
+        a.cuts = reinterpret_cast<GroupedCut*>(base + L.cuts);
         a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
         a.part_o = reinterpret_cast<float*>(base + L.part_o);
         a.row_lse = reinterpret_cast<float*>(base + L.row_lse);
@@ -1045,7 +1051,7 @@ dsa_status dsa_grouped_evict(const dsa_grouped_dims* dims, const float* weights,
     if (st != DSA_OK) return st;
     if (keep <= 0 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > keep || new_max_blocks <= 0)
         return DSA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(new_max_blocks) * kBlock >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(new_max_blocks) * kBlock > kGroupedPositions) return DSA_ERR_UNSUPPORTED;
     if (keep > new_max_blocks * kBlock) return DSA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(dims->B) * dims->H_kv * ((keep + kBlock - 1) / kBlock) >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
     if (!weights || !block_table || !seq_lens || !new_table || !k_cache || !k_scale || !v_cache || !v_scale || !kept ||

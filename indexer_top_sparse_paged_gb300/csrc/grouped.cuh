@@ -73,36 +73,41 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* total, int64
     return before + y - x;
 }
 
-struct GroupedShare {
-    int64_t total;  // tiles of the call
-    int64_t per;    // tiles of a CTA
-    int b;          // the sequence that holds the share's first tile
-    int64_t base;   // the first tile of that sequence
-};
-
-// The sequence that holds unit `at` of the line that count(b) units of every sequence b make, and the first unit of that
-// sequence; at < 0 or past the end: only the total. All threads of the block call it, with the same `at`.
-template <int kThreads, typename Count>
-__device__ __forceinline__ void find_sequence(int B, int64_t at, Count count, int64_t* total, int* b_out, int64_t* base_out,
+// The total of count(b) over all sequences b, and, with at = where(total), the sequence whose units hold unit `at` of their
+// line, and the first unit of that sequence (b -1: there is none). All threads of the block call it.
+template <int kThreads, typename Count, typename Where>
+__device__ __forceinline__ int64_t find_place(int B, Count count, Where where, int64_t* total, int* b_out, int64_t* base_out,
                                               int64_t* warp_sums, int64_t* found) {
-    int64_t sum = 0;
     if (threadIdx.x == 0) found[0] = -1;
+    int64_t sum = 0, n = 0, before = 0, at = 0;
+    const bool once = B <= kThreads;  // a thread's sequence stays in registers
     for (int b0 = 0; b0 < B; b0 += kThreads) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        const int64_t n = b < B ? count(b) : 0;
+        n = b < B ? count(b) : 0;
         int64_t all;
-        const int64_t before = sum + block_prefix<kThreads>(n, &all, warp_sums);
+        before = block_prefix<kThreads>(n, &all, warp_sums);
+        sum += all;
+    }
+    at = where(sum);
+    int64_t done = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        int64_t all = 0;
+        if (!once) {
+            n = b < B ? count(b) : 0;
+            before = done + block_prefix<kThreads>(n, &all, warp_sums);
+        }
         if (at >= before && at < before + n) {
             found[0] = b;
             found[1] = before;
         }
-        sum += all;
+        done += all;
     }
     __syncthreads();
     *total = sum;
     *b_out = static_cast<int>(found[0]);
     *base_out = found[1];
-    __syncthreads();
+    return at;
 }
 
 // Slot of the partial that CTA c leaves of an item: its share's first item, if that is cut, uses slot 2c, and the last
@@ -129,10 +134,41 @@ __device__ __forceinline__ void e4m3x16_values(const uint4& in, float (&x)[16]) 
     }
 }
 
+// The scale that takes amax to the largest code.
+__device__ __forceinline__ float unit_scale(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
+
+// Division by one value many times, correctly rounded, in three operations: with r = 1 / s correctly rounded and q = x r,
+// q + r (x - q s) is x / s correctly rounded (Markstein's theorem), where nothing underflows or overflows. Scales outside
+// [2^-80, 2^80] divide as usual. (A dividend so small that its remainder underflows has a quotient far below the smallest
+// code's half, and becomes the code 0 either way.)
+struct Divisor {
+    float value, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float s)
+        : value(s), r(1.0f / s), plain(!(s >= 8.271806125530277e-25f && s <= 1.2089258196146292e24f)) {}
+    __device__ __forceinline__ float operator()(float x) const {
+        const float q = x * r, y = fmaf(r, fmaf(-q, value, x), q);
+        return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // (-0 / s comes out as +0)
+    }
+};
+
 __device__ __forceinline__ uint32_t e4m3x4_codes(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
+}
+
+// RNE_e4m3(x / scale) of 16 values, saturating at +-448.
+__device__ __forceinline__ uint4 codes16(float (&x)[16], const Divisor& scale) {
+    if (scale.plain) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] /= scale.value;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = scale(x[i]);
+    }
+    return make_uint4(e4m3x4_codes(x[0], x[1], x[2], x[3]), e4m3x4_codes(x[4], x[5], x[6], x[7]),
+                      e4m3x4_codes(x[8], x[9], x[10], x[11]), e4m3x4_codes(x[12], x[13], x[14], x[15]));
 }
 
 }  // namespace dsa

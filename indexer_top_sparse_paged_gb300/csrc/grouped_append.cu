@@ -30,13 +30,6 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
     }
 }
 
-__device__ __forceinline__ uint4 codes16(const float (&x)[16], float scale) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3x4_codes(x[4 * i] / scale, x[4 * i + 1] / scale, x[4 * i + 2] / scale, x[4 * i + 3] / scale);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 struct AppendSeq {
     int row0, n;       // the sequence's new rows
     int first;         // position of the first one that is written
@@ -73,8 +66,9 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
     const bool value = blockIdx.y & 1;
     int64_t total, base;
     int b;
-    find_sequence<kGroupedAppendThreads>(a.B, blockIdx.x, [&](int i) { return static_cast<int64_t>(append_seq(a, i, blockIdx.x == 0 && blockIdx.y == 0).blocks); },
-                                         &total, &b, &base, warp_sums, found);
+    find_place<kGroupedAppendThreads>(
+        a.B, [&](int i) { return static_cast<int64_t>(append_seq(a, i, blockIdx.x == 0 && blockIdx.y == 0).blocks); },
+        [](int64_t) { return static_cast<int64_t>(blockIdx.x); }, &total, &b, &base, warp_sums, found);
     if (b < 0) return;
     const AppendSeq s = append_seq(a, b, false);
     const int lb = s.first / kBlock + static_cast<int>(blockIdx.x - base);
@@ -104,13 +98,13 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kGroupedAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    const float scale = slot0 ? fmaxf(old, amax / 448.0f) : amax > 0.0f ? amax / 448.0f : 1.0f;
+    const Divisor scale(slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax));
     for (int i = tid; i < n; i += kGroupedAppendThreads) {
         float y[16];
         load16(x + (i / groups) * st + (i % groups) * 16, y);
         codes[slot0 * groups + i] = codes16(y, scale);
     }
-    if (slot0 && scale > old) {
+    if (slot0 && scale.value > old) {
         for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) {
             float y[16];
             e4m3x16_values(codes[i], y);
@@ -119,7 +113,7 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
             codes[i] = codes16(y, scale);
         }
     }
-    if (tid == 0) *scale_at = scale;
+    if (tid == 0) *scale_at = scale.value;
 }
 
 bool launch_grouped_append(const GroupedAppendArgs& a, cudaStream_t s, int* launches) {

@@ -1,100 +1,202 @@
 // Eviction from the grouped-head cache by accumulated attention weight: one kernel selects the positions that every
 // sequence and key head keeps, a second one moves their rows into the new blocks.
 //
-// The selection finds the weight of the last kept position by its bits, eight at a time from the top (a histogram of the
-// positions that agree so far), and then writes the kept positions in order: all above it, and of those equal to it the
-// first ones.
+// Selection: a cluster of CTAs for each (sequence, head), each with a run of its positions. The weight of the last kept
+// position is found by its bits, eleven at a time from the top: every CTA counts the positions that agree so far in a
+// histogram of the next bits, reads the others' through distributed shared memory, and all find the same bin. Keys stay
+// in shared memory from the first pass on, as far as they fit (else they are read again). Then every warp counts what it
+// keeps of its run -- all above the last weight, and of those equal to it the first ones -- and writes it in order.
+// Latency bounds it (five cluster barriers): 128K positions for each of 8 heads take FIXME us, 8 x 8 heads of 16K FIXME.
+//
+// Move: a CTA for each (new block, sequence and head), keys and values together since they share the chain kept position
+// -> block -> row. A thread keeps its 16-byte pieces in registers between the largest magnitude (of the codes' 7 low
+// bits, which order as the values do) and the rounding against the new scale.
 #include "grouped.cuh"
 
 namespace dsa {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectBins = 2048;
+constexpr int kSelectMaxCluster = 8;
+constexpr int kSelectKeys = 49152;  // keys that shared memory holds, beside the histograms
 constexpr int kMoveThreads = 256;
 
 // Order of the weights as unsigned integers; NaN is the lowest, together with -infinity.
 __device__ __forceinline__ uint32_t weight_key(float w) { return ordered_bits(w != w ? -INFINITY : w); }
 
-__global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedEvictArgs a) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t chosen, left;
-    __shared__ int64_t warp_sums[kSelectThreads / 32];
-    const int tid = threadIdx.x, b = blockIdx.x / a.H_kv, h = blockIdx.x - b * a.H_kv;
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+struct SelectShared {
+    uint32_t hist[3][kSelectBins];
+    uint32_t counts[2];             // of this CTA's run: kept above the last weight (or by place), equal to it
+    uint32_t warp_counts[kSelectWarps][2];
+    uint32_t warp_sums[kSelectWarps];
+    uint32_t bin, need;
+};
+
+// The bin (from the top) that holds the `need`-th position of the cluster's histograms, and the rank within it.
+__device__ __forceinline__ void find_bin(SelectShared& S, int pass, int ctas, uint32_t need) {
+    constexpr int kPer = kSelectBins / kSelectThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = kSelectBins - kPer * (tid + 1);  // thread 0 has the top bins
+    uint32_t n[kPer] = {};
+    for (int c = 0; c < ctas; ++c) {
+        const uint32_t at = mapa_shared(smem_u32(&S.hist[pass][first]), c);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n[i] += ld_cluster_u32(at + 4 * i);
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) mine += n[i];
+    uint32_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) S.warp_sums[warp] = x;
+    __syncthreads();
+    uint32_t before = x - mine;
+    for (int w = 0; w < warp; ++w) before += S.warp_sums[w];
+    if (before < need && need <= before + mine) {
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i) {
+            if (before < need && need <= before + n[i]) {
+                S.bin = first + i;
+                S.need = need - before;
+            }
+            before += n[i];
+        }
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedEvictArgs a, int ctas, int cached) {
+    extern __shared__ uint32_t keys[];  // [cached]
+    __shared__ SelectShared S;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int bh = blockIdx.x / ctas, rank = blockIdx.x - bh * ctas, b = bh / a.H_kv;
     griddep_launch_dependents();
     int n = a.seq_lens[b];
     if (n < 0 || n > a.max_blocks * kBlock) {
         if (tid == 0) atomicOr(a.err, DSA_FAULT_INDEX);
         n = 0;
     }
-    const int64_t bh = blockIdx.x;
-    const float* w = a.weights + bh * a.max_blocks * kBlock;
-    int32_t* kept = a.kept + bh * a.keep;
-    float* out = a.weights_out + bh * a.new_max_blocks * kBlock;
-    const int m = min(n, a.keep);
-    if (h == 0 && tid == 0) a.new_lens[b] = m;
-    for (int i = m + tid; i < a.keep; i += kSelectThreads) kept[i] = -1;
-    for (int i = m + tid; i < a.new_max_blocks * kBlock; i += kSelectThreads) out[i] = 0.0f;
-    if (n <= a.keep) {
-        for (int i = tid; i < n; i += kSelectThreads) {
+    const float* w = a.weights + static_cast<int64_t>(bh) * a.max_blocks * kBlock;
+    int32_t* kept = a.kept + static_cast<int64_t>(bh) * a.keep;
+    float* out = a.weights_out + static_cast<int64_t>(bh) * a.new_max_blocks * kBlock;
+    const int m = min(n, a.keep), all = tid + rank * kSelectThreads, step = ctas * kSelectThreads;
+    if (bh - b * a.H_kv == 0 && rank == 0 && tid == 0) a.new_lens[b] = m;
+    for (int i = m + all; i < a.keep; i += step) kept[i] = -1;
+    for (int64_t i = m + all; i < static_cast<int64_t>(a.new_max_blocks) * kBlock; i += step) out[i] = 0.0f;
+    if (n <= a.keep) {  // (for all CTAs of the cluster)
+        for (int i = all; i < n; i += step) {
             kept[i] = i;
             out[i] = w[i];
         }
         return;
     }
-    const int lo = a.sink, hi = n - a.recent, want = a.keep - a.sink - a.recent;  // `want` of the positions lo .. hi - 1
-    uint32_t prefix = 0;
-    if (tid == 0) left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    // this CTA's run [r0, r1), each warp's a part of it in whole 32s
+    const int run = ((n + ctas - 1) / ctas + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+    const int r0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * run)), r1 = min(n, r0 + run);
+    const int lo = a.sink, hi = n - a.recent;  // the positions to choose from
+    const uint32_t want = a.keep - a.sink - a.recent;
+    auto key_at = [&](int i) { return i - r0 < cached ? keys[i - r0] : weight_key(w[i]); };
+    uint32_t prefix = 0, need = want;
+    if (want > 0) {
+        for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) S.hist[0][i] = 0;
         __syncthreads();
-        for (int i = lo + tid; i < hi; i += kSelectThreads) {
+#pragma unroll 4
+        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
             const uint32_t k = weight_key(w[i]);
-            if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+            if (i - r0 < cached) keys[i - r0] = k;
+            if (i >= lo && i < hi) atomicAdd(&S.hist[0][k >> 21], 1u);
         }
-        __syncthreads();
-        if (tid == 0) {
-            uint32_t need = left, bin = 255;
-            while (bin > 0 && hist[bin] < need) need -= hist[bin--];
-            left = need;
-            chosen = bin;
+        cluster_sync_all();
+        find_bin(S, 0, ctas, need);
+        prefix = S.bin, need = S.need;
+        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
+            const uint32_t k = key_at(i);
+            if (k >> 21 == prefix && i >= lo && i < hi) atomicAdd(&S.hist[1][(k >> 10) & 2047], 1u);
         }
-        __syncthreads();
-        prefix = prefix << 8 | chosen;
+        cluster_sync_all();
+        find_bin(S, 1, ctas, need);
+        prefix = prefix << 11 | S.bin, need = S.need;
+        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
+            const uint32_t k = key_at(i);
+            if (k >> 10 == prefix && i >= lo && i < hi) atomicAdd(&S.hist[2][k & 1023], 1u);
+        }
+        cluster_sync_all();
+        find_bin(S, 2, ctas, need);
+        prefix = prefix << 10 | S.bin, need = S.need;  // the last kept weight's key; how many of its equals are kept
+    } else {
+        prefix = 0xFFFFFFFFu;  // above every key: positions are kept by their place alone
     }
-    const uint32_t ties = left;  // of the positions whose weight is the last kept one's
-    int64_t before = 0;          // kept so far, and ties so far in the upper half
-    for (int i0 = 0; i0 < n; i0 += kSelectThreads) {
-        const int i = i0 + tid;
-        bool keep = false, tie = false;
-        float x = 0.0f;
-        if (i < n) {
-            x = w[i];
-            const uint32_t k = weight_key(x);
-            keep = i < lo || i >= hi || k > prefix;
-            tie = !keep && k == prefix;
-        }
-        int64_t all;
-        const int64_t at = before + block_prefix<kSelectThreads>(tie ? 1ll << 32 : keep ? 1 : 0, &all, warp_sums);
-        const uint32_t ties_before = static_cast<uint32_t>(at >> 32);
-        const int slot = static_cast<int>(at & 0xFFFFFFFF) + static_cast<int>(min(ties_before, ties));
-        if (keep || (tie && ties_before < ties)) {
+    // counts of the warps' parts, then of the CTAs' runs
+    const int part = ((r1 - r0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int p0 = min(r1, r0 + warp * part), p1 = min(r1, p0 + part);
+    uint32_t above = 0, equal = 0;
+    for (int i0 = p0; i0 < p1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0;
+        const bool keep = i < p1 && (i < lo || i >= hi || k > prefix), tie = i < p1 && !keep && k == prefix;
+        above += __popc(__ballot_sync(0xFFFFFFFFu, keep));
+        equal += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+    }
+    if (lane == 0) S.warp_counts[warp][0] = above, S.warp_counts[warp][1] = equal;
+    __syncthreads();
+    if (tid < 2) {
+        uint32_t sum = 0;
+        for (int i = 0; i < kSelectWarps; ++i) sum += S.warp_counts[i][tid];
+        S.counts[tid] = sum;
+    }
+    cluster_sync_all();
+    uint32_t above_before = 0, equal_before = 0;
+    for (int c = 0; c < rank; ++c) {
+        const uint32_t at = mapa_shared(smem_u32(S.counts), c);
+        above_before += ld_cluster_u32(at);
+        equal_before += ld_cluster_u32(at + 4);
+    }
+    for (int i = 0; i < warp; ++i) {
+        above_before += S.warp_counts[i][0];
+        equal_before += S.warp_counts[i][1];
+    }
+    for (int i0 = p0; i0 < p1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0, below = (1u << lane) - 1;
+        const bool keep = i < p1 && (i < lo || i >= hi || k > prefix), tie = i < p1 && !keep && k == prefix;
+        const uint32_t keeps = __ballot_sync(0xFFFFFFFFu, keep), ties = __ballot_sync(0xFFFFFFFFu, tie);
+        const uint32_t t = equal_before + __popc(ties & below);
+        if (keep || (tie && t < need)) {
+            const uint32_t slot = above_before + __popc(keeps & below) + min(t, need);
             kept[slot] = i;
-            out[slot] = x;
+            out[slot] = w[i];
         }
-        before += all;
+        above_before += __popc(keeps);
+        equal_before += __popc(ties);
     }
+    cluster_sync_all();  // no CTA's shared memory goes while another may read it
 }
 
-// One CTA per (new block, sequence and head, keys or values).
-__global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvictArgs a) {
+// The largest of 16 codes' magnitudes: e4m3 values order as their 7 low bits.
+__device__ __forceinline__ uint32_t top_code(const uint4& v) {
+    uint32_t t = __vmaxu4(__vmaxu4(v.x & 0x7F7F7F7Fu, v.y & 0x7F7F7F7Fu), __vmaxu4(v.z & 0x7F7F7F7Fu, v.w & 0x7F7F7F7Fu));
+    t = __vmaxu4(t, t >> 16);
+    return max(t & 0xFFu, (t >> 8) & 0xFFu);
+}
+
+template <int kPieces>  // 16-byte pieces of a thread: 64 rows of (d_qk + d_v) / 16
+__global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvictArgs a, uint32_t magic) {
     __shared__ int64_t src_row[kBlock];
-    __shared__ float src_scale[kBlock];
-    __shared__ float red[kMoveThreads / 32];
+    __shared__ float src_scale[kBlock][2];
+    __shared__ float red[kMoveThreads / 32][2];
     const int tid = threadIdx.x, blocks = (a.keep + kBlock - 1) / kBlock;
     const int bh_in = blockIdx.x / blocks, j = blockIdx.x - bh_in * blocks, b = bh_in / a.H_kv, h = bh_in - b * a.H_kv;
-    const bool value = blockIdx.y;
-    const int d = value ? a.d_v : a.d_qk, groups = d / 16;
-    uint8_t* cache = value ? a.v : a.k;
-    float* scales = value ? a.v_scale : a.k_scale;
     int n = a.seq_lens[b];
     if (n < 0 || n > a.max_blocks * kBlock) n = 0;
     const int m = min(n, a.keep), rows = min(kBlock, m - j * kBlock);
@@ -104,67 +206,109 @@ __global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvict
     if (!to_ok && tid == 0) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
     griddep_wait();
     if (tid < rows) {
-        const int i = a.kept[(static_cast<int64_t>(b) * a.H_kv + h) * a.keep + j * kBlock + tid];
+        const int i = a.kept[static_cast<int64_t>(bh_in) * a.keep + j * kBlock + tid];
         const int blk = a.block_table[static_cast<int64_t>(b) * a.max_blocks + i / kBlock];
         const bool ok = blk >= 0 && blk < a.num_blocks;
         if (!ok) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
         const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + h;
         src_row[tid] = ok ? bh * kBlock + i % kBlock : -1;
-        src_scale[tid] = ok ? scales[bh] : 0.0f;
+        src_scale[tid][0] = ok ? a.k_scale[bh] : 0.0f;
+        src_scale[tid][1] = ok ? a.v_scale[bh] : 0.0f;
     }
     __syncthreads();
     if (!to_ok) return;
     const int64_t to_bh = static_cast<int64_t>(to) * a.H_kv + h;
-    uint4* dst = reinterpret_cast<uint4*>(cache + to_bh * kBlock * d);
-    if (n <= a.keep) {  // whole: copied as it is
-        if (src_row[0] == to_bh * kBlock) return;
-        for (int i = tid; i < rows * groups; i += kMoveThreads) {
-            const int r = i / groups;
-            if (src_row[r] >= 0) dst[i] = reinterpret_cast<const uint4*>(cache + src_row[r] * d)[i - r * groups];
+    const int gk = a.d_qk / 16, groups = gk + a.d_v / 16, total = rows * groups;
+    const bool whole = n <= a.keep;
+    if (whole && src_row[0] == to_bh * kBlock) return;
+    uint4 x[kPieces];
+    float k_top = 0.0f, v_top = 0.0f;
+    auto place = [&](int p, int& r, int& u) {  // piece p of the thread: its row and the piece of the row
+        const int i = tid + p * kMoveThreads;
+        r = static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
+        u = i - r * groups;
+        return i < total && src_row[r] >= 0;
+    };
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        int r, u;
+        if (!place(p, r, u)) continue;
+        x[p] = u < gk ? reinterpret_cast<const uint4*>(a.k + src_row[r] * a.d_qk)[u]
+                      : reinterpret_cast<const uint4*>(a.v + src_row[r] * a.d_v)[u - gk];
+    }
+    if (!whole) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            int r, u;
+            if (!place(p, r, u)) continue;
+            const float top = e4m3_to_float(top_code(x[p])) * src_scale[r][u >= gk];
+            if (u < gk) k_top = fmaxf(k_top, top);
+            else v_top = fmaxf(v_top, top);
         }
-        if (tid == 0 && src_row[0] >= 0) scales[to_bh] = src_scale[0];
-        return;
-    }
-    float amax = 0.0f;
-    for (int i = tid; i < rows * groups; i += kMoveThreads) {
-        const int r = i / groups;
-        if (src_row[r] < 0) continue;
-        float x[16];
-        e4m3x16_values(reinterpret_cast<const uint4*>(cache + src_row[r] * d)[i - r * groups], x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e] * src_scale[r]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kMoveThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    const float scale = amax > 0.0f ? amax / 448.0f : 1.0f;
-    for (int i = tid; i < rows * groups; i += kMoveThreads) {
-        const int r = i / groups;
-        if (src_row[r] < 0) continue;
-        float x[16];
-        e4m3x16_values(reinterpret_cast<const uint4*>(cache + src_row[r] * d)[i - r * groups], x);
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float y[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) y[f] = x[4 * e + f] * src_scale[r] / scale;
-            w[e] = e4m3x4_codes(y[0], y[1], y[2], y[3]);
+        for (int o = 16; o > 0; o >>= 1) {
+            k_top = fmaxf(k_top, __shfl_xor_sync(0xFFFFFFFFu, k_top, o));
+            v_top = fmaxf(v_top, __shfl_xor_sync(0xFFFFFFFFu, v_top, o));
         }
-        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        if ((tid & 31) == 0) red[tid >> 5][0] = k_top, red[tid >> 5][1] = v_top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kMoveThreads / 32; ++w) {
+            k_top = fmaxf(k_top, red[w][0]);
+            v_top = fmaxf(v_top, red[w][1]);
+        }
     }
-    if (tid == 0) scales[to_bh] = scale;
+    const Divisor k_scale(whole ? src_scale[0][0] : unit_scale(k_top)), v_scale(whole ? src_scale[0][1] : unit_scale(v_top));
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        int r, u;
+        if (!place(p, r, u)) continue;
+        if (!whole) {
+            float y[16];
+            e4m3x16_values(x[p], y);
+            const float s = src_scale[r][u >= gk];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] *= s;
+            x[p] = codes16(y, u < gk ? k_scale : v_scale);
+        }
+        if (u < gk) reinterpret_cast<uint4*>(a.k + (to_bh * kBlock + r) * a.d_qk)[u] = x[p];
+        else reinterpret_cast<uint4*>(a.v + (to_bh * kBlock + r) * a.d_v)[u - gk] = x[p];
+    }
+    if (tid == 0 && (!whole || src_row[0] >= 0)) {
+        a.k_scale[to_bh] = k_scale.value;
+        a.v_scale[to_bh] = v_scale.value;
+    }
 }
 
 bool launch_grouped_evict(const GroupedEvictArgs& a, cudaStream_t s, int* launches) {
     const unsigned heads = static_cast<unsigned>(a.B) * a.H_kv;
-    if (!launch_kernel(false, grouped_select_kernel, dim3(heads), dim3(kSelectThreads), 0, s, a)) return false;
+    // CTAs of a cluster: one turn of the SMs, and no fewer than 2048 positions each
+    const int most = a.max_blocks * kBlock;
+    int ctas = 1;
+    while (ctas < kSelectMaxCluster && static_cast<int64_t>(heads) * 2 * ctas <= device_sm_count() && most >= 2 * ctas * 2048) ctas *= 2;
+    const int run = ((most + ctas - 1) / ctas + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
+    const int cached = run < kSelectKeys ? run : kSelectKeys;
+    const size_t smem = sizeof(uint32_t) * static_cast<size_t>(cached);
+    if (!set_max_dynamic_smem(reinterpret_cast<const void*>(grouped_select_kernel), sizeof(uint32_t) * kSelectKeys)) return false;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(heads * ctas);
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, grouped_select_kernel, a, ctas, cached) != cudaSuccess) return false;
     ++*launches;
-    const dim3 grid(heads * ((a.keep + kBlock - 1) / kBlock), 2);
-    if (!launch_kernel(true, grouped_move_kernel, grid, dim3(kMoveThreads), 0, s, a)) return false;
+    const dim3 grid(heads * ((a.keep + kBlock - 1) / kBlock));
+    const uint32_t groups = (a.d_qk + a.d_v) / 16, pieces = (kBlock * groups + kMoveThreads - 1) / kMoveThreads;
+    // umulhi(i, ceil(2^32 / groups)) = i / groups for i < 2^32 / groups
+    const uint32_t magic = static_cast<uint32_t>(((1ll << 32) + groups - 1) / groups);
+    auto* move = pieces <= 2 ? grouped_move_kernel<2> : pieces <= 4 ? grouped_move_kernel<4> : grouped_move_kernel<8>;
+    if (!launch_kernel(true, move, grid, dim3(kMoveThreads), 0, s, a, magic)) return false;
     ++*launches;
     return true;
 }

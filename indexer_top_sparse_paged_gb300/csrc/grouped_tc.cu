@@ -291,12 +291,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     }
     griddep_launch_dependents();
     // this CTA's share
-    auto count = [&](int b) { return grouped_seq_tiles(a, grouped_seq(a, b, blockIdx.x == 0)); };
     int64_t total, base;
     int b0;
-    find_sequence<F::kThreads>(a.B, -1, count, &total, &b0, &base, S.warp_sums, S.found);
-    const int64_t per = (total + a.ctas - 1) / a.ctas, begin = per * blockIdx.x, end = min(total, begin + per);
-    find_sequence<F::kThreads>(a.B, begin, count, &total, &b0, &base, S.warp_sums, S.found);
+    const int64_t begin = find_place<F::kThreads>(
+        a.B, [&](int b) { return grouped_seq_tiles(a, grouped_seq(a, b, blockIdx.x == 0)); },
+        [&](int64_t all) { return (all + a.ctas - 1) / a.ctas * blockIdx.x; }, &total, &b0, &base, S.warp_sums, S.found);
+    const int64_t per = (total + a.ctas - 1) / a.ctas, end = min(total, begin + per);
     tc_fence_before();
     block_sync();
     tc_fence_after();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     Piece p;
 
     if (begin >= end) {
-        // no tiles
+        if (threadIdx.x == 0) a.cuts[blockIdx.x].rows = 0;
     } else if (warp == kWarpLoad) {
         // --------------------------------------------------------------------------- TMA: keys and values
         // Lane l holds the table entry and scales of every 32nd block of the piece, the next 32 fetched while these load.
@@ -421,7 +421,20 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         if (lane == 0) mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
-        // Two warps split the rows of the next item's queries into parts; lane l holds columns 8l .. 8l + 7.
+        // Two warps split the rows of the next item's queries into parts; lane l holds columns 8l .. 8l + 7. First one
+        // of them leaves word of the item that the share's begin cuts, for the join.
+        if (threadIdx.x == kWarpQ * 32) {
+            Walk w1 = w;
+            next_piece(a, w1, p);
+            const int64_t u0 = p.t - p.tile0, u1 = u0 + p.s.tiles;
+            GroupedCut cut{};
+            if (p.tile0 > 0 && begin - per <= u0) {
+                const int c0 = blockIdx.x - 1;
+                cut = GroupedCut{p.s.q0, p.h, p.row0, p.rows, grouped_slot(begin - per, u0, c0),
+                                 static_cast<int>((u1 - 1) / per) - c0 + 1, {0, 0}};
+            }
+            a.cuts[blockIdx.x] = cut;
+        }
         int item = 0;
         bool ok = true;
         const T* q = static_cast<const T*>(a.q);
@@ -547,9 +560,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     }
                 }
                 if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
-                    float* to = a.z + ((p.t + tile - p.tile0) * kGroupedTile + j) * kRows + group * kRW;
+                    float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
-                    for (int r = 0; r < kRW; r += 4) *reinterpret_cast<float4*>(to + r) = make_float4(z[r], z[r + 1], z[r + 2], z[r + 3]);
+                    for (int r = 0; r < kRW; ++r)
+                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = z[r];
                 }
                 // the rows' maxima over the tile
 #pragma unroll

@@ -224,6 +224,15 @@ bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches);
 
 // ---- grouped-head cache -------------------------------------------------------------------------
 
+// Where a CTA's share of the grouped-head attention begins inside an item that no share before it cut: the item's rows,
+// and the partials to join.
+struct alignas(16) GroupedCut {
+    int q0, h, row0, rows;  // rows 0: nothing to join
+    int slot0;              // the first partial; the others are slots 2 * (slot0 / 2 + 1), + 2, ...
+    int parts;
+    int pad[2];
+};
+
 struct GroupedArgs {
     int type;
     int B, max_blocks, num_blocks;
@@ -246,10 +255,11 @@ struct GroupedArgs {
     int* err;
     int row_tile;       // rows of an item
     int ctas;           // CTAs of the attention
+    GroupedCut* cuts;   // [ctas]
     float* part_o;      // [2 * ctas][row_tile][d_v] unnormalised outputs of cut items
     float2* part_ml;    // [2 * ctas][row_tile] (running maximum in powers of two, sum)
     float* row_lse;     // [T][H] log2 of the sums of 2^z (weights only)
-    float* z;           // [max_tiles][128][row_tile] logits in powers of two (weights only)
+    float* z;           // [max_tiles][row_tile][128] logits in powers of two (weights only)
     int64_t max_tiles;
 };
 
