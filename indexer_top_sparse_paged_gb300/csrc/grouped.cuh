@@ -50,6 +50,11 @@ __device__ __forceinline__ int64_t grouped_seq_tiles(const GroupedArgs& a, const
     return static_cast<int64_t>(s.items) * s.tiles * a.H_kv;
 }
 
+// Tiles of a CTA's share.
+__device__ __forceinline__ int64_t grouped_share(const GroupedArgs& a, int64_t total) {
+    return total < (1ll << 30) ? (static_cast<int>(total) + a.ctas - 1) / a.ctas : (total + a.ctas - 1) / a.ctas;
+}
+
 // Sum over the block's threads, and the sum of the threads before this one.
 template <int kThreads>
 __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* total, int64_t* warp_sums) {

@@ -15,8 +15,10 @@
 //
 // Bytes bound it: 2 x 128 of a head's position at d = 128, and 4 products of N = 16 or 32 columns take a tenth of the time
 // those bytes take. One CTA an SM works through its even share of the tiles (see grouped.cuh): a warp of TMA loads runs
-// ahead as far as the ring allows, whatever items it crosses, one warp issues the products, kGroups warpgroups the softmax
-// of kRW rows each, two warps bring the next item's queries.
+// ahead as far as the ring allows, whatever items it crosses, one warp issues the products, two warps bring the next
+// item's queries, and the softmax's warps, kRW rows a thread, take tiles in turn in kSets sets, each with a maximum, a sum
+// and an O^T of its own: the chain logits -> maximum -> weights of one tile (about 1500 cycles) is longer than its bytes
+// take (1400). The set that has an item's last tile puts the two together.
 #include "grouped.cuh"
 
 namespace dsa {
@@ -28,18 +30,52 @@ constexpr size_t kSmemLimit = 232448;
 
 __host__ __device__ constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
 
-// Compiled forms: rows of a softmax thread, warpgroups that share a tile's rows, parts of a query and of a weight.
-template <int kRW_, int kGroups_, int kQP_, int kPP_>
+// Where a CTA stands in its share; next_piece takes the next item, or what the share holds of it.
+struct Walk {
+    GroupedSeq s;
+    int b, item, tile;  // the next piece's sequence, item of it (key head and row tile) and first tile
+    int64_t left, t;    // tiles of the share from there on; place of that tile in the call's line
+};
+
+struct Piece {
+    int h, row0, rows, tile0, tile1;
+    int64_t t;
+};
+
+__device__ __forceinline__ bool next_piece(const GroupedArgs& a, Walk& w, Piece& p) {
+    if (w.left <= 0) return false;
+    while (!w.s.tiles || w.item >= w.s.items * a.H_kv) {  // (left > 0: there is a next one)
+        w.s = grouped_seq(a, ++w.b, false);
+        w.item = 0;
+    }
+    p.h = w.s.items == 1 ? w.item : w.item / w.s.items;
+    p.row0 = (w.item - p.h * w.s.items) * a.row_tile;
+    p.rows = min(a.row_tile, w.s.n * a.G - p.row0);
+    p.tile0 = w.tile;
+    p.tile1 = static_cast<int>(min(static_cast<int64_t>(w.s.tiles), w.tile + w.left));
+    p.t = w.t;
+    const int n = p.tile1 - p.tile0;
+    w.t += n;
+    w.left -= n;
+    w.tile = 0;
+    ++w.item;
+    return true;
+}
+
+// Compiled forms: rows of a softmax thread, warpgroups that share a tile's rows, sets that take tiles in turn, parts of a
+// query and of a weight, buffers of logits.
+template <int kRW_, int kGroups_, int kSets_, int kQP_, int kPP_, int kSB_>
 struct Form {
-    static constexpr int kRW = kRW_, kGroups = kGroups_, kQP = kQP_, kPP = kPP_;
+    static constexpr int kRW = kRW_, kGroups = kGroups_, kSets = kSets_, kQP = kQP_, kPP = kPP_, kSB = kSB_;
     static constexpr int kRows = kRW * kGroups;
-    static constexpr int kSN = kQP * kRows;         // columns of S^T; thread-group g's are kQP * kRW from g * kQP * kRW
+    static constexpr int kSN = kQP * kRows;         // columns of S^T; group g's are kQP * kRW from g * kQP * kRW
     static constexpr int kPN = pad16(kPP * kRows);  // columns of O^T
-    static constexpr int kSoftWarps = 4 * kGroups;
-    static constexpr int kThreads = 128 * kGroups + 128;
+    static constexpr int kSetWarps = 4 * kGroups, kSoftWarps = kSets * kSetWarps;
+    static constexpr int kQWarps = 2;  // (12 warps in all leave 168 registers a thread)
+    static constexpr int kThreads = 32 * (kSoftWarps + 2 + kQWarps);
     static constexpr int kVCMax = kRows > 32 ? 1 : 2;  // chunks of 128 value columns (O^T's share of tensor memory)
-    static constexpr int kColO = 2 * kSN;
-    static constexpr int kCols = kColO + kVCMax * kPN + 8;  // (reads of 32 columns go past the last 24)
+    static constexpr int kColO = kSB * kSN;
+    static constexpr int kCols = kColO + kSets * kVCMax * kPN;
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kQBytes = kSN * 128;   // one 128-column chunk of the split queries
     static constexpr int kPBytes = kPN * 128;   // the split weights of a tile
@@ -49,16 +85,21 @@ struct Form {
 template <typename F>
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], mma_done, met[F::kGroups];
+    uint64_t q_full[2], q_empty[2], s_full[F::kSB], p_full[2], pv_done[2], mma_done, met[F::kSets * F::kGroups], fin, o_free;
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
-    alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e), NaN for a query that is not finite
+    alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
     alignas(16) int seen[2][F::kRows];        // positions below this are seen (rows past the last: 0)
-    alignas(16) float red[2][F::kGroups][F::kRW][4];
+    alignas(16) int row_at[2][F::kRows];      // token * H + head
+    alignas(16) float red[2][F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
+    alignas(16) float neg_m[F::kSoftWarps][F::kRW], fac[F::kSoftWarps][F::kRW];  // each warp's own
+    alignas(16) float fin_l[2][F::kSets][F::kRows][4], fin_m[2][F::kSets][F::kRows];  // a set's share of an item
+    float fin_unit[2][F::kSets];  // of its O^T; 0: it had no tile
     uint32_t tmem_base;
     int abort_flag;
     int64_t warp_sums[F::kThreads / 32];
     int64_t found[2];
+    Walk start;
 };
 
 template <typename F>
@@ -144,11 +185,21 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
-// Columns addr .. addr + N - 1 of this thread's lane (N = 16, 24, 32 or 48; 24: the eight behind them are read too).
+// Columns addr .. addr + N - 1 of this thread's lane.
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t addr, float (&x)[N]) {
-    static_assert(N == 16 || N == 24 || N == 32 || N == 48, "column counts of the compiled forms");
-    if constexpr (N == 16) {
+    static_assert(N == 8 || N == 16 || N == 32 || N == 48, "column counts of the compiled forms");
+    if constexpr (N == 8) {
+        uint32_t u[8];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+            : "r"(addr)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+    } else if constexpr (N == 16) {
         uint32_t u[16];
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -164,7 +215,7 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&x)[N]) {
         tmem_ld32(addr, u);
         tmem_ld_wait(u);
 #pragma unroll
-        for (int i = 0; i < 32 && i < N; ++i) x[i] = __uint_as_float(u[i]);
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(u[i]);
         if constexpr (N == 48) {
             float y[16];
             load_columns<16>(addr + 32, y);
@@ -176,63 +227,61 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&x)[N]) {
 
 template <int N>
 __device__ __forceinline__ void store_columns(uint32_t addr, const float (&x)[N]) {
-    static_assert(N == 24 || N == 48, "column counts of the compiled forms");
-    if constexpr (N == 24) {
-        uint32_t u[16], w[8];
+    static_assert(N == 8 || N == 16 || N == 32, "column counts of the compiled forms");
+    uint32_t u[N];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(x[i]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[16 + i]);
-        tmem_st16(addr, u);
-        tmem_st8(addr + 16, w);
-    } else {
-        uint32_t u[32], w[16];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(x[i]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[32 + i]);
-        tmem_st32(addr, u);
-        tmem_st16(addr + 32, w);
-    }
+    for (int i = 0; i < N; ++i) u[i] = __float_as_uint(x[i]);
+    if constexpr (N == 8) tmem_st8(addr, u);
+    else if constexpr (N == 16) tmem_st16(addr, u);
+    else tmem_st32(addr, u);
 }
 
-// ------------------------------------------------------------------------------------------------
-// the pieces of a CTA's share
-// ------------------------------------------------------------------------------------------------
-
-struct Piece {
-    int b, h, row0, rows, tile0, tile1;
-    GroupedSeq s;
-    int64_t t;  // its first tile in the call's line
-};
-
-struct Walk {
-    int64_t t, end, base;
-    int b;
-};
-
-__device__ __forceinline__ bool next_piece(const GroupedArgs& a, Walk& w, Piece& p) {
-    while (w.t < w.end) {
-        p.s = grouped_seq(a, w.b, false);
-        const int64_t here = grouped_seq_tiles(a, p.s), local = w.t - w.base;
-        if (local >= here) {
-            w.base += here;
-            ++w.b;
-            continue;
+// This thread's logits, from the sums of products with each part of the queries (part i's rows side by side).
+template <int kQP, int kRW>
+__device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
+    if constexpr (kRW <= 16) {
+        float x[kQP * kRW];
+        load_columns<kQP * kRW>(addr, x);
+#pragma unroll
+        for (int r = 0; r < kRW; ++r) {
+            s[r] = x[(kQP - 1) * kRW + r];
+#pragma unroll
+            for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
         }
-        const int item = static_cast<int>(local / p.s.tiles);
-        p.b = w.b;
-        p.h = item / p.s.items;
-        p.row0 = (item - p.h * p.s.items) * a.row_tile;
-        p.rows = min(a.row_tile, p.s.n * a.G - p.row0);
-        p.tile0 = static_cast<int>(local - static_cast<int64_t>(item) * p.s.tiles);
-        p.tile1 = static_cast<int>(min(static_cast<int64_t>(p.s.tiles), p.tile0 + (w.end - w.t)));
-        p.t = w.t;
-        w.t += p.tile1 - p.tile0;
-        return true;
+    } else {
+        static_assert(kQP == 2 && kRW == 32, "two parts of 32 rows");
+        load_columns<32>(addr + 32, s);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float x[16];
+            load_columns<16>(addr + 16 * half, x);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[16 * half + r] = fmaf(s[16 * half + r], 0.0625f, x[r]);
+        }
     }
-    return false;
 }
+
+// Sums of kRW values over the warp's lanes; lane r's result is that of row r (kRW < 32: of row r % kRW, in every lane).
+template <int kRW>
+__device__ __forceinline__ float sum_rows(float (&x)[kRW], int lane) {
+    // halve the rows a lane holds and double the lanes each sum covers: lane bit kRW / 2, then kRW / 4, ... chooses the half
+#pragma unroll
+    for (int w = kRW / 2; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float give = up ? x[i] : x[i + w], own = up ? x[i + w] : x[i];
+            x[i] = own + __shfl_xor_sync(0xFFFFFFFFu, give, w);
+        }
+    }
+#pragma unroll
+    for (int o = kRW; o < 32; o <<= 1) x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], o);
+    return x[0];
+}
+
+// ------------------------------------------------------------------------------------------------
+// queries and outputs
+// ------------------------------------------------------------------------------------------------
 
 // 8 elements of a query row.
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -255,7 +304,7 @@ __device__ __forceinline__ void store_act(__nv_bfloat16* p, float x) { *p = __fl
 template <typename T, typename F>
 __global__ void __launch_bounds__(F::kThreads, 1)
     grouped_tc_kernel(GroupedArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-    constexpr int kRW = F::kRW, kRows = F::kRows, kGroups = F::kGroups;
+    constexpr int kRW = F::kRW, kRows = F::kRows, kGroups = F::kGroups, kSets = F::kSets;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int kc = (a.d_qk + 127) / 128, vc = (a.d_v + 127) / 128;
@@ -273,14 +322,16 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             mbar_init(smem_u32(&S.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&S.q_full[i]), 2);
-            mbar_init(smem_u32(&S.q_empty[i]), 1 + F::kSoftWarps);  // the products that read it, and the softmax's factors
-            mbar_init(smem_u32(&S.s_full[i]), 1);
-            mbar_init(smem_u32(&S.p_full[i]), F::kSoftWarps);
+            mbar_init(smem_u32(&S.q_full[i]), F::kQWarps);
+            mbar_init(smem_u32(&S.q_empty[i]), 1 + F::kSoftWarps);  // the products that read it, and the softmax
+            mbar_init(smem_u32(&S.p_full[i]), F::kSetWarps);
             mbar_init(smem_u32(&S.pv_done[i]), 1);
         }
+        for (int i = 0; i < F::kSB; ++i) mbar_init(smem_u32(&S.s_full[i]), 1);
+        for (int i = 0; i < kSets * kGroups; ++i) mbar_init(smem_u32(&S.met[i]), 4);
         mbar_init(smem_u32(&S.mma_done), 1);
-        for (int g = 0; g < kGroups; ++g) mbar_init(smem_u32(&S.met[g]), 4);
+        mbar_init(smem_u32(&S.fin), F::kSoftWarps);
+        mbar_init(smem_u32(&S.o_free), F::kSetWarps);
         S.abort_flag = 0;
         fence_mbar_init();
     }
@@ -289,31 +340,58 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         tmem_alloc(smem_u32(&S.tmem_base), F::kTmemCols);
         tmem_relinquish();
     }
+    if (warp == kWarpLoad && lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     griddep_launch_dependents();
     // this CTA's share
     int64_t total, base;
     int b0;
     const int64_t begin = find_place<F::kThreads>(
         a.B, [&](int b) { return grouped_seq_tiles(a, grouped_seq(a, b, blockIdx.x == 0)); },
-        [&](int64_t all) { return (all + a.ctas - 1) / a.ctas * blockIdx.x; }, &total, &b0, &base, S.warp_sums, S.found);
-    const int64_t per = (total + a.ctas - 1) / a.ctas, end = min(total, begin + per);
+        [&](int64_t all) { return grouped_share(a, all) * blockIdx.x; }, &total, &b0, &base, S.warp_sums, S.found);
+    const int64_t per = grouped_share(a, total), end = min(total, begin + per);
+    if (threadIdx.x == kWarpQ * 32) {
+        Walk w{};
+        GroupedCut cut{};
+        if (begin < end) {
+            w.s = grouped_seq(a, b0, false);
+            w.b = b0;
+            const int64_t local = begin - base;
+            w.item = local < (1ll << 31) ? static_cast<int>(local) / w.s.tiles : static_cast<int>(local / w.s.tiles);
+            w.tile = static_cast<int>(local - static_cast<int64_t>(w.item) * w.s.tiles);
+            w.left = end - begin;
+            w.t = begin;
+            // word of the item that the share's begin cuts, for the join (of the first share that cuts it)
+            const int64_t u0 = begin - w.tile, u1 = u0 + w.s.tiles;
+            if (w.tile > 0 && begin - per <= u0) {
+                Walk w1 = w;
+                Piece p1;
+                next_piece(a, w1, p1);
+                int parts = 2;  // (the shares that hold a tile of it; begin < u1)
+                while (begin + (parts - 1) * per < u1) ++parts;
+                cut = GroupedCut{w.s.q0, p1.h, p1.row0, p1.rows, grouped_slot(begin - per, u0, blockIdx.x - 1), parts, {0, 0}};
+            }
+        }
+        S.start = w;
+        a.cuts[blockIdx.x] = cut;
+    }
     tc_fence_before();
     block_sync();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem_base, 0);
-    Walk w{begin, end, base, b0};
+    Walk w = S.start;
     Piece p;
 
-    if (begin >= end) {
-        if (threadIdx.x == 0) a.cuts[blockIdx.x].rows = 0;
-    } else if (warp == kWarpLoad) {
+    if (warp == kWarpLoad) {
         // --------------------------------------------------------------------------- TMA: keys and values
         // Lane l holds the table entry and scales of every 32nd block of the piece, the next 32 fetched while these load.
         int st = 0, phase = 1, tiles = 0;
         bool ok = true;
         while (ok && next_piece(a, w, p)) {
-            const int32_t* table = a.block_table + static_cast<int64_t>(p.b) * a.max_blocks;
-            const int blocks = min(2 * p.tile1, (p.s.len + kBlock - 1) / kBlock);
+            const int32_t* table = a.block_table + static_cast<int64_t>(w.b) * a.max_blocks;
+            const int blocks = min(2 * p.tile1, (w.s.len + kBlock - 1) / kBlock);
             auto fetch = [&](int first, int& row, float& ks, float& vs) {
                 const int i = first + lane;
                 row = -1, ks = vs = 0.0f;
@@ -337,18 +415,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     fetch(2 * tile + 32, row_next, ks_next, vs_next);
                 }
                 const int r0 = __shfl_sync(0xFFFFFFFFu, row, 2 * j), r1 = __shfl_sync(0xFFFFFFFFu, row, 2 * j + 1);
-                float4 sc;
-                sc.x = __shfl_sync(0xFFFFFFFFu, ks, 2 * j), sc.y = __shfl_sync(0xFFFFFFFFu, ks, 2 * j + 1);
-                sc.z = __shfl_sync(0xFFFFFFFFu, vs, 2 * j), sc.w = __shfl_sync(0xFFFFFFFFu, vs, 2 * j + 1);
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.empty[st]), phase, abort_flag, a.err));
                 if (!ok) break;
+                const uint32_t bar = smem_u32(&S.full[st]), dst = sRing + st * stage_bytes;
                 if (lane == 0) {
-                    const uint32_t bar = smem_u32(&S.full[st]), dst = sRing + st * stage_bytes;
-                    S.scales[st] = sc;
-                    S.valid[st] = (r0 >= 0 ? 1 : 0) | (r1 >= 0 ? 2 : 0);
                     const uint32_t n = (r0 >= 0 ? 1 : 0) + (r1 >= 0 ? 1 : 0);
-                    if (n) mbar_arrive_expect_tx(bar, n * (kc + vc) * kChunk);
-                    else mbar_arrive(bar);
+                    if (n) mbar_expect_tx(bar, n * (kc + vc) * kChunk);
                     for (int c = 0; c < kc; ++c) {
                         if (r0 >= 0) tma_load_2d(dst + 2 * c * kChunk, &map_k, c * 128, r0 * kBlock, bar);
                         if (r1 >= 0) tma_load_2d(dst + (2 * c + 1) * kChunk, &map_k, c * 128, r1 * kBlock, bar);
@@ -357,6 +429,15 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         if (r0 >= 0) tma_load_2d(dst + v_off + 2 * c * kChunk, &map_v, c * 128, r0 * kBlock, bar);
                         if (r1 >= 0) tma_load_2d(dst + v_off + (2 * c + 1) * kChunk, &map_v, c * 128, r1 * kBlock, bar);
                     }
+                }
+                // the scales may still be on their way: they follow
+                float4 sc;
+                sc.x = __shfl_sync(0xFFFFFFFFu, ks, 2 * j), sc.y = __shfl_sync(0xFFFFFFFFu, ks, 2 * j + 1);
+                sc.z = __shfl_sync(0xFFFFFFFFu, vs, 2 * j), sc.w = __shfl_sync(0xFFFFFFFFu, vs, 2 * j + 1);
+                if (lane == 0) {
+                    S.scales[st] = sc;
+                    S.valid[st] = (r0 >= 0 ? 1 : 0) | (r1 >= 0 ? 2 : 0);
+                    mbar_arrive(bar);
                 }
                 __syncwarp();
                 ++tiles;
@@ -372,74 +453,87 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         }
     } else if (warp == kWarpMma) {
         // --------------------------------------------------------------------------------- products
-        // K Q^T of a tile runs one tile ahead of V^T P^T.
-        int st = 0, phase = 0, st_v = 0, n = 0, item = 0;  // n: tiles whose logits were issued
-        bool ok = true, open = false, first = false, first_v = false;  // open: the last tile's V^T P^T is still to come
+        // K Q^T of a tile runs `lead` tiles ahead of V^T P^T (whose stages it must leave to the loads).
+        const int lead = min(F::kSB / 2, stages - 1);
+        int st = 0, phase = 0, st_v = 0, n = 0, done = 0, item = 0;  // tiles whose logits, whose values were issued
+        int last = 0;  // first tile of the item before
+        uint32_t first = 0;  // bit n % 32: tile n is the first of its item in its set
+        bool ok = true;
         const int ksteps = (a.d_qk + 31) / 32;
-        auto values = [&](int j) {  // V^T P^T of tile j
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[j & 1]), (j >> 1) & 1, abort_flag, a.err));
+        auto values = [&]() {  // V^T P^T of tile `done`
+            const int j = done & 1, set = kSets == 2 ? j : 0;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[j]), (done >> 1) & 1, abort_flag, a.err));
             if (!ok) return;
             tc_fence_after();
+            const bool fresh = (first >> (done & 31)) & 1;
             for (int c = 0; c < vc; ++c) {
                 const uint64_t da = sw128_desc(sRing + st_v * stage_bytes + v_off + 2 * c * kChunk, 0, 1024);
-                const uint64_t db = plain_desc(sP + (j & 1) * F::kPBytes, 128, 2048);
+                const uint64_t db = plain_desc(sP + j * F::kPBytes, 128, 2048);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    warp_mma_f8(tmem + F::kColO + c * F::kPN, da + k * (4096 >> 4), db + k * (512 >> 4), idesc_f8(F::kPN, 1u, 1u),
-                                (first_v && k == 0) ? 0u : 1u);
+                    warp_mma_f8(tmem + F::kColO + (set * F::kVCMax + c) * F::kPN, da + k * (4096 >> 4), db + k * (512 >> 4),
+                                idesc_f8(F::kPN, 1u, 1u), fresh && k == 0 ? 0u : 1u);
             }
             warp_tc_commit(smem_u32(&S.empty[st_v]));
-            warp_tc_commit(smem_u32(&S.pv_done[j & 1]));
+            warp_tc_commit(smem_u32(&S.pv_done[j]));
             if (++st_v == stages) st_v = 0;
+            ++done;
         };
         while (ok && next_piece(a, w, p)) {
             const int qb = item & 1;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            while (ok && done < last) values();  // the item before that one must end for this one's queries to come
+            last = n;
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
             for (int tile = p.tile0; ok && tile < p.tile1; ++tile) {
-                first = tile == p.tile0;
-                // S[n & 1] is free: V^T P^T of tile n - 2 was issued after its weights came
+                // this buffer of logits is free: V^T P^T of tile n - kSB has been issued, after its weights came
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), phase, abort_flag, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 for (int k = 0; k < ksteps; ++k) {
                     const uint64_t da = sw128_desc(sRing + st * stage_bytes + (k >> 2) * 2 * kChunk, 0, 1024) + (k & 3) * 2;
                     const uint64_t db = sw128_desc(sQ + (qb * kc + (k >> 2)) * F::kQBytes, 0, 1024) + (k & 3) * 2;
-                    warp_mma_f8(tmem + (n & 1) * F::kSN, da, db, idesc_f8(F::kSN, 0u, 0u), k ? 1u : 0u);
+                    warp_mma_f8(tmem + (n & (F::kSB - 1)) * F::kSN, da, db, idesc_f8(F::kSN, 0u, 0u), k ? 1u : 0u);
                 }
-                warp_tc_commit(smem_u32(&S.s_full[n & 1]));
+                warp_tc_commit(smem_u32(&S.s_full[n & (F::kSB - 1)]));
                 if (tile + 1 == p.tile1) warp_tc_commit(smem_u32(&S.q_empty[qb]));
-                if (open) values(n - 1);
-                open = true;
-                first_v = first;
+                const uint32_t bit = 1u << (n & 31);
+                first = tile - p.tile0 < kSets ? first | bit : first & ~bit;
                 ++n;
                 if (++st == stages) st = 0, phase ^= 1;
+                if (n - done > lead) values();
             }
             ++item;
         }
-        if (ok && open) values(n - 1);
+        while (ok && done < n) values();
         warp_tc_commit(smem_u32(&S.mma_done));  // every product issued so far
         if (lane == 0) mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
-        // Two warps split the rows of the next item's queries into parts; lane l holds columns 8l .. 8l + 7. First one
-        // of them leaves word of the item that the share's begin cuts, for the join.
-        if (threadIdx.x == kWarpQ * 32) {
-            Walk w1 = w;
-            next_piece(a, w1, p);
-            const int64_t u0 = p.t - p.tile0, u1 = u0 + p.s.tiles;
-            GroupedCut cut{};
-            if (p.tile0 > 0 && begin - per <= u0) {
-                const int c0 = blockIdx.x - 1;
-                cut = GroupedCut{p.s.q0, p.h, p.row0, p.rows, grouped_slot(begin - per, u0, c0),
-                                 static_cast<int>((u1 - 1) / per) - c0 + 1, {0, 0}};
-            }
-            a.cuts[blockIdx.x] = cut;
-        }
+        // Two warps split the rows of the next item's queries into parts; lane l holds columns 8l .. 8l + 7.
         int item = 0;
         bool ok = true;
         const T* q = static_cast<const T*>(a.q);
+        const int col = lane * 8;
+        const bool in = col < a.d_qk;
         while (ok && next_piece(a, w, p)) {
             const int qb = item & 1;
+            constexpr int kBatch = 4;  // rows in flight
+            float x[kBatch][8];
+            int row_at[kBatch], seen[kBatch];
+            auto load = [&](int r0) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * F::kQWarps, row = p.row0 + r, tok = row / a.G, head = p.h * a.G + row - tok * a.G;
+                    const bool live = r < p.rows;
+                    row_at[k] = live ? (w.s.q0 + tok) * a.H + head : 0;
+                    seen[k] = live ? w.s.len - w.s.n + tok + 1 : 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[k][i] = 0.0f;
+                    if (live && in)
+                        load8(q + static_cast<int64_t>(w.s.q0 + tok) * a.q_stride_t + static_cast<int64_t>(head) * a.q_stride_h + col, x[k]);
+                }
+            };
+            load(warp - kWarpQ);
             // (this wait lasts as long as an item; what stalls in it gives up by itself)
             const long long t0 = clock64();
             while (ok && !mbar_try_wait(smem_u32(&S.q_empty[qb]), ((item >> 1) & 1) ^ 1)) {
@@ -452,48 +546,42 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            const int col = lane * 8;
-#pragma unroll 4
-            for (int r = warp - kWarpQ; r < kRows; r += 2) {
-                float x[8];
+#pragma unroll 1
+            for (int r0 = warp - kWarpQ; r0 < kRows; r0 += kBatch * F::kQWarps) {
+                if (r0 >= kBatch * F::kQWarps) load(r0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-                const int row = p.row0 + r, i_tok = row / a.G;
-                if (r < p.rows && col < a.d_qk)
-                    load8(q + static_cast<int64_t>(p.s.q0 + i_tok) * a.q_stride_t + static_cast<int64_t>(p.h * a.G + row - i_tok * a.G) * a.q_stride_h + col, x);
-                float top = 0.0f;
-                bool fine = true;
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = r0 + k * F::kQWarps;
+                    if (r >= kRows) break;
+                    // 2^-e takes the largest element into (224, 448]; a query that is not finite becomes codes of NaN
+                    uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    top = fmaxf(top, fabsf(x[i]));
-                    fine = fine && isfinite(x[i]);
-                }
-                top = warp_max(top);
-                fine = __all_sync(0xFFFFFFFFu, fine);
-                // 2^-e takes the largest element into (224, 448]
-                int e = 0;
-                if (fine && top > 0.0f) {
-                    e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 8, -120);
-                    if (top * exp2f(static_cast<float>(-e)) > 448.0f) ++e;
-                }
-                const float down = exp2f(static_cast<float>(-e));
-                uint32_t parts[4][F::kQP];
+                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    const bool fine = top < 0x7F800000u;
+                    int e = max(static_cast<int>(top >> 23) - 127 - 8, -120);
+                    if ((top & 0x7FFFFFu) > 0x600000u) ++e;  // a significand above 1.75
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    uint32_t parts[4][F::kQP];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split_pair<F::kQP>(fine ? x[2 * i] * down : 0.0f, fine ? x[2 * i + 1] * down : 0.0f, parts[i]);
-                if (col < kc * 128) {
-                    const uint32_t chunk = sQ + (qb * kc + (col >> 7)) * F::kQBytes;
+                    for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[k][2 * i] * down, x[k][2 * i + 1] * down, parts[i]);
+                    if (col < kc * 128) {
+                        const uint32_t chunk = sQ + (qb * kc + (col >> 7)) * F::kQBytes;
+                        const int nrow = (r / kRW) * (F::kQP * kRW) + r % kRW, c16 = (col & 127) >> 4;
 #pragma unroll
-                    for (int i = 0; i < F::kQP; ++i) {
-                        const int nrow = (r / kRW) * (F::kQP * kRW) + i * kRW + r % kRW, c16 = (col & 127) >> 4;
-                        const uint32_t at = chunk + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
-                                     "r"(parts[2][i] | parts[3][i] << 16)
-                                     : "memory");
+                        for (int i = 0; i < F::kQP; ++i) {  // (kRW is a multiple of 8: the parts' rows swizzle alike)
+                            const uint32_t at = chunk + (nrow + i * kRW) * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
+                                         "r"(fine ? parts[0][i] | parts[1][i] << 16 : 0x7F7F7F7Fu),
+                                         "r"(fine ? parts[2][i] | parts[3][i] << 16 : 0x7F7F7F7Fu)
+                                         : "memory");
+                        }
                     }
-                }
-                if (lane == 0) {
-                    S.q_factor[qb][r] = fine ? exp2f(static_cast<float>(e)) * (a.sm_scale * 1.4426950408889634f) : NAN;
-                    S.seen[qb][r] = r < p.rows ? p.s.len - p.s.n + i_tok + 1 : 0;
+                    if (lane == 0) {
+                        S.q_factor[qb][r] = __uint_as_float(static_cast<uint32_t>(127 + (fine ? e : 0)) << 23) * (a.sm_scale * 1.4426950408889634f);
+                        S.seen[qb][r] = seen[k];
+                        S.row_at[qb][r] = row_at[k];
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -503,53 +591,58 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         }
     } else {
         // --------------------------------------------------------------------------------- softmax
-        const int group = warp >> 2, quarter = warp & 3, j = quarter * 32 + lane;  // j: position of the tile, TMEM lane
+        const int set = warp / F::kSetWarps, group = (warp >> 2) % kGroups, quarter = warp & 3;
+        const int j = quarter * 32 + lane;  // position of the tile, TMEM lane
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_col = lane_base + F::kColO + group * F::kPP * kRW;
-        int n = 0, st = 0, sphase = 0, item = 0, met = 0;
+        float* neg_m = S.neg_m[warp];
+        float* fac = S.fac[warp];
+        int n = set, n_item = 0, st = set, sphase = 0, item = 0, met = 0, turn = 0;  // n: this set's next tile, n_item: the item's first
         bool ok = true;
         // The group's four warps meet (a barrier whose wait gives up, as every other).
         auto group_sync = [&]() {
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.met[group]));
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[group]), met, abort_flag, a.err));
+            if (lane == 0) mbar_arrive(smem_u32(&S.met[set * kGroups + group]));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[set * kGroups + group]), met, abort_flag, a.err));
             met ^= 1;
         };
         while (ok && next_piece(a, w, p)) {
-            const int qb = item & 1;
+            const int qb = item & 1, n_end = n_item + p.tile1 - p.tile0, len = w.s.len;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
-            float m[kRW], l[kRW], v_ref = 7.8886090522101181e-31f;  // 2^-100
+            float l[kRW], v_ref = 7.8886090522101181e-31f;  // 2^-100
+            float m = -INFINITY;                              // of row lane % kRW
 #pragma unroll
-            for (int r = 0; r < kRW; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+            for (int r = 0; r < kRW; ++r) l[r] = 0.0f;
+            __syncwarp();
+            if (lane < kRW) neg_m[lane] = 0.0f;
             const float* factor = S.q_factor[qb] + group * kRW;
             const int* seen = S.seen[qb] + group * kRW;
             // every row sees the positions below this
-            const int all_see = p.s.len - p.s.n + p.row0 / a.G + 1;
-            for (int tile = p.tile0; ok && tile < p.tile1; ++tile, ++n) {
+            const int all_see = min(len, len - w.s.n + p.row0 / a.G + 1);
+            // the item before this has left O^T and the sets' shares
+            bool waited = kSets == 1 || item == 0;
+            auto wait_free = [&]() {
+                if (waited) return;
+                waited = true;
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.o_free), (item - 1) & 1, abort_flag, a.err));
+            };
+            const bool any = n < n_end;
+            bool fresh = true;
+            for (; ok && n < n_end; n += kSets) {
+                const int tile = p.tile0 + n - n_item;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), sphase, abort_flag, a.err) &&
-                                                 mbar_wait(smem_u32(&S.s_full[n & 1]), (n >> 1) & 1, abort_flag, a.err));
+                                                 mbar_wait(smem_u32(&S.s_full[n & (F::kSB - 1)]), (n / F::kSB) & 1, abort_flag, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 const float4 sc = S.scales[st];
                 const int valid = S.valid[st], pos = tile * kGroupedTile + j;
-                const float ks = quarter < 2 ? sc.x : sc.y, vs = quarter < 2 ? sc.z : sc.w;
-                const bool here = (valid >> (quarter >> 1)) & 1 && pos < p.s.len;
-                float z[kRW];
-                {
-                    float x[F::kQP * kRW];
-                    load_columns<F::kQP * kRW>(lane_base + (n & 1) * F::kSN + group * F::kQP * kRW, x);
+                const bool here = (valid >> (quarter >> 1)) & 1 && pos < len;
+                const float ks = !here ? 1.0f : quarter < 2 ? sc.x : sc.y;
+                float s[kRW];
+                load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, s);
+                if (valid != 3 || (tile + 1) * kGroupedTile > all_see) {
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r) {
-                        float y = x[(F::kQP - 1) * kRW + r];
-#pragma unroll
-                        for (int i = F::kQP - 2; i >= 0; --i) y = fmaf(y, 0.0625f, x[i * kRW + r]);
-                        z[r] = y * (factor[r] * ks);
-                    }
-                }
-                const bool whole = valid == 3 && (tile + 1) * kGroupedTile <= min(all_see, p.s.len);
-                if (!whole) {
-#pragma unroll
-                    for (int r = 0; r < kRW; ++r) z[r] = here && pos < seen[r] ? z[r] : -INFINITY;
+                    for (int r = 0; r < kRW; ++r) s[r] = here && pos < seen[r] ? s[r] : -INFINITY;
                     if (group == 0 && !here) {  // what the slot holds must not reach the products: 0 * NaN is NaN
                         for (int c = 0; c < vc; ++c) {
                             const uint32_t at = sRing + st * stage_bytes + v_off + 2 * c * kChunk + j * 128;
@@ -563,137 +656,187 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
                     for (int r = 0; r < kRW; ++r)
-                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = z[r];
+                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * (factor[r] * ks);
                 }
-                // the rows' maxima over the tile
+                // The rows' maxima over the tile: every warp's, then lane r of each warp looks after row r. A factor is
+                // positive and the same for a warp's positions.
+                float top = -INFINITY;
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) {
-                    const float top = warp_max(z[r]);
-                    if (lane == (r & 31)) S.red[n & 1][group][r][quarter] = top;
+                    const float x = warp_max(s[r]);
+                    if (lane == r) top = x;
                 }
+                const float k_warp = quarter < 2 ? (valid & 1 ? sc.x : 1.0f) : (valid & 2 ? sc.y : 1.0f);
+                if (lane < kRW) S.red[turn][set * kGroups + group][lane][quarter] = top * (factor[lane] * k_warp);
                 group_sync();
                 if (!ok) break;
-                bool grown = false;
-                float fac[kRW];
-#pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const float4 t = *reinterpret_cast<const float4*>(S.red[n & 1][group][r]);
-                    const float top = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m[r]);
-                    grown = grown || top > m[r];
-                    fac[r] = top == -INFINITY ? 1.0f : ex2(m[r] - top);
-                    m[r] = top;
-                }
+                const float4 t = *reinterpret_cast<const float4*>(S.red[turn][set * kGroups + group][lane % kRW]);
+                turn ^= 1;
+                const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
                 // The weights carry their block's value scale, against a power of two no smaller than any so far.
                 const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
-                float v_fac = 1.0f;
-                if (v_top > v_ref) {
-                    const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
-                    v_fac = v_ref / ref;
-                    grown = true;
-                    v_ref = ref;
-                }
+                const bool grown = __any_sync(0xFFFFFFFFu, m_new > m) || v_top > v_ref;
+                // this buffer of weights has been read, and O^T is this set's to rescale
+                if (n >= 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
+                if (fresh) wait_free();
+                if (!ok) break;
                 if (grown) {  // the same for all of the group's threads
+                    float v_fac = 1.0f;
+                    if (v_top > v_ref) {
+                        const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
+                        v_fac = v_ref / ref;
+                        v_ref = ref;
+                    }
+                    if (lane < kRW) {
+                        fac[lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
+                        neg_m[lane] = m_new == -INFINITY ? 0.0f : -m_new;
+                    }
+                    m = m_new;
+                    __syncwarp();
+                    if (!fresh) {
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
-                    if (tile > p.tile0) {
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
-                        if (!ok) break;
+                        for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
+                        if (kSets == 1) {
+                            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
+                            if (!ok) break;
+                        }
                         tc_fence_after();
                         for (int c = 0; c < vc; ++c) {
-                            float o[F::kPP * kRW];
-                            load_columns<F::kPP * kRW>(o_col + c * F::kPN, o);
 #pragma unroll
-                            for (int i = 0; i < F::kPP; ++i)
+                            for (int i = 0; i < F::kPP; ++i) {
+                                float o[kRW];
+                                const uint32_t at = o_col + (set * F::kVCMax + c) * F::kPN + i * kRW;
+                                load_columns<kRW>(at, o);
 #pragma unroll
-                                for (int r = 0; r < kRW; ++r) o[i * kRW + r] *= fac[r] * v_fac;
-                            store_columns<F::kPP * kRW>(o_col + c * F::kPN, o);
+                                for (int r = 0; r < kRW; ++r) o[r] *= fac[r] * v_fac;
+                                store_columns<kRW>(at, o);
+                            }
                         }
                         tmem_st_wait();
                     }
                 }
-                if (n >= 2) {  // the products that read this buffer of weights are done
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
-                    if (!ok) break;
-                }
-                const float tv = here ? vs * (256.0f / v_ref) : 0.0f;
+                fresh = false;
+                const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (256.0f / v_ref) : 0.0f;
                 const uint32_t p_buf = sP + (n & 1) * F::kPBytes + j * 16;
+                constexpr int kChunkRows = kRW < 16 ? 8 : 16;
 #pragma unroll
-                for (int r8 = 0; r8 < kRW; r8 += 8) {
-                    uint32_t parts[4][F::kPP];
+                for (int r0 = 0; r0 < kRW; r0 += kChunkRows) {
+                    uint32_t parts[kChunkRows / 2][F::kPP];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r8 + 2 * i;
-                        const float p0 = ex2(z[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
-                        const float p1 = ex2(z[r + 1] - (m[r + 1] == -INFINITY ? 0.0f : m[r + 1]));
+                    for (int i = 0; i < kChunkRows / 2; ++i) {
+                        const int r = r0 + 2 * i;
+                        const float p0 = ex2(fmaf(s[r], factor[r] * ks, neg_m[r]));
+                        const float p1 = ex2(fmaf(s[r + 1], factor[r + 1] * ks, neg_m[r + 1]));
                         l[r] += p0;
                         l[r + 1] += p1;
                         split_pair<F::kPP>(p0 * tv, p1 * tv, parts[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < F::kPP; ++i) {
-                        const int col = group * F::kPP * kRW + i * kRW + r8;
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_buf + (col >> 4) * 2048 + (col & 8)),
-                                     "r"(parts[0][i] | parts[1][i] << 16), "r"(parts[2][i] | parts[3][i] << 16)
-                                     : "memory");
+                        const int col = group * F::kPP * kRW + i * kRW + r0;
+                        const uint32_t at = p_buf + (col >> 4) * 2048 + (col & 8);
+                        if constexpr (kChunkRows == 8)
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
+                                         "r"(parts[2][i] | parts[3][i] << 16)
+                                         : "memory");
+                        else
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
+                                         "r"(parts[2][i] | parts[3][i] << 16),
+                                         "r"(parts[kChunkRows / 2 - 4][i] | parts[kChunkRows / 2 - 3][i] << 16),
+                                         "r"(parts[kChunkRows / 2 - 2][i] | parts[kChunkRows / 2 - 1][i] << 16)
+                                         : "memory");
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.p_full[n & 1]));
-                if (++st == stages) st = 0, sphase ^= 1;
+                st += kSets;
+                if (st >= stages) st -= stages, sphase ^= 1;
             }
             if (!ok) break;
+            wait_free();
+            // the item's end: this set's share of it
+            const float sum = sum_rows<kRW>(l, lane);
+            if (lane < kRW) {
+                S.fin_l[qb][set][group * kRW + lane][quarter] = sum;
+                S.fin_m[qb][set][group * kRW + lane] = m;
+            }
+            if (lane == 0) S.fin_unit[qb][set] = any ? v_ref * (1.0f / 256.0f) : 0.0f;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.q_empty[qb]));
-            ++item;
-            // the item's end: sums over the positions, then the rows, or their partial
+            if (lane == 0) mbar_arrive(smem_u32(&S.fin));
+            if (kSets == 1 || ((n_end - 1) & 1) == set) {
+                // the last tile was this set's: the rows, or their partial
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
+                                                       mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & 1]), ((n_end - 1) >> 1) & 1, abort_flag, a.err));
+                if (!ok) break;
+                tc_fence_after();
+                // lane r: row r's maximum and sum over both sets, and what each set's O^T is to be multiplied by
+                const bool complete = p.tile0 == 0 && p.tile1 == w.s.tiles;
+                const int slot = grouped_slot(begin, p.t, blockIdx.x), rr = group * kRW + lane % kRW;
+                float top = -INFINITY, all = 0.0f, f[kSets];
 #pragma unroll
-            for (int r = 0; r < kRW; ++r) {
+                for (int i = 0; i < kSets; ++i) top = fmaxf(top, S.fin_m[qb][i][rr]);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
-            }
-            // (the maxima of the last tile have been read by all; those of the one before, long since)
+                for (int i = 0; i < kSets; ++i) {
+                    const float4 x = *reinterpret_cast<const float4*>(S.fin_l[qb][i][rr]);
+                    const float u = S.fin_unit[qb][i];
+                    f[i] = top == -INFINITY ? 1.0f : ex2(S.fin_m[qb][i][rr] - top);
+                    if (u != 0.0f) all = fmaf((x.x + x.y) + (x.z + x.w), f[i], all);
+                    f[i] *= u;
+                }
+                const float inv = all == 0.0f ? 0.0f : complete ? 1.0f / all : 1.0f;
+                const int row_at = S.row_at[qb][rr];
+                if (quarter == 0 && lane < kRW && rr < p.rows) {
+                    const float lse2 = all == 0.0f ? -INFINITY : top + log2f(all);
+                    if (!complete) a.part_ml[slot * kRows + rr] = make_float2(top, all);
+                    if (complete && a.lse) a.lse[row_at] = lse2 * 0.6931471805599453f;
+                    if (complete && a.weights_out) a.row_lse[row_at] = lse2;
+                }
+                const int other = kSets == 1 ? 0 : 1 - set;
+                const bool both = kSets == 2 && S.fin_unit[qb][other] != 0.0f;
+                const float f_own = f[kSets == 1 ? 0 : set] * inv, f_other = f[other] * inv;
+                for (int c = 0; c < vc; ++c) {
+                    float y[kRW];
 #pragma unroll
-            for (int r = 0; r < kRW; ++r)
-                if (lane == (r & 31)) S.red[n & 1][group][r][quarter] = l[r];
-            group_sync();
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
-            if (!ok) break;
-            tc_fence_after();
-            const bool complete = p.tile0 == 0 && p.tile1 == p.s.tiles;
-            const int slot = grouped_slot(begin, p.t, blockIdx.x);
-            const float unit = v_ref * (1.0f / 256.0f);
-            for (int c = 0; c < vc; ++c) {
-                float o[F::kPP * kRW];
-                load_columns<F::kPP * kRW>(o_col + c * F::kPN, o);
-                const int e = c * 128 + j;
+                    for (int i = F::kPP - 1; i >= 0; --i) {
+                        float o[kRW];
+                        load_columns<kRW>(o_col + (set * F::kVCMax + c) * F::kPN + i * kRW, o);
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const int rr = group * kRW + r;
-                    if (rr >= p.rows) break;
-                    float y = o[(F::kPP - 1) * kRW + r];
-#pragma unroll
-                    for (int i = F::kPP - 2; i >= 0; --i) y = fmaf(y, 0.0625f, o[i * kRW + r]);
-                    y *= unit;
-                    const float4 t = *reinterpret_cast<const float4*>(S.red[n & 1][group][r]);
-                    const float sum = (t.x + t.y) + (t.z + t.w);
-                    const int row = p.row0 + rr, i_tok = row / a.G;
-                    const int64_t at = static_cast<int64_t>(p.s.q0 + i_tok) * a.H + p.h * a.G + row - i_tok * a.G;
-                    if (e < a.d_v) {
-                        if (complete) store_act(static_cast<T*>(a.out) + at * a.d_v + e, sum == 0.0f ? 0.0f : y / sum);
-                        else a.part_o[(static_cast<int64_t>(slot) * kRows + rr) * a.d_v + e] = sum == 0.0f ? 0.0f : y;
+                        for (int r = 0; r < kRW; ++r) y[r] = i == F::kPP - 1 ? o[r] : fmaf(y[r], 0.0625f, o[r]);
                     }
-                    if (c == 0 && j == 0) {
-                        const float lse2 = sum == 0.0f ? -INFINITY : m[r] + log2f(sum);
-                        if (!complete) a.part_ml[slot * kRows + rr] = make_float2(m[r], sum);
-                        if (complete && a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
-                        if (complete && a.weights_out) a.row_lse[at] = lse2;
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r) y[r] *= __shfl_sync(0xFFFFFFFFu, f_own, r);
+                    if (both) {
+                        float x[kRW];
+#pragma unroll
+                        for (int i = F::kPP - 1; i >= 0; --i) {
+                            float o[kRW];
+                            load_columns<kRW>(o_col + (other * F::kVCMax + c) * F::kPN + i * kRW, o);
+#pragma unroll
+                            for (int r = 0; r < kRW; ++r) x[r] = i == F::kPP - 1 ? o[r] : fmaf(x[r], 0.0625f, o[r]);
+                        }
+#pragma unroll
+                        for (int r = 0; r < kRW; ++r) y[r] = fmaf(x[r], __shfl_sync(0xFFFFFFFFu, f_other, r), y[r]);
+                    }
+                    const int e = c * 128 + j;
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r) {
+                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r);
+                        if (group * kRW + r < p.rows && e < a.d_v) {
+                            if (complete) store_act(static_cast<T*>(a.out) + at * a.d_v + e, y[r]);
+                            else a.part_o[(static_cast<int64_t>(slot) * kRows + group * kRW + r) * a.d_v + e] = y[r];
+                        }
                     }
                 }
+                tc_fence_before();  // O^T has been read before the next item's first product may overwrite it
+                __syncwarp();
+                if (lane == 0 && kSets == 2) mbar_arrive(smem_u32(&S.o_free));
             }
-            tc_fence_before();  // O has been read before the next item's first product may overwrite it
-            group_sync();       // and so have the sums, before the next item's maxima
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.q_empty[qb]));
+            n_item = n_end;
+            ++item;
         }
     }
     tc_fence_before();
@@ -738,13 +881,13 @@ bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches) {
     using namespace gtc;
     bool ok = false;
     if (a.type == DSA_F32) {
-        ok = a.row_tile == 8 ? launch_form<float, Form<8, 1, 6, 6>>(a, s) : launch_form<float, Form<8, 2, 6, 6>>(a, s);
+        ok = a.row_tile == 8 ? launch_form<float, Form<8, 1, 2, 6, 6, 4>>(a, s) : launch_form<float, Form<8, 2, 1, 6, 6, 2>>(a, s);
     } else {
         switch (a.row_tile) {
-            case 8: ok = launch_form<__nv_bfloat16, Form<8, 1, 2, 3>>(a, s); break;
-            case 16: ok = launch_form<__nv_bfloat16, Form<8, 2, 2, 3>>(a, s); break;
-            case 32: ok = launch_form<__nv_bfloat16, Form<16, 2, 2, 3>>(a, s); break;
-            default: ok = launch_form<__nv_bfloat16, Form<16, 4, 2, 3>>(a, s); break;
+            case 8: ok = launch_form<__nv_bfloat16, Form<8, 1, 2, 2, 3, 4>>(a, s); break;
+            case 16: ok = launch_form<__nv_bfloat16, Form<16, 1, 2, 2, 3, 4>>(a, s); break;
+            case 32: ok = launch_form<__nv_bfloat16, Form<32, 1, 2, 2, 3, 2>>(a, s); break;
+            default: ok = launch_form<__nv_bfloat16, Form<32, 2, 1, 2, 3, 2>>(a, s); break;
         }
     }
     if (ok) ++*launches;
