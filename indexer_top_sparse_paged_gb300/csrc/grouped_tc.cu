@@ -85,14 +85,15 @@ struct Form {
 template <typename F>
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[F::kSB], p_full[2], pv_done[2], mma_done, met[F::kSets * F::kGroups], fin, o_free;
+    uint64_t q_first, q_full[2], q_empty[2], s_full[F::kSB], p_full[2], pv_done[2], mma_done, met[F::kSets * F::kGroups], fin, o_free;
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
     alignas(16) int seen[2][F::kRows];        // positions below this are seen (rows past the last: 0)
     alignas(16) int row_at[2][F::kRows];      // token * H + head
     alignas(16) float red[2][F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
-    alignas(16) float neg_m[F::kSoftWarps][F::kRW], fac[F::kSoftWarps][F::kRW];  // each warp's own
+    alignas(16) float2 fm[F::kSoftWarps][F::kRW];  // each warp's own: a row's factor in this tile, minus its maximum
+    alignas(16) float fac[F::kSoftWarps][F::kRW];  // and what its sums are to be multiplied by
     alignas(16) float fin_l[2][F::kSets][F::kRows][4], fin_m[2][F::kSets][F::kRows];  // a set's share of an item
     float fin_unit[2][F::kSets];  // of its O^T; 0: it had no tile
     uint32_t tmem_base;
@@ -236,28 +237,30 @@ __device__ __forceinline__ void store_columns(uint32_t addr, const float (&x)[N]
     else tmem_st32(addr, u);
 }
 
+// Multiplies a row's columns, kStep apart, by x.
+template <int kN, int kStep>
+__device__ __forceinline__ void scale_columns(uint32_t addr, float x) {
+    uint32_t u[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(u[i]) : "r"(addr + i * kStep));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        asm volatile("" : "+r"(u[i]));  // (written by the wait, to the compiler)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr + i * kStep), "r"(__float_as_uint(__uint_as_float(u[i]) * x)) : "memory");
+    }
+}
+
 // This thread's logits, from the sums of products with each part of the queries (part i's rows side by side).
 template <int kQP, int kRW>
 __device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
-    if constexpr (kRW <= 16) {
-        float x[kQP * kRW];
-        load_columns<kQP * kRW>(addr, x);
+    float x[kQP * kRW];
+    load_columns<kQP * kRW>(addr, x);
 #pragma unroll
-        for (int r = 0; r < kRW; ++r) {
-            s[r] = x[(kQP - 1) * kRW + r];
+    for (int r = 0; r < kRW; ++r) {
+        s[r] = x[(kQP - 1) * kRW + r];
 #pragma unroll
-            for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
-        }
-    } else {
-        static_assert(kQP == 2 && kRW == 32, "two parts of 32 rows");
-        load_columns<32>(addr + 32, s);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float x[16];
-            load_columns<16>(addr + 16 * half, x);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[16 * half + r] = fmaf(s[16 * half + r], 0.0625f, x[r]);
-        }
+        for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
     }
 }
 
@@ -298,6 +301,69 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
     }
 }
 
+// Splits rows first, first + step, ... of an item's queries into parts, in shared memory as the products read them; lane l
+// holds columns 8l .. 8l + 7.
+template <typename T, typename F>
+__device__ __forceinline__ void split_queries(const GroupedArgs& a, const GroupedSeq& seq, const Piece& p, Ctl<F>& S, int qb, uint32_t dst,
+                                              int kc, int first, int step) {
+    constexpr int kBatch = 4;  // rows in flight
+    const int lane = threadIdx.x & 31, col = lane * 8;
+    for (int r0 = first; r0 < F::kRows; r0 += kBatch * step) {
+        // lane k looks after row r0 + k * step: its token and head
+        const int mine = r0 + (lane % kBatch) * step, row = p.row0 + mine, tok = row / a.G, head = p.h * a.G + row - tok * a.G;
+        const bool live = mine < p.rows;
+        const int64_t at = static_cast<int64_t>(seq.q0 + tok) * a.q_stride_t + static_cast<int64_t>(head) * a.q_stride_h;
+        float x[kBatch][8];
+        uint32_t top[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[k][i] = 0.0f;
+            if (r0 + k * step < p.rows && col < a.d_qk) load8(static_cast<const T*>(a.q) + from + col, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            top[k] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[k] = max(top[k], __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
+            top[k] = __reduce_max_sync(0xFFFFFFFFu, top[k]);
+        }
+        uint32_t own = 0;  // lane k: row k's
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (lane == k) own = top[k];
+        // 2^-e takes the largest element into (224, 448]; a query that is not finite becomes codes of NaN
+        auto exponent = [](uint32_t t) {
+            return t >= 0x7F800000u ? 0 : max(static_cast<int>(t >> 23) - 127 - 8, -120) + ((t & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        };
+        if (lane < kBatch && mine < F::kRows) {
+            S.q_factor[qb][mine] = __uint_as_float(static_cast<uint32_t>(127 + exponent(own)) << 23) * (a.sm_scale * 1.4426950408889634f);
+            S.seen[qb][mine] = live ? seq.len - seq.n + tok + 1 : 0;
+            S.row_at[qb][mine] = live ? (seq.q0 + tok) * a.H + head : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = r0 + k * step;
+            const bool fine = top[k] < 0x7F800000u;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent(top[k])) << 23);
+            uint32_t parts[4][F::kQP];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[k][2 * i] * down, x[k][2 * i + 1] * down, parts[i]);
+            if (r >= F::kRows || col >= kc * 128) continue;
+            const int nrow = (r / F::kRW) * (F::kQP * F::kRW) + r % F::kRW, c16 = (col & 127) >> 4;
+            const uint32_t to = dst + (col >> 7) * F::kQBytes + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
+#pragma unroll
+            for (int i = 0; i < F::kQP; ++i)  // (kRW is a multiple of 8: the parts' rows swizzle alike)
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + i * F::kRW * 128),
+                             "r"(fine ? parts[0][i] | parts[1][i] << 16 : 0x7F7F7F7Fu),
+                             "r"(fine ? parts[2][i] | parts[3][i] << 16 : 0x7F7F7F7Fu));
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 __device__ __forceinline__ void store_act(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_act(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -330,6 +396,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         for (int i = 0; i < F::kSB; ++i) mbar_init(smem_u32(&S.s_full[i]), 1);
         for (int i = 0; i < kSets * kGroups; ++i) mbar_init(smem_u32(&S.met[i]), 4);
         mbar_init(smem_u32(&S.mma_done), 1);
+        mbar_init(smem_u32(&S.q_first), F::kSoftWarps);
         mbar_init(smem_u32(&S.fin), F::kSoftWarps);
         mbar_init(smem_u32(&S.o_free), F::kSetWarps);
         S.abort_flag = 0;
@@ -483,7 +550,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const int qb = item & 1;
             while (ok && done < last) values();  // the item before that one must end for this one's queries to come
             last = n;
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(item ? &S.q_full[qb] : &S.q_first), (item >> 1) & 1, abort_flag, a.err));
             for (int tile = p.tile0; ok && tile < p.tile1; ++tile) {
                 // this buffer of logits is free: V^T P^T of tile n - kSB has been issued, after its weights came
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), phase, abort_flag, a.err));
@@ -509,83 +576,26 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         if (lane == 0) mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
-        // Two warps split the rows of the next item's queries into parts; lane l holds columns 8l .. 8l + 7.
+        // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do).
         int item = 0;
         bool ok = true;
-        const T* q = static_cast<const T*>(a.q);
-        const int col = lane * 8;
-        const bool in = col < a.d_qk;
         while (ok && next_piece(a, w, p)) {
             const int qb = item & 1;
-            constexpr int kBatch = 4;  // rows in flight
-            float x[kBatch][8];
-            int row_at[kBatch], seen[kBatch];
-            auto load = [&](int r0) {
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int r = r0 + k * F::kQWarps, row = p.row0 + r, tok = row / a.G, head = p.h * a.G + row - tok * a.G;
-                    const bool live = r < p.rows;
-                    row_at[k] = live ? (w.s.q0 + tok) * a.H + head : 0;
-                    seen[k] = live ? w.s.len - w.s.n + tok + 1 : 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[k][i] = 0.0f;
-                    if (live && in)
-                        load8(q + static_cast<int64_t>(w.s.q0 + tok) * a.q_stride_t + static_cast<int64_t>(head) * a.q_stride_h + col, x[k]);
-                }
-            };
-            load(warp - kWarpQ);
-            // (this wait lasts as long as an item; what stalls in it gives up by itself)
-            const long long t0 = clock64();
-            while (ok && !mbar_try_wait(smem_u32(&S.q_empty[qb]), ((item >> 1) & 1) ^ 1)) {
-                if (clock64() - t0 > 64 * kWaitCycles) {
-                    *abort_flag = 1;
-                    atomicOr(a.err, DSA_FAULT_TIMEOUT);
-                }
-                ok = !*abort_flag;
-                __nanosleep(64);
-            }
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-#pragma unroll 1
-            for (int r0 = warp - kWarpQ; r0 < kRows; r0 += kBatch * F::kQWarps) {
-                if (r0 >= kBatch * F::kQWarps) load(r0);
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int r = r0 + k * F::kQWarps;
-                    if (r >= kRows) break;
-                    // 2^-e takes the largest element into (224, 448]; a query that is not finite becomes codes of NaN
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
-                    top = __reduce_max_sync(0xFFFFFFFFu, top);
-                    const bool fine = top < 0x7F800000u;
-                    int e = max(static_cast<int>(top >> 23) - 127 - 8, -120);
-                    if ((top & 0x7FFFFFu) > 0x600000u) ++e;  // a significand above 1.75
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    uint32_t parts[4][F::kQP];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[k][2 * i] * down, x[k][2 * i + 1] * down, parts[i]);
-                    if (col < kc * 128) {
-                        const uint32_t chunk = sQ + (qb * kc + (col >> 7)) * F::kQBytes;
-                        const int nrow = (r / kRW) * (F::kQP * kRW) + r % kRW, c16 = (col & 127) >> 4;
-#pragma unroll
-                        for (int i = 0; i < F::kQP; ++i) {  // (kRW is a multiple of 8: the parts' rows swizzle alike)
-                            const uint32_t at = chunk + (nrow + i * kRW) * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at),
-                                         "r"(fine ? parts[0][i] | parts[1][i] << 16 : 0x7F7F7F7Fu),
-                                         "r"(fine ? parts[2][i] | parts[3][i] << 16 : 0x7F7F7F7Fu)
-                                         : "memory");
-                        }
+            if (item > 0) {
+                // (this wait lasts as long as an item; what stalls in it gives up by itself)
+                const long long t0 = clock64();
+                while (ok && !mbar_try_wait(smem_u32(&S.q_empty[qb]), ((item >> 1) & 1) ^ 1)) {
+                    if (clock64() - t0 > 64 * kWaitCycles) {
+                        *abort_flag = 1;
+                        atomicOr(a.err, DSA_FAULT_TIMEOUT);
                     }
-                    if (lane == 0) {
-                        S.q_factor[qb][r] = __uint_as_float(static_cast<uint32_t>(127 + (fine ? e : 0)) << 23) * (a.sm_scale * 1.4426950408889634f);
-                        S.seen[qb][r] = seen[k];
-                        S.row_at[qb][r] = row_at[k];
-                    }
+                    ok = !*abort_flag;
+                    __nanosleep(64);
                 }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                split_queries<T, F>(a, w.s, p, S, qb, sQ + qb * kc * F::kQBytes, kc, warp - kWarpQ, F::kQWarps);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.q_full[qb]));
             ++item;
         }
@@ -595,7 +605,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         const int j = quarter * 32 + lane;  // position of the tile, TMEM lane
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_col = lane_base + F::kColO + group * F::kPP * kRW;
-        float* neg_m = S.neg_m[warp];
+        float2* fm = S.fm[warp];
         float* fac = S.fac[warp];
         int n = set, n_item = 0, st = set, sphase = 0, item = 0, met = 0, turn = 0;  // n: this set's next tile, n_item: the item's first
         bool ok = true;
@@ -608,13 +618,15 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         };
         while (ok && next_piece(a, w, p)) {
             const int qb = item & 1, n_end = n_item + p.tile1 - p.tile0, len = w.s.len;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            if (item == 0) {
+                split_queries<T, F>(a, w.s, p, S, 0, sQ, kc, warp, F::kSoftWarps);
+                if (lane == 0) mbar_arrive(smem_u32(&S.q_first));
+            }
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(item ? &S.q_full[qb] : &S.q_first), (item >> 1) & 1, abort_flag, a.err));
             float l[kRW], v_ref = 7.8886090522101181e-31f;  // 2^-100
             float m = -INFINITY;                              // of row lane % kRW
 #pragma unroll
             for (int r = 0; r < kRW; ++r) l[r] = 0.0f;
-            __syncwarp();
-            if (lane < kRW) neg_m[lane] = 0.0f;
             const float* factor = S.q_factor[qb] + group * kRW;
             const int* seen = S.seen[qb] + group * kRW;
             // every row sees the positions below this
@@ -637,7 +649,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const float4 sc = S.scales[st];
                 const int valid = S.valid[st], pos = tile * kGroupedTile + j;
                 const bool here = (valid >> (quarter >> 1)) & 1 && pos < len;
-                const float ks = !here ? 1.0f : quarter < 2 ? sc.x : sc.y;
                 float s[kRW];
                 load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, s);
                 if (valid != 3 || (tile + 1) * kGroupedTile > all_see) {
@@ -652,12 +663,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         }
                     }
                 }
-                if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
-                    float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
-#pragma unroll
-                    for (int r = 0; r < kRW; ++r)
-                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * (factor[r] * ks);
-                }
                 // The rows' maxima over the tile: every warp's, then lane r of each warp looks after row r. A factor is
                 // positive and the same for a warp's positions.
                 float top = -INFINITY;
@@ -666,8 +671,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     const float x = warp_max(s[r]);
                     if (lane == r) top = x;
                 }
-                const float k_warp = quarter < 2 ? (valid & 1 ? sc.x : 1.0f) : (valid & 2 ? sc.y : 1.0f);
-                if (lane < kRW) S.red[turn][set * kGroups + group][lane][quarter] = top * (factor[lane] * k_warp);
+                const float f = factor[lane % kRW] * (quarter < 2 ? (valid & 1 ? sc.x : 1.0f) : (valid & 2 ? sc.y : 1.0f));
+                if (lane < kRW) S.red[turn][set * kGroups + group][lane][quarter] = top * f;
                 group_sync();
                 if (!ok) break;
                 const float4 t = *reinterpret_cast<const float4*>(S.red[turn][set * kGroups + group][lane % kRW]);
@@ -675,22 +680,21 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
                 // The weights carry their block's value scale, against a power of two no smaller than any so far.
                 const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
-                const bool grown = __any_sync(0xFFFFFFFFu, m_new > m) || v_top > v_ref;
+                const uint32_t rows_up = __ballot_sync(0xFFFFFFFFu, m_new > m && lane < kRW);
+                if (lane < kRW) fm[lane] = make_float2(f, m_new == -INFINITY ? 0.0f : -m_new);
                 // this buffer of weights has been read, and O^T is this set's to rescale
                 if (n >= 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
                 if (fresh) wait_free();
                 if (!ok) break;
-                if (grown) {  // the same for all of the group's threads
+                if (rows_up || v_top > v_ref) {  // the same for all of the group's threads
                     float v_fac = 1.0f;
                     if (v_top > v_ref) {
                         const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
                         v_fac = v_ref / ref;
                         v_ref = ref;
                     }
-                    if (lane < kRW) {
-                        fac[lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
-                        neg_m[lane] = m_new == -INFINITY ? 0.0f : -m_new;
-                    }
+                    const float up = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
+                    if (lane < kRW) fac[lane] = up;
                     m = m_new;
                     __syncwarp();
                     if (!fresh) {
@@ -701,21 +705,37 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             if (!ok) break;
                         }
                         tc_fence_after();
-                        for (int c = 0; c < vc; ++c) {
+                        if (v_fac == 1.0f && __popc(rows_up) <= kRW / 4) {  // few rows: their columns alone
+                            for (uint32_t left = rows_up; left; left &= left - 1) {
+                                const int r = __ffs(left) - 1;
+                                const float x = __shfl_sync(0xFFFFFFFFu, up, r);
+                                for (int c = 0; c < vc; ++c) scale_columns<F::kPP, kRW>(o_col + (set * F::kVCMax + c) * F::kPN + r, x);
+                            }
+                        } else {
+                            for (int c = 0; c < vc; ++c) {
 #pragma unroll
-                            for (int i = 0; i < F::kPP; ++i) {
-                                float o[kRW];
-                                const uint32_t at = o_col + (set * F::kVCMax + c) * F::kPN + i * kRW;
-                                load_columns<kRW>(at, o);
+                                for (int i = 0; i < F::kPP; ++i) {
+                                    float o[kRW];
+                                    const uint32_t at = o_col + (set * F::kVCMax + c) * F::kPN + i * kRW;
+                                    load_columns<kRW>(at, o);
 #pragma unroll
-                                for (int r = 0; r < kRW; ++r) o[r] *= fac[r] * v_fac;
-                                store_columns<kRW>(at, o);
+                                    for (int r = 0; r < kRW; ++r) o[r] *= fac[r] * v_fac;
+                                    store_columns<kRW>(at, o);
+                                }
                             }
                         }
                         tmem_st_wait();
                     }
+                } else {
+                    __syncwarp();
                 }
                 fresh = false;
+                if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
+                    float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r)
+                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * fm[r].x;
+                }
                 const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (256.0f / v_ref) : 0.0f;
                 const uint32_t p_buf = sP + (n & 1) * F::kPBytes + j * 16;
                 constexpr int kChunkRows = kRW < 16 ? 8 : 16;
@@ -725,8 +745,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kChunkRows / 2; ++i) {
                         const int r = r0 + 2 * i;
-                        const float p0 = ex2(fmaf(s[r], factor[r] * ks, neg_m[r]));
-                        const float p1 = ex2(fmaf(s[r + 1], factor[r + 1] * ks, neg_m[r + 1]));
+                        const float4 g = *reinterpret_cast<const float4*>(fm + r);
+                        const float p0 = ex2(fmaf(s[r], g.x, g.y)), p1 = ex2(fmaf(s[r + 1], g.z, g.w));
                         l[r] += p0;
                         l[r + 1] += p1;
                         split_pair<F::kPP>(p0 * tv, p1 * tv, parts[i]);
@@ -886,8 +906,8 @@ bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches) {
         switch (a.row_tile) {
             case 8: ok = launch_form<__nv_bfloat16, Form<8, 1, 2, 2, 3, 4>>(a, s); break;
             case 16: ok = launch_form<__nv_bfloat16, Form<16, 1, 2, 2, 3, 4>>(a, s); break;
-            case 32: ok = launch_form<__nv_bfloat16, Form<32, 1, 2, 2, 3, 2>>(a, s); break;
-            default: ok = launch_form<__nv_bfloat16, Form<32, 2, 1, 2, 3, 2>>(a, s); break;
+            case 32: ok = launch_form<__nv_bfloat16, Form<16, 2, 2, 2, 3, 2>>(a, s); break;
+            default: ok = launch_form<__nv_bfloat16, Form<16, 4, 1, 2, 3, 2>>(a, s); break;
         }
     }
     if (ok) ++*launches;
