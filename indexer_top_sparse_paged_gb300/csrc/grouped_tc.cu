@@ -19,6 +19,8 @@
 // item's queries, and the softmax's warps, kRW rows a thread, take tiles in turn in kSets sets, each with a maximum, a sum
 // and an O^T of its own: the chain logits -> maximum -> weights of one tile (about 1500 cycles) is longer than its bytes
 // take (1400). The set that has an item's last tile puts the two together.
+#include <cstddef>
+
 #include "grouped.cuh"
 
 namespace dsa {
@@ -84,8 +86,9 @@ struct Form {
 
 template <typename F>
 struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_first, q_full[2], q_empty[2], s_full[F::kSB], p_full[2], pv_done[2], mma_done, met[F::kSets * F::kGroups], fin, o_free;
+    // barriers, with their arrivals in barrier_count
+    uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[2], mma_done;
+    uint64_t q_full[2], met[F::kSets * F::kGroups], p_full[2], o_free, q_first, fin, q_empty[2];
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
@@ -100,8 +103,18 @@ struct Ctl {
     int abort_flag;
     int64_t warp_sums[F::kThreads / 32];
     int64_t found[2];
-    Walk start;
 };
+
+template <typename F>
+__device__ __forceinline__ int barrier_count(int i) {
+    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kMet = kOnes + 2, kSet = kMet + F::kSets * F::kGroups, kSoft = kSet + 3, kLast = kSoft + 2;
+    static_assert(offsetof(Ctl<F>, q_empty) == kLast * 8, "barriers in order");
+    if (i < kOnes) return 1;
+    if (i < kMet) return F::kQWarps;
+    if (i < kSet) return 4;                 // a group's warps
+    if (i < kSoft) return F::kSetWarps;     // p_full, o_free
+    return i < kLast ? F::kSoftWarps : 1 + F::kSoftWarps;  // q_empty: the products that read it, too
+}
 
 template <typename F>
 struct Layout {  // byte offsets; kc, vc: chunks of 128 columns of keys and values
@@ -286,79 +299,81 @@ __device__ __forceinline__ float sum_rows(float (&x)[kRW], int lane) {
 // queries and outputs
 // ------------------------------------------------------------------------------------------------
 
-// 8 elements of a query row.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// 8 elements of a query row, as they are loaded.
+template <typename T>
+struct Elements;
+template <>
+struct Elements<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
-}
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <>
+struct Elements<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
 
 // Splits rows first, first + step, ... of an item's queries into parts, in shared memory as the products read them; lane l
 // holds columns 8l .. 8l + 7.
 template <typename T, typename F>
 __device__ __forceinline__ void split_queries(const GroupedArgs& a, const GroupedSeq& seq, const Piece& p, Ctl<F>& S, int qb, uint32_t dst,
                                               int kc, int first, int step) {
-    constexpr int kBatch = 4;  // rows in flight
+    // (a rolled loop, the next row's elements on their way: its instructions are fetched once)
     const int lane = threadIdx.x & 31, col = lane * 8;
-    for (int r0 = first; r0 < F::kRows; r0 += kBatch * step) {
-        // lane k looks after row r0 + k * step: its token and head
-        const int mine = r0 + (lane % kBatch) * step, row = p.row0 + mine, tok = row / a.G, head = p.h * a.G + row - tok * a.G;
-        const bool live = mine < p.rows;
-        const int64_t at = static_cast<int64_t>(seq.q0 + tok) * a.q_stride_t + static_cast<int64_t>(head) * a.q_stride_h;
-        float x[kBatch][8];
-        uint32_t top[kBatch];
+    // lane k looks after row first + k * step: its token and head
+    const int mine = first + lane * step, row = p.row0 + mine, tok = row / a.G, head = p.h * a.G + row - tok * a.G;
+    const bool live = mine < p.rows;
+    const int64_t at = static_cast<int64_t>(seq.q0 + tok) * a.q_stride_t + static_cast<int64_t>(head) * a.q_stride_h;
+    if (mine < F::kRows) {
+        S.seen[qb][mine] = live ? seq.len - seq.n + tok + 1 : 0;
+        S.row_at[qb][mine] = live ? (seq.q0 + tok) * a.H + head : 0;
+    }
+    Elements<T> next;
+    auto load = [&](int k) {
+        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k);
+        next = Elements<T>{};
+        if (first + k * step < p.rows && col < a.d_qk) next.load(static_cast<const T*>(a.q) + from + col);
+    };
+    load(0);
+#pragma unroll 1
+    for (int k = 0, r = first; r < F::kRows; ++k, r += step) {
+        float x[8];
+        next.values(x);
+        load((k + 1) & 31);
+        uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int64_t from = __shfl_sync(0xFFFFFFFFu, at, k);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][i] = 0.0f;
-            if (r0 + k * step < p.rows && col < a.d_qk) load8(static_cast<const T*>(a.q) + from + col, x[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            top[k] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top[k] = max(top[k], __float_as_uint(x[k][i]) & 0x7FFFFFFFu);
-            top[k] = __reduce_max_sync(0xFFFFFFFFu, top[k]);
-        }
-        uint32_t own = 0;  // lane k: row k's
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (lane == k) own = top[k];
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
         // 2^-e takes the largest element into (224, 448]; a query that is not finite becomes codes of NaN
-        auto exponent = [](uint32_t t) {
-            return t >= 0x7F800000u ? 0 : max(static_cast<int>(t >> 23) - 127 - 8, -120) + ((t & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        };
-        if (lane < kBatch && mine < F::kRows) {
-            S.q_factor[qb][mine] = __uint_as_float(static_cast<uint32_t>(127 + exponent(own)) << 23) * (a.sm_scale * 1.4426950408889634f);
-            S.seen[qb][mine] = live ? seq.len - seq.n + tok + 1 : 0;
-            S.row_at[qb][mine] = live ? (seq.q0 + tok) * a.H + head : 0;
-        }
+        const bool fine = top < 0x7F800000u;
+        const int e = !fine ? 0 : max(static_cast<int>(top >> 23) - 127 - 8, -120) + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        if (lane == 0) S.q_factor[qb][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.sm_scale * 1.4426950408889634f);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        uint32_t parts[4][F::kQP];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int r = r0 + k * step;
-            const bool fine = top[k] < 0x7F800000u;
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent(top[k])) << 23);
-            uint32_t parts[4][F::kQP];
+        for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[2 * i] * down, x[2 * i + 1] * down, parts[i]);
+        if (col >= kc * 128) continue;
+        const int nrow = (r / F::kRW) * (F::kQP * F::kRW) + r % F::kRW, c16 = (col & 127) >> 4;
+        const uint32_t to = dst + (col >> 7) * F::kQBytes + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[k][2 * i] * down, x[k][2 * i + 1] * down, parts[i]);
-            if (r >= F::kRows || col >= kc * 128) continue;
-            const int nrow = (r / F::kRW) * (F::kQP * F::kRW) + r % F::kRW, c16 = (col & 127) >> 4;
-            const uint32_t to = dst + (col >> 7) * F::kQBytes + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
-#pragma unroll
-            for (int i = 0; i < F::kQP; ++i)  // (kRW is a multiple of 8: the parts' rows swizzle alike)
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + i * F::kRW * 128),
-                             "r"(fine ? parts[0][i] | parts[1][i] << 16 : 0x7F7F7F7Fu),
-                             "r"(fine ? parts[2][i] | parts[3][i] << 16 : 0x7F7F7F7Fu));
-        }
+        for (int i = 0; i < F::kQP; ++i)  // (kRW is a multiple of 8: the parts' rows swizzle alike)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + i * F::kRW * 128),
+                         "r"(fine ? parts[0][i] | parts[1][i] << 16 : 0x7F7F7F7Fu),
+                         "r"(fine ? parts[2][i] | parts[3][i] << 16 : 0x7F7F7F7Fu));
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -382,73 +397,67 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     volatile int* abort_flag = &S.abort_flag;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(smem_u32(&S.full[i]), 1);
-            mbar_init(smem_u32(&S.empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&S.q_full[i]), F::kQWarps);
-            mbar_init(smem_u32(&S.q_empty[i]), 1 + F::kSoftWarps);  // the products that read it, and the softmax
-            mbar_init(smem_u32(&S.p_full[i]), F::kSetWarps);
-            mbar_init(smem_u32(&S.pv_done[i]), 1);
-        }
-        for (int i = 0; i < F::kSB; ++i) mbar_init(smem_u32(&S.s_full[i]), 1);
-        for (int i = 0; i < kSets * kGroups; ++i) mbar_init(smem_u32(&S.met[i]), 4);
-        mbar_init(smem_u32(&S.mma_done), 1);
-        mbar_init(smem_u32(&S.q_first), F::kSoftWarps);
-        mbar_init(smem_u32(&S.fin), F::kSoftWarps);
-        mbar_init(smem_u32(&S.o_free), F::kSetWarps);
-        S.abort_flag = 0;
-        fence_mbar_init();
-    }
     constexpr int kWarpLoad = F::kSoftWarps, kWarpMma = kWarpLoad + 1, kWarpQ = kWarpLoad + 2;
-    if (warp == kWarpMma) {
+    if (warp == 0) {
+        for (int i = lane; i * 8 < static_cast<int>(offsetof(Ctl<F>, q_empty)) + 16; i += 32)
+            mbar_init(smem_u32(&S) + i * 8, barrier_count<F>(i));
+        if (lane == 0) S.abort_flag = 0;
+        fence_mbar_init();
+    } else if (warp == kWarpMma) {
         tmem_alloc(smem_u32(&S.tmem_base), F::kTmemCols);
         tmem_relinquish();
-    }
-    if (warp == kWarpLoad && lane == 0) {
+    } else if (warp == kWarpLoad && lane == 0) {
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
     }
     griddep_launch_dependents();
-    // this CTA's share
-    int64_t total, base;
-    int b0;
-    const int64_t begin = find_place<F::kThreads>(
-        a.B, [&](int b) { return grouped_seq_tiles(a, grouped_seq(a, b, blockIdx.x == 0)); },
-        [&](int64_t all) { return grouped_share(a, all) * blockIdx.x; }, &total, &b0, &base, S.warp_sums, S.found);
-    const int64_t per = grouped_share(a, total), end = min(total, begin + per);
-    if (threadIdx.x == kWarpQ * 32) {
-        Walk w{};
-        GroupedCut cut{};
-        if (begin < end) {
-            w.s = grouped_seq(a, b0, false);
-            w.b = b0;
-            const int64_t local = begin - base;
-            w.item = local < (1ll << 31) ? static_cast<int>(local) / w.s.tiles : static_cast<int>(local / w.s.tiles);
-            w.tile = static_cast<int>(local - static_cast<int64_t>(w.item) * w.s.tiles);
-            w.left = end - begin;
-            w.t = begin;
-            // word of the item that the share's begin cuts, for the join (of the first share that cuts it)
-            const int64_t u0 = begin - w.tile, u1 = u0 + w.s.tiles;
-            if (w.tile > 0 && begin - per <= u0) {
-                Walk w1 = w;
-                Piece p1;
-                next_piece(a, w1, p1);
-                int parts = 2;  // (the shares that hold a tile of it; begin < u1)
-                while (begin + (parts - 1) * per < u1) ++parts;
-                cut = GroupedCut{w.s.q0, p1.h, p1.row0, p1.rows, grouped_slot(begin - per, u0, blockIdx.x - 1), parts, {0, 0}};
-            }
+    // This CTA's share. Few sequences: every warp finds it for itself.
+    Walk w{};
+    int64_t per, begin;
+    if (a.B <= 32) {
+        if (lane < a.B) w.s = grouped_seq(a, lane, blockIdx.x == 0 && warp == 0);
+        const int64_t n = grouped_seq_tiles(a, w.s);
+        int64_t x = n;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
         }
-        S.start = w;
-        a.cuts[blockIdx.x] = cut;
+        const int64_t total = __shfl_sync(0xFFFFFFFFu, x, 31);
+        per = grouped_share(a, total);
+        begin = per * blockIdx.x;
+        w.left = min(total, begin + per) - begin;
+        // the last sequence that begins at or before the share does and has tiles there
+        w.b = __ffs(__ballot_sync(0xFFFFFFFFu, begin >= x - n && begin < x)) - 1;
+        const int from = max(w.b, 0);
+        const int64_t local = begin - __shfl_sync(0xFFFFFFFFu, x - n, from);
+        w.s.q0 = __shfl_sync(0xFFFFFFFFu, w.s.q0, from);
+        w.s.n = __shfl_sync(0xFFFFFFFFu, w.s.n, from);
+        w.s.len = __shfl_sync(0xFFFFFFFFu, w.s.len, from);
+        w.s.items = __shfl_sync(0xFFFFFFFFu, w.s.items, from);
+        w.s.tiles = __shfl_sync(0xFFFFFFFFu, w.s.tiles, from);
+        w.t = local;
+        tc_fence_before();
+        block_sync();
+    } else {
+        int64_t total, base;
+        begin = find_place<F::kThreads>(
+            a.B, [&](int b) { return grouped_seq_tiles(a, grouped_seq(a, b, blockIdx.x == 0)); },
+            [&](int64_t all) { return grouped_share(a, all) * blockIdx.x; }, &total, &w.b, &base, S.warp_sums, S.found);
+        per = grouped_share(a, total);
+        w.left = min(total, begin + per) - begin;
+        if (w.left > 0) w.s = grouped_seq(a, w.b, false);
+        w.t = begin - base;
+        tc_fence_before();
+        block_sync();
     }
-    tc_fence_before();
-    block_sync();
     tc_fence_after();
+    if (w.left > 0) {  // (w.t: the share's begin in its sequence's tiles)
+        w.item = w.t < (1ll << 31) ? static_cast<int>(w.t) / w.s.tiles : static_cast<int>(w.t / w.s.tiles);
+        w.tile = static_cast<int>(w.t - static_cast<int64_t>(w.item) * w.s.tiles);
+    }
+    w.t = begin;
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, S.tmem_base, 0);
-    Walk w = S.start;
     Piece p;
 
     if (warp == kWarpLoad) {
@@ -576,7 +585,21 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         if (lane == 0) mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
-        // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do).
+        // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do). First,
+        // word of the item that the share's begin cuts, for the join (of the first share that cuts it).
+        if (threadIdx.x == kWarpQ * 32) {
+            GroupedCut cut{};
+            const int64_t u0 = begin - w.tile, u1 = u0 + w.s.tiles;
+            if (w.left > 0 && w.tile > 0 && begin - per <= u0) {
+                Walk w1 = w;
+                next_piece(a, w1, p);
+                int parts = 2;  // the shares that hold a tile of it (begin < u1)
+                while (begin + (parts - 1) * per < u1) ++parts;
+                cut = GroupedCut{w.s.q0, p.h, p.row0, p.rows, grouped_slot(begin - per, u0, blockIdx.x - 1), parts, {0, 0}};
+            }
+            a.cuts[blockIdx.x] = cut;
+        }
+        __syncwarp();
         int item = 0;
         bool ok = true;
         while (ok && next_piece(a, w, p)) {
