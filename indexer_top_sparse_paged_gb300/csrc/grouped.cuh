@@ -126,36 +126,8 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
     return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// 16 codes as fp32 values (exact).
-__device__ __forceinline__ void e4m3x16_values(const uint4& in, float (&x)[16]) {
-    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-        const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
 // The scale that takes amax to the largest code.
 __device__ __forceinline__ float unit_scale(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
-
-// Division by one value many times, correctly rounded, in three operations: with r = 1 / s correctly rounded and q = x r,
-// q + r (x - q s) is x / s correctly rounded (Markstein's theorem), where nothing underflows or overflows. Scales outside
-// [2^-80, 2^80] divide as usual. (A dividend so small that its remainder underflows has a quotient far below the smallest
-// code's half, and becomes the code 0 either way.)
-struct Divisor {
-    float value, r;
-    bool plain;
-    __device__ __forceinline__ explicit Divisor(float s)
-        : value(s), r(1.0f / s), plain(!(s >= 8.271806125530277e-25f && s <= 1.2089258196146292e24f)) {}
-    __device__ __forceinline__ float operator()(float x) const {
-        const float q = x * r, y = fmaf(r, fmaf(-q, value, x), q);
-        return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // (-0 / s comes out as +0)
-    }
-};
 
 __device__ __forceinline__ uint32_t e4m3x4_codes(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -163,17 +135,66 @@ __device__ __forceinline__ uint32_t e4m3x4_codes(float a, float b, float c, floa
     return lo | hi << 16;
 }
 
-// RNE_e4m3(x / scale) of 16 values, saturating at +-448.
-__device__ __forceinline__ uint4 codes16(float (&x)[16], const Divisor& scale) {
-    if (scale.plain) {
+// Rounded quotients without the division, checked: the formulas' results are off the exact quotient by two roundings of
+// 2^-24 at most, relatively, and x times (1 / scale, drawn in or out by 2^-21) by four, so the two products enclose them.
+// Where both round to the same code, so does the formula's result; where they do not (a value next to the middle of two
+// codes, one in some 2^17), the formula is followed. (Underflowing products belong to the code 0 either way.)
+constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {  // one instruction
+    uint64_t x, y, z;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(z));
+    return a;
+}
+
+// Codes of 16 values times r; false: some lie too near the middle of two codes.
+__device__ __forceinline__ bool near_codes(const float2 (&x)[8], float r, uint4* codes) {
+    const float2 below = make_float2(r * kBelow, r * kBelow), above = make_float2(r * kAbove, r * kAbove);
+    uint32_t w[4], differ = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] /= scale.value;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = scale(x[i]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 a0 = mul2(x[2 * i], below), a1 = mul2(x[2 * i + 1], below);
+        const float2 b0 = mul2(x[2 * i], above), b1 = mul2(x[2 * i + 1], above);
+        w[i] = e4m3x4_codes(a0.x, a0.y, a1.x, a1.y);
+        differ |= w[i] ^ e4m3x4_codes(b0.x, b0.y, b1.x, b1.y);
     }
-    return make_uint4(e4m3x4_codes(x[0], x[1], x[2], x[3]), e4m3x4_codes(x[4], x[5], x[6], x[7]),
-                      e4m3x4_codes(x[8], x[9], x[10], x[11]), e4m3x4_codes(x[12], x[13], x[14], x[15]));
+    *codes = make_uint4(w[0], w[1], w[2], w[3]);
+    return differ == 0;
+}
+
+static __device__ __noinline__ uint4 divided_codes(float2 x0, float2 x1, float2 x2, float2 x3, float2 x4, float2 x5, float2 x6, float2 x7, float s) {
+    return make_uint4(e4m3x4_codes(x0.x / s, x0.y / s, x1.x / s, x1.y / s), e4m3x4_codes(x2.x / s, x2.y / s, x3.x / s, x3.y / s),
+                      e4m3x4_codes(x4.x / s, x4.y / s, x5.x / s, x5.y / s), e4m3x4_codes(x6.x / s, x6.y / s, x7.x / s, x7.y / s));
+}
+
+// Scales whose reciprocal, and products with it, neither overflow nor lose bits: the others divide.
+__device__ __forceinline__ bool plain_scale(float scale) { return scale >= 0x1p-80f && scale <= 0x1p80f; }
+
+// RNE_e4m3(x / scale) of 16 values, saturating at +-448.
+__device__ __forceinline__ uint4 codes16(const float2 (&x)[8], float scale) {
+    uint4 codes;
+    if (plain_scale(scale) && near_codes(x, 1.0f / scale, &codes)) return codes;
+    return divided_codes(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
+}
+
+// RNE_e4m3(fl(code * from) / scale) of 16 codes, saturating; per: 1 / scale.
+__device__ __forceinline__ uint4 requantise16(const uint4& in, float from, float scale, float per) {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    float2 x[8];
+    uint4 codes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+        x[i] = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    }
+    const float r = from * per;
+    if (plain_scale(scale) && plain_scale(from) && r <= 0x1p100f && near_codes(x, r, &codes)) return codes;  // (codes of 0 may have any scale)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i].x *= from, x[i].y *= from;
+    return divided_codes(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
 }
 
 }  // namespace dsa

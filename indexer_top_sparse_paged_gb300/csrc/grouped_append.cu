@@ -10,23 +10,22 @@ namespace dsa {
 
 constexpr int kGroupedAppendThreads = 256;
 
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+// 16 elements of a new row.
+__device__ __forceinline__ void load16(const float* p, float2 (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float4 v = reinterpret_cast<const float4*>(p)[i];
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        x[2 * i] = make_float2(v.x, v.y);
+        x[2 * i + 1] = make_float2(v.z, v.w);
     }
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float2 (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint4 v = reinterpret_cast<const uint4*>(p)[i];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
+        for (int j = 0; j < 4; ++j) x[4 * i + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
     }
 }
 
@@ -86,10 +85,10 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
     float* scale_at = (value ? a.v_scale : a.k_scale) + bh;
     float amax = 0.0f;
     for (int i = tid; i < n; i += kGroupedAppendThreads) {
-        float y[16];
+        float2 y[8];
         load16(x + (i / groups) * st + (i % groups) * 16, y);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(y[j]));
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -98,22 +97,18 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kGroupedAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    const Divisor scale(slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax));
+    const float scale = slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax);
     for (int i = tid; i < n; i += kGroupedAppendThreads) {
-        float y[16];
+        float2 y[8];
         load16(x + (i / groups) * st + (i % groups) * 16, y);
         codes[slot0 * groups + i] = codes16(y, scale);
     }
-    if (slot0 && scale.value > old) {
+    if (slot0 && scale > old) {
         for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) {
-            float y[16];
-            e4m3x16_values(codes[i], y);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] *= old;
-            codes[i] = codes16(y, scale);
+            codes[i] = requantise16(codes[i], old, scale, 1.0f / scale);
         }
     }
-    if (tid == 0) *scale_at = scale.value;
+    if (tid == 0) *scale_at = scale;
 }
 
 bool launch_grouped_append(const GroupedAppendArgs& a, cudaStream_t s, int* launches) {

@@ -15,19 +15,25 @@
 
 namespace dsa {
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
+static_assert(kSelectWarps == 32, "a lane for every warp");
 constexpr int kSelectBins = 2048;
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectKeys = 49152;  // keys that shared memory holds, beside the histograms
+constexpr int kSelectBatch = 8;     // of a thread's, in flight
 constexpr int kMoveThreads = 256;
 
 // Order of the weights as unsigned integers; NaN is the lowest, together with -infinity.
 __device__ __forceinline__ uint32_t weight_key(float w) { return ordered_bits(w != w ? -INFINITY : w); }
 
+// The weight of a key that is not -infinity's (-0 comes back as 0).
+__device__ __forceinline__ float key_weight(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+constexpr uint32_t kLowestKey = 0x007FFFFFu;  // that of -infinity and of NaN
+
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 
@@ -45,11 +51,17 @@ __device__ __forceinline__ void find_bin(SelectShared& S, int pass, int ctas, ui
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int first = kSelectBins - kPer * (tid + 1);  // thread 0 has the top bins
     uint32_t n[kPer] = {};
-    for (int c = 0; c < ctas; ++c) {
-        const uint32_t at = mapa_shared(smem_u32(&S.hist[pass][first]), c);
+    uint32_t theirs[kSelectMaxCluster][kPer];  // (all on their way at once)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) n[i] += ld_cluster_u32(at + 4 * i);
+    for (int c = 0; c < kSelectMaxCluster; ++c) {
+        const uint32_t at = mapa_shared(smem_u32(&S.hist[pass][first]), c < ctas ? c : 0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) theirs[c][i] = c < ctas ? ld_cluster_u32(at + 4 * i) : 0;
     }
+#pragma unroll
+    for (int c = 0; c < kSelectMaxCluster; ++c)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n[i] += theirs[c][i];
     uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += n[i];
@@ -61,8 +73,7 @@ __device__ __forceinline__ void find_bin(SelectShared& S, int pass, int ctas, ui
     }
     if (lane == 31) S.warp_sums[warp] = x;
     __syncthreads();
-    uint32_t before = x - mine;
-    for (int w = 0; w < warp; ++w) before += S.warp_sums[w];
+    uint32_t before = x - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? S.warp_sums[lane] : 0);
     if (before < need && need <= before + mine) {
 #pragma unroll
         for (int i = kPer - 1; i >= 0; --i) {
@@ -111,28 +122,40 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
     if (want > 0) {
         for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) S.hist[0][i] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
-            const uint32_t k = weight_key(w[i]);
-            if (i - r0 < cached) keys[i - r0] = k;
-            if (i >= lo && i < hi) atomicAdd(&S.hist[0][k >> 21], 1u);
+        for (int i0 = r0 + tid; i0 < r1; i0 += kSelectBatch * kSelectThreads) {
+            float x[kSelectBatch];
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e) x[e] = i0 + e * kSelectThreads < r1 ? w[i0 + e * kSelectThreads] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e) {
+                const int i = i0 + e * kSelectThreads;
+                if (i >= r1) break;
+                const uint32_t k = weight_key(x[e]);
+                if (i - r0 < cached) keys[i - r0] = k;
+                if (i >= lo && i < hi) atomicAdd(&S.hist[0][k >> 21], 1u);
+            }
         }
         cluster_sync_all();
         find_bin(S, 0, ctas, need);
         prefix = S.bin, need = S.need;
-        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
-            const uint32_t k = key_at(i);
-            if (k >> 21 == prefix && i >= lo && i < hi) atomicAdd(&S.hist[1][(k >> 10) & 2047], 1u);
-        }
-        cluster_sync_all();
-        find_bin(S, 1, ctas, need);
+        // the next bits of the positions that agree so far
+        auto next_pass = [&](int pass, int above, int shift, uint32_t mask) {
+            for (int i0 = r0 + tid; i0 < r1; i0 += kSelectBatch * kSelectThreads) {
+                uint32_t k[kSelectBatch];
+#pragma unroll
+                for (int e = 0; e < kSelectBatch; ++e) k[e] = i0 + e * kSelectThreads < r1 ? key_at(i0 + e * kSelectThreads) : 0;
+#pragma unroll
+                for (int e = 0; e < kSelectBatch; ++e) {
+                    const int i = i0 + e * kSelectThreads;
+                    if (i < r1 && k[e] >> above == prefix && i >= lo && i < hi) atomicAdd(&S.hist[pass][(k[e] >> shift) & mask], 1u);
+                }
+            }
+            cluster_sync_all();
+            find_bin(S, pass, ctas, need);
+        };
+        next_pass(1, 21, 10, 2047);
         prefix = prefix << 11 | S.bin, need = S.need;
-        for (int i = r0 + tid; i < r1; i += kSelectThreads) {
-            const uint32_t k = key_at(i);
-            if (k >> 10 == prefix && i >= lo && i < hi) atomicAdd(&S.hist[2][k & 1023], 1u);
-        }
-        cluster_sync_all();
-        find_bin(S, 2, ctas, need);
+        next_pass(2, 10, 0, 1023);
         prefix = prefix << 10 | S.bin, need = S.need;  // the last kept weight's key; how many of its equals are kept
     } else {
         prefix = 0xFFFFFFFFu;  // above every key: positions are kept by their place alone
@@ -141,6 +164,7 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
     const int part = ((r1 - r0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
     const int p0 = min(r1, r0 + warp * part), p1 = min(r1, p0 + part);
     uint32_t above = 0, equal = 0;
+#pragma unroll 4
     for (int i0 = p0; i0 < p1; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0;
@@ -150,22 +174,18 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
     }
     if (lane == 0) S.warp_counts[warp][0] = above, S.warp_counts[warp][1] = equal;
     __syncthreads();
-    if (tid < 2) {
-        uint32_t sum = 0;
-        for (int i = 0; i < kSelectWarps; ++i) sum += S.warp_counts[i][tid];
-        S.counts[tid] = sum;
+    const uint32_t warp_above = S.warp_counts[lane][0], warp_equal = S.warp_counts[lane][1];
+    if (warp == 0) {
+        const uint32_t all_above = __reduce_add_sync(0xFFFFFFFFu, warp_above), all_equal = __reduce_add_sync(0xFFFFFFFFu, warp_equal);
+        if (lane == 0) S.counts[0] = all_above, S.counts[1] = all_equal;
     }
     cluster_sync_all();
-    uint32_t above_before = 0, equal_before = 0;
-    for (int c = 0; c < rank; ++c) {
-        const uint32_t at = mapa_shared(smem_u32(S.counts), c);
-        above_before += ld_cluster_u32(at);
-        equal_before += ld_cluster_u32(at + 4);
-    }
-    for (int i = 0; i < warp; ++i) {
-        above_before += S.warp_counts[i][0];
-        equal_before += S.warp_counts[i][1];
-    }
+    // lane c: the counts of CTA c
+    const uint32_t at = mapa_shared(smem_u32(S.counts), lane < rank ? lane : 0);
+    const uint32_t cta_above = lane < rank ? ld_cluster_u32(at) : 0, cta_equal = lane < rank ? ld_cluster_u32(at + 4) : 0;
+    uint32_t above_before = __reduce_add_sync(0xFFFFFFFFu, cta_above + (lane < warp ? warp_above : 0));
+    uint32_t equal_before = __reduce_add_sync(0xFFFFFFFFu, cta_equal + (lane < warp ? warp_equal : 0));
+#pragma unroll 4
     for (int i0 = p0; i0 < p1; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0, below = (1u << lane) - 1;
@@ -175,7 +195,7 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
         if (keep || (tie && t < need)) {
             const uint32_t slot = above_before + __popc(keeps & below) + min(t, need);
             kept[slot] = i;
-            out[slot] = w[i];
+            out[slot] = want > 0 && k != kLowestKey ? key_weight(k) : w[i];
         }
         above_before += __popc(keeps);
         equal_before += __popc(ties);
@@ -222,34 +242,30 @@ __global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvict
     const bool whole = n <= a.keep;
     if (whole && src_row[0] == to_bh * kBlock) return;
     uint4 x[kPieces];
+    int row[kPieces], unit[kPieces];  // -1: nothing there; the piece of the row
     float k_top = 0.0f, v_top = 0.0f;
-    auto place = [&](int p, int& r, int& u) {  // piece p of the thread: its row and the piece of the row
-        const int i = tid + p * kMoveThreads;
-        r = static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
-        u = i - r * groups;
-        return i < total && src_row[r] >= 0;
-    };
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-        int r, u;
-        if (!place(p, r, u)) continue;
-        x[p] = u < gk ? reinterpret_cast<const uint4*>(a.k + src_row[r] * a.d_qk)[u]
-                      : reinterpret_cast<const uint4*>(a.v + src_row[r] * a.d_v)[u - gk];
+        const int i = tid + p * kMoveThreads;
+        const int r = static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
+        unit[p] = i - r * groups;
+        const int64_t src = i < total ? src_row[r] : -1;
+        row[p] = src >= 0 ? r : -1;
+        if (src >= 0)
+            x[p] = unit[p] < gk ? reinterpret_cast<const uint4*>(a.k + src * a.d_qk)[unit[p]]
+                                : reinterpret_cast<const uint4*>(a.v + src * a.d_v)[unit[p] - gk];
     }
     if (!whole) {
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            int r, u;
-            if (!place(p, r, u)) continue;
-            const float top = e4m3_to_float(top_code(x[p])) * src_scale[r][u >= gk];
-            if (u < gk) k_top = fmaxf(k_top, top);
+            if (row[p] < 0) continue;
+            const float top = e4m3_to_float(top_code(x[p])) * src_scale[row[p]][unit[p] >= gk];
+            if (unit[p] < gk) k_top = fmaxf(k_top, top);
             else v_top = fmaxf(v_top, top);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            k_top = fmaxf(k_top, __shfl_xor_sync(0xFFFFFFFFu, k_top, o));
-            v_top = fmaxf(v_top, __shfl_xor_sync(0xFFFFFFFFu, v_top, o));
-        }
+        // (magnitudes order as their bits do)
+        k_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(k_top)));
+        v_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v_top)));
         if ((tid & 31) == 0) red[tid >> 5][0] = k_top, red[tid >> 5][1] = v_top;
         __syncthreads();
 #pragma unroll
@@ -258,25 +274,19 @@ __global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvict
             v_top = fmaxf(v_top, red[w][1]);
         }
     }
-    const Divisor k_scale(whole ? src_scale[0][0] : unit_scale(k_top)), v_scale(whole ? src_scale[0][1] : unit_scale(v_top));
+    const float k_per = 1.0f / unit_scale(k_top), v_per = 1.0f / unit_scale(v_top);
+    const float k_scale = whole ? src_scale[0][0] : unit_scale(k_top), v_scale = whole ? src_scale[0][1] : unit_scale(v_top);
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-        int r, u;
-        if (!place(p, r, u)) continue;
-        if (!whole) {
-            float y[16];
-            e4m3x16_values(x[p], y);
-            const float s = src_scale[r][u >= gk];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] *= s;
-            x[p] = codes16(y, u < gk ? k_scale : v_scale);
-        }
-        if (u < gk) reinterpret_cast<uint4*>(a.k + (to_bh * kBlock + r) * a.d_qk)[u] = x[p];
-        else reinterpret_cast<uint4*>(a.v + (to_bh * kBlock + r) * a.d_v)[u - gk] = x[p];
+        if (row[p] < 0) continue;
+        const bool key = unit[p] < gk;
+        if (!whole) x[p] = requantise16(x[p], src_scale[row[p]][!key], key ? k_scale : v_scale, key ? k_per : v_per);
+        if (key) reinterpret_cast<uint4*>(a.k + (to_bh * kBlock + row[p]) * a.d_qk)[unit[p]] = x[p];
+        else reinterpret_cast<uint4*>(a.v + (to_bh * kBlock + row[p]) * a.d_v)[unit[p] - gk] = x[p];
     }
     if (tid == 0 && (!whole || src_row[0] >= 0)) {
-        a.k_scale[to_bh] = k_scale.value;
-        a.v_scale[to_bh] = v_scale.value;
+        a.k_scale[to_bh] = k_scale;
+        a.v_scale[to_bh] = v_scale;
     }
 }
 

@@ -92,16 +92,6 @@ struct GroupedChunk {
     int64_t warp_sums[kGroupedJoinThreads / 32];
 };
 
-__device__ __forceinline__ int chunk_find(const GroupedChunk& c, int n, int64_t u) {
-    int lo = 0, hi = n - 1;  // the last sequence whose first unit is at or before u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c.units[mid] <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 __device__ __forceinline__ int64_t chunk_load(const GroupedArgs& a, GroupedChunk& c, int b0, int64_t tiles_before) {
     const int tid = threadIdx.x, b = b0 + tid;
     GroupedSeq s{};
@@ -117,10 +107,11 @@ __device__ __forceinline__ int64_t chunk_load(const GroupedArgs& a, GroupedChunk
     return all_tiles;
 }
 
-// weights_out = weights + the sum over the rows of 2^(z - lse): two position tiles a CTA at a time.
+// weights_out = weights + the sum over the rows of 2^(z - lse): a warp for each position tile of a key head, four positions
+// a lane, so that a row's 128 logits are four coalesced loads.
 __global__ void __launch_bounds__(kGroupedJoinThreads) grouped_weights_kernel(GroupedArgs a) {
     __shared__ GroupedChunk c;
-    const int tid = threadIdx.x, part = tid >> 7, j = tid & 127;
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kGroupedJoinThreads / 32);
     int64_t before = 0;
     bool waited = false;
     for (int b0 = 0; b0 < a.B; b0 += kGroupedJoinThreads) {
@@ -129,28 +120,46 @@ __global__ void __launch_bounds__(kGroupedJoinThreads) grouped_weights_kernel(Gr
         if (!waited) griddep_wait();
         waited = true;
         const int64_t n = c.units[kGroupedJoinThreads];
-        for (int64_t u = 2 * static_cast<int64_t>(blockIdx.x) + part; u < n; u += 2 * static_cast<int64_t>(gridDim.x)) {
-            const int i = chunk_find(c, min(kGroupedJoinThreads, a.B - b0), u);
+        for (int64_t u = blockIdx.x + static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x; u < n; u += warps) {
+            int i = 0, hi = min(kGroupedJoinThreads, a.B - b0) - 1;  // the last sequence whose first unit is at or before u
+            while (i < hi) {
+                const int mid = (i + hi + 1) >> 1;
+                if (c.units[mid] <= u) i = mid;
+                else hi = mid - 1;
+            }
             const GroupedSeq s = c.seq[i];
             const int place = static_cast<int>(u - c.units[i]), h = place / s.tiles, tile = place - h * s.tiles;
-            const int pos = tile * kGroupedTile + j;
-            if (pos >= s.len) continue;
-            float w = 0.0f;
+            const int pos = tile * kGroupedTile + lane, left = s.len - pos;  // positions pos, pos + 32, + 64, + 96 below len
+            const int64_t at = (static_cast<int64_t>(b0 + i) * a.H_kv + h) * a.max_blocks * kBlock + pos;
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = a.weights && 32 * k < left ? a.weights[at + 32 * k] : 0.0f;
+            const float* lse = a.row_lse + static_cast<int64_t>(s.q0) * a.H + h * a.G;
             for (int it = 0; it < s.items; ++it) {
                 const int64_t t = c.tiles[i] + (static_cast<int64_t>(h) * s.items + it) * s.tiles + tile;
                 if (t >= a.max_tiles) break;
                 const int row0 = it * a.row_tile, rows = min(a.row_tile, s.n * a.G - row0);
-                const float* z = a.z + t * a.row_tile * kGroupedTile + j;
-                int tok = row0 / a.G, g = row0 - tok * a.G;
+                const float* z = a.z + t * a.row_tile * kGroupedTile + lane;
+                for (int r0 = 0; r0 < rows; r0 += 32) {
+                    // lane k: row r0 + k's sum, as a logarithm
+                    const int row = row0 + r0 + lane, tok = row / a.G;
+                    const float e = r0 + lane < rows ? lse[static_cast<int64_t>(tok) * a.H + row - tok * a.G] : 0.0f;
+                    const int n_rows = min(32, rows - r0);
 #pragma unroll 4
-                for (int r = 0; r < rows; ++r) {
-                    const float x = z[r * kGroupedTile], e = a.row_lse[static_cast<int64_t>(s.q0 + tok) * a.H + h * a.G + g];
-                    if (x != -INFINITY) w += exp2f(x - e);
-                    if (++g == a.G) g = 0, ++tok;
+                    for (int r = 0; r < n_rows; ++r) {
+                        const float er = __shfl_sync(0xFFFFFFFFu, e, r);
+                        float x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = z[(r0 + r) * kGroupedTile + 32 * k];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (x[k] != -INFINITY) w[k] += exp2f(x[k] - er);
+                    }
                 }
             }
-            const int64_t at = (static_cast<int64_t>(b0 + i) * a.H_kv + h) * a.max_blocks * kBlock + pos;
-            a.weights_out[at] = a.weights ? a.weights[at] + w : w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (32 * k < left) a.weights_out[at + 32 * k] = w[k];
         }
     }
 }
