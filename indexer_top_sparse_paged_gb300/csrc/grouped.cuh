@@ -180,8 +180,8 @@ __device__ __forceinline__ uint4 codes16(const float2 (&x)[8], float scale) {
     return divided_codes(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
 }
 
-// RNE_e4m3(fl(code * from) / scale) of 16 codes, saturating; per: 1 / scale.
-__device__ __forceinline__ uint4 requantise16(const uint4& in, float from, float scale, float per) {
+// RNE_e4m3(fl(code * from) / scale) of 16 codes, saturating.
+static __device__ __noinline__ uint4 requantise16(uint4 in, float from, float scale) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     float2 x[8];
     uint4 codes;
@@ -190,7 +190,7 @@ __device__ __forceinline__ uint4 requantise16(const uint4& in, float from, float
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
         x[i] = __half22float2(*reinterpret_cast<const __half2*>(&h));
     }
-    const float r = from * per;
+    const float r = from * (1.0f / scale);
     if (plain_scale(scale) && plain_scale(from) && r <= 0x1p100f && near_codes(x, r, &codes)) return codes;  // (codes of 0 may have any scale)
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i].x *= from, x[i].y *= from;

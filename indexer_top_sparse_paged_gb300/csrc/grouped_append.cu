@@ -10,24 +10,52 @@ namespace dsa {
 
 constexpr int kGroupedAppendThreads = 256;
 
-// 16 elements of a new row.
-__device__ __forceinline__ void load16(const float* p, float2 (&x)[8]) {
+// 16 elements of a new row, as they are loaded; top: the bits of their largest magnitude (NaN above all).
+template <typename T>
+struct Elements16;
+template <>
+struct Elements16<float> {
+    float4 v[4];
+    __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(p)[i];
-        x[2 * i] = make_float2(v.x, v.y);
-        x[2 * i + 1] = make_float2(v.z, v.w);
+        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
     }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float2 (&x)[8]) {
+    __device__ __forceinline__ void values(float2 (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * i + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = make_float2(v[i].x, v[i].y);
+            x[2 * i + 1] = make_float2(v[i].z, v[i].w);
+        }
     }
-}
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t = max(t, max(max(__float_as_uint(v[i].x) & 0x7FFFFFFFu, __float_as_uint(v[i].y) & 0x7FFFFFFFu),
+                           max(__float_as_uint(v[i].z) & 0x7FFFFFFFu, __float_as_uint(v[i].w) & 0x7FFFFFFFu)));
+        return t;
+    }
+};
+template <>
+struct Elements16<__nv_bfloat16> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        v[0] = reinterpret_cast<const uint4*>(p)[0];
+        v[1] = reinterpret_cast<const uint4*>(p)[1];
+    }
+    __device__ __forceinline__ void values(float2 (&x)[8]) const {
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t m = 0x7FFF7FFFu;
+        const uint32_t a = __vmaxu2(__vmaxu2(v[0].x & m, v[0].y & m), __vmaxu2(v[0].z & m, v[0].w & m));
+        const uint32_t b = __vmaxu2(__vmaxu2(v[1].x & m, v[1].y & m), __vmaxu2(v[1].z & m, v[1].w & m));
+        const uint32_t t = __vmaxu2(a, b);
+        return max(t << 16, t & 0xFFFF0000u);
+    }
+};
 
 struct AppendSeq {
     int row0, n;       // the sequence's new rows
@@ -57,18 +85,23 @@ __device__ __forceinline__ AppendSeq append_seq(const GroupedAppendArgs& a, int 
     return s;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(GroupedAppendArgs a) {
+template <typename T, int kPieces>  // pieces of 16 elements a thread holds: 64 rows of a head
+__global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(GroupedAppendArgs a, uint32_t k_magic, uint32_t v_magic) {
     __shared__ int64_t warp_sums[kGroupedAppendThreads / 32], found[2];
-    __shared__ float red[kGroupedAppendThreads / 32];
-    const int tid = threadIdx.x, h = blockIdx.y >> 1;
-    const bool value = blockIdx.y & 1;
+    __shared__ float red[2][kGroupedAppendThreads / 32];
+    const int tid = threadIdx.x;
+    // the block: unit blockIdx.x of the line of blocks that the sequences' new rows reach into
     int64_t total, base;
     int b;
-    find_place<kGroupedAppendThreads>(
-        a.B, [&](int i) { return static_cast<int64_t>(append_seq(a, i, blockIdx.x == 0 && blockIdx.y == 0).blocks); },
-        [](int64_t) { return static_cast<int64_t>(blockIdx.x); }, &total, &b, &base, warp_sums, found);
-    if (b < 0) return;
+    const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+    if (!a.cu) {
+        b = blockIdx.x, base = b;  // one row, one block for each
+        if (append_seq(a, b, blockIdx.y == 0 && tid == 0).blocks == 0) return;
+    } else {
+        find_place<kGroupedAppendThreads>(a.B, [&](int i) { return static_cast<int64_t>(append_seq(a, i, report).blocks); },
+                                          [](int64_t) { return static_cast<int64_t>(blockIdx.x); }, &total, &b, &base, warp_sums, found);
+        if (b < 0) return;
+    }
     const AppendSeq s = append_seq(a, b, false);
     const int lb = s.first / kBlock + static_cast<int>(blockIdx.x - base);
     const int p0 = max(s.first, lb * kBlock), p1 = min(s.first + s.n - s.skipped, (lb + 1) * kBlock);  // new positions here
@@ -77,47 +110,71 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
         if (tid == 0) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
         return;
     }
-    const int d = value ? a.d_v : a.d_qk, groups = d / 16, slot0 = p0 - lb * kBlock, n = (p1 - p0) * groups;
-    const int64_t st = value ? a.v_stride_t : a.k_stride_t, sh = value ? a.v_stride_h : a.k_stride_h;
-    const T* x = static_cast<const T*>(value ? a.v_new : a.k_new) + (s.row0 + s.skipped + p0 - s.first) * st + h * sh;
-    const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + h;
-    uint4* codes = reinterpret_cast<uint4*>((value ? a.v : a.k) + bh * kBlock * d);
-    float* scale_at = (value ? a.v_scale : a.k_scale) + bh;
-    float amax = 0.0f;
-    for (int i = tid; i < n; i += kGroupedAppendThreads) {
-        float2 y[8];
-        load16(x + (i / groups) * st + (i % groups) * 16, y);
+    const int slot0 = p0 - lb * kBlock;
+    // its heads, keys and values in turn
+    for (int y = blockIdx.y, turn = 0; y < 2 * a.H_kv; y += gridDim.y, turn ^= 1) {
+        const int h = y >> 1;
+        const bool value = y & 1;
+        const int d = value ? a.d_v : a.d_qk, groups = d / 16, n = (p1 - p0) * groups;
+        const uint32_t magic = value ? v_magic : k_magic;
+        const int64_t st = value ? a.v_stride_t : a.k_stride_t, sh = value ? a.v_stride_h : a.k_stride_h;
+        const T* x = static_cast<const T*>(value ? a.v_new : a.k_new) + (s.row0 + s.skipped + p0 - s.first) * st + h * sh;
+        const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + h;
+        uint4* codes = reinterpret_cast<uint4*>((value ? a.v : a.k) + bh * kBlock * d);
+        float* scale_at = (value ? a.v_scale : a.k_scale) + bh;
+        const float old = slot0 ? *scale_at : 0.0f;
+        Elements16<T> piece[kPieces];
+        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    const float old = slot0 ? *scale_at : 0.0f;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kGroupedAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    const float scale = slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax);
-    for (int i = tid; i < n; i += kGroupedAppendThreads) {
-        float2 y[8];
-        load16(x + (i / groups) * st + (i % groups) * 16, y);
-        codes[slot0 * groups + i] = codes16(y, scale);
-    }
-    if (slot0 && scale > old) {
-        for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) {
-            codes[i] = requantise16(codes[i], old, scale, 1.0f / scale);
+        for (int p = 0; p < kPieces; ++p) {
+            const int i = tid + p * kGroupedAppendThreads;
+            const int r = groups == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
+            if (i < n) piece[p].load(x + r * st + (i - r * groups) * 16);
         }
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+            if (tid + p * kGroupedAppendThreads < n) top = max(top, piece[p].top());
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if ((tid & 31) == 0) red[turn][tid >> 5] = __uint_as_float(top);
+        __syncthreads();
+        float amax = 0.0f;  // (fmaxf passes NaN over)
+#pragma unroll
+        for (int w = 0; w < kGroupedAppendThreads / 32; ++w) amax = fmaxf(amax, red[turn][w]);
+        const float scale = slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int i = tid + p * kGroupedAppendThreads;
+            if (i >= n) break;
+            float2 v[8];
+            piece[p].values(v);
+            codes[slot0 * groups + i] = codes16(v, scale);
+        }
+        if (slot0 && scale > old) {
+            for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) codes[i] = requantise16(codes[i], old, scale);
+        }
+        if (tid == 0) *scale_at = scale;
     }
-    if (tid == 0) *scale_at = scale;
+}
+
+template <typename T>
+static bool launch_typed(const GroupedAppendArgs& a, cudaStream_t s) {
+    // a sequence's rows reach into (n + 126) / 64 blocks at most, and into n
+    const int64_t most = static_cast<int64_t>(a.T) / kBlock + 2ll * a.B, units = most < a.T ? most : a.T;
+    // two turns of eight CTAs an SM, or a CTA for every head's keys and values
+    int64_t heads = (16ll * device_sm_count() + units - 1) / units;
+    if (heads > 2 * a.H_kv) heads = 2 * a.H_kv;
+    const int most_groups = (a.d_qk > a.d_v ? a.d_qk : a.d_v) / 16;
+    const uint32_t gk = a.d_qk / 16, gv = a.d_v / 16;
+    // umulhi(i, ceil(2^32 / groups)) = i / groups for i < 2^32 / groups
+    const uint32_t k_magic = static_cast<uint32_t>(((1ll << 32) + gk - 1) / gk), v_magic = static_cast<uint32_t>(((1ll << 32) + gv - 1) / gv);
+    auto* kernel = most_groups <= 8 ? grouped_append_kernel<T, 2> : grouped_append_kernel<T, 4>;
+    return launch_kernel(false, kernel, dim3(static_cast<unsigned>(units), static_cast<unsigned>(heads)), dim3(kGroupedAppendThreads), 0, s, a,
+                         k_magic, v_magic);
 }
 
 bool launch_grouped_append(const GroupedAppendArgs& a, cudaStream_t s, int* launches) {
     if (a.T == 0) return true;
-    // a sequence's rows reach into (n + 126) / 64 blocks at most, and into n
-    const int64_t most = static_cast<int64_t>(a.T) / kBlock + 2ll * a.B;
-    const dim3 grid(static_cast<unsigned>(most < a.T ? most : a.T), 2 * a.H_kv);
-    auto* kernel = a.type == DSA_F32 ? grouped_append_kernel<float> : grouped_append_kernel<__nv_bfloat16>;
-    if (!launch_kernel(false, kernel, grid, dim3(kGroupedAppendThreads), 0, s, a)) return false;
+    if (!(a.type == DSA_F32 ? launch_typed<float>(a, s) : launch_typed<__nv_bfloat16>(a, s))) return false;
     ++*launches;
     return true;
 }

@@ -205,88 +205,174 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
 
 // The largest of 16 codes' magnitudes: e4m3 values order as their 7 low bits.
 __device__ __forceinline__ uint32_t top_code(const uint4& v) {
-    uint32_t t = __vmaxu4(__vmaxu4(v.x & 0x7F7F7F7Fu, v.y & 0x7F7F7F7Fu), __vmaxu4(v.z & 0x7F7F7F7Fu, v.w & 0x7F7F7F7Fu));
-    t = __vmaxu4(t, t >> 16);
-    return max(t & 0xFFu, (t >> 8) & 0xFFu);
+    const uint32_t m = 0x007F007Fu;
+    const uint32_t lo = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    const uint32_t hi = __vmaxu2(__vmaxu2(v.x >> 8 & m, v.y >> 8 & m), __vmaxu2(v.z >> 8 & m, v.w >> 8 & m));
+    const uint32_t t = __vmaxu2(lo, hi);
+    return max(t & 0xFFFFu, t >> 16);
 }
 
-template <int kPieces>  // 16-byte pieces of a thread: 64 rows of (d_qk + d_v) / 16
-__global__ void __launch_bounds__(kMoveThreads) grouped_move_kernel(GroupedEvictArgs a, uint32_t magic) {
-    __shared__ int64_t src_row[kBlock];
-    __shared__ float src_scale[kBlock][2];
-    __shared__ float red[kMoveThreads / 32][2];
-    const int tid = threadIdx.x, blocks = (a.keep + kBlock - 1) / kBlock;
-    const int bh_in = blockIdx.x / blocks, j = blockIdx.x - bh_in * blocks, b = bh_in / a.H_kv, h = bh_in - b * a.H_kv;
+// How a row's codes change with its scale. Where a code and its rounded quotient are normal numbers, the quotient's 4-bit
+// significand and its distance in powers of two depend on the code's 3 mantissa bits alone, and so does the difference of
+// the two codes as integers (exponent above mantissa): eight differences, modulo 128, to be looked up by byte
+// permutations, four codes at a time. Codes too small for that (`floor` turns their sum's bit 7 off) take the formula:
+// with normally distributed values one piece in some hundreds.
+struct alignas(16) CodeStep {
+    uint2 diff;      // bytes: difference for mantissa 0 .. 7
+    uint32_t floor;  // each byte: 128 - the least magnitude it holds for (0: for none)
+};
+
+// Half of a row's differences (mantissas 4 * half + 0 .. 3) for the ratio of its scale to the new one, and whether all are
+// certain: with the ratio as f 2^k, 1 <= f < 2, code (8 + mantissa) 2^e becomes (8 + mantissa) f 2^(e + k), whose
+// significand is rounded in steps of 1 below 16 and of 2 from there on. A value within 2^-14 of the middle of two steps
+// leaves it to the formula (the ratio and the products are off by some 2^-22 relatively).
+__device__ __forceinline__ bool step_differences(float ratio, int half, uint32_t* diff, int* least) {
+    const int k = static_cast<int>(__float_as_uint(ratio) >> 23) - 127;
+    const float f = __uint_as_float((__float_as_uint(ratio) & 0x7FFFFFu) | 0x3F800000u);
+    bool sure = k >= -5 && k < 7;
+    *diff = 0;
+    *least = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int mant = 4 * half + i;
+        const float y = static_cast<float>(8 + mant) * f, z = y < 16.0f ? y : 0.5f * y;
+        const float up = z + 12582912.0f, whole = up - 12582912.0f;  // 1.5 * 2^23: the nearest whole number, and its bits
+        sure = sure && fabsf(fabsf(z - whole) - 0.5f) > 0x1p-14f;
+        const int d = static_cast<int>(__float_as_uint(up) & 31u) - (y < 16.0f ? 8 : 0) + 8 * k - mant;
+        *diff |= static_cast<uint32_t>(d & 0x7F) << (8 * i);
+        *least = min(*least, d);
+    }
+    return sure;
+}
+
+__device__ __forceinline__ bool step_codes(const uint4& in, const CodeStep& c, uint4* out) {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    uint32_t r[4], large = 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mag = w[i] & 0x7F7F7F7Fu;
+        large &= mag + c.floor;
+        uint32_t pick = w[i] & 0x07070707u;  // the mantissas, side by side as the permutation's four selectors
+        pick = (pick | pick >> 4) & 0x00FF00FFu;
+        pick |= pick >> 8;
+        const uint32_t sum = mag + __byte_perm(c.diff.x, c.diff.y, pick & 0xFFFFu);  // (at most 254 in a byte)
+        r[i] = (sum & 0x7F7F7F7Fu) | (w[i] & 0x80808080u);
+    }
+    if (large != 0x80808080u) return false;
+    *out = make_uint4(r[0], r[1], r[2], r[3]);
+    return true;
+}
+
+// kVec: 16-byte vectors of a piece (two where the widths allow it: half the addresses); kPieces: pieces of a thread, which
+// hold 64 rows of d_qk + d_v bytes together.
+template <int kVec, int kPieces>
+__global__ void __launch_bounds__(kMoveThreads, kVec * kPieces <= 4 ? 5 : 3) grouped_move_kernel(GroupedEvictArgs a, uint32_t magic) {
+    __shared__ int32_t src_row[kBlock];
+    __shared__ float src_scale[2][kBlock];
+    __shared__ CodeStep step[2][kBlock];
+    __shared__ float2 red[kMoveThreads / 32];
+    constexpr int kBytes = 16 * kVec;
+    const int tid = threadIdx.x, bh_in = blockIdx.x, b = bh_in / a.H_kv, h = bh_in - b * a.H_kv;
     int n = a.seq_lens[b];
     if (n < 0 || n > a.max_blocks * kBlock) n = 0;
-    const int m = min(n, a.keep), rows = min(kBlock, m - j * kBlock);
-    if (rows <= 0) return;
-    const int to = a.new_table[static_cast<int64_t>(b) * a.new_max_blocks + j];
-    const bool to_ok = to >= 0 && to < a.num_blocks;
-    if (!to_ok && tid == 0) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
-    griddep_wait();
-    if (tid < rows) {
-        const int i = a.kept[static_cast<int64_t>(bh_in) * a.keep + j * kBlock + tid];
-        const int blk = a.block_table[static_cast<int64_t>(b) * a.max_blocks + i / kBlock];
-        const bool ok = blk >= 0 && blk < a.num_blocks;
-        if (!ok) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
-        const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + h;
-        src_row[tid] = ok ? bh * kBlock + i % kBlock : -1;
-        src_scale[tid][0] = ok ? a.k_scale[bh] : 0.0f;
-        src_scale[tid][1] = ok ? a.v_scale[bh] : 0.0f;
-    }
-    __syncthreads();
-    if (!to_ok) return;
-    const int64_t to_bh = static_cast<int64_t>(to) * a.H_kv + h;
-    const int gk = a.d_qk / 16, groups = gk + a.d_v / 16, total = rows * groups;
+    const int m = min(n, a.keep);
     const bool whole = n <= a.keep;
-    if (whole && src_row[0] == to_bh * kBlock) return;
-    uint4 x[kPieces];
-    int row[kPieces], unit[kPieces];  // -1: nothing there; the piece of the row
-    float k_top = 0.0f, v_top = 0.0f;
+    const int gk = a.d_qk / kBytes, groups = gk + a.d_v / kBytes;
+    griddep_wait();
+    for (int j = blockIdx.y; j * kBlock < m; j += gridDim.y) {
+        const int rows = min(kBlock, m - j * kBlock), total = rows * groups;
+        const int to = a.new_table[static_cast<int64_t>(b) * a.new_max_blocks + j];
+        const bool to_ok = to >= 0 && to < a.num_blocks;
+        if (!to_ok && tid == 0) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
+        __syncthreads();  // the last block's rows have been read
+        if (tid < rows) {
+            const int i = a.kept[static_cast<int64_t>(bh_in) * a.keep + j * kBlock + tid];
+            const int blk = a.block_table[static_cast<int64_t>(b) * a.max_blocks + i / kBlock];
+            const bool ok = blk >= 0 && blk < a.num_blocks;
+            if (!ok) atomicOr(a.err, DSA_FAULT_BLOCK_TABLE);
+            const int bh = blk * a.H_kv + h;  // (the caches' rows are counted in 32 bits)
+            src_row[tid] = ok ? bh * kBlock + i % kBlock : -1;
+            src_scale[0][tid] = ok ? a.k_scale[bh] : 0.0f;
+            src_scale[1][tid] = ok ? a.v_scale[bh] : 0.0f;
+        }
+        __syncthreads();
+        const int to_bh = to * a.H_kv + h;
+        if (!to_ok || (whole && src_row[0] == to_bh * kBlock)) continue;
+        auto piece_at = [&](int of_row, int u) {  // piece u of a cache row: of its keys, then of its values
+            const bool value = u >= gk;
+            return reinterpret_cast<uint4*>((value ? a.v : a.k) + static_cast<int64_t>(of_row) * (value ? a.d_v : a.d_qk) + (value ? u - gk : u) * kBytes);
+        };
+        uint4 x[kPieces][kVec];
+        int row[kPieces], unit[kPieces];  // -1: nothing there; the piece of the row
+        float top[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-        const int i = tid + p * kMoveThreads;
-        const int r = static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
-        unit[p] = i - r * groups;
-        const int64_t src = i < total ? src_row[r] : -1;
-        row[p] = src >= 0 ? r : -1;
-        if (src >= 0)
-            x[p] = unit[p] < gk ? reinterpret_cast<const uint4*>(a.k + src * a.d_qk)[unit[p]]
-                                : reinterpret_cast<const uint4*>(a.v + src * a.d_v)[unit[p] - gk];
-    }
-    if (!whole) {
+        for (int p = 0; p < kPieces; ++p) {
+            const int i = tid + p * kMoveThreads;
+            const int r = groups == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
+            unit[p] = i - r * groups;
+            const int src = i < total ? src_row[r] : -1;
+            row[p] = src >= 0 ? r : -1;
+            if (src >= 0) {
+                const uint4* from = piece_at(src, unit[p]);
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) x[p][v] = from[v];
+            }
+        }
+        float scale[2] = {src_scale[0][0], src_scale[1][0]};
+        if (!whole) {
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                if (row[p] < 0) continue;
+                const bool value = unit[p] >= gk;
+                uint32_t code = top_code(x[p][0]);
+                if (kVec == 2) code = max(code, top_code(x[p][kVec - 1]));
+                const float y = e4m3_to_float(code) * src_scale[value][row[p]];
+                top[0] = fmaxf(top[0], value ? 0.0f : y);
+                top[1] = fmaxf(top[1], value ? y : 0.0f);
+            }
+            // (magnitudes order as their bits do)
+            const float k_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top[0])));
+            const float v_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top[1])));
+            if ((tid & 31) == 0) red[tid >> 5] = make_float2(k_top, v_top);
+            __syncthreads();
+            float2 t = red[0];
+#pragma unroll
+            for (int w = 1; w < kMoveThreads / 32; ++w) t = make_float2(fmaxf(t.x, red[w].x), fmaxf(t.y, red[w].y));
+            scale[0] = unit_scale(t.x);
+            scale[1] = unit_scale(t.y);
+            // the rows' steps: two threads a row (of keys or of values)
+            const int v = tid >> 7, r = (tid >> 1) & 63, half = tid & 1;
+            const float from = src_scale[v][r], to_scale = v ? scale[1] : scale[0];
+            uint32_t diff;
+            int least;
+            bool sure = step_differences(__fdividef(from, to_scale), half, &diff, &least);
+            sure = __shfl_xor_sync(0xFFFFFFFFu, sure, 1) && sure && plain_scale(from) && plain_scale(to_scale);
+            least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, 1));
+            (&step[v][r].diff.x)[half] = diff;
+            if (half == 0) step[v][r].floor = sure ? (120 + least) * 0x01010101u : 0;
+            __syncthreads();
+        }
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             if (row[p] < 0) continue;
-            const float top = e4m3_to_float(top_code(x[p])) * src_scale[row[p]][unit[p] >= gk];
-            if (unit[p] < gk) k_top = fmaxf(k_top, top);
-            else v_top = fmaxf(v_top, top);
-        }
-        // (magnitudes order as their bits do)
-        k_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(k_top)));
-        v_top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v_top)));
-        if ((tid & 31) == 0) red[tid >> 5][0] = k_top, red[tid >> 5][1] = v_top;
-        __syncthreads();
+            const bool value = unit[p] >= gk;
+            if (!whole) {
+                const CodeStep c = step[value][row[p]];
+                bool stepped = step_codes(x[p][0], c, &x[p][0]);
+                if (!stepped) x[p][0] = requantise16(x[p][0], src_scale[value][row[p]], value ? scale[1] : scale[0]);
+                if (kVec == 2) {
+                    stepped = step_codes(x[p][kVec - 1], c, &x[p][kVec - 1]);
+                    if (!stepped) x[p][kVec - 1] = requantise16(x[p][kVec - 1], src_scale[value][row[p]], value ? scale[1] : scale[0]);
+                }
+            }
+            uint4* out = piece_at(to_bh * kBlock + row[p], unit[p]);
 #pragma unroll
-        for (int w = 0; w < kMoveThreads / 32; ++w) {
-            k_top = fmaxf(k_top, red[w][0]);
-            v_top = fmaxf(v_top, red[w][1]);
+            for (int v = 0; v < kVec; ++v) out[v] = x[p][v];
         }
-    }
-    const float k_per = 1.0f / unit_scale(k_top), v_per = 1.0f / unit_scale(v_top);
-    const float k_scale = whole ? src_scale[0][0] : unit_scale(k_top), v_scale = whole ? src_scale[0][1] : unit_scale(v_top);
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-        if (row[p] < 0) continue;
-        const bool key = unit[p] < gk;
-        if (!whole) x[p] = requantise16(x[p], src_scale[row[p]][!key], key ? k_scale : v_scale, key ? k_per : v_per);
-        if (key) reinterpret_cast<uint4*>(a.k + (to_bh * kBlock + row[p]) * a.d_qk)[unit[p]] = x[p];
-        else reinterpret_cast<uint4*>(a.v + (to_bh * kBlock + row[p]) * a.d_v)[unit[p] - gk] = x[p];
-    }
-    if (tid == 0 && (!whole || src_row[0] >= 0)) {
-        a.k_scale[to_bh] = k_scale;
-        a.v_scale[to_bh] = v_scale;
+        if (tid == 0 && (!whole || src_row[0] >= 0)) {
+            a.k_scale[to_bh] = scale[0];
+            a.v_scale[to_bh] = scale[1];
+        }
     }
 }
 
@@ -313,11 +399,14 @@ bool launch_grouped_evict(const GroupedEvictArgs& a, cudaStream_t s, int* launch
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, grouped_select_kernel, a, ctas, cached) != cudaSuccess) return false;
     ++*launches;
-    const dim3 grid(heads * ((a.keep + kBlock - 1) / kBlock));
-    const uint32_t groups = (a.d_qk + a.d_v) / 16, pieces = (kBlock * groups + kMoveThreads - 1) / kMoveThreads;
+    const int blocks = (a.keep + kBlock - 1) / kBlock;
+    const dim3 grid(heads, blocks < 65535 ? blocks : 65535);
+    const int vec = a.d_qk % 32 == 0 && a.d_v % 32 == 0 ? 2 : 1;
+    const uint32_t groups = (a.d_qk + a.d_v) / (16 * vec), pieces = (kBlock * groups + kMoveThreads - 1) / kMoveThreads;
     // umulhi(i, ceil(2^32 / groups)) = i / groups for i < 2^32 / groups
     const uint32_t magic = static_cast<uint32_t>(((1ll << 32) + groups - 1) / groups);
-    auto* move = pieces <= 2 ? grouped_move_kernel<2> : pieces <= 4 ? grouped_move_kernel<4> : grouped_move_kernel<8>;
+    auto* move = vec == 2 ? (pieces <= 2 ? grouped_move_kernel<2, 2> : grouped_move_kernel<2, 4>)
+                          : (pieces <= 4 ? grouped_move_kernel<1, 4> : grouped_move_kernel<1, 8>);
     if (!launch_kernel(true, move, grid, dim3(kMoveThreads), 0, s, a, magic)) return false;
     ++*launches;
     return true;
