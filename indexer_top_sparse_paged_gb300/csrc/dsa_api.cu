@@ -496,8 +496,11 @@ static bool ws_ok(const void* ws, size_t ws_bytes, size_t need) {
     return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && ws_bytes >= need;
 }
 
+// The arrivals stand behind the error word, in the 256 bytes that dsa_workspace_init clears and no other call writes.
+constexpr size_t kGroupedArrived = 16;
+
 struct GroupedLayout {
-    size_t cuts, part_ml, part_o, row_lse, z, total;
+    size_t part_ml, part_o, row_lse, z, total;
     int row_tile, ctas;
     int64_t max_tiles;
 };
@@ -512,8 +515,6 @@ static GroupedLayout grouped_layout(const dsa_grouped_dims& d, int T, bool weigh
     w.max_tiles = (T * G / w.row_tile + d.B) * d.H_kv * ((d.max_blocks + 1) / 2);
     size_t off = 256;  // the error word
     const size_t slot_rows = static_cast<size_t>(2) * w.ctas * w.row_tile;
-    w.cuts = off;
-    off = align256(off + sizeof(GroupedCut) * w.ctas);
     w.part_ml = off;
     off = align256(off + sizeof(float2) * slot_rows);
     w.part_o = off;
@@ -1030,13 +1031,13 @@ dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t
         a.err = reinterpret_cast<int*>(base);
         a.row_tile = L.row_tile;
         a.ctas = L.ctas;
-        a.cuts = reinterpret_cast<GroupedCut*>(base + L.cuts);
+        a.arrived = reinterpret_cast<uint32_t*>(base + kGroupedArrived);
         a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
         a.part_o = reinterpret_cast<float*>(base + L.part_o);
         a.row_lse = reinterpret_cast<float*>(base + L.row_lse);
         a.z = reinterpret_cast<float*>(base + L.z);
         a.max_tiles = L.max_tiles;
-        if (!launch_grouped_attn(a, s, &launches) || !launch_grouped_join(a, s, &launches)) st = DSA_ERR_LAUNCH;
+        if (!launch_grouped_attn(a, s, &launches) || (weights_out && !launch_grouped_weights(a, s, &launches))) st = DSA_ERR_LAUNCH;
     }
     g_last_launches = launches;
     return st;

@@ -5,8 +5,8 @@
 // n * G rows, row r = token r / G, head r % G of the group. An item is (sequence, key head, row_tile of those rows); its
 // positions are cut into tiles of 128. All tiles of all items, in this order, are one line, and CTA c of C takes the
 // tiles [c * per, (c + 1) * per), per = ceil(total / C): an even share of the cached bytes whatever the lengths. An item
-// cut by that leaves a partial (maximum, sum, unnormalised output) in its CTA's slot, and the join puts them together in
-// order of positions, so that results do not depend on timing.
+// cut by that leaves a partial (maximum, sum, unnormalised output) in its CTA's slot, and the CTA that leaves the last one
+// joins them in order of positions, so that results do not depend on timing.
 #pragma once
 
 #include "internal.h"
@@ -119,6 +119,74 @@ __device__ __forceinline__ int64_t find_place(int B, Count count, Where where, i
 // one 2c + 1 (an item that fills the whole share is its first).
 __device__ __forceinline__ int grouped_slot(int64_t share_begin, int64_t piece_begin, int c) {
     return 2 * c + (piece_begin > share_begin ? 1 : 0);
+}
+
+__device__ __forceinline__ void store_quad(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store_quad(__nv_bfloat16* p, float4 x) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Joins an item's partials: slot0, then the first ones of the next CTAs. A warp takes kRows rows at a time (warp, + warps,
+// ...), four columns a lane, kBatch partials of each on their way at once. row_at: the rows' places in lse and out.
+template <typename T, int kRows, int kBatch>
+__device__ __noinline__ void grouped_join(const GroupedArgs& a, const int* row_at, int rows, int slot0, int parts, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    for (int r0 = warp; r0 < rows; r0 += kRows * warps) {
+        for (int e = 4 * lane; e < a.d_v; e += 128) {
+            float top[kRows], sum[kRows];
+            float4 o[kRows];
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) top[q] = -INFINITY, sum[q] = 0.0f, o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int p0 = 0; p0 < parts; p0 += kBatch) {
+                float2 ml[kRows][kBatch];
+                float4 x[kRows][kBatch];
+#pragma unroll
+                for (int q = 0; q < kRows; ++q)
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int p = min(p0 + k, parts - 1), r = min(r0 + q * warps, rows - 1);
+                        const int slot = (p ? 2 * (slot0 / 2 + p) : slot0) * a.row_tile + r;
+                        ml[q][k] = __ldcg(a.part_ml + slot);
+                        x[q][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(slot) * a.d_v + e));
+                    }
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) {
+                    float most = top[q];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        if (p0 + k >= parts) ml[q][k] = make_float2(-INFINITY, 0.0f), x[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        most = fmaxf(most, ml[q][k].x);
+                    }
+                    const float ref = most == -INFINITY ? 0.0f : most, old = exp2f(top[q] - ref);
+                    sum[q] *= old;
+                    o[q].x *= old, o[q].y *= old, o[q].z *= old, o[q].w *= old;
+                    top[q] = most;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const float f = exp2f(ml[q][k].x - ref);
+                        const float4 y = x[q][k];
+                        sum[q] = fmaf(f, ml[q][k].y, sum[q]);
+                        o[q].x = fmaf(f, y.x, o[q].x), o[q].y = fmaf(f, y.y, o[q].y), o[q].z = fmaf(f, y.z, o[q].z), o[q].w = fmaf(f, y.w, o[q].w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                const int r = r0 + q * warps;
+                if (r >= rows) break;
+                const int at = row_at[r];
+                const float inv = sum[q] == 0.0f ? 0.0f : 1.0f / sum[q];
+                store_quad(static_cast<T*>(a.out) + static_cast<int64_t>(at) * a.d_v + e, make_float4(o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv));
+                if (e == 0) {
+                    const float lse2 = sum[q] == 0.0f ? -INFINITY : top[q] + log2f(sum[q]);
+                    if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
+                    if (a.weights_out) a.row_lse[at] = lse2;
+                }
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ float e4m3_to_float(uint32_t code) {

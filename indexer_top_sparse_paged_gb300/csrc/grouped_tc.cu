@@ -28,6 +28,8 @@ namespace gtc {
 
 constexpr int kChunk = 64 * 128;  // bytes of one block's 128 columns of codes
 constexpr int kMaxStages = 6;
+constexpr float kSlack = 4.0f;  // a weight is 2^kSlack at most,
+constexpr float kTop = 16.0f;   // and kTop * 2^kSlack = 256 as it is split into codes (which end at 448)
 constexpr size_t kSmemLimit = 232448;
 
 __host__ __device__ constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
@@ -75,7 +77,7 @@ struct Form {
     static constexpr int kSetWarps = 4 * kGroups, kSoftWarps = kSets * kSetWarps;
     static constexpr int kQWarps = 2;  // (12 warps in all leave 168 registers a thread)
     static constexpr int kThreads = 32 * (kSoftWarps + 2 + kQWarps);
-    static constexpr int kVCMax = kRows > 32 ? 1 : 2;  // chunks of 128 value columns (O^T's share of tensor memory)
+    static constexpr int kVCMax = kRows > 16 ? 1 : 2;  // chunks of 128 value columns (O^T's share of tensor memory)
     static constexpr int kColO = kSB * kSN;
     static constexpr int kCols = kColO + kSets * kVCMax * kPN;
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -88,31 +90,33 @@ template <typename F>
 struct Ctl {
     // barriers, with their arrivals in barrier_count
     uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[2], mma_done;
-    uint64_t q_full[2], met[F::kSets * F::kGroups], p_full[2], o_free, q_first, fin, q_empty[2];
+    uint64_t q_full[2], met[F::kSets * F::kGroups], p_full[2], o_free, left[2], q_first, fin, q_empty[2];
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
     alignas(16) int seen[2][F::kRows];        // positions below this are seen (rows past the last: 0)
     alignas(16) int row_at[2][F::kRows];      // token * H + head
-    alignas(16) float red[2][F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
+    alignas(16) float red[F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
+    alignas(16) uint32_t flag[2][F::kSets * F::kGroups][4];   // a warp's word on whether they must move
     alignas(16) float2 fm[F::kSoftWarps][F::kRW];  // each warp's own: a row's factor in this tile, minus its maximum
     alignas(16) float fac[F::kSoftWarps][F::kRW];  // and what its sums are to be multiplied by
     alignas(16) float fin_l[2][F::kSets][F::kRows][4], fin_m[2][F::kSets][F::kRows];  // a set's share of an item
     float fin_unit[2][F::kSets];  // of its O^T; 0: it had no tile
     uint32_t tmem_base;
     int abort_flag;
+    int last_part;  // whether the CTA left the last partial of an item
     int64_t warp_sums[F::kThreads / 32];
     int64_t found[2];
 };
 
 template <typename F>
 __device__ __forceinline__ int barrier_count(int i) {
-    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kMet = kOnes + 2, kSet = kMet + F::kSets * F::kGroups, kSoft = kSet + 3, kLast = kSoft + 2;
+    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kMet = kOnes + 2, kSet = kMet + F::kSets * F::kGroups, kSoft = kSet + 5, kLast = kSoft + 2;
     static_assert(offsetof(Ctl<F>, q_empty) == kLast * 8, "barriers in order");
     if (i < kOnes) return 1;
     if (i < kMet) return F::kQWarps;
     if (i < kSet) return 4;                 // a group's warps
-    if (i < kSoft) return F::kSetWarps;     // p_full, o_free
+    if (i < kSoft) return F::kSetWarps;     // p_full, o_free, left
     return i < kLast ? F::kSoftWarps : 1 + F::kSoftWarps;  // q_empty: the products that read it, too
 }
 
@@ -168,7 +172,7 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
 // Splits two values (magnitudes up to 448) into kParts pairs of codes. bf16 calls split fp16 values: exact differences.
 template <int kParts>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&parts)[kParts]) {
-    if constexpr (kParts <= 3) {
+    if constexpr (kParts <= 4) {
         __half2 t = __floats2half2_rn(a, b);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
@@ -250,20 +254,6 @@ __device__ __forceinline__ void store_columns(uint32_t addr, const float (&x)[N]
     else tmem_st32(addr, u);
 }
 
-// Multiplies a row's columns, kStep apart, by x.
-template <int kN, int kStep>
-__device__ __forceinline__ void scale_columns(uint32_t addr, float x) {
-    uint32_t u[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(u[i]) : "r"(addr + i * kStep));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        asm volatile("" : "+r"(u[i]));  // (written by the wait, to the compiler)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr + i * kStep), "r"(__float_as_uint(__uint_as_float(u[i]) * x)) : "memory");
-    }
-}
-
 // This thread's logits, from the sums of products with each part of the queries (part i's rows side by side).
 template <int kQP, int kRW>
 __device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
@@ -274,6 +264,19 @@ __device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
         s[r] = x[(kQP - 1) * kRW + r];
 #pragma unroll
         for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
+    }
+}
+
+// Eight rows' columns of O^T, put together from their parts, kStep columns apart.
+template <int kPP, int kStep>
+__device__ __forceinline__ void join_parts(uint32_t addr, float (&y)[8]) {
+    load_columns<8>(addr + (kPP - 1) * kStep, y);
+#pragma unroll
+    for (int i = kPP - 2; i >= 0; --i) {
+        float o[8];
+        load_columns<8>(addr + i * kStep, o);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) y[r] = fmaf(y[r], 0.0625f, o[r]);
     }
 }
 
@@ -586,18 +589,18 @@ __global__ void __launch_bounds__(F::kThreads, 1)
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
         // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do). First,
-        // word of the item that the share's begin cuts, for the join (of the first share that cuts it).
-        if (threadIdx.x == kWarpQ * 32) {
-            GroupedCut cut{};
-            const int64_t u0 = begin - w.tile, u1 = u0 + w.s.tiles;
-            if (w.left > 0 && w.tile > 0 && begin - per <= u0) {
-                Walk w1 = w;
-                next_piece(a, w1, p);
-                int parts = 2;  // the shares that hold a tile of it (begin < u1)
-                while (begin + (parts - 1) * per < u1) ++parts;
-                cut = GroupedCut{w.s.q0, p.h, p.row0, p.rows, grouped_slot(begin - per, u0, blockIdx.x - 1), parts, {0, 0}};
+        // some of the rows that have no positions.
+        for (int b = blockIdx.x; b < a.B; b += a.ctas) {
+            const GroupedSeq none = grouped_seq(a, b, false);
+            if (none.tiles) continue;
+            for (int64_t i = threadIdx.x - kWarpQ * 32; i < static_cast<int64_t>(none.n) * a.H * a.d_v; i += F::kQWarps * 32) {
+                const int64_t at = static_cast<int64_t>(none.q0) * a.H * a.d_v + i;
+                store_act(static_cast<T*>(a.out) + at, 0.0f);
+                if (i % a.d_v == 0) {
+                    if (a.lse) a.lse[at / a.d_v] = -INFINITY;
+                    if (a.weights_out) a.row_lse[at / a.d_v] = -INFINITY;
+                }
             }
-            a.cuts[blockIdx.x] = cut;
         }
         __syncwarp();
         int item = 0;
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         const uint32_t o_col = lane_base + F::kColO + group * F::kPP * kRW;
         float2* fm = S.fm[warp];
         float* fac = S.fac[warp];
-        int n = set, n_item = 0, st = set, sphase = 0, item = 0, met = 0, turn = 0;  // n: this set's next tile, n_item: the item's first
+        int n = set, n_item = 0, st = set, sphase = 0, item = 0, met = 0, turn = 0, left = 0;  // n: this set's next tile, n_item: the item's first
         bool ok = true;
         // The group's four warps meet (a barrier whose wait gives up, as every other).
         auto group_sync = [&]() {
@@ -646,8 +649,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&S.q_first));
             }
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(item ? &S.q_full[qb] : &S.q_first), (item >> 1) & 1, abort_flag, a.err));
-            float l[kRW], v_ref = 7.8886090522101181e-31f;  // 2^-100
-            float m = -INFINITY;                              // of row lane % kRW
+            float l[kRW], v_ref = 0x1p-100f;
+            float m = -INFINITY;  // what the weights of row lane % kRW refer to: its maximum so far, or up to kSlack less
 #pragma unroll
             for (int r = 0; r < kRW; ++r) l[r] = 0.0f;
             const float* factor = S.q_factor[qb] + group * kRW;
@@ -671,125 +674,145 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 tc_fence_after();
                 const float4 sc = S.scales[st];
                 const int valid = S.valid[st], pos = tile * kGroupedTile + j;
-                const bool here = (valid >> (quarter >> 1)) & 1 && pos < len;
-                float s[kRW];
-                load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, s);
-                if (valid != 3 || (tile + 1) * kGroupedTile > all_see) {
+                const bool here = (valid >> (quarter >> 1)) & 1 && pos < len, whole = valid == 3 && (tile + 1) * kGroupedTile <= all_see;
+                if (!whole && group == 0 && !here) {  // what the slot holds must not reach the products: 0 * NaN is NaN
+                    for (int c = 0; c < vc; ++c) {
+                        const uint32_t at = sRing + st * stage_bytes + v_off + 2 * c * kChunk + j * 128;
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r) s[r] = here && pos < seen[r] ? s[r] : -INFINITY;
-                    if (group == 0 && !here) {  // what the slot holds must not reach the products: 0 * NaN is NaN
-                        for (int c = 0; c < vc; ++c) {
-                            const uint32_t at = sRing + st * stage_bytes + v_off + 2 * c * kChunk + j * 128;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0) : "memory");
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0) : "memory");
                     }
                 }
-                // The rows' maxima over the tile: every warp's, then lane r of each warp looks after row r. A factor is
-                // positive and the same for a warp's positions.
-                float top = -INFINITY;
-#pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const float x = warp_max(s[r]);
-                    if (lane == r) top = x;
-                }
+                // lane r: row r's factor in this tile (positive, and the same for a warp's positions)
                 const float f = factor[lane % kRW] * (quarter < 2 ? (valid & 1 ? sc.x : 1.0f) : (valid & 2 ? sc.y : 1.0f));
-                if (lane < kRW) S.red[turn][set * kGroups + group][lane][quarter] = top * f;
-                group_sync();
-                if (!ok) break;
-                const float4 t = *reinterpret_cast<const float4*>(S.red[turn][set * kGroups + group][lane % kRW]);
-                turn ^= 1;
-                const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
-                // The weights carry their block's value scale, against a power of two no smaller than any so far.
                 const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
-                const uint32_t rows_up = __ballot_sync(0xFFFFFFFFu, m_new > m && lane < kRW);
-                if (lane < kRW) fm[lane] = make_float2(f, m_new == -INFINITY ? 0.0f : -m_new);
-                // this buffer of weights has been read, and O^T is this set's to rescale
-                if (n >= 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
-                if (fresh) wait_free();
-                if (!ok) break;
-                if (rows_up || v_top > v_ref) {  // the same for all of the group's threads
-                    float v_fac = 1.0f;
-                    if (v_top > v_ref) {
-                        const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
-                        v_fac = v_ref / ref;
-                        v_ref = ref;
+                uint32_t* flag = S.flag[turn][set * kGroups + group];
+                // The weights are formed against the maxima as they stand. Where a logit passes one by more than kSlack, in
+                // any of the group's warps, they are moved up first and the weights formed again.
+                bool move = fresh || v_top > v_ref, sure = false;
+                // (waited for as late as may be: this set's last weights have been read, and O^T is its own)
+                auto wait_values = [&]() {
+                    if (n >= 2) ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
+                    if (fresh) wait_free();
+                };
+                for (;;) {
+                    float s[kRW];
+                    load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, s);
+                    if (!whole) {
+#pragma unroll
+                        for (int r = 0; r < kRW; ++r) s[r] = here && pos < seen[r] ? s[r] : -INFINITY;
                     }
-                    const float up = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
-                    if (lane < kRW) fac[lane] = up;
-                    m = m_new;
-                    __syncwarp();
-                    if (!fresh) {
+                    if (move) {
+                        sure = true;
+                        // the rows' maxima over the tile: every warp's, then lane r of each warp looks after row r
+                        float top = -INFINITY;
 #pragma unroll
-                        for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
-                        if (kSets == 1) {
-                            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
-                            if (!ok) break;
+                        for (int r = 0; r < kRW; ++r) {
+                            const float x = warp_max(s[r]);
+                            if (lane == r) top = x;
                         }
-                        tc_fence_after();
-                        if (v_fac == 1.0f && __popc(rows_up) <= kRW / 4) {  // few rows: their columns alone
-                            for (uint32_t left = rows_up; left; left &= left - 1) {
-                                const int r = __ffs(left) - 1;
-                                const float x = __shfl_sync(0xFFFFFFFFu, up, r);
-                                for (int c = 0; c < vc; ++c) scale_columns<F::kPP, kRW>(o_col + (set * F::kVCMax + c) * F::kPN + r, x);
-                            }
-                        } else {
+                        if (lane < kRW) S.red[set * kGroups + group][lane][quarter] = top * f;
+                        group_sync();
+                        if (!ok) break;
+                        const float4 t = *reinterpret_cast<const float4*>(S.red[set * kGroups + group][lane % kRW]);
+                        const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
+                        // the weights carry their block's value scale, against a power of two no smaller than any so far
+                        float v_fac = 1.0f;
+                        if (v_top > v_ref) {
+                            const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
+                            v_fac = v_ref / ref;
+                            v_ref = ref;
+                        }
+                        if (lane < kRW) fac[lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
+                        m = m_new;
+                        __syncwarp();
+                        if (!fresh) {
+#pragma unroll
+                            for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
+                            wait_values();
+                            if (kSets == 1) ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
+                            if (!ok) break;
+                            tc_fence_after();
                             for (int c = 0; c < vc; ++c) {
+#pragma unroll 1
+                                for (int i = 0; i < F::kPP * kRW; i += 8) {
+                                    float o[8];
+                                    const uint32_t at = o_col + (set * F::kVCMax + c) * F::kPN + i;
+                                    load_columns<8>(at, o);
 #pragma unroll
-                                for (int i = 0; i < F::kPP; ++i) {
-                                    float o[kRW];
-                                    const uint32_t at = o_col + (set * F::kVCMax + c) * F::kPN + i * kRW;
-                                    load_columns<kRW>(at, o);
-#pragma unroll
-                                    for (int r = 0; r < kRW; ++r) o[r] *= fac[r] * v_fac;
-                                    store_columns<kRW>(at, o);
+                                    for (int r = 0; r < 8; ++r) o[r] *= fac[(i + r) % kRW] * v_fac;
+                                    store_columns<8>(at, o);
                                 }
                             }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
+                        group_sync();  // the maxima have been read
+                        if (!ok) break;
                     }
-                } else {
+                    // (a row without positions so far: any logit moves it)
                     __syncwarp();
-                }
-                fresh = false;
-                if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
-                    float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
+                    if (lane < kRW) fm[lane] = make_float2(f, m == -INFINITY ? 1e30f : -m);
+                    __syncwarp();
+                    if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
+                        float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r)
-                        if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * fm[r].x;
-                }
-                const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (256.0f / v_ref) : 0.0f;
-                const uint32_t p_buf = sP + (n & 1) * F::kPBytes + j * 16;
-                constexpr int kChunkRows = kRW < 16 ? 8 : 16;
+                        for (int r = 0; r < kRW; ++r)
+                            if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * fm[r].x;
+                    }
+                    float over = -INFINITY;
 #pragma unroll
-                for (int r0 = 0; r0 < kRW; r0 += kChunkRows) {
-                    uint32_t parts[kChunkRows / 2][F::kPP];
-#pragma unroll
-                    for (int i = 0; i < kChunkRows / 2; ++i) {
-                        const int r = r0 + 2 * i;
+                    for (int r = 0; r < kRW; r += 2) {
                         const float4 g = *reinterpret_cast<const float4*>(fm + r);
-                        const float p0 = ex2(fmaf(s[r], g.x, g.y)), p1 = ex2(fmaf(s[r + 1], g.z, g.w));
-                        l[r] += p0;
-                        l[r + 1] += p1;
-                        split_pair<F::kPP>(p0 * tv, p1 * tv, parts[i]);
+                        s[r] = fmaf(s[r], g.x, g.y);
+                        s[r + 1] = fmaf(s[r + 1], g.z, g.w);
+                        over = fmaxf(over, fmaxf(s[r], s[r + 1]));
+                    }
+                    if (!sure) {  // the others' word is waited for when the weights are done
+                        const bool up = __any_sync(0xFFFFFFFFu, over > kSlack);
+                        if (lane == 0) {
+                            flag[quarter] = up;
+                            mbar_arrive(smem_u32(&S.met[set * kGroups + group]));
+                        }
+                    }
+                    wait_values();
+                    if (!ok) break;
+                    const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (kTop / v_ref) : 0.0f;
+                    const uint32_t p_buf = sP + (n & 1) * F::kPBytes + j * 16;
+#pragma unroll
+                    for (int r0 = 0; r0 < kRW; r0 += 8) {
+                        uint32_t parts[4][F::kPP];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + 2 * i;
+                            s[r] = ex2(s[r]);
+                            s[r + 1] = ex2(s[r + 1]);
+                            split_pair<F::kPP>(s[r] * tv, s[r + 1] * tv, parts[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < F::kPP; ++i) {
+                            const int col = group * F::kPP * kRW + i * kRW + r0;
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_buf + (col >> 4) * 2048 + (col & 8)),
+                                         "r"(parts[0][i] | parts[1][i] << 16), "r"(parts[2][i] | parts[3][i] << 16)
+                                         : "memory");
+                        }
+                    }
+                    if (!sure) {
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[set * kGroups + group]), met, abort_flag, a.err));
+                        met ^= 1;
+                        if (!ok) break;
+                        const uint4 u = *reinterpret_cast<const uint4*>(flag);
+                        if (u.x | u.y | u.z | u.w) {
+                            move = true;
+                            continue;
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < F::kPP; ++i) {
-                        const int col = group * F::kPP * kRW + i * kRW + r0;
-                        const uint32_t at = p_buf + (col >> 4) * 2048 + (col & 8);
-                        if constexpr (kChunkRows == 8)
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
-                                         "r"(parts[2][i] | parts[3][i] << 16)
-                                         : "memory");
-                        else
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
-                                         "r"(parts[2][i] | parts[3][i] << 16),
-                                         "r"(parts[kChunkRows / 2 - 4][i] | parts[kChunkRows / 2 - 3][i] << 16),
-                                         "r"(parts[kChunkRows / 2 - 2][i] | parts[kChunkRows / 2 - 1][i] << 16)
-                                         : "memory");
-                    }
+                    for (int r = 0; r < kRW; ++r) l[r] += s[r];
+                    break;
                 }
+                if (!ok) break;
+                turn ^= 1;
+                fresh = false;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -805,9 +828,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 S.fin_l[qb][set][group * kRW + lane][quarter] = sum;
                 S.fin_m[qb][set][group * kRW + lane] = m;
             }
-            if (lane == 0) S.fin_unit[qb][set] = any ? v_ref * (1.0f / 256.0f) : 0.0f;
+            if (lane == 0) S.fin_unit[qb][set] = any ? v_ref * (1.0f / kTop) : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.fin));
+            const bool complete = p.tile0 == 0 && p.tile1 == w.s.tiles;
             if (kSets == 1 || ((n_end - 1) & 1) == set) {
                 // the last tile was this set's: the rows, or their partial
                 ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
@@ -815,7 +839,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 // lane r: row r's maximum and sum over both sets, and what each set's O^T is to be multiplied by
-                const bool complete = p.tile0 == 0 && p.tile1 == w.s.tiles;
                 const int slot = grouped_slot(begin, p.t, blockIdx.x), rr = group * kRW + lane % kRW;
                 float top = -INFINITY, all = 0.0f, f[kSets];
 #pragma unroll
@@ -840,46 +863,65 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const bool both = kSets == 2 && S.fin_unit[qb][other] != 0.0f;
                 const float f_own = f[kSets == 1 ? 0 : set] * inv, f_other = f[other] * inv;
                 for (int c = 0; c < vc; ++c) {
-                    float y[kRW];
-#pragma unroll
-                    for (int i = F::kPP - 1; i >= 0; --i) {
-                        float o[kRW];
-                        load_columns<kRW>(o_col + (set * F::kVCMax + c) * F::kPN + i * kRW, o);
-#pragma unroll
-                        for (int r = 0; r < kRW; ++r) y[r] = i == F::kPP - 1 ? o[r] : fmaf(y[r], 0.0625f, o[r]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < kRW; ++r) y[r] *= __shfl_sync(0xFFFFFFFFu, f_own, r);
-                    if (both) {
-                        float x[kRW];
-#pragma unroll
-                        for (int i = F::kPP - 1; i >= 0; --i) {
-                            float o[kRW];
-                            load_columns<kRW>(o_col + (other * F::kVCMax + c) * F::kPN + i * kRW, o);
-#pragma unroll
-                            for (int r = 0; r < kRW; ++r) x[r] = i == F::kPP - 1 ? o[r] : fmaf(x[r], 0.0625f, o[r]);
-                        }
-#pragma unroll
-                        for (int r = 0; r < kRW; ++r) y[r] = fmaf(x[r], __shfl_sync(0xFFFFFFFFu, f_other, r), y[r]);
-                    }
                     const int e = c * 128 + j;
+                    const uint32_t own_col = o_col + (set * F::kVCMax + c) * F::kPN, other_col = o_col + (other * F::kVCMax + c) * F::kPN;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < kRW; r0 += 8) {
+                        float y[8], x[8];
+                        join_parts<F::kPP, kRW>(own_col + r0, y);
+                        if (both) join_parts<F::kPP, kRW>(other_col + r0, x);
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r) {
-                        const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r);
-                        if (group * kRW + r < p.rows && e < a.d_v) {
-                            if (complete) store_act(static_cast<T*>(a.out) + at * a.d_v + e, y[r]);
-                            else a.part_o[(static_cast<int64_t>(slot) * kRows + group * kRW + r) * a.d_v + e] = y[r];
+                        for (int r = 0; r < 8; ++r) {
+                            y[r] *= __shfl_sync(0xFFFFFFFFu, f_own, r0 + r);
+                            const float fo = __shfl_sync(0xFFFFFFFFu, f_other, r0 + r);
+                            if (both) y[r] = fmaf(x[r], fo, y[r]);
+                            const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r0 + r);
+                            const int of_item = group * kRW + r0 + r;
+                            if (of_item < p.rows && e < a.d_v) {
+                                if (complete) store_act(static_cast<T*>(a.out) + at * a.d_v + e, y[r]);
+                                else a.part_o[(static_cast<int64_t>(slot) * kRows + of_item) * a.d_v + e] = y[r];
+                            }
                         }
                     }
                 }
                 tc_fence_before();  // O^T has been read before the next item's first product may overwrite it
                 __syncwarp();
                 if (lane == 0 && kSets == 2) mbar_arrive(smem_u32(&S.o_free));
+                if (!complete) {
+                    // The CTA that leaves an item's last partial joins them, in order. (Mostly the one whose share ends in
+                    // it, with nothing left to do: the others got theirs out at their shares' begin.)
+                    const int64_t u0 = p.t - p.tile0, u1 = u0 + w.s.tiles;
+                    const int c0 = static_cast<int>(u0 < (1ll << 31) && per < (1ll << 31) ? static_cast<uint32_t>(u0) / static_cast<uint32_t>(per) : u0 / per);
+                    int parts = 2;
+                    while ((c0 + parts) * per < u1) ++parts;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&S.left[0]));
+                    if (warp == set * F::kSetWarps) {
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[0]), left, abort_flag, a.err));
+                        if (lane == 0) {
+                            __threadfence();
+                            const int shift = 8 * (c0 & 3);
+                            const uint32_t old = ok ? atomicAdd(a.arrived + (c0 >> 2), 1u << shift) : 0;
+                            const bool last = ok && static_cast<int>((old >> shift) & 255u) == parts - 1;
+                            if (last) atomicSub(a.arrived + (c0 >> 2), static_cast<uint32_t>(parts) << shift);  // for the next call
+                            __threadfence();
+                            S.last_part = last;
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(smem_u32(&S.left[1]));
+                    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[1]), left, abort_flag, a.err));
+                    if (!ok) break;
+                    if (S.last_part)
+                        grouped_join<T, kRows < 32 ? 2 : 4, kRows < 32 ? 4 : 2>(a, S.row_at[qb], p.rows, grouped_slot(c0 * per, u0, c0), parts,
+                                                                                warp - set * F::kSetWarps, F::kSetWarps);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.q_empty[qb]));
             n_item = n_end;
             ++item;
+            if (!complete) left ^= 1;  // (whichever set it was)
         }
     }
     tc_fence_before();
@@ -909,16 +951,19 @@ static bool launch_form(const GroupedArgs& a, cudaStream_t s) {
 }  // namespace gtc
 
 // Rows of an item: as many as the average sequence of the call has for a key head, in powers of two. Of fp32 queries and
-// of wide values fewer: their parts fill tensor memory.
+// of wide values fewer: their parts fill tensor memory (and of wide keys, shared memory).
 int grouped_row_tile(const dsa_grouped_dims& d, int T) {
     const int64_t rows = (static_cast<int64_t>(T) + d.B - 1) / d.B * (d.H / d.H_kv);
-    const int most = d.type == DSA_F32 ? 16 : d.d_v > 128 ? 32 : 64;
+    const int most = d.type == DSA_F32 || d.d_v > 128 ? 16 : d.d_qk > 128 ? 32 : 64;
     int tile = 8;
     while (tile < rows && tile < most) tile *= 2;
     return tile;
 }
 
-int grouped_ctas(const dsa_grouped_dims&) { return device_sm_count(); }
+int grouped_ctas(const dsa_grouped_dims&) {
+    const int sms = device_sm_count();
+    return sms < 240 ? sms : 240;  // (a byte for each in the workspace's first 256)
+}
 
 bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches) {
     using namespace gtc;
@@ -927,10 +972,10 @@ bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches) {
         ok = a.row_tile == 8 ? launch_form<float, Form<8, 1, 2, 6, 6, 4>>(a, s) : launch_form<float, Form<8, 2, 1, 6, 6, 2>>(a, s);
     } else {
         switch (a.row_tile) {
-            case 8: ok = launch_form<__nv_bfloat16, Form<8, 1, 2, 2, 3, 4>>(a, s); break;
-            case 16: ok = launch_form<__nv_bfloat16, Form<16, 1, 2, 2, 3, 4>>(a, s); break;
-            case 32: ok = launch_form<__nv_bfloat16, Form<16, 2, 2, 2, 3, 2>>(a, s); break;
-            default: ok = launch_form<__nv_bfloat16, Form<16, 4, 1, 2, 3, 2>>(a, s); break;
+            case 8: ok = launch_form<__nv_bfloat16, Form<8, 1, 2, 2, 4, 4>>(a, s); break;
+            case 16: ok = launch_form<__nv_bfloat16, Form<16, 1, 2, 2, 4, 4>>(a, s); break;
+            case 32: ok = launch_form<__nv_bfloat16, Form<16, 2, 1, 2, 4, 2>>(a, s); break;
+            default: ok = launch_form<__nv_bfloat16, Form<16, 4, 1, 2, 4, 2>>(a, s); break;
         }
     }
     if (ok) ++*launches;

@@ -224,15 +224,6 @@ bool launch_prompt_tc(const PromptArgs& a, cudaStream_t s, int* launches);
 
 // ---- grouped-head cache -------------------------------------------------------------------------
 
-// Where a CTA's share of the grouped-head attention begins inside an item that no share before it cut: the item's rows,
-// and the partials to join.
-struct alignas(16) GroupedCut {
-    int q0, h, row0, rows;  // rows 0: nothing to join
-    int slot0;              // the first partial; the others are slots 2 * (slot0 / 2 + 1), + 2, ...
-    int parts;
-    int pad[2];
-};
-
 struct GroupedArgs {
     int type;
     int B, max_blocks, num_blocks;
@@ -255,7 +246,7 @@ struct GroupedArgs {
     int* err;
     int row_tile;       // rows of an item
     int ctas;           // CTAs of the attention
-    GroupedCut* cuts;   // [ctas]
+    uint32_t* arrived;  // partials of the item that share c cuts first: byte c (all 0 between calls)
     float* part_o;      // [2 * ctas][row_tile][d_v] unnormalised outputs of cut items
     float2* part_ml;    // [2 * ctas][row_tile] (running maximum in powers of two, sum)
     float* row_lse;     // [T][H] log2 of the sums of 2^z (weights only)
@@ -301,7 +292,7 @@ int grouped_row_tile(const dsa_grouped_dims& d, int T);
 int grouped_ctas(const dsa_grouped_dims& d);
 bool launch_grouped_append(const GroupedAppendArgs& a, cudaStream_t s, int* launches);
 bool launch_grouped_attn(const GroupedArgs& a, cudaStream_t s, int* launches);
-bool launch_grouped_join(const GroupedArgs& a, cudaStream_t s, int* launches);
+bool launch_grouped_weights(const GroupedArgs& a, cudaStream_t s, int* launches);
 bool launch_grouped_evict(const GroupedEvictArgs& a, cudaStream_t s, int* launches);
 
 bool launch_attn_tc(const AttnArgs& a, cudaStream_t s, int* launches);
