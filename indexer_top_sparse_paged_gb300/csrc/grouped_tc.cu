@@ -66,6 +66,17 @@ __device__ __forceinline__ bool next_piece(const GroupedArgs& a, Walk& w, Piece&
     return true;
 }
 
+// What the products and the softmax need to know of a piece, beside its queries. tiles 0: there are no more.
+struct Item {
+    int tile0, tiles, len;
+    int all_see;         // every row sees the positions below this
+    int rows;
+    int complete;        // the piece is a whole item; otherwise:
+    int slot;            // its partial
+    int c0, join_slot, parts;  // the CTA and slot of the item's first partial, and their number
+    int64_t t;           // its first tile in the call's line
+};
+
 // Compiled forms: rows of a softmax thread, warpgroups that share a tile's rows, sets that take tiles in turn, parts of a
 // query and of a weight, buffers of logits.
 template <int kRW_, int kGroups_, int kSets_, int kQP_, int kPP_, int kSB_>
@@ -98,10 +109,11 @@ struct Ctl {
     alignas(16) int row_at[2][F::kRows];      // token * H + head
     alignas(16) float red[F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
     alignas(16) uint32_t flag[2][F::kSets * F::kGroups][4];   // a warp's word on whether they must move
-    alignas(16) float2 fm[F::kSoftWarps][F::kRW];  // each warp's own: a row's factor in this tile, minus its maximum
+    alignas(16) float2 fm[F::kSoftWarps][F::kRW];  // each warp's own: a row's factor, minus what its weights refer to
     alignas(16) float fac[F::kSoftWarps][F::kRW];  // and what its sums are to be multiplied by
     alignas(16) float fin_l[2][F::kSets][F::kRows][4], fin_m[2][F::kSets][F::kRows];  // a set's share of an item
     float fin_unit[2][F::kSets];  // of its O^T; 0: it had no tile
+    Item item[2];
     uint32_t tmem_base;
     int abort_flag;
     int last_part;  // whether the CTA left the last partial of an item
@@ -254,9 +266,9 @@ __device__ __forceinline__ void store_columns(uint32_t addr, const float (&x)[N]
     else tmem_st32(addr, u);
 }
 
-// This thread's logits, from the sums of products with each part of the queries (part i's rows side by side).
+// This thread's products with the keys (times their block's scale), from the sums with each part of the queries (part i's rows side by side).
 template <int kQP, int kRW>
-__device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
+__device__ __forceinline__ void load_logits(uint32_t addr, float scale, float (&s)[kRW]) {
     float x[kQP * kRW];
     load_columns<kQP * kRW>(addr, x);
 #pragma unroll
@@ -264,6 +276,7 @@ __device__ __forceinline__ void load_logits(uint32_t addr, float (&s)[kRW]) {
         s[r] = x[(kQP - 1) * kRW + r];
 #pragma unroll
         for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
+        s[r] *= scale;
     }
 }
 
@@ -558,12 +571,16 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             if (++st_v == stages) st_v = 0;
             ++done;
         };
-        while (ok && next_piece(a, w, p)) {
+        for (;; ++item) {
             const int qb = item & 1;
             while (ok && done < last) values();  // the item before that one must end for this one's queries to come
             last = n;
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(item ? &S.q_full[qb] : &S.q_first), (item >> 1) & 1, abort_flag, a.err));
-            for (int tile = p.tile0; ok && tile < p.tile1; ++tile) {
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            const int tiles = ok ? S.item[qb].tiles : 0;
+            if (!tiles) break;
+            ok = __all_sync(0xFFFFFFFFu, item || mbar_wait(smem_u32(&S.q_first), 0, abort_flag, a.err));
+            if (!ok) break;
+            for (int tile = 0; tile < tiles; ++tile) {
                 // this buffer of logits is free: V^T P^T of tile n - kSB has been issued, after its weights came
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), phase, abort_flag, a.err));
                 if (!ok) break;
@@ -574,39 +591,25 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     warp_mma_f8(tmem + (n & (F::kSB - 1)) * F::kSN, da, db, idesc_f8(F::kSN, 0u, 0u), k ? 1u : 0u);
                 }
                 warp_tc_commit(smem_u32(&S.s_full[n & (F::kSB - 1)]));
-                if (tile + 1 == p.tile1) warp_tc_commit(smem_u32(&S.q_empty[qb]));
+                if (tile + 1 == tiles) warp_tc_commit(smem_u32(&S.q_empty[qb]));
                 const uint32_t bit = 1u << (n & 31);
-                first = tile - p.tile0 < kSets ? first | bit : first & ~bit;
+                first = tile < kSets ? first | bit : first & ~bit;
                 ++n;
                 if (++st == stages) st = 0, phase ^= 1;
                 if (n - done > lead) values();
+                if (!ok) break;
             }
-            ++item;
         }
         while (ok && done < n) values();
         warp_tc_commit(smem_u32(&S.mma_done));  // every product issued so far
         if (lane == 0) mbar_wait_drain(smem_u32(&S.mma_done), 0, a.err);
     } else if (warp >= kWarpQ) {
         // --------------------------------------------------------------------------------- queries
-        // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do). First,
-        // some of the rows that have no positions.
-        for (int b = blockIdx.x; b < a.B; b += a.ctas) {
-            const GroupedSeq none = grouped_seq(a, b, false);
-            if (none.tiles) continue;
-            for (int64_t i = threadIdx.x - kWarpQ * 32; i < static_cast<int64_t>(none.n) * a.H * a.d_v; i += F::kQWarps * 32) {
-                const int64_t at = static_cast<int64_t>(none.q0) * a.H * a.d_v + i;
-                store_act(static_cast<T*>(a.out) + at, 0.0f);
-                if (i % a.d_v == 0) {
-                    if (a.lse) a.lse[at / a.d_v] = -INFINITY;
-                    if (a.weights_out) a.row_lse[at / a.d_v] = -INFINITY;
-                }
-            }
-        }
-        __syncwarp();
-        int item = 0;
-        bool ok = true;
-        while (ok && next_piece(a, w, p)) {
+        // Two warps bring the queries of the next item while this one runs (of the first, the softmax's warps do).
+        for (int item = 0;; ++item) {
             const int qb = item & 1;
+            const bool more = next_piece(a, w, p);
+            bool ok = true;
             if (item > 0) {
                 // (this wait lasts as long as an item; what stalls in it gives up by itself)
                 const long long t0 = clock64();
@@ -620,10 +623,42 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                split_queries<T, F>(a, w.s, p, S, qb, sQ + qb * kc * F::kQBytes, kc, warp - kWarpQ, F::kQWarps);
+                if (more) split_queries<T, F>(a, w.s, p, S, qb, sQ + qb * kc * F::kQBytes, kc, warp - kWarpQ, F::kQWarps);
             }
-            if (lane == 0) mbar_arrive(smem_u32(&S.q_full[qb]));
-            ++item;
+            if (lane == 0) {
+                if (warp == kWarpQ) {
+                    Item it{};
+                    if (more) {
+                        it.tile0 = p.tile0, it.tiles = p.tile1 - p.tile0, it.len = w.s.len, it.rows = p.rows, it.t = p.t;
+                        it.all_see = min(w.s.len, w.s.len - w.s.n + p.row0 / a.G + 1);
+                        it.complete = p.tile0 == 0 && p.tile1 == w.s.tiles;
+                        if (!it.complete) {
+                            const int64_t u0 = p.t - p.tile0, u1 = u0 + w.s.tiles;
+                            it.slot = grouped_slot(begin, p.t, blockIdx.x);
+                            it.c0 = static_cast<int>(u0 < (1ll << 31) && per < (1ll << 31) ? static_cast<uint32_t>(u0) / static_cast<uint32_t>(per) : u0 / per);
+                            it.join_slot = grouped_slot(it.c0 * per, u0, it.c0);
+                            it.parts = 2;
+                            while ((it.c0 + it.parts) * per < u1) ++it.parts;
+                        }
+                    }
+                    S.item[qb] = it;
+                }
+                mbar_arrive(smem_u32(&S.q_full[qb]));
+            }
+            if (!more) break;
+        }
+        // and then some of the rows that have no positions
+        for (int b = blockIdx.x; b < a.B; b += a.ctas) {
+            const GroupedSeq none = grouped_seq(a, b, false);
+            if (none.tiles) continue;
+            for (int64_t i = threadIdx.x - kWarpQ * 32; i < static_cast<int64_t>(none.n) * a.H * a.d_v; i += F::kQWarps * 32) {
+                const int64_t at = static_cast<int64_t>(none.q0) * a.H * a.d_v + i;
+                store_act(static_cast<T*>(a.out) + at, 0.0f);
+                if (i % a.d_v == 0) {
+                    if (a.lse) a.lse[at / a.d_v] = -INFINITY;
+                    if (a.weights_out) a.row_lse[at / a.d_v] = -INFINITY;
+                }
+            }
         }
     } else {
         // --------------------------------------------------------------------------------- softmax
@@ -642,21 +677,23 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[set * kGroups + group]), met, abort_flag, a.err));
             met ^= 1;
         };
-        while (ok && next_piece(a, w, p)) {
-            const int qb = item & 1, n_end = n_item + p.tile1 - p.tile0, len = w.s.len;
-            if (item == 0) {
-                split_queries<T, F>(a, w.s, p, S, 0, sQ, kc, warp, F::kSoftWarps);
-                if (lane == 0) mbar_arrive(smem_u32(&S.q_first));
-            }
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(item ? &S.q_full[qb] : &S.q_first), (item >> 1) & 1, abort_flag, a.err));
+        if (next_piece(a, w, p)) {
+            split_queries<T, F>(a, w.s, p, S, 0, sQ, kc, warp, F::kSoftWarps);
+            if (lane == 0) mbar_arrive(smem_u32(&S.q_first));
+        }
+        for (;; ++item) {
+            const int qb = item & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            const Item& it = S.item[qb];
+            if (!ok || !it.tiles) break;
+            ok = __all_sync(0xFFFFFFFFu, item || mbar_wait(smem_u32(&S.q_first), 0, abort_flag, a.err));
+            const int n_end = n_item + it.tiles, len = it.len, all_see = it.all_see;
             float l[kRW], v_ref = 0x1p-100f;
             float m = -INFINITY;  // what the weights of row lane % kRW refer to: its maximum so far, or up to kSlack less
 #pragma unroll
             for (int r = 0; r < kRW; ++r) l[r] = 0.0f;
-            const float* factor = S.q_factor[qb] + group * kRW;
+            const float f_lane = S.q_factor[qb][group * kRW + lane % kRW];  // lane r: row r's factor (positive)
             const int* seen = S.seen[qb] + group * kRW;
-            // every row sees the positions below this
-            const int all_see = min(len, len - w.s.n + p.row0 / a.G + 1);
             // the item before this has left O^T and the sets' shares
             bool waited = kSets == 1 || item == 0;
             auto wait_free = [&]() {
@@ -667,7 +704,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const bool any = n < n_end;
             bool fresh = true;
             for (; ok && n < n_end; n += kSets) {
-                const int tile = p.tile0 + n - n_item;
+                const int tile = it.tile0 + n - n_item;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), sphase, abort_flag, a.err) &&
                                                  mbar_wait(smem_u32(&S.s_full[n & (F::kSB - 1)]), (n / F::kSB) & 1, abort_flag, a.err));
                 if (!ok) break;
@@ -683,8 +720,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0) : "memory");
                     }
                 }
-                // lane r: row r's factor in this tile (positive, and the same for a warp's positions)
-                const float f = factor[lane % kRW] * (quarter < 2 ? (valid & 1 ? sc.x : 1.0f) : (valid & 2 ? sc.y : 1.0f));
+                const float ks = !here ? 1.0f : quarter < 2 ? sc.x : sc.y;
                 const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
                 uint32_t* flag = S.flag[turn][set * kGroups + group];
                 // The weights are formed against the maxima as they stand. Where a logit passes one by more than kSlack, in
@@ -697,7 +733,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 };
                 for (;;) {
                     float s[kRW];
-                    load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, s);
+                    load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, ks, s);
                     if (!whole) {
 #pragma unroll
                         for (int r = 0; r < kRW; ++r) s[r] = here && pos < seen[r] ? s[r] : -INFINITY;
@@ -711,7 +747,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             const float x = warp_max(s[r]);
                             if (lane == r) top = x;
                         }
-                        if (lane < kRW) S.red[set * kGroups + group][lane][quarter] = top * f;
+                        if (lane < kRW) S.red[set * kGroups + group][lane][quarter] = top * f_lane;
                         group_sync();
                         if (!ok) break;
                         const float4 t = *reinterpret_cast<const float4*>(S.red[set * kGroups + group][lane % kRW]);
@@ -725,6 +761,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         }
                         if (lane < kRW) fac[lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
                         m = m_new;
+                        // (a row without positions so far: any logit moves it)
+                        if (lane < kRW) fm[lane] = make_float2(f_lane, m == -INFINITY ? 1e30f : -m);
                         __syncwarp();
                         if (!fresh) {
 #pragma unroll
@@ -749,15 +787,11 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         group_sync();  // the maxima have been read
                         if (!ok) break;
                     }
-                    // (a row without positions so far: any logit moves it)
-                    __syncwarp();
-                    if (lane < kRW) fm[lane] = make_float2(f, m == -INFINITY ? 1e30f : -m);
-                    __syncwarp();
-                    if (a.weights_out && p.t + tile - p.tile0 < a.max_tiles) {
-                        float* to = a.z + ((p.t + tile - p.tile0) * kRows + group * kRW) * kGroupedTile + j;
+                    if (a.weights_out && it.t + n - n_item < a.max_tiles) {
+                        float* to = a.z + ((it.t + n - n_item) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
                         for (int r = 0; r < kRW; ++r)
-                            if (group * kRW + r < p.rows) to[r * kGroupedTile] = s[r] * fm[r].x;
+                            if (group * kRW + r < it.rows) to[r * kGroupedTile] = s[r] * fm[r].x;
                     }
                     float over = -INFINITY;
 #pragma unroll
@@ -831,7 +865,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             if (lane == 0) S.fin_unit[qb][set] = any ? v_ref * (1.0f / kTop) : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.fin));
-            const bool complete = p.tile0 == 0 && p.tile1 == w.s.tiles;
+            const bool complete = it.complete;
             if (kSets == 1 || ((n_end - 1) & 1) == set) {
                 // the last tile was this set's: the rows, or their partial
                 ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
@@ -839,7 +873,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 // lane r: row r's maximum and sum over both sets, and what each set's O^T is to be multiplied by
-                const int slot = grouped_slot(begin, p.t, blockIdx.x), rr = group * kRW + lane % kRW;
+                const int slot = it.slot, rr = group * kRW + lane % kRW;
                 float top = -INFINITY, all = 0.0f, f[kSets];
 #pragma unroll
                 for (int i = 0; i < kSets; ++i) top = fmaxf(top, S.fin_m[qb][i][rr]);
@@ -853,7 +887,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 }
                 const float inv = all == 0.0f ? 0.0f : complete ? 1.0f / all : 1.0f;
                 const int row_at = S.row_at[qb][rr];
-                if (quarter == 0 && lane < kRW && rr < p.rows) {
+                if (quarter == 0 && lane < kRW && rr < it.rows) {
                     const float lse2 = all == 0.0f ? -INFINITY : top + log2f(all);
                     if (!complete) a.part_ml[slot * kRows + rr] = make_float2(top, all);
                     if (complete && a.lse) a.lse[row_at] = lse2 * 0.6931471805599453f;
@@ -877,7 +911,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             if (both) y[r] = fmaf(x[r], fo, y[r]);
                             const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r0 + r);
                             const int of_item = group * kRW + r0 + r;
-                            if (of_item < p.rows && e < a.d_v) {
+                            if (of_item < it.rows && e < a.d_v) {
                                 if (complete) store_act(static_cast<T*>(a.out) + at * a.d_v + e, y[r]);
                                 else a.part_o[(static_cast<int64_t>(slot) * kRows + of_item) * a.d_v + e] = y[r];
                             }
@@ -890,20 +924,16 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (!complete) {
                     // The CTA that leaves an item's last partial joins them, in order. (Mostly the one whose share ends in
                     // it, with nothing left to do: the others got theirs out at their shares' begin.)
-                    const int64_t u0 = p.t - p.tile0, u1 = u0 + w.s.tiles;
-                    const int c0 = static_cast<int>(u0 < (1ll << 31) && per < (1ll << 31) ? static_cast<uint32_t>(u0) / static_cast<uint32_t>(per) : u0 / per);
-                    int parts = 2;
-                    while ((c0 + parts) * per < u1) ++parts;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.left[0]));
                     if (warp == set * F::kSetWarps) {
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[0]), left, abort_flag, a.err));
                         if (lane == 0) {
                             __threadfence();
-                            const int shift = 8 * (c0 & 3);
-                            const uint32_t old = ok ? atomicAdd(a.arrived + (c0 >> 2), 1u << shift) : 0;
+                            const int shift = 8 * (it.c0 & 3), parts = it.parts;
+                            const uint32_t old = ok ? atomicAdd(a.arrived + (it.c0 >> 2), 1u << shift) : 0;
                             const bool last = ok && static_cast<int>((old >> shift) & 255u) == parts - 1;
-                            if (last) atomicSub(a.arrived + (c0 >> 2), static_cast<uint32_t>(parts) << shift);  // for the next call
+                            if (last) atomicSub(a.arrived + (it.c0 >> 2), static_cast<uint32_t>(parts) << shift);  // for the next call
                             __threadfence();
                             S.last_part = last;
                         }
@@ -913,14 +943,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[1]), left, abort_flag, a.err));
                     if (!ok) break;
                     if (S.last_part)
-                        grouped_join<T, kRows < 32 ? 2 : 4, kRows < 32 ? 4 : 2>(a, S.row_at[qb], p.rows, grouped_slot(c0 * per, u0, c0), parts,
+                        grouped_join<T, kRows < 32 ? 2 : 4, kRows < 32 ? 4 : 2>(a, S.row_at[qb], it.rows, it.join_slot, it.parts,
                                                                                 warp - set * F::kSetWarps, F::kSetWarps);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.q_empty[qb]));
             n_item = n_end;
-            ++item;
             if (!complete) left ^= 1;  // (whichever set it was)
         }
     }
