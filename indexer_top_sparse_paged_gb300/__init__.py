@@ -339,6 +339,9 @@ ROPE_SCALINGS = {"linear": 0, "base": 1, "yarn": 2}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
@@ -621,17 +624,35 @@ def _fp32(t, n: int, name: str):
         raise ValueError(f"{name} must be a float32 tensor of {n} elements")
 
 
+def _all_fit(wanted, dev: int):
+    """The addresses of tensors that all are as they should be -- (tensor, type, elements) -- or None: the checks one by
+    one, which take longer, then say what is wrong."""
+    grad = torch.is_grad_enabled()
+    at = []
+    for t, dtype, n in wanted:
+        if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous() or (grad and t.requires_grad):
+            return None
+        at.append(t.data_ptr())
+    return at
+
+
 def grouped_append(dims: GroupedDims, k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu=None, *,
                    ws, stream=None) -> None:
     """Writes new tokens (k_new[T][H_kv][d_qk], v_new[T][H_kv][d_v], strided views allowed) into the caches as e4m3 codes
     with one scale per block and head: rows cu[b] .. cu[b + 1] - 1 are the last of sequence b's seq_lens[b] positions."""
     T = k_new.shape[0]
-    dev = _device(k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu, ws)
+    dev = _device(k_new, v_new, cu)
     k = _grouped_rows(k_new, T, dims.H_kv, dims.d_qk, dims, "k_new")
     v = _grouped_rows(v_new, T, dims.H_kv, dims.d_v, dims, "v_new")
-    _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
-    st = lib().dsa_grouped_append(dims, *k, *v, _at(block_table), _at(seq_lens), _at(cu), T, _at(k_cache), _at(k_scale),
-                                  _at(v_cache), _at(v_scale), _at(ws), ws.numel(), _raw_stream(dev, stream))
+    rows = dims.num_blocks * dims.H_kv
+    at = _all_fit(((block_table, _I32, dims.B * dims.max_blocks), (seq_lens, _I32, dims.B), (k_cache, _U8, 64 * rows * dims.d_qk),
+                   (k_scale, _F32, rows), (v_cache, _U8, 64 * rows * dims.d_v), (v_scale, _F32, rows), (ws, _U8, 0)), dev)
+    if at is None or cu is not None or T != dims.B:
+        _device(k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu, ws)
+        _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
+        at = [_at(t) for t in (block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, ws)]
+    st = lib().dsa_grouped_append(dims, *k, *v, at[0], at[1], _at(cu), T, at[2], at[3], at[4], at[5], at[6], ws.numel(),
+                                  _raw_stream(dev, stream))
     if st:
         _check("dsa_grouped_append", st)
 
@@ -646,9 +667,15 @@ def grouped_attn(dims: GroupedDims, q, k_cache, k_scale, v_cache, v_scale, block
     T = q.shape[0]
     if weights_out is None:
         weights_out = weights
-    dev = _device(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, weights, weights_out, out, lse, ws)
-    rows = _grouped_rows(q, T, dims.H, dims.d_qk, dims, "q")
-    _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
+    dev = _device(q, cu, weights, weights_out, out, lse)
+    row = _grouped_rows(q, T, dims.H, dims.d_qk, dims, "q")
+    rows = dims.num_blocks * dims.H_kv
+    at = _all_fit(((k_cache, _U8, 64 * rows * dims.d_qk), (k_scale, _F32, rows), (v_cache, _U8, 64 * rows * dims.d_v),
+                   (v_scale, _F32, rows), (block_table, _I32, dims.B * dims.max_blocks), (seq_lens, _I32, dims.B), (ws, _U8, 0)), dev)
+    if at is None or cu is not None or T != dims.B:
+        _device(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, ws)
+        _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
+        at = [_at(t) for t in (k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, ws)]
     for t, name in ((weights, "weights"), (weights_out, "weights_out")):
         if t is not None:
             _fp32(t, dims.B * dims.H_kv * dims.max_blocks * 64, name)
@@ -660,9 +687,8 @@ def grouped_attn(dims: GroupedDims, q, k_cache, k_scale, v_cache, v_scale, block
         lse = _empty((T, dims.H), torch.float32, q.device, stream)
     else:
         _fp32(lse, T * dims.H, "lse")
-    st = lib().dsa_grouped_attn(dims, *rows, _at(k_cache), _at(k_scale), _at(v_cache), _at(v_scale), _at(block_table),
-                                _at(seq_lens), _at(cu), T, sm_scale, _at(out), _at(lse), _at(weights), _at(weights_out),
-                                _at(ws), ws.numel(), _raw_stream(dev, stream))
+    st = lib().dsa_grouped_attn(dims, *row, at[0], at[1], at[2], at[3], at[4], at[5], _at(cu), T, sm_scale, _at(out), _at(lse),
+                                _at(weights), _at(weights_out), at[6], ws.numel(), _raw_stream(dev, stream))
     if st:
         _check("dsa_grouped_attn", st)
     increment_version((out, lse) if weights_out is None else (out, lse, weights_out))

@@ -20,8 +20,9 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 static_assert(kSelectWarps == 32, "a lane for every warp");
 constexpr int kSelectBins = 2048;
 constexpr int kSelectMaxCluster = 8;
-constexpr int kSelectKeys = 49152;  // keys that shared memory holds, beside the histograms
+constexpr int kSelectKeys = 40960;  // keys that shared memory holds, beside the histograms
 constexpr int kSelectBatch = 8;     // of a thread's, in flight
+constexpr int kSelectWords = 8;     // 32 positions each, that a warp marks at a time
 constexpr int kMoveThreads = 256;
 
 // Order of the weights as unsigned integers; NaN is the lowest, together with -infinity.
@@ -39,58 +40,189 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 
 struct SelectShared {
     uint32_t hist[3][kSelectBins];
-    uint32_t counts[2];             // of this CTA's run: kept above the last weight (or by place), equal to it
+    uint32_t slice[3][kSelectBins / 2];  // of every CTA's histogram, the bins that this CTA sums up
+    uint32_t slice_total[3];
+    uint32_t counts[2];  // of this CTA's run: kept above the last weight (or by place), equal to it
     uint32_t warp_counts[kSelectWarps][2];
     uint32_t warp_sums[kSelectWarps];
     uint32_t bin, need;
 };
 
-// The bin (from the top) that holds the `need`-th position of the cluster's histograms, and the rank within it.
-__device__ __forceinline__ void find_bin(SelectShared& S, int pass, int ctas, uint32_t need) {
-    constexpr int kPer = kSelectBins / kSelectThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int first = kSelectBins - kPer * (tid + 1);  // thread 0 has the top bins
-    uint32_t n[kPer] = {};
-    uint32_t theirs[kSelectMaxCluster][kPer];  // (all on their way at once)
-#pragma unroll
-    for (int c = 0; c < kSelectMaxCluster; ++c) {
-        const uint32_t at = mapa_shared(smem_u32(&S.hist[pass][first]), c < ctas ? c : 0);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) theirs[c][i] = c < ctas ? ld_cluster_u32(at + 4 * i) : 0;
-    }
-#pragma unroll
-    for (int c = 0; c < kSelectMaxCluster; ++c)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) n[i] += theirs[c][i];
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += n[i];
-    uint32_t x = mine;
+// Inclusive sums over the block's threads; `all` is their total.
+__device__ __forceinline__ uint32_t block_sums(SelectShared& S, uint32_t v, uint32_t* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
     }
+    __syncthreads();
     if (lane == 31) S.warp_sums[warp] = x;
     __syncthreads();
-    uint32_t before = x - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? S.warp_sums[lane] : 0);
-    if (before < need && need <= before + mine) {
+    const uint32_t w = S.warp_sums[lane];
+    *all = __reduce_add_sync(0xFFFFFFFFu, w);
+    return x + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
+}
+
+// The bin (from the top) that holds the `need`-th position of the cluster's histograms, and the rank within it. CTA r sums
+// up the r-th slice of the bins over all CTAs; then all read the slices' totals, and the bins of the one slice that matters.
+__device__ __forceinline__ void find_bin(SelectShared& S, int pass, int ctas, int rank, uint32_t need) {
+    const int tid = threadIdx.x, lane = tid & 31, width = kSelectBins / ctas;  // (256 at least)
+    // slice r: the bins down from kSelectBins - 1 - r * width
+    uint32_t mine = 0, all = 0;
+    if (ctas > 1) {
+        if (tid < width) {
+            const uint32_t at = smem_u32(&S.hist[pass][kSelectBins - 1 - rank * width - tid]);
+            uint32_t theirs[kSelectMaxCluster];  // (all on their way at once)
 #pragma unroll
-        for (int i = kPer - 1; i >= 0; --i) {
-            if (before < need && need <= before + n[i]) {
-                S.bin = first + i;
-                S.need = need - before;
-            }
-            before += n[i];
+            for (int c = 0; c < kSelectMaxCluster; ++c) theirs[c] = c < ctas ? ld_cluster_u32(mapa_shared(at, c)) : 0;
+#pragma unroll
+            for (int c = 0; c < kSelectMaxCluster; ++c) mine += theirs[c];
+            S.slice[pass][tid] = mine;
+        }
+        block_sums(S, mine, &all);
+        if (tid == 0) S.slice_total[pass] = all;
+        cluster_sync_all();
+        uint32_t t = lane < ctas ? ld_cluster_u32(mapa_shared(smem_u32(&S.slice_total[pass]), lane)) : 0, x = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, x >= need && x - t < need)) - 1;  // (there is one)
+        need -= __shfl_sync(0xFFFFFFFFu, x - t, from);
+        mine = tid < width ? ld_cluster_u32(mapa_shared(smem_u32(&S.slice[pass][tid]), from)) : 0;
+        const uint32_t sum = block_sums(S, mine, &all);
+        if (sum >= need && sum - mine < need) {
+            S.bin = kSelectBins - 1 - from * width - tid;
+            S.need = need - (sum - mine);
+        }
+    } else {  // two bins a thread
+        const int top = kSelectBins - 1 - 2 * tid;
+        const uint32_t n0 = S.hist[pass][top], n1 = S.hist[pass][top - 1];
+        const uint32_t sum = block_sums(S, n0 + n1, &all), before = sum - n0 - n1;
+        if (sum >= need && before < need) {
+            const bool first = before + n0 >= need;
+            S.bin = first ? top : top - 1;
+            S.need = need - before - (first ? 0 : n0);
         }
     }
     __syncthreads();
+}
+static_assert(kSelectBins == 2 * kSelectThreads, "two bins a thread");
+
+// One CTA's part of a row's selection. kCached: the keys of its run [r0, r1) fit shared memory.
+template <bool kCached>
+__device__ __forceinline__ void select_run(const GroupedEvictArgs& a, SelectShared& S, uint32_t* keys, const float* w, int32_t* kept, float* out,
+                                           int n, int r0, int r1, int ctas, int rank) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lo = a.sink, hi = n - a.recent;  // the positions to choose from
+    const uint32_t want = a.keep - a.sink - a.recent;
+    auto key_at = [&](int i) { return kCached ? keys[i - r0] : weight_key(w[i]); };
+    uint32_t prefix = 0xFFFFFFFFu, need = 0;  // above every key: with none wanted, positions are kept by their place alone
+    if (want > 0) {
+        for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) S.hist[0][i] = 0;
+        __syncthreads();
+        for (int i0 = r0 + tid; i0 < r1; i0 += kSelectBatch * kSelectThreads) {
+            float x[kSelectBatch];
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e) x[e] = i0 + e * kSelectThreads < r1 ? w[i0 + e * kSelectThreads] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kSelectBatch; ++e) {
+                const int i = i0 + e * kSelectThreads;
+                const uint32_t k = weight_key(x[e]);
+                if (kCached && i < r1) keys[i - r0] = k;
+                if (i >= lo && i < min(hi, r1)) atomicAdd(&S.hist[0][k >> 21], 1u);
+            }
+        }
+        if (ctas > 1) cluster_sync_all();
+        else __syncthreads();
+        find_bin(S, 0, ctas, rank, want);
+        prefix = S.bin, need = S.need;
+        // the next bits of the positions that agree so far
+        const int from = max(r0, lo), to = min(r1, hi);
+        auto next_pass = [&](int pass, int above, int shift, uint32_t mask) {
+            for (int i0 = from + tid; i0 < to; i0 += kSelectBatch * kSelectThreads) {
+                uint32_t k[kSelectBatch];
+#pragma unroll
+                for (int e = 0; e < kSelectBatch; ++e) k[e] = i0 + e * kSelectThreads < to ? key_at(i0 + e * kSelectThreads) : 0;
+#pragma unroll
+                for (int e = 0; e < kSelectBatch; ++e)
+                    if (i0 + e * kSelectThreads < to && k[e] >> above == prefix) atomicAdd(&S.hist[pass][(k[e] >> shift) & mask], 1u);
+            }
+            if (ctas > 1) cluster_sync_all();
+            else __syncthreads();
+            find_bin(S, pass, ctas, rank, need);
+        };
+        next_pass(1, 21, 10, 2047);
+        prefix = prefix << 11 | S.bin, need = S.need;
+        next_pass(2, 10, 0, 1023);
+        prefix = prefix << 10 | S.bin, need = S.need;  // the last kept weight's key; how many of its equals are kept
+    }
+    // every warp's part of the run: what it keeps, and what equals the last weight, as bits
+    const int part = ((r1 - r0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int p0 = min(r1, r0 + warp * part), p1 = min(r1, p0 + part);
+    uint32_t key[kSelectWords], keeps[kSelectWords], ties[kSelectWords];  // of kSelectWords times 32 positions
+    auto mark = [&](int i0) {
+        const bool inside = want > 0 && i0 >= lo && min(i0 + 32 * kSelectWords, p1) <= hi;  // (all by their weights)
+#pragma unroll
+        for (int e = 0; e < kSelectWords; ++e) {
+            const int i = i0 + 32 * e + lane;
+            key[e] = i < p1 && want > 0 ? key_at(i) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < kSelectWords; ++e) {
+            const int i = i0 + 32 * e + lane;
+            const bool held = !inside && (i < lo || i >= hi);
+            keeps[e] = __ballot_sync(0xFFFFFFFFu, i < p1 && (held || key[e] > prefix));
+            ties[e] = __ballot_sync(0xFFFFFFFFu, i < p1 && !held && key[e] == prefix);
+        }
+    };
+    uint32_t above = 0, equal = 0;
+    for (int i0 = p0; i0 < p1; i0 += 32 * kSelectWords) {
+        mark(i0);
+#pragma unroll
+        for (int e = 0; e < kSelectWords; ++e) above += __popc(keeps[e]), equal += __popc(ties[e]);
+    }
+    if (lane == 0) S.warp_counts[warp][0] = above, S.warp_counts[warp][1] = equal;
+    __syncthreads();
+    const uint32_t warp_above = S.warp_counts[lane][0], warp_equal = S.warp_counts[lane][1];
+    if (warp == 0) {
+        const uint32_t all_above = __reduce_add_sync(0xFFFFFFFFu, warp_above), all_equal = __reduce_add_sync(0xFFFFFFFFu, warp_equal);
+        if (lane == 0) S.counts[0] = all_above, S.counts[1] = all_equal;
+    }
+    uint32_t cta_above = 0, cta_equal = 0;
+    if (ctas > 1) {
+        cluster_sync_all();
+        const uint32_t at = mapa_shared(smem_u32(S.counts), lane < rank ? lane : 0);  // lane c: the counts of CTA c
+        cta_above = lane < rank ? ld_cluster_u32(at) : 0, cta_equal = lane < rank ? ld_cluster_u32(at + 4) : 0;
+    }
+    uint32_t above_before = __reduce_add_sync(0xFFFFFFFFu, cta_above + (lane < warp ? warp_above : 0));
+    uint32_t equal_before = __reduce_add_sync(0xFFFFFFFFu, cta_equal + (lane < warp ? warp_equal : 0));
+    const uint32_t below = (1u << lane) - 1;
+    for (int i0 = p0; i0 < p1; i0 += 32 * kSelectWords) {
+        if (part > 32 * kSelectWords) mark(i0);
+#pragma unroll
+        for (int e = 0; e < kSelectWords; ++e) {
+            const uint32_t t = equal_before + __popc(ties[e] & below);
+            if ((keeps[e] >> lane & 1) || ((ties[e] >> lane & 1) && t < need)) {
+                const uint32_t slot = above_before + __popc(keeps[e] & below) + min(t, need);
+                const int i = i0 + 32 * e + lane;
+                kept[slot] = i;
+                out[slot] = want > 0 && key[e] != kLowestKey ? key_weight(key[e]) : w[i];
+            }
+            above_before += __popc(keeps[e]);
+            equal_before += __popc(ties[e]);
+        }
+    }
+    if (ctas > 1) cluster_sync_all();  // no CTA's shared memory goes while another may read it
 }
 
 __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedEvictArgs a, int ctas, int cached) {
     extern __shared__ uint32_t keys[];  // [cached]
     __shared__ SelectShared S;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int bh = blockIdx.x / ctas, rank = blockIdx.x - bh * ctas, b = bh / a.H_kv;
     griddep_launch_dependents();
     int n = a.seq_lens[b];
@@ -112,95 +244,11 @@ __global__ void __launch_bounds__(kSelectThreads) grouped_select_kernel(GroupedE
         }
         return;
     }
-    // this CTA's run [r0, r1), each warp's a part of it in whole 32s
+    // this CTA's run [r0, r1)
     const int run = ((n + ctas - 1) / ctas + kSelectThreads - 1) / kSelectThreads * kSelectThreads;
     const int r0 = static_cast<int>(min(static_cast<int64_t>(n), static_cast<int64_t>(rank) * run)), r1 = min(n, r0 + run);
-    const int lo = a.sink, hi = n - a.recent;  // the positions to choose from
-    const uint32_t want = a.keep - a.sink - a.recent;
-    auto key_at = [&](int i) { return i - r0 < cached ? keys[i - r0] : weight_key(w[i]); };
-    uint32_t prefix = 0, need = want;
-    if (want > 0) {
-        for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) S.hist[0][i] = 0;
-        __syncthreads();
-        for (int i0 = r0 + tid; i0 < r1; i0 += kSelectBatch * kSelectThreads) {
-            float x[kSelectBatch];
-#pragma unroll
-            for (int e = 0; e < kSelectBatch; ++e) x[e] = i0 + e * kSelectThreads < r1 ? w[i0 + e * kSelectThreads] : 0.0f;
-#pragma unroll
-            for (int e = 0; e < kSelectBatch; ++e) {
-                const int i = i0 + e * kSelectThreads;
-                if (i >= r1) break;
-                const uint32_t k = weight_key(x[e]);
-                if (i - r0 < cached) keys[i - r0] = k;
-                if (i >= lo && i < hi) atomicAdd(&S.hist[0][k >> 21], 1u);
-            }
-        }
-        cluster_sync_all();
-        find_bin(S, 0, ctas, need);
-        prefix = S.bin, need = S.need;
-        // the next bits of the positions that agree so far
-        auto next_pass = [&](int pass, int above, int shift, uint32_t mask) {
-            for (int i0 = r0 + tid; i0 < r1; i0 += kSelectBatch * kSelectThreads) {
-                uint32_t k[kSelectBatch];
-#pragma unroll
-                for (int e = 0; e < kSelectBatch; ++e) k[e] = i0 + e * kSelectThreads < r1 ? key_at(i0 + e * kSelectThreads) : 0;
-#pragma unroll
-                for (int e = 0; e < kSelectBatch; ++e) {
-                    const int i = i0 + e * kSelectThreads;
-                    if (i < r1 && k[e] >> above == prefix && i >= lo && i < hi) atomicAdd(&S.hist[pass][(k[e] >> shift) & mask], 1u);
-                }
-            }
-            cluster_sync_all();
-            find_bin(S, pass, ctas, need);
-        };
-        next_pass(1, 21, 10, 2047);
-        prefix = prefix << 11 | S.bin, need = S.need;
-        next_pass(2, 10, 0, 1023);
-        prefix = prefix << 10 | S.bin, need = S.need;  // the last kept weight's key; how many of its equals are kept
-    } else {
-        prefix = 0xFFFFFFFFu;  // above every key: positions are kept by their place alone
-    }
-    // counts of the warps' parts, then of the CTAs' runs
-    const int part = ((r1 - r0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int p0 = min(r1, r0 + warp * part), p1 = min(r1, p0 + part);
-    uint32_t above = 0, equal = 0;
-#pragma unroll 4
-    for (int i0 = p0; i0 < p1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0;
-        const bool keep = i < p1 && (i < lo || i >= hi || k > prefix), tie = i < p1 && !keep && k == prefix;
-        above += __popc(__ballot_sync(0xFFFFFFFFu, keep));
-        equal += __popc(__ballot_sync(0xFFFFFFFFu, tie));
-    }
-    if (lane == 0) S.warp_counts[warp][0] = above, S.warp_counts[warp][1] = equal;
-    __syncthreads();
-    const uint32_t warp_above = S.warp_counts[lane][0], warp_equal = S.warp_counts[lane][1];
-    if (warp == 0) {
-        const uint32_t all_above = __reduce_add_sync(0xFFFFFFFFu, warp_above), all_equal = __reduce_add_sync(0xFFFFFFFFu, warp_equal);
-        if (lane == 0) S.counts[0] = all_above, S.counts[1] = all_equal;
-    }
-    cluster_sync_all();
-    // lane c: the counts of CTA c
-    const uint32_t at = mapa_shared(smem_u32(S.counts), lane < rank ? lane : 0);
-    const uint32_t cta_above = lane < rank ? ld_cluster_u32(at) : 0, cta_equal = lane < rank ? ld_cluster_u32(at + 4) : 0;
-    uint32_t above_before = __reduce_add_sync(0xFFFFFFFFu, cta_above + (lane < warp ? warp_above : 0));
-    uint32_t equal_before = __reduce_add_sync(0xFFFFFFFFu, cta_equal + (lane < warp ? warp_equal : 0));
-#pragma unroll 4
-    for (int i0 = p0; i0 < p1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < p1 && want > 0 ? key_at(i) : 0, below = (1u << lane) - 1;
-        const bool keep = i < p1 && (i < lo || i >= hi || k > prefix), tie = i < p1 && !keep && k == prefix;
-        const uint32_t keeps = __ballot_sync(0xFFFFFFFFu, keep), ties = __ballot_sync(0xFFFFFFFFu, tie);
-        const uint32_t t = equal_before + __popc(ties & below);
-        if (keep || (tie && t < need)) {
-            const uint32_t slot = above_before + __popc(keeps & below) + min(t, need);
-            kept[slot] = i;
-            out[slot] = want > 0 && k != kLowestKey ? key_weight(k) : w[i];
-        }
-        above_before += __popc(keeps);
-        equal_before += __popc(ties);
-    }
-    cluster_sync_all();  // no CTA's shared memory goes while another may read it
+    if (run <= cached) select_run<true>(a, S, keys, w, kept, out, n, r0, r1, ctas, rank);
+    else select_run<false>(a, S, keys, w, kept, out, n, r0, r1, ctas, rank);
 }
 
 // The largest of 16 codes' magnitudes: e4m3 values order as their 7 low bits.
