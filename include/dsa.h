@@ -378,7 +378,8 @@ typedef struct {
  *   max(old scale, a / 448)       if it did; when that is larger, the earlier codes become
  *                                 RNE_e4m3(code * old scale / scale)
  * and each new code RNE_e4m3(x / scale), saturating at +-448. Slots behind the new tokens stay as they were. A token
- * whose position is negative or whose block is invalid is skipped and reported. New values are finite.
+ * whose position is negative or whose block is invalid is skipped and reported. New values are finite; a block that
+ * receives tokens belongs to one sequence alone.
  * ws as for dsa_cache_append (only its error word is used).
  */
 dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, int64_t k_stride_t, int64_t k_stride_h,
@@ -397,6 +398,9 @@ dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, i
  *        the others stay as they were.
  * Positions in invalid blocks are left out and reported. What unused slots of a block hold does not matter, NaN codes
  * included. A query of NaN or infinities gives a row of NaN (and NaN weights); other inputs are finite. sm_scale > 0.
+ * DSA_BF16: queries enter the products exactly but for elements below 2^-13 of their row's largest (an absolute error of
+ * 2^-21 of that), softmax weights with 11 significant bits (and 2^-26 of their row's largest); DSA_F32: both with 24 bits.
+ * Sums keep fp32. The result of a call does not depend on timing.
  * ws: at least dsa_grouped_workspace_size(dims, T, weights wanted) bytes, 256-byte aligned, initialised with
  * dsa_workspace_init.
  */
@@ -507,7 +511,8 @@ dsa_status dsa_indexer_topk_noalloc(const dsa_dims* dims, const void* q_I, const
                                     int32_t* fault_word, dsa_stream_t stream);
 
 /* Synchronises `stream`, copies the device error word of `ws` to *fault_bits (may be NULL) and
- * clears it. Returns DSA_OK when no bit was set, DSA_ERR_TIMEOUT when DSA_FAULT_TIMEOUT was set,
+ * clears it (after a timeout with what else the first 256 bytes of the workspace hold: call it before the workspace is
+ * used again). Returns DSA_OK when no bit was set, DSA_ERR_TIMEOUT when DSA_FAULT_TIMEOUT was set,
  * DSA_ERR_DEVICE for any other bit, DSA_ERR_LAUNCH if the copy failed. */
 dsa_status dsa_read_error(void* ws, int32_t* fault_bits, dsa_stream_t stream);
 

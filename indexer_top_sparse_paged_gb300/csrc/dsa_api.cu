@@ -1188,7 +1188,8 @@ dsa_status dsa_read_error(void* ws, int32_t* fault_bits, dsa_stream_t stream) {
     int32_t v = 0;
     if (cudaStreamSynchronize(s) != cudaSuccess) return DSA_ERR_LAUNCH;
     if (cudaMemcpy(&v, ws, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_LAUNCH;
-    if (cudaMemset(ws, 0, sizeof v) != cudaSuccess) return DSA_ERR_LAUNCH;
+    // a call that gave up may have left arrivals behind the error word
+    if (cudaMemset(ws, 0, v & DSA_FAULT_TIMEOUT ? 256 : sizeof v) != cudaSuccess) return DSA_ERR_LAUNCH;
     if (fault_bits) *fault_bits = v;
     if (v & DSA_FAULT_TIMEOUT) return DSA_ERR_TIMEOUT;
     return v ? DSA_ERR_DEVICE : DSA_OK;

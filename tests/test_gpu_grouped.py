@@ -356,6 +356,75 @@ def test_a_larger_workspace_serves_smaller_calls():
             check(c, q, [m] * B, got, 0.1, None, w)
 
 
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("d_qk,d_v", [(128, 128), (192, 128), (64, 256), (256, 256), (16, 16)])
+@pytest.mark.parametrize("G,new", [(5, 2), (8, 2), (16, 2), (32, 2), (40, 5)])
+def test_rows_of_an_item_by_widths(type, d_qk, d_v, G, new):
+    """Every number of rows that share a tile, with every number of 128-column chunks; items that CTAs cut and whole ones."""
+    lens = [130, 3000]
+    c = Cache(lens, G, 1, d_qk, d_v, type, seed=G + d_qk)
+    q = c.queries(new + 1)
+    w = torch.zeros((2, 1, c.width * 64), device="cuda")
+    got = attend(c, q, [new, 1], d_qk ** -0.5, weights_out=w)
+    check(c, q, [new, 1], got, d_qk ** -0.5, None, w)
+
+
+def test_weights_of_many_sequences():
+    lens = [(i * 53) % 300 for i in range(300)]
+    c = Cache(lens, 6, 2, 16, 16, seed=14)
+    q = c.queries(300)
+    w = torch.rand((300, 2, c.width * 64), device="cuda")
+    base = w.clone()
+    check(c, q, [1] * 300, attend(c, q, [1] * 300, 0.25, weights=w), 0.25, base, w)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_logits_that_pass_the_maximum_by_a_little_and_by_much(type):
+    """Maxima that rise from tile to tile by less than the slack of the weights' reference, by about it, and by far more; rows
+    whose first tiles show them nothing (invalid blocks)."""
+    for rise in (0.5, 2.5, 4.0, 6.0, 40.0):
+        c = Cache([2100], 8, 1, 16, 16, type, seed=15)
+        c.k[c.table[0, :33].long()] = 0
+        c.k[c.table[0, :33].long(), 0, :, 0] = 0x38  # 1.0
+        for j in range(33):
+            c.ks[int(c.table[0, j])] = 0.01 + rise * (j // 2) * math.log(2.0)
+        c.table[0, 0:5] = -1
+        q = torch.zeros((1, 8, 16), dtype=ACT[type], device="cuda")
+        q[0, :, 0] = torch.linspace(0.125, 1.0, 8, device="cuda").to(ACT[type])
+        check(c, q, [1], attend(c, q, [1], 1.0, faults=1), 1.0)
+
+
+def test_a_read_timeout_clears_what_a_call_left():
+    c = Cache([700], 8, 2, 64, 64, seed=16)
+    q = c.queries(1)
+    ws = dsa.grouped_workspace(c.dims(), 1)
+    ref = dsa.grouped_attn(c.dims(), q, *c.args(), 0.125, ws=ws)
+    assert not ws[:256].any()  # arrivals are all taken back
+    ws[16:200] = 3
+    ws[:4] = torch.tensor([4, 0, 0, 0], dtype=torch.uint8)  # the timeout bit
+    assert dsa.read_error(ws) == 4 and not ws[:256].any()
+    got = dsa.grouped_attn(c.dims(), q, *c.args(), 0.125, ws=ws)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_one_workspace_for_the_librarys_calls():
+    """A workspace that other calls of the library have written into serves this one."""
+    c = Cache([9000, 300], 16, 2, 64, 64, seed=17)
+    q = c.queries(2)
+    p = torch.randn((300, 16, 64), device="cuda").bfloat16()
+    kv = torch.randn((300, 2, 64), device="cuda").bfloat16()
+    pd = dsa.prompt_dims(p, kv, kv, 1)
+    n = max(dsa.grouped_workspace(c.dims(), 2).numel(), dsa.prompt_workspace(pd, 300).numel())
+    ws = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = ws[-ws.data_ptr() % 256:][:n]
+    ws[:256] = 0
+    ref = attend(c, q, [1, 1], 0.125)
+    for _ in range(3):
+        dsa.prompt_attn(pd, p, kv, kv, starts([300]), starts([300]), 0.125, ws=ws)
+        got = dsa.grouped_attn(c.dims(), q, *c.args(), 0.125, ws=ws)
+        assert dsa.read_error(ws) == 0 and torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 # ------------------------------------------------------------------------------------------------ append
 
 def expected_append(codes, scale, table, x, first):
