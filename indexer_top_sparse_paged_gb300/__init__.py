@@ -647,7 +647,7 @@ def grouped_append(dims: GroupedDims, k_new, v_new, block_table, seq_lens, k_cac
     rows = dims.num_blocks * dims.H_kv
     at = _all_fit(((block_table, _I32, dims.B * dims.max_blocks), (seq_lens, _I32, dims.B), (k_cache, _U8, 64 * rows * dims.d_qk),
                    (k_scale, _F32, rows), (v_cache, _U8, 64 * rows * dims.d_v), (v_scale, _F32, rows), (ws, _U8, 0)), dev)
-    if at is None or cu is not None or T != dims.B:
+    if at is None or (T != dims.B if cu is None else cu.dtype is not _I32 or cu.numel() <= dims.B):
         _device(k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu, ws)
         _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
         at = [_at(t) for t in (block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, ws)]
@@ -672,7 +672,7 @@ def grouped_attn(dims: GroupedDims, q, k_cache, k_scale, v_cache, v_scale, block
     rows = dims.num_blocks * dims.H_kv
     at = _all_fit(((k_cache, _U8, 64 * rows * dims.d_qk), (k_scale, _F32, rows), (v_cache, _U8, 64 * rows * dims.d_v),
                    (v_scale, _F32, rows), (block_table, _I32, dims.B * dims.max_blocks), (seq_lens, _I32, dims.B), (ws, _U8, 0)), dev)
-    if at is None or cu is not None or T != dims.B:
+    if at is None or (T != dims.B if cu is None else cu.dtype is not _I32 or cu.numel() <= dims.B):
         _device(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, ws)
         _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
         at = [_at(t) for t in (k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, ws)]

@@ -97,6 +97,18 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
     if (!a.cu) {
         b = blockIdx.x, base = b;  // one row, one block for each
         if (append_seq(a, b, blockIdx.y == 0 && tid == 0).blocks == 0) return;
+    } else if (a.B <= 32) {  // every warp finds it for itself
+        const int lane = tid & 31, blocks = lane < a.B ? append_seq(a, lane, report && tid < 32).blocks : 0;
+        int x = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        const int at = blockIdx.x;
+        b = __ffs(__ballot_sync(0xFFFFFFFFu, at >= x - blocks && at < x)) - 1;
+        if (b < 0) return;
+        base = __shfl_sync(0xFFFFFFFFu, x - blocks, b);
     } else {
         find_place<kGroupedAppendThreads>(a.B, [&](int i) { return static_cast<int64_t>(append_seq(a, i, report).blocks); },
                                           [](int64_t) { return static_cast<int64_t>(blockIdx.x); }, &total, &b, &base, warp_sums, found);
@@ -111,29 +123,38 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
         return;
     }
     const int slot0 = p0 - lb * kBlock;
-    // its heads, keys and values in turn
-    for (int y = blockIdx.y, turn = 0; y < 2 * a.H_kv; y += gridDim.y, turn ^= 1) {
-        const int h = y >> 1;
+    // its heads, keys and values in turn, the next one's rows on their way while this one's are written
+    Elements16<T> next[kPieces];
+    float next_old = 0.0f;
+    auto load = [&](int y) {
+        if (y >= 2 * a.H_kv) return;
         const bool value = y & 1;
-        const int d = value ? a.d_v : a.d_qk, groups = d / 16, n = (p1 - p0) * groups;
-        const uint32_t magic = value ? v_magic : k_magic;
+        const int groups = (value ? a.d_v : a.d_qk) / 16, n = (p1 - p0) * groups;
         const int64_t st = value ? a.v_stride_t : a.k_stride_t, sh = value ? a.v_stride_h : a.k_stride_h;
-        const T* x = static_cast<const T*>(value ? a.v_new : a.k_new) + (s.row0 + s.skipped + p0 - s.first) * st + h * sh;
-        const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + h;
-        uint4* codes = reinterpret_cast<uint4*>((value ? a.v : a.k) + bh * kBlock * d);
-        float* scale_at = (value ? a.v_scale : a.k_scale) + bh;
-        const float old = slot0 ? *scale_at : 0.0f;
-        Elements16<T> piece[kPieces];
-        uint32_t top = 0;
+        const T* x = static_cast<const T*>(value ? a.v_new : a.k_new) + (s.row0 + s.skipped + p0 - s.first) * st + (y >> 1) * sh;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int i = tid + p * kGroupedAppendThreads;
-            const int r = groups == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
-            if (i < n) piece[p].load(x + r * st + (i - r * groups) * 16);
+            const int r = groups == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), value ? v_magic : k_magic));
+            if (i < n) next[p].load(x + r * st + (i - r * groups) * 16);
         }
+        next_old = slot0 ? (value ? a.v_scale : a.k_scale)[static_cast<int64_t>(blk) * a.H_kv + (y >> 1)] : 0.0f;
+    };
+    load(blockIdx.y);
+    for (int y = blockIdx.y, turn = 0; y < 2 * a.H_kv; y += gridDim.y, turn ^= 1) {
+        const bool value = y & 1;
+        const int d = value ? a.d_v : a.d_qk, groups = d / 16, n = (p1 - p0) * groups;
+        const int64_t bh = static_cast<int64_t>(blk) * a.H_kv + (y >> 1);
+        uint4* codes = reinterpret_cast<uint4*>((value ? a.v : a.k) + bh * kBlock * d);
+        Elements16<T> piece[kPieces];
+        const float old = next_old;
+        uint32_t top = 0;
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p)
+        for (int p = 0; p < kPieces; ++p) {
+            piece[p] = next[p];
             if (tid + p * kGroupedAppendThreads < n) top = max(top, piece[p].top());
+        }
+        load(y + gridDim.y);
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         if ((tid & 31) == 0) red[turn][tid >> 5] = __uint_as_float(top);
         __syncthreads();
@@ -152,7 +173,7 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
         if (slot0 && scale > old) {
             for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) codes[i] = requantise16(codes[i], old, scale);
         }
-        if (tid == 0) *scale_at = scale;
+        if (tid == 0) (value ? a.v_scale : a.k_scale)[bh] = scale;
     }
 }
 
@@ -160,9 +181,9 @@ template <typename T>
 static bool launch_typed(const GroupedAppendArgs& a, cudaStream_t s) {
     // a sequence's rows reach into (n + 126) / 64 blocks at most, and into n
     const int64_t most = static_cast<int64_t>(a.T) / kBlock + 2ll * a.B, units = most < a.T ? most : a.T;
-    // two turns of eight CTAs an SM, or a CTA for every head's keys and values
-    int64_t heads = (16ll * device_sm_count() + units - 1) / units;
-    if (heads > 2 * a.H_kv) heads = 2 * a.H_kv;
+    // one turn of six CTAs an SM, each with the same number of heads' keys and values, or a CTA for every one
+    const int64_t turns = (2ll * a.H_kv * units + 6 * device_sm_count() - 1) / (6 * device_sm_count());
+    const int64_t heads = (2 * a.H_kv + turns - 1) / turns;
     const int most_groups = (a.d_qk > a.d_v ? a.d_qk : a.d_v) / 16;
     const uint32_t gk = a.d_qk / 16, gv = a.d_v / 16;
     // umulhi(i, ceil(2^32 / groups)) = i / groups for i < 2^32 / groups
