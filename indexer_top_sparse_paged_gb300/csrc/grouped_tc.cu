@@ -94,6 +94,8 @@ struct Form {
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kQBytes = kSN * 128;   // one 128-column chunk of the split queries
     static constexpr int kPBytes = kPN * 128;   // the split weights of a tile
+    // Buffers of weights: the logits of a tile are there only when the products that read its buffer last have ended.
+    static constexpr int kPB = kSets == 2 ? 4 : 2;
     static_assert(kSN % 16 == 0 && kSN <= 256 && kPN <= 256 && kCols <= 512, "shapes of the products");
 };
 
@@ -101,7 +103,7 @@ template <typename F>
 struct Ctl {
     // barriers, with their arrivals in barrier_count
     uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[2], mma_done;
-    uint64_t q_full[2], met[F::kSets * F::kGroups], p_full[2], o_free, left[2], q_first, fin, q_empty[2];
+    uint64_t q_full[2], p_full[2], o_free, left[2], q_first, fin, q_empty[2];
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
@@ -109,6 +111,7 @@ struct Ctl {
     alignas(16) int row_at[2][F::kRows];      // token * H + head
     alignas(16) float red[F::kSets * F::kGroups][F::kRW][4];  // maxima of a tile's rows, by warp
     alignas(16) uint32_t flag[2][F::kSets * F::kGroups][4];   // a warp's word on whether they must move
+    int go[2][F::kSets * F::kGroups];         // whether the waits of a group's first warp ended well
     alignas(16) float2 fm[F::kSoftWarps][F::kRW];  // each warp's own: a row's factor, minus what its weights refer to
     alignas(16) float fac[F::kSoftWarps][F::kRW];  // and what its sums are to be multiplied by
     alignas(16) float fin_l[2][F::kSets][F::kRows][4], fin_m[2][F::kSets][F::kRows];  // a set's share of an item
@@ -123,11 +126,10 @@ struct Ctl {
 
 template <typename F>
 __device__ __forceinline__ int barrier_count(int i) {
-    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kMet = kOnes + 2, kSet = kMet + F::kSets * F::kGroups, kSoft = kSet + 5, kLast = kSoft + 2;
+    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kSet = kOnes + 2, kSoft = kSet + 5, kLast = kSoft + 2;
     static_assert(offsetof(Ctl<F>, q_empty) == kLast * 8, "barriers in order");
     if (i < kOnes) return 1;
-    if (i < kMet) return F::kQWarps;
-    if (i < kSet) return 4;                 // a group's warps
+    if (i < kSet) return F::kQWarps;
     if (i < kSoft) return F::kSetWarps;     // p_full, o_free, left
     return i < kLast ? F::kSoftWarps : 1 + F::kSoftWarps;  // q_empty: the products that read it, too
 }
@@ -138,13 +140,13 @@ struct Layout {  // byte offsets; kc, vc: chunks of 128 columns of keys and valu
     size_t stage, ring, q, p, ctl, total;
     __host__ __device__ Layout(int kc, int vc) {
         stage = static_cast<size_t>(2) * (kc + vc) * kChunk;
-        const size_t rest = 2 * (static_cast<size_t>(kc) * F::kQBytes + F::kPBytes) + sizeof(Ctl<F>) + 1024;
+        const size_t rest = 2 * static_cast<size_t>(kc) * F::kQBytes + F::kPB * F::kPBytes + sizeof(Ctl<F>) + 1024;
         stages = static_cast<int>((kSmemLimit - rest) / stage);
         if (stages > kMaxStages) stages = kMaxStages;
         ring = 0;
         q = ring + stages * stage;
         p = q + 2 * static_cast<size_t>(kc) * F::kQBytes;
-        ctl = p + 2 * static_cast<size_t>(F::kPBytes);
+        ctl = p + F::kPB * static_cast<size_t>(F::kPBytes);
         total = ctl + sizeof(Ctl<F>) + 1024;
     }
 };
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const bool fresh = (first >> (done & 31)) & 1;
             for (int c = 0; c < vc; ++c) {
                 const uint64_t da = sw128_desc(sRing + st_v * stage_bytes + v_off + 2 * c * kChunk, 0, 1024);
-                const uint64_t db = plain_desc(sP + j * F::kPBytes, 128, 2048);
+                const uint64_t db = plain_desc(sP + (done & (F::kPB - 1)) * F::kPBytes, 128, 2048);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     warp_mma_f8(tmem + F::kColO + (set * F::kVCMax + c) * F::kPN, da + k * (4096 >> 4), db + k * (512 >> 4),
@@ -668,14 +670,22 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         const uint32_t o_col = lane_base + F::kColO + group * F::kPP * kRW;
         float2* fm = S.fm[warp];
         float* fac = S.fac[warp];
-        int n = set, n_item = 0, st = set, sphase = 0, item = 0, met = 0, turn = 0, left = 0;  // n: this set's next tile, n_item: the item's first
+        const int mates = set * kGroups + group;
+        int n = set, n_item = 0, st = set, sphase = 0, item = 0, turn = 0, left = 0, asked = 0;  // n: this set's next tile, n_item: the item's first
         bool ok = true;
-        // The group's four warps meet (a barrier whose wait gives up, as every other).
-        auto group_sync = [&]() {
+        // The group's four warps meet at a barrier of the hardware, at which they sleep (asking a barrier in memory again and
+        // again, four warps slow each other: 2 rows a token 108 us, so 92). Only the first warp waits for other roles, with
+        // its limit; the others take its word, so that all of them go on or none does.
+        auto group_sync = [&]() { named_bar_sync(1 + mates, 128); };
+        auto group_ask = [&](auto wait) {
+            if (quarter == 0) {
+                const bool came = __all_sync(0xFFFFFFFFu, wait());
+                if (lane == 0) S.go[asked][mates] = came;
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&S.met[set * kGroups + group]));
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[set * kGroups + group]), met, abort_flag, a.err));
-            met ^= 1;
+            group_sync();
+            ok = S.go[asked][mates];
+            asked ^= 1;
         };
         if (next_piece(a, w, p)) {
             split_queries<T, F>(a, w.s, p, S, 0, sQ, kc, warp, F::kSoftWarps);
@@ -683,10 +693,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         }
         for (;; ++item) {
             const int qb = item & 1;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
+            group_ask([&]() {
+                return mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err) &&
+                       (item || !S.item[0].tiles || mbar_wait(smem_u32(&S.q_first), 0, abort_flag, a.err));
+            });
             const Item& it = S.item[qb];
             if (!ok || !it.tiles) break;
-            ok = __all_sync(0xFFFFFFFFu, item || mbar_wait(smem_u32(&S.q_first), 0, abort_flag, a.err));
             const int n_end = n_item + it.tiles, len = it.len, all_see = it.all_see;
             float l[kRW], v_ref = 0x1p-100f;
             float m = -INFINITY;  // what the weights of row lane % kRW refer to: its maximum so far, or up to kSlack less
@@ -696,17 +708,15 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const int* seen = S.seen[qb] + group * kRW;
             // the item before this has left O^T and the sets' shares
             bool waited = kSets == 1 || item == 0;
-            auto wait_free = [&]() {
-                if (waited) return;
-                waited = true;
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.o_free), (item - 1) & 1, abort_flag, a.err));
-            };
+            auto o_left = [&]() { return waited || mbar_wait(smem_u32(&S.o_free), (item - 1) & 1, abort_flag, a.err); };
             const bool any = n < n_end;
             bool fresh = true;
             for (; ok && n < n_end; n += kSets) {
                 const int tile = it.tile0 + n - n_item;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), sphase, abort_flag, a.err) &&
-                                                 mbar_wait(smem_u32(&S.s_full[n & (F::kSB - 1)]), (n / F::kSB) & 1, abort_flag, a.err));
+                group_ask([&]() {
+                    return mbar_wait(smem_u32(&S.full[st]), sphase, abort_flag, a.err) &&
+                           mbar_wait(smem_u32(&S.s_full[n & (F::kSB - 1)]), (n / F::kSB) & 1, abort_flag, a.err);
+                });
                 if (!ok) break;
                 tc_fence_after();
                 const float4 sc = S.scales[st];
@@ -722,15 +732,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 }
                 const float ks = !here ? 1.0f : quarter < 2 ? sc.x : sc.y;
                 const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
-                uint32_t* flag = S.flag[turn][set * kGroups + group];
+                uint32_t* flag = S.flag[turn][mates];
                 // The weights are formed against the maxima as they stand. Where a logit passes one by more than kSlack, in
                 // any of the group's warps, they are moved up first and the weights formed again.
                 bool move = fresh || v_top > v_ref, sure = false;
-                // (waited for as late as may be: this set's last weights have been read, and O^T is its own)
-                auto wait_values = [&]() {
-                    if (n >= 2) ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[n & 1]), ((n - 2) >> 1) & 1, abort_flag, a.err));
-                    if (fresh) wait_free();
-                };
                 for (;;) {
                     float s[kRW];
                     load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, ks, s);
@@ -747,10 +752,14 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             const float x = warp_max(s[r]);
                             if (lane == r) top = x;
                         }
-                        if (lane < kRW) S.red[set * kGroups + group][lane][quarter] = top * f_lane;
-                        group_sync();
+                        if (lane < kRW) S.red[mates][lane][quarter] = top * f_lane;
+                        group_ask([&]() {  // O^T is this set's own, and the products into it have ended
+                            constexpr int kBack = kSets == 2 ? 2 : 1;
+                            return fresh ? o_left() : mbar_wait(smem_u32(&S.pv_done[(n - kBack) & 1]), ((n - kBack) >> 1) & 1, abort_flag, a.err);
+                        });
                         if (!ok) break;
-                        const float4 t = *reinterpret_cast<const float4*>(S.red[set * kGroups + group][lane % kRW]);
+                        if (fresh) waited = true;
+                        const float4 t = *reinterpret_cast<const float4*>(S.red[mates][lane % kRW]);
                         const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
                         // the weights carry their block's value scale, against a power of two no smaller than any so far
                         float v_fac = 1.0f;
@@ -767,9 +776,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         if (!fresh) {
 #pragma unroll
                             for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
-                            wait_values();
-                            if (kSets == 1) ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.pv_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, abort_flag, a.err));
-                            if (!ok) break;
                             tc_fence_after();
                             for (int c = 0; c < vc; ++c) {
 #pragma unroll 1
@@ -785,7 +791,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             tmem_st_wait();
                         }
                         group_sync();  // the maxima have been read
-                        if (!ok) break;
                     }
                     if (a.weights_out && it.t + n - n_item < a.max_tiles) {
                         float* to = a.z + ((it.t + n - n_item) * kRows + group * kRW) * kGroupedTile + j;
@@ -803,20 +808,18 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     }
                     if (!sure) {  // the others' word is waited for when the weights are done
                         const bool up = __any_sync(0xFFFFFFFFu, over > kSlack);
-                        if (lane == 0) {
-                            flag[quarter] = up;
-                            mbar_arrive(smem_u32(&S.met[set * kGroups + group]));
-                        }
+                        if (lane == 0) flag[quarter] = up;
+                        __syncwarp();
+                        asm volatile("barrier.arrive %0, 256;" ::"r"(1 + kSets * kGroups + mates) : "memory");
                     }
-                    wait_values();
-                    if (!ok) break;
                     const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (kTop / v_ref) : 0.0f;
-                    const uint32_t p_buf = sP + (n & 1) * F::kPBytes + j * 16;
+                    const uint32_t p_buf = sP + (n & (F::kPB - 1)) * F::kPBytes + j * 16;
+                    constexpr int kRun = kRW < 16 ? 8 : 16;  // rows whose codes stand side by side
 #pragma unroll
-                    for (int r0 = 0; r0 < kRW; r0 += 8) {
-                        uint32_t parts[4][F::kPP];
+                    for (int r0 = 0; r0 < kRW; r0 += kRun) {
+                        uint32_t parts[kRun / 2][F::kPP];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kRun / 2; ++i) {
                             const int r = r0 + 2 * i;
                             s[r] = ex2(s[r]);
                             s[r + 1] = ex2(s[r + 1]);
@@ -825,15 +828,20 @@ __global__ void __launch_bounds__(F::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < F::kPP; ++i) {
                             const int col = group * F::kPP * kRW + i * kRW + r0;
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_buf + (col >> 4) * 2048 + (col & 8)),
-                                         "r"(parts[0][i] | parts[1][i] << 16), "r"(parts[2][i] | parts[3][i] << 16)
-                                         : "memory");
+                            const uint32_t at = p_buf + (col >> 4) * 2048 + (col & 8);
+                            if constexpr (kRun == 8)
+                                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
+                                             "r"(parts[2][i] | parts[3][i] << 16)
+                                             : "memory");
+                            else
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(parts[0][i] | parts[1][i] << 16),
+                                             "r"(parts[2][i] | parts[3][i] << 16), "r"(parts[kRun / 2 - 4][i] | parts[kRun / 2 - 3][i] << 16),
+                                             "r"(parts[kRun / 2 - 2][i] | parts[kRun / 2 - 1][i] << 16)
+                                             : "memory");
                         }
                     }
                     if (!sure) {
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.met[set * kGroups + group]), met, abort_flag, a.err));
-                        met ^= 1;
-                        if (!ok) break;
+                        named_bar_sync(1 + kSets * kGroups + mates, 256);  // (its other 128 arrivals were those above)
                         const uint4 u = *reinterpret_cast<const uint4*>(flag);
                         if (u.x | u.y | u.z | u.w) {
                             move = true;
@@ -855,7 +863,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (st >= stages) st -= stages, sphase ^= 1;
             }
             if (!ok) break;
-            wait_free();
+            if (!waited) group_ask(o_left);
+            if (!ok) break;
             // the item's end: this set's share of it
             const float sum = sum_rows<kRW>(l, lane);
             if (lane < kRW) {
@@ -868,8 +877,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const bool complete = it.complete;
             if (kSets == 1 || ((n_end - 1) & 1) == set) {
                 // the last tile was this set's: the rows, or their partial
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
-                                                       mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & 1]), ((n_end - 1) >> 1) & 1, abort_flag, a.err));
+                group_ask([&]() {
+                    return mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
+                           mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & 1]), ((n_end - 1) >> 1) & 1, abort_flag, a.err);
+                });
                 if (!ok) break;
                 tc_fence_after();
                 // lane r: row r's maximum and sum over both sets, and what each set's O^T is to be multiplied by
@@ -927,12 +938,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.left[0]));
                     if (warp == set * F::kSetWarps) {
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[0]), left, abort_flag, a.err));
+                        const bool came = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[0]), left, abort_flag, a.err));
                         if (lane == 0) {
                             __threadfence();
                             const int shift = 8 * (it.c0 & 3), parts = it.parts;
-                            const uint32_t old = ok ? atomicAdd(a.arrived + (it.c0 >> 2), 1u << shift) : 0;
-                            const bool last = ok && static_cast<int>((old >> shift) & 255u) == parts - 1;
+                            const uint32_t old = came ? atomicAdd(a.arrived + (it.c0 >> 2), 1u << shift) : 0;
+                            const bool last = came && static_cast<int>((old >> shift) & 255u) == parts - 1;
                             if (last) atomicSub(a.arrived + (it.c0 >> 2), static_cast<uint32_t>(parts) << shift);  // for the next call
                             __threadfence();
                             S.last_part = last;
@@ -940,7 +951,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         __syncwarp();
                     }
                     if (lane == 0) mbar_arrive(smem_u32(&S.left[1]));
-                    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.left[1]), left, abort_flag, a.err));
+                    group_ask([&]() { return mbar_wait(smem_u32(&S.left[1]), left, abort_flag, a.err); });
                     if (!ok) break;
                     if (S.last_part)
                         grouped_join<T, kRows < 32 ? 2 : 4, kRows < 32 ? 4 : 2>(a, S.row_at[qb], it.rows, it.join_slot, it.parts,
