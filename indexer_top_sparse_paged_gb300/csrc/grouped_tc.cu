@@ -94,7 +94,9 @@ struct Form {
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kQBytes = kSN * 128;   // one 128-column chunk of the split queries
     static constexpr int kPBytes = kPN * 128;   // the split weights of a tile
-    // Buffers of weights: the logits of a tile are there only when the products that read its buffer last have ended.
+    // Buffers of weights, each with its barrier. The logits of tile n are there only when the values' products of the tile
+    // that had its buffer before have ended: n - 4 of two sets (their products are issued before those of the keys of
+    // n - 1), n - 2 of one. With fewer, a set could fill a buffer again before the last filling had been noticed.
     static constexpr int kPB = kSets == 2 ? 4 : 2;
     static_assert(kSN % 16 == 0 && kSN <= 256 && kPN <= 256 && kCols <= 512, "shapes of the products");
 };
@@ -103,7 +105,7 @@ template <typename F>
 struct Ctl {
     // barriers, with their arrivals in barrier_count
     uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[2], mma_done;
-    uint64_t q_full[2], p_full[2], o_free, left[2], q_first, fin, q_empty[2];
+    uint64_t q_full[2], p_full[F::kPB], o_free, left[2], q_first, fin, q_empty[2];
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
@@ -126,7 +128,7 @@ struct Ctl {
 
 template <typename F>
 __device__ __forceinline__ int barrier_count(int i) {
-    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kSet = kOnes + 2, kSoft = kSet + 5, kLast = kSoft + 2;
+    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kSet = kOnes + 2, kSoft = kSet + F::kPB + 3, kLast = kSoft + 2;
     static_assert(offsetof(Ctl<F>, q_empty) == kLast * 8, "barriers in order");
     if (i < kOnes) return 1;
     if (i < kSet) return F::kQWarps;
@@ -555,14 +557,14 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         bool ok = true;
         const int ksteps = (a.d_qk + 31) / 32;
         auto values = [&]() {  // V^T P^T of tile `done`
-            const int j = done & 1, set = kSets == 2 ? j : 0;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[j]), (done >> 1) & 1, abort_flag, a.err));
+            const int j = done & 1, set = kSets == 2 ? j : 0, buf = done & (F::kPB - 1);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[buf]), (done / F::kPB) & 1, abort_flag, a.err));
             if (!ok) return;
             tc_fence_after();
             const bool fresh = (first >> (done & 31)) & 1;
             for (int c = 0; c < vc; ++c) {
                 const uint64_t da = sw128_desc(sRing + st_v * stage_bytes + v_off + 2 * c * kChunk, 0, 1024);
-                const uint64_t db = plain_desc(sP + (done & (F::kPB - 1)) * F::kPBytes, 128, 2048);
+                const uint64_t db = plain_desc(sP + buf * F::kPBytes, 128, 2048);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     warp_mma_f8(tmem + F::kColO + (set * F::kVCMax + c) * F::kPN, da + k * (4096 >> 4), db + k * (512 >> 4),
@@ -573,18 +575,39 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             if (++st_v == stages) st_v = 0;
             ++done;
         };
+        // Waits until the values of the tiles before `least` have been issued and the barrier's phase has ended, and issues
+        // the values of any tile whose weights come meanwhile: an item's last would otherwise stand back until the next
+        // item's first tiles have landed, and O^T with them.
+        auto await = [&](int least, uint32_t bar, uint32_t parity) {
+            long long t0 = clock64();
+            while (ok && (done < least || !__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))) {
+                if (done == n) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, a.err));
+                } else if (__all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[done & (F::kPB - 1)]), (done / F::kPB) & 1))) {
+                    values();
+                    t0 = clock64();
+                } else {
+                    const bool late = clock64() - t0 > kWaitCycles;
+                    if (late) {
+                        *abort_flag = 1;
+                        atomicOr(a.err, DSA_FAULT_TIMEOUT);
+                    }
+                    ok = __all_sync(0xFFFFFFFFu, !late && !*abort_flag);
+                }
+            }
+        };
         for (;; ++item) {
             const int qb = item & 1;
-            while (ok && done < last) values();  // the item before that one must end for this one's queries to come
+            // (the item before the last must end for this one's queries to come)
+            await(last, smem_u32(&S.q_full[qb]), (item >> 1) & 1);
             last = n;
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.q_full[qb]), (item >> 1) & 1, abort_flag, a.err));
             const int tiles = ok ? S.item[qb].tiles : 0;
             if (!tiles) break;
             ok = __all_sync(0xFFFFFFFFu, item || mbar_wait(smem_u32(&S.q_first), 0, abort_flag, a.err));
             if (!ok) break;
             for (int tile = 0; tile < tiles; ++tile) {
-                // this buffer of logits is free: V^T P^T of tile n - kSB has been issued, after its weights came
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.full[st]), phase, abort_flag, a.err));
+                // this buffer of logits is free then: V^T P^T of tile n - kSB has been issued, after its weights came
+                await(n - lead, smem_u32(&S.full[st]), phase);
                 if (!ok) break;
                 tc_fence_after();
                 for (int k = 0; k < ksteps; ++k) {
@@ -598,8 +621,6 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 first = tile < kSets ? first | bit : first & ~bit;
                 ++n;
                 if (++st == stages) st = 0, phase ^= 1;
-                if (n - done > lead) values();
-                if (!ok) break;
             }
         }
         while (ok && done < n) values();
@@ -858,7 +879,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&S.p_full[n & 1]));
+                if (lane == 0) mbar_arrive(smem_u32(&S.p_full[n & (F::kPB - 1)]));
                 st += kSets;
                 if (st >= stages) st -= stages, sphase ^= 1;
             }
