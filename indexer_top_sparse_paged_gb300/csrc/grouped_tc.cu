@@ -94,9 +94,10 @@ struct Form {
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kQBytes = kSN * 128;   // one 128-column chunk of the split queries
     static constexpr int kPBytes = kPN * 128;   // the split weights of a tile
-    // Buffers of weights, each with its barrier. The logits of tile n are there only when the values' products of the tile
-    // that had its buffer before have ended: n - 4 of two sets (their products are issued before those of the keys of
-    // n - 1), n - 2 of one. With fewer, a set could fill a buffer again before the last filling had been noticed.
+    // Buffers of weights, and barriers for their coming and for the end of the products that read them. Before the keys'
+    // products of tile n the values' are issued of all before n - kSB / 2 (tile n - 3 and before of two sets, n - 2 of one),
+    // so that whoever has the logits of n knows that the phase before n's, tile n - kPB's, has ended on each of these
+    // barriers. With two barriers for two sets, n - 2 might not have: the wait for n could take the phase before for its own.
     static constexpr int kPB = kSets == 2 ? 4 : 2;
     static_assert(kSN % 16 == 0 && kSN <= 256 && kPN <= 256 && kCols <= 512, "shapes of the products");
 };
@@ -104,7 +105,7 @@ struct Form {
 template <typename F>
 struct Ctl {
     // barriers, with their arrivals in barrier_count
-    uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[2], mma_done;
+    uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[F::kPB], mma_done;
     uint64_t q_full[2], p_full[F::kPB], o_free, left[2], q_first, fin, q_empty[2];
     float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
     int valid[kMaxStages];                    // bits 0, 1: the blocks are there
@@ -128,7 +129,7 @@ struct Ctl {
 
 template <typename F>
 __device__ __forceinline__ int barrier_count(int i) {
-    constexpr int kOnes = 2 * kMaxStages + F::kSB + 3, kSet = kOnes + 2, kSoft = kSet + F::kPB + 3, kLast = kSoft + 2;
+    constexpr int kOnes = 2 * kMaxStages + F::kSB + F::kPB + 1, kSet = kOnes + 2, kSoft = kSet + F::kPB + 3, kLast = kSoft + 2;
     static_assert(offsetof(Ctl<F>, q_empty) == kLast * 8, "barriers in order");
     if (i < kOnes) return 1;
     if (i < kSet) return F::kQWarps;
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         bool ok = true;
         const int ksteps = (a.d_qk + 31) / 32;
         auto values = [&]() {  // V^T P^T of tile `done`
-            const int j = done & 1, set = kSets == 2 ? j : 0, buf = done & (F::kPB - 1);
+            const int set = kSets == 2 ? done & 1 : 0, buf = done & (F::kPB - 1);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[buf]), (done / F::kPB) & 1, abort_flag, a.err));
             if (!ok) return;
             tc_fence_after();
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                                 idesc_f8(F::kPN, 1u, 1u), fresh && k == 0 ? 0u : 1u);
             }
             warp_tc_commit(smem_u32(&S.empty[st_v]));
-            warp_tc_commit(smem_u32(&S.pv_done[j]));
+            warp_tc_commit(smem_u32(&S.pv_done[buf]));
             if (++st_v == stages) st_v = 0;
             ++done;
         };
@@ -776,7 +777,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         if (lane < kRW) S.red[mates][lane][quarter] = top * f_lane;
                         group_ask([&]() {  // O^T is this set's own, and the products into it have ended
                             constexpr int kBack = kSets == 2 ? 2 : 1;
-                            return fresh ? o_left() : mbar_wait(smem_u32(&S.pv_done[(n - kBack) & 1]), ((n - kBack) >> 1) & 1, abort_flag, a.err);
+                            const int back = n - kBack;
+                            return fresh ? o_left() : mbar_wait(smem_u32(&S.pv_done[back & (F::kPB - 1)]), (back / F::kPB) & 1, abort_flag, a.err);
                         });
                         if (!ok) break;
                         if (fresh) waited = true;
@@ -900,7 +902,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 // the last tile was this set's: the rows, or their partial
                 group_ask([&]() {
                     return mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
-                           mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & 1]), ((n_end - 1) >> 1) & 1, abort_flag, a.err);
+                           mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & (F::kPB - 1)]), ((n_end - 1) / F::kPB) & 1, abort_flag, a.err);
                 });
                 if (!ok) break;
                 tc_fence_after();

@@ -369,6 +369,24 @@ def test_rows_of_an_item_by_widths(type, d_qk, d_v, G, new):
     check(c, q, [new, 1], got, d_qk ** -0.5, None, w)
 
 
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G,new", [(8, 1), (8, 2), (8, 4), (8, 8)])
+def test_two_hundred_calls_in_a_row(type, d, G, new):
+    """Every SM with several items, again and again: no wait runs out, and the last call has the bits of the first."""
+    lens = [600 + 400 * b for b in range(10)]
+    c = Cache(lens, 8 * G, 8, d, d, type, seed=d + new, room=[n + 8 for n in lens])
+    q = c.queries(10 * new)
+    ws = dsa.grouped_workspace(c.dims(), 10 * new)
+    cu = starts([new] * 10)
+    out, lse = dsa.grouped_attn(c.dims(), q, *c.args(), d ** -0.5, cu, ws=ws)
+    first = out.clone(), lse.clone()
+    for _ in range(200):
+        dsa.grouped_attn(c.dims(), q, *c.args(), d ** -0.5, cu, out=out, lse=lse, ws=ws)
+    assert dsa.read_error(ws) == 0
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 def test_weights_of_many_sequences():
     lens = [(i * 53) % 300 for i in range(300)]
     c = Cache(lens, 6, 2, 16, 16, seed=14)
