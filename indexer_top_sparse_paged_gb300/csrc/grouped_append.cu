@@ -4,6 +4,10 @@
 // scale (no smaller than the one its earlier tokens have), then the rows are written as codes; where the scale has
 // grown, the earlier codes are rounded anew against it. So a scale only ever grows while a block fills, and codes whose
 // scale stays are not touched.
+//
+// One row a sequence: latency bounds it (32 sequences, 8 heads of 128 and 128: 5.1 us of kernel time, 17 us a call in a
+// stream), which is why a CTA reads its rows once, into registers, and keeps the next on their way. A prompt's many rows: the
+// instructions of rounding (2 x 4096 tokens: 16.9 us; its 50 MB take 7.4; 65% of the issue slots busy).
 #include "grouped.cuh"
 
 namespace dsa {

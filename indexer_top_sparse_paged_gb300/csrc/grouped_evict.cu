@@ -6,11 +6,15 @@
 // histogram of the next bits, reads the others' through distributed shared memory, and all find the same bin. Keys stay
 // in shared memory from the first pass on, as far as they fit (else they are read again). Then every warp counts what it
 // keeps of its run -- all above the last weight, and of those equal to it the first ones -- and writes it in order.
-// Latency bounds it (five cluster barriers): 128K positions for each of 8 heads take FIXME us, 8 x 8 heads of 16K FIXME.
+// Latency and shared-memory atomics bound it (five cluster barriers; the weights are 4 MB): 128K positions for each of 8
+// heads take 26 us, 8 x 8 heads of 16K 17. Clusters of 8 CTAs at most: of 16, which may not be spread over as many SMs, the
+// former took 116 us. Each CTA sums a slice of the bins for all (33 us when every CTA summed them all).
 //
 // Move: a CTA for each (new block, sequence and head), keys and values together since they share the chain kept position
 // -> block -> row. A thread keeps its 16-byte pieces in registers between the largest magnitude (of the codes' 7 low
-// bits, which order as the values do) and the rounding against the new scale.
+// bits, which order as the values do) and the rounding against the new scale. The rounding's instructions bound it: 8
+// sequences cut from 16K to 8K, 8 heads of 128 and 128, 81 us (237 MB; copying the codes without rounding them takes 61,
+// the bytes 41), 65% of the issue slots busy; with a division for each code it took 128.
 #include "grouped.cuh"
 
 namespace dsa {

@@ -6,19 +6,32 @@
 // significand bits,
 //   t = q 2^-e,  t = t_0 + t_1 / 16 + t_2 / 256 + ...,  t_i = e4m3(16^i * what is left),
 // and so are the weights. Two parts hold a bf16 query exactly (elements below 2^-13 of its largest keep an absolute error
-// of 2^-21 of that), three parts 11 bits of a weight (rounded to fp16 first; an absolute error of 2^-26 of the largest),
-// six parts hold fp32. With the cached rows as the M side of both products the parts are extra columns:
+// of 2^-21 of that), four parts a weight that was rounded to fp16 (three would lose its last bit; 2^-26 of the largest is
+// left of small ones), six parts hold fp32. With the cached rows as the M side of both products the parts are extra columns:
 //   S^T [128 positions x (parts * rows)] = K tile [128 x d_qk] . Q^T,   K-major, from shared memory as TMA wrote it
 //   O^T [d_v x (parts * rows)] += V tile^T [d_v x 128] . P^T,            MN-major: the same row layout read the other way
-// (M = 128, N = 16 .. 192), 32 bytes of K a step. Position = TMEM lane: a softmax thread holds its position's logits of
-// all rows, only the running maximum crosses lanes, and O's rescaling touches few columns.
+// (M = 128, N = 16 .. 256), 32 bytes of K a step: 46 cycles each up to N = 64, 128 at N = 256. Position = TMEM lane: a
+// softmax thread holds its position's logits of all rows, so only maxima cross lanes, and O's rescaling touches few columns.
 //
-// Bytes bound it: 2 x 128 of a head's position at d = 128, and 4 products of N = 16 or 32 columns take a tenth of the time
-// those bytes take. One CTA an SM works through its even share of the tiles (see grouped.cuh): a warp of TMA loads runs
-// ahead as far as the ring allows, whatever items it crosses, one warp issues the products, two warps bring the next
-// item's queries, and the softmax's warps, kRW rows a thread, take tiles in turn in kSets sets, each with a maximum, a sum
-// and an O^T of its own: the chain logits -> maximum -> weights of one tile (about 1500 cycles) is longer than its bytes
-// take (1400). The set that has an item's last tile puts the two together.
+// Softmax: weights are formed against a row's reference m, its maximum when that was last looked at. As long as no logit of
+// a tile passes m by more than 4 (in powers of two) the weights stay below 2^4 and are kept as they are; else m moves to the
+// maximum, O^T and the sums are multiplied by 2^(m_old - m), and the tile's weights are formed again. So most tiles need no
+// maxima across lanes, and no tile's weights wait for them: the warps exchange one flag, read after the weights are
+// written (drafts of 16 x 4 147 us with maxima in every tile, 121 without). The block's value scale is a factor of the
+// weights, against a power of two that grows with the scales met.
+//
+// What bounds it. One row a token and 8 heads a key head (N = 16 and 32): bytes; 32 sequences of 16K - 32K 259 us, 1.55 GB
+// at 6.0 TB/s, 88% of a copy's rate; one of 1M 346 us, 91%. More rows: the softmax's instructions and their latencies, a
+// row at a time (2 rows a token 93 us, 4 112, 8 180 where the bytes take 37). Few bytes: the launch and the items' chains.
+// A tile's chain logits -> weights (about 1500 cycles) is longer than its bytes take (1400), so two sets of warps take
+// tiles in turn, each with a maximum, a sum and an O^T of its own, and the set with an item's last tile puts the two
+// together; where rows fill the warps of both, one set of kGroups warpgroups shares a tile's rows (see the forms below).
+// One CTA an SM works through its even share of the tiles (see grouped.cuh): a warp of TMA loads runs ahead as far as the
+// ring allows, whatever items it crosses; one warp issues the products, the values' as soon as their weights are there
+// (d = 256, where the ring has 3 stages: 134 us when they stood behind the next keys', 102 so); two warps bring the next
+// item's queries. 12 warps leave 168 registers a thread; more, of fewer rows or with spills, were slower but for 64 rows.
+// An item's end costs about 4 us of the products' and the softmax's latencies: 128 sequences of 1024 take 100 us where the
+// bytes take 40, of 16K and more a tenth above them.
 #include <cstddef>
 
 #include "grouped.cuh"
@@ -78,7 +91,8 @@ struct Item {
 };
 
 // Compiled forms: rows of a softmax thread, warpgroups that share a tile's rows, sets that take tiles in turn, parts of a
-// query and of a weight, buffers of logits.
+// query and of a weight, buffers of logits. (32 rows, drafts of 16 x 4: two warpgroups of 16 rows a thread 115 us; one of 32
+// rows in each of two sets, four of 8 rows, or two of 16 rows in each of two sets 152 - 182.)
 template <int kRW_, int kGroups_, int kSets_, int kQP_, int kPP_, int kSB_>
 struct Form {
     static constexpr int kRW = kRW_, kGroups = kGroups_, kSets = kSets_, kQP = kQP_, kPP = kPP_, kSB = kSB_;
@@ -1014,7 +1028,10 @@ static bool launch_form(const GroupedArgs& a, cudaStream_t s) {
 }  // namespace gtc
 
 // Rows of an item: as many as the average sequence of the call has for a key head, in powers of two. Of fp32 queries and
-// of wide values fewer: their parts fill tensor memory (and of wide keys, shared memory).
+// of wide values fewer: their parts fill tensor memory (and of wide keys, shared memory). More rows an item read the cache
+// fewer times (16 sequences of 8000 on average, 8 heads of 128, 8 query heads each; us): 16 rows a sequence 123 in items of
+// 8, 93 in one of 16; 32 rows 170 in items of 16, 112 in one of 32; 64 rows 208 in items of 32, 180 in one of 64; fp32, 16
+// rows 159 in items of 8, 95 in one of 16.
 int grouped_row_tile(const dsa_grouped_dims& d, int T) {
     const int64_t rows = (static_cast<int64_t>(T) + d.B - 1) / d.B * (d.H / d.H_kv);
     const int most = d.type == DSA_F32 || d.d_v > 128 ? 16 : d.d_qk > 128 ? 32 : 64;
