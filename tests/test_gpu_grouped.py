@@ -397,6 +397,17 @@ def test_weights_of_many_sequences():
 
 
 @pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,new,G", [([900, 0, 130], [10, 2, 3], 64), ([20000, 3000], [3, 5], 40), ([70], [1], 3), ([500] * 260, [3] * 260, 4)])
+def test_weights_of_many_rows(type, lens, new, G):
+    """Few position tiles, whose rows a CTA's warps share, and more tiles than CTAs; sequences past the first 256."""
+    c = Cache(lens, G, 1, 32, 16, type, seed=G)
+    q = c.queries(sum(new))
+    w = torch.rand((len(lens), 1, c.width * 64), device="cuda")
+    base = w.clone()
+    check(c, q, new, attend(c, q, new, 0.2, weights=w, weights_out=w), 0.2, base, w)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
 def test_logits_that_pass_the_maximum_by_a_little_and_by_much(type):
     """Maxima that rise from tile to tile by less than the slack of the weights' reference, by about it, and by far more; rows
     whose first tiles show them nothing (invalid blocks)."""
