@@ -399,8 +399,9 @@ dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, i
  * Positions in invalid blocks are left out and reported. What unused slots of a block hold does not matter, NaN codes
  * included. A query of NaN or infinities gives a row of NaN (and NaN weights); other inputs are finite. sm_scale > 0.
  * DSA_BF16: queries enter the products exactly but for elements below 2^-13 of their row's largest (an absolute error of
- * 2^-21 of that), softmax weights with 11 significant bits (and 2^-26 of their row's largest); DSA_F32: both with 24 bits.
- * Sums keep fp32. The result of a call does not depend on timing.
+ * 2^-21 of that), softmax weights with 11 significant bits, small ones with an error of 2^-22 of their row's largest weight;
+ * DSA_F32: both with 24 bits, small weights with an error of 2^-30 of the largest. That holds whatever the blocks' value
+ * scales are, within 2^60 of each other. Sums keep fp32. The result of a call does not depend on timing.
  * ws: at least dsa_grouped_workspace_size(dims, T, weights wanted) bytes, 256-byte aligned, initialised with
  * dsa_workspace_init.
  */

@@ -5,9 +5,11 @@
 // core's cost here goes with the cached rows, not with the few query rows: a query row is split into e4m3 parts of 4
 // significand bits,
 //   t = q 2^-e,  t = t_0 + t_1 / 16 + t_2 / 256 + ...,  t_i = e4m3(16^i * what is left),
-// and so are the weights. Two parts hold a bf16 query exactly (elements below 2^-13 of its largest keep an absolute error
-// of 2^-21 of that), four parts a weight that was rounded to fp16 (three would lose its last bit; 2^-26 of the largest is
-// left of small ones), six parts hold fp32. With the cached rows as the M side of both products the parts are extra columns:
+// and so are the weights, their last part in units of 1/256 of the one before. Two parts hold a bf16 query exactly (elements
+// below 2^-13 of its largest keep an absolute error of 2^-21 of that), six parts hold fp32. Four parts hold a weight that was
+// rounded to fp16 exactly down to 2^-12, in what it is split in (a row's largest weight is 1 there, or more); smaller ones
+// are off by 2^-23, those below 2^-20 by fp16's 2^-25 alone (with 1/16: 2^-22 for all). With the cached rows as the M side
+// of both products the parts are extra columns:
 //   S^T [128 positions x (parts * rows)] = K tile [128 x d_qk] . Q^T,   K-major, from shared memory as TMA wrote it
 //   O^T [d_v x (parts * rows)] += V tile^T [d_v x 128] . P^T,            MN-major: the same row layout read the other way
 // (M = 128, N = 16 .. 256), 32 bytes of K a step: 46 cycles each up to N = 64, 128 at N = 256. Position = TMEM lane: a
@@ -18,7 +20,10 @@
 // maximum, O^T and the sums are multiplied by 2^(m_old - m), and the tile's weights are formed again. So most tiles need no
 // maxima across lanes, and no tile's weights wait for them: the warps exchange one flag, read after the weights are
 // written (drafts of 16 x 4 147 us with maxima in every tile, 121 without). The block's value scale is a factor of the
-// weights, against a power of two that grows with the scales met.
+// weights, 1 .. 16 times: it stands against a power of two that the loads' warp chooses by the scales of 32 blocks at a time,
+// 16^-i of it for smaller ones. Where that power changes, O^T is multiplied by the old one over the new (exactly); where it
+// changes within a tile, the blocks take turns: weights of the first, its products, O^T moved, weights of the second. So a
+// block with a large scale, be it of zeros, takes no bits from the light weights of others.
 //
 // What bounds it. One row a token and 8 heads a key head (N = 16 and 32): bytes; 32 sequences of 16K - 32K 259 us, 1.55 GB
 // at 6.0 TB/s, 88% of a copy's rate; one of 1M 346 us, 91%. More rows: the softmax's instructions and their latencies, a
@@ -43,6 +48,9 @@ constexpr int kChunk = 64 * 128;  // bytes of one block's 128 columns of codes
 constexpr int kMaxStages = 6;
 constexpr float kSlack = 4.0f;  // a weight is 2^kSlack at most,
 constexpr float kTop = 16.0f;   // and kTop * 2^kSlack = 256 as it is split into codes (which end at 448)
+constexpr int kLastPart = 256;  // a weight's last part against the one before it
+constexpr int kLeastRef = 27;   // exponents (127: of 1) of what value scales refer to: the least,
+constexpr int kRefRange = 60;   // and how far they fall below an item's largest
 constexpr size_t kSmemLimit = 232448;
 
 __host__ __device__ constexpr int pad16(int n) { return (n + 15) / 16 * 16; }
@@ -112,6 +120,7 @@ struct Form {
     // products of tile n the values' are issued of all before n - kSB / 2 (tile n - 3 and before of two sets, n - 2 of one),
     // so that whoever has the logits of n knows that the phase before n's, tile n - kPB's, has ended on each of these
     // barriers. With two barriers for two sets, n - 2 might not have: the wait for n could take the phase before for its own.
+    // (A tile whose blocks take turns has two phases of each; the first has been waited for when the second's weights come.)
     static constexpr int kPB = kSets == 2 ? 4 : 2;
     static_assert(kSN % 16 == 0 && kSN <= 256 && kPN <= 256 && kCols <= 512, "shapes of the products");
 };
@@ -121,8 +130,9 @@ struct Ctl {
     // barriers, with their arrivals in barrier_count
     uint64_t full[kMaxStages], empty[kMaxStages], s_full[F::kSB], pv_done[F::kPB], mma_done;
     uint64_t q_full[2], p_full[F::kPB], o_free, left[2], q_first, fin, q_empty[2];
-    float4 scales[kMaxStages];                // of a tile's two blocks: keys, keys, values, values
-    int valid[kMaxStages];                    // bits 0, 1: the blocks are there
+    alignas(16) float2 scales[kMaxStages][2];  // of a tile's blocks: the keys' scale, the values' times kTop / what it refers to
+    uint32_t refs[kMaxStages];                // bits 0, 1: the blocks are there; 2: they refer to different powers of two and
+                                              // take turns; from 8 and 16: the exponents of these
     alignas(16) float q_factor[2][F::kRows];  // 2^e * sm_scale * log2(e)
     alignas(16) int seen[2][F::kRows];        // positions below this are seen (rows past the last: 0)
     alignas(16) int row_at[2][F::kRows];      // token * H + head
@@ -200,23 +210,24 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
     return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3));
 }
 
-// Splits two values (magnitudes up to 448) into kParts pairs of codes. bf16 calls split fp16 values: exact differences.
-template <int kParts>
+// Splits two values (magnitudes up to 448) into kParts pairs of codes, each part in units of 1/16 of the one before and the
+// last of 1/kLast. bf16 calls split fp16 values: exact differences.
+template <int kParts, int kLast>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&parts)[kParts]) {
     if constexpr (kParts <= 4) {
         __half2 t = __floats2half2_rn(a, b);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             parts[i] = cvt_e4m3x2(t);
-            if (i + 1 < kParts) t = __hmul2(__hsub2(t, half2_of(parts[i])), __float2half2_rn(16.0f));
+            if (i + 1 < kParts) t = __hmul2(__hsub2(t, half2_of(parts[i])), __float2half2_rn(i + 2 < kParts ? 16.0f : kLast));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             parts[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
             const float2 f = __half22float2(half2_of(parts[i]));
-            a = (a - f.x) * 16.0f;
-            b = (b - f.y) * 16.0f;
+            a = (a - f.x) * (i + 2 < kParts ? 16.0f : kLast);
+            b = (b - f.y) * (i + 2 < kParts ? 16.0f : kLast);
         }
     }
 }
@@ -308,7 +319,7 @@ __device__ __forceinline__ void join_parts(uint32_t addr, float (&y)[8]) {
         float o[8];
         load_columns<8>(addr + i * kStep, o);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) y[r] = fmaf(y[r], 0.0625f, o[r]);
+        for (int r = 0; r < 8; ++r) y[r] = fmaf(y[r], i == kPP - 2 ? 1.0f / kLastPart : 0.0625f, o[r]);
     }
 }
 
@@ -400,7 +411,7 @@ __device__ __forceinline__ void split_queries(const GroupedArgs& a, const Groupe
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         uint32_t parts[4][F::kQP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_pair<F::kQP>(x[2 * i] * down, x[2 * i + 1] * down, parts[i]);
+        for (int i = 0; i < 4; ++i) split_pair<F::kQP, 16>(x[2 * i] * down, x[2 * i + 1] * down, parts[i]);
         if (col >= kc * 128) continue;
         const int nrow = (r / F::kRW) * (F::kQP * F::kRW) + r % F::kRW, c16 = (col & 127) >> 4;
         const uint32_t to = dst + (col >> 7) * F::kQBytes + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
@@ -518,6 +529,26 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             };
             int row, row_next;
             float ks, vs, ks_next, vs_next;
+            // What the weights of 32 blocks refer their value scales to: a power of two no smaller than any of them, kept from
+            // before unless it is 4 times too large, or 16^-i of it for a scale that is 16^i times smaller or more. So a block's
+            // weights keep their bits whatever the scales of others are, and O^T is seldom moved to another power (which loses
+            // nothing, as long as they stay within 2^kRefRange of an item's largest).
+            int unit = 0, most = 0;
+            uint32_t refs;
+            auto refer = [&]() {
+                const bool there = row >= 0;
+                const uint32_t bits = there ? __float_as_uint(vs) & 0x7FFFFFFFu : 0u;
+                const int e = min(max(static_cast<int>((bits + 0x7FFFFFu) >> 23), kLeastRef), 254);  // 2^(e - 127) >= the scale
+                const int top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(e)));
+                if (top > unit || top + 2 <= unit) unit = top;
+                most = max(most, unit);
+                const int mine = max(max(unit - ((unit - e) & ~3), most - kRefRange), kLeastRef);
+                vs = __uint_as_float(bits) * __uint_as_float(static_cast<uint32_t>(258 - mine) << 23);  // kTop / 2^(mine - 127)
+                const int next = __shfl_down_sync(0xFFFFFFFFu, mine, 1);
+                const bool next_there = __shfl_down_sync(0xFFFFFFFFu, there, 1);
+                const int first = there ? mine : next_there ? next : unit, second = next_there ? next : first;  // (even lanes: of their tile)
+                refs = (there ? 1u : 0u) | (next_there ? 2u : 0u) | (first != second ? 4u : 0u) | first << 8 | second << 16;
+            };
             fetch(2 * p.tile0, row_next, ks_next, vs_next);
             for (int tile = p.tile0; ok && tile < p.tile1; ++tile) {
                 const int j = (tile - p.tile0) & 15;
@@ -542,15 +573,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     }
                 }
                 // the scales may still be on their way: they follow
-                float4 sc;
-                sc.x = __shfl_sync(0xFFFFFFFFu, ks, 2 * j), sc.y = __shfl_sync(0xFFFFFFFFu, ks, 2 * j + 1);
-                sc.z = __shfl_sync(0xFFFFFFFFu, vs, 2 * j), sc.w = __shfl_sync(0xFFFFFFFFu, vs, 2 * j + 1);
-                if (lane == 0) {
-                    S.scales[st] = sc;
-                    S.valid[st] = (r0 >= 0 ? 1 : 0) | (r1 >= 0 ? 2 : 0);
-                    mbar_arrive(bar);
+                if (j == 0) refer();
+                if (lane >> 1 == j) {
+                    S.scales[st][lane & 1] = make_float2(ks, vs);
+                    if (!(lane & 1)) S.refs[st] = refs;
                 }
                 __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
                 ++tiles;
                 if (++st == stages) st = 0, phase ^= 1;
             }
@@ -569,13 +598,17 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         int st = 0, phase = 0, st_v = 0, n = 0, done = 0, item = 0;  // tiles whose logits, whose values were issued
         int last = 0;  // first tile of the item before
         uint32_t first = 0;  // bit n % 32: tile n is the first of its item in its set
+        uint32_t came = 0;   // bit b: the phase of p_full[b] to wait for
+        bool half = false;   // tile `done` has scales far apart, and its first block's values were issued
         bool ok = true;
         const int ksteps = (a.d_qk + 31) / 32;
         auto values = [&]() {  // V^T P^T of tile `done`
             const int set = kSets == 2 ? done & 1 : 0, buf = done & (F::kPB - 1);
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[buf]), (done / F::kPB) & 1, abort_flag, a.err));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&S.p_full[buf]), (came >> buf) & 1, abort_flag, a.err));
             if (!ok) return;
             tc_fence_after();
+            came ^= 1u << buf;
+            half = !half && (S.refs[st_v] & 4);
             const bool fresh = (first >> (done & 31)) & 1;
             for (int c = 0; c < vc; ++c) {
                 const uint64_t da = sw128_desc(sRing + st_v * stage_bytes + v_off + 2 * c * kChunk, 0, 1024);
@@ -584,6 +617,11 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 for (int k = 0; k < 4; ++k)
                     warp_mma_f8(tmem + F::kColO + (set * F::kVCMax + c) * F::kPN, da + k * (4096 >> 4), db + k * (512 >> 4),
                                 idesc_f8(F::kPN, 1u, 1u), fresh && k == 0 ? 0u : 1u);
+            }
+            if (half) {  // the other block's weights follow
+                warp_tc_commit(smem_u32(&S.pv_done[buf]));
+                first &= ~(1u << (done & 31));
+                return;
             }
             warp_tc_commit(smem_u32(&S.empty[st_v]));
             warp_tc_commit(smem_u32(&S.pv_done[buf]));
@@ -598,7 +636,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             while (ok && (done < least || !__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))) {
                 if (done == n) {
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, a.err));
-                } else if (__all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[done & (F::kPB - 1)]), (done / F::kPB) & 1))) {
+                } else if (__all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&S.p_full[done & (F::kPB - 1)]), (came >> (done & (F::kPB - 1))) & 1))) {
                     values();
                     t0 = clock64();
                 } else {
@@ -708,6 +746,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         float* fac = S.fac[warp];
         const int mates = set * kGroups + group;
         int n = set, n_item = 0, st = set, sphase = 0, item = 0, turn = 0, left = 0, asked = 0;  // n: this set's next tile, n_item: the item's first
+        uint32_t sent = ~0u;  // bit b: the phase of pv_done[b] that ends with the products of what was last put in buffer b
+        int round = 0;        // 1: of a tile with scales far apart, the second block
         bool ok = true;
         // The group's four warps meet at a barrier of the hardware, at which they sleep (asking a barrier in memory again and
         // again, four warps slow each other: 2 rows a token 108 us, so 92). Only the first warp waits for other roles, with
@@ -736,7 +776,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             const Item& it = S.item[qb];
             if (!ok || !it.tiles) break;
             const int n_end = n_item + it.tiles, len = it.len, all_see = it.all_see;
-            float l[kRW], v_ref = 0x1p-100f;
+            float l[kRW];
+            int v_ref = kLeastRef;  // exponent of what value scales refer to in O^T
             float m = -INFINITY;  // what the weights of row lane % kRW refer to: its maximum so far, or up to kSlack less
 #pragma unroll
             for (int r = 0; r < kRW; ++r) l[r] = 0.0f;
@@ -747,7 +788,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             auto o_left = [&]() { return waited || mbar_wait(smem_u32(&S.o_free), (item - 1) & 1, abort_flag, a.err); };
             const bool any = n < n_end;
             bool fresh = true;
-            for (; ok && n < n_end; n += kSets) {
+            while (ok && n < n_end) {
                 const int tile = it.tile0 + n - n_item;
                 group_ask([&]() {
                     return mbar_wait(smem_u32(&S.full[st]), sphase, abort_flag, a.err) &&
@@ -755,10 +796,13 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 });
                 if (!ok) break;
                 tc_fence_after();
-                const float4 sc = S.scales[st];
-                const int valid = S.valid[st], pos = tile * kGroupedTile + j;
-                const bool here = (valid >> (quarter >> 1)) & 1 && pos < len, whole = valid == 3 && (tile + 1) * kGroupedTile <= all_see;
-                if (!whole && group == 0 && !here) {  // what the slot holds must not reach the products: 0 * NaN is NaN
+                const float2 sc = S.scales[st][quarter >> 1];
+                const uint32_t refs = S.refs[st];
+                const int valid = refs & 7, pos = tile * kGroupedTile + j;
+                const bool there = valid >> (quarter >> 1) & 1 && pos < len, whole = valid == 3 && (tile + 1) * kGroupedTile <= all_see;
+                // blocks with scales far apart take turns
+                const bool mine = !(valid & 4) || (quarter >> 1) == round, here = there && mine;
+                if (!whole && group == 0 && !there && !round) {  // what the slot holds must not reach the products: 0 * NaN is NaN
                     for (int c = 0; c < vc; ++c) {
                         const uint32_t at = sRing + st * stage_bytes + v_off + 2 * c * kChunk + j * 128;
 #pragma unroll
@@ -766,12 +810,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + 16 * i), "r"(0) : "memory");
                     }
                 }
-                const float ks = !here ? 1.0f : quarter < 2 ? sc.x : sc.y;
-                const float v_top = fmaxf(valid & 1 ? fabsf(sc.z) : 0.0f, valid & 2 ? fabsf(sc.w) : 0.0f);
+                const float ks = here ? sc.x : 1.0f;
+                const int ref = refs >> (round ? 16 : 8) & 255;
                 uint32_t* flag = S.flag[turn][mates];
                 // The weights are formed against the maxima as they stand. Where a logit passes one by more than kSlack, in
                 // any of the group's warps, they are moved up first and the weights formed again.
-                bool move = fresh || v_top > v_ref, sure = false;
+                bool move = fresh || ref != v_ref, sure = false;
                 for (;;) {
                     float s[kRW];
                     load_logits<F::kQP, kRW>(lane_base + (n & (F::kSB - 1)) * F::kSN + group * F::kQP * kRW, ks, s);
@@ -791,20 +835,15 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         if (lane < kRW) S.red[mates][lane][quarter] = top * f_lane;
                         group_ask([&]() {  // O^T is this set's own, and the products into it have ended
                             constexpr int kBack = kSets == 2 ? 2 : 1;
-                            const int back = n - kBack;
-                            return fresh ? o_left() : mbar_wait(smem_u32(&S.pv_done[back & (F::kPB - 1)]), (back / F::kPB) & 1, abort_flag, a.err);
+                            const int back = (round ? n : n - kBack) & (F::kPB - 1);
+                            return fresh ? o_left() : mbar_wait(smem_u32(&S.pv_done[back]), (sent >> back) & 1, abort_flag, a.err);
                         });
                         if (!ok) break;
                         if (fresh) waited = true;
                         const float4 t = *reinterpret_cast<const float4*>(S.red[mates][lane % kRW]);
                         const float m_new = fmaxf(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)), m);
-                        // the weights carry their block's value scale, against a power of two no smaller than any so far
-                        float v_fac = 1.0f;
-                        if (v_top > v_ref) {
-                            const float ref = __uint_as_float((__float_as_uint(v_top) + 0x7FFFFFu) & 0x7F800000u);
-                            v_fac = v_ref / ref;
-                            v_ref = ref;
-                        }
+                        const float v_fac = __uint_as_float(static_cast<uint32_t>(max(127 + v_ref - ref, 0)) << 23);
+                        v_ref = ref;
                         if (lane < kRW) fac[lane] = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
                         m = m_new;
                         // (a row without positions so far: any logit moves it)
@@ -829,7 +868,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         }
                         group_sync();  // the maxima have been read
                     }
-                    if (a.weights_out && it.t + n - n_item < a.max_tiles) {
+                    if (a.weights_out && mine && it.t + n - n_item < a.max_tiles) {
                         float* to = a.z + ((it.t + n - n_item) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
                         for (int r = 0; r < kRW; ++r)
@@ -849,7 +888,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         __syncwarp();
                         asm volatile("barrier.arrive %0, 256;" ::"r"(1 + kSets * kGroups + mates) : "memory");
                     }
-                    const float tv = here ? (quarter < 2 ? sc.z : sc.w) * (kTop / v_ref) : 0.0f;
+                    const float tv = here ? sc.y : 0.0f;
                     const uint32_t p_buf = sP + (n & (F::kPB - 1)) * F::kPBytes + j * 16;
                     constexpr int kRun = kRW < 16 ? 8 : 16;  // rows whose codes stand side by side
 #pragma unroll
@@ -860,7 +899,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             const int r = r0 + 2 * i;
                             s[r] = ex2(s[r]);
                             s[r + 1] = ex2(s[r + 1]);
-                            split_pair<F::kPP>(s[r] * tv, s[r + 1] * tv, parts[i]);
+                            split_pair<F::kPP, kLastPart>(s[r] * tv, s[r + 1] * tv, parts[i]);
                         }
 #pragma unroll
                         for (int i = 0; i < F::kPP; ++i) {
@@ -896,6 +935,10 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.p_full[n & (F::kPB - 1)]));
+                sent ^= 1u << (n & (F::kPB - 1));
+                round = valid & 4 ? round ^ 1 : 0;
+                if (round) continue;  // the tile's other block
+                n += kSets;
                 st += kSets;
                 if (st >= stages) st -= stages, sphase ^= 1;
             }
@@ -908,7 +951,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 S.fin_l[qb][set][group * kRW + lane][quarter] = sum;
                 S.fin_m[qb][set][group * kRW + lane] = m;
             }
-            if (lane == 0) S.fin_unit[qb][set] = any ? v_ref * (1.0f / kTop) : 0.0f;
+            if (lane == 0) S.fin_unit[qb][set] = any ? __uint_as_float(static_cast<uint32_t>(v_ref) << 23) * (1.0f / kTop) : 0.0f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.fin));
             const bool complete = it.complete;
@@ -916,7 +959,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 // the last tile was this set's: the rows, or their partial
                 group_ask([&]() {
                     return mbar_wait(smem_u32(&S.fin), item & 1, abort_flag, a.err) &&
-                           mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & (F::kPB - 1)]), ((n_end - 1) / F::kPB) & 1, abort_flag, a.err);
+                           mbar_wait(smem_u32(&S.pv_done[(n_end - 1) & (F::kPB - 1)]), (sent >> ((n_end - 1) & (F::kPB - 1))) & 1, abort_flag, a.err);
                 });
                 if (!ok) break;
                 tc_fence_after();

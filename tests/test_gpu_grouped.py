@@ -712,3 +712,101 @@ def test_decode_loop_with_eviction(type):
     for i in range(3):
         step([1, 1, 1])
     step([5, 1, 2])
+
+
+# ------------------------------------------------------------------------------------------------ value scales that lie apart
+
+def light_and_heavy(type, H, n, d_v=32, new=1, seed=50):
+    """One sequence of n positions whose logits are 0 but for those set by `louder`: head h of H multiplies that by its own gap."""
+    c = Cache([n], H, 1, 16, d_v, type, seed=seed)
+    at = c.table[0, :(n + 63) // 64].long()
+    c.k[at] = 0
+    c.ks[at] = 1.0
+    c.v[at] &= 0x7F  # all of one sign: errors of one sign would add up
+    q = torch.zeros((new, H, 16), dtype=ACT[type], device="cuda")
+    q[..., 0] = (torch.linspace(0.0, 20.0, H, device="cuda") * math.log(2.0)).to(ACT[type])
+    return c, q, at
+
+
+def louder(c, pos):
+    c.k[int(c.table[0, pos // 64]), 0, pos % 64, 0] = 0x38  # 1.0
+
+
+SHAPES = [("f32", 8, 1), ("f32", 16, 1), ("bf16", 8, 1), ("bf16", 16, 1), ("bf16", 32, 1), ("bf16", 64, 1), ("bf16", 8, 7)]
+
+
+@pytest.mark.parametrize("type,H,new", SHAPES)
+@pytest.mark.parametrize("value,block", [(0.1, 0), (0.02, 1), (0.005, 37), (0.02, 68)])
+def test_a_heavy_block_of_zeros_beside_small_values(type, H, new, value, block):
+    """A block of zero values, whose scale is 1, takes up to all but a millionth of a row's weight; the others' small values
+    are held against their own scales."""
+    n = 69 * 64 - 5
+    c, q, at = light_and_heavy(type, H, n, new=new)
+    c.vs[at] = value / 448
+    c.v[at[block]] = 0
+    c.vs[at[block]] = 1.0
+    for pos in range(64 * block, min(64 * block + 64, n)):
+        louder(c, pos)
+    w = torch.zeros((1, 1, c.width * 64), device="cuda")
+    got = attend(c, q, [new], 1.0, weights_out=w)
+    check(c, q, [new], got, 1.0, None, w)
+
+
+@pytest.mark.parametrize("type,H,new", SHAPES)
+def test_a_heavy_position_in_a_block_of_large_values(type, H, new):
+    """A position of zero values that takes most of the weight, in a block that a single value of another one gives a large
+    scale: the columns without that value keep the light positions' weights."""
+    for block in (0, 1, 30):
+        c, q, at = light_and_heavy(type, H, 64 * 64, new=new)
+        c.vs[at] = 2.0 ** -13
+        c.v[at[block]] = 0
+        c.v[at[block], 0, 9, 0] = 0x7E  # 448
+        c.vs[at[block]] = 1.0
+        louder(c, 64 * block + 3)
+        check(c, q, [new], attend(c, q, [new], 1.0), 1.0)
+
+
+@pytest.mark.parametrize("type,H,new", SHAPES)
+def test_scales_that_change_from_block_to_block(type, H, new):
+    """Blocks with scales far apart in turn (also with the smaller ones first, and with invalid blocks between them); large
+    values stand in one column, so that the others have the small ones alone."""
+    for first, gone in ((0, ()), (1, ()), (0, (6, 9, 20))):
+        c, q, at = light_and_heavy(type, H, 50 * 64 - 30, new=new)
+        c.vs[at] = 2.0 ** -13
+        large = at[first::2]
+        c.v[large, :, :, 1:] = 0
+        c.vs[large] = 3.0
+        for pos in (70, 200, 2000):
+            louder(c, pos)
+        for j in gone:
+            c.table[0, j] = -1
+        w = torch.rand((1, 1, c.width * 64), device="cuda")
+        base = w.clone()
+        got = attend(c, q, [new], 1.0, faults=1 if gone else 0, weights=w)
+        check(c, q, [new], got, 1.0, base, w)
+
+
+@pytest.mark.parametrize("type,H,new", SHAPES)
+@pytest.mark.parametrize("step", [1.25, -1.25, 0.5, -2.5])
+def test_scales_that_rise_and_fall_by_steps(type, H, new, step):
+    """Scales that drift by a few powers of two a block, up or down, up to 2^54 in all; block j has values in column j % 32 alone."""
+    blocks = 44 if abs(step) < 2 else 22
+    c, q, at = light_and_heavy(type, H, 64 * blocks, new=new)
+    for j in range(blocks):
+        keep = c.v[at[j], :, :, j % 32].clone()
+        c.v[at[j]] = 0
+        c.v[at[j], :, :, j % 32] = keep
+        c.vs[at[j]] = 2.0 ** (step * (j - blocks // 2)) / 448
+    for pos in (3, 64 * blocks - 9 - new):
+        louder(c, pos)
+    out, _ = attend(c, q, [new], 1.0)
+    k, v, _ = c.rows(0, 0)
+    for i in range(new):
+        z = (q[i].double() @ k.T).masked_fill(torch.arange(64 * blocks, device="cuda") > 64 * blocks - new + i, -math.inf)
+        p = torch.softmax(z, -1)
+        # the header's bounds: 11 bits of a weight in bf16 and 2^-22 of the row's largest, in fp32 24 bits and 2^-30; logits of one
+        # product each, up to 14 (20 ln 2): 2^-22 of that in the factor and the subtraction, twice (logit and sum); the sums' roundings
+        rel = (2.0 ** -10 + 2.0 ** -8 if type == "bf16" else 2.0 ** -21) + 2 * 2.0 ** -22 * 15 + 64 * blocks * 2.0 ** -24
+        tol = rel * (p @ v) + (2.0 ** -22 if type == "bf16" else 2.0 ** -30) * p.amax(-1, keepdim=True) * v.sum(0) + 1e-30
+        err = (out[i].double() - p @ v).abs()
+        assert bool((err <= tol).all()), (i, float((err / tol).max()))
