@@ -374,8 +374,9 @@ typedef struct {
 /*
  * Append of the sequences' new tokens (k_new [T][H_kv][d_qk], v_new [T][H_kv][d_v]), in fp32. With a the largest
  * magnitude among the new rows that a block receives for a head, its scale becomes
- *   a / 448 (1 when a is 0)       if the block held no earlier token of the sequence
- *   max(old scale, a / 448)       if it did; when that is larger, the earlier codes become
+ *   a / 448 (1 when a is 0)       if the block held no earlier token of the sequence, or zeros alone (its scale is 1 and
+ *                                 the head's earlier codes are all 0)
+ *   max(old scale, a / 448)       otherwise; when that is larger, the earlier codes become
  *                                 RNE_e4m3(code * old scale / scale)
  * and each new code RNE_e4m3(x / scale), saturating at +-448. Slots behind the new tokens stay as they were. A token
  * whose position is negative or whose block is invalid is skipped and reported. New values are finite; a block that

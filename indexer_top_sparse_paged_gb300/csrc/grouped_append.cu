@@ -2,8 +2,8 @@
 //
 // One CTA per (block that gets new tokens, head, keys or values): the new rows' largest magnitude gives the block's
 // scale (no smaller than the one its earlier tokens have), then the rows are written as codes; where the scale has
-// grown, the earlier codes are rounded anew against it. So a scale only ever grows while a block fills, and codes whose
-// scale stays are not touched.
+// grown, the earlier codes are rounded anew against it. So a scale only ever grows while a block fills (but for that of
+// nothing but zeros), and codes whose scale stays are not touched.
 //
 // One row a sequence: latency bounds it (32 sequences, 8 heads of 128 and 128: 5.1 us of kernel time, 17 us a call in a
 // stream), which is why a CTA reads its rows once, into registers, and keeps the next on their way. A prompt's many rows: the
@@ -165,7 +165,16 @@ __global__ void __launch_bounds__(kGroupedAppendThreads) grouped_append_kernel(G
         float amax = 0.0f;  // (fmaxf passes NaN over)
 #pragma unroll
         for (int w = 0; w < kGroupedAppendThreads / 32; ++w) amax = fmaxf(amax, red[turn][w]);
-        const float scale = slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax);
+        float scale = slot0 ? fmaxf(old, amax / 448.0f) : unit_scale(amax);
+        if (slot0 && old == 1.0f && amax < 448.0f) {  // (the same for all threads)
+            // Tokens of zeros leave the scale 1, against which smaller values would lose their bits: they count as none.
+            uint32_t held = 0;
+            for (int i = tid; i < slot0 * groups; i += kGroupedAppendThreads) {
+                const uint4 c = codes[i];
+                held |= (c.x | c.y | c.z | c.w) & 0x7F7F7F7Fu;
+            }
+            if (!__syncthreads_or(held != 0)) scale = unit_scale(amax);
+        }
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int i = tid + p * kGroupedAppendThreads;

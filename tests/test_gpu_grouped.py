@@ -543,6 +543,46 @@ def test_append_of_zeros_extremes_and_a_batch_of_many():
     append_and_check(c, [i % 3 for i in range(600)])
 
 
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [16, 128, 256])
+def test_zeros_before_small_values(type, d):
+    """Tokens of zeros (of either sign) leave a block without a scale: the first others set it. One head's zeros, or the keys'
+    alone, do no more; a scale of 1 that values have stays."""
+    c = Cache([0, 0, 0], 4, 2, d, d, type, seed=26, room=[140, 140, 140])
+    ws = dsa.grouped_workspace(c.dims(), 8)
+
+    def append(rows, new):
+        k, v = (torch.stack(x).to(ACT[type]).cuda() for x in rows)
+        c.lens = [n + m for n, m in zip(c.lens, new)]
+        c.seq_lens.copy_(ints(c.lens))
+        dsa.grouped_append(c.dims(), k, v, c.table, c.seq_lens, c.k, c.ks, c.v, c.vs, starts(new), ws=ws)
+        assert dsa.read_error(ws) == 0
+        return k, v
+
+    g = torch.Generator().manual_seed(d)
+    small = lambda: 0.02 * torch.randn((2, d), generator=g)  # noqa: E731
+    zero, one = torch.zeros((2, d)), torch.zeros((2, d))
+    one[1, 5] = 448.0  # head 1: a value whose scale is 1
+    first = lambda x: int(c.table[x, 0])  # noqa: E731
+    for _ in range(9):  # sequence 0: zeros; 1: head 1 has a value; 2: the keys alone are zeros
+        append(([zero, one, -zero], [-zero, zero, one + 1.0]), [1, 1, 1])
+    assert bool((c.ks[[first(0), first(1), first(2)]] == 1.0).all())
+    k, v = append(([small() for _ in range(3)], [small() for _ in range(3)]), [1, 1, 1])
+    top = lambda x: (x.cpu().float().abs().amax(-1) / 448.0).cuda()  # noqa: E731  (a quotient: on the GPU torch multiplies by 1 / 448)
+    assert torch.equal(c.ks[first(0)], top(k[0])) and torch.equal(c.vs[first(0)], top(v[0]))
+    assert torch.equal(c.ks[first(1), :1], top(k[1, :1])) and float(c.ks[first(1), 1]) == 1.0 and torch.equal(c.vs[first(1)], top(v[1]))
+    assert torch.equal(c.ks[first(2)], top(k[2])) and torch.equal(c.vs[first(2)], top((one + 1.0).to(ACT[type])))
+    for x, codes, scale in ((k, c.k, c.ks), (v, c.v, c.vs)):
+        for b in range(3):
+            s = scale[first(b)]
+            want = (x[b].float().cpu() / s.cpu()[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            assert torch.equal(codes[first(b), :, 9].cpu(), want)
+    assert not (c.k[first(0), :, :9] & 0x7F).any() and not (c.v[first(0), :, :9] & 0x7F).any()
+    append_and_check(c, [120, 3, 70])  # and on as ever
+    q = c.queries(3)
+    check(c, q, [1, 1, 1], attend(c, q, [1, 1, 1], 0.1), 0.1)
+
+
 def test_append_faults():
     c = Cache([10, 20, 30], 4, 2, 32, 32, "bf16", seed=25, room=[80, 80, 80])
     k, v = (torch.randn((3, 2, 32), device="cuda").bfloat16() for _ in range(2))
