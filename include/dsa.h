@@ -374,7 +374,7 @@ typedef struct {
 /*
  * Append of the sequences' new tokens (k_new [T][H_kv][d_qk], v_new [T][H_kv][d_v]), in fp32. With a the largest
  * magnitude among the new rows that a block receives for a head, its scale becomes
- *   a / 448 (1 when a is 0)       if the block held no earlier token of the sequence, or zeros alone (its scale is 1 and
+ *   a / 448 (1 when that is 0)    if the block held no earlier token of the sequence, or zeros alone (its scale is 1 and
  *                                 the head's earlier codes are all 0)
  *   max(old scale, a / 448)       otherwise; when that is larger, the earlier codes become
  *                                 RNE_e4m3(code * old scale / scale)

@@ -194,8 +194,11 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
     return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// The scale that takes amax to the largest code.
-__device__ __forceinline__ float unit_scale(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
+// The scale that takes amax to the largest code (1 where that is 0, as it also is for the smallest magnitudes).
+__device__ __forceinline__ float unit_scale(float amax) {
+    const float s = amax / 448.0f;
+    return s > 0.0f ? s : 1.0f;
+}
 
 __device__ __forceinline__ uint32_t e4m3x4_codes(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

@@ -583,6 +583,15 @@ def test_zeros_before_small_values(type, d):
     check(c, q, [1, 1, 1], attend(c, q, [1, 1, 1], 0.1), 0.1)
 
 
+def test_append_of_the_smallest_values():
+    """Magnitudes whose 448th part is 0 in fp32: a scale of 1 and codes of 0, not a scale of 0 and NaN."""
+    for spread in (1e-44, 1e-42, 3e-39):
+        c = Cache([0, 0, 70], 2, 1, 16, 32, "f32", seed=27, room=[140, 140, 140])
+        append_and_check(c, [65, 3, 60], spread=spread)
+        append_and_check(c, [1, 1, 1], spread=spread)
+        assert bool((c.ks[c.table[:, 0].long()] > 0).all()) and not (value(c.k[c.table[1, 0].long(), 0, :4])).isnan().any()
+
+
 def test_append_faults():
     c = Cache([10, 20, 30], 4, 2, 32, 32, "bf16", seed=25, room=[80, 80, 80])
     k, v = (torch.randn((3, 2, 32), device="cuda").bfloat16() for _ in range(2))
@@ -692,6 +701,23 @@ def test_evict_ties_and_special_weights():
     w[5] = 1.0 + torch.randint(0, 4, w[5].shape, device="cuda") * 2.0 ** -23
     for keep in (100, 250, 499):
         evict_and_check(Cache([500] * 6, 2, 1, 16, 16, seed=31), w, keep, 5, 20)
+
+
+def test_evict_of_the_smallest_values():
+    """Kept rows whose largest magnitude has 0 for its 448th part."""
+    c = Cache([300, 200], 2, 1, 16, 32, seed=36)
+    for t, scale in ((c.k, c.ks), (c.v, c.vs)):
+        used = torch.cat([c.table[0, :5], c.table[1, :4]]).long()
+        t[used] &= 0xBF  # codes below 2
+        scale[used] = 2.0 ** -149
+    w = torch.rand((2, 1, c.width * 64), generator=c.g, device="cuda")
+    to = torch.arange(c.blocks, c.blocks + 4, dtype=torch.int32, device="cuda").view(2, 2)
+    for name, fill in (("k", NAN_CODE), ("v", NAN_CODE), ("ks", float("nan")), ("vs", float("nan"))):
+        t = getattr(c, name)
+        setattr(c, name, torch.cat([t, torch.full((4,) + t.shape[1:], fill, dtype=t.dtype, device="cuda")]))
+    c.blocks += 4
+    evict_and_check(c, w, 100, 2, 8, new_table=to)
+    assert bool((c.ks[to.long()] == 1.0).all()) and not value(c.k[to[:, 0].long()]).isnan().any()
 
 
 def test_evict_long_sequences():
