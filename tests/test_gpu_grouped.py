@@ -746,6 +746,30 @@ def test_evict_in_place_and_faults():
     evict_and_check(c, torch.rand((3, 2, c.width * 64), device="cuda"), 200, 2, 8, faults=2)
 
 
+def test_rows_of_another_width_are_refused():
+    """Tables, weights and kept positions of more dimensions whose rows are longer than the call reads them."""
+    c = Cache([100, 70], 4, 2, 32, 32, seed=37, room=[200, 200])
+    gd, ws = c.dims(), dsa.grouped_workspace(c.dims(), 2, weights=True)
+    q, kv = c.queries(2), torch.randn((2, 2, 32), device="cuda").bfloat16()
+    w = torch.zeros((2, 2, c.width * 64), device="cuda")
+    wide = lambda t: torch.cat([t, t[..., :64]], -1).contiguous()  # noqa: E731
+    to, before = c.table[:, 2:4].contiguous(), [t.clone() for t in (c.k, c.ks, c.v, c.vs)]
+    append = lambda t=c.table: dsa.grouped_append(gd, kv, kv, t, c.seq_lens, c.k, c.ks, c.v, c.vs, ws=ws)  # noqa: E731
+    attn = lambda t=c.table, **kw: dsa.grouped_attn(gd, q, c.k, c.ks, c.v, c.vs, t, c.seq_lens, 0.1, ws=ws, **kw)  # noqa: E731
+    evict = lambda t=c.table, w=w, **kw: dsa.grouped_evict(gd, w, 64, t, c.seq_lens, to, c.k, c.ks, c.v, c.vs, ws=ws, **kw)  # noqa: E731
+    for call, what in ((lambda: append(wide(c.table)), "block_table"), (lambda: attn(wide(c.table)), "block_table"),
+                       (lambda: evict(wide(c.table)), "block_table"), (lambda: attn(weights=wide(w)), "weights"),
+                       (lambda: attn(weights_out=wide(w)), "weights_out"), (lambda: evict(w=wide(w)), "weights"),
+                       (lambda: evict(weights_out=torch.empty((2, 2, 192), device="cuda")), "weights_out"),
+                       (lambda: evict(kept=torch.empty((2, 2, 65), dtype=torch.int32, device="cuda")), "kept")):
+        with pytest.raises(ValueError, match="rows of " + what):
+            call()
+    assert all(same(a, b) for a, b in zip((c.k, c.ks, c.v, c.vs), before))
+    ref = attn(weights=w.clone())
+    got = attn(c.table.flatten(), weights=w.flatten())  # without dimensions of their own
+    assert torch.equal(got[0], ref[0]) and dsa.read_error(ws) == 0
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("type", ["f32", "bf16"])
