@@ -425,7 +425,10 @@ dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t
  *   weights_out [B][H_kv][new_max_blocks * 64]  fp32 out: the kept weights, then zeros; not weights itself
  * New blocks are distinct from every block that the call reads, but that a sequence which is not cut may keep its own
  * blocks (an entry equal to the old one is left alone). keep <= new_max_blocks * 64; sink, recent >= 0, together at
- * most keep. Keys carry the rotation of the positions they were appended at; later tokens go on from new_lens.
+ * most keep. What was kept goes on as a sequence of new_lens positions in new_table (with max_blocks = new_max_blocks, also
+ * of the weights): later tokens take the slots from new_lens on, and seq_lens counts these. Keys keep the rotation of the
+ * positions they were appended at, so later queries and keys are rotated at the sequence's own positions, which go on as if
+ * nothing had been evicted (dsa_rope with q_pos: without it, it takes them from seq_lens).
  * Rows from or into invalid blocks are skipped (their codes stay as they were) and reported. ws as for
  * dsa_cache_append (only its error word is used).
  */

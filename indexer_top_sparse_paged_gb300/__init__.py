@@ -708,7 +708,8 @@ def grouped_evict(dims: GroupedDims, weights, keep: int, block_table, seq_lens, 
                   *, sink: int = 0, recent: int = 0, ws, kept=None, new_lens=None, weights_out=None, stream=None):
     """(kept[B][H_kv][keep], new_lens[B], weights_out[B][H_kv][blocks * 64]): every sequence cut to ``keep`` positions for each
     key head -- the first ``sink``, the last ``recent`` and the heaviest of the rest by ``weights`` -- and the kept rows
-    copied into the blocks of ``new_table`` ([B][blocks]), requantised. Go on with new_table, new_lens and weights_out."""
+    copied into the blocks of ``new_table`` ([B][blocks]), requantised. Go on with new_table (dims of its width), new_lens as
+    seq_lens, and weights_out; rotate later queries and keys at their own positions (``rope(..., q_pos=)``), not by new_lens."""
     _need(new_table.dim() == 2 and new_table.shape[0] == dims.B, "new_table must be [B][blocks]")
     dev = _device(weights, block_table, seq_lens, new_table, k_cache, k_scale, v_cache, v_scale, ws, kept, new_lens, weights_out)
     _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, None, -1)

@@ -900,3 +900,46 @@ def test_scales_that_rise_and_fall_by_steps(type, H, new, step):
         tol = rel * (p @ v) + (2.0 ** -22 if type == "bf16" else 2.0 ** -30) * p.amax(-1, keepdim=True) * v.sum(0) + 1e-30
         err = (out[i].double() - p @ v).abs()
         assert bool((err <= tol).all()), (i, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_rotation_goes_on_over_an_eviction(type):
+    """Tokens rotated at their own positions before and after an eviction: the logit of a query at p with a key of s is the
+    cosine of p - s, although the cache counts fewer positions."""
+    H, H_kv, d, keep, sm = 4, 2, 64, 80, 2.0
+    lens = [150, 90]
+    c = Cache([0, 0], H, H_kv, d, d, type, seed=51, room=[400, 400])
+    freq = torch.zeros(d // 2, dtype=torch.float64, device="cuda")
+    freq[0] = 1.0
+    gd, ws = c.dims(), dsa.grouped_workspace(c.dims(), 300, weights=True)
+
+    def rows(pos, heads):  # 1 in the first column, turned by the position
+        x = torch.zeros((len(pos), heads, d), dtype=ACT[type], device="cuda")
+        x[..., 0] = 1.0
+        return dsa.rope(x, freq, q_pos=ints(pos), layout="half")
+
+    pos = list(range(150)) + list(range(90))
+    table, at = c.table, [torch.arange(n, device="cuda").expand(H_kv, n) for n in lens]  # own positions of the cached rows
+    seq_lens = ints(lens)
+    dsa.grouped_append(gd, rows(pos, H_kv), rows(pos, H_kv), table, seq_lens, c.k, c.ks, c.v, c.vs, starts(lens), ws=ws)
+    w = torch.rand((2, H_kv, c.width * 64), device="cuda")
+    new_table = c.table[:, -4:-2].contiguous()
+    kept, seq_lens, w = dsa.grouped_evict(gd, w, keep, table, seq_lens, new_table, c.k, c.ks, c.v, c.vs, sink=2, recent=8, ws=ws)
+    assert seq_lens.tolist() == [keep, keep]
+    at = [kept[b].long() for b in range(2)]
+    gd = dsa.grouped_dims(type, 2, new_table.shape[1], c.blocks, H, H_kv, d, d)
+    for step in range(3):
+        own = [n + step for n in lens]
+        seq_lens += 1
+        at = [torch.cat([a, torch.full((H_kv, 1), p, device="cuda")], 1) for a, p in zip(at, own)]
+        x = rows(own, H_kv)
+        dsa.grouped_append(gd, x, x, new_table, seq_lens, c.k, c.ks, c.v, c.vs, ws=ws)
+        got = torch.zeros_like(w)
+        dsa.grouped_attn(gd, rows(own, H), c.k, c.ks, c.v, c.vs, new_table, seq_lens, sm, weights_out=got, ws=ws)
+        assert dsa.read_error(ws) == 0
+        for b in range(2):
+            want = torch.softmax(sm * torch.cos((own[b] - at[b]).double()), -1) * (H // H_kv)
+            # a cached element was rounded three times at most, each by 2^-4 of it (or a step of the smallest codes, 2^-10 of a scale
+            # of 1 / 448), after bf16's 2^-8: a logit is off by 2 * 0.2, and the sum with it
+            off = (got[b, :, :want.shape[1]].double() / want).log().abs().max()
+            assert float(off) <= 2 * sm * 0.2, (step, b, float(off))
