@@ -404,7 +404,9 @@ dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, i
  * DSA_F32: both with 24 bits, small weights with an error of 2^-30 of the largest. That holds whatever the blocks' value
  * scales are, within 2^60 of each other. Sums keep fp32. The result of a call does not depend on timing.
  * ws: at least dsa_grouped_workspace_size(dims, T, weights wanted) bytes, 256-byte aligned, initialised with
- * dsa_workspace_init.
+ * dsa_workspace_init. With weights it holds the logits, 4 bytes for each query row and position of max_blocks * 64: 268 MB
+ * for 32 single tokens of 64 / 8 heads with 32K positions each. Rows are counted in items of 8, 16, 32 or 64 of a key head
+ * (about as many as a sequence has), so few heads a key head cost as much as 8.
  */
 size_t dsa_grouped_workspace_size(const dsa_grouped_dims* dims, int32_t T, int32_t weights);
 dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t q_stride_t, int64_t q_stride_h,

@@ -511,8 +511,10 @@ static GroupedLayout grouped_layout(const dsa_grouped_dims& d, int T, bool weigh
     const int64_t G = d.H / d.H_kv;
     w.row_tile = grouped_row_tile(d, T);
     w.ctas = grouped_ctas(d);
-    // every sequence fills whole items but its last
-    w.max_tiles = (T * G / w.row_tile + d.B) * d.H_kv * ((d.max_blocks + 1) / 2);
+    // Items of a key head: every sequence with rows fills whole ones but its last, which may hold a single row; where a token's
+    // heads fill whole items, all are full.
+    const int64_t some = T < d.B ? T : d.B, last = G % w.row_tile ? some * (w.row_tile - 1) : 0;
+    w.max_tiles = (T * G + last) / w.row_tile * d.H_kv * ((d.max_blocks + 1) / 2);
     size_t off = 256;  // the error word
     const size_t slot_rows = static_cast<size_t>(2) * w.ctas * w.row_tile;
     w.part_ml = off;

@@ -1,6 +1,7 @@
 """Refusals of the grouped-head calls, before anything is launched (no GPU needed)."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -150,3 +151,35 @@ def test_binding_refusals(L):
         dsa.grouped_evict(d, w, 64, table, lens, table[:1], cache, sc, cache, sc, ws=ws)
     with pytest.raises(ValueError, match="dims"):
         dsa.grouped_workspace(_raw(H=7), 2)
+
+
+def _row_tile(d, T):
+    """Rows of an item: as many as the average sequence has for a key head, in powers of two."""
+    rows, tile = -(-T // d.B) * (d.H // d.H_kv), 8
+    while tile < rows and tile < (16 if d.type == 0 or d.d_v > 128 else 32 if d.d_qk > 128 else 64):
+        tile *= 2
+    return tile
+
+
+def test_workspace_of_the_weights(L):
+    """Room for the logits of every item that T rows in B sequences can make, and no more; never less for more rows."""
+    size = lambda d, T, w=0: L.dsa_grouped_workspace_size(ctypes.byref(d), T, w)  # noqa: E731
+    d = _dims(B=32, max_blocks=512, H=64, H_kv=8, num_blocks=64)
+    logits = 32 * 8 * 256 * 8 * 128 * 4  # sequences, key heads, tiles, heads of a group, positions, bytes
+    assert logits <= size(d, 32, 1) - size(d, 32) <= logits + 4 * 32 * 64 + 1024
+    d = _dims(B=64, max_blocks=512, H=32, H_kv=32, num_blocks=64)
+    assert size(d, 64, 1) - size(d, 64) <= 64 * 32 * 256 * 8 * 128 * 4 + 4 * 64 * 32 + 1024
+    rng = random.Random(1)
+    for _ in range(300):
+        H_kv = rng.choice([1, 2, 8])
+        d = _dims(type=rng.choice(["f32", "bf16"]), B=rng.choice([1, 2, 5, 40]), max_blocks=rng.choice([1, 2, 9]), H_kv=H_kv,
+                  H=H_kv * rng.choice([1, 3, 5, 8, 12, 16, 64, 130]), d_qk=rng.choice([64, 192]), d_v=rng.choice([64, 192]))
+        T = rng.randint(1, 4 * d.B)
+        cuts = sorted(rng.randint(0, T) for _ in range(d.B - 1))
+        G, tile = d.H // d.H_kv, _row_tile(d, T)
+        items = sum(-(-n * G // tile) for n in (b - a for a, b in zip([0] + cuts, cuts + [T])))
+        room = size(d, T, 1) - size(d, T)
+        assert room >= items * tile * d.H_kv * ((d.max_blocks + 1) // 2) * 512 + 4 * T * d.H, (d.B, T, G, tile)
+        for w in (0, 1):
+            sizes = [size(d, n, w) for n in range(T + 1)]
+            assert sizes == sorted(sizes)
