@@ -18,7 +18,7 @@
 // Softmax: weights are formed against a row's reference m, its maximum when that was last looked at. As long as no logit of
 // a tile passes m by more than 4 (in powers of two) the weights stay below 2^4 and are kept as they are; else m moves to the
 // maximum, O^T and the sums are multiplied by 2^(m_old - m), and the tile's weights are formed again. So most tiles need no
-// maxima across lanes, and no tile's weights wait for them: the warps exchange one flag, read after the weights are
+// maxima across lanes, and no tile's weights wait for them: the warps exchange one flag at a barrier after the weights are
 // written (drafts of 16 x 4 147 us with maxima in every tile, 121 without). The block's value scale is a factor of the
 // weights, 1 .. 16 times: it stands against a power of two that the loads' warp chooses by the scales of 32 blocks at a time,
 // 16^-i of it for smaller ones. Where that power changes, O^T is multiplied by the old one over the new (exactly); where it
@@ -882,11 +882,9 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         s[r + 1] = fmaf(s[r + 1], g.z, g.w);
                         over = fmaxf(over, fmaxf(s[r], s[r + 1]));
                     }
-                    if (!sure) {  // the others' word is waited for when the weights are done
+                    if (!sure) {  // (read by the others when they all have their weights)
                         const bool up = __any_sync(0xFFFFFFFFu, over > kSlack);
                         if (lane == 0) flag[quarter] = up;
-                        __syncwarp();
-                        asm volatile("barrier.arrive %0, 256;" ::"r"(1 + kSets * kGroups + mates) : "memory");
                     }
                     const float tv = here ? sc.y : 0.0f;
                     const uint32_t p_buf = sP + (n & (F::kPB - 1)) * F::kPBytes + j * 16;
@@ -917,7 +915,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         }
                     }
                     if (!sure) {
-                        named_bar_sync(1 + kSets * kGroups + mates, 256);  // (its other 128 arrivals were those above)
+                        __syncwarp();
+                        group_sync();
                         const uint4 u = *reinterpret_cast<const uint4*>(flag);
                         if (u.x | u.y | u.z | u.w) {
                             move = true;
