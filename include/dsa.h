@@ -392,11 +392,11 @@ dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, i
  * Attention over the cache: query i of a sequence's n sees its positions s <= seq_lens[b] - n + i,
  *   z = sm_scale * q . k_s,  out = sum softmax(z)_s v_s,  lse = ln sum exp(z_s).
  *   q    [T][H][d_qk]; out [T][H][d_v] in q's type and lse [T][H] fp32 (may be NULL), dense. A query that sees no
- *        position gives out = 0, lse = -inf.
+ *        position gives out = 0, lse = -inf. Neither may overlap an input.
  *   weights, weights_out  [B][H_kv][max_blocks * 64] fp32, both NULL or weights_out given: the attention weight of every
  *        position, summed over the sequence's queries and the query heads of its key head, is added to weights
- *        (NULL: to 0; it may be weights_out itself) and written to weights_out for the positions below seq_lens[b];
- *        the others stay as they were.
+ *        (NULL: to 0; it may be weights_out itself, but not overlap it otherwise) and written to weights_out for the
+ *        positions below seq_lens[b]; the others stay as they were.
  * Positions in invalid blocks are left out and reported. What unused slots of a block hold does not matter, NaN codes
  * included. A query of NaN or infinities gives a row of NaN (and NaN weights); other inputs are finite. sm_scale > 0.
  * DSA_BF16: queries enter the products exactly but for elements below 2^-13 of their row's largest (an absolute error of
@@ -423,8 +423,9 @@ dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t
  * A sequence of up to `keep` positions is copied as it is.
  *   weights [B][H_kv][max_blocks * 64] fp32, only read
  *   kept [B][H_kv][keep]  int32 out: the kept positions, ascending, then -1
- *   new_lens [B]          int32 out: min(seq_len, keep); neither seq_lens nor anything else read here
- *   weights_out [B][H_kv][new_max_blocks * 64]  fp32 out: the kept weights, then zeros; not weights itself
+ *   new_lens [B]          int32 out: min(seq_len, keep)
+ *   weights_out [B][H_kv][new_max_blocks * 64]  fp32 out: the kept weights, then zeros
+ * The three outputs overlap nothing that is read here (weights and seq_lens in particular), nor each other.
  * New blocks are distinct from every block that the call reads, but that a sequence which is not cut may keep its own
  * blocks (an entry equal to the old one is left alone). keep <= new_max_blocks * 64; sink, recent >= 0, together at
  * most keep. What was kept goes on as a sequence of new_lens positions in new_table (with max_blocks = new_max_blocks, also

@@ -496,6 +496,16 @@ static bool ws_ok(const void* ws, size_t ws_bytes, size_t need) {
     return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && ws_bytes >= need;
 }
 
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+// Bytes of the weights of `blocks` blocks a sequence.
+static size_t weights_bytes(const dsa_grouped_dims& d, int blocks) {
+    return sizeof(float) * static_cast<size_t>(d.B) * d.H_kv * blocks * kBlock;
+}
+
 // The arrivals stand behind the error word, in the 256 bytes that dsa_workspace_init clears and no other call writes.
 constexpr size_t kGroupedArrived = 16;
 
@@ -998,6 +1008,8 @@ dsa_status dsa_grouped_attn(const dsa_grouped_dims* dims, const void* q, int64_t
         return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     if (weights && !weights_out) return DSA_ERR_INVALID_ARG;
+    const size_t w_bytes = weights_bytes(*dims, dims->max_blocks);
+    if (weights != weights_out && overlap(weights, w_bytes, weights_out, w_bytes)) return DSA_ERR_INVALID_ARG;
     const GroupedLayout L = grouped_layout(*dims, T, weights_out != nullptr);
     if (!ws_ok(ws, ws_bytes, L.total)) return DSA_ERR_WORKSPACE;
     int launches = 0;
@@ -1060,7 +1072,10 @@ dsa_status dsa_grouped_evict(const dsa_grouped_dims* dims, const float* weights,
     if (!weights || !block_table || !seq_lens || !new_table || !k_cache || !k_scale || !v_cache || !v_scale || !kept ||
         !new_lens || !weights_out)
         return DSA_ERR_INVALID_ARG;
-    if (weights == weights_out || seq_lens == new_lens) return DSA_ERR_INVALID_ARG;
+    const size_t lens_bytes = sizeof(int32_t) * dims->B;
+    if (overlap(weights, weights_bytes(*dims, dims->max_blocks), weights_out, weights_bytes(*dims, new_max_blocks)) ||
+        overlap(seq_lens, lens_bytes, new_lens, lens_bytes))
+        return DSA_ERR_INVALID_ARG;
     if (!aligned16(k_cache) || !aligned16(v_cache)) return DSA_ERR_INVALID_ARG;
     if (!ws_ok(ws, ws_bytes, 256)) return DSA_ERR_WORKSPACE;
     int launches = 0;

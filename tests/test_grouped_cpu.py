@@ -183,3 +183,18 @@ def test_workspace_of_the_weights(L):
         for w in (0, 1):
             sizes = [size(d, n, w) for n in range(T + 1)]
             assert sizes == sorted(sizes)
+
+
+def test_overlapping_outputs_are_refused(L):
+    """Weights and lengths that are written while others still read them, by whatever part of them."""
+    at = lambda n: ctypes.c_void_p((1 << 20) + n)  # noqa: E731
+    size = 4 * 2 * 2 * 4 * 64  # bytes of the weights of 2 sequences, 2 heads and 4 blocks
+    for off in (256, size - 256, -256, -size // 2 + 256):  # (the new ones have 2 blocks)
+        assert _evict(L, wo=at(off)) == 1, off
+    assert _evict(L, new_lens=at(4)) == 1 and _evict(L, new_lens=at(-4)) == 1
+    for off in (256, size - 256, -256, 256 - size):
+        assert _attn(L, w=FAKE, wo=at(off)) == 1, off
+    for off in (0, size, -size):  # itself, or beside it: up to the workspace, which is too small
+        assert _attn(L, w=FAKE, wo=at(off), nbytes=0) == 3, off
+    assert _evict(L, wo=at(size), nbytes=0) == 3 and _evict(L, wo=at(-size // 2), nbytes=0) == 3 and _evict(L, new_lens=at(8), nbytes=0) == 3
+    assert L.dsa_last_launch_count() == 0
