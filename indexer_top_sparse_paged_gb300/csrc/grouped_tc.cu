@@ -37,6 +37,7 @@
 // item's queries. 12 warps leave 168 registers a thread; more, of fewer rows or with spills, were slower but for 64 rows.
 // An item's end costs about 4 us of the products' and the softmax's latencies: 128 sequences of 1024 take 100 us where the
 // bytes take 40, of 16K and more a tenth above them.
+#include <cfloat>
 #include <cstddef>
 
 #include "grouped.cuh"
@@ -407,7 +408,9 @@ __device__ __forceinline__ void split_queries(const GroupedArgs& a, const Groupe
         // 2^-e takes the largest element into (224, 448]; a query that is not finite becomes codes of NaN
         const bool fine = top < 0x7F800000u;
         const int e = !fine ? 0 : max(static_cast<int>(top >> 23) - 127 - 8, -120) + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        if (lane == 0) S.q_factor[qb][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.sm_scale * 1.4426950408889634f);
+        // (finite and not 0: a position that is not seen has the logit -inf, and 0 times it were NaN)
+        const float factor = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.sm_scale * 1.4426950408889634f);
+        if (lane == 0) S.q_factor[qb][r] = fminf(fmaxf(factor, 0x1p-126f), FLT_MAX);
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         uint32_t parts[4][F::kQP];
 #pragma unroll

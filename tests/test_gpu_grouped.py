@@ -247,6 +247,19 @@ def test_queries_of_nan_and_infinity(type):
 
 
 @pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-10, 1e30, 3e38])
+def test_queries_of_zeros_and_tiny_ones(type, scale):
+    """Logits of 0, whatever the scale: the mean of what is seen, also where a tile holds positions that are not."""
+    c = Cache([200, 3, 128], 8, 2, 32, 32, type, seed=18)
+    new = [3, 1, 1]
+    q = torch.zeros((5, 8, 32), dtype=ACT[type], device="cuda")
+    if scale < 1:
+        q[:, 1] = 1e-30  # a logit far below 2^-126
+    w = torch.zeros((3, 2, c.width * 64), device="cuda")
+    check(c, q, new, attend(c, q, new, scale, weights_out=w), scale, None, w)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
 def test_invalid_blocks_and_sequences(type):
     c = Cache([700, 300, 130], 8, 2, 64, 64, type, seed=8)
     q = c.queries(3)
