@@ -5,11 +5,11 @@
 // core's cost here goes with the cached rows, not with the few query rows: a query row is split into e4m3 parts of 4
 // significand bits,
 //   t = q 2^-e,  t = t_0 + t_1 / 16 + t_2 / 256 + ...,  t_i = e4m3(16^i * what is left),
-// and so are the weights, their last part in units of 1/256 of the one before. Two parts hold a bf16 query exactly (elements
-// below 2^-13 of its largest keep an absolute error of 2^-21 of that), six parts hold fp32. Four parts hold a weight that was
-// rounded to fp16 exactly down to 2^-12, in what it is split in (a row's largest weight is 1 there, or more); smaller ones
-// are off by 2^-23, those below 2^-20 by fp16's 2^-25 alone (with 1/16: 2^-22 for all). With the cached rows as the M side
-// of both products the parts are extra columns:
+// and so are the weights, in steps of 32 (what rounding leaves is half a step at most and has a sign, so a part is worth 5
+// bits; queries go up to 448, where 32 times that half step would leave the codes' range). Two parts hold a bf16 query exactly
+// (elements below 2^-13 of its largest keep an absolute error of 2^-21 of that), four parts every fp16 number up to 256, to
+// which a weight is rounded (in steps of 16 small ones would be off by 2^-22, fp16's rounding is by 2^-25), six parts fp32 (small
+// weights with an absolute error of 2^-35). With the cached rows as the M side of both products the parts are extra columns:
 //   S^T [128 positions x (parts * rows)] = K tile [128 x d_qk] . Q^T,   K-major, from shared memory as TMA wrote it
 //   O^T [d_v x (parts * rows)] += V tile^T [d_v x 128] . P^T,            MN-major: the same row layout read the other way
 // (M = 128, N = 16 .. 256), 32 bytes of K a step: 46 cycles each up to N = 64, 128 at N = 256. Position = TMEM lane: a
@@ -20,8 +20,8 @@
 // maximum, O^T and the sums are multiplied by 2^(m_old - m), and the tile's weights are formed again. So most tiles need no
 // maxima across lanes, and no tile's weights wait for them: the warps exchange one flag at a barrier after the weights are
 // written (drafts of 16 x 4 147 us with maxima in every tile, 121 without). The block's value scale is a factor of the
-// weights, 1 .. 16 times: it stands against a power of two that the loads' warp chooses by the scales of 32 blocks at a time,
-// 16^-i of it for smaller ones. Where that power changes, O^T is multiplied by the old one over the new (exactly); where it
+// weights, 1/4 .. 16 times: it stands against a power of two that the loads' warp chooses by the scales of 32 blocks at a time,
+// 64^-i of it for smaller ones. Where that power changes, O^T is multiplied by the old one over the new (exactly); where it
 // changes within a tile, the blocks take turns: weights of the first, its products, O^T moved, weights of the second. So a
 // block with a large scale, be it of zeros, takes no bits from the light weights of others.
 //
@@ -49,7 +49,7 @@ constexpr int kChunk = 64 * 128;  // bytes of one block's 128 columns of codes
 constexpr int kMaxStages = 6;
 constexpr float kSlack = 4.0f;  // a weight is 2^kSlack at most,
 constexpr float kTop = 16.0f;   // and kTop * 2^kSlack = 256 as it is split into codes (which end at 448)
-constexpr int kLastPart = 256;  // a weight's last part against the one before it
+constexpr int kQStep = 16, kPStep = 32;  // a part of a query, and of a weight, against the next
 constexpr int kLeastRef = 27;   // exponents (127: of 1) of what value scales refer to: the least,
 constexpr int kRefRange = 60;   // and how far they fall below an item's largest
 constexpr size_t kSmemLimit = 232448;
@@ -211,24 +211,23 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
     return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3));
 }
 
-// Splits two values (magnitudes up to 448) into kParts pairs of codes, each part in units of 1/16 of the one before and the
-// last of 1/kLast. bf16 calls split fp16 values: exact differences.
-template <int kParts, int kLast>
+// Splits two values (magnitudes up to 448) into kParts pairs of codes. bf16 calls split fp16 values: exact differences.
+template <int kStep, int kParts>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&parts)[kParts]) {
     if constexpr (kParts <= 4) {
         __half2 t = __floats2half2_rn(a, b);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             parts[i] = cvt_e4m3x2(t);
-            if (i + 1 < kParts) t = __hmul2(__hsub2(t, half2_of(parts[i])), __float2half2_rn(i + 2 < kParts ? 16.0f : kLast));
+            if (i + 1 < kParts) t = __hmul2(__hsub2(t, half2_of(parts[i])), __float2half2_rn(kStep));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             parts[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
             const float2 f = __half22float2(half2_of(parts[i]));
-            a = (a - f.x) * (i + 2 < kParts ? 16.0f : kLast);
-            b = (b - f.y) * (i + 2 < kParts ? 16.0f : kLast);
+            a = (a - f.x) * kStep;
+            b = (b - f.y) * kStep;
         }
     }
 }
@@ -306,7 +305,7 @@ __device__ __forceinline__ void load_logits(uint32_t addr, float scale, float (&
     for (int r = 0; r < kRW; ++r) {
         s[r] = x[(kQP - 1) * kRW + r];
 #pragma unroll
-        for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 0.0625f, x[i * kRW + r]);
+        for (int i = kQP - 2; i >= 0; --i) s[r] = fmaf(s[r], 1.0f / kQStep, x[i * kRW + r]);
         s[r] *= scale;
     }
 }
@@ -320,7 +319,7 @@ __device__ __forceinline__ void join_parts(uint32_t addr, float (&y)[8]) {
         float o[8];
         load_columns<8>(addr + i * kStep, o);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) y[r] = fmaf(y[r], i == kPP - 2 ? 1.0f / kLastPart : 0.0625f, o[r]);
+        for (int r = 0; r < 8; ++r) y[r] = fmaf(y[r], 1.0f / kPStep, o[r]);
     }
 }
 
@@ -414,7 +413,7 @@ __device__ __forceinline__ void split_queries(const GroupedArgs& a, const Groupe
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         uint32_t parts[4][F::kQP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_pair<F::kQP, 16>(x[2 * i] * down, x[2 * i + 1] * down, parts[i]);
+        for (int i = 0; i < 4; ++i) split_pair<kQStep>(x[2 * i] * down, x[2 * i + 1] * down, parts[i]);
         if (col >= kc * 128) continue;
         const int nrow = (r / F::kRW) * (F::kQP * F::kRW) + r % F::kRW, c16 = (col & 127) >> 4;
         const uint32_t to = dst + (col >> 7) * F::kQBytes + nrow * 128 + ((c16 ^ (nrow & 7)) << 4) + (col & 8);
@@ -533,7 +532,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             int row, row_next;
             float ks, vs, ks_next, vs_next;
             // What the weights of 32 blocks refer their value scales to: a power of two no smaller than any of them, kept from
-            // before unless it is 4 times too large, or 16^-i of it for a scale that is 16^i times smaller or more. So a block's
+            // before unless it is 4 times too large, or 64^-i of it for a scale that is 64^i times smaller or more. So a block's
             // weights keep their bits whatever the scales of others are, and O^T is seldom moved to another power (which loses
             // nothing, as long as they stay within 2^kRefRange of an item's largest).
             int unit = 0, most = 0;
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const int top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(e)));
                 if (top > unit || top + 2 <= unit) unit = top;
                 most = max(most, unit);
-                const int mine = max(max(unit - ((unit - e) & ~3), most - kRefRange), kLeastRef);
+                const int mine = max(max(unit - (unit - e) / 6 * 6, most - kRefRange), kLeastRef);
                 vs = __uint_as_float(bits) * __uint_as_float(static_cast<uint32_t>(258 - mine) << 23);  // kTop / 2^(mine - 127)
                 const int next = __shfl_down_sync(0xFFFFFFFFu, mine, 1);
                 const bool next_there = __shfl_down_sync(0xFFFFFFFFu, there, 1);
@@ -900,7 +899,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                             const int r = r0 + 2 * i;
                             s[r] = ex2(s[r]);
                             s[r + 1] = ex2(s[r + 1]);
-                            split_pair<F::kPP, kLastPart>(s[r] * tv, s[r + 1] * tv, parts[i]);
+                            split_pair<kPStep>(s[r] * tv, s[r + 1] * tv, parts[i]);
                         }
 #pragma unroll
                         for (int i = 0; i < F::kPP; ++i) {
