@@ -362,7 +362,8 @@ dsa_status dsa_prompt_attn(const dsa_prompt_dims* dims, const void* q, const voi
  *                Rows at and past cu[B] are not read as values and not written.
  *   strides      of q, k_new and v_new in elements (token, head): multiples of 16 bytes, 0 or more; columns dense
  * A sequence whose cu entries descend or leave [0, T], or whose seq_lens entry leaves [0, max_blocks * 64], is
- * skipped by the append, has no positions in the attention and counts as empty in the eviction (DSA_FAULT_INDEX).
+ * skipped by the append, has no positions in the attention and counts as empty in the eviction (DSA_FAULT_INDEX). Where cu
+ * descends, others may come to share rows: what these get is not defined.
  */
 typedef struct {
     int32_t type;
@@ -402,7 +403,7 @@ dsa_status dsa_grouped_append(const dsa_grouped_dims* dims, const void* k_new, i
  * DSA_BF16: queries enter the products exactly but for elements below 2^-13 of their row's largest (an absolute error of
  * 2^-21 of that), softmax weights with 11 significant bits, small ones with an error of 2^-22 of their row's largest weight;
  * DSA_F32: both with 24 bits, small weights with an error of 2^-30 of the largest. That holds whatever the blocks' value
- * scales are, within 2^60 of each other. Sums keep fp32. The result of a call does not depend on timing.
+ * scales are, within 2^60 of each other and above 2^-100. Sums keep fp32. The result of a call does not depend on timing.
  * ws: at least dsa_grouped_workspace_size(dims, T, weights wanted) bytes, 256-byte aligned, initialised with
  * dsa_workspace_init. With weights it holds the logits, 4 bytes for each query row and position of max_blocks * 64: 268 MB
  * for 32 single tokens of 64 / 8 heads with 32K positions each. Rows are counted in items of 8, 16, 32 or 64 of a key head
