@@ -400,6 +400,27 @@ def test_two_hundred_calls_in_a_row(type, d, G, new):
     assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G,new", [(8, 1), (8, 2), (8, 4), (8, 8)])
+def test_two_hundred_calls_with_scales_apart(type, d, G, new):
+    """Tiles whose blocks take turns among others: no wait runs out, and the last call has the bits of the first, which are right."""
+    lens = [300 + 500 * b for b in range(10)]
+    c = Cache(lens, 8 * G, 8, d, d, type, seed=d + new, room=[n + 8 for n in lens])
+    c.vs *= torch.exp2(4.0 * torch.randn(c.vs.shape, generator=c.g, device="cuda"))
+    q = c.queries(10 * new)
+    w = torch.zeros((10, 8, c.width * 64), device="cuda")
+    ws = dsa.grouped_workspace(c.dims(), 10 * new, weights=True)
+    cu = starts([new] * 10)
+    out, lse = dsa.grouped_attn(c.dims(), q, *c.args(), d ** -0.5, cu, weights_out=w, ws=ws)
+    first = out.clone(), lse.clone(), w.clone()
+    for _ in range(200):
+        dsa.grouped_attn(c.dims(), q, *c.args(), d ** -0.5, cu, out=out, lse=lse, weights_out=w, ws=ws)
+    assert dsa.read_error(ws) == 0
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1]) and torch.equal(w, first[2])
+    check(c, q, [new] * 10, first[:2], d ** -0.5, None, w)
+
+
 def test_weights_of_many_sequences():
     lens = [(i * 53) % 300 for i in range(300)]
     c = Cache(lens, 6, 2, 16, 16, seed=14)
@@ -956,3 +977,56 @@ def test_rotation_goes_on_over_an_eviction(type):
             # of 1 / 448), after bf16's 2^-8: a logit is off by 2 * 0.2, and the sum with it
             off = (got[b, :, :want.shape[1]].double() / want).log().abs().max()
             assert float(off) <= 2 * sm * 0.2, (step, b, float(off))
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_two_graphs_share_a_workspace(type):
+    """A decode step (append, attention, weights) and an eviction, captured apart with one workspace, replayed in turn on new
+    inputs: what the same calls give one by one."""
+    H, H_kv, d, keep = 8, 2, 64, 300
+    c = Cache([900, 40, 2000], H, H_kv, d, d, type, seed=52, room=[1000, 1000, 2100])
+    c.vs *= torch.exp2(4.0 * torch.randn(c.vs.shape, generator=c.g, device="cuda"))
+    gd, ws = c.dims(), dsa.grouped_workspace(c.dims(), 3, weights=True)
+    to = (c.blocks + torch.arange(15, device="cuda")).to(torch.int32).view(3, 5)
+    for name in ("k", "v", "ks", "vs"):
+        t = getattr(c, name)
+        setattr(c, name, torch.cat([t, t[:15]]))
+    gd.num_blocks += 15
+    x = [c.queries(3)[:, :H_kv].contiguous() for _ in range(2)]
+    q, w = c.queries(3), torch.rand((3, H_kv, c.width * 64), device="cuda")
+    kept, lens, left = torch.empty((3, H_kv, keep), dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty((3, H_kv, 320), device="cuda")
+    out, lse = torch.empty((3, H, d), dtype=ACT[type], device="cuda"), torch.empty((3, H), device="cuda")
+
+    def step():
+        dsa.grouped_append(gd, *x, c.table, c.seq_lens, c.k, c.ks, c.v, c.vs, ws=ws)
+        dsa.grouped_attn(gd, q, *c.args(), 0.125, weights=w, out=out, lse=lse, ws=ws)
+
+    def evict():
+        dsa.grouped_evict(gd, w, keep, c.table, c.seq_lens, to, c.k, c.ks, c.v, c.vs, sink=4, recent=30, kept=kept, new_lens=lens, weights_out=left, ws=ws)
+
+    state = [c.k, c.ks, c.v, c.vs, w, out, lse, kept, lens, left]
+    graphs, side = [torch.cuda.CUDAGraph() for _ in range(2)], torch.cuda.Stream()
+    step(), evict()  # (what a first call sets up)
+    torch.cuda.synchronize()
+    for g, call in zip(graphs, (step, evict)):
+        with torch.cuda.graph(g, stream=side):
+            call()
+    torch.cuda.synchronize()
+    start = [t.clone() for t in state]
+    for turn in range(3):
+        q.copy_(c.queries(3))
+        for t in x:
+            t.copy_(c.queries(3)[:, :H_kv])
+        c.seq_lens += 1
+        for t, s in zip(state, start):
+            t.copy_(s)
+        step(), evict()
+        want = [t.clone() for t in state]
+        for t, s in zip(state, start):
+            t.copy_(s)
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert all(same(t, s) for t, s in zip(state, want)), turn
+        start = want
+    assert dsa.read_error(ws) == 0 and not ws[:256].any()
