@@ -35,6 +35,9 @@
 // ring allows, whatever items it crosses; one warp issues the products, the values' as soon as their weights are there
 // (d = 256, where the ring has 3 stages: 134 us when they stood behind the next keys', 102 so); two warps bring the next
 // item's queries. 12 warps leave 168 registers a thread; more, of fewer rows or with spills, were slower but for 64 rows.
+// The roles' loops drive each other out of the instruction cache, so what runs once or twice a tile is not unrolled (loops
+// over the chunks of 128 columns, left to the compiler, made the code half again as long: 2 rows a token 82 us, so 102; the
+// keys' products are, as their issue is what the decode batch waits for: 254 us, rolled 267).
 // An item's end costs about 4 us of the products' and the softmax's latencies: 128 sequences of 1024 take 100 us where the
 // bytes take 40, of 16K and more a tenth above them.
 #include <cfloat>
@@ -565,10 +568,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (lane == 0) {
                     const uint32_t n = (r0 >= 0 ? 1 : 0) + (r1 >= 0 ? 1 : 0);
                     if (n) mbar_expect_tx(bar, n * (kc + vc) * kChunk);
+#pragma unroll 1
                     for (int c = 0; c < kc; ++c) {
                         if (r0 >= 0) tma_load_2d(dst + 2 * c * kChunk, &map_k, c * 128, r0 * kBlock, bar);
                         if (r1 >= 0) tma_load_2d(dst + (2 * c + 1) * kChunk, &map_k, c * 128, r1 * kBlock, bar);
                     }
+#pragma unroll 1
                     for (int c = 0; c < vc; ++c) {
                         if (r0 >= 0) tma_load_2d(dst + v_off + 2 * c * kChunk, &map_v, c * 128, r0 * kBlock, bar);
                         if (r1 >= 0) tma_load_2d(dst + v_off + (2 * c + 1) * kChunk, &map_v, c * 128, r1 * kBlock, bar);
@@ -600,6 +605,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         int st = 0, phase = 0, st_v = 0, n = 0, done = 0, item = 0;  // tiles whose logits, whose values were issued
         int last = 0;  // first tile of the item before
         uint32_t first = 0;  // bit n % 32: tile n is the first of its item in its set
+        uint32_t turns = 0;  // and bit n % 32: its blocks take turns
         uint32_t came = 0;   // bit b: the phase of p_full[b] to wait for
         bool half = false;   // tile `done` has scales far apart, and its first block's values were issued
         bool ok = true;
@@ -610,8 +616,9 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             if (!ok) return;
             tc_fence_after();
             came ^= 1u << buf;
-            half = !half && (S.refs[st_v] & 4);
+            half = !half && (turns >> (done & 31) & 1);
             const bool fresh = (first >> (done & 31)) & 1;
+#pragma unroll 1
             for (int c = 0; c < vc; ++c) {
                 const uint64_t da = sw128_desc(sRing + st_v * stage_bytes + v_off + 2 * c * kChunk, 0, 1024);
                 const uint64_t db = plain_desc(sP + buf * F::kPBytes, 128, 2048);
@@ -674,6 +681,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 if (tile + 1 == tiles) warp_tc_commit(smem_u32(&S.q_empty[qb]));
                 const uint32_t bit = 1u << (n & 31);
                 first = tile < kSets ? first | bit : first & ~bit;
+                turns = S.refs[st] & 4 ? turns | bit : turns & ~bit;
                 ++n;
                 if (++st == stages) st = 0, phase ^= 1;
             }
@@ -748,9 +756,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         float* fac = S.fac[warp];
         const int mates = set * kGroups + group;
         int n = set, n_item = 0, st = set, sphase = 0, item = 0, turn = 0, left = 0, asked = 0;  // n: this set's next tile, n_item: the item's first
-        uint32_t sent = ~0u;  // bit b: the phase of pv_done[b] that ends with the products of what was last put in buffer b
-        int round = 0;        // 1: of a tile with scales far apart, the second block
-        bool ok = true;
+        uint32_t sent = ~0u;  // bit b: the phase of pv_done[b] that ends with the products of what was last put in buffer b;
+        bool ok = true;       // bit 31: 0 while the second block of a tile whose blocks take turns is dealt with
         // The group's four warps meet at a barrier of the hardware, at which they sleep (asking a barrier in memory again and
         // again, four warps slow each other: 2 rows a token 108 us, so 92). Only the first warp waits for other roles, with
         // its limit; the others take its word, so that all of them go on or none does.
@@ -798,13 +805,16 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 });
                 if (!ok) break;
                 tc_fence_after();
+                const int round = sent >> 31 ^ 1;
                 const float2 sc = S.scales[st][quarter >> 1];
                 const uint32_t refs = S.refs[st];
                 const int valid = refs & 7, pos = tile * kGroupedTile + j;
                 const bool there = valid >> (quarter >> 1) & 1 && pos < len, whole = valid == 3 && (tile + 1) * kGroupedTile <= all_see;
                 // blocks with scales far apart take turns
-                const bool mine = !(valid & 4) || (quarter >> 1) == round, here = there && mine;
+                auto turns_now = [&]() { return *static_cast<volatile uint32_t*>(&S.refs[st]) & 4; };
+                const bool here = there && (!(valid & 4) || (quarter >> 1) == round);
                 if (!whole && group == 0 && !there && !round) {  // what the slot holds must not reach the products: 0 * NaN is NaN
+#pragma unroll 1
                     for (int c = 0; c < vc; ++c) {
                         const uint32_t at = sRing + st * stage_bytes + v_off + 2 * c * kChunk + j * 128;
 #pragma unroll
@@ -855,6 +865,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
 #pragma unroll
                             for (int r = 0; r < kRW; ++r) l[r] *= fac[r];
                             tc_fence_after();
+#pragma unroll 1
                             for (int c = 0; c < vc; ++c) {
 #pragma unroll 1
                                 for (int i = 0; i < F::kPP * kRW; i += 8) {
@@ -870,7 +881,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                         }
                         group_sync();  // the maxima have been read
                     }
-                    if (a.weights_out && mine && it.t + n - n_item < a.max_tiles) {
+                    if (a.weights_out && (!turns_now() || (quarter >> 1) == round) && it.t + n - n_item < a.max_tiles) {
                         float* to = a.z + ((it.t + n - n_item) * kRows + group * kRW) * kGroupedTile + j;
 #pragma unroll
                         for (int r = 0; r < kRW; ++r)
@@ -934,11 +945,14 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 fresh = false;
                 fence_proxy_async_smem();
                 tc_fence_before();
+                const bool turns = turns_now();  // (the stage may be filled again once the weights are out)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&S.p_full[n & (F::kPB - 1)]));
                 sent ^= 1u << (n & (F::kPB - 1));
-                round = valid & 4 ? round ^ 1 : 0;
-                if (round) continue;  // the tile's other block
+                if (turns) {
+                    sent ^= 1u << 31;
+                    if (!round) continue;  // the tile's other block
+                }
                 n += kSets;
                 st += kSets;
                 if (st >= stages) st -= stages, sphase ^= 1;
@@ -988,6 +1002,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const int other = kSets == 1 ? 0 : 1 - set;
                 const bool both = kSets == 2 && S.fin_unit[qb][other] != 0.0f;
                 const float f_own = f[kSets == 1 ? 0 : set] * inv, f_other = f[other] * inv;
+#pragma unroll 1
                 for (int c = 0; c < vc; ++c) {
                     const int e = c * 128 + j;
                     const uint32_t own_col = o_col + (set * F::kVCMax + c) * F::kPN, other_col = o_col + (other * F::kVCMax + c) * F::kPN;
