@@ -5,9 +5,10 @@
 // grown, the earlier codes are rounded anew against it. So a scale only ever grows while a block fills (but for that of
 // nothing but zeros), and codes whose scale stays are not touched.
 //
-// One row a sequence: latency bounds it (32 sequences, 8 heads of 128 and 128: 5.1 us of kernel time, 17 us a call in a
+// One row a sequence: latency bounds it (32 sequences, 8 heads of 128 and 128: 5.2 us of kernel time, 17 - 18 us a call in a
 // stream), which is why a CTA reads its rows once, into registers, and keeps the next on their way. A prompt's many rows: the
-// instructions of rounding (2 x 4096 tokens: 16.9 us; its 50 MB take 7.4; 65% of the issue slots busy).
+// instructions of rounding (2 x 4096 tokens: 17 us; its 50 MB take 7.4; 65% of the issue slots busy; every code is converted
+// twice, so that a value near the middle of two codes is noticed).
 #include "grouped.cuh"
 
 namespace dsa {

@@ -25,9 +25,11 @@
 // changes within a tile, the blocks take turns: weights of the first, its products, O^T moved, weights of the second. So a
 // block with a large scale, be it of zeros, takes no bits from the light weights of others.
 //
-// What bounds it. One row a token and 8 heads a key head (N = 16 and 32): bytes; 32 sequences of 16K - 32K 259 us, 1.55 GB
-// at 6.0 TB/s, 88% of a copy's rate; one of 1M 346 us, 91%. More rows: the softmax's instructions and their latencies, a
-// row at a time (2 rows a token 93 us, 4 112, 8 180 where the bytes take 37). Few bytes: the launch and the items' chains.
+// What bounds it. One row a token and 8 heads a key head (N = 16 and 32): bytes; 32 sequences of 16K - 32K 254 us, 1.55 GB
+// at 6.1 TB/s, 90% of a copy's rate; one of 1M 341 us, 93%. More rows: the softmax's instructions and their latencies, a
+// row at a time (2 rows a token 82 us, 4 107, 8 184 where the bytes take 37). Few bytes: the launch and the items' chains.
+// Scales that vary by two powers of two from block to block (standard deviation), where every other tile's blocks take turns:
+// the decode batch 388 us; by one power 260.
 // A tile's chain logits -> weights (about 1500 cycles) is longer than its bytes take (1400), so two sets of warps take
 // tiles in turn, each with a maximum, a sum and an O^T of its own, and the set with an item's last tile puts the two
 // together; where rows fill the warps of both, one set of kGroups warpgroups shares a tile's rows (see the forms below).
@@ -38,8 +40,8 @@
 // The roles' loops drive each other out of the instruction cache, so what runs once or twice a tile is not unrolled (loops
 // over the chunks of 128 columns, left to the compiler, made the code half again as long: 2 rows a token 82 us, so 102; the
 // keys' products are, as their issue is what the decode batch waits for: 254 us, rolled 267).
-// An item's end costs about 4 us of the products' and the softmax's latencies: 128 sequences of 1024 take 100 us where the
-// bytes take 40, of 16K and more a tenth above them.
+// An item's end costs the products' and the softmax's latencies, which two sets overlap in part: 128 sequences of 1024 take 80
+// us where the bytes take 40, of 16K and more a tenth above them.
 #include <cfloat>
 #include <cstddef>
 
@@ -103,8 +105,8 @@ struct Item {
 };
 
 // Compiled forms: rows of a softmax thread, warpgroups that share a tile's rows, sets that take tiles in turn, parts of a
-// query and of a weight, buffers of logits. (32 rows, drafts of 16 x 4: two warpgroups of 16 rows a thread 115 us; one of 32
-// rows in each of two sets, four of 8 rows, or two of 16 rows in each of two sets 152 - 182.)
+// query and of a weight, buffers of logits. (32 rows, drafts of 16 x 4, when they were tried: two warpgroups of 16 rows a thread
+// 115 us, 106 now; one of 32 rows in each of two sets, four of 8 rows, or two of 16 rows in each of two sets 152 - 182.)
 template <int kRW_, int kGroups_, int kSets_, int kQP_, int kPP_, int kSB_>
 struct Form {
     static constexpr int kRW = kRW_, kGroups = kGroups_, kSets = kSets_, kQP = kQP_, kPP = kPP_, kSB = kSB_;
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
         uint32_t sent = ~0u;  // bit b: the phase of pv_done[b] that ends with the products of what was last put in buffer b;
         bool ok = true;       // bit 31: 0 while the second block of a tile whose blocks take turns is dealt with
         // The group's four warps meet at a barrier of the hardware, at which they sleep (asking a barrier in memory again and
-        // again, four warps slow each other: 2 rows a token 108 us, so 92). Only the first warp waits for other roles, with
+        // again, four warps slow each other: when this was changed, 2 rows a token went from 108 us to 92). Only the first warp waits for other roles, with
         // its limit; the others take its word, so that all of them go on or none does.
         auto group_sync = [&]() { named_bar_sync(1 + mates, 128); };
         auto group_ask = [&](auto wait) {
@@ -1088,9 +1090,9 @@ static bool launch_form(const GroupedArgs& a, cudaStream_t s) {
 
 // Rows of an item: as many as the average sequence of the call has for a key head, in powers of two. Of fp32 queries and
 // of wide values fewer: their parts fill tensor memory (and of wide keys, shared memory). More rows an item read the cache
-// fewer times (16 sequences of 8000 on average, 8 heads of 128, 8 query heads each; us): 16 rows a sequence 123 in items of
-// 8, 93 in one of 16; 32 rows 170 in items of 16, 112 in one of 32; 64 rows 208 in items of 32, 180 in one of 64; fp32, 16
-// rows 159 in items of 8, 95 in one of 16.
+// fewer times (16 sequences of 8000 on average, 8 heads of 128, 8 query heads each; us): 16 rows a sequence 116 in items of
+// 8, 82 in one of 16; 32 rows 145 in items of 16, 107 in one of 32; 64 rows 192 in items of 32, 183 in one of 64; fp32, 16
+// rows 126 in items of 8, 92 in one of 16.
 int grouped_row_tile(const dsa_grouped_dims& d, int T) {
     const int64_t rows = (static_cast<int64_t>(T) + d.B - 1) / d.B * (d.H / d.H_kv);
     const int most = d.type == DSA_F32 || d.d_v > 128 ? 16 : d.d_qk > 128 ? 32 : 64;

@@ -1,7 +1,7 @@
 // After the attention over the grouped-head cache, where they are wanted: the positions' weights, summed from the logits.
 // They need the rows' final sums, so the attention leaves its logits in the workspace (4 bytes a row and position, mostly
 // in L2 still when they are read here: 22 MB of 67 come from memory). Latency of those reads bounds it: 32 sequences of 8K,
-// 8 heads, 8 rows take 12 us beside the attention's 77.
+// 8 heads, 8 rows take 14 us beside the attention's 75 (kernel times).
 #include <type_traits>
 
 #include "grouped.cuh"
