@@ -619,9 +619,17 @@ def _grouped_caches(dims: GroupedDims, k_cache, k_scale, v_cache, v_scale, block
         _need(T == dims.B, "without cu there is one row for each sequence")
 
 
-def _row_width(t, n: int, name: str):
-    """Rows of a tensor of more than one dimension are as long as the call reads them (a wider one is no less than it needs)."""
-    if t.dim() > 1 and t.shape[-1] != n:
+def _row_width(t, n: int, total: int, name: str):
+    """A tensor of more than one dimension and more elements than the call needs has them in further rows, not in longer ones:
+    its last dimensions make up rows of n elements."""
+    if t.numel() == total or t.dim() < 2:
+        return
+    p = 1
+    for s in reversed(t.shape):
+        p *= s
+        if p >= n:
+            break
+    if p != n:
         raise ValueError(f"rows of {name} must have {n} elements")
 
 
@@ -657,7 +665,7 @@ def grouped_append(dims: GroupedDims, k_new, v_new, block_table, seq_lens, k_cac
         _device(k_new, v_new, block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, cu, ws)
         _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
         at = [_at(t) for t in (block_table, seq_lens, k_cache, k_scale, v_cache, v_scale, ws)]
-    _row_width(block_table, dims.max_blocks, "block_table")
+    _row_width(block_table, dims.max_blocks, dims.B * dims.max_blocks, "block_table")
     st = lib().dsa_grouped_append(dims, *k, *v, at[0], at[1], _at(cu), T, at[2], at[3], at[4], at[5], at[6], ws.numel(),
                                   _raw_stream(dev, stream))
     if st:
@@ -683,11 +691,12 @@ def grouped_attn(dims: GroupedDims, q, k_cache, k_scale, v_cache, v_scale, block
         _device(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, ws)
         _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T)
         at = [_at(t) for t in (k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, ws)]
-    _row_width(block_table, dims.max_blocks, "block_table")
+    _row_width(block_table, dims.max_blocks, dims.B * dims.max_blocks, "block_table")
     for t, name in ((weights, "weights"), (weights_out, "weights_out")):
         if t is not None:
-            _fp32(t, dims.B * dims.H_kv * dims.max_blocks * 64, name)
-            _row_width(t, dims.max_blocks * 64, name)
+            n = dims.max_blocks * 64
+            _fp32(t, dims.B * dims.H_kv * n, name)
+            _row_width(t, n, dims.B * dims.H_kv * n, name)
     if out is None:
         out = _empty((T, dims.H, dims.d_v), q.dtype, q.device, stream)
     elif out.dtype is not q.dtype or out.numel() < T * dims.H * dims.d_v:
@@ -714,23 +723,24 @@ def grouped_evict(dims: GroupedDims, weights, keep: int, block_table, seq_lens, 
     dev = _device(weights, block_table, seq_lens, new_table, k_cache, k_scale, v_cache, v_scale, ws, kept, new_lens, weights_out)
     _grouped_caches(dims, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, None, -1)
     _int32(new_table, 0, "new_table")
-    _fp32(weights, dims.B * dims.H_kv * dims.max_blocks * 64, "weights")
-    _row_width(block_table, dims.max_blocks, "block_table")
-    _row_width(weights, dims.max_blocks * 64, "weights")
+    heads = dims.B * dims.H_kv
+    _fp32(weights, heads * dims.max_blocks * 64, "weights")
+    _row_width(block_table, dims.max_blocks, dims.B * dims.max_blocks, "block_table")
+    _row_width(weights, dims.max_blocks * 64, heads * dims.max_blocks * 64, "weights")
     blocks = new_table.shape[1]
     if kept is None:
         kept = _empty((dims.B, dims.H_kv, max(0, keep)), torch.int32, ws.device, stream)
     else:
-        _int32(kept, dims.B * dims.H_kv * keep, "kept")
-        _row_width(kept, keep, "kept")
+        _int32(kept, heads * keep, "kept")
+        _row_width(kept, keep, heads * keep, "kept")
     if new_lens is None:
         new_lens = _empty((dims.B,), torch.int32, ws.device, stream)
     _int32(new_lens, dims.B, "new_lens")
     if weights_out is None:
         weights_out = _empty((dims.B, dims.H_kv, blocks * 64), torch.float32, ws.device, stream)
     else:
-        _fp32(weights_out, dims.B * dims.H_kv * blocks * 64, "weights_out")
-        _row_width(weights_out, blocks * 64, "weights_out")
+        _fp32(weights_out, heads * blocks * 64, "weights_out")
+        _row_width(weights_out, blocks * 64, heads * blocks * 64, "weights_out")
     st = lib().dsa_grouped_evict(dims, _at(weights), keep, sink, recent, _at(block_table), _at(seq_lens), _at(new_table), blocks,
                                  _at(k_cache), _at(k_scale), _at(v_cache), _at(v_scale), _at(kept), _at(new_lens),
                                  _at(weights_out), _at(ws), ws.numel(), _raw_stream(dev, stream))

@@ -802,6 +802,11 @@ def test_rows_of_another_width_are_refused():
     ref = attn(weights=w.clone())
     got = attn(c.table.flatten(), weights=w.flatten())  # without dimensions of their own
     assert torch.equal(got[0], ref[0]) and dsa.read_error(ws) == 0
+    # the same rows in other dimensions, and more of them
+    for weights in (w.view(2, 2, -1, 64), w.view(2, -1), w.view(4, -1), torch.cat([w, w]), torch.cat([w, w]).view(4, 2, -1, 64)):
+        for table in (c.table, torch.cat([c.table, c.table])):
+            got = attn(table, weights=weights.clone())
+            assert torch.equal(got[0], ref[0]) and dsa.read_error(ws) == 0
 
 
 # ------------------------------------------------------------------------------------------------ together

@@ -198,3 +198,12 @@ def test_overlapping_outputs_are_refused(L):
         assert _attn(L, w=FAKE, wo=at(off), nbytes=0) == 3, off
     assert _evict(L, wo=at(size), nbytes=0) == 3 and _evict(L, wo=at(-size // 2), nbytes=0) == 3 and _evict(L, new_lens=at(8), nbytes=0) == 3
     assert L.dsa_last_launch_count() == 0
+
+
+def test_widths_of_rows():
+    """What is as large as needed is taken; what is larger has whole rows in its last dimensions."""
+    for shape in ((4, 6), (24,), (30,), (2, 12), (4, 2, 3), (5, 6), (2, 2, 6), (7, 2, 3), (1, 4, 3, 2)):
+        dsa._row_width(torch.empty(shape), 6, 24, "x")
+    for shape in ((4, 7), (2, 13), (4, 12), (5, 2, 4), (4, 2, 4)):
+        with pytest.raises(ValueError, match="rows of x must have 6"):
+            dsa._row_width(torch.empty(shape), 6, 24, "x")
