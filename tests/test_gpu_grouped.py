@@ -916,6 +916,32 @@ def test_scales_that_change_from_block_to_block(type, H, new):
 
 
 @pytest.mark.parametrize("type,H,new", SHAPES)
+def test_scales_of_any_size(type, H, new):
+    """Value scales near both ends of their range, alone, and 2^50 and more apart: the largest ones' columns are right, and the
+    smaller ones' too as far as 2^60 below."""
+    for low, high in ((-88, -88), (100, 100), (60, 110), (-88, -40), (-20, 70)):
+        c, q, at = light_and_heavy(type, H, 30 * 64 - 7, new=new)
+        c.vs[at] = 2.0 ** high
+        c.vs[at[::3]] = 2.0 ** low
+        if low != high:  # the small blocks alone have columns of their own
+            other = torch.ones(30, dtype=torch.bool, device="cuda")
+            other[::3] = False
+            c.v[at[other], :, :, :8] = 0
+        louder(c, 100)
+        out, lse = attend(c, q, [new], 1.0)
+        cols = range(8, 32) if high - low > 60 else range(32)
+        for scale, part in ((high, [e for e in cols if e >= 8]), (low, [e for e in cols if e < 8])):
+            k, v, ok = c.rows(0, 0)
+            for i in range(new):
+                p = torch.softmax((q[i].double() @ k.T).masked_fill(torch.arange(len(k), device="cuda") > len(k) - new + i, -math.inf), -1)
+                want = (p @ v)[:, part] * 2.0 ** -scale
+                # as for scales that rise and fall
+                rel = (2.0 ** -10 + 2.0 ** -8 if type == "bf16" else 2.0 ** -21) + 2 * 2.0 ** -22 * 15 + len(k) * 2.0 ** -24
+                tol = rel * want + (2.0 ** -22 if type == "bf16" else 2.0 ** -30) * p.amax(-1, keepdim=True) * v.sum(0)[part] * 2.0 ** -scale
+                assert bool(((out[i][:, part].double() * 2.0 ** -scale - want).abs() <= tol).all()), (low, high, scale)
+
+
+@pytest.mark.parametrize("type,H,new", SHAPES)
 @pytest.mark.parametrize("step", [1.25, -1.25, 0.5, -2.5])
 def test_scales_that_rise_and_fall_by_steps(type, H, new, step):
     """Scales that drift by a few powers of two a block, up or down, up to 2^54 in all; block j has values in column j % 32 alone."""
